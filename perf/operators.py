@@ -333,7 +333,7 @@ def _resize_plain(s):
     rc = rc.scatter_add(0, torch.where(cow_done, last, 0), -cow_done.long())
     rc = rc.scatter_add(0, torch.where(cow_done, own_page, 0), cow_done.long())
     rc = rc.scatter_add(0, torch.where(fresh, got, 0).flatten(), fresh.long().flatten())
-    _copy_plain(s, last, torch.where(cow_done, own_page, last))
+    _copy_plain(s, last[cow_done], own_page[cow_done])
     return dict(page_table=out.int(), kv_len=out_len.int(), refcount=rc.int(), free_pages=(rc == 0).sum().int()[None],
                 k=s["k"], v=s["v"])
 
@@ -362,7 +362,7 @@ def _fork_plain(s):
     out, out_len = tab.clone(), L.clone()
     out[child] = rows
     out_len[child] = torch.where(part & ~done, full * S, n)
-    _copy_plain(s, src, torch.where(done, fresh, src))
+    _copy_plain(s, src[done], fresh[done])
     return dict(page_table=out.int(), kv_len=out_len.int(), refcount=rc.int(), free_pages=(rc == 0).sum().int()[None],
                 k=s["k"], v=s["v"])
 
