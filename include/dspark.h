@@ -95,6 +95,10 @@ enum { DSPARK_GROUP = 32 };
  * verify draw's wait for its bulk copy of a target row); the outputs of that
  * call are then not valid, and the context stays usable. */
 enum { DSPARK_DEV_BAD_INPUT = 1, DSPARK_DEV_TIMEOUT = 2 };
+/* DSPARK_DEV_NO_PAGES: a page pool had fewer free pages than a call asked for
+ * (dspark_pages_resize, dspark_pages_fork); the lengths the call returns say
+ * what each request got. */
+enum { DSPARK_DEV_NO_PAGES = 4 };
 
 /* Text of a status code; static storage. */
 const char* dspark_status_string(int status);
@@ -388,6 +392,168 @@ int dspark_verify_noalloc(const int32_t* x, const float* logp, const float* lse,
                           int32_t* tokens, int32_t* n_emit, float* cstar, float* lse_t,
                           void* stream);
 
+/* ========================================================================
+ * The target model's side of a round: the paged K/V cache, the attention of a
+ * chunk of new tokens over it, the management of its pages, and the
+ * log-probabilities that a server answers with.  A round is
+ *
+ *   dspark_pages_resize (room for the chunk) -> per layer: dspark_cache_append,
+ *   dspark_paged_attention -> target logits Z -> dspark_verify ->
+ *   dspark_logprobs -> dspark_pages_resize (the rejected suffix is cut off)
+ *
+ * The cache: K and V of every layer as pages of page_size positions,
+ * [layers, n_pages, page_size, heads, head_dim] with the strides below (in
+ * elements, the same for K and V, head_dim contiguous), so that positions may
+ * lie before heads in a page or heads before positions, and K and V may be
+ * parts of one array.  Request r's position j is in page
+ * page_table[r][j / page_size] at place j % page_size, the same page in every
+ * layer.  `dspark_cache` itself is a HOST struct that the call reads.
+ * refcount[p] is the number of requests whose tables hold page p (0: free).
+ *
+ * Limits (else DSPARK_ERR_UNSUPPORTED): R <= 65535, heads <= 1024, head_dim <=
+ * 256, page_size <= 65536, R * max_pages < 2^31; kv_len counts positions and
+ * is at most max_pages * page_size.
+ * ======================================================================== */
+typedef struct {
+  void* k; /* DEVICE: page 0 of layer 0 */
+  void* v;
+  int dtype; /* DSPARK_F32 or DSPARK_BF16 */
+  int layers, n_pages, page_size, heads, head_dim;
+  long long layer_stride, page_stride, token_stride, head_stride;
+} dspark_cache;
+
+/* ------------------------------------------------------------------------
+ * dspark_cache_append -- writes the new tokens' K and V of one layer.  Request
+ * r's chunk is rows q_offsets[r] .. q_offsets[r + 1] - 1 of k_new and v_new; its
+ * last token gets position kv_len[r] - 1 (kv_len counts the new tokens).
+ *
+ * k_new, v_new [n_tokens, heads, head_dim], cache dtype, the strides given in
+ *              elements and the same for both (they may be parts of one
+ *              projection's output); head_dim contiguous
+ * q_offsets    [R + 1] int32, non-decreasing, from 0; rows at or past
+ *              q_offsets[R] are padding and are not used
+ * kv_len       [R] int32; page_table [R, max_pages] int32
+ * Tokens whose position or page is out of range are flagged
+ * (DSPARK_DEV_BAD_INPUT) and left out.  The pages written must not be shared
+ * (dspark_pages_resize sees to that).  n_tokens may be 0.
+ * workspace: >= 256 bytes, 256-byte aligned (the status word).
+ * ---------------------------------------------------------------------- */
+int dspark_cache_append(const dspark_cache* cache, int layer, const void* k_new, const void* v_new,
+                        long long new_token_stride, long long new_head_stride,
+                        const int32_t* q_offsets, const int32_t* kv_len, const int32_t* page_table,
+                        int R, int n_tokens, int max_pages, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * dspark_paged_attention -- attention of the chunk over one layer of the
+ * cache.  Token i of request r's n = q_offsets[r + 1] - q_offsets[r] new tokens
+ * has position p = kv_len[r] - n + i and sees the cached positions 0 .. p (its
+ * own K and V appended before).  Query head h reads K/V head h / (Hq / heads):
+ *   s_j = scale q . k_j,  out = sum_j softmax(s)_j v_j,  lse = ln sum_j e^{s_j}
+ * A token with p < 0 sees nothing: out = 0, lse = -inf.  A chunk of one token
+ * is plain decoding.  Sums and softmax statistics are fp32; the bf16 kernel
+ * rounds the probabilities to bf16 for the second product.
+ *
+ * q    [n_tokens, Hq, head_dim] cache dtype, strides in elements, head_dim
+ *      contiguous; Hq a multiple of the cache's heads
+ * out  [n_tokens, Hq, head_dim] cache dtype, dense
+ * lse  [n_tokens, Hq] float
+ * Rows at or past q_offsets[R] are neither read nor written.  Cache positions at or past
+ * kv_len[r] never reach the outputs, whatever they hold; those before it, of
+ * the pages in use, have to be finite (a value that is not may reach every
+ * row of its request's chunk, also tokens before it).  Offsets, lengths or pages out
+ * of range are flagged (DSPARK_DEV_BAD_INPUT) and clamped.
+ * workspace: >= dspark_paged_attention_workspace_bytes(cache) bytes,
+ *   256-byte aligned.
+ * ---------------------------------------------------------------------- */
+size_t dspark_paged_attention_workspace_bytes(const dspark_cache* cache);
+int dspark_paged_attention(const void* q, long long q_token_stride, long long q_head_stride, int Hq,
+                           const dspark_cache* cache, int layer, const int32_t* q_offsets,
+                           const int32_t* kv_len, const int32_t* page_table, int R, int n_tokens,
+                           int max_pages, float scale, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Page management.  Each call reads the state (page_table, kv_len, refcount)
+ * and writes the new one; an output may be the input's own array (then only
+ * what changes is written) or a separate one, but may not overlap it otherwise.
+ * Entries of a table past its request's pages are left as they are.  Pages are taken in a
+ * fixed order, the lowest free ids first, so equal inputs give equal tables.
+ * The cache's K and V are changed in place: pages are copied in all layers.
+ *
+ * dspark_pages_resize -- gives request r room for new_len[r] positions.
+ *   Shorter: pages past ceil(new_len / page_size) lose a reference (0: free;
+ *   their table entries become -1); new_len = 0 ends the request.  Longer: in
+ *   the order of r, pages freed by this call included, the lowest free pages are added.
+ *   If the last page is partly filled and shared (refcount > 1 after the
+ *   releases), the request first gets a copy of its own; pages that no
+ *   request holds any more after that are free from the next call on.
+ *   kv_len_out[r] = new_len[r], or less where the pool ran out
+ *   (DSPARK_DEV_NO_PAGES): as much as the pages at hand allow.
+ * dspark_pages_fork -- request child[i] becomes a copy of parent[i], i < n
+ *   (n <= R), as the parent is before the call: it shares its full pages; a partly filled last page is
+ *   copied into the lowest free page, in the order of i.  A child must be
+ *   empty (kv_len 0) and named once; pairs that break this are flagged
+ *   (DSPARK_DEV_BAD_INPUT) and skipped.  If the pool runs out, the child's
+ *   length is that of its full pages.
+ * dspark_pages_compact -- moves the live pages (refcount > 0) to the lowest
+ *   ids: with n live pages, the i-th live page with id >= n goes to the i-th
+ *   free id < n.  page_map[p] = page p's id afterwards (-1: free);
+ *   n_live [1] = n; kv_len is unchanged.
+ * dspark_pages_copy -- copies pages src[i] -> dst[i], i < n, in all layers.
+ *   The dst are distinct and none of them is a src.
+ *
+ * page_table(_out) [R, max_pages], kv_len(_out), new_len [R], refcount(_out)
+ * [n_pages], parent, child, src, dst [n], free_pages [1] (free pages
+ * afterwards), page_map [n_pages]: int32, DEVICE.
+ * workspace: >= dspark_pages_workspace_bytes(R, n_pages) bytes, 256-byte
+ *   aligned (dspark_pages_copy: 256 bytes).
+ * ---------------------------------------------------------------------- */
+size_t dspark_pages_workspace_bytes(int R, int n_pages);
+int dspark_pages_resize(const dspark_cache* cache, const int32_t* page_table, const int32_t* kv_len,
+                        const int32_t* new_len, const int32_t* refcount, int R, int max_pages,
+                        int32_t* page_table_out, int32_t* kv_len_out, int32_t* refcount_out,
+                        int32_t* free_pages, void* workspace, size_t workspace_bytes, void* stream);
+int dspark_pages_fork(const dspark_cache* cache, const int32_t* page_table, const int32_t* kv_len,
+                      const int32_t* refcount, const int32_t* parent, const int32_t* child, int n,
+                      int R, int max_pages, int32_t* page_table_out, int32_t* kv_len_out,
+                      int32_t* refcount_out, int32_t* free_pages, void* workspace,
+                      size_t workspace_bytes, void* stream);
+int dspark_pages_compact(const dspark_cache* cache, const int32_t* page_table,
+                         const int32_t* kv_len, const int32_t* refcount, int R, int max_pages,
+                         int32_t* page_table_out, int32_t* refcount_out, int32_t* page_map,
+                         int32_t* n_live, void* workspace, size_t workspace_bytes, void* stream);
+int dspark_pages_copy(const dspark_cache* cache, const int32_t* src, const int32_t* dst, int n,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * dspark_logprobs -- what a server reports beside the emitted tokens.  For
+ * every row i with tokens[i] >= 0, with x = Z[i] / T over the V ids:
+ *   lse = ln sum e^x, logp = x[tokens[i]] - lse, entropy = lse - sum p x,
+ *   top_ids / top_logp = the `top` ids in the order (logit descending, id
+ *   ascending) with x - lse.
+ * Rows with a negative token are not read and get NaN and -1: with Z of
+ * dspark_verify as [R * (gamma + 1), V] rows and its `tokens`, these are the
+ * positions after the last emitted token.
+ *
+ * Z        [n_rows, V] dtype, rows row_stride elements apart, 16-byte aligned
+ *          rows (pointer and stride)
+ * tokens   [n_rows] int32; an id >= V is flagged (DSPARK_DEV_BAD_INPUT), logp NaN
+ * logp, entropy, lse [n_rows] float; top_ids [n_rows, top] int32, top_logp
+ *          [n_rows, top] float (both may be NULL when top = 0)
+ * Masked ids (-inf) have probability 0 and come last among the alternatives,
+ * with logp -inf; a row of nothing but -inf gives lse = -inf and NaN
+ * otherwise.  NaN or +inf in a row makes lse, logp and entropy NaN; NaN ranks as -inf.
+ * Limits: 8 <= V <= 2^30, V % 8 == 0, 0 <= top <= min(32, V).
+ * workspace: >= dspark_logprobs_workspace_bytes(n_rows, V) bytes, 256-byte
+ *   aligned.
+ * ---------------------------------------------------------------------- */
+size_t dspark_logprobs_workspace_bytes(int n_rows, int V);
+int dspark_logprobs(const void* Z, int dtype, long long row_stride, const int32_t* tokens,
+                    int n_rows, int V, float temperature, int top, float* logp, float* entropy,
+                    float* lse, int32_t* top_ids, float* top_logp, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 /* Copies the device status word of `workspace` (as written by the last call
  * that used it) to *out after synchronising `stream`.  *out is a HOST pointer.
  * Returns DSPARK_OK, or DSPARK_ERR_CUDA if the copy failed. */
@@ -423,6 +589,19 @@ enum {
 };
 int dspark_profile_start(void);
 int dspark_profile_stop(double* ms_by_kind, int* launches_by_kind, int* timed_launches);
+/* dspark_profile_stop_kinds -- the same for n_kinds kinds: also those of the
+ * serving operators, which dspark_profile_stop (DSPARK_KERNEL_KINDS entries)
+ * counts as timed launches but does not report.  The arrays hold n_kinds
+ * entries; kinds that the library does not have are left alone. */
+enum {
+  DSPARK_KERNEL_APPEND = 8,     /* dspark_cache_append */
+  DSPARK_KERNEL_ATTENTION = 9,  /* dspark_paged_attention: all its launches as one */
+  DSPARK_KERNEL_PAGES = 10,     /* dspark_pages_*: all launches of a call as one */
+  DSPARK_KERNEL_LOGPROBS = 11,  /* dspark_logprobs: all launches as one */
+  DSPARK_KERNEL_ALL_KINDS = 12
+};
+int dspark_profile_stop_kinds(int n_kinds, double* ms_by_kind, int* launches_by_kind,
+                              int* timed_launches);
 
 /* ------------------------------------------------------------------------
  * dspark_stream_probe -- a bandwidth probe: out[i] = (float)in[i] for n bf16

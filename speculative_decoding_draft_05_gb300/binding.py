@@ -96,6 +96,29 @@ def load() -> ctypes.CDLL:
     L.dspark_selftest_draft_timeout.argtypes = [P, P, P, P, I, I, I, I, ctypes.c_longlong, P, P, P, P,
                                                 P, SZ, P]
     L.dspark_selftest_draft_timeout.restype = I
+    LL = ctypes.c_longlong
+    L.dspark_profile_stop_kinds.argtypes = [I, P, P, P]
+    L.dspark_profile_stop_kinds.restype = I
+    L.dspark_cache_append.argtypes = [P, I, P, P, LL, LL, P, P, P, I, I, I, P, SZ, P]
+    L.dspark_cache_append.restype = I
+    L.dspark_paged_attention_workspace_bytes.argtypes = [P]
+    L.dspark_paged_attention_workspace_bytes.restype = SZ
+    L.dspark_paged_attention.argtypes = [P, LL, LL, I, P, I, P, P, P, I, I, I, F, P, P, P, SZ, P]
+    L.dspark_paged_attention.restype = I
+    L.dspark_pages_workspace_bytes.argtypes = [I, I]
+    L.dspark_pages_workspace_bytes.restype = SZ
+    L.dspark_pages_resize.argtypes = [P, P, P, P, P, I, I, P, P, P, P, P, SZ, P]
+    L.dspark_pages_resize.restype = I
+    L.dspark_pages_fork.argtypes = [P, P, P, P, P, P, I, I, I, P, P, P, P, P, SZ, P]
+    L.dspark_pages_fork.restype = I
+    L.dspark_pages_compact.argtypes = [P, P, P, P, I, I, P, P, P, P, P, SZ, P]
+    L.dspark_pages_compact.restype = I
+    L.dspark_pages_copy.argtypes = [P, P, P, I, P, SZ, P]
+    L.dspark_pages_copy.restype = I
+    L.dspark_logprobs_workspace_bytes.argtypes = [I, I]
+    L.dspark_logprobs_workspace_bytes.restype = SZ
+    L.dspark_logprobs.argtypes = [P, I, LL, P, I, I, F, I, P, P, P, P, P, P, SZ, P]
+    L.dspark_logprobs.restype = I
     _lib = L
     return L
 
@@ -417,7 +440,7 @@ def dspark_read_device_status(workspace: torch.Tensor, stream=None) -> int:
 
 
 KERNEL_KINDS = ["prepare", "draft_tile", "draft_combine", "schedule", "verify_rows", "verify_draw",
-                "rnn_state", "verify_emit"]
+                "rnn_state", "verify_emit", "cache_append", "paged_attention", "pages", "logprobs"]
 
 
 def dspark_stream_probe(inp, out, stream=None) -> None:
@@ -442,7 +465,8 @@ def dspark_profile_stop() -> dict:
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_int * n)()
     timed = ctypes.c_int(0)
-    _check("dspark_profile_stop", load().dspark_profile_stop(ms, cnt, ctypes.byref(timed)))
+    _check("dspark_profile_stop_kinds",
+           load().dspark_profile_stop_kinds(n, ms, cnt, ctypes.byref(timed)))
     out = {k: (float(ms[i]), int(cnt[i])) for i, k in enumerate(KERNEL_KINDS)}
     out["_timed_launches"] = int(timed.value)
     return out

@@ -10,14 +10,20 @@
 
 #include "../../include/dspark.h"
 #include "kernels.h"
+#include "serving.h"
 
 namespace dspark {
 
 static thread_local char g_last_error[256] = "";
 
-static int cuda_fail(cudaError_t e, const char* where) {
+int cuda_fail(cudaError_t e, const char* where) {
   snprintf(g_last_error, sizeof(g_last_error), "%s: %s", where, cudaGetErrorString(e));
   return DSPARK_ERR_CUDA;
+}
+
+int unsupported(const char* why) {
+  snprintf(g_last_error, sizeof(g_last_error), "%s", why);
+  return DSPARK_ERR_UNSUPPORTED;
 }
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -82,7 +88,7 @@ struct Profiler {
 };
 static Profiler g_prof;
 
-static void prof_begin(int kind, cudaStream_t s) {
+void prof_begin(int kind, cudaStream_t s) {
   if (!g_prof.on) return;
   g_prof.launches[kind] += 1;
   if (g_prof.n < Profiler::kMax) {
@@ -91,7 +97,7 @@ static void prof_begin(int kind, cudaStream_t s) {
   }
 }
 
-static void prof_end(cudaStream_t s) {
+void prof_end(cudaStream_t s) {
   if (!g_prof.on || g_prof.n >= Profiler::kMax) return;
   cudaEventRecord(g_prof.ev[2 * g_prof.n + 1], s);
   g_prof.n += 1;
@@ -706,10 +712,12 @@ int dspark_stream_probe(const void* in, float* out, size_t n, void* stream) {
   return DSPARK_OK;
 }
 
-int dspark_profile_stop(double* ms_by_kind, int* launches_by_kind, int* timed_launches) {
-  if (!g_prof.on) return DSPARK_ERR_INVALID_ARG;
+int dspark_profile_stop_kinds(int n_kinds, double* ms_by_kind, int* launches_by_kind,
+                              int* timed_launches) {
+  if (!g_prof.on || n_kinds < 0) return DSPARK_ERR_INVALID_ARG;
   g_prof.on = false;
-  for (int k = 0; k < kKindCount; ++k) {
+  if (n_kinds > kKindCount) n_kinds = kKindCount;
+  for (int k = 0; k < n_kinds; ++k) {
     if (ms_by_kind) ms_by_kind[k] = 0.0;
     if (launches_by_kind) launches_by_kind[k] = g_prof.launches[k];
   }
@@ -721,9 +729,13 @@ int dspark_profile_stop(double* ms_by_kind, int* launches_by_kind, int* timed_la
     float ms = 0.0f;
     e = cudaEventElapsedTime(&ms, g_prof.ev[2 * i], g_prof.ev[2 * i + 1]);
     if (e != cudaSuccess) return cuda_fail(e, "profile elapsed");
-    if (ms_by_kind) ms_by_kind[g_prof.kind[i]] += ms;
+    if (ms_by_kind && g_prof.kind[i] < n_kinds) ms_by_kind[g_prof.kind[i]] += ms;
   }
   return DSPARK_OK;
+}
+
+int dspark_profile_stop(double* ms_by_kind, int* launches_by_kind, int* timed_launches) {
+  return dspark_profile_stop_kinds(DSPARK_KERNEL_KINDS, ms_by_kind, launches_by_kind, timed_launches);
 }
 
 }  // extern "C"

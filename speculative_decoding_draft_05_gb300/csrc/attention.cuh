@@ -1,0 +1,267 @@
+// attention.cuh -- what the kernels of attention over the paged cache share:
+// the division of the work and the partial results that a division leaves.
+//
+// An item is a block of up to MR rows of one request's chunk for one K/V head.
+// A row is (token, query head of the group): row = token * G + g, so all G
+// query heads that share a K/V head read its tiles once.  An item walks its
+// keys in tiles of TN; a unit of work is one tile of one item (an item without
+// keys is one unit).  The units of all items, in the order request, row block,
+// head, tile, are cut into equal contiguous shares, one a CTA: short and long
+// requests, many rows and few, all load every SM alike.  An item cut by a
+// share's end leaves partial results (max, sum, unnormalised output in fp32),
+// which the combine kernel adds in the order of the shares, so results do not
+// depend on timing.
+#pragma once
+
+#include "common.cuh"
+#include "serving.h"
+
+namespace dspark {
+
+constexpr int kAttnMaxCtas = 320;  // CTAs of one attention launch, at most
+
+// A cut item, written by the CTA whose share begins inside it.
+struct CutItem {
+  int valid, r, m, h;     // request, row block, K/V head
+  int n, q0, rows, n_tiles;  // chunk length, first token, rows of the block, tiles
+  long long u0;           // the item's first unit
+  long long pad;
+};
+
+// Workspace: status word, [256] total units, cut items, partial (m, l) and O.
+struct AttnWorkspace {
+  size_t units, cuts, stats, out, total;
+};
+inline AttnWorkspace attn_workspace_layout(int MR, int D) {
+  AttnWorkspace w;
+  w.units = 64;
+  w.cuts = 256;
+  w.stats = align_up256(w.cuts + kAttnMaxCtas * sizeof(CutItem));
+  w.out = align_up256(w.stats + (size_t)kAttnMaxCtas * 2 * MR * sizeof(float2));
+  w.total = align_up256(w.out + (size_t)kAttnMaxCtas * 2 * MR * D * sizeof(float));
+  return w;
+}
+
+struct AttnParams {
+  AttnArgs a;
+  int* status;
+  long long* units;  // total units (for the combine)
+  CutItem* cuts;     // [grid]
+  float2* stats;     // [grid][2][MR] (m, l), m in log2 units
+  float* part;       // [grid][2][MR][D]
+  float scale_log2;  // scale * log2(e)
+};
+
+struct AttnRequest {
+  int q0, n, L;  // first token, chunk length, cached positions
+};
+
+__device__ __forceinline__ AttnRequest attn_request(const ChunkArgs& a, int page_size, int r,
+                                                    int* status) {
+  AttnRequest q;
+  int b = a.q_offsets[r], e = a.q_offsets[r + 1], L = a.kv_len[r];
+  const long long most_l = (long long)a.max_pages * page_size;
+  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  if (b < 0 || e < b || e > a.n_tokens || L < 0 || L > most) {
+    flag_status(status, DSPARK_DEV_BAD_INPUT);
+    b = b < 0 ? 0 : b > a.n_tokens ? a.n_tokens : b;
+    e = e < b ? b : e > a.n_tokens ? a.n_tokens : e;
+    L = L < 0 ? 0 : L > most ? most : L;
+  }
+  q.q0 = b;
+  q.n = e - b;
+  q.L = L;
+  return q;
+}
+
+// Keys that the rows of block m see: positions 0 .. end - 1.
+template <int MR>
+__device__ __forceinline__ int attn_item_end(const AttnRequest& q, int G, int m) {
+  int last = ((m + 1) * MR - 1) / G;
+  last = last < q.n - 1 ? last : q.n - 1;
+  const int end = q.L - q.n + last + 1;
+  return end < 0 ? 0 : end;
+}
+
+template <int TN>
+__device__ __forceinline__ int attn_tiles(int end) {
+  return end <= TN ? 1 : (end + TN - 1) / TN;
+}
+
+template <int MR, int TN>
+__device__ __forceinline__ long long attn_request_units(const AttnRequest& q, int G, int Hkv) {
+  const long long rows = (long long)q.n * G;
+  if (rows == 0) return 0;
+  if (rows <= MR) return (long long)Hkv * attn_tiles<TN>(q.L);
+  const int blocks = (int)((rows + MR - 1) / MR);
+  long long u = 0;
+  for (int m = 0; m < blocks; ++m) u += attn_tiles<TN>(attn_item_end<MR>(q, G, m));
+  return u * Hkv;
+}
+
+// First unit of CTA c's share.  With fewer units than CTAs the first `units`
+// CTAs get one each, so that no share between two others is empty.
+__device__ __forceinline__ long long attn_share(long long units, int ctas, int c) {
+  const long long n = units < ctas ? units : ctas;
+  return c >= n ? units : units * c / n;
+}
+
+// The walk of one CTA (or one warp role of it) over its share.
+template <int MR, int TN>
+struct AttnWalk {
+  const AttnParams* p;
+  AttnRequest q;
+  int r, m, h;           // current item
+  int end, n_tiles;      // its keys and tiles
+  long long u0;          // its first unit
+  long long u, stop;     // next unit, end of the share
+
+  // Places the walk at the item that holds unit `u`, given the request r that
+  // holds it and that request's first unit.
+  __device__ __forceinline__ void seek(int request, long long first) {
+    const int G = p->a.G, Hkv = p->a.c.heads;
+    r = request;
+    q = attn_request(p->a.a, p->a.c.page_size, r, p->status);
+    u0 = first;
+    m = 0;
+    for (;;) {
+      end = attn_item_end<MR>(q, G, m);
+      n_tiles = attn_tiles<TN>(end);
+      if (u < u0 + (long long)n_tiles * Hkv || (long long)(m + 1) * MR >= (long long)q.n * G) break;
+      u0 += (long long)n_tiles * Hkv;
+      ++m;
+    }
+    h = (int)((u - u0) / n_tiles);
+    u0 += (long long)h * n_tiles;
+  }
+
+  __device__ __forceinline__ bool done() const { return u >= stop; }
+  __device__ __forceinline__ int first_tile() const { return (int)(u - u0); }
+  __device__ __forceinline__ int last_tile() const {  // one past the last tile of this share
+    const long long e = stop - u0;
+    return e < n_tiles ? (int)e : n_tiles;
+  }
+  __device__ __forceinline__ int block_rows() const {
+    const long long left = (long long)q.n * p->a.G - (long long)m * MR;
+    return left < MR ? (int)left : MR;
+  }
+
+  __device__ __forceinline__ void next() {
+    u = u0 + last_tile();
+    if (done()) return;
+    const int G = p->a.G, Hkv = p->a.c.heads;
+    u0 += n_tiles;
+    if (++h < Hkv) return;
+    h = 0;
+    if ((long long)(++m) * MR >= (long long)q.n * G) {
+      m = 0;
+      do {
+        if (++r >= p->a.a.R) {  // (not reached: the units count the items)
+          u = stop;
+          return;
+        }
+        q = attn_request(p->a.a, p->a.c.page_size, r, p->status);
+      } while (q.n == 0);
+    }
+    end = attn_item_end<MR>(q, G, m);
+    n_tiles = attn_tiles<TN>(end);
+  }
+};
+
+// What a CTA's threads work out together at the start: the total units, and
+// the request in which the CTA's share begins.
+struct AttnStart {
+  long long units, first;  // total; first unit of `request`
+  int request;
+  long long scan[33];
+};
+
+// All threads of the CTA (a multiple of 32, at most 1024).  Ends with a barrier.
+template <int MR, int TN>
+__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int R = p.a.a.R;
+  const int per = (R + (int)blockDim.x - 1) / (int)blockDim.x;
+  const int r0 = min(R, (int)threadIdx.x * per), r1 = min(R, r0 + per);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r)
+    mine += attn_request_units<MR, TN>(attn_request(p.a.a, p.a.c.page_size, r, p.status), p.a.G,
+                                       p.a.c.heads);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) st->scan[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const long long own = lane < warps ? st->scan[lane] : 0;
+    long long v = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane < warps) st->scan[lane] = v - own;
+    if (lane == 31) st->units = v;
+  }
+  __syncthreads();
+  const long long units = st->units;
+  const long long start = attn_share(units, gridDim.x, blockIdx.x);
+  long long at = st->scan[warp] + incl - mine;
+  if (start >= at && start < at + mine) {
+    for (int r = r0; r < r1; ++r) {
+      const long long k = attn_request_units<MR, TN>(
+          attn_request(p.a.a, p.a.c.page_size, r, p.status), p.a.G, p.a.c.heads);
+      if (start < at + k) {
+        st->request = r;
+        st->first = at;
+        break;
+      }
+      at += k;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.units = units;
+  __syncthreads();
+}
+
+template <int MR, int TN>
+__device__ __forceinline__ AttnWalk<MR, TN> attn_walk(const AttnParams& p, const AttnStart& st) {
+  AttnWalk<MR, TN> w;
+  w.p = &p;
+  w.u = attn_share(st.units, gridDim.x, blockIdx.x);
+  w.stop = attn_share(st.units, gridDim.x, blockIdx.x + 1);
+  if (!w.done()) w.seek(st.request, st.first);
+  return w;
+}
+
+// Written once a CTA: whether its share begins inside an item, and which.
+template <int MR, int TN>
+__device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnWalk<MR, TN>& w) {
+  CutItem c;
+  c.valid = !w.done() && w.first_tile() > 0;
+  if (c.valid) {
+    c.r = w.r, c.m = w.m, c.h = w.h;
+    c.n = w.q.n, c.q0 = w.q.q0, c.rows = w.block_rows(), c.n_tiles = w.n_tiles;
+    c.u0 = w.u0;
+  }
+  p.cuts[blockIdx.x] = c;
+}
+
+// Where the walk's current piece of its item goes: -1 whole (straight to the
+// output), 0 the item began in an earlier share, 1 it goes on in a later one.
+template <int MR, int TN>
+__device__ __forceinline__ int attn_slot(const AttnWalk<MR, TN>& w) {
+  if (w.first_tile() > 0) return 0;
+  return w.last_tile() < w.n_tiles ? 1 : -1;
+}
+
+cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStream_t s);
+
+// The tensor-core path (attention_tc.cu).
+bool attention_tc_supported(const AttnArgs& a);
+size_t attention_tc_workspace_bytes(int head_dim);
+cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s);
+
+}  // namespace dspark

@@ -157,7 +157,11 @@ enum KernelKind {
   kKindVerifyDraw = 5,  // stage 1 of the residual / bonus draw
   kKindRnnState = 6,    // RNN head: state update before each draft step
   kKindVerifyEmit = 7,  // stage 2 of the draw and the emitted tokens
-  kKindCount = 8
+  kKindAppend = 8,      // new K and V written to the paged cache
+  kKindAttention = 9,   // attention over the paged cache, with its combine
+  kKindPages = 10,      // page tables, counts and page copies
+  kKindLogprobs = 11,   // token log-probabilities
+  kKindCount = 12
 };
 
 }  // namespace dspark

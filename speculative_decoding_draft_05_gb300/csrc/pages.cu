@@ -1,0 +1,726 @@
+// pages.cu -- writing new tokens' K and V into the paged cache, and the
+// management of its pages: reserving and freeing (resize), forking, compacting,
+// copying.
+//
+// The tables (page table, lengths, reference counts) are small next to the
+// cache; what costs there is latency, so each operation is one kernel of one
+// thread-block cluster (8 CTAs x 1024 threads, phases separated by the
+// hardware's cluster barrier) instead of a chain of launches.  Which page an
+// allocation takes depends on nothing but the inputs: the lowest free ids, in
+// the order of the requests, found by a prefix sum over the counts.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "serving.h"
+
+namespace cg = cooperative_groups;
+
+namespace dspark {
+
+namespace {
+
+constexpr int kClusterCtas = 8;
+constexpr int kPageThreads = 1024;
+constexpr int kPageWarps = kPageThreads / 32;
+
+// Counter words at the start of the workspace (the status word is word 0).
+enum { kCtrStatus = 0, kCtrNeed = 1, kCtrCopies = 2, kCtrFreed = 3, kCtrWords = 4 };
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ int warp_sum_int(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ int warp_scan_incl(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Exclusive prefix of v over the CTA's threads; *total gets the sum.  Uses
+// sm[0 .. kPageWarps].
+__device__ __forceinline__ int block_scan_excl(int v, int* sm, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int incl = warp_scan_incl(v);
+  if (lane == 31) sm[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = sm[lane];
+    const int wi = warp_scan_incl(w);
+    sm[lane] = wi - w;
+    if (lane == 31) sm[kPageWarps] = wi;
+  }
+  __syncthreads();
+  const int r = sm[warp] + incl - v;
+  *total = sm[kPageWarps];
+  __syncthreads();
+  return r;
+}
+
+// A warp's contiguous share of the pages, in cluster order (CTA rank, warp).
+__device__ __forceinline__ void page_share(int n_pages, int rank, int& lo, int& hi) {
+  const int warps = kClusterCtas * kPageWarps;
+  const int per = ceil_div(ceil_div(n_pages, warps), 32) * 32;
+  const long long a = (long long)(rank * kPageWarps + (threadIdx.x >> 5)) * per;
+  lo = a < n_pages ? (int)a : n_pages;
+  hi = a + per < n_pages ? (int)(a + per) : n_pages;
+}
+
+// Counts per warp -> this warp's exclusive prefix over the whole cluster and
+// the cluster's total.  Ends with a cluster barrier, so that it can be called
+// again; all threads of the cluster call it.
+__device__ __forceinline__ int cluster_prefix(cg::cluster_group& cl, int warp_count, int* sm,
+                                              int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) sm[warp] = warp_count;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = sm[lane];
+    const int wi = warp_scan_incl(w);
+    sm[lane] = wi - w;
+    if (lane == 31) sm[kPageWarps] = wi;  // this CTA's total
+  }
+  cl.sync();
+  int before = 0, all = 0;
+  const int rank = (int)cl.block_rank();
+  for (int c = 0; c < kClusterCtas; ++c) {
+    const int t = *cl.map_shared_rank(&sm[kPageWarps], c);
+    all += t;
+    if (c < rank) before += t;
+  }
+  const int r = before + sm[warp];
+  *total = all;
+  cl.sync();
+  return r;
+}
+
+// Counts the pages of [lo, hi) for which pred(p) holds, by one warp.
+template <typename Pred>
+__device__ __forceinline__ int warp_count(int lo, int hi, Pred pred) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+#pragma unroll 4
+  for (int p = lo + lane; p < hi; p += 32) n += pred(p) ? 1 : 0;
+  return warp_sum_int(n);
+}
+
+// Calls put(rank, p) for the pages of [lo, hi) with pred(p), in order, ranks
+// from `at`, as long as rank < most.
+template <typename Pred, typename Put>
+__device__ __forceinline__ void warp_list(int lo, int hi, int at, int most, Pred pred, Put put) {
+  const int lane = threadIdx.x & 31;
+  for (int b = lo; b < hi && at < most; b += 32) {
+    const int p = b + lane;
+    const bool y = p < hi && pred(p);
+    const unsigned m = __ballot_sync(0xffffffffu, y);
+    const int r = at + __popc(m & ((1u << lane) - 1u));
+    if (y && r < most) put(r, p);
+    at += __popc(m);
+  }
+}
+
+__device__ __forceinline__ int clamp_len(int n, int most, int* status) {
+  if (n < 0 || n > most) {
+    flag_status(status, DSPARK_DEV_BAD_INPUT);
+    return n < 0 ? 0 : most;
+  }
+  return n;
+}
+
+struct ResizeArgs {
+  PageMeta m;
+  const int32_t* new_len;
+  int32_t* free_pages;
+  int* ctr;     // counter words
+  int* start;   // [R]: first allocation of the request, bit 31: it copies a shared page
+  int* list;    // [n_pages]: the lowest free pages in order
+  int* src;     // [R] copy list
+  int* dst;
+};
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
+pages_resize_kernel(const ResizeArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int sm[kPageWarps + 1];
+  const int rank = (int)cl.block_rank();
+  const int lane = threadIdx.x & 31;
+  const int gwarp = rank * kPageWarps + (threadIdx.x >> 5), warps = kClusterCtas * kPageWarps;
+  const PageMeta& m = a.m;
+  const int S = m.page_size, P = m.max_pages;
+  const long long most_l = (long long)P * S;
+  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  int* const rc = m.refcount_out;
+  int* const status = a.ctr + kCtrStatus;
+
+  // 1. Pages past the new length lose a reference.
+  for (int r = gwarp; r < m.R; r += warps) {
+    const int L = clamp_len(m.kv_len[r], most, status), N = clamp_len(a.new_len[r], most, status);
+    int32_t* row = m.table_out + (size_t)r * P;
+    for (int j = ceil_div(N, S) + lane; j < ceil_div(L, S); j += 32) {
+      const int p = row[j];
+      if (p < 0 || p >= m.n_pages)
+        flag_status(status, DSPARK_DEV_BAD_INPUT);
+      else
+        atomicSub(&rc[p], 1);
+      row[j] = -1;
+    }
+  }
+  cl.sync();
+
+  // 2. Free pages of this warp's share; the requests' needs, in order, by CTA 0.
+  int lo, hi;
+  page_share(m.n_pages, rank, lo, hi);
+  const auto is_free = [&](int p) { return __ldcg(&rc[p]) == 0; };
+  const int mine = warp_count(lo, hi, is_free);
+  if (rank == 0) {
+    int base = 0;
+    for (int r0 = 0; r0 < m.R; r0 += kPageThreads) {
+      const int r = r0 + (int)threadIdx.x;
+      int need = 0, cow = 0;
+      if (r < m.R) {
+        const int L = clamp_len(m.kv_len[r], most, status), N = clamp_len(a.new_len[r], most, status);
+        if (N > L) {
+          if (L % S != 0) {
+            const int p = m.table_out[(size_t)r * P + L / S];
+            if (p < 0 || p >= m.n_pages)
+              flag_status(status, DSPARK_DEV_BAD_INPUT);
+            else
+              cow = __ldcg(&rc[p]) > 1 ? 1 : 0;
+          }
+          need = cow + ceil_div(N, S) - ceil_div(L, S);
+        }
+      }
+      int total;
+      const int at = block_scan_excl(need, sm, &total);
+      if (r < m.R) a.start[r] = (int)((unsigned)(base + at) | (cow ? 0x80000000u : 0u));
+      base += total;
+    }
+    if (threadIdx.x == 0) a.ctr[kCtrNeed] = base;
+  }
+  int n_free;
+  const int at = cluster_prefix(cl, mine, sm, &n_free);
+  const int need_all = __ldcg(&a.ctr[kCtrNeed]);
+  if (need_all > n_free && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
+
+  // 3. The lowest free pages, as many as are wanted.
+  warp_list(lo, hi, at, need_all, is_free, [&](int i, int p) { a.list[i] = p; });
+  cl.sync();
+
+  // 4. Each request takes its share of the list.
+  for (int r = gwarp; r < m.R; r += warps) {
+    const int L = clamp_len(m.kv_len[r], most, status), N = clamp_len(a.new_len[r], most, status);
+    int out_len = N;
+    if (N > L) {
+      const unsigned st = (unsigned)__ldcg(&a.start[r]);
+      const int cow = (int)(st >> 31), first = (int)(st & 0x7fffffffu);
+      const int old = ceil_div(L, S), need = cow + ceil_div(N, S) - old;
+      int got = n_free - first;
+      got = got < 0 ? 0 : got > need ? need : got;
+      if (cow && got == 0) {
+        out_len = L;
+      } else {
+        const int grown = got - cow;
+        int32_t* row = m.table_out + (size_t)r * P;
+        for (int j = lane; j < grown; j += 32) {
+          const int p = __ldcg(&a.list[first + cow + j]);
+          row[old + j] = p;
+          rc[p] = 1;
+        }
+        if (cow && lane == 0) {
+          const int from = row[L / S], to = __ldcg(&a.list[first]);
+          row[L / S] = to;
+          rc[to] = 1;
+          if (atomicSub(&rc[from], 1) == 1) atomicAdd(&a.ctr[kCtrFreed], 1);
+          const int i = atomicAdd(&a.ctr[kCtrCopies], 1);
+          a.src[i] = from;
+          a.dst[i] = to;
+        }
+        const long long room = (long long)(old + grown) * S;
+        out_len = room < N ? (int)room : N;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) m.kv_len_out[r] = out_len;
+  }
+  cl.sync();
+  if (rank == 0 && threadIdx.x == 0)
+    *a.free_pages = n_free - (need_all < n_free ? need_all : n_free) + __ldcg(&a.ctr[kCtrFreed]);
+}
+
+struct ForkArgs {
+  PageMeta m;
+  const int32_t *parent, *child;
+  int n;
+  int32_t* free_pages;
+  int* ctr;
+  int* start;  // [n <= R]: first allocation, bit 31: a partly filled page is copied; -1 skipped
+  int* len;    // [n] the parent's length
+  int* list;
+  int* src;
+  int* dst;
+};
+
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
+pages_fork_kernel(const ForkArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int sm[kPageWarps + 1];
+  const int rank = (int)cl.block_rank();
+  const int lane = threadIdx.x & 31;
+  const int gthread = rank * kPageThreads + (int)threadIdx.x;
+  const int gwarp = rank * kPageWarps + (threadIdx.x >> 5), warps = kClusterCtas * kPageWarps;
+  const PageMeta& m = a.m;
+  const int S = m.page_size, P = m.max_pages;
+  const long long most_l = (long long)P * S;
+  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  int* const rc = m.refcount_out;
+  int* const status = a.ctr + kCtrStatus;
+  int* const owner = a.dst;  // [R], before dst is written: the first pair that names a child
+
+  for (int r = gthread; r < m.R; r += kClusterCtas * kPageThreads) owner[r] = 0x7fffffff;
+  cl.sync();
+  for (int i = gthread; i < a.n; i += kClusterCtas * kPageThreads) {
+    const int c = a.child[i];
+    if (c >= 0 && c < m.R) atomicMin(&owner[c], i);
+  }
+  int lo, hi;
+  page_share(m.n_pages, rank, lo, hi);
+  const auto is_free = [&](int p) { return __ldcg(&rc[p]) == 0; };
+  const int mine = warp_count(lo, hi, is_free);
+  cl.sync();
+
+  // The pairs' needs, in order, by CTA 0.  A pair whose child holds pages, is
+  // named twice or is out of range is skipped and flagged.
+  if (rank == 0) {
+    int base = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kPageThreads) {
+      const int i = i0 + (int)threadIdx.x;
+      int need = 0, L = -1;
+      if (i < a.n) {
+        const int p = a.parent[i], c = a.child[i];
+        const bool ok = p >= 0 && p < m.R && c >= 0 && c < m.R && m.kv_len[c] == 0 &&
+                        __ldcg(&owner[c]) == i;
+        if (ok) {
+          L = clamp_len(m.kv_len[p], most, status);
+          need = L % S != 0 ? 1 : 0;
+          if (need) {
+            const int q = m.table[(size_t)p * P + L / S];
+            if (q < 0 || q >= m.n_pages) {
+              flag_status(status, DSPARK_DEV_BAD_INPUT);
+              L = L / S * S;
+              need = 0;
+            }
+          }
+        } else {
+          flag_status(status, DSPARK_DEV_BAD_INPUT);
+        }
+      }
+      int total;
+      const int at = block_scan_excl(need, sm, &total);
+      if (i < a.n) {
+        a.start[i] = base + at;
+        a.len[i] = L;
+      }
+      base += total;
+    }
+    if (threadIdx.x == 0) a.ctr[kCtrNeed] = base;
+  }
+  int n_free;
+  const int at = cluster_prefix(cl, mine, sm, &n_free);
+  const int need_all = __ldcg(&a.ctr[kCtrNeed]);
+  if (need_all > n_free && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
+  warp_list(lo, hi, at, need_all, is_free, [&](int i, int p) { a.list[i] = p; });
+  cl.sync();
+
+  for (int i = gwarp; i < a.n; i += warps) {
+    const int L = __ldcg(&a.len[i]);
+    if (L < 0) continue;
+    const int32_t* from = m.table_out + (size_t)a.parent[i] * P;
+    int32_t* to = m.table_out + (size_t)a.child[i] * P;
+    const int full = L / S;
+    for (int j = lane; j < full; j += 32) {
+      const int p = from[j];
+      if (p < 0 || p >= m.n_pages)
+        flag_status(status, DSPARK_DEV_BAD_INPUT);
+      else
+        atomicAdd(&rc[p], 1);
+      to[j] = p;
+    }
+    if (lane == 0) {
+      int out_len = full * S;
+      if (L % S != 0) {
+        const int k = __ldcg(&a.start[i]);
+        if (k < n_free) {
+          const int p = __ldcg(&a.list[k]);
+          to[full] = p;
+          rc[p] = 1;
+          const int s = atomicAdd(&a.ctr[kCtrCopies], 1);
+          a.src[s] = from[full];
+          a.dst[s] = p;
+          out_len = L;
+        }
+      }
+      m.kv_len_out[a.child[i]] = out_len;
+    }
+  }
+  if (rank == 0 && threadIdx.x == 0)
+    *a.free_pages = n_free - (need_all < n_free ? need_all : n_free);
+}
+
+struct CompactArgs {
+  PageMeta m;
+  int32_t* page_map;
+  int32_t* n_live;
+  int* ctr;
+  int* src;
+  int* dst;
+};
+
+// Lists the moves: the i-th live page with id >= n_live goes to the i-th free
+// id < n_live, where n_live is the number of live pages.
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
+pages_compact_kernel(const CompactArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ int sm[kPageWarps + 1];
+  const int rank = (int)cl.block_rank();
+  const int lane = threadIdx.x & 31;
+  const PageMeta& m = a.m;
+  const int32_t* rc = m.refcount;
+  int lo, hi, n_live, moves, n_low;
+  page_share(m.n_pages, rank, lo, hi);
+  cluster_prefix(cl, warp_count(lo, hi, [&](int p) { return rc[p] > 0; }), sm, &n_live);
+  const auto high = [&](int p) { return p >= n_live && rc[p] > 0; };
+  const auto low = [&](int p) { return p < n_live && rc[p] <= 0; };
+  const int at_high = cluster_prefix(cl, warp_count(lo, hi, high), sm, &moves);
+  const int at_low = cluster_prefix(cl, warp_count(lo, hi, low), sm, &n_low);
+  warp_list(lo, hi, at_high, moves, high, [&](int i, int p) { a.src[i] = p; });
+  warp_list(lo, hi, at_low, n_low, low, [&](int i, int p) { a.dst[i] = p; });
+  for (int p = lo + lane; p < hi; p += 32)
+    if (!high(p)) a.page_map[p] = rc[p] > 0 ? p : -1;
+  cl.sync();
+  for (int i = rank * kPageThreads + (int)threadIdx.x; i < moves; i += kClusterCtas * kPageThreads) {
+    const int s = __ldcg(&a.src[i]), d = __ldcg(&a.dst[i]);
+    a.page_map[s] = d;
+    m.refcount_out[d] = rc[s];
+    m.refcount_out[s] = 0;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    *a.n_live = n_live;
+    a.ctr[kCtrCopies] = moves;
+  }
+}
+
+__global__ void __launch_bounds__(256)
+table_map_kernel(const PageMeta m, const int32_t* page_map, int* status) {
+  const size_t n = (size_t)m.R * m.max_pages;
+  const long long most_l = (long long)m.max_pages * m.page_size;
+  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (size_t)gridDim.x * blockDim.x) {
+    const int r = (int)(i / m.max_pages), j = (int)(i - (size_t)r * m.max_pages);
+    int p = m.table[i];
+    const int L = clamp_len(m.kv_len[r], most, status);
+    if (j < ceil_div(L, m.page_size)) {
+      const int q = p >= 0 && p < m.n_pages ? page_map[p] : -1;
+      if (q < 0)
+        flag_status(status, DSPARK_DEV_BAD_INPUT);
+      else
+        p = q;
+    }
+    m.table_out[i] = p;
+  }
+}
+
+// Copies the tables into the outputs where those are arrays of their own.
+struct MetaCopy {
+  const int32_t* from[3];
+  int32_t* to[3];
+  size_t n[3];
+};
+__global__ void __launch_bounds__(256) meta_copy_kernel(const MetaCopy c) {
+  const size_t t = (size_t)blockIdx.x * blockDim.x + threadIdx.x, T = (size_t)gridDim.x * blockDim.x;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (c.from[k] == c.to[k]) continue;
+    const bool vec = (((uintptr_t)c.from[k] | (uintptr_t)c.to[k]) & 15u) == 0;
+    const size_t n4 = vec ? c.n[k] / 4 : 0;
+    for (size_t i = t; i < n4; i += T) ((int4*)c.to[k])[i] = ((const int4*)c.from[k])[i];
+    for (size_t i = 4 * n4 + t; i < c.n[k]; i += T) c.to[k][i] = c.from[k][i];
+  }
+}
+
+cudaError_t copy_meta(const PageMeta& m, bool table, bool len, bool counts, cudaStream_t s) {
+  MetaCopy c;
+  c.from[0] = m.table, c.to[0] = table ? m.table_out : (int32_t*)m.table;
+  c.n[0] = (size_t)m.R * m.max_pages;
+  c.from[1] = m.kv_len, c.to[1] = len ? m.kv_len_out : (int32_t*)m.kv_len, c.n[1] = (size_t)m.R;
+  c.from[2] = m.refcount, c.to[2] = counts ? m.refcount_out : (int32_t*)m.refcount;
+  c.n[2] = (size_t)m.n_pages;
+  size_t most = 0;
+  for (int k = 0; k < 3; ++k)
+    if (c.from[k] != c.to[k] && c.n[k] > most) most = c.n[k];
+  if (most == 0) return cudaSuccess;
+  size_t ctas = (most + 1023) / 1024;
+  if (ctas > 608) ctas = 608;
+  meta_copy_kernel<<<(int)ctas, 256, 0, s>>>(c);
+  return cudaGetLastError();
+}
+
+// One page of one layer's K or V per (copy, layer, K/V); 16-byte pieces where a
+// page is one dense block on 16-byte boundaries.
+struct CopyArgs {
+  CacheView c;
+  int layers, esize, n_max;
+  long long layer_stride;
+  const int32_t *src, *dst;
+  const int* count;
+  int* status;
+};
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;  // 16-byte loads in flight a thread
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_dense_kernel(const CopyArgs a) {
+  int n = a.count ? *a.count : a.n_max;
+  n = n < a.n_max ? n : a.n_max;
+  const int vecs = (int)((size_t)a.c.page_size * a.c.heads * a.c.head_dim * a.esize / 16);
+  const int piece = kCopyThreads * kCopyUnroll;
+  const int pieces = (vecs + piece - 1) / piece;
+  const long long units = (long long)n * 2 * a.layers * pieces;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int pc = (int)(u % pieces);
+    long long w = u / pieces;
+    const bool is_v = w & 1;
+    w >>= 1;
+    const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
+    const int s = a.src[i], d = a.dst[i];
+    if (s < 0 || s >= a.c.n_pages || d < 0 || d >= a.c.n_pages) {
+      if (threadIdx.x == 0) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
+      continue;
+    }
+    char* base = (char*)(is_v ? a.c.v : a.c.k);
+    const uint4* from =
+        (const uint4*)(base + (layer * a.layer_stride + s * a.c.page_stride) * a.esize);
+    uint4* to = (uint4*)(base + (layer * a.layer_stride + d * a.c.page_stride) * a.esize);
+    const int v0 = pc * piece + (int)threadIdx.x;
+    uint4 x[kCopyUnroll];
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k)
+      if (v0 + k * kCopyThreads < vecs) x[k] = __ldcs(&from[v0 + k * kCopyThreads]);
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k)
+      if (v0 + k * kCopyThreads < vecs) __stcs(&to[v0 + k * kCopyThreads], x[k]);
+  }
+}
+
+// Any strides: element by element, the head dimension over the lanes.
+template <typename E>
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(const CopyArgs a) {
+  int n = a.count ? *a.count : a.n_max;
+  n = n < a.n_max ? n : a.n_max;
+  const int rows = a.c.page_size * a.c.heads;
+  const long long units = (long long)n * 2 * a.layers * rows;
+  const int lane = threadIdx.x & 31;
+  for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < units;
+       u += (long long)gridDim.x * (kCopyThreads / 32)) {
+    const int row = (int)(u % rows);
+    long long w = u / rows;
+    const bool is_v = w & 1;
+    w >>= 1;
+    const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
+    const int s = a.src[i], d = a.dst[i];
+    if (s < 0 || s >= a.c.n_pages || d < 0 || d >= a.c.n_pages) {
+      if (lane == 0) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
+      continue;
+    }
+    E* base = (E*)(is_v ? a.c.v : a.c.k) + layer * a.layer_stride +
+              (row / a.c.heads) * a.c.token_stride + (row % a.c.heads) * a.c.head_stride;
+    const E* from = base + s * a.c.page_stride;
+    E* to = base + d * a.c.page_stride;
+    for (int e = lane; e < a.c.head_dim; e += 32) to[e] = from[e];
+  }
+}
+
+// ------------------------------------------------------------------ append
+struct AppendArgs {
+  CacheView c;
+  ChunkArgs a;
+  const void *k_new, *v_new;
+  long long tok_stride, head_stride;  // of the new rows
+  int* status;
+};
+
+// The request whose chunk holds token t: the largest r with q_offsets[r] <= t
+// (later empty requests have larger offsets or follow it with the same one).
+// 32 probes a step: two dependent loads for up to 1024 requests.
+__device__ __forceinline__ int find_request(const int32_t* off, int R, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = R;  // off[lo] <= t (taken as given for lo = 0), off[hi] > t
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + (lane + 1) * step;
+    const bool le = i < hi && off[i] <= t;
+    const int k = __popc(__ballot_sync(0xffffffffu, le));
+    const int nlo = lo + k * step;
+    const int nhi = nlo + step;
+    lo = nlo;
+    hi = nhi < hi ? nhi : hi;
+  }
+  return lo;
+}
+
+// One warp a token: VE elements (16 bytes, or one where alignment does not allow) a lane and step.
+template <typename E, int VE>
+__global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
+  struct alignas(sizeof(E) * VE) Vec {
+    E e[VE];
+  };
+  const int lane = threadIdx.x & 31;
+  const int S = p.c.page_size;
+  const int per_head = p.c.head_dim / VE, n = p.c.heads * per_head;
+  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.a.n_tokens; t += gridDim.x * 8) {
+    const int r = find_request(p.a.q_offsets, p.a.R, t);
+    const int end = p.a.q_offsets[r + 1];
+    const long long pos = (long long)p.a.kv_len[r] - end + t;
+    long long slot = pos / S;
+    int page = -1;
+    if (t >= p.a.q_offsets[r] && t < end && pos >= 0 && slot < p.a.max_pages)
+      page = p.a.page_table[(size_t)r * p.a.max_pages + slot];
+    if (page < 0 || page >= p.c.n_pages) {
+      // (rows past the last request's are padding, not an error)
+      if (lane == 0 && t < p.a.q_offsets[p.a.R]) flag_status(p.status, DSPARK_DEV_BAD_INPUT);
+      continue;
+    }
+    const long long dst0 = page * p.c.page_stride + (pos - slot * S) * p.c.token_stride;
+    const E* kn = (const E*)p.k_new + t * p.tok_stride;
+    const E* vn = (const E*)p.v_new + t * p.tok_stride;
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) {
+      const int h = i / per_head, d = (i - h * per_head) * VE;
+      const Vec kx = *(const Vec*)(kn + h * p.head_stride + d);
+      const Vec vx = *(const Vec*)(vn + h * p.head_stride + d);
+      *(Vec*)((E*)p.c.k + dst0 + h * p.c.head_stride + d) = kx;
+      *(Vec*)((E*)p.c.v + dst0 + h * p.c.head_stride + d) = vx;
+    }
+  }
+}
+
+bool dense_page(const CacheView& c) {
+  const long long D = c.head_dim;
+  const bool thd = (c.heads == 1 || c.head_stride == D) &&
+                   (c.page_size == 1 || c.token_stride == c.heads * D);
+  const bool htd = (c.page_size == 1 || c.token_stride == D) &&
+                   (c.heads == 1 || c.head_stride == c.page_size * D);
+  return thd || htd;
+}
+
+}  // namespace
+
+PagesWorkspace pages_workspace_layout(int R, int n_pages) {
+  PagesWorkspace w;
+  const size_t lists = (size_t)(R > n_pages ? R : n_pages) * sizeof(int);
+  w.counters = 0;
+  w.start = 256;
+  w.owner = align_up256(w.start + (size_t)R * sizeof(int));
+  w.list = align_up256(w.owner + (size_t)R * sizeof(int));
+  w.src = align_up256(w.list + (size_t)n_pages * sizeof(int));
+  w.dst = align_up256(w.src + lists);
+  w.total = align_up256(w.dst + lists);
+  return w;
+}
+
+cudaError_t launch_pages_resize(const PageMeta& m, const int32_t* new_len, int32_t* free_pages,
+                                char* ws, const PagesWorkspace& w, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(ws + w.counters, 0, kCtrWords * sizeof(int), s);
+  if (e == cudaSuccess) e = copy_meta(m, true, false, true, s);
+  if (e != cudaSuccess) return e;
+  ResizeArgs a{m, new_len, free_pages, (int*)(ws + w.counters), (int*)(ws + w.start),
+               (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst)};
+  pages_resize_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PageMeta& m, const int32_t* parent, const int32_t* child, int n,
+                              int32_t* free_pages, char* ws, const PagesWorkspace& w,
+                              cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(ws + w.counters, 0, kCtrWords * sizeof(int), s);
+  if (e == cudaSuccess) e = copy_meta(m, true, true, true, s);
+  if (e != cudaSuccess) return e;
+  ForkArgs a{m, parent, child, n, free_pages, (int*)(ws + w.counters), (int*)(ws + w.start),
+             (int*)(ws + w.owner), (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst)};
+  pages_fork_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PageMeta& m, int32_t* page_map, int32_t* n_live, char* ws,
+                                 const PagesWorkspace& w, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(ws + w.counters, 0, kCtrWords * sizeof(int), s);
+  if (e == cudaSuccess) e = copy_meta(m, false, false, true, s);
+  if (e != cudaSuccess) return e;
+  CompactArgs a{m, page_map, n_live, (int*)(ws + w.counters), (int*)(ws + w.src),
+                (int*)(ws + w.dst)};
+  pages_compact_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  size_t ctas = ((size_t)m.R * m.max_pages + 255) / 256;
+  if (ctas > 1216) ctas = 1216;
+  table_map_kernel<<<(int)ctas, 256, 0, s>>>(m, page_map, (int*)ws);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_copy(const CacheView& c, int esize, int layers, long long layer_stride,
+                              const int32_t* src, const int32_t* dst, const int* count, int n_max,
+                              int* status, cudaStream_t s) {
+  if (n_max <= 0) return cudaSuccess;
+  CopyArgs a{c, layers, esize, n_max, layer_stride, src, dst, count, status};
+  const size_t page_bytes = (size_t)c.page_size * c.heads * c.head_dim * esize;
+  const bool vec = dense_page(c) && page_bytes % 16 == 0 && (c.page_stride * esize) % 16 == 0 &&
+                   (layer_stride * esize) % 16 == 0 && (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) == 0;
+  long long units = vec ? (long long)n_max * 2 * layers *
+                              ((page_bytes / 16 + kCopyThreads * kCopyUnroll - 1) /
+                               (kCopyThreads * kCopyUnroll))
+                        : ((long long)n_max * 2 * layers * c.page_size * c.heads + 7) / 8;
+  const int ctas = (int)(units < 1216 ? units : 1216);
+  if (vec)
+    pages_copy_dense_kernel<<<ctas, kCopyThreads, 0, s>>>(a);
+  else if (esize == 2)
+    pages_copy_rows_kernel<uint16_t><<<ctas, kCopyThreads, 0, s>>>(a);
+  else
+    pages_copy_rows_kernel<uint32_t><<<ctas, kCopyThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new, const void* v_new,
+                                long long new_token_stride, long long new_head_stride,
+                                const ChunkArgs& a, int* status, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), s);
+  if (e != cudaSuccess || a.n_tokens == 0) return e;
+  AppendArgs p{c, a, k_new, v_new, new_token_stride, new_head_stride, status};
+  const int ve = 16 / esize;
+  const bool vec = c.head_dim % ve == 0 && c.page_stride % ve == 0 && c.token_stride % ve == 0 &&
+                   c.head_stride % ve == 0 && new_token_stride % ve == 0 &&
+                   new_head_stride % ve == 0 &&
+                   (((uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)k_new | (uintptr_t)v_new) & 15u) == 0;
+  int ctas = (a.n_tokens + 7) / 8;
+  if (ctas > 1216) ctas = 1216;
+  if (esize == 2) {
+    if (vec)
+      cache_append_kernel<uint16_t, 8><<<ctas, 256, 0, s>>>(p);
+    else
+      cache_append_kernel<uint16_t, 1><<<ctas, 256, 0, s>>>(p);
+  } else {
+    if (vec)
+      cache_append_kernel<uint32_t, 4><<<ctas, 256, 0, s>>>(p);
+    else
+      cache_append_kernel<uint32_t, 1><<<ctas, 256, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace dspark

@@ -1,0 +1,92 @@
+// serving.h -- host-side launchers of the serving operators (paged K/V cache,
+// attention over it, page management, token log-probabilities), internal to
+// libdspark.so.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/dspark.h"
+
+namespace dspark {
+
+// Shared by the C-ABI files (defined in api.cu).
+int cuda_fail(cudaError_t e, const char* where);
+int unsupported(const char* why);  // sets dspark_last_error's text
+void prof_begin(int kind, cudaStream_t s);
+void prof_end(cudaStream_t s);
+
+inline size_t align_up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// One layer's K and V (or, for page copies, layer 0's) as kernels see them.
+// Strides in elements; K and V share them.
+struct CacheView {
+  void* k;
+  void* v;
+  int n_pages, page_size, heads, head_dim;
+  long long page_stride, token_stride, head_stride;
+};
+
+// The chunk of new tokens and the lengths of a call.
+struct ChunkArgs {
+  const int32_t* q_offsets;   // [R + 1]
+  const int32_t* kv_len;      // [R]
+  const int32_t* page_table;  // [R, max_pages]
+  int R, n_tokens, max_pages;
+};
+
+cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new, const void* v_new,
+                                long long new_token_stride, long long new_head_stride,
+                                const ChunkArgs& a, int* status, cudaStream_t s);
+
+// Page management.  Workspace (byte offsets, 256-aligned): counters (status
+// word first), per-request or per-pair scratch, the free list and copy list.
+struct PagesWorkspace {
+  size_t counters, start, owner, list, src, dst, total;
+};
+PagesWorkspace pages_workspace_layout(int R, int n_pages);
+
+struct PageMeta {
+  const int32_t *table, *kv_len, *refcount;
+  int32_t *table_out, *kv_len_out, *refcount_out;
+  int R, max_pages, n_pages, page_size;
+};
+cudaError_t launch_pages_resize(const PageMeta& m, const int32_t* new_len, int32_t* free_pages,
+                                char* ws, const PagesWorkspace& w, cudaStream_t s);
+cudaError_t launch_pages_fork(const PageMeta& m, const int32_t* parent, const int32_t* child, int n,
+                              int32_t* free_pages, char* ws, const PagesWorkspace& w,
+                              cudaStream_t s);
+cudaError_t launch_pages_compact(const PageMeta& m, int32_t* page_map, int32_t* n_live, char* ws,
+                                 const PagesWorkspace& w, cudaStream_t s);
+// Copies pages src[i] -> dst[i], i < *count (or n_max where count is null), of
+// K and V in all layers.
+cudaError_t launch_pages_copy(const CacheView& c, int esize, int layers, long long layer_stride,
+                              const int32_t* src, const int32_t* dst, const int* count, int n_max,
+                              int* status, cudaStream_t s);
+
+// Token log-probabilities.
+struct LogprobsWorkspace {
+  size_t count, list, parts, gmax, total;
+};
+LogprobsWorkspace logprobs_workspace_layout(int n_rows, int V);
+cudaError_t launch_logprobs(const void* Z, int dtype, long long row_stride, const int32_t* tokens,
+                            int n_rows, int V, float invT, int top, float* logp, float* entropy,
+                            float* lse, int32_t* top_ids, float* top_logp, char* ws,
+                            const LogprobsWorkspace& w, cudaStream_t s);
+
+// Attention over the paged cache.
+struct AttnArgs {
+  ChunkArgs a;
+  CacheView c;
+  const void* q;
+  long long q_token_stride, q_head_stride;  // elements
+  int Hq, G, dtype;
+  float scale;
+  void* out;    // [n_tokens, Hq, D]
+  float* lse;   // [n_tokens, Hq]
+};
+size_t attention_workspace_bytes(int dtype, int head_dim);
+cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s);
+
+}  // namespace dspark

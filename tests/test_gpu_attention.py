@@ -1,0 +1,343 @@
+"""dspark_paged_attention and dspark_cache_append against the definition in 64 bits.
+
+Tolerances, per output element, from the formulas.  With u = 2^-24, scores of
+the fp32 sums are off by at most ds = (D + 3) u scale sum |q k| (plus the
+rounding of the exponent's argument, 2 u max|s|), so a probability is off by
+the factor e^{+-2 ds}; sums over L keys add (L + 8) u; the bf16 kernel rounds
+each probability (2^-9 relative) and the output (2^-9).  All of it is relative
+to sum_j p_j |v_j|, which the reference computes.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_draft_05_gb300 as dspark
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def make(dtype, chunks, lens, Hq, Hkv, D, page, layout="thd", seed=0, layers=1, spare=2, poison=True):
+    """Random inputs; everything past kv_len in the cache, and unused pages, hold NaN."""
+    g = torch.Generator().manual_seed(seed)
+    R = len(lens)
+    held = [-(-n // page) for n in lens]
+    n_pages = sum(held) + spare
+    P = max(held + [1]) + 1
+    perm = torch.randperm(n_pages, generator=g)
+    table = torch.full((R, P), -1, dtype=torch.int32)
+    at = 0
+    for r, h in enumerate(held):
+        table[r, :h] = perm[at:at + h].int()
+        at += h
+    shape = [layers, n_pages, page, Hkv, D]
+    k, v = (torch.randn(shape, generator=g).to(dtype) for _ in range(2))
+    if poison:
+        live = torch.zeros(n_pages, page, dtype=torch.bool)
+        for r, n in enumerate(lens):
+            for j in range(held[r]):
+                live[table[r, j], : min(page, n - j * page)] = True
+        k[:, ~live] = math.nan
+        v[:, ~live] = math.nan
+    T = sum(chunks)
+    # q is a part of a wider projection, so its rows are strided
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g).to(dtype)
+    dev = "cuda"
+
+    def put(t):
+        if layout == "htd":
+            return t.transpose(2, 3).contiguous().to(dev).transpose(2, 3)
+        return t.to(dev)
+
+    off = torch.tensor(np.concatenate([[0], np.cumsum(chunks)]), dtype=torch.int32)
+    return dict(k=put(k), v=put(v), qkv=qkv.to(dev), q=qkv.to(dev)[:, :Hq], off=off.to(dev),
+                lens=torch.tensor(lens, dtype=torch.int32).to(dev), table=table.to(dev), scale=1 / math.sqrt(D),
+                chunks=chunks, L=lens, Hq=Hq, Hkv=Hkv, D=D, page=page)
+
+
+def reference(i, layer=0):
+    T, Hq, D, G = sum(i["chunks"]), i["Hq"], i["D"], i["Hq"] // i["Hkv"]
+    out, lse = torch.zeros(T, Hq, D, dtype=torch.float64), torch.full((T, Hq), -math.inf, dtype=torch.float64)
+    tol, tol_lse = torch.zeros(T, Hq, D, dtype=torch.float64), torch.zeros(T, Hq, dtype=torch.float64)
+    table, q = i["table"].cpu().long(), i["q"].cpu().double()
+    k, v = i["k"][layer].cpu(), i["v"][layer].cpu()
+    bf = i["k"].dtype == BF16
+    t = 0
+    for r, (n, L) in enumerate(zip(i["chunks"], i["L"])):
+        pg = table[r, : -(-L // i["page"])]
+        K = k[pg].reshape(-1, i["Hkv"], D)[:L].double()
+        V = v[pg].reshape(-1, i["Hkv"], D)[:L].double()
+        for a in range(n):
+            p = L - n + a
+            if p >= 0:
+                Kh, Vh = (x[: p + 1].repeat_interleave(G, 1) for x in (K, V))
+                s = torch.einsum("hd,jhd->hj", q[t], Kh) * i["scale"]
+                ds = ((D + 3) * U * i["scale"] * torch.einsum("hd,jhd->hj", q[t].abs(), Kh.abs())).amax(1)
+                ds = ds + 2 * U * s.abs().amax(1)
+                lse[t] = torch.logsumexp(s, 1)
+                pr = torch.exp(s - lse[t][:, None])
+                out[t] = torch.einsum("hj,jhd->hd", pr, Vh)
+                mix = torch.einsum("hj,jhd->hd", pr, Vh.abs())
+                rel = 4 * ds + (2 * p + 16) * U + (2.0 ** -8 if bf else 0)
+                tol[t] = rel[:, None] * mix + (2.0 ** -9 * out[t].abs() if bf else 0)
+                tol_lse[t] = 2 * ds + (2 * p + 16) * U + 4 * U * lse[t].abs()
+            t += 1
+    return out, lse, tol, tol_lse
+
+
+def check(i, res, layer=0):
+    out, lse, tol, tol_lse = reference(i, layer)
+    got, got_lse = res["out"].cpu().double(), res["lse"].cpu().double()
+    assert not got.isnan().any()
+    bad = (got - out).abs() > tol
+    assert not bad.any(), f"out: {int(bad.sum())} off, worst {(got - out).abs()[bad].max():.3g}"
+    none = torch.isinf(lse)
+    assert (got_lse[none] == -math.inf).all() and (got[none] == 0).all()
+    bad = (got_lse - lse).abs()[~none] > tol_lse[~none]
+    assert not bad.any(), f"lse: {int(bad.sum())} off, worst {(got_lse - lse).abs()[~none][bad].max():.3g}"
+
+
+def attend(i, layer=0, **kw):
+    cache = dspark.PagedCache(i["k"], i["v"])
+    r = dspark.dspark_paged_attention(i["q"], cache, layer, i["off"], i["lens"], i["table"], i["scale"], **kw)
+    assert dspark.dspark_read_device_status(r["workspace"], kw.get("stream")) == 0
+    return r
+
+
+SHAPES = [
+    # chunks, lens, Hq, Hkv, D, page
+    ([1], [1], 1, 1, 64, 16),
+    ([1], [1], 8, 2, 128, 16),
+    ([1, 1, 1], [1, 2, 17], 4, 4, 64, 1),
+    ([1] * 5, [127, 128, 129, 1, 300], 8, 2, 128, 16),
+    ([3, 0, 2], [5, 0, 40], 4, 2, 64, 16),            # a request without tokens
+    ([5, 4], [3, 4], 4, 2, 64, 16),                   # the first two tokens see nothing
+    ([17, 1, 9], [255, 256, 257], 32, 8, 128, 64),
+    ([17, 17], [400, 17], 40, 8, 128, 32),            # 5 query heads a K/V head
+    ([16, 3], [131, 64], 7, 1, 96, 16),
+    ([2, 5], [33, 250], 6, 3, 80, 128),
+    ([4, 4], [70, 513], 16, 1, 128, 256),             # a page longer than a tile
+    ([4, 7], [70, 50], 8, 4, 64, 8),
+    ([2, 3], [65, 100], 4, 2, 40, 24),                # a page size that is no power of two
+    ([2, 1], [65, 34], 4, 2, 256, 16),                # wider than the tensor-core kernel takes
+    ([3, 2], [19, 40], 2, 2, 12, 5),
+    ([300], [300], 8, 1, 128, 64),                    # several row blocks, causal from the start
+    ([129, 40], [700, 40], 16, 2, 64, 16),
+    ([1], [5000], 8, 1, 128, 64),                     # one item over many CTAs
+    ([20], [6001], 32, 2, 128, 16),
+    ([1] * 130, [(7 * r) % 300 + 1 for r in range(130)], 4, 2, 64, 16),
+    ([2] * 700, [(r % 5) + 1 for r in range(700)], 2, 1, 64, 16),  # more requests than threads
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n", range(len(SHAPES)))
+def test_attention_matches_the_definition(dtype, n):
+    i = make(dtype, *SHAPES[n], layout="htd" if n % 2 else "thd", seed=n)
+    check(i, attend(i))
+
+
+def test_attention_of_a_later_layer_and_given_outputs():
+    i = make(BF16, [3, 1], [90, 20], 8, 2, 128, 16, layers=3, seed=5)
+    T = 4
+    out = torch.full((T, 8, 128), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((T, 8), 7.0, device="cuda")
+    r = attend(i, layer=2, out=out, lse=lse)
+    assert r["out"] is out and r["lse"] is lse
+    check(i, r, layer=2)
+
+
+def test_attention_with_large_scores_and_a_growing_maximum():
+    # keys in order of rising score: every tile raises the running maximum
+    for dtype in (F32, BF16):
+        i = make(dtype, [4], [1000], 4, 2, 64, 16, seed=9)
+        ramp = torch.linspace(0, 30, 1008)
+        pages = i["table"][0, :63].long()
+        unit = torch.zeros(64)
+        unit[0] = 1
+        k = (ramp.view(63, 16, 1, 1) * unit).expand(63, 16, 2, 64).to(dtype)
+        i["k"][0][pages] = k.cuda()
+        i["qkv"][:] = 0
+        i["qkv"][:, :, 0] = 16.0
+        check(i, attend(i))
+
+
+def test_padding_rows_are_left_alone():
+    i = make(BF16, [2, 3], [40, 60], 8, 2, 128, 16, seed=11)
+    q = torch.cat([i["q"], torch.full_like(i["q"][:2], math.nan)])
+    out = torch.full((7, 8, 128), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((7, 8), 7.0, device="cuda")
+    cache = dspark.PagedCache(i["k"], i["v"])
+    r = dspark.dspark_paged_attention(q, cache, 0, i["off"], i["lens"], i["table"], i["scale"], out=out, lse=lse)
+    assert dspark.dspark_read_device_status(r["workspace"]) == 0
+    assert (out[5:] == 7).all() and (lse[5:] == 7).all()
+    check(i, dict(out=out[:5], lse=lse[:5]))
+
+
+def test_results_do_not_change_between_calls_or_with_a_used_workspace():
+    i = make(BF16, [17, 1, 5], [3000, 900, 77], 32, 8, 128, 16, seed=12)
+    a = attend(i)
+    ws = torch.randint(0, 255, (a["workspace"].numel(),), dtype=torch.uint8, device="cuda")
+    b = attend(i, workspace=ws)
+    assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_another_stream():
+    i = make(BF16, [17, 1], [600, 90], 32, 8, 128, 16, seed=13)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    r = attend(i, stream=s)
+    s.synchronize()
+    check(i, r)
+
+
+@pytest.mark.parametrize("layout", ["thd", "htd"])
+def test_pools_past_32_bit_offsets(layout):
+    # 2.7 G elements in K and in V; the pages in use are the last ones
+    n_pages, page, Hkv, D = 41000, 64, 8, 128
+    shape = (1, n_pages, page, Hkv, D) if layout == "thd" else (1, n_pages, Hkv, page, D)
+    free, _ = torch.cuda.mem_get_info()
+    if free < 4 * n_pages * page * Hkv * D + (4 << 30):
+        pytest.skip("not enough free device memory")
+    i = make(BF16, [17, 1], [200, 130], 16, Hkv, D, page, seed=14, spare=0)
+    k, v = (torch.empty(shape, dtype=BF16, device="cuda") for _ in range(2))
+    kk, vv = (t if layout == "thd" else t.transpose(2, 3) for t in (k, v))
+    m = i["k"].shape[1]
+    kk[:, -m:] = i["k"]
+    vv[:, -m:] = i["v"]
+    big = dict(i, k=kk, v=vv, table=torch.where(i["table"] >= 0, i["table"] + (n_pages - m), -1).int())
+    r = attend(big)
+    check(i, r)
+
+
+def test_bad_device_inputs_are_flagged_and_stay_in_bounds():
+    i = make(BF16, [2, 3], [40, 60], 8, 2, 128, 16, seed=15, poison=False)
+    cache = dspark.PagedCache(i["k"], i["v"])
+    n_pages = i["k"].shape[1]
+
+    def status(**kw):
+        a = dict(i, **kw)
+        r = dspark.dspark_paged_attention(a["q"], cache, 0, a["off"], a["lens"], a["table"], a["scale"])
+        return dspark.dspark_read_device_status(r["workspace"])
+
+    bad = i["table"].clone()
+    bad[0, 1] = n_pages
+    assert status(table=bad) == 1
+    bad[0, 1] = -1
+    assert status(table=bad) == 1
+    assert status(lens=torch.tensor([40, 1 << 20], dtype=torch.int32, device="cuda")) == 1
+    assert status(lens=torch.tensor([-3, 60], dtype=torch.int32, device="cuda")) == 1
+    assert status(off=torch.tensor([0, 2, 9], dtype=torch.int32, device="cuda")) == 1
+    assert status(off=torch.tensor([0, 4, 2], dtype=torch.int32, device="cuda")) == 1
+    assert status() == 0
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["thd", "htd"])
+@pytest.mark.parametrize("chunks,lens,Hkv,D,page", [
+    ([1], [1], 1, 64, 16), ([17, 0, 1, 5], [17, 3, 40, 64], 8, 128, 16), ([3, 2], [3, 9], 2, 12, 5),
+    ([1] * 300, [r % 7 + 1 for r in range(300)], 2, 64, 4), ([200, 300], [200, 900], 4, 128, 64), ([7], [7], 3, 20, 1),
+])
+def test_append_writes_the_chunk_and_nothing_else(dtype, layout, chunks, lens, Hkv, D, page):
+    i = make(dtype, chunks, lens, Hkv, Hkv, D, page, layout=layout, layers=2, seed=3, poison=False)
+    k0, v0 = i["k"].clone(), i["v"].clone()
+    kn, vn = i["qkv"][:, Hkv:2 * Hkv], i["qkv"][:, 2 * Hkv:]
+    r = dspark.dspark_cache_append(dspark.PagedCache(i["k"], i["v"]), 1, kn, vn, i["off"], i["lens"], i["table"])
+    assert dspark.dspark_read_device_status(r["workspace"]) == 0
+    table, t = i["table"].cpu(), 0
+    for q, (n, L) in enumerate(zip(chunks, lens)):
+        for a in range(n):
+            p = L - n + a
+            pg = int(table[q, p // page])
+            k0[1, pg, p % page] = kn[t]
+            v0[1, pg, p % page] = vn[t]
+            t += 1
+    assert torch.equal(i["k"], k0) and torch.equal(i["v"], v0)
+
+
+def test_append_leaves_out_what_is_out_of_range():
+    i = make(BF16, [4, 2], [2, 30], 2, 2, 64, 16, seed=4, poison=False)
+    k0 = i["k"].clone()
+    kn, vn = i["qkv"][:, 2:4], i["qkv"][:, 4:]
+    cache = dspark.PagedCache(i["k"], i["v"])
+    r = dspark.dspark_cache_append(cache, 0, kn, vn, i["off"], i["lens"], i["table"])  # positions -2, -1
+    assert dspark.dspark_read_device_status(r["workspace"]) == 1
+    t = i["table"].cpu()
+    for row, (q, p) in zip((2, 3, 4, 5), ((0, 0), (0, 1), (1, 28), (1, 29))):
+        k0[0, int(t[q, p // 16]), p % 16] = kn[row]
+    assert torch.equal(i["k"], k0)
+    bad = i["table"].clone()
+    bad[1, 1] = 99
+    r = dspark.dspark_cache_append(cache, 0, kn[4:], vn[4:], torch.tensor([0, 0, 2], dtype=torch.int32, device="cuda"),
+                                   i["lens"], bad)
+    assert dspark.dspark_read_device_status(r["workspace"]) == 1
+    assert torch.equal(i["k"], k0)
+
+
+def test_append_of_unaligned_rows():
+    # rows that start one element off a 16-byte boundary, and a pool that does
+    for dtype in (F32, BF16):
+        i = make(dtype, [3, 4], [20, 9], 2, 2, 64, 16, seed=6, poison=False)
+        flat = torch.zeros(i["k"].numel() + 1, dtype=dtype, device="cuda")
+        flat_v = torch.zeros_like(flat)
+        k, v = flat[1:].view(i["k"].shape), flat_v[1:].view(i["k"].shape)
+        k.copy_(i["k"])
+        v.copy_(i["v"])
+        wide = torch.randn(7, 4 * 64 + 1, device="cuda").to(dtype)
+        kn, vn = wide[:, 1:129].unflatten(1, (2, 64)), wide[:, 129:].unflatten(1, (2, 64))
+        dspark.dspark_cache_append(dspark.PagedCache(k, v), 0, kn, vn, i["off"], i["lens"], i["table"])
+        dspark.dspark_cache_append(dspark.PagedCache(i["k"], i["v"]), 0, kn.contiguous(), vn.contiguous(), i["off"],
+                                   i["lens"], i["table"])
+        assert torch.equal(k, i["k"]) and torch.equal(v, i["v"])
+        i["q"] = wide[:, 1:129].unflatten(1, (2, 64))
+        i["k"], i["v"] = k, v
+        check(i, attend(i))
+
+
+# ------------------------------------------------------------------ refusals
+def test_refusals():
+    i = make(BF16, [2, 3], [40, 60], 8, 2, 128, 16, seed=7)
+    k, v = i["k"], i["v"]
+    with pytest.raises(ValueError):
+        dspark.PagedCache(k, v[:, :-1])
+    with pytest.raises(ValueError):
+        dspark.PagedCache(k, v.transpose(2, 3).contiguous().transpose(2, 3))
+    with pytest.raises(ValueError):
+        dspark.PagedCache(k[0], v[0])
+    with pytest.raises(TypeError):
+        dspark.PagedCache(k.cpu(), v.cpu())
+    with pytest.raises(TypeError):
+        dspark.PagedCache(k.half(), v.half())
+    cache = dspark.PagedCache(k, v)
+    a = dict(q=i["q"], cache=cache, layer=0, q_offsets=i["off"], kv_len=i["lens"], page_table=i["table"], scale=0.1)
+
+    def refused(kind, **kw):
+        with pytest.raises(kind):
+            dspark.dspark_paged_attention(**{**a, **kw})
+
+    refused(TypeError, q=i["q"].float())
+    refused(ValueError, q=i["q"][:, :, :64])
+    refused(dspark.DSparkError, q=i["q"][:, :7])          # not a multiple of the K/V heads
+    refused(dspark.DSparkError, layer=1)
+    refused(dspark.DSparkError, layer=-1)
+    refused(dspark.DSparkError, scale=math.nan)
+    refused(TypeError, kv_len=i["lens"].long())
+    refused(ValueError, kv_len=i["lens"][:1])
+    refused(ValueError, q_offsets=i["off"][:2])
+    refused(ValueError, page_table=i["table"][0])
+    refused(ValueError, page_table=i["table"][:, ::2])
+    refused(ValueError, out=torch.empty(5, 8, 64, dtype=BF16, device="cuda"))
+    refused(TypeError, lse=torch.empty(5, 8, dtype=BF16, device="cuda"))
+    refused(ValueError, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    kn = i["qkv"][:, 8:10]
+    with pytest.raises(ValueError):
+        dspark.dspark_cache_append(cache, 0, kn, kn.contiguous(), i["off"], i["lens"], i["table"])
+    with pytest.raises(ValueError):
+        dspark.dspark_cache_append(cache, 0, i["qkv"][:, :3], i["qkv"][:, :3], i["off"], i["lens"], i["table"])
+    empty = dspark.dspark_paged_attention(i["q"][:0], cache, 0, torch.zeros_like(i["off"]), i["lens"], i["table"], 0.1)
+    assert empty["out"].shape == (0, 8, 128)
