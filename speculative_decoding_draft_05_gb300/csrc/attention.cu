@@ -38,8 +38,9 @@ attention_simt_kernel(const AttnParams p) {
   const int S = p.a.c.page_size, G = p.a.G;
 
   attn_plan<kMR, kTN>(p, &st);
-  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, st);
-  if (threadIdx.x == 0) attn_write_cut(p, w);
+  long long u0;
+  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, st, &u0);
+  if (threadIdx.x == 0) attn_write_cut(p, w, u0);
 
   for (; !w.done(); w.next()) {
     const int rows = w.block_rows(), row0 = w.m * kMR;
@@ -251,13 +252,15 @@ cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStrea
 
 size_t attention_workspace_bytes(int dtype, int head_dim) {
   const size_t simt = attn_workspace_layout(kMR, head_dim).total;
-  (void)dtype;
-  return simt;
+  if (dtype != DSPARK_BF16 || head_dim > 128) return simt;
+  const size_t tc = attention_tc_workspace_bytes(head_dim);
+  return tc > simt ? tc : simt;
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
   if (e != cudaSuccess || a.a.n_tokens == 0) return e;
+  if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
   AttnParams p{a, (int*)ws, (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
                (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f};

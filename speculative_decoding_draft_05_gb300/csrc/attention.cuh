@@ -111,59 +111,38 @@ template <int MR, int TN>
 struct AttnWalk {
   const AttnParams* p;
   AttnRequest q;
-  int r, m, h;           // current item
-  int end, n_tiles;      // its keys and tiles
-  long long u0;          // its first unit
-  long long u, stop;     // next unit, end of the share
+  int r, m, h;       // current item: request, row block, K/V head
+  int end, n_tiles;  // its keys and tiles
+  int t0;            // first tile of the current piece
+  int left;          // units of the share from t0 on
 
-  // Places the walk at the item that holds unit `u`, given the request r that
-  // holds it and that request's first unit.
-  __device__ __forceinline__ void seek(int request, long long first) {
-    const int G = p->a.G, Hkv = p->a.c.heads;
-    r = request;
-    q = attn_request(p->a.a, p->a.c.page_size, r, p->status);
-    u0 = first;
-    m = 0;
-    for (;;) {
-      end = attn_item_end<MR>(q, G, m);
-      n_tiles = attn_tiles<TN>(end);
-      if (u < u0 + (long long)n_tiles * Hkv || (long long)(m + 1) * MR >= (long long)q.n * G) break;
-      u0 += (long long)n_tiles * Hkv;
-      ++m;
-    }
-    h = (int)((u - u0) / n_tiles);
-    u0 += (long long)h * n_tiles;
-  }
-
-  __device__ __forceinline__ bool done() const { return u >= stop; }
-  __device__ __forceinline__ int first_tile() const { return (int)(u - u0); }
-  __device__ __forceinline__ int last_tile() const {  // one past the last tile of this share
-    const long long e = stop - u0;
-    return e < n_tiles ? (int)e : n_tiles;
+  __device__ __forceinline__ bool done() const { return left <= 0; }
+  __device__ __forceinline__ int first_tile() const { return t0; }
+  __device__ __forceinline__ int last_tile() const {  // one past the piece's last tile
+    return n_tiles - t0 < left ? n_tiles : t0 + left;
   }
   __device__ __forceinline__ int block_rows() const {
-    const long long left = (long long)q.n * p->a.G - (long long)m * MR;
-    return left < MR ? (int)left : MR;
+    const long long rest = (long long)q.n * p->a.G - (long long)m * MR;
+    return rest < MR ? (int)rest : MR;
   }
 
   __device__ __forceinline__ void next() {
-    u = u0 + last_tile();
+    left -= last_tile() - t0;
     if (done()) return;
-    const int G = p->a.G, Hkv = p->a.c.heads;
-    u0 += n_tiles;
-    if (++h < Hkv) return;
+    t0 = 0;
+    if (++h < p->a.c.heads) return;
     h = 0;
-    if ((long long)(++m) * MR >= (long long)q.n * G) {
+    if ((long long)(++m) * MR >= (long long)q.n * p->a.G) {
       m = 0;
       do {
         if (++r >= p->a.a.R) {  // (not reached: the units count the items)
-          u = stop;
+          left = 0;
           return;
         }
         q = attn_request(p->a.a, p->a.c.page_size, r, p->status);
       } while (q.n == 0);
     }
-    end = attn_item_end<MR>(q, G, m);
+    end = attn_item_end<MR>(q, p->a.G, m);
     n_tiles = attn_tiles<TN>(end);
   }
 };
@@ -226,25 +205,47 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st) {
   __syncthreads();
 }
 
+// The walk over this CTA's share, from its first item; *u0 gets that item's
+// first unit.
 template <int MR, int TN>
-__device__ __forceinline__ AttnWalk<MR, TN> attn_walk(const AttnParams& p, const AttnStart& st) {
+__device__ __forceinline__ AttnWalk<MR, TN> attn_walk(const AttnParams& p, const AttnStart& st,
+                                                      long long* u0) {
   AttnWalk<MR, TN> w;
   w.p = &p;
-  w.u = attn_share(st.units, gridDim.x, blockIdx.x);
-  w.stop = attn_share(st.units, gridDim.x, blockIdx.x + 1);
-  if (!w.done()) w.seek(st.request, st.first);
+  const long long u = attn_share(st.units, gridDim.x, blockIdx.x);
+  w.left = (int)(attn_share(st.units, gridDim.x, blockIdx.x + 1) - u);
+  long long at = st.first;
+  if (w.left > 0) {
+    const int G = p.a.G, Hkv = p.a.c.heads;
+    w.r = st.request;
+    w.q = attn_request(p.a.a, p.a.c.page_size, w.r, p.status);
+    w.m = 0;
+    for (;;) {
+      w.end = attn_item_end<MR>(w.q, G, w.m);
+      w.n_tiles = attn_tiles<TN>(w.end);
+      const long long k = (long long)w.n_tiles * Hkv;
+      if (u < at + k || (long long)(w.m + 1) * MR >= (long long)w.q.n * G) break;
+      at += k;
+      ++w.m;
+    }
+    w.h = (int)((u - at) / w.n_tiles);
+    at += (long long)w.h * w.n_tiles;
+    w.t0 = (int)(u - at);
+  }
+  *u0 = at;
   return w;
 }
 
 // Written once a CTA: whether its share begins inside an item, and which.
 template <int MR, int TN>
-__device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnWalk<MR, TN>& w) {
+__device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnWalk<MR, TN>& w,
+                                               long long u0) {
   CutItem c;
-  c.valid = !w.done() && w.first_tile() > 0;
+  c.valid = !w.done() && w.t0 > 0;
   if (c.valid) {
     c.r = w.r, c.m = w.m, c.h = w.h;
     c.n = w.q.n, c.q0 = w.q.q0, c.rows = w.block_rows(), c.n_tiles = w.n_tiles;
-    c.u0 = w.u0;
+    c.u0 = u0;
   }
   p.cuts[blockIdx.x] = c;
 }

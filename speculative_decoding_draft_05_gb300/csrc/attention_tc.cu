@@ -1,0 +1,793 @@
+// attention_tc.cu -- bf16 attention of a chunk over the paged cache on the
+// 5th-generation tensor cores (sm_103a).
+//
+// Per item (up to 256 rows, the G query heads of a K/V head side by side) and
+// tile of 128 keys: S = Q K^T (128 x 128 x D), the online softmax
+//   m' = max(m, max_j s_j),  p_j = 2^{s_j - m'},  l' = l 2^{m-m'} + sum_j p_j,
+//   O' = O 2^{m-m'} + P V
+// in units of log2, with S and O in TMEM and P (bf16) written over S in TMEM as
+// the first operand of P V.  A larger maximum rescales O and l only when it
+// grew by more than 2^8: until then p_j <= 2^8 stays far inside bf16's and
+// fp32's range, and out = O / l is the same whatever m the two share.
+//
+// Structure (one CTA an SM, persistent over its share of the work):
+//   * warp 8 (producer): TMA of K and V pages into a ring of tiles; each lane
+//     owns one (page, 64-column half) box of a tile, so a tile of 16-token
+//     pages is 16 boxes issued at once.  Page ids are read a group of tiles
+//     ahead.
+//   * warp 9 (MMA): one thread issues tcgen05.mma; S from shared-memory
+//     descriptors, P V with P in TMEM and V as stored ([keys, D]: the N-major
+//     second operand).
+//   * warps 0..3 and 4..7: two softmax streams, one row a thread.  With more
+//     than 128 rows the streams are the two row blocks and share each K/V tile;
+//     with fewer they are the even and the odd tiles of the same rows, and
+//     merge at the end.  While one stream is in its softmax the tensor cores
+//     run the other's products.
+//   * Keys at or past an item's end: pages past it are not loaded, S is
+//     replaced by -inf, and V's rows are overwritten with zeros, since 0 x NaN of
+//     an unused cache slot would reach the sum.
+//   * Every mbarrier wait is bounded; on expiry the CTA flags
+//     DSPARK_DEV_TIMEOUT, drains what it issued, frees TMEM and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "attention.cuh"
+#include "ptx.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kMR = 256;  // rows of an item
+constexpr int kTN = 128;  // keys of a tile
+constexpr int kThreads = 384;  // three warpgroups: two of softmax, one with the producer and MMA warps
+// Registers a thread after the split: 256 x 208 + 128 x 80 of the launch's 384 x 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kTmemCols = 512;  // S0, S1, O0, O1: 128 columns each
+
+// Shared memory for head_dim padded to DP (64 or 128), from a 1024-aligned base.
+template <int DP>
+struct Layout {
+  static constexpr int kHalves = DP / 64;
+  static constexpr int kHalfBytes = 128 * 128;             // 128 rows of 128 bytes
+  static constexpr int kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
+  static constexpr int kStages = DP == 128 ? 5 : 10;
+  static constexpr int kOffQ = 0;  // two row blocks
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 1 + 1 + 1 + 1;
+  static constexpr int kOffStart = kOffBar + ((kBars * 8 + 16 + 15) & ~15);
+  static constexpr int kBytes = kOffStart + (int)sizeof(AttnStart) + 1024;
+};
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem], K = 16.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], K = 16: A is 8 columns of bf16 pairs.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle, version 1.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 operands, A K-major.
+__host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// 32 lanes x 32 columns of 32 bits: thread i gets row i's.  No wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+
+// Two columns (a stream's m and l) to and from TMEM.
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"r"(__float_as_uint(a)),
+               "r"(__float_as_uint(b)), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ float2 tmem_ld2(uint32_t taddr) {
+  uint32_t a, b;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// {hi, lo} rounded to bf16 and packed.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct TcParams {
+  AttnParams p;
+  int box_tokens;  // tokens of a TMA box: min(page_size, 128)
+  int q_vec;       // q rows can be read in 16-byte pieces
+  float sign;      // of the scale; |scale| is in p.scale_log2
+  long long wait_budget;
+};
+
+// Byte offset of 16-byte chunk c (0..7) of row r in a 128-byte-row swizzled tile.
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// One piece: the part of an item that lies in this CTA's share.
+struct Piece {
+  int t0, nt, rows;  // first tile, tiles, rows of the block
+  bool two;          // two row blocks (else two interleaved tile streams)
+};
+template <typename W>
+__device__ __forceinline__ Piece piece_of(const W& w) {
+  Piece c;
+  c.t0 = w.first_tile();
+  c.nt = w.last_tile() - c.t0;
+  c.rows = w.block_rows();
+  c.two = c.rows > 128;
+  return c;
+}
+
+// Position of tile j's V in the ring, from the piece's first slot.  Order: two
+// row blocks K0 V0 K1 V1 ..; tile streams K0 K1 V0 K2 V1 K3 .. (a K ahead).
+__device__ __forceinline__ int v_slot(const Piece& c, int j) {
+  if (c.two) return 2 * j + 1;
+  return j < c.nt - 1 ? 2 * j + 2 : 2 * c.nt - 1;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ TcParams tp) {
+  using Lo = Layout<DP>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)(smem + Lo::kOffBar);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_empty = bars + Lo::kStages;
+  uint64_t* s_full = kv_empty + Lo::kStages;  // [2] S of a stream ready
+  uint64_t* p_full = s_full + 2;              // [2] P of a stream written (4 warps)
+  uint64_t* q_full = p_full + 2;              // Q of a piece loaded (8 warps)
+  uint64_t* o_full = q_full + 1;              // a piece's last product done
+  uint64_t* pair = o_full + 1;                // the two streams meet (8 warps)
+  uint64_t* drain = pair + 1;
+  uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  AttnStart* st = (AttnStart*)(smem + Lo::kOffStart);
+
+  const AttnParams& p = tp.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Lo::kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(o_full, 1);
+    mbar_init(pair, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  attn_plan<kMR, kTN>(p, st);  // ends with a barrier
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  long long u0;
+  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, &u0);
+  if (threadIdx.x == 0) attn_write_cut(p, w, u0);
+  bool ok = true;
+
+  // (The register split stands in each role's own branch: after a join the
+  // compiler would hold every role to the smaller number.)
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    regs_dec<kRegsOther>();
+    const int bt = tp.box_tokens, E = kTN / bt;  // boxes along a tile's keys
+    const int S = p.a.c.page_size;
+    const int e = lane / Lo::kHalves, half = lane % Lo::kHalves;  // this lane's box
+    uint32_t slot = 0;  // ring slots used so far
+    for (; !w.done() && ok; w.next()) {
+      const Piece c = piece_of(w);
+      const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
+      // The page of box e of tile t, and the token in it (pages longer than a
+      // tile); -1 past the item's end.
+      auto page_at = [&](int t) {
+        const int key = t * kTN + e * bt;
+        if (e >= E || key >= w.end) return -1;
+        int pg = __ldg(table + key / S);
+        if (pg < 0 || pg >= p.a.c.n_pages) {
+          flag_status(p.status, DSPARK_DEV_BAD_INPUT);
+          pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+        }
+        return pg;
+      };
+      auto load = [&](const CUtensorMap* map, int t, int pg) {
+        const int stage = (int)(slot % Lo::kStages);
+        const uint32_t phase = (slot / Lo::kStages) & 1u;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, tp.wait_budget)))
+          return false;
+        const unsigned boxes = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) mbar_expect_tx(&kv_full[stage], (uint32_t)__popc(boxes) * bt * 128);
+        __syncwarp();
+        if (pg >= 0)
+          tma_load_4d(smem + Lo::kOffRing + stage * Lo::kTileBytes + half * Lo::kHalfBytes +
+                          e * bt * 128,
+                      map, half * 64, (t * kTN + e * bt) % S, w.h, pg, &kv_full[stage]);
+        ++slot;
+        return true;
+      };
+      // Page ids are read one tile ahead of their use.
+      int pg = page_at(c.t0), pg_next = c.nt > 1 ? page_at(c.t0 + 1) : -1;
+      ok = load(&tmK, c.t0, pg);
+      for (int j = 0; j < c.nt && ok; ++j) {
+        const int pg_after = j + 2 < c.nt ? page_at(c.t0 + j + 2) : -1;
+        if (c.two) ok = load(&tmV, c.t0 + j, pg);
+        if (ok && j + 1 < c.nt) ok = load(&tmK, c.t0 + j + 1, pg_next);
+        if (ok && !c.two) ok = load(&tmV, c.t0 + j, pg);
+        pg = pg_next;
+        pg_next = pg_after;
+      }
+    }
+    if (!ok && lane == 0) {
+      // Drain: wait (bounded) for the loads still in flight before leaving.
+      for (uint32_t i = slot > Lo::kStages ? slot - Lo::kStages : 0; i < slot; ++i)
+        mbar_drain(&kv_full[i % Lo::kStages], (i / Lo::kStages) & 1u, tp.wait_budget);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    regs_dec<kRegsOther>();
+    if (lane == 0) {
+      const uint32_t id_s = make_idesc(128, kTN, false), id_o = make_idesc(128, DP, true);
+      const uint32_t q0 = smem_addr(smem + Lo::kOffQ), ring = smem_addr(smem + Lo::kOffRing);
+      uint32_t base = 0;  // ring slot of the piece's first tile
+      uint32_t n_pieces = 0, steps0 = 0, steps1 = 0;  // pieces, P tiles of each stream so far
+      auto wait_full = [&](uint32_t sl) {
+        return mbar_wait(&kv_full[sl % Lo::kStages], (sl / Lo::kStages) & 1u, abort_flag,
+                         tp.wait_budget);
+      };
+      // Descriptors differ in their address field (16-byte units) alone.
+      const uint64_t q_desc = smem_desc(q0, 16, 1024), k_desc = smem_desc(ring, 16, 1024),
+                     v_desc = smem_desc(ring, Lo::kHalfBytes, 1024);
+      auto qk = [&](int s, int block, uint32_t sl) {  // S_s = Q_block K^T
+        const uint64_t kt = k_desc + (sl % Lo::kStages) * (Lo::kTileBytes >> 4);
+        const uint64_t qt = q_desc + block * (Lo::kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const int off = ((kk / 4) * Lo::kHalfBytes + (kk % 4) * 32) >> 4;
+          mma_ss(tmem + s * 128, qt + off, kt + off, id_s, kk != 0);
+        }
+        tc_commit(&s_full[s]);
+      };
+      auto pv = [&](int s, uint32_t sl, bool first) {  // O_s (+)= P_s V
+        const uint64_t vt = v_desc + (sl % Lo::kStages) * (Lo::kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kTN / 16; ++kk)
+          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, vt + kk * (2048 >> 4), id_o,
+                 !(first && kk == 0));
+      };
+      auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages]); };
+      auto wait_p = [&](int s) {
+        uint32_t& n = s ? steps1 : steps0;
+        const bool r = mbar_wait(&p_full[s], n++ & 1u, abort_flag, tp.wait_budget);
+        tc_fence_after();
+        return r;
+      };
+      for (; !w.done() && ok; w.next()) {
+        const Piece c = piece_of(w);
+        ok = mbar_wait(q_full, n_pieces & 1u, abort_flag, tp.wait_budget);
+        ++n_pieces;
+        tc_fence_after();
+        if (c.two) {
+          if (ok && (ok = wait_full(base))) {
+            tc_fence_after();
+            qk(0, 0, base);
+            qk(1, 1, base);
+            release(base);
+          }
+          for (int j = 0; j < c.nt && ok; ++j) {
+            const uint32_t vs = base + 2 * j + 1, ks = base + 2 * j + 2;
+            const bool more = j + 1 < c.nt;
+            ok = wait_full(vs) && wait_p(0);
+            if (!ok) break;
+            tc_fence_after();
+            pv(0, vs, j == 0);
+            if (more) {
+              if (!(ok = wait_full(ks))) break;
+              tc_fence_after();
+              qk(0, 0, ks);
+            }
+            if (!(ok = wait_p(1))) break;
+            pv(1, vs, j == 0);
+            release(vs);
+            if (more) {
+              qk(1, 1, ks);
+              release(ks);
+            }
+          }
+        } else {
+          for (int j = 0; j < 2 && j < c.nt && ok; ++j) {
+            if (!(ok = wait_full(base + j))) break;
+            tc_fence_after();
+            qk(j, 0, base + j);
+            release(base + j);
+          }
+          for (int j = 0; j < c.nt && ok; ++j) {
+            const int s = j & 1;
+            const uint32_t vs = base + v_slot(c, j);
+            ok = wait_full(vs) && wait_p(s);
+            if (!ok) break;
+            tc_fence_after();
+            pv(s, vs, j < 2);
+            release(vs);
+            if (j + 2 < c.nt) {
+              const uint32_t ks = base + 2 * (j + 2) - 1;
+              if (!(ok = wait_full(ks))) break;
+              tc_fence_after();
+              qk(s, 0, ks);
+              release(ks);
+            }
+          }
+        }
+        tc_commit(o_full);
+        base += 2 * c.nt;
+      }
+      // All products done before TMEM is freed.
+      tc_commit(drain);
+      mbar_drain(drain, 0, tp.wait_budget);
+    }
+  } else if (warp < kProducerWarp) {
+    // ------------------------------------------------------------ softmax
+    regs_inc<kRegsSoftmax>();
+    const int s = warp >> 2;               // stream
+    const int trow = threadIdx.x & 127;    // row in the 128-row tile (TMEM lane)
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp
+    const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + 256;
+    const int G = p.a.G, D = p.a.c.head_dim;
+    uint32_t base = 0, n_pieces = 0, steps = 0, meets = 0;
+    // Both streams' warps reach this point (bounded, unlike a named barrier).
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      return (bool)__all_sync(0xffffffffu, mbar_wait(pair, meets++ & 1u, abort_flag,
+                                                     tp.wait_budget));
+    };
+
+    // Q rows of the walk's item into the swizzled tiles.  Columns past D are
+    // zero (K's are, by the tensor map's fill); rows past the block's are not
+    // written: their results are not read.
+    auto load_q = [&](const AttnWalk<kMR, kTN>& u) {
+      const Piece c = piece_of(u);
+      const int n = c.two ? 32 : 16;                // rows this warp loads
+      const int a0 = c.two ? warp * 32 : warp * 16;  // from this row of the block
+      constexpr int kChunks = DP / 8;               // 16-byte chunks a row
+      constexpr int kRows = 32 / kChunks;           // rows a step
+      for (int i = 0; i < n; i += kRows) {
+        const int a = a0 + i + lane / kChunks, ch = lane % kChunks;
+        if (a >= c.rows) continue;
+        const int row = u.m * kMR + a, tok = row / G, g = row - tok * G;
+        const __nv_bfloat16* src = (const __nv_bfloat16*)p.a.q +
+                                   (long long)(u.q.q0 + tok) * p.a.q_token_stride +
+                                   (long long)(u.h * G + g) * p.a.q_head_stride;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (ch * 8 < D) {  // D % 8 == 0
+          if (tp.q_vec) {
+            x = __ldg((const uint4*)src + ch);
+          } else {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = (uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k]) |
+                     ((uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k + 1]) << 16);
+            x = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          if (tp.sign < 0.0f) {
+            x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
+          }
+        }
+        *(uint4*)(smem + Lo::kOffQ + (a >> 7) * Lo::kTileBytes + (ch >> 3) * Lo::kHalfBytes +
+                  swz(a & 127, ch & 7)) = x;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+
+    if (!w.done()) load_q(w);
+    while (!w.done() && ok) {
+      const Piece c = piece_of(w);
+      const int a = c.two ? s * 128 + trow : trow;  // row of the block
+      const bool live = a < c.rows;
+      const bool warp_live = (c.two ? s * 128 : 0) + (warp & 3) * 32 < c.rows;
+      const int lim = live ? w.q.L - w.q.n + (w.m * kMR + a) / G + 1 : 0;  // keys the row sees
+      float m = -INFINITY, l = 0.0f;
+      bool first = true;
+      for (int j = c.two ? 0 : s; j < c.nt; j += c.two ? 1 : 2) {
+        const int k0 = (c.t0 + j) * kTN;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], steps & 1u, abort_flag,
+                                               tp.wait_budget));
+        ++steps;
+        if (!ok) break;
+        tc_fence_after();
+        // V rows past the item's end become zeros (by the stream that multiplies first).
+        if (k0 + kTN > w.end && (!c.two || s == 0)) {
+          const uint32_t sl = base + v_slot(c, j);
+          const int stage = (int)(sl % Lo::kStages);
+          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[stage], (sl / Lo::kStages) & 1u,
+                                                 abort_flag, tp.wait_budget));
+          if (!ok) break;
+          if (k0 + trow >= w.end) {
+            uint8_t* v = smem + Lo::kOffRing + stage * Lo::kTileBytes + trow * 128;
+#pragma unroll
+            for (int i = 0; i < Lo::kHalves * 8; ++i)
+              *(uint4*)(v + (i >> 3) * Lo::kHalfBytes + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+        }
+        if (warp_live) {
+          uint32_t x[128];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, x + 32 * k);
+          tmem_wait_ld();
+          const int n = lim - k0;  // keys of the tile that the row sees
+          if (__any_sync(0xffffffffu, n < kTN)) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (k >= n) x[k] = 0xff800000u;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 128; k += 4)
+            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))),
+                       fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
+          mx *= p.scale_log2;
+          const bool grow = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mx : m;
+            const float f = grow ? ex2(m - mn) : 1.0f;  // 0 where nothing was summed yet
+            if (!first) {
+#pragma unroll
+              for (int k = 0; k < DP; k += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + s * 128 + k, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(tO + s * 128 + k, o);
+              }
+            }
+            l *= f;
+            m = mn;
+          }
+          first = false;
+          const float ms = m == -INFINITY ? 0.0f : m;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = ex2(fmaf(__uint_as_float(x[32 * k + 2 * i]), p.scale_log2, -ms));
+              const float e1 = ex2(fmaf(__uint_as_float(x[32 * k + 2 * i + 1]), p.scale_log2, -ms));
+              sum[i & 3] += e0 + e1;
+              pk[i] = pack_bf16(e0, e1);
+            }
+            tmem_st16(tS + 16 * k, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(o_full, n_pieces & 1u, abort_flag, tp.wait_budget));
+      ++n_pieces;
+      if (!ok) break;
+      tc_fence_after();
+      base += 2 * c.nt;
+      // ---- the piece's result
+      const int dst = attn_slot(w);
+      const int row = w.m * kMR + a, tok = row / G, g = row - tok * G;
+      const size_t orow = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + g;
+      const size_t prow = ((size_t)blockIdx.x * 2 + (dst < 0 ? 0 : dst)) * kMR + a;
+      int c_lo = 0, c_hi = DP;
+      float w0 = 1.0f, w1 = 0.0f;  // weights of O0 and O1 (tile streams)
+      const bool both = !c.two && c.nt > 1;
+      if (!c.two) {
+        // The streams trade (m, l) through two columns of their S, which no
+        // product writes before all eight warps have loaded the next Q.
+        tmem_st2(tS + 64, m, l);
+        tmem_wait_st();
+        tc_fence_before();
+        if (!(ok = meet())) break;
+        tc_fence_after();
+        const float2 x0 = tmem_ld2(tmem + lane_base + 64), x1 = tmem_ld2(tmem + lane_base + 192);
+        tmem_wait_ld();
+        m = fmaxf(x0.x, x1.x);
+        const float ms = m == -INFINITY ? 0.0f : m;
+        w0 = ex2(x0.x - ms);
+        w1 = ex2(x1.x - ms);
+        l = x0.y * w0 + x1.y * w1;
+        c_lo = s * (DP / 2);  // each stream's threads write half of the columns
+        c_hi = c_lo + DP / 2;
+        tc_fence_before();
+      }
+      // The next item's Q first, so that its first product runs beside the rest of this one.
+      w.next();
+      if (!w.done()) load_q(w);
+      const float inv = dst >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+      const uint32_t own = c.two ? tO + s * 128 : tO;
+      if (warp_live) {
+        for (int k = c_lo; k < c_hi; k += 32) {
+          uint32_t o[32];
+          tmem_ld32(own + k, o);
+          if (both) {
+            uint32_t o1[32];
+            tmem_ld32(tO + 128 + k, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + __uint_as_float(o1[i]) * w1);
+          } else {
+            tmem_wait_ld();
+          }
+          if (live) {
+            if (dst < 0) {
+              uint4* out = (uint4*)((__nv_bfloat16*)p.a.out + orow * D + k);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (k + 8 * i < D) {
+                  uint32_t v[4];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    v[q] = pack_bf16(__uint_as_float(o[8 * i + 2 * q]) * inv,
+                                     __uint_as_float(o[8 * i + 2 * q + 1]) * inv);
+                  out[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+              }
+            } else {
+              float4* out = (float4*)(p.part + prow * D + k);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (k + 4 * i < D)
+                  out[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+          }
+        }
+        if (live && (c.two || s == 0)) {
+          if (dst < 0)
+            p.a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+          else
+            p.stats[prow] = make_float2(m, l);
+        }
+      }
+      // O0 and O1 are read by both streams' threads before the next item's products overwrite them.
+      tc_fence_before();
+      if (!c.two) ok = meet();
+    }
+  } else {
+    regs_dec<kRegsOther>();
+  }
+  if (*abort_flag && lane == 0) flag_status(p.status, DSPARK_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (PFN_cuTensorMapEncodeTiled_v12000)ptr;
+  });
+  return fn;
+}
+
+// K or V as (head_dim, token in page, head, page); boxes of 64 columns and box_tokens tokens.
+bool encode_cache(CUtensorMap* map, const void* base, const CacheView& c, int box_tokens) {
+  const auto fn = get_encode();
+  if (!fn) return false;
+  // The stride of a dimension of size 1 is not used: any valid one.
+  const cuuint64_t tok = c.page_size == 1 ? 16 : (cuuint64_t)c.token_stride * 2;
+  const cuuint64_t head = c.heads == 1 ? 16 : (cuuint64_t)c.head_stride * 2;
+  const cuuint64_t page = c.n_pages == 1 ? 16 : (cuuint64_t)c.page_stride * 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads,
+                              (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[3] = {tok, head, page};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      v = 1;
+    return v < kAttnMaxCtas ? v : kAttnMaxCtas;
+  }();
+  return n;
+}
+
+template <int DP>
+cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      attention_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
+  if (attr != cudaSuccess) return attr;
+  attention_tc_kernel<DP><<<sm_count(), kThreads, Layout<DP>::kBytes, s>>>(k, v, tp);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// The tensor-core kernel takes bf16 with head_dim a multiple of 8 up to 128 (two
+// 64-column halves of 128-byte rows), pages of 2^k >= 8 tokens (whole
+// 8-row swizzle groups; a power of two divides the 128-key tile or is a multiple of it), and what TMA asks
+// of addresses and strides (16 bytes).
+bool attention_tc_supported(const AttnArgs& a) {
+  const CacheView& c = a.c;
+  if (a.dtype != DSPARK_BF16 || c.head_dim % 8 != 0 || c.head_dim > 128) return false;
+  if (c.page_size < 8 || (c.page_size & (c.page_size - 1)) != 0) return false;
+  if (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) return false;
+  const long long most = 1ll << 39;  // elements: 2^40 bytes
+  if (c.token_stride % 8 != 0 || c.token_stride >= most) return false;
+  if (c.heads > 1 && (c.head_stride % 8 != 0 || c.head_stride >= most)) return false;
+  if (c.n_pages > 1 && (c.page_stride % 8 != 0 || c.page_stride >= most)) return false;
+  return get_encode() != nullptr;
+}
+
+size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout(kMR, head_dim).total; }
+
+cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
+  const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
+  TcParams tp;
+  tp.p = AttnParams{a, (int*)ws, (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
+                    (float2*)(ws + w.stats), (float*)(ws + w.out),
+                    // (not 0: a masked score is -inf times this)
+                    fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f)};
+  tp.sign = a.scale < 0 ? -1.0f : 1.0f;
+  tp.box_tokens = a.c.page_size < kTN ? a.c.page_size : kTN;
+  tp.q_vec = ((uintptr_t)a.q & 15u) == 0 && a.q_token_stride % 8 == 0 && a.q_head_stride % 8 == 0;
+  tp.wait_budget = kWaitBudget;
+  CUtensorMap mk, mv;
+  if (!encode_cache(&mk, a.c.k, a.c, tp.box_tokens) || !encode_cache(&mv, a.c.v, a.c, tp.box_tokens))
+    return cudaErrorInvalidValue;
+  cudaError_t e = a.c.head_dim <= 64 ? launch<64>(tp, mk, mv, s) : launch<128>(tp, mk, mv, s);
+  if (e != cudaSuccess) return e;
+  return launch_attn_combine(tp.p, kMR, sm_count(), s);
+}
+
+}  // namespace dspark

@@ -4,7 +4,7 @@ Tolerances, per output element, from the formulas.  With u = 2^-24, scores of
 the fp32 sums are off by at most ds = (D + 3) u scale sum |q k| (plus the
 rounding of the exponent's argument, 2 u max|s|), so a probability is off by
 the factor e^{+-2 ds}; sums over L keys add (L + 8) u; the bf16 kernel rounds
-each probability (2^-9 relative) and the output (2^-9).  All of it is relative
+each probability and the output to 8 bits (2^-8 relative each).  All of it is relative
 to sum_j p_j |v_j|, which the reference computes.
 """
 import math
@@ -83,7 +83,7 @@ def reference(i, layer=0):
                 out[t] = torch.einsum("hj,jhd->hd", pr, Vh)
                 mix = torch.einsum("hj,jhd->hd", pr, Vh.abs())
                 rel = 4 * ds + (2 * p + 16) * U + (2.0 ** -8 if bf else 0)
-                tol[t] = rel[:, None] * mix + (2.0 ** -9 * out[t].abs() if bf else 0)
+                tol[t] = rel[:, None] * mix + (2.0 ** -8 * out[t].abs() if bf else 0)
                 tol_lse[t] = 2 * ds + (2 * p + 16) * U + 4 * U * lse[t].abs()
             t += 1
     return out, lse, tol, tol_lse
