@@ -5,7 +5,7 @@
 // tile of 128 keys: S = Q K^T (128 x 128 x D), the online softmax
 //   m' = max(m, max_j s_j),  p_j = 2^{s_j - m'},  l' = l 2^{m-m'} + sum_j p_j,
 //   O' = O 2^{m-m'} + P V
-// in units of log2, with S and O in TMEM and P (bf16) written over S in TMEM as
+// in units of log2, with S and O in TMEM and P (bf16) written over half of S in TMEM as
 // the first operand of P V.  A larger maximum rescales O and l only when it
 // grew by more than 2^8: until then p_j <= 2^8 stays far inside bf16's and
 // fp32's range, and out = O / l is the same whatever m the two share.
@@ -13,16 +13,20 @@
 // Structure (one CTA an SM, persistent over its share of the work):
 //   * warp 8 (producer): TMA of K and V pages into a ring of tiles; each lane
 //     owns one (page, 64-column half) box of a tile, so a tile of 16-token
-//     pages is 16 boxes issued at once.  Page ids are read a group of tiles
-//     ahead.
+//     pages is 16 boxes issued at once.
 //   * warp 9 (MMA): one thread issues tcgen05.mma; S from shared-memory
 //     descriptors, P V with P in TMEM and V as stored ([keys, D]: the N-major
 //     second operand).
 //   * warps 0..3 and 4..7: two softmax streams, one row a thread.  With more
 //     than 128 rows the streams are the two row blocks and share each K/V tile;
-//     with fewer they are the even and the odd tiles of the same rows, and
-//     merge at the end.  While one stream is in its softmax the tensor cores
+//     with fewer they are alternate tiles of the same rows, and merge at the
+//     end of the item.  While one stream is in its softmax the tensor cores
 //     run the other's products.
+//   * warps 10, 11 (loaders): walk the share ahead of the others, load each
+//     piece's Q and publish what it is.  Pieces of up to 128 rows alternate
+//     between the two Q tiles, so the products of a run of such pieces follow
+//     one another without a gap: the next piece's Q K^T is issued while
+//     the last tiles of this one are in their softmax.
 //   * Keys at or past an item's end: pages past it are not loaded, S is
 //     replaced by -inf, and V's rows are overwritten with zeros, since 0 x NaN of
 //     an unused cache slot would reach the sum.
@@ -44,8 +48,8 @@ namespace {
 constexpr int kMR = 256;  // rows of an item
 constexpr int kTN = 128;  // keys of a tile
 constexpr int kThreads = 384;  // three warpgroups: two of softmax, one with the producer and MMA warps
-// Registers a thread after the split: 256 x 208 + 128 x 80 of the launch's 384 x 168.
-constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+// Registers a thread after the split: 256 x 184 + 128 x 128 of the launch's 384 x 168.
+constexpr int kRegsSoftmax = 184, kRegsOther = 128;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -58,13 +62,19 @@ struct Layout {
   static constexpr int kHalfBytes = 128 * 128;             // 128 rows of 128 bytes
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
   static constexpr int kStages = DP == 128 ? 5 : 10;
-  static constexpr int kOffQ = 0;  // two row blocks
+  static constexpr int kOffQ = 0;  // two row blocks, or this piece's and the next one's rows
   static constexpr int kOffRing = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffRing + kStages * kTileBytes;
-  static constexpr int kBars = 2 * kStages + 2 + 2 + 1 + 1 + 1 + 1;
-  static constexpr int kOffStart = kOffBar + ((kBars * 8 + 16 + 15) & ~15);
-  static constexpr int kBytes = kOffStart + (int)sizeof(AttnStart) + 1024;
+  static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
+  static constexpr int kOffStart = kOffMerge;                        // (before the first merge)
+  static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1;
+  static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 8 + 15) & ~15);  // PieceInfo [2]
+  static constexpr int kEnd = kOffPiece + 2 * 64;
+  // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
+  // static shared memory; the slack covers most others, and the kernel checks.
+  static constexpr int kBytes = kEnd + 1024 < 232448 ? kEnd + 1024 : 232448;
 };
+static_assert(Layout<128>::kEnd <= 232448, "shared memory");
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             int w, uint64_t* bar) {
@@ -73,6 +83,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
+}
+
+// 16 bytes global -> shared without a register in between; `bytes` of them read, the rest zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async() {
@@ -144,8 +163,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
         "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// Waits for the loads so far; the operands tie the uses of v behind the wait.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+                 "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
+                 "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+                 "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -171,22 +198,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// Two columns (a stream's m and l) to and from TMEM.
-__device__ __forceinline__ void tmem_st2(uint32_t taddr, float a, float b) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"r"(__float_as_uint(a)),
-               "r"(__float_as_uint(b)), "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ float2 tmem_ld2(uint32_t taddr) {
-  uint32_t a, b;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(taddr));
-  return make_float2(__uint_as_float(a), __uint_as_float(b));
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Scores of keys at or past the first `n` become -inf.
+template <int N>
+__device__ __forceinline__ void mask_from(uint32_t* x, int n) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k >= n) x[k] = 0xff800000u;
 }
 
 // {hi, lo} rounded to bf16 and packed.
@@ -219,26 +249,17 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 }
 
 // One piece: the part of an item that lies in this CTA's share.
-struct Piece {
-  int t0, nt, rows;  // first tile, tiles, rows of the block
-  bool two;          // two row blocks (else two interleaved tile streams)
+struct alignas(16) PieceInfo {
+  int t0, nt;       // first tile, tiles (0: no more pieces)
+  int rows, row0;   // rows of the block (more than 128: two row blocks), first row of the chunk
+  int h, q0;        // K/V head, the chunk's first token
+  int lim;          // keys that the chunk's token 0 sees (L - n + 1; may be <= 0)
+  int end;          // keys of the item
+  int slot;         // where the result goes (attn_slot)
+  int next_joined;  // both this piece and the next one have up to 128 rows
+  int pad[2];
 };
-template <typename W>
-__device__ __forceinline__ Piece piece_of(const W& w) {
-  Piece c;
-  c.t0 = w.first_tile();
-  c.nt = w.last_tile() - c.t0;
-  c.rows = w.block_rows();
-  c.two = c.rows > 128;
-  return c;
-}
-
-// Position of tile j's V in the ring, from the piece's first slot.  Order: two
-// row blocks K0 V0 K1 V1 ..; tile streams K0 K1 V0 K2 V1 K3 .. (a K ahead).
-__device__ __forceinline__ int v_slot(const Piece& c, int j) {
-  if (c.two) return 2 * j + 1;
-  return j < c.nt - 1 ? 2 * j + 2 : 2 * c.nt - 1;
-}
+static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -247,20 +268,27 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   using Lo = Layout<DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const AttnParams& p = tp.p;
+  if (smem + Lo::kEnd > smem_raw + Lo::kBytes) {  // (never: see Layout)
+    if (threadIdx.x == 0) flag_status(p.status, DSPARK_DEV_TIMEOUT);
+    return;
+  }
   uint64_t* bars = (uint64_t*)(smem + Lo::kOffBar);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = bars + Lo::kStages;
   uint64_t* s_full = kv_empty + Lo::kStages;  // [2] S of a stream ready
   uint64_t* p_full = s_full + 2;              // [2] P of a stream written (4 warps)
-  uint64_t* q_full = p_full + 2;              // Q of a piece loaded (8 warps)
-  uint64_t* o_full = q_full + 1;              // a piece's last product done
-  uint64_t* pair = o_full + 1;                // the two streams meet (8 warps)
+  uint64_t* q_full = p_full + 2;   // [2] piece n (n & 1) published and its Q loaded (2 warps)
+  uint64_t* q_empty = q_full + 2;  // [2] its last Q K^T done (1) and its info read (8 warps)
+  uint64_t* o_full = q_empty + 2;  // [2] piece n's last product done
+  uint64_t* pair = o_full + 2;     // the two streams meet (8 warps)
   uint64_t* drain = pair + 1;
   uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   AttnStart* st = (AttnStart*)(smem + Lo::kOffStart);
+  float2* merge = (float2*)(smem + Lo::kOffMerge);
+  PieceInfo* infos = (PieceInfo*)(smem + Lo::kOffPiece);
 
-  const AttnParams& p = tp.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lo::kStages; ++i) {
@@ -270,9 +298,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&q_full[i], 2);
+      mbar_init(&q_empty[i], 9);
+      mbar_init(&o_full[i], 1);
     }
-    mbar_init(q_full, 8);
-    mbar_init(o_full, 1);
     mbar_init(pair, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -290,9 +319,6 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  long long u0;
-  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, &u0);
-  if (threadIdx.x == 0) attn_write_cut(p, w, u0);
   bool ok = true;
 
   // (The register split stands in each role's own branch: after a join the
@@ -300,15 +326,35 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     regs_dec<kRegsOther>();
+    long long u0;
+    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, &u0);
     const int bt = tp.box_tokens, E = kTN / bt;  // boxes along a tile's keys
     const int S = p.a.c.page_size;
     const int e = lane / Lo::kHalves, half = lane % Lo::kHalves;  // this lane's box
     uint32_t slot = 0;  // ring slots used so far
+    auto load = [&](const CUtensorMap* map, int t, int h, int pg) {
+      const int stage = (int)(slot % Lo::kStages);
+      const uint32_t phase = (slot / Lo::kStages) & 1u;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, tp.wait_budget)))
+        return false;
+      const unsigned boxes = __ballot_sync(0xffffffffu, pg >= 0);
+      if (lane == 0) mbar_expect_tx(&kv_full[stage], (uint32_t)__popc(boxes) * bt * 128);
+      __syncwarp();
+      if (pg >= 0)
+        tma_load_4d(smem + Lo::kOffRing + stage * Lo::kTileBytes + half * Lo::kHalfBytes +
+                        e * bt * 128,
+                    map, half * 64, (t * kTN + e * bt) % S, h, pg, &kv_full[stage]);
+      ++slot;
+      return true;
+    };
+    // Ring order: with two row blocks K0 V0 K1 V1 ..; over a run of smaller
+    // pieces, whose products run a tile ahead, K0 K1 V0 K2 V1 ..
+    bool pending = false;  // a V that the next K goes before
+    int pend_t = 0, pend_h = 0, pend_pg = -1;
     for (; !w.done() && ok; w.next()) {
-      const Piece c = piece_of(w);
       const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
-      // The page of box e of tile t, and the token in it (pages longer than a
-      // tile); -1 past the item's end.
+      // The page of this lane's box of tile t; -1 past the item's end.
       auto page_at = [&](int t) {
         const int key = t * kTN + e * bt;
         if (e >= E || key >= w.end) return -1;
@@ -319,34 +365,27 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         return pg;
       };
-      auto load = [&](const CUtensorMap* map, int t, int pg) {
-        const int stage = (int)(slot % Lo::kStages);
-        const uint32_t phase = (slot / Lo::kStages) & 1u;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&kv_empty[stage], phase ^ 1u, abort_flag, tp.wait_budget)))
-          return false;
-        const unsigned boxes = __ballot_sync(0xffffffffu, pg >= 0);
-        if (lane == 0) mbar_expect_tx(&kv_full[stage], (uint32_t)__popc(boxes) * bt * 128);
-        __syncwarp();
-        if (pg >= 0)
-          tma_load_4d(smem + Lo::kOffRing + stage * Lo::kTileBytes + half * Lo::kHalfBytes +
-                          e * bt * 128,
-                      map, half * 64, (t * kTN + e * bt) % S, w.h, pg, &kv_full[stage]);
-        ++slot;
-        return true;
-      };
-      // Page ids are read one tile ahead of their use.
-      int pg = page_at(c.t0), pg_next = c.nt > 1 ? page_at(c.t0 + 1) : -1;
-      ok = load(&tmK, c.t0, pg);
-      for (int j = 0; j < c.nt && ok; ++j) {
-        const int pg_after = j + 2 < c.nt ? page_at(c.t0 + j + 2) : -1;
-        if (c.two) ok = load(&tmV, c.t0 + j, pg);
-        if (ok && j + 1 < c.nt) ok = load(&tmK, c.t0 + j + 1, pg_next);
-        if (ok && !c.two) ok = load(&tmV, c.t0 + j, pg);
+      const int t1 = w.last_tile();
+      const bool two = w.block_rows() > 128;
+      if (two && pending) {
+        ok = load(&tmV, pend_t, pend_h, pend_pg);
+        pending = false;
+      }
+      int pg = page_at(w.first_tile());
+      for (int t = w.first_tile(); t < t1 && ok; ++t) {
+        const int pg_next = t + 1 < t1 ? page_at(t + 1) : -1;  // read a tile ahead
+        ok = load(&tmK, t, w.h, pg);
+        if (two) {
+          ok = ok && load(&tmV, t, w.h, pg);
+        } else {
+          if (pending) ok = ok && load(&tmV, pend_t, pend_h, pend_pg);
+          pending = true;
+          pend_t = t, pend_h = w.h, pend_pg = pg;
+        }
         pg = pg_next;
-        pg_next = pg_after;
       }
     }
+    if (ok && pending) ok = load(&tmV, pend_t, pend_h, pend_pg);
     if (!ok && lane == 0) {
       // Drain: wait (bounded) for the loads still in flight before leaving.
       for (uint32_t i = slot > Lo::kStages ? slot - Lo::kStages : 0; i < slot; ++i)
@@ -358,11 +397,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if (lane == 0) {
       const uint32_t id_s = make_idesc(128, kTN, false), id_o = make_idesc(128, DP, true);
       const uint32_t q0 = smem_addr(smem + Lo::kOffQ), ring = smem_addr(smem + Lo::kOffRing);
-      uint32_t base = 0;  // ring slot of the piece's first tile
-      uint32_t n_pieces = 0, steps0 = 0, steps1 = 0;  // pieces, P tiles of each stream so far
+      uint32_t slot = 0;  // next ring slot, in the order of use
+      uint32_t n = 0, steps0 = 0, steps1 = 0;  // piece, P tiles of each stream so far
       auto wait_full = [&](uint32_t sl) {
-        return mbar_wait(&kv_full[sl % Lo::kStages], (sl / Lo::kStages) & 1u, abort_flag,
-                         tp.wait_budget);
+        const bool r = mbar_wait(&kv_full[sl % Lo::kStages], (sl / Lo::kStages) & 1u, abort_flag,
+                                 tp.wait_budget);
+        tc_fence_after();
+        return r;
       };
       // Descriptors differ in their address field (16-byte units) alone.
       const uint64_t q_desc = smem_desc(q0, 16, 1024), k_desc = smem_desc(ring, 16, 1024),
@@ -381,38 +422,39 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const uint64_t vt = v_desc + (sl % Lo::kStages) * (Lo::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTN / 16; ++kk)
-          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, vt + kk * (2048 >> 4), id_o,
+          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, vt + kk * (2048 >> 4), id_o,
                  !(first && kk == 0));
       };
       auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages]); };
       auto wait_p = [&](int s) {
-        uint32_t& n = s ? steps1 : steps0;
-        const bool r = mbar_wait(&p_full[s], n++ & 1u, abort_flag, tp.wait_budget);
+        uint32_t& k = s ? steps1 : steps0;
+        const bool r = mbar_wait(&p_full[s], k++ & 1u, abort_flag, tp.wait_budget);
         tc_fence_after();
         return r;
       };
-      for (; !w.done() && ok; w.next()) {
-        const Piece c = piece_of(w);
-        ok = mbar_wait(q_full, n_pieces & 1u, abort_flag, tp.wait_budget);
-        ++n_pieces;
+      auto wait_piece = [&] {  // piece n published
+        const bool r = mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget);
         tc_fence_after();
-        if (c.two) {
-          if (ok && (ok = wait_full(base))) {
-            tc_fence_after();
-            qk(0, 0, base);
-            qk(1, 1, base);
-            release(base);
-          }
-          for (int j = 0; j < c.nt && ok; ++j) {
-            const uint32_t vs = base + 2 * j + 1, ks = base + 2 * j + 2;
-            const bool more = j + 1 < c.nt;
-            ok = wait_full(vs) && wait_p(0);
-            if (!ok) break;
-            tc_fence_after();
+        return r;
+      };
+      while (ok) {
+        if (!(ok = wait_piece())) break;
+        int nt = infos[n & 1].nt;
+        if (nt == 0) break;
+        if (infos[n & 1].rows > 128) {
+          ok = wait_full(slot);
+          if (!ok) break;
+          qk(0, 0, slot);
+          qk(1, 1, slot);
+          release(slot);
+          if (nt == 1) tc_commit(&q_empty[n & 1]);
+          for (int j = 0; j < nt; ++j) {
+            const uint32_t vs = slot + 1, ks = slot + 2;
+            const bool more = j + 1 < nt;
+            if (!(ok = wait_full(vs) && wait_p(0))) break;
             pv(0, vs, j == 0);
             if (more) {
               if (!(ok = wait_full(ks))) break;
-              tc_fence_after();
               qk(0, 0, ks);
             }
             if (!(ok = wait_p(1))) break;
@@ -421,34 +463,52 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (more) {
               qk(1, 1, ks);
               release(ks);
+              if (j + 2 == nt) tc_commit(&q_empty[n & 1]);
             }
+            slot += 2;
           }
+          tc_commit(&o_full[n & 1]);
+          ++n;
         } else {
-          for (int j = 0; j < 2 && j < c.nt && ok; ++j) {
-            if (!(ok = wait_full(base + j))) break;
-            tc_fence_after();
-            qk(j, 0, base + j);
-            release(base + j);
-          }
-          for (int j = 0; j < c.nt && ok; ++j) {
-            const int s = j & 1;
-            const uint32_t vs = base + v_slot(c, j);
-            ok = wait_full(vs) && wait_p(s);
-            if (!ok) break;
-            tc_fence_after();
-            pv(s, vs, j < 2);
-            release(vs);
-            if (j + 2 < c.nt) {
-              const uint32_t ks = base + 2 * (j + 2) - 1;
-              if (!(ok = wait_full(ks))) break;
-              tc_fence_after();
-              qk(s, 0, ks);
-              release(ks);
+          // A run of pieces of up to 128 rows: step i on stream i & 1; the
+          // first product of step i + 2 follows the second of step i.
+          int jq = 0;
+          uint32_t iq = 0;           // steps whose first product is issued
+          uint32_t flags0 = 0, flags1 = 0;  // of the step in flight on a stream: 1 first, 2 last tile
+          bool open = true;
+          uint32_t np = n;           // the piece of the second products
+          auto issue_qk = [&] {
+            if (jq == nt) {  // the next piece, if it belongs to the run
+              ++n;
+              if (!(ok = wait_piece())) return;
+              nt = infos[n & 1].nt;
+              if (nt == 0 || infos[n & 1].rows > 128) {
+                open = false;
+                return;
+              }
+              jq = 0;
             }
+            if (!(ok = wait_full(slot))) return;
+            const int s = iq & 1;
+            qk(s, n & 1, slot);
+            release(slot++);
+            const bool last = ++jq == nt;
+            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u);
+            if (last) tc_commit(&q_empty[n & 1]);
+            ++iq;
+          };
+          issue_qk();
+          if (ok) issue_qk();
+          for (uint32_t i = 0; i < iq && ok; ++i) {
+            const int s = i & 1;
+            if (!(ok = wait_full(slot) && wait_p(s))) break;
+            const uint32_t f = s ? flags1 : flags0;
+            pv(s, slot, f & 1u);
+            release(slot++);
+            if (f & 2u) tc_commit(&o_full[np++ & 1]);
+            if (open) issue_qk();
           }
         }
-        tc_commit(o_full);
-        base += 2 * c.nt;
       }
       // All products done before TMEM is freed.
       tc_commit(drain);
@@ -461,80 +521,48 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const int trow = threadIdx.x & 127;    // row in the 128-row tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp
     const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + 256;
-    const int G = p.a.G, D = p.a.c.head_dim;
-    uint32_t base = 0, n_pieces = 0, steps = 0, meets = 0;
+    uint32_t base = 0;  // ring slot of the run's (or two-block piece's) first tile
+    uint32_t run = 0;   // steps of the run before this piece
+    uint32_t n = 0, steps = 0, meets = 0;
     // Both streams' warps reach this point (bounded, unlike a named barrier).
     auto meet = [&] {
       __syncwarp();
       if (lane == 0) mbar_arrive(pair);
-      return (bool)__all_sync(0xffffffffu, mbar_wait(pair, meets++ & 1u, abort_flag,
-                                                     tp.wait_budget));
+      return (bool)__all_sync(0xffffffffu,
+                              mbar_wait(pair, meets++ & 1u, abort_flag, tp.wait_budget));
     };
 
-    // Q rows of the walk's item into the swizzled tiles.  Columns past D are
-    // zero (K's are, by the tensor map's fill); rows past the block's are not
-    // written: their results are not read.
-    auto load_q = [&](const AttnWalk<kMR, kTN>& u) {
-      const Piece c = piece_of(u);
-      const int n = c.two ? 32 : 16;                // rows this warp loads
-      const int a0 = c.two ? warp * 32 : warp * 16;  // from this row of the block
-      constexpr int kChunks = DP / 8;               // 16-byte chunks a row
-      constexpr int kRows = 32 / kChunks;           // rows a step
-      for (int i = 0; i < n; i += kRows) {
-        const int a = a0 + i + lane / kChunks, ch = lane % kChunks;
-        if (a >= c.rows) continue;
-        const int row = u.m * kMR + a, tok = row / G, g = row - tok * G;
-        const __nv_bfloat16* src = (const __nv_bfloat16*)p.a.q +
-                                   (long long)(u.q.q0 + tok) * p.a.q_token_stride +
-                                   (long long)(u.h * G + g) * p.a.q_head_stride;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (ch * 8 < D) {  // D % 8 == 0
-          if (tp.q_vec) {
-            x = __ldg((const uint4*)src + ch);
-          } else {
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              v[k] = (uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k]) |
-                     ((uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k + 1]) << 16);
-            x = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-          if (tp.sign < 0.0f) {
-            x.x ^= 0x80008000u, x.y ^= 0x80008000u, x.z ^= 0x80008000u, x.w ^= 0x80008000u;
-          }
-        }
-        *(uint4*)(smem + Lo::kOffQ + (a >> 7) * Lo::kTileBytes + (ch >> 3) * Lo::kHalfBytes +
-                  swz(a & 127, ch & 7)) = x;
-      }
-      fence_proxy_async();
+    while (true) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget));
+      if (!ok) break;
+      const PieceInfo c = infos[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    };
-
-    if (!w.done()) load_q(w);
-    while (!w.done() && ok) {
-      const Piece c = piece_of(w);
-      const int a = c.two ? s * 128 + trow : trow;  // row of the block
+      if (lane == 0) mbar_arrive(&q_empty[n & 1]);
+      if (c.nt == 0) break;
+      const bool two = c.rows > 128;
+      const int a = two ? s * 128 + trow : trow;  // row of the block
       const bool live = a < c.rows;
-      const bool warp_live = (c.two ? s * 128 : 0) + (warp & 3) * 32 < c.rows;
-      const int lim = live ? w.q.L - w.q.n + (w.m * kMR + a) / G + 1 : 0;  // keys the row sees
+      const bool warp_live = (two ? s * 128 : 0) + (warp & 3) * 32 < c.rows;
+      const int lim = live ? c.lim + (c.row0 + a) / p.a.G : 0;  // keys the row sees
       float m = -INFINITY, l = 0.0f;
       bool first = true;
-      for (int j = c.two ? 0 : s; j < c.nt; j += c.two ? 1 : 2) {
+      // This stream's tiles: all with two row blocks, else those on steps of its parity.
+      for (int j = two ? 0 : (int)((s ^ run) & 1u); j < c.nt; j += two ? 1 : 2) {
         const int k0 = (c.t0 + j) * kTN;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], steps & 1u, abort_flag,
-                                               tp.wait_budget));
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&s_full[s], steps & 1u, abort_flag, tp.wait_budget));
         ++steps;
         if (!ok) break;
         tc_fence_after();
         // V rows past the item's end become zeros (by the stream that multiplies first).
-        if (k0 + kTN > w.end && (!c.two || s == 0)) {
-          const uint32_t sl = base + v_slot(c, j);
+        if (k0 + kTN > c.end && (!two || s == 0)) {
+          const uint32_t i = run + j;
+          const uint32_t sl = base + (two ? 2 * j + 1 : j + 1 < c.nt || c.next_joined ? 2 * i + 2 : 2 * i + 1);
           const int stage = (int)(sl % Lo::kStages);
-          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[stage], (sl / Lo::kStages) & 1u,
-                                                 abort_flag, tp.wait_budget));
+          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[stage], (sl / Lo::kStages) & 1u, abort_flag,
+                                                 tp.wait_budget));
           if (!ok) break;
-          if (k0 + trow >= w.end) {
+          if (k0 + trow >= c.end) {
             uint8_t* v = smem + Lo::kOffRing + stage * Lo::kTileBytes + trow * 128;
 #pragma unroll
             for (int i = 0; i < Lo::kHalves * 8; ++i)
@@ -543,21 +571,24 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           fence_proxy_async();
         }
         if (warp_live) {
-          uint32_t x[128];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, x + 32 * k);
-          tmem_wait_ld();
-          const int n = lim - k0;  // keys of the tile that the row sees
-          if (__any_sync(0xffffffffu, n < kTN)) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (k >= n) x[k] = 0xff800000u;
-          }
+          // Two passes over S: the maximum, columns 0..63 then 64..127; then the
+          // probabilities, 64..127 from registers and 0..63 read again (all 128
+          // columns in registers would spill).  P goes to columns 64..127.
+          const int vis = lim - k0;  // keys of the tile that the row sees
+          const bool masked = __any_sync(0xffffffffu, vis < kTN);
+          uint32_t x[64];
           float mx = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 128; k += 4)
-            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))),
-                       fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
+          for (int hh = 0; hh < 2; ++hh) {
+            tmem_ld32(tS + 64 * hh, x);
+            tmem_ld32(tS + 64 * hh + 32, x + 32);
+            tmem_wait_ld32(x);
+            tmem_wait_ld32(x + 32);
+            if (masked) mask_from<64>(x, vis - 64 * hh);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2)
+              mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          }
           mx *= p.scale_log2;
           const bool grow = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
@@ -568,7 +599,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               for (int k = 0; k < DP; k += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + s * 128 + k, o);
-                tmem_wait_ld();
+                tmem_wait_ld32(o);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                 tmem_st32(tO + s * 128 + k, o);
@@ -580,18 +611,28 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           first = false;
           const float ms = m == -INFINITY ? 0.0f : m;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          auto probs = [&](const uint32_t* v, int k) {  // 32 columns -> P's columns k ..
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[32 * k + 2 * i]), p.scale_log2, -ms));
-              const float e1 = ex2(fmaf(__uint_as_float(x[32 * k + 2 * i + 1]), p.scale_log2, -ms));
+              const float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, -ms));
+              const float e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, -ms));
               sum[i & 3] += e0 + e1;
               pk[i] = pack_bf16(e0, e1);
             }
-            tmem_st16(tS + 16 * k, pk);
-          }
+            tmem_st16(tS + 64 + k, pk);
+          };
+          uint32_t y[32];
+          tmem_ld32(tS, y);
+          probs(x, 32);
+          probs(x + 32, 48);
+          tmem_wait_ld32(y);
+          tmem_ld32(tS + 32, x);
+          if (masked) mask_from<32>(y, vis);
+          probs(y, 0);
+          tmem_wait_ld32(x);
+          if (masked) mask_from<32>(x, vis - 32);
+          probs(x, 16);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
@@ -601,59 +642,50 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       if (!ok) break;
       ok = __all_sync(0xffffffffu,
-                      mbar_wait(o_full, n_pieces & 1u, abort_flag, tp.wait_budget));
-      ++n_pieces;
+                      mbar_wait(&o_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget));
       if (!ok) break;
       tc_fence_after();
-      base += 2 * c.nt;
+
       // ---- the piece's result
-      const int dst = attn_slot(w);
-      const int row = w.m * kMR + a, tok = row / G, g = row - tok * G;
-      const size_t orow = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + g;
-      const size_t prow = ((size_t)blockIdx.x * 2 + (dst < 0 ? 0 : dst)) * kMR + a;
+      const int row = c.row0 + a, tok = row / p.a.G, g = row - tok * p.a.G, D = p.a.c.head_dim;
+      const size_t orow = (size_t)(c.q0 + tok) * p.a.Hq + c.h * p.a.G + g;
+      const size_t prow = ((size_t)blockIdx.x * 2 + (c.slot < 0 ? 0 : c.slot)) * kMR + a;
       int c_lo = 0, c_hi = DP;
-      float w0 = 1.0f, w1 = 0.0f;  // weights of O0 and O1 (tile streams)
-      const bool both = !c.two && c.nt > 1;
-      if (!c.two) {
-        // The streams trade (m, l) through two columns of their S, which no
-        // product writes before all eight warps have loaded the next Q.
-        tmem_st2(tS + 64, m, l);
-        tmem_wait_st();
-        tc_fence_before();
+      float w0 = 1.0f, w1 = 0.0f;  // weights of the two streams' O
+      uint32_t own = tO + s * 128;
+      const bool both = !two && c.nt > 1;
+      if (!two) {
+        merge[s * 128 + trow] = make_float2(m, l);
         if (!(ok = meet())) break;
-        tc_fence_after();
-        const float2 x0 = tmem_ld2(tmem + lane_base + 64), x1 = tmem_ld2(tmem + lane_base + 192);
-        tmem_wait_ld();
+        const int s0 = run & 1;  // the stream of the piece's first tile
+        const float2 x0 = merge[s0 * 128 + trow], x1 = merge[(s0 ^ 1) * 128 + trow];
         m = fmaxf(x0.x, x1.x);
         const float ms = m == -INFINITY ? 0.0f : m;
         w0 = ex2(x0.x - ms);
         w1 = ex2(x1.x - ms);
         l = x0.y * w0 + x1.y * w1;
+        own = tO + s0 * 128;
         c_lo = s * (DP / 2);  // each stream's threads write half of the columns
         c_hi = c_lo + DP / 2;
-        tc_fence_before();
       }
-      // The next item's Q first, so that its first product runs beside the rest of this one.
-      w.next();
-      if (!w.done()) load_q(w);
-      const float inv = dst >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-      const uint32_t own = c.two ? tO + s * 128 : tO;
+      const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
       if (warp_live) {
         for (int k = c_lo; k < c_hi; k += 32) {
           uint32_t o[32];
           tmem_ld32(own + k, o);
           if (both) {
             uint32_t o1[32];
-            tmem_ld32(tO + 128 + k, o1);
-            tmem_wait_ld();
+            tmem_ld32((own ^ 128u) + k, o1);  // tO + 128 (s0 ^ 1): the base is 256-aligned
+            tmem_wait_ld32(o);
+            tmem_wait_ld32(o1);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + __uint_as_float(o1[i]) * w1);
           } else {
-            tmem_wait_ld();
+            tmem_wait_ld32(o);
           }
           if (live) {
-            if (dst < 0) {
+            if (c.slot < 0) {
               uint4* out = (uint4*)((__nv_bfloat16*)p.a.out + orow * D + k);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -676,19 +708,102 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
           }
         }
-        if (live && (c.two || s == 0)) {
-          if (dst < 0)
+        if (live && (two || s == 0)) {
+          if (c.slot < 0)
             p.a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
           else
             p.stats[prow] = make_float2(m, l);
         }
       }
-      // O0 and O1 are read by both streams' threads before the next item's products overwrite them.
+      // The next piece's second products overwrite O0 and O1, which both streams' threads read.
       tc_fence_before();
-      if (!c.two) ok = meet();
+      if (!two && !(ok = meet())) break;
+      if (two) {
+        base += 2 * c.nt;
+      } else {
+        run += c.nt;
+        if (!c.next_joined) {
+          base += 2 * run;
+          run = 0;
+        }
+      }
+      ++n;
     }
   } else {
+    // ------------------------------------------------------------ loaders
     regs_dec<kRegsOther>();
+    long long u0;
+    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, &u0);
+    if (threadIdx.x == (kMmaWarp + 1) * 32) attn_write_cut(p, w, u0);
+    const int D = p.a.c.head_dim, G = p.a.G;
+    const int lt = threadIdx.x - (kMmaWarp + 1) * 32;  // 0 .. 63
+    bool prev_two = false;
+    for (uint32_t n = 0;; ++n) {
+      const bool end = w.done();
+      PieceInfo c;
+      c.t0 = w.t0;
+      c.nt = end ? 0 : w.last_tile() - w.t0;
+      c.rows = end ? 0 : w.block_rows();
+      c.row0 = w.m * kMR;
+      c.h = w.h;
+      c.q0 = w.q.q0;
+      c.lim = w.q.L - w.q.n + 1;
+      c.end = w.end;
+      c.slot = end ? 0 : attn_slot(w);
+      c.next_joined = 0;
+      const bool two = c.rows > 128;
+      // The Q tile(s) of this piece and its info slot are free again: piece n - 2
+      // is done with them, and piece n - 1 where either of the two takes both.
+      if (n >= 2)
+        ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_empty[n & 1], ((n - 2) >> 1) & 1u, abort_flag,
+                                               tp.wait_budget));
+      if (ok && n >= 1 && (two || prev_two))
+        ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_empty[(n - 1) & 1], ((n - 1) >> 1) & 1u,
+                                               abort_flag, tp.wait_budget));
+      if (!ok) break;
+      if (!end) {
+        // Rows into the swizzled tiles.  Columns past D are zero (K's are, by
+        // the tensor map's fill); rows past the block's are not written: their
+        // results are not read.
+        constexpr int kChunks = DP / 8;  // 16-byte chunks a row
+        uint8_t* tile = smem + Lo::kOffQ + (two ? 0 : (int)(n & 1) * Lo::kTileBytes);
+        const uint32_t tile_s = smem_addr(tile);
+        const bool async = tp.q_vec && tp.sign > 0.0f;
+        for (int i = lt; i < c.rows * kChunks; i += 64) {
+          const int a = i / kChunks, ch = i % kChunks;
+          const unsigned row = c.row0 + a, tok = row / (unsigned)G, g = row - tok * G;
+          const __nv_bfloat16* src = (const __nv_bfloat16*)p.a.q +
+                                     (long long)(c.q0 + tok) * p.a.q_token_stride +
+                                     (long long)(c.h * G + g) * p.a.q_head_stride;
+          const uint32_t off = (uint32_t)((a >> 7) * Lo::kTileBytes + (ch >> 3) * Lo::kHalfBytes) +
+                               swz(a & 127, ch & 7);
+          const bool in = ch * 8 < D;  // D % 8 == 0
+          if (async) {  // (no bytes read past D: zeros)
+            cp_async16(tile_s + off, in ? src + ch * 8 : src, in ? 16 : 0);
+            continue;
+          }
+          uint32_t v[4] = {0u, 0u, 0u, 0u};
+          if (in) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[k] = (uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k]) |
+                     ((uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k + 1]) << 16);
+              if (tp.sign < 0.0f) v[k] ^= 0x80008000u;
+            }
+          }
+          *(uint4*)(tile + off) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        cp_async_wait();
+        fence_proxy_async();
+        w.next();
+        c.next_joined = !two && !w.done() && w.block_rows() <= 128;
+      }
+      if (lt == 0) infos[n & 1] = c;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[n & 1]);
+      if (end) break;
+      prev_two = two;
+    }
   }
   if (*abort_flag && lane == 0) flag_status(p.status, DSPARK_DEV_TIMEOUT);
   tc_fence_before();

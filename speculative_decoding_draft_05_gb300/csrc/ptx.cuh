@@ -56,6 +56,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait for roles that run ahead and wait long: sleeps between polls, so
+// that the poll takes no issue slots from the warps that compute.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort_flag, long long budget) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    __nanosleep(200);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > budget) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
 // Bounded wait without the abort flag, for draining copies already in flight.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, long long budget) {
   const long long t0 = clock64();
