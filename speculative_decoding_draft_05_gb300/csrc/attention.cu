@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kThreads)
 attention_simt_kernel(const AttnParams p) {
   extern __shared__ float4 smem4[];
   __shared__ AttnStart st;
+  __shared__ int flags;
   __shared__ __align__(16) float sp[kThreads / 32][kTN][kRowsPerWarp];  // probabilities of a warp's rows
   const int D = p.a.c.head_dim, ld = NI * 32 + 4;
   float* sq = (float*)smem4;       // [kMR][ld], scaled by scale * log2 e
@@ -37,9 +38,12 @@ attention_simt_kernel(const AttnParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int S = p.a.c.page_size, G = p.a.G;
 
-  attn_plan<kMR, kTN>(p, &st);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) flags = 0;
+  __syncthreads();
+  attn_plan<kMR, kTN>(p, &st, &flags);
   long long u0;
-  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, st, &u0);
+  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, st, &flags, &u0);
   if (threadIdx.x == 0) attn_write_cut(p, w, u0);
 
   for (; !w.done(); w.next()) {
@@ -75,7 +79,7 @@ attention_simt_kernel(const AttnParams p) {
         if (j < w.end) {
           page = p.a.a.page_table[(size_t)w.r * p.a.a.max_pages + j / S];
           if (page < 0 || page >= p.a.c.n_pages) {
-            if (lane == 0) flag_status(p.status, DSPARK_DEV_BAD_INPUT);
+            if (lane == 0) flag_status(&flags, DSPARK_DEV_BAD_INPUT);
             page = page < 0 ? 0 : p.a.c.n_pages - 1;
           }
         }
@@ -165,6 +169,8 @@ attention_simt_kernel(const AttnParams p) {
       }
     }
   }
+  __syncthreads();
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = flags;
 }
 
 // Adds the pieces of the items that shares cut.  Block (b, y): the item that
@@ -173,7 +179,16 @@ attention_simt_kernel(const AttnParams p) {
 template <typename T>
 __global__ void __launch_bounds__(256)
 attention_combine_kernel(const AttnParams p, int MR, int ctas) {
+  // Launched while the attention kernel runs; everything below reads what it wrote.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // the call's status word
+    int f = 0;
+    for (int i = threadIdx.x; i < ctas; i += 32) f |= __ldcg(p.flags + i);
+    f = __reduce_or_sync(0xffffffffu, f);
+    if (threadIdx.x == 0) *p.status = f;
+  }
   const int c = blockIdx.x + 1;
+  if (c >= ctas) return;
   const CutItem it = p.cuts[c];
   if (!it.valid) return;
   const long long units = *p.units;
@@ -242,12 +257,18 @@ cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStream_t s) {
-  const dim3 grid(ctas - 1, MR / 32);
-  if (p.a.dtype == DSPARK_BF16)
-    attention_combine_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p, MR, ctas);
-  else
-    attention_combine_kernel<float><<<grid, 256, 0, s>>>(p, MR, ctas);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas > 1 ? ctas - 1 : 1, MR / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.a.dtype == DSPARK_BF16
+             ? cudaLaunchKernelEx(&cfg, attention_combine_kernel<__nv_bfloat16>, p, MR, ctas)
+             : cudaLaunchKernelEx(&cfg, attention_combine_kernel<float>, p, MR, ctas);
 }
 
 size_t attention_workspace_bytes(int dtype, int head_dim) {
@@ -258,13 +279,12 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
-  if (e != cudaSuccess || a.a.n_tokens == 0) return e;
+  if (a.a.n_tokens == 0) return cudaMemsetAsync(ws, 0, sizeof(int), s);
   if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
-  AttnParams p{a, (int*)ws, (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
+  AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
                (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f};
-  e = a.dtype == DSPARK_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);
+  const cudaError_t e = a.dtype == DSPARK_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(p, kMR, kSimtCtas, s);
 }

@@ -4,13 +4,13 @@
 // An item is a block of up to MR rows of one request's chunk for one K/V head.
 // A row is (token, query head of the group): row = token * G + g, so all G
 // query heads that share a K/V head read its tiles once.  An item walks its
-// keys in tiles of TN; a unit of work is one tile of one item (an item without
-// keys is one unit).  The units of all items, in the order request, row block,
-// head, tile, are cut into equal contiguous shares, one a CTA: short and long
-// requests, many rows and few, all load every SM alike.  An item cut by a
-// share's end leaves partial results (max, sum, unnormalised output in fp32),
-// which the combine kernel adds in the order of the shares, so results do not
-// depend on timing.
+// keys in tiles of TN; its work is counted as one unit a tile (an item without
+// keys has one) and kAttnItemUnits more for its start and end.  The units of
+// all items, in the order request, row block, head, tile, are cut into equal
+// contiguous shares, one a CTA: short and long requests, many rows and few,
+// all load every SM alike.  An item cut by a share's end leaves partial results
+// (max, sum, unnormalised output in fp32), which the combine kernel adds in
+// the order of the shares, so results do not depend on timing.
 #pragma once
 
 #include "common.cuh"
@@ -20,22 +20,30 @@ namespace dspark {
 
 constexpr int kAttnMaxCtas = 320;  // CTAs of one attention launch, at most
 
+// Units that an item counts beyond its tiles: its start and end (Q, merging the
+// streams, writing the result) cost a CTA about as much as two tiles.  Measured
+// with 64 requests of 500 .. 8192 positions (verify chunks, 8 K/V heads): the
+// CTAs' times spread over 165 .. 244 us without it, around 190 us with it.
+constexpr int kAttnItemUnits = 2;
+
 // A cut item, written by the CTA whose share begins inside it.
 struct CutItem {
   int valid, r, m, h;     // request, row block, K/V head
   int n, q0, rows, n_tiles;  // chunk length, first token, rows of the block, tiles
-  long long u0;           // the item's first unit
+  long long u0;           // the unit of the item's first tile
   long long pad;
 };
 
-// Workspace: status word, [256] total units, cut items, partial (m, l) and O.
+// Workspace: status word, total units, per-CTA status bits, cut items, partial
+// (m, l) and O.  Nothing in it has to be cleared before a call.
 struct AttnWorkspace {
-  size_t units, cuts, stats, out, total;
+  size_t units, flags, cuts, stats, out, total;
 };
 inline AttnWorkspace attn_workspace_layout(int MR, int D) {
   AttnWorkspace w;
   w.units = 64;
-  w.cuts = 256;
+  w.flags = 256;
+  w.cuts = align_up256(w.flags + kAttnMaxCtas * sizeof(int));
   w.stats = align_up256(w.cuts + kAttnMaxCtas * sizeof(CutItem));
   w.out = align_up256(w.stats + (size_t)kAttnMaxCtas * 2 * MR * sizeof(float2));
   w.total = align_up256(w.out + (size_t)kAttnMaxCtas * 2 * MR * D * sizeof(float));
@@ -44,7 +52,8 @@ inline AttnWorkspace attn_workspace_layout(int MR, int D) {
 
 struct AttnParams {
   AttnArgs a;
-  int* status;
+  int* status;       // written by the combine
+  int* flags;        // [grid] status bits of each CTA
   long long* units;  // total units (for the combine)
   CutItem* cuts;     // [grid]
   float2* stats;     // [grid][2][MR] (m, l), m in log2 units
@@ -92,9 +101,9 @@ template <int MR, int TN>
 __device__ __forceinline__ long long attn_request_units(const AttnRequest& q, int G, int Hkv) {
   const long long rows = (long long)q.n * G;
   if (rows == 0) return 0;
-  if (rows <= MR) return (long long)Hkv * attn_tiles<TN>(q.L);
+  if (rows <= MR) return (long long)Hkv * (attn_tiles<TN>(q.L) + kAttnItemUnits);
   const int blocks = (int)((rows + MR - 1) / MR);
-  long long u = 0;
+  long long u = (long long)blocks * kAttnItemUnits;
   for (int m = 0; m < blocks; ++m) u += attn_tiles<TN>(attn_item_end<MR>(q, G, m));
   return u * Hkv;
 }
@@ -110,16 +119,25 @@ __device__ __forceinline__ long long attn_share(long long units, int ctas, int c
 template <int MR, int TN>
 struct AttnWalk {
   const AttnParams* p;
+  int* flags;        // the CTA's status bits (shared memory)
   AttnRequest q;
   int r, m, h;       // current item: request, row block, K/V head
   int end, n_tiles;  // its keys and tiles
-  int t0;            // first tile of the current piece
-  int left;          // units of the share from t0 on
+  int pos;           // the piece's first unit within the item
+  int left;          // units of the share from there on
 
   __device__ __forceinline__ bool done() const { return left <= 0; }
-  __device__ __forceinline__ int first_tile() const { return t0; }
+  // (the item's first kAttnItemUnits units stand for no tile)
+  __device__ __forceinline__ int first_tile() const {
+    return pos > kAttnItemUnits ? pos - kAttnItemUnits : 0;
+  }
   __device__ __forceinline__ int last_tile() const {  // one past the piece's last tile
-    return n_tiles - t0 < left ? n_tiles : t0 + left;
+    const int e = pos + left - kAttnItemUnits;
+    return e < n_tiles ? e : n_tiles;
+  }
+  // A share that ends before the item's first tile has nothing of it.
+  __device__ __forceinline__ void drop_empty() {
+    if (left > 0 && last_tile() <= first_tile()) left = 0;
   }
   __device__ __forceinline__ int block_rows() const {
     const long long rest = (long long)q.n * p->a.G - (long long)m * MR;
@@ -127,23 +145,25 @@ struct AttnWalk {
   }
 
   __device__ __forceinline__ void next() {
-    left -= last_tile() - t0;
+    left -= n_tiles + kAttnItemUnits - pos;
     if (done()) return;
-    t0 = 0;
-    if (++h < p->a.c.heads) return;
-    h = 0;
-    if ((long long)(++m) * MR >= (long long)q.n * p->a.G) {
-      m = 0;
-      do {
-        if (++r >= p->a.a.R) {  // (not reached: the units count the items)
-          left = 0;
-          return;
-        }
-        q = attn_request(p->a.a, p->a.c.page_size, r, p->status);
-      } while (q.n == 0);
+    pos = 0;
+    if (++h >= p->a.c.heads) {
+      h = 0;
+      if ((long long)(++m) * MR >= (long long)q.n * p->a.G) {
+        m = 0;
+        do {
+          if (++r >= p->a.a.R) {  // (not reached: the units count the items)
+            left = 0;
+            return;
+          }
+          q = attn_request(p->a.a, p->a.c.page_size, r, flags);
+        } while (q.n == 0);
+      }
+      end = attn_item_end<MR>(q, p->a.G, m);
+      n_tiles = attn_tiles<TN>(end);
     }
-    end = attn_item_end<MR>(q, p->a.G, m);
-    n_tiles = attn_tiles<TN>(end);
+    drop_empty();
   }
 };
 
@@ -156,15 +176,16 @@ struct AttnStart {
 };
 
 // All threads of the CTA (a multiple of 32, at most 1024).  Ends with a barrier.
+// *flags (shared memory) collects the CTA's status bits.
 template <int MR, int TN>
-__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st) {
+__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st, int* flags) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int R = p.a.a.R;
   const int per = (R + (int)blockDim.x - 1) / (int)blockDim.x;
   const int r0 = min(R, (int)threadIdx.x * per), r1 = min(R, r0 + per);
   long long mine = 0;
   for (int r = r0; r < r1; ++r)
-    mine += attn_request_units<MR, TN>(attn_request(p.a.a, p.a.c.page_size, r, p.status), p.a.G,
+    mine += attn_request_units<MR, TN>(attn_request(p.a.a, p.a.c.page_size, r, flags), p.a.G,
                                        p.a.c.heads);
   long long incl = mine;
 #pragma unroll
@@ -192,7 +213,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st) {
   if (start >= at && start < at + mine) {
     for (int r = r0; r < r1; ++r) {
       const long long k = attn_request_units<MR, TN>(
-          attn_request(p.a.a, p.a.c.page_size, r, p.status), p.a.G, p.a.c.heads);
+          attn_request(p.a.a, p.a.c.page_size, r, flags), p.a.G, p.a.c.heads);
       if (start < at + k) {
         st->request = r;
         st->first = at;
@@ -205,34 +226,38 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st) {
   __syncthreads();
 }
 
-// The walk over this CTA's share, from its first item; *u0 gets that item's
-// first unit.
+// The walk over this CTA's share, from its first item; *u0 gets the unit of
+// that item's first tile.
 template <int MR, int TN>
 __device__ __forceinline__ AttnWalk<MR, TN> attn_walk(const AttnParams& p, const AttnStart& st,
-                                                      long long* u0) {
+                                                      int* flags, long long* u0) {
   AttnWalk<MR, TN> w;
   w.p = &p;
+  w.flags = flags;
   const long long u = attn_share(st.units, gridDim.x, blockIdx.x);
   w.left = (int)(attn_share(st.units, gridDim.x, blockIdx.x + 1) - u);
   long long at = st.first;
   if (w.left > 0) {
     const int G = p.a.G, Hkv = p.a.c.heads;
     w.r = st.request;
-    w.q = attn_request(p.a.a, p.a.c.page_size, w.r, p.status);
+    w.q = attn_request(p.a.a, p.a.c.page_size, w.r, flags);
     w.m = 0;
+    int per;
     for (;;) {
       w.end = attn_item_end<MR>(w.q, G, w.m);
       w.n_tiles = attn_tiles<TN>(w.end);
-      const long long k = (long long)w.n_tiles * Hkv;
+      per = w.n_tiles + kAttnItemUnits;
+      const long long k = (long long)per * Hkv;
       if (u < at + k || (long long)(w.m + 1) * MR >= (long long)w.q.n * G) break;
       at += k;
       ++w.m;
     }
-    w.h = (int)((u - at) / w.n_tiles);
-    at += (long long)w.h * w.n_tiles;
-    w.t0 = (int)(u - at);
+    w.h = (int)((u - at) / per);
+    at += (long long)w.h * per;
+    w.pos = (int)(u - at);
+    w.drop_empty();
   }
-  *u0 = at;
+  *u0 = at + kAttnItemUnits;
   return w;
 }
 
@@ -241,7 +266,7 @@ template <int MR, int TN>
 __device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnWalk<MR, TN>& w,
                                                long long u0) {
   CutItem c;
-  c.valid = !w.done() && w.t0 > 0;
+  c.valid = !w.done() && w.first_tile() > 0;
   if (c.valid) {
     c.r = w.r, c.m = w.m, c.h = w.h;
     c.n = w.q.n, c.q0 = w.q.q0, c.rows = w.block_rows(), c.n_tiles = w.n_tiles;

@@ -68,7 +68,7 @@ struct Layout {
   static constexpr int kOffStart = kOffMerge;                        // (before the first merge)
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
   static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1;
-  static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 8 + 15) & ~15);  // PieceInfo [2]
+  static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 12 + 15) & ~15);  // PieceInfo [2]
   static constexpr int kEnd = kOffPiece + 2 * 64;
   // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
   // static shared memory; the slack covers most others, and the kernel checks.
@@ -269,8 +269,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const AttnParams& p = tp.p;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (smem + Lo::kEnd > smem_raw + Lo::kBytes) {  // (never: see Layout)
-    if (threadIdx.x == 0) flag_status(p.status, DSPARK_DEV_TIMEOUT);
+    if (threadIdx.x == 0) p.flags[blockIdx.x] = DSPARK_DEV_TIMEOUT;
     return;
   }
   uint64_t* bars = (uint64_t*)(smem + Lo::kOffBar);
@@ -285,6 +286,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* drain = pair + 1;
   uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  int* flags = (int*)(tmem_slot + 2);  // the CTA's status bits
   AttnStart* st = (AttnStart*)(smem + Lo::kOffStart);
   float2* merge = (float2*)(smem + Lo::kOffMerge);
   PieceInfo* infos = (PieceInfo*)(smem + Lo::kOffPiece);
@@ -305,8 +307,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     mbar_init(pair, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *flags = 0;
     fence_barrier_init();
   }
+  __syncthreads();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
@@ -314,7 +318,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  attn_plan<kMR, kTN>(p, st);  // ends with a barrier
+  attn_plan<kMR, kTN>(p, st, flags);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -327,7 +331,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // ------------------------------------------------------------ producer
     regs_dec<kRegsOther>();
     long long u0;
-    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, &u0);
+    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, flags, &u0);
     const int bt = tp.box_tokens, E = kTN / bt;  // boxes along a tile's keys
     const int S = p.a.c.page_size;
     const int e = lane / Lo::kHalves, half = lane % Lo::kHalves;  // this lane's box
@@ -360,7 +364,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (e >= E || key >= w.end) return -1;
         int pg = __ldg(table + key / S);
         if (pg < 0 || pg >= p.a.c.n_pages) {
-          flag_status(p.status, DSPARK_DEV_BAD_INPUT);
+          flag_status(flags, DSPARK_DEV_BAD_INPUT);
           pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
         }
         return pg;
@@ -733,7 +737,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // ------------------------------------------------------------ loaders
     regs_dec<kRegsOther>();
     long long u0;
-    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, &u0);
+    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, flags, &u0);
     if (threadIdx.x == (kMmaWarp + 1) * 32) attn_write_cut(p, w, u0);
     const int D = p.a.c.head_dim, G = p.a.G;
     const int lt = threadIdx.x - (kMmaWarp + 1) * 32;  // 0 .. 63
@@ -741,8 +745,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     for (uint32_t n = 0;; ++n) {
       const bool end = w.done();
       PieceInfo c;
-      c.t0 = w.t0;
-      c.nt = end ? 0 : w.last_tile() - w.t0;
+      c.t0 = end ? 0 : w.first_tile();
+      c.nt = end ? 0 : w.last_tile() - c.t0;
       c.rows = end ? 0 : w.block_rows();
       c.row0 = w.m * kMR;
       c.h = w.h;
@@ -805,9 +809,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       prev_two = two;
     }
   }
-  if (*abort_flag && lane == 0) flag_status(p.status, DSPARK_DEV_TIMEOUT);
+  if (*abort_flag && lane == 0) flag_status(flags, DSPARK_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = *flags;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");
@@ -889,7 +894,7 @@ size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout
 cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
   TcParams tp;
-  tp.p = AttnParams{a, (int*)ws, (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
+  tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),
                     // (not 0: a masked score is -inf times this)
                     fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f)};
