@@ -54,6 +54,10 @@ CacheView layer_view(const dspark_cache* c, int layer) {
   return v;
 }
 
+PagePool pool_of(const dspark_cache* c) {
+  return PagePool{layer_view(c, 0), esize_of(c->dtype), c->layers, c->layer_stride};
+}
+
 int check_meta(const dspark_cache* cache, const PageMeta& m, void* workspace, size_t bytes) {
   int st = check_cache(cache, 0);
   if (st != DSPARK_OK) return st;
@@ -152,11 +156,7 @@ int dspark_pages_resize(const dspark_cache* cache, const int32_t* page_table, co
   char* ws = (char*)workspace;
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(kKindPages, s);
-  cudaError_t e = launch_pages_resize(m, new_len, free_pages, ws, w, s);
-  if (e == cudaSuccess)
-    e = launch_pages_copy(layer_view(cache, 0), esize_of(cache->dtype), cache->layers,
-                          cache->layer_stride, (int*)(ws + w.src), (int*)(ws + w.dst),
-                          (int*)(ws + w.counters) + 2, R, (int*)ws, s);
+  const cudaError_t e = launch_pages_resize(pool_of(cache), m, new_len, free_pages, ws, w, s);
   prof_end(s);
   return e != cudaSuccess ? cuda_fail(e, "pages_resize") : DSPARK_OK;
 }
@@ -176,11 +176,8 @@ int dspark_pages_fork(const dspark_cache* cache, const int32_t* page_table, cons
   char* ws = (char*)workspace;
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(kKindPages, s);
-  cudaError_t e = launch_pages_fork(m, parent, child, n, free_pages, ws, w, s);
-  if (e == cudaSuccess)
-    e = launch_pages_copy(layer_view(cache, 0), esize_of(cache->dtype), cache->layers,
-                          cache->layer_stride, (int*)(ws + w.src), (int*)(ws + w.dst),
-                          (int*)(ws + w.counters) + 2, n, (int*)ws, s);
+  const cudaError_t e =
+      launch_pages_fork(pool_of(cache), m, parent, child, n, free_pages, ws, w, s);
   prof_end(s);
   return e != cudaSuccess ? cuda_fail(e, "pages_fork") : DSPARK_OK;
 }
@@ -198,11 +195,7 @@ int dspark_pages_compact(const dspark_cache* cache, const int32_t* page_table,
   char* ws = (char*)workspace;
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(kKindPages, s);
-  cudaError_t e = launch_pages_compact(m, page_map, n_live, ws, w, s);
-  if (e == cudaSuccess)
-    e = launch_pages_copy(layer_view(cache, 0), esize_of(cache->dtype), cache->layers,
-                          cache->layer_stride, (int*)(ws + w.src), (int*)(ws + w.dst),
-                          (int*)(ws + w.counters) + 2, cache->n_pages, (int*)ws, s);
+  const cudaError_t e = launch_pages_compact(pool_of(cache), m, page_map, n_live, ws, w, s);
   prof_end(s);
   return e != cudaSuccess ? cuda_fail(e, "pages_compact") : DSPARK_OK;
 }
@@ -216,10 +209,7 @@ int dspark_pages_copy(const dspark_cache* cache, const int32_t* src, const int32
   if (st != DSPARK_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(kKindPages, s);
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
-  if (e == cudaSuccess)
-    e = launch_pages_copy(layer_view(cache, 0), esize_of(cache->dtype), cache->layers,
-                          cache->layer_stride, src, dst, nullptr, n, (int*)workspace, s);
+  const cudaError_t e = launch_pages_copy(pool_of(cache), src, dst, n, (int*)workspace, s);
   prof_end(s);
   return e != cudaSuccess ? cuda_fail(e, "pages_copy") : DSPARK_OK;
 }

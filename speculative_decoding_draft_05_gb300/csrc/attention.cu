@@ -194,8 +194,9 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
   const long long units = *p.units;
   if (it.u0 < attn_share(units, ctas, c - 1)) return;
   const long long end = it.u0 + it.n_tiles;
-  int last = c;  // the last share with a piece
-  while (last + 1 < ctas && attn_share(units, ctas, last + 1) < end) ++last;
+  // The last share with a piece: the one that holds unit end - 1.
+  const long long shares = units < ctas ? units : ctas;
+  const int last = (int)((end * shares - 1) / units);
   const int n = last - c + 2;  // pieces: slot 1 of CTA c - 1, slot 0 of c .. last
   const int lane = threadIdx.x & 31, D = p.a.c.head_dim, G = p.a.G;
   const int warps = gridDim.y * 8;
@@ -209,6 +210,7 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
     const float ms = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
     float o[8] = {};
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const size_t at = (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
       const float2 st = p.stats[at];

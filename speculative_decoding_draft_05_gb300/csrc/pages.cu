@@ -5,7 +5,8 @@
 // The tables (page table, lengths, reference counts) are small next to the
 // cache; what costs there is latency, so each operation is one kernel of one
 // thread-block cluster (8 CTAs x 1024 threads, phases separated by the
-// hardware's cluster barrier) instead of a chain of launches.  Which page an
+// hardware's cluster barrier) and the copy kernel behind it, instead of a
+// chain of launches.  Which page an
 // allocation takes depends on nothing but the inputs: the lowest free ids, in
 // the order of the requests, found by a prefix sum over the counts.
 #include <cooperative_groups.h>
@@ -23,8 +24,11 @@ constexpr int kClusterCtas = 8;
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
 
-// Counter words at the start of the workspace (the status word is word 0).
-enum { kCtrStatus = 0, kCtrNeed = 1, kCtrCopies = 2, kCtrFreed = 3, kCtrWords = 4 };
+// Words at the start of the workspace.  The table kernels run in one cluster
+// and leave what the copy kernel behind them (which ends every call) needs:
+// each CTA's status bits and count of pages that became free, the number of
+// copies, and the free pages without those.
+enum { kWordStatus = 0, kWordCopies = 1, kWordFree = 2, kWordFlags = 8, kWordFreed = 16 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -73,32 +77,38 @@ __device__ __forceinline__ void page_share(int n_pages, int rank, int& lo, int& 
   hi = a + per < n_pages ? (int)(a + per) : n_pages;
 }
 
-// Counts per warp -> this warp's exclusive prefix over the whole cluster and
-// the cluster's total.  Ends with a cluster barrier, so that it can be called
-// again; all threads of the cluster call it.
-__device__ __forceinline__ int cluster_prefix(cg::cluster_group& cl, int warp_count, int* sm,
-                                              int* total) {
+// N counts per warp -> this warp's exclusive prefixes over the whole cluster
+// and the cluster's totals, with one cluster barrier.  sm[N][kPageWarps + 1] is
+// this call's own; no CTA may leave the kernel before a further barrier (the
+// others read its totals).
+template <int N>
+__device__ __forceinline__ void cluster_prefix(cg::cluster_group& cl, const int (&warp_count)[N],
+                                               int (*sm)[kPageWarps + 1], int (&prefix)[N],
+                                               int (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) sm[warp] = warp_count;
+  if (lane == 0)
+    for (int k = 0; k < N; ++k) sm[k][warp] = warp_count[k];
   __syncthreads();
-  if (warp == 0) {
-    const int w = sm[lane];
+  if (warp < N) {
+    const int w = sm[warp][lane];
     const int wi = warp_scan_incl(w);
-    sm[lane] = wi - w;
-    if (lane == 31) sm[kPageWarps] = wi;  // this CTA's total
+    sm[warp][lane] = wi - w;
+    if (lane == 31) sm[warp][kPageWarps] = wi;  // this CTA's total
   }
   cl.sync();
-  int before = 0, all = 0;
   const int rank = (int)cl.block_rank();
-  for (int c = 0; c < kClusterCtas; ++c) {
-    const int t = *cl.map_shared_rank(&sm[kPageWarps], c);
-    all += t;
-    if (c < rank) before += t;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int c = 0; c < kClusterCtas; ++c) {
+      const int t = *cl.map_shared_rank(&sm[k][kPageWarps], c);
+      all += t;
+      if (c < rank) before += t;
+    }
+    prefix[k] = before + sm[k][warp];
+    total[k] = all;
   }
-  const int r = before + sm[warp];
-  *total = all;
-  cl.sync();
-  return r;
 }
 
 // Counts the pages of [lo, hi) for which pred(p) holds, by one warp.
@@ -134,30 +144,58 @@ __device__ __forceinline__ int clamp_len(int n, int most, int* status) {
   return n;
 }
 
+// Copies the tables into the outputs where those are arrays of their own.
+struct MetaCopy {
+  const int32_t* from[3];
+  int32_t* to[3];
+  size_t n[3];
+};
+__device__ __forceinline__ void copy_meta(const MetaCopy& c, size_t t, size_t T) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (c.from[k] == c.to[k]) continue;
+    const bool vec = (((uintptr_t)c.from[k] | (uintptr_t)c.to[k]) & 15u) == 0;
+    const size_t n4 = vec ? c.n[k] / 4 : 0;
+#pragma unroll 4
+    for (size_t i = t; i < n4; i += T) ((int4*)c.to[k])[i] = ((const int4*)c.from[k])[i];
+    for (size_t i = 4 * n4 + t; i < c.n[k]; i += T) c.to[k][i] = c.from[k][i];
+  }
+}
+__global__ void __launch_bounds__(256) meta_copy_kernel(const MetaCopy c) {
+  copy_meta(c, (size_t)blockIdx.x * blockDim.x + threadIdx.x, (size_t)gridDim.x * blockDim.x);
+}
+
 struct ResizeArgs {
   PageMeta m;
+  MetaCopy copy;  // done here first (all from == to: not)
   const int32_t* new_len;
-  int32_t* free_pages;
-  int* ctr;     // counter words
-  int* start;   // [R]: first allocation of the request, bit 31: it copies a shared page
-  int* list;    // [n_pages]: the lowest free pages in order
-  int* src;     // [R] copy list
+  int* words;
+  int* start;  // [R]: first allocation of the request
+  int* cow;    // [R]: copies before it; bit 31: it copies a shared page
+  int* list;   // [n_pages]: the lowest free pages in order
+  int* src;    // [R] copy list
   int* dst;
 };
 
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
 pages_resize_kernel(const ResizeArgs a) {
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int sm[kPageWarps + 1];
+  __shared__ int sm[1][kPageWarps + 1], scan[kPageWarps + 1], flags, freed, need_sm;
   const int rank = (int)cl.block_rank();
   const int lane = threadIdx.x & 31;
+  const int gthread = rank * kPageThreads + (int)threadIdx.x;
   const int gwarp = rank * kPageWarps + (threadIdx.x >> 5), warps = kClusterCtas * kPageWarps;
   const PageMeta& m = a.m;
   const int S = m.page_size, P = m.max_pages;
   const long long most_l = (long long)P * S;
   const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
   int* const rc = m.refcount_out;
-  int* const status = a.ctr + kCtrStatus;
+  int* const status = &flags;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) flags = freed = 0;
+  __syncthreads();
+  copy_meta(a.copy, gthread, kClusterCtas * kPageThreads);
+  cl.sync();
 
   // 1. Pages past the new length lose a reference.
   for (int r = gwarp; r < m.R; r += warps) {
@@ -178,9 +216,9 @@ pages_resize_kernel(const ResizeArgs a) {
   int lo, hi;
   page_share(m.n_pages, rank, lo, hi);
   const auto is_free = [&](int p) { return __ldcg(&rc[p]) == 0; };
-  const int mine = warp_count(lo, hi, is_free);
+  const int mine[1] = {warp_count(lo, hi, is_free)};
   if (rank == 0) {
-    int base = 0;
+    int base = 0, copies = 0;
     for (int r0 = 0; r0 < m.R; r0 += kPageThreads) {
       const int r = r0 + (int)threadIdx.x;
       int need = 0, cow = 0;
@@ -188,7 +226,7 @@ pages_resize_kernel(const ResizeArgs a) {
         const int L = clamp_len(m.kv_len[r], most, status), N = clamp_len(a.new_len[r], most, status);
         if (N > L) {
           if (L % S != 0) {
-            const int p = m.table_out[(size_t)r * P + L / S];
+            const int p = __ldcg(&m.table_out[(size_t)r * P + L / S]);
             if (p < 0 || p >= m.n_pages)
               flag_status(status, DSPARK_DEV_BAD_INPUT);
             else
@@ -197,20 +235,28 @@ pages_resize_kernel(const ResizeArgs a) {
           need = cow + ceil_div(N, S) - ceil_div(L, S);
         }
       }
-      int total;
-      const int at = block_scan_excl(need, sm, &total);
-      if (r < m.R) a.start[r] = (int)((unsigned)(base + at) | (cow ? 0x80000000u : 0u));
+      int total, n_cow;
+      const int at = block_scan_excl(need, scan, &total);
+      const int ci = block_scan_excl(cow, scan, &n_cow);
+      if (r < m.R) {
+        a.start[r] = base + at;
+        a.cow[r] = (int)((unsigned)(copies + ci) | (cow ? 0x80000000u : 0u));
+      }
       base += total;
+      copies += n_cow;
     }
-    if (threadIdx.x == 0) a.ctr[kCtrNeed] = base;
+    if (threadIdx.x == 0) {
+      need_sm = base;
+      a.words[kWordCopies] = copies;
+    }
   }
-  int n_free;
-  const int at = cluster_prefix(cl, mine, sm, &n_free);
-  const int need_all = __ldcg(&a.ctr[kCtrNeed]);
-  if (need_all > n_free && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
+  int at[1], n_free[1];
+  cluster_prefix<1>(cl, mine, sm, at, n_free);
+  const int need_all = *cl.map_shared_rank(&need_sm, 0);
+  if (need_all > n_free[0] && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
 
   // 3. The lowest free pages, as many as are wanted.
-  warp_list(lo, hi, at, need_all, is_free, [&](int i, int p) { a.list[i] = p; });
+  warp_list(lo, hi, at[0], need_all, is_free, [&](int i, int p) { a.list[i] = p; });
   cl.sync();
 
   // 4. Each request takes its share of the list.
@@ -218,50 +264,57 @@ pages_resize_kernel(const ResizeArgs a) {
     const int L = clamp_len(m.kv_len[r], most, status), N = clamp_len(a.new_len[r], most, status);
     int out_len = N;
     if (N > L) {
-      const unsigned st = (unsigned)__ldcg(&a.start[r]);
-      const int cow = (int)(st >> 31), first = (int)(st & 0x7fffffffu);
+      const unsigned cw = (unsigned)__ldcg(&a.cow[r]);
+      const int cow = (int)(cw >> 31), first = __ldcg(&a.start[r]);
       const int old = ceil_div(L, S), need = cow + ceil_div(N, S) - old;
-      int got = n_free - first;
+      int got = n_free[0] - first;
       got = got < 0 ? 0 : got > need ? need : got;
+      int32_t* row = m.table_out + (size_t)r * P;
+      int from = -1, to = -1;
       if (cow && got == 0) {
         out_len = L;
       } else {
         const int grown = got - cow;
-        int32_t* row = m.table_out + (size_t)r * P;
         for (int j = lane; j < grown; j += 32) {
           const int p = __ldcg(&a.list[first + cow + j]);
           row[old + j] = p;
           rc[p] = 1;
         }
         if (cow && lane == 0) {
-          const int from = row[L / S], to = __ldcg(&a.list[first]);
+          from = __ldcg(&row[L / S]);
+          to = __ldcg(&a.list[first]);
           row[L / S] = to;
           rc[to] = 1;
-          if (atomicSub(&rc[from], 1) == 1) atomicAdd(&a.ctr[kCtrFreed], 1);
-          const int i = atomicAdd(&a.ctr[kCtrCopies], 1);
-          a.src[i] = from;
-          a.dst[i] = to;
+          if (atomicSub(&rc[from], 1) == 1) atomicAdd(&freed, 1);
         }
         const long long room = (long long)(old + grown) * S;
         out_len = room < N ? (int)room : N;
+      }
+      if (cow && lane == 0) {
+        a.src[cw & 0x7fffffffu] = from;
+        a.dst[cw & 0x7fffffffu] = to;  // -1: not copied, the pool ran out
       }
     }
     __syncwarp();
     if (lane == 0) m.kv_len_out[r] = out_len;
   }
-  cl.sync();
-  if (rank == 0 && threadIdx.x == 0)
-    *a.free_pages = n_free - (need_all < n_free ? need_all : n_free) + __ldcg(&a.ctr[kCtrFreed]);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.words[kWordFlags + rank] = flags;
+    a.words[kWordFreed + rank] = freed;
+    if (rank == 0) a.words[kWordFree] = n_free[0] - (need_all < n_free[0] ? need_all : n_free[0]);
+  }
 }
 
 struct ForkArgs {
   PageMeta m;
+  MetaCopy copy;
   const int32_t *parent, *child;
   int n;
-  int32_t* free_pages;
-  int* ctr;
-  int* start;  // [n <= R]: first allocation, bit 31: a partly filled page is copied; -1 skipped
-  int* len;    // [n] the parent's length
+  int* words;
+  int* start;  // [n <= R]: first allocation
+  int* len;    // [n] the parent's length, -1: the pair is skipped
+  int* owner;  // [R]: the first pair that names a child
   int* list;
   int* src;
   int* dst;
@@ -270,34 +323,35 @@ struct ForkArgs {
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
 pages_fork_kernel(const ForkArgs a) {
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int sm[kPageWarps + 1];
+  __shared__ int sm[1][kPageWarps + 1], scan[kPageWarps + 1], flags, need_sm;
   const int rank = (int)cl.block_rank();
   const int lane = threadIdx.x & 31;
-  const int gthread = rank * kPageThreads + (int)threadIdx.x;
   const int gwarp = rank * kPageWarps + (threadIdx.x >> 5), warps = kClusterCtas * kPageWarps;
   const PageMeta& m = a.m;
   const int S = m.page_size, P = m.max_pages;
   const long long most_l = (long long)P * S;
   const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
   int* const rc = m.refcount_out;
-  int* const status = a.ctr + kCtrStatus;
-  int* const owner = a.dst;  // [R], before dst is written: the first pair that names a child
-
-  for (int r = gthread; r < m.R; r += kClusterCtas * kPageThreads) owner[r] = 0x7fffffff;
-  cl.sync();
-  for (int i = gthread; i < a.n; i += kClusterCtas * kPageThreads) {
-    const int c = a.child[i];
-    if (c >= 0 && c < m.R) atomicMin(&owner[c], i);
-  }
+  int* const status = &flags;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) flags = 0;
+  __syncthreads();
+  // Up to the last barrier only the inputs are read and, where the outputs are
+  // arrays of their own, those filled from them.
   int lo, hi;
   page_share(m.n_pages, rank, lo, hi);
-  const auto is_free = [&](int p) { return __ldcg(&rc[p]) == 0; };
-  const int mine = warp_count(lo, hi, is_free);
-  cl.sync();
-
+  const auto is_free = [&](int p) { return m.refcount[p] == 0; };
+  const int mine[1] = {warp_count(lo, hi, is_free)};
   // The pairs' needs, in order, by CTA 0.  A pair whose child holds pages, is
   // named twice or is out of range is skipped and flagged.
   if (rank == 0) {
+    for (int r = threadIdx.x; r < m.R; r += kPageThreads) a.owner[r] = 0x7fffffff;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n; i += kPageThreads) {
+      const int c = a.child[i];
+      if (c >= 0 && c < m.R) atomicMin(&a.owner[c], i);
+    }
+    __syncthreads();
     int base = 0;
     for (int i0 = 0; i0 < a.n; i0 += kPageThreads) {
       const int i = i0 + (int)threadIdx.x;
@@ -305,7 +359,7 @@ pages_fork_kernel(const ForkArgs a) {
       if (i < a.n) {
         const int p = a.parent[i], c = a.child[i];
         const bool ok = p >= 0 && p < m.R && c >= 0 && c < m.R && m.kv_len[c] == 0 &&
-                        __ldcg(&owner[c]) == i;
+                        __ldcg(&a.owner[c]) == i;
         if (ok) {
           L = clamp_len(m.kv_len[p], most, status);
           need = L % S != 0 ? 1 : 0;
@@ -322,20 +376,25 @@ pages_fork_kernel(const ForkArgs a) {
         }
       }
       int total;
-      const int at = block_scan_excl(need, sm, &total);
+      const int at = block_scan_excl(need, scan, &total);
       if (i < a.n) {
         a.start[i] = base + at;
         a.len[i] = L;
       }
       base += total;
     }
-    if (threadIdx.x == 0) a.ctr[kCtrNeed] = base;
+    if (threadIdx.x == 0) {
+      need_sm = base;
+      a.words[kWordCopies] = base;
+    }
+  } else {
+    copy_meta(a.copy, gwarp * 32 + lane - kPageThreads, (kClusterCtas - 1) * kPageThreads);
   }
-  int n_free;
-  const int at = cluster_prefix(cl, mine, sm, &n_free);
-  const int need_all = __ldcg(&a.ctr[kCtrNeed]);
-  if (need_all > n_free && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
-  warp_list(lo, hi, at, need_all, is_free, [&](int i, int p) { a.list[i] = p; });
+  int at[1], n_free[1];
+  cluster_prefix<1>(cl, mine, sm, at, n_free);
+  const int need_all = *cl.map_shared_rank(&need_sm, 0);
+  if (need_all > n_free[0] && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
+  warp_list(lo, hi, at[0], need_all, is_free, [&](int i, int p) { a.list[i] = p; });
   cl.sync();
 
   for (int i = gwarp; i < a.n; i += warps) {
@@ -345,7 +404,7 @@ pages_fork_kernel(const ForkArgs a) {
     int32_t* to = m.table_out + (size_t)a.child[i] * P;
     const int full = L / S;
     for (int j = lane; j < full; j += 32) {
-      const int p = from[j];
+      const int p = __ldcg(&from[j]);
       if (p < 0 || p >= m.n_pages)
         flag_status(status, DSPARK_DEV_BAD_INPUT);
       else
@@ -355,29 +414,34 @@ pages_fork_kernel(const ForkArgs a) {
     if (lane == 0) {
       int out_len = full * S;
       if (L % S != 0) {
-        const int k = __ldcg(&a.start[i]);
-        if (k < n_free) {
-          const int p = __ldcg(&a.list[k]);
+        const int k = __ldcg(&a.start[i]);  // also this copy's place in the list
+        int p = -1;
+        if (k < n_free[0]) {
+          p = __ldcg(&a.list[k]);
           to[full] = p;
           rc[p] = 1;
-          const int s = atomicAdd(&a.ctr[kCtrCopies], 1);
-          a.src[s] = from[full];
-          a.dst[s] = p;
           out_len = L;
         }
+        a.src[k] = __ldcg(&from[full]);
+        a.dst[k] = p;
       }
       m.kv_len_out[a.child[i]] = out_len;
     }
   }
-  if (rank == 0 && threadIdx.x == 0)
-    *a.free_pages = n_free - (need_all < n_free ? need_all : n_free);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.words[kWordFlags + rank] = flags;
+    a.words[kWordFreed + rank] = 0;
+    if (rank == 0) a.words[kWordFree] = n_free[0] - (need_all < n_free[0] ? need_all : n_free[0]);
+  }
 }
 
 struct CompactArgs {
   PageMeta m;
+  MetaCopy copy;
   int32_t* page_map;
   int32_t* n_live;
-  int* ctr;
+  int* words;
   int* src;
   int* dst;
 };
@@ -387,90 +451,76 @@ struct CompactArgs {
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
 pages_compact_kernel(const CompactArgs a) {
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int sm[kPageWarps + 1];
+  __shared__ int sm1[1][kPageWarps + 1], sm2[2][kPageWarps + 1];
   const int rank = (int)cl.block_rank();
   const int lane = threadIdx.x & 31;
   const PageMeta& m = a.m;
   const int32_t* rc = m.refcount;
-  int lo, hi, n_live, moves, n_low;
+  int lo, hi, none[1], live[1], at[2], n[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   page_share(m.n_pages, rank, lo, hi);
-  cluster_prefix(cl, warp_count(lo, hi, [&](int p) { return rc[p] > 0; }), sm, &n_live);
+  copy_meta(a.copy, rank * kPageThreads + (int)threadIdx.x, kClusterCtas * kPageThreads);
+  const int n_mine[1] = {warp_count(lo, hi, [&](int p) { return rc[p] > 0; })};
+  cluster_prefix<1>(cl, n_mine, sm1, none, live);
+  const int n_live = live[0];
   const auto high = [&](int p) { return p >= n_live && rc[p] > 0; };
   const auto low = [&](int p) { return p < n_live && rc[p] <= 0; };
-  const int at_high = cluster_prefix(cl, warp_count(lo, hi, high), sm, &moves);
-  const int at_low = cluster_prefix(cl, warp_count(lo, hi, low), sm, &n_low);
-  warp_list(lo, hi, at_high, moves, high, [&](int i, int p) { a.src[i] = p; });
-  warp_list(lo, hi, at_low, n_low, low, [&](int i, int p) { a.dst[i] = p; });
+  const int n_both[2] = {warp_count(lo, hi, high), warp_count(lo, hi, low)};
+  cluster_prefix<2>(cl, n_both, sm2, at, n);
+  warp_list(lo, hi, at[0], n[0], high, [&](int i, int p) { a.src[i] = p; });
+  warp_list(lo, hi, at[1], n[1], low, [&](int i, int p) { a.dst[i] = p; });
   for (int p = lo + lane; p < hi; p += 32)
     if (!high(p)) a.page_map[p] = rc[p] > 0 ? p : -1;
   cl.sync();
-  for (int i = rank * kPageThreads + (int)threadIdx.x; i < moves; i += kClusterCtas * kPageThreads) {
+  for (int i = rank * kPageThreads + (int)threadIdx.x; i < n[0]; i += kClusterCtas * kPageThreads) {
     const int s = __ldcg(&a.src[i]), d = __ldcg(&a.dst[i]);
     a.page_map[s] = d;
-    m.refcount_out[d] = rc[s];
+    m.refcount_out[d] = __ldcg(&rc[s]);
     m.refcount_out[s] = 0;
   }
   if (rank == 0 && threadIdx.x == 0) {
     *a.n_live = n_live;
-    a.ctr[kCtrCopies] = moves;
+    a.words[kWordCopies] = n[0];
+    a.words[kWordStatus] = 0;  // (raised by the table rewrite behind this kernel)
   }
 }
 
-__global__ void __launch_bounds__(256)
-table_map_kernel(const PageMeta m, const int32_t* page_map, int* status) {
-  const size_t n = (size_t)m.R * m.max_pages;
-  const long long most_l = (long long)m.max_pages * m.page_size;
-  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (size_t)gridDim.x * blockDim.x) {
-    const int r = (int)(i / m.max_pages), j = (int)(i - (size_t)r * m.max_pages);
-    int p = m.table[i];
-    const int L = clamp_len(m.kv_len[r], most, status);
-    if (j < ceil_div(L, m.page_size)) {
-      const int q = p >= 0 && p < m.n_pages ? page_map[p] : -1;
-      if (q < 0)
-        flag_status(status, DSPARK_DEV_BAD_INPUT);
-      else
-        p = q;
-    }
-    m.table_out[i] = p;
-  }
-}
-
-// Copies the tables into the outputs where those are arrays of their own.
-struct MetaCopy {
-  const int32_t* from[3];
-  int32_t* to[3];
-  size_t n[3];
-};
-__global__ void __launch_bounds__(256) meta_copy_kernel(const MetaCopy c) {
-  const size_t t = (size_t)blockIdx.x * blockDim.x + threadIdx.x, T = (size_t)gridDim.x * blockDim.x;
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (c.from[k] == c.to[k]) continue;
-    const bool vec = (((uintptr_t)c.from[k] | (uintptr_t)c.to[k]) & 15u) == 0;
-    const size_t n4 = vec ? c.n[k] / 4 : 0;
-    for (size_t i = t; i < n4; i += T) ((int4*)c.to[k])[i] = ((const int4*)c.from[k])[i];
-    for (size_t i = 4 * n4 + t; i < c.n[k]; i += T) c.to[k][i] = c.from[k][i];
-  }
-}
-
-cudaError_t copy_meta(const PageMeta& m, bool table, bool len, bool counts, cudaStream_t s) {
+MetaCopy meta_args(const PageMeta& m, bool table, bool len) {
   MetaCopy c;
   c.from[0] = m.table, c.to[0] = table ? m.table_out : (int32_t*)m.table;
   c.n[0] = (size_t)m.R * m.max_pages;
   c.from[1] = m.kv_len, c.to[1] = len ? m.kv_len_out : (int32_t*)m.kv_len, c.n[1] = (size_t)m.R;
-  c.from[2] = m.refcount, c.to[2] = counts ? m.refcount_out : (int32_t*)m.refcount;
+  c.from[2] = m.refcount, c.to[2] = m.refcount_out;
   c.n[2] = (size_t)m.n_pages;
-  size_t most = 0;
+  return c;
+}
+
+// Tables of up to kMetaInKernel entries are copied by the cluster kernel
+// itself, larger ones by a launch of their own over all SMs (8 SMs move about
+// an eighth of a TB/s each way: at 1 M entries that is about the launch saved).
+constexpr size_t kMetaInKernel = 1u << 20;
+cudaError_t split_meta(MetaCopy* c, cudaStream_t s) {
+  size_t most = 0, all = 0;
   for (int k = 0; k < 3; ++k)
-    if (c.from[k] != c.to[k] && c.n[k] > most) most = c.n[k];
-  if (most == 0) return cudaSuccess;
+    if (c->from[k] != c->to[k]) {
+      most = most < c->n[k] ? c->n[k] : most;
+      all += c->n[k];
+    }
+  if (all <= kMetaInKernel) return cudaSuccess;
   size_t ctas = (most + 1023) / 1024;
   if (ctas > 608) ctas = 608;
-  meta_copy_kernel<<<(int)ctas, 256, 0, s>>>(c);
+  meta_copy_kernel<<<(int)ctas, 256, 0, s>>>(*c);
+  for (int k = 0; k < 3; ++k) c->from[k] = c->to[k];
   return cudaGetLastError();
 }
+
+// What the copy kernels do beside the copies, as the end of a call.
+struct CopyTail {
+  const int* words;     // the table kernel's words (null: a plain copy)
+  int32_t* free_pages;  // resize, fork: gets the free pages
+  PageMeta m;           // compact: the table is rewritten through page_map
+  const int32_t* page_map;
+};
 
 // One page of one layer's K or V per (copy, layer, K/V); 16-byte pieces where a
 // page is one dense block on 16-byte boundaries.
@@ -479,16 +529,61 @@ struct CopyArgs {
   int layers, esize, n_max;
   long long layer_stride;
   const int32_t *src, *dst;
-  const int* count;
   int* status;
+  CopyTail tail;
 };
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;  // 16-byte loads in flight a thread
 
+// Number of copies; before it, the tail of a table kernel's call.
+__device__ __forceinline__ int copy_begin(const CopyArgs& a) {
+  const CopyTail& t = a.tail;
+  if (!t.words) return a.n_max;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t.free_pages && blockIdx.x == 0 && threadIdx.x == 0) {
+    int f = 0, freed = 0;
+    for (int i = 0; i < kClusterCtas; ++i) {
+      f |= __ldcg(t.words + kWordFlags + i);
+      freed += __ldcg(t.words + kWordFreed + i);
+    }
+    *t.free_pages = __ldcg(t.words + kWordFree) + freed;
+    *a.status = f;
+  }
+  if (t.page_map) {
+    const PageMeta& m = t.m;
+    const size_t n = (size_t)m.R * m.max_pages;
+    const long long most_l = (long long)m.max_pages * m.page_size;
+    const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+    for (size_t i = (size_t)blockIdx.x * kCopyThreads + threadIdx.x; i < n;
+         i += (size_t)gridDim.x * kCopyThreads) {
+      const int r = (int)(i / m.max_pages), j = (int)(i - (size_t)r * m.max_pages);
+      int p = m.table[i];
+      const int L = clamp_len(m.kv_len[r], most, a.status);
+      if (j < ceil_div(L, m.page_size)) {
+        const int q = p >= 0 && p < m.n_pages ? __ldcg(t.page_map + p) : -1;
+        if (q < 0)
+          flag_status(a.status, DSPARK_DEV_BAD_INPUT);
+        else
+          p = q;
+      }
+      m.table_out[i] = p;
+    }
+  }
+  const int n = __ldcg(t.words + kWordCopies);
+  return n < a.n_max ? n : a.n_max;
+}
+
+// Copy i's pages; false: nothing to copy (in a call of dspark_pages_copy, out of range).
+__device__ __forceinline__ bool copy_pair(const CopyArgs& a, int i, bool flag, int& s, int& d) {
+  s = __ldcg(a.src + i), d = __ldcg(a.dst + i);
+  if (s >= 0 && s < a.c.n_pages && d >= 0 && d < a.c.n_pages) return true;
+  if (!a.tail.words && flag) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
+  return false;
+}
+
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_dense_kernel(const CopyArgs a) {
-  int n = a.count ? *a.count : a.n_max;
-  n = n < a.n_max ? n : a.n_max;
+  const int n = copy_begin(a);
   const int vecs = (int)((size_t)a.c.page_size * a.c.heads * a.c.head_dim * a.esize / 16);
   const int piece = kCopyThreads * kCopyUnroll;
   const int pieces = (vecs + piece - 1) / piece;
@@ -499,11 +594,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_dense_kernel(const Co
     const bool is_v = w & 1;
     w >>= 1;
     const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
-    const int s = a.src[i], d = a.dst[i];
-    if (s < 0 || s >= a.c.n_pages || d < 0 || d >= a.c.n_pages) {
-      if (threadIdx.x == 0) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
-      continue;
-    }
+    int s, d;
+    if (!copy_pair(a, i, threadIdx.x == 0, s, d)) continue;
     char* base = (char*)(is_v ? a.c.v : a.c.k);
     const uint4* from =
         (const uint4*)(base + (layer * a.layer_stride + s * a.c.page_stride) * a.esize);
@@ -522,8 +614,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_dense_kernel(const Co
 // Any strides: element by element, the head dimension over the lanes.
 template <typename E>
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(const CopyArgs a) {
-  int n = a.count ? *a.count : a.n_max;
-  n = n < a.n_max ? n : a.n_max;
+  const int n = copy_begin(a);
   const int rows = a.c.page_size * a.c.heads;
   const long long units = (long long)n * 2 * a.layers * rows;
   const int lane = threadIdx.x & 31;
@@ -534,11 +625,8 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(const Cop
     const bool is_v = w & 1;
     w >>= 1;
     const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
-    const int s = a.src[i], d = a.dst[i];
-    if (s < 0 || s >= a.c.n_pages || d < 0 || d >= a.c.n_pages) {
-      if (lane == 0) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
-      continue;
-    }
+    int s, d;
+    if (!copy_pair(a, i, lane == 0, s, d)) continue;
     E* base = (E*)(is_v ? a.c.v : a.c.k) + layer * a.layer_stride +
               (row / a.c.heads) * a.c.token_stride + (row % a.c.heads) * a.c.head_stride;
     const E* from = base + s * a.c.page_stride;
@@ -625,9 +713,10 @@ bool dense_page(const CacheView& c) {
 PagesWorkspace pages_workspace_layout(int R, int n_pages) {
   PagesWorkspace w;
   const size_t lists = (size_t)(R > n_pages ? R : n_pages) * sizeof(int);
-  w.counters = 0;
+  w.words = 0;
   w.start = 256;
-  w.owner = align_up256(w.start + (size_t)R * sizeof(int));
+  w.len = align_up256(w.start + (size_t)R * sizeof(int));
+  w.owner = align_up256(w.len + (size_t)R * sizeof(int));
   w.list = align_up256(w.owner + (size_t)R * sizeof(int));
   w.src = align_up256(w.list + (size_t)n_pages * sizeof(int));
   w.dst = align_up256(w.src + lists);
@@ -635,65 +724,83 @@ PagesWorkspace pages_workspace_layout(int R, int n_pages) {
   return w;
 }
 
-cudaError_t launch_pages_resize(const PageMeta& m, const int32_t* new_len, int32_t* free_pages,
-                                char* ws, const PagesWorkspace& w, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(ws + w.counters, 0, kCtrWords * sizeof(int), s);
-  if (e == cudaSuccess) e = copy_meta(m, true, false, true, s);
+static cudaError_t launch_copy(const CopyArgs& a, cudaStream_t s) {
+  const CacheView& c = a.c;
+  const size_t page_bytes = (size_t)c.page_size * c.heads * c.head_dim * a.esize;
+  const bool vec = dense_page(c) && page_bytes % 16 == 0 && (c.page_stride * a.esize) % 16 == 0 &&
+                   (a.layer_stride * a.esize) % 16 == 0 &&
+                   (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) == 0;
+  const long long per = vec ? (long long)((page_bytes / 16 + kCopyThreads * kCopyUnroll - 1) /
+                                          (kCopyThreads * kCopyUnroll))
+                            : ((long long)c.page_size * c.heads + 7) / 8;
+  // Up to 8 CTAs an SM.
+  const long long units = per * 2 * a.layers * (a.n_max > 0 ? a.n_max : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units < 1216 ? units : 1216));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.tail.words ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, vec            ? pages_copy_dense_kernel
+                                  : a.esize == 2 ? pages_copy_rows_kernel<uint16_t>
+                                                 : pages_copy_rows_kernel<uint32_t>,
+                            a);
+}
+
+cudaError_t launch_pages_resize(const PagePool& pool, const PageMeta& m, const int32_t* new_len,
+                                int32_t* free_pages, char* ws, const PagesWorkspace& w,
+                                cudaStream_t s) {
+  int* words = (int*)(ws + w.words);
+  ResizeArgs a{m, meta_args(m, true, false), new_len, words, (int*)(ws + w.start),
+               (int*)(ws + w.owner), (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst)};
+  cudaError_t e = split_meta(&a.copy, s);
   if (e != cudaSuccess) return e;
-  ResizeArgs a{m, new_len, free_pages, (int*)(ws + w.counters), (int*)(ws + w.start),
-               (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst)};
   pages_resize_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, m.R, pool.layer_stride, a.src, a.dst,
+                              words, CopyTail{words, free_pages, m, nullptr}}, s);
 }
 
-cudaError_t launch_pages_fork(const PageMeta& m, const int32_t* parent, const int32_t* child, int n,
-                              int32_t* free_pages, char* ws, const PagesWorkspace& w,
-                              cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(ws + w.counters, 0, kCtrWords * sizeof(int), s);
-  if (e == cudaSuccess) e = copy_meta(m, true, true, true, s);
+cudaError_t launch_pages_fork(const PagePool& pool, const PageMeta& m, const int32_t* parent,
+                              const int32_t* child, int n, int32_t* free_pages, char* ws,
+                              const PagesWorkspace& w, cudaStream_t s) {
+  int* words = (int*)(ws + w.words);
+  ForkArgs a{m, meta_args(m, true, true), parent, child, n, words, (int*)(ws + w.start),
+             (int*)(ws + w.len), (int*)(ws + w.owner), (int*)(ws + w.list), (int*)(ws + w.src),
+             (int*)(ws + w.dst)};
+  cudaError_t e = split_meta(&a.copy, s);
   if (e != cudaSuccess) return e;
-  ForkArgs a{m, parent, child, n, free_pages, (int*)(ws + w.counters), (int*)(ws + w.start),
-             (int*)(ws + w.owner), (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst)};
   pages_fork_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, n, pool.layer_stride, a.src, a.dst,
+                              words, CopyTail{words, free_pages, m, nullptr}}, s);
 }
 
-cudaError_t launch_pages_compact(const PageMeta& m, int32_t* page_map, int32_t* n_live, char* ws,
-                                 const PagesWorkspace& w, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(ws + w.counters, 0, kCtrWords * sizeof(int), s);
-  if (e == cudaSuccess) e = copy_meta(m, false, false, true, s);
-  if (e != cudaSuccess) return e;
-  CompactArgs a{m, page_map, n_live, (int*)(ws + w.counters), (int*)(ws + w.src),
+cudaError_t launch_pages_compact(const PagePool& pool, const PageMeta& m, int32_t* page_map,
+                                 int32_t* n_live, char* ws, const PagesWorkspace& w, cudaStream_t s) {
+  int* words = (int*)(ws + w.words);
+  CompactArgs a{m, meta_args(m, false, false), page_map, n_live, words, (int*)(ws + w.src),
                 (int*)(ws + w.dst)};
+  cudaError_t e = split_meta(&a.copy, s);
+  if (e != cudaSuccess) return e;
   pages_compact_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  size_t ctas = ((size_t)m.R * m.max_pages + 255) / 256;
-  if (ctas > 1216) ctas = 1216;
-  table_map_kernel<<<(int)ctas, 256, 0, s>>>(m, page_map, (int*)ws);
-  return cudaGetLastError();
+  return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, m.n_pages, pool.layer_stride, a.src,
+                              a.dst, words, CopyTail{words, nullptr, m, page_map}}, s);
 }
 
-cudaError_t launch_pages_copy(const CacheView& c, int esize, int layers, long long layer_stride,
-                              const int32_t* src, const int32_t* dst, const int* count, int n_max,
+cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int n,
                               int* status, cudaStream_t s) {
-  if (n_max <= 0) return cudaSuccess;
-  CopyArgs a{c, layers, esize, n_max, layer_stride, src, dst, count, status};
-  const size_t page_bytes = (size_t)c.page_size * c.heads * c.head_dim * esize;
-  const bool vec = dense_page(c) && page_bytes % 16 == 0 && (c.page_stride * esize) % 16 == 0 &&
-                   (layer_stride * esize) % 16 == 0 && (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) == 0;
-  long long units = vec ? (long long)n_max * 2 * layers *
-                              ((page_bytes / 16 + kCopyThreads * kCopyUnroll - 1) /
-                               (kCopyThreads * kCopyUnroll))
-                        : ((long long)n_max * 2 * layers * c.page_size * c.heads + 7) / 8;
-  const int ctas = (int)(units < 1216 ? units : 1216);
-  if (vec)
-    pages_copy_dense_kernel<<<ctas, kCopyThreads, 0, s>>>(a);
-  else if (esize == 2)
-    pages_copy_rows_kernel<uint16_t><<<ctas, kCopyThreads, 0, s>>>(a);
-  else
-    pages_copy_rows_kernel<uint32_t><<<ctas, kCopyThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), s);
+  if (e != cudaSuccess || n == 0) return e;
+  return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, n, pool.layer_stride, src, dst, status,
+                              CopyTail{}}, s);
 }
 
 cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new, const void* v_new,

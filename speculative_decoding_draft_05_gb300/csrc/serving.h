@@ -40,34 +40,40 @@ cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new
                                 long long new_token_stride, long long new_head_stride,
                                 const ChunkArgs& a, int* status, cudaStream_t s);
 
-// Page management.  Workspace (byte offsets, 256-aligned): counters (status
+// Page management.  Workspace (byte offsets, 256-aligned): words (the status
 // word first), per-request or per-pair scratch, the free list and copy list.
 struct PagesWorkspace {
-  size_t counters, start, owner, list, src, dst, total;
+  size_t words, start, len, owner, list, src, dst, total;
 };
 PagesWorkspace pages_workspace_layout(int R, int n_pages);
 
+// The cache as page copies see it: layer 0's view and the step between layers.
+struct PagePool {
+  CacheView c;
+  int esize, layers;
+  long long layer_stride;
+};
 struct PageMeta {
   const int32_t *table, *kv_len, *refcount;
   int32_t *table_out, *kv_len_out, *refcount_out;
   int R, max_pages, n_pages, page_size;
 };
-cudaError_t launch_pages_resize(const PageMeta& m, const int32_t* new_len, int32_t* free_pages,
-                                char* ws, const PagesWorkspace& w, cudaStream_t s);
-cudaError_t launch_pages_fork(const PageMeta& m, const int32_t* parent, const int32_t* child, int n,
-                              int32_t* free_pages, char* ws, const PagesWorkspace& w,
-                              cudaStream_t s);
-cudaError_t launch_pages_compact(const PageMeta& m, int32_t* page_map, int32_t* n_live, char* ws,
-                                 const PagesWorkspace& w, cudaStream_t s);
-// Copies pages src[i] -> dst[i], i < *count (or n_max where count is null), of
-// K and V in all layers.
-cudaError_t launch_pages_copy(const CacheView& c, int esize, int layers, long long layer_stride,
-                              const int32_t* src, const int32_t* dst, const int* count, int n_max,
+cudaError_t launch_pages_resize(const PagePool& pool, const PageMeta& m, const int32_t* new_len,
+                                int32_t* free_pages, char* ws, const PagesWorkspace& w,
+                                cudaStream_t s);
+cudaError_t launch_pages_fork(const PagePool& pool, const PageMeta& m, const int32_t* parent,
+                              const int32_t* child, int n, int32_t* free_pages, char* ws,
+                              const PagesWorkspace& w, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagePool& pool, const PageMeta& m, int32_t* page_map,
+                                 int32_t* n_live, char* ws, const PagesWorkspace& w,
+                                 cudaStream_t s);
+// Pages src[i] -> dst[i], i < n, of K and V in all layers.
+cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const int32_t* dst, int n,
                               int* status, cudaStream_t s);
 
 // Token log-probabilities.
 struct LogprobsWorkspace {
-  size_t count, list, parts, gmax, total;
+  size_t parts, gmax, total;
 };
 LogprobsWorkspace logprobs_workspace_layout(int n_rows, int V);
 cudaError_t launch_logprobs(const void* Z, int dtype, long long row_stride, const int32_t* tokens,
