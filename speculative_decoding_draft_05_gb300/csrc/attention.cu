@@ -175,8 +175,8 @@ attention_simt_kernel(const AttnParams p) {
 
 // Adds the pieces of the items that shares cut.  Block (b, y): the item that
 // CTA b + 1's share begins inside of, if its first piece lies in CTA b's share
-// (so exactly one b takes it); warps take its rows.
-template <typename T>
+// (so exactly one b takes it); a warp takes one of its rows.
+template <typename T, int NI>
 __global__ void __launch_bounds__(256)
 attention_combine_kernel(const AttnParams p, int MR, int ctas) {
   // Launched while the attention kernel runs; everything below reads what it wrote.
@@ -198,41 +198,48 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
   const long long shares = units < ctas ? units : ctas;
   const int last = (int)((end * shares - 1) / units);
   const int n = last - c + 2;  // pieces: slot 1 of CTA c - 1, slot 0 of c .. last
+  const int a = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (a >= it.rows) return;
   const int lane = threadIdx.x & 31, D = p.a.c.head_dim, G = p.a.G;
-  const int warps = gridDim.y * 8;
-  for (int a = blockIdx.y * 8 + (threadIdx.x >> 5); a < it.rows; a += warps) {
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-      const size_t at = (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
-      m = fmaxf(m, p.stats[at].x);
+  const auto at = [&](int i) {
+    return (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
+  };
+  // The weights of 32 pieces at a time, one a lane; columns lane + 32 k.
+  float m = -INFINITY, l = 0.0f;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[at(i)].x);
+  m = warp_max(m);
+  const float ms = m == -INFINITY ? 0.0f : m;
+  float o[NI] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float f = 0.0f, lf = 0.0f;
+    if (i0 + lane < n) {
+      const float2 st = p.stats[at(i0 + lane)];
+      f = exp2f(st.x - ms);
+      lf = st.y * f;
     }
-    m = warp_max(m);
-    const float ms = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    float o[8] = {};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const size_t at = (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
-      const float2 st = p.stats[at];
-      const float f = exp2f(st.x - ms);
-      l = fmaf(st.y, f, l);
+    l += warp_sum(lf);
+    const int k1 = n - i0 < 32 ? n - i0 : 32;
+#pragma unroll 8
+    for (int i = 0; i < k1; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      const float* part = p.part + at(i0 + i) * D;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (lane + 32 * k < D) o[k] = fmaf(p.part[at * D + lane + 32 * k], f, o[k]);
+      for (int k = 0; k < NI; ++k)
+        if (lane + 32 * k < D) o[k] = fmaf(part[lane + 32 * k], w, o[k]);
     }
-    const int row = it.m * MR + a, tok = row / G, g = row - tok * G;
-    const size_t at = (size_t)(it.q0 + tok) * p.a.Hq + it.h * G + g;
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (lane + 32 * k < D) {
-        if (std::is_same<T, float>::value)
-          ((float*)p.a.out)[at * D + lane + 32 * k] = o[k] * inv;
-        else
-          ((__nv_bfloat16*)p.a.out)[at * D + lane + 32 * k] = __float2bfloat16(o[k] * inv);
-      }
-    if (lane == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
   }
+  const int row = it.m * MR + a, tok = row / G, g = row - tok * G;
+  const size_t dst = (size_t)(it.q0 + tok) * p.a.Hq + it.h * G + g;
+  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+#pragma unroll
+  for (int k = 0; k < NI; ++k)
+    if (lane + 32 * k < D) {
+      if (std::is_same<T, float>::value)
+        ((float*)p.a.out)[dst * D + lane + 32 * k] = o[k] * inv;
+      else
+        ((__nv_bfloat16*)p.a.out)[dst * D + lane + 32 * k] = __float2bfloat16(o[k] * inv);
+    }
+  if (lane == 0) p.a.lse[dst] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 constexpr int kSimtCtas = 304;
@@ -260,7 +267,8 @@ cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
 
 cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas > 1 ? ctas - 1 : 1, MR / 32);
+  const long long rows = (long long)p.a.a.n_tokens * p.a.G;  // of an item, at most
+  cfg.gridDim = dim3(ctas > 1 ? ctas - 1 : 1, (unsigned)((rows < MR ? rows : MR) + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -268,9 +276,12 @@ cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const bool wide = p.a.c.head_dim > 128;
   return p.a.dtype == DSPARK_BF16
-             ? cudaLaunchKernelEx(&cfg, attention_combine_kernel<__nv_bfloat16>, p, MR, ctas)
-             : cudaLaunchKernelEx(&cfg, attention_combine_kernel<float>, p, MR, ctas);
+             ? cudaLaunchKernelEx(&cfg, wide ? attention_combine_kernel<__nv_bfloat16, 8>
+                                             : attention_combine_kernel<__nv_bfloat16, 4>, p, MR, ctas)
+             : cudaLaunchKernelEx(&cfg, wide ? attention_combine_kernel<float, 8>
+                                             : attention_combine_kernel<float, 4>, p, MR, ctas);
 }
 
 size_t attention_workspace_bytes(int dtype, int head_dim) {
