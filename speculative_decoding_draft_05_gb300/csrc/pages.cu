@@ -165,6 +165,136 @@ __global__ void __launch_bounds__(256) meta_copy_kernel(const MetaCopy c) {
   copy_meta(c, (size_t)blockIdx.x * blockDim.x + threadIdx.x, (size_t)gridDim.x * blockDim.x);
 }
 
+// What the copy kernels do beside the copies, as the end of a call.
+struct CopyTail {
+  const int* words;     // the table kernel's words (null: a plain copy)
+  int32_t* free_pages;  // resize, fork: gets the free pages
+  PageMeta m;           // compact: the table is rewritten through page_map
+  const int32_t* page_map;
+};
+
+// One page of one layer's K or V per (copy, layer, K/V); 16-byte pieces where a
+// page is one dense block on 16-byte boundaries.
+struct CopyArgs {
+  CacheView c;
+  int layers, esize, n_max;
+  long long layer_stride;
+  const int32_t *src, *dst;
+  int* status;
+  CopyTail tail;
+};
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;  // 16-byte loads in flight a thread
+
+// Number of copies; before it, the tail of a table kernel's call.
+__device__ __forceinline__ int copy_begin(const CopyArgs& a) {
+  const CopyTail& t = a.tail;
+  if (!t.words) return a.n_max;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t.free_pages && blockIdx.x == 0 && threadIdx.x == 0) {
+    int f = 0, freed = 0;
+    for (int i = 0; i < kClusterCtas; ++i) {
+      f |= __ldcg(t.words + kWordFlags + i);
+      freed += __ldcg(t.words + kWordFreed + i);
+    }
+    *t.free_pages = __ldcg(t.words + kWordFree) + freed;
+    *a.status = f;
+  }
+  if (t.page_map) {
+    const PageMeta& m = t.m;
+    const size_t n = (size_t)m.R * m.max_pages;
+    const long long most_l = (long long)m.max_pages * m.page_size;
+    const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+    for (size_t i = (size_t)blockIdx.x * kCopyThreads + threadIdx.x; i < n;
+         i += (size_t)gridDim.x * kCopyThreads) {
+      const int r = (int)(i / m.max_pages), j = (int)(i - (size_t)r * m.max_pages);
+      int p = m.table[i];
+      const int L = clamp_len(m.kv_len[r], most, a.status);
+      if (j < ceil_div(L, m.page_size)) {
+        const int q = p >= 0 && p < m.n_pages ? __ldcg(t.page_map + p) : -1;
+        if (q < 0)
+          flag_status(a.status, DSPARK_DEV_BAD_INPUT);
+        else
+          p = q;
+      }
+      m.table_out[i] = p;
+    }
+  }
+  const int n = __ldcg(t.words + kWordCopies);
+  return n < a.n_max ? n : a.n_max;
+}
+
+// Copy i's pages; false: nothing to copy (in a call of dspark_pages_copy, out of range).
+__device__ __forceinline__ bool copy_pair(const CopyArgs& a, int i, bool flag, int& s, int& d) {
+  s = __ldcg(a.src + i), d = __ldcg(a.dst + i);
+  if (s >= 0 && s < a.c.n_pages && d >= 0 && d < a.c.n_pages) return true;
+  if (!a.tail.words && flag) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
+  return false;
+}
+
+// The copies of n pairs by `teams` teams of kThreads threads (a CTA, or a
+// warp), of which this is number `team` and `t` its thread.
+template <int kThreads>
+__device__ __forceinline__ void copy_dense(const CopyArgs& a, int n, int team, int teams, int t) {
+  const int vecs = (int)((size_t)a.c.page_size * a.c.heads * a.c.head_dim * a.esize / 16);
+  const int piece = kThreads * kCopyUnroll;
+  const int pieces = (vecs + piece - 1) / piece;
+  const long long units = (long long)n * 2 * a.layers * pieces;
+  for (long long u = team; u < units; u += teams) {
+    const int pc = (int)(u % pieces);
+    long long w = u / pieces;
+    const bool is_v = w & 1;
+    w >>= 1;
+    const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
+    int s, d;
+    if (!copy_pair(a, i, t == 0, s, d)) continue;
+    char* base = (char*)(is_v ? a.c.v : a.c.k);
+    const uint4* from =
+        (const uint4*)(base + (layer * a.layer_stride + s * a.c.page_stride) * a.esize);
+    uint4* to = (uint4*)(base + (layer * a.layer_stride + d * a.c.page_stride) * a.esize);
+    const int v0 = pc * piece + t;
+    uint4 x[kCopyUnroll];
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k)
+      if (v0 + k * kThreads < vecs) x[k] = __ldcs(&from[v0 + k * kThreads]);
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k)
+      if (v0 + k * kThreads < vecs) __stcs(&to[v0 + k * kThreads], x[k]);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_dense_kernel(const CopyArgs a) {
+  copy_dense<kCopyThreads>(a, copy_begin(a), blockIdx.x, gridDim.x, threadIdx.x);
+}
+
+// Any strides: element by element, the head dimension over the lanes.
+template <typename E>
+__device__ __forceinline__ void copy_rows(const CopyArgs& a, int n, int warp, int warps) {
+  const int rows = a.c.page_size * a.c.heads;
+  const long long units = (long long)n * 2 * a.layers * rows;
+  const int lane = threadIdx.x & 31;
+  for (long long u = warp; u < units; u += warps) {
+    const int row = (int)(u % rows);
+    long long w = u / rows;
+    const bool is_v = w & 1;
+    w >>= 1;
+    const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
+    int s, d;
+    if (!copy_pair(a, i, lane == 0, s, d)) continue;
+    E* base = (E*)(is_v ? a.c.v : a.c.k) + layer * a.layer_stride +
+              (row / a.c.heads) * a.c.token_stride + (row % a.c.heads) * a.c.head_stride;
+    const E* from = base + s * a.c.page_stride;
+    E* to = base + d * a.c.page_stride;
+    for (int e = lane; e < a.c.head_dim; e += 32) to[e] = from[e];
+  }
+}
+template <typename E>
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(const CopyArgs a) {
+  copy_rows<E>(a, copy_begin(a), blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5),
+               gridDim.x * (kCopyThreads / 32));
+}
+
 struct ResizeArgs {
   PageMeta m;
   MetaCopy copy;  // done here first (all from == to: not)
@@ -175,12 +305,15 @@ struct ResizeArgs {
   int* list;   // [n_pages]: the lowest free pages in order
   int* src;    // [R] copy list
   int* dst;
+  int32_t* free_pages;
+  CopyArgs pages;  // the copies, where this kernel makes them itself
+  int copy_here;   // 0: the copy kernel behind it does, 1: dense pages, 2: row by row
 };
 
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPageThreads, 1)
 pages_resize_kernel(const ResizeArgs a) {
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int sm[1][kPageWarps + 1], scan[kPageWarps + 1], flags, freed, need_sm;
+  __shared__ int sm[1][kPageWarps + 1], scan[kPageWarps + 1], flags, freed, need_sm, copies_sm;
   const int rank = (int)cl.block_rank();
   const int lane = threadIdx.x & 31;
   const int gthread = rank * kPageThreads + (int)threadIdx.x;
@@ -196,6 +329,16 @@ pages_resize_kernel(const ResizeArgs a) {
   __syncthreads();
   copy_meta(a.copy, gthread, kClusterCtas * kPageThreads);
   cl.sync();
+
+  // CTA 0's first requests, for step 2: lengths and a grower's partly filled
+  // last page (no release touches either).
+  int pre_L = 0, pre_N = 0, pre_p = -1;
+  if (rank == 0 && (int)threadIdx.x < m.R) {
+    pre_L = clamp_len(m.kv_len[threadIdx.x], most, status);
+    pre_N = clamp_len(a.new_len[threadIdx.x], most, status);
+    if (pre_N > pre_L && pre_L % S != 0)
+      pre_p = __ldcg(&m.table_out[(size_t)threadIdx.x * P + pre_L / S]);
+  }
 
   // 1. Pages past the new length lose a reference.
   for (int r = gwarp; r < m.R; r += warps) {
@@ -223,10 +366,11 @@ pages_resize_kernel(const ResizeArgs a) {
       const int r = r0 + (int)threadIdx.x;
       int need = 0, cow = 0;
       if (r < m.R) {
-        const int L = clamp_len(m.kv_len[r], most, status), N = clamp_len(a.new_len[r], most, status);
+        const int L = r0 == 0 ? pre_L : clamp_len(m.kv_len[r], most, status);
+        const int N = r0 == 0 ? pre_N : clamp_len(a.new_len[r], most, status);
         if (N > L) {
           if (L % S != 0) {
-            const int p = __ldcg(&m.table_out[(size_t)r * P + L / S]);
+            const int p = r0 == 0 ? pre_p : __ldcg(&m.table_out[(size_t)r * P + L / S]);
             if (p < 0 || p >= m.n_pages)
               flag_status(status, DSPARK_DEV_BAD_INPUT);
             else
@@ -247,12 +391,14 @@ pages_resize_kernel(const ResizeArgs a) {
     }
     if (threadIdx.x == 0) {
       need_sm = base;
+      copies_sm = copies;
       a.words[kWordCopies] = copies;
     }
   }
   int at[1], n_free[1];
   cluster_prefix<1>(cl, mine, sm, at, n_free);
   const int need_all = *cl.map_shared_rank(&need_sm, 0);
+  const int copies = *cl.map_shared_rank(&copies_sm, 0);
   if (need_all > n_free[0] && threadIdx.x == 0 && rank == 0) flag_status(status, DSPARK_DEV_NO_PAGES);
 
   // 3. The lowest free pages, as many as are wanted.
@@ -298,12 +444,35 @@ pages_resize_kernel(const ResizeArgs a) {
     __syncwarp();
     if (lane == 0) m.kv_len_out[r] = out_len;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    a.words[kWordFlags + rank] = flags;
-    a.words[kWordFreed + rank] = freed;
-    if (rank == 0) a.words[kWordFree] = n_free[0] - (need_all < n_free[0] ? need_all : n_free[0]);
+  const int left = n_free[0] - (need_all < n_free[0] ? need_all : n_free[0]);
+  if (!a.copy_here) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      a.words[kWordFlags + rank] = flags;
+      a.words[kWordFreed + rank] = freed;
+      if (rank == 0) a.words[kWordFree] = left;
+    }
+    return;
   }
+  cl.sync();
+  if (copies) {
+    if (a.copy_here == 1)
+      copy_dense<32>(a.pages, copies, gwarp, warps, lane);
+    else if (a.pages.esize == 2)
+      copy_rows<uint16_t>(a.pages, copies, gwarp, warps);
+    else
+      copy_rows<uint32_t>(a.pages, copies, gwarp, warps);
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    int f = 0, more = 0;
+    for (int c = 0; c < kClusterCtas; ++c) {
+      f |= *cl.map_shared_rank(&flags, c);
+      more += *cl.map_shared_rank(&freed, c);
+    }
+    a.words[kWordStatus] = f;
+    *a.free_pages = left + more;
+  }
+  cl.sync();  // (rank 0 reads the others' shared memory)
 }
 
 struct ForkArgs {
@@ -499,6 +668,10 @@ MetaCopy meta_args(const PageMeta& m, bool table, bool len) {
 // itself, larger ones by a launch of their own over all SMs (8 SMs move about
 // an eighth of a TB/s each way: at 1 M entries that is about the launch saved).
 constexpr size_t kMetaInKernel = 1u << 20;
+// A resize copies the shared pages that it has to split in the cluster kernel
+// where even all requests' pages come to this many bytes (8 SMs move about
+// 1 TB/s; it mostly has none or a few, and the second launch costs 5 us).
+constexpr size_t kCopyInKernel = 16u << 20;
 cudaError_t split_meta(MetaCopy* c, cudaStream_t s) {
   size_t most = 0, all = 0;
   for (int k = 0; k < 3; ++k)
@@ -512,127 +685,6 @@ cudaError_t split_meta(MetaCopy* c, cudaStream_t s) {
   meta_copy_kernel<<<(int)ctas, 256, 0, s>>>(*c);
   for (int k = 0; k < 3; ++k) c->from[k] = c->to[k];
   return cudaGetLastError();
-}
-
-// What the copy kernels do beside the copies, as the end of a call.
-struct CopyTail {
-  const int* words;     // the table kernel's words (null: a plain copy)
-  int32_t* free_pages;  // resize, fork: gets the free pages
-  PageMeta m;           // compact: the table is rewritten through page_map
-  const int32_t* page_map;
-};
-
-// One page of one layer's K or V per (copy, layer, K/V); 16-byte pieces where a
-// page is one dense block on 16-byte boundaries.
-struct CopyArgs {
-  CacheView c;
-  int layers, esize, n_max;
-  long long layer_stride;
-  const int32_t *src, *dst;
-  int* status;
-  CopyTail tail;
-};
-
-constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 4;  // 16-byte loads in flight a thread
-
-// Number of copies; before it, the tail of a table kernel's call.
-__device__ __forceinline__ int copy_begin(const CopyArgs& a) {
-  const CopyTail& t = a.tail;
-  if (!t.words) return a.n_max;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (t.free_pages && blockIdx.x == 0 && threadIdx.x == 0) {
-    int f = 0, freed = 0;
-    for (int i = 0; i < kClusterCtas; ++i) {
-      f |= __ldcg(t.words + kWordFlags + i);
-      freed += __ldcg(t.words + kWordFreed + i);
-    }
-    *t.free_pages = __ldcg(t.words + kWordFree) + freed;
-    *a.status = f;
-  }
-  if (t.page_map) {
-    const PageMeta& m = t.m;
-    const size_t n = (size_t)m.R * m.max_pages;
-    const long long most_l = (long long)m.max_pages * m.page_size;
-    const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
-    for (size_t i = (size_t)blockIdx.x * kCopyThreads + threadIdx.x; i < n;
-         i += (size_t)gridDim.x * kCopyThreads) {
-      const int r = (int)(i / m.max_pages), j = (int)(i - (size_t)r * m.max_pages);
-      int p = m.table[i];
-      const int L = clamp_len(m.kv_len[r], most, a.status);
-      if (j < ceil_div(L, m.page_size)) {
-        const int q = p >= 0 && p < m.n_pages ? __ldcg(t.page_map + p) : -1;
-        if (q < 0)
-          flag_status(a.status, DSPARK_DEV_BAD_INPUT);
-        else
-          p = q;
-      }
-      m.table_out[i] = p;
-    }
-  }
-  const int n = __ldcg(t.words + kWordCopies);
-  return n < a.n_max ? n : a.n_max;
-}
-
-// Copy i's pages; false: nothing to copy (in a call of dspark_pages_copy, out of range).
-__device__ __forceinline__ bool copy_pair(const CopyArgs& a, int i, bool flag, int& s, int& d) {
-  s = __ldcg(a.src + i), d = __ldcg(a.dst + i);
-  if (s >= 0 && s < a.c.n_pages && d >= 0 && d < a.c.n_pages) return true;
-  if (!a.tail.words && flag) flag_status(a.status, DSPARK_DEV_BAD_INPUT);
-  return false;
-}
-
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_dense_kernel(const CopyArgs a) {
-  const int n = copy_begin(a);
-  const int vecs = (int)((size_t)a.c.page_size * a.c.heads * a.c.head_dim * a.esize / 16);
-  const int piece = kCopyThreads * kCopyUnroll;
-  const int pieces = (vecs + piece - 1) / piece;
-  const long long units = (long long)n * 2 * a.layers * pieces;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int pc = (int)(u % pieces);
-    long long w = u / pieces;
-    const bool is_v = w & 1;
-    w >>= 1;
-    const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
-    int s, d;
-    if (!copy_pair(a, i, threadIdx.x == 0, s, d)) continue;
-    char* base = (char*)(is_v ? a.c.v : a.c.k);
-    const uint4* from =
-        (const uint4*)(base + (layer * a.layer_stride + s * a.c.page_stride) * a.esize);
-    uint4* to = (uint4*)(base + (layer * a.layer_stride + d * a.c.page_stride) * a.esize);
-    const int v0 = pc * piece + (int)threadIdx.x;
-    uint4 x[kCopyUnroll];
-#pragma unroll
-    for (int k = 0; k < kCopyUnroll; ++k)
-      if (v0 + k * kCopyThreads < vecs) x[k] = __ldcs(&from[v0 + k * kCopyThreads]);
-#pragma unroll
-    for (int k = 0; k < kCopyUnroll; ++k)
-      if (v0 + k * kCopyThreads < vecs) __stcs(&to[v0 + k * kCopyThreads], x[k]);
-  }
-}
-
-// Any strides: element by element, the head dimension over the lanes.
-template <typename E>
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(const CopyArgs a) {
-  const int n = copy_begin(a);
-  const int rows = a.c.page_size * a.c.heads;
-  const long long units = (long long)n * 2 * a.layers * rows;
-  const int lane = threadIdx.x & 31;
-  for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * (kCopyThreads / 32)) {
-    const int row = (int)(u % rows);
-    long long w = u / rows;
-    const bool is_v = w & 1;
-    w >>= 1;
-    const int layer = (int)(w % a.layers), i = (int)(w / a.layers);
-    int s, d;
-    if (!copy_pair(a, i, lane == 0, s, d)) continue;
-    E* base = (E*)(is_v ? a.c.v : a.c.k) + layer * a.layer_stride +
-              (row / a.c.heads) * a.c.token_stride + (row % a.c.heads) * a.c.head_stride;
-    const E* from = base + s * a.c.page_stride;
-    E* to = base + d * a.c.page_stride;
-    for (int e = lane; e < a.c.head_dim; e += 32) to[e] = from[e];
-  }
 }
 
 // ------------------------------------------------------------------ append
@@ -724,12 +776,21 @@ PagesWorkspace pages_workspace_layout(int R, int n_pages) {
   return w;
 }
 
+static size_t page_bytes_of(const CopyArgs& a) {
+  return (size_t)a.c.page_size * a.c.heads * a.c.head_dim * a.esize;
+}
+
+// Whether pages are dense blocks that move in 16-byte pieces.
+static bool copy_vec(const CopyArgs& a) {
+  const CacheView& c = a.c;
+  return dense_page(c) && page_bytes_of(a) % 16 == 0 && (c.page_stride * a.esize) % 16 == 0 &&
+         (a.layer_stride * a.esize) % 16 == 0 && (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) == 0;
+}
+
 static cudaError_t launch_copy(const CopyArgs& a, cudaStream_t s) {
   const CacheView& c = a.c;
-  const size_t page_bytes = (size_t)c.page_size * c.heads * c.head_dim * a.esize;
-  const bool vec = dense_page(c) && page_bytes % 16 == 0 && (c.page_stride * a.esize) % 16 == 0 &&
-                   (a.layer_stride * a.esize) % 16 == 0 &&
-                   (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) == 0;
+  const size_t page_bytes = page_bytes_of(a);
+  const bool vec = copy_vec(a);
   const long long per = vec ? (long long)((page_bytes / 16 + kCopyThreads * kCopyUnroll - 1) /
                                           (kCopyThreads * kCopyUnroll))
                             : ((long long)c.page_size * c.heads + 7) / 8;
@@ -755,14 +816,18 @@ cudaError_t launch_pages_resize(const PagePool& pool, const PageMeta& m, const i
                                 cudaStream_t s) {
   int* words = (int*)(ws + w.words);
   ResizeArgs a{m, meta_args(m, true, false), new_len, words, (int*)(ws + w.start),
-               (int*)(ws + w.owner), (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst)};
+               (int*)(ws + w.owner), (int*)(ws + w.list), (int*)(ws + w.src), (int*)(ws + w.dst),
+               free_pages, CopyArgs{}, 0};
+  a.pages = CopyArgs{pool.c, pool.layers, pool.esize, m.R, pool.layer_stride, a.src, a.dst,
+                     words, CopyTail{words, free_pages, m, nullptr}};
+  if ((size_t)m.R * 2 * pool.layers * page_bytes_of(a.pages) <= kCopyInKernel)
+    a.copy_here = copy_vec(a.pages) ? 1 : 2;
   cudaError_t e = split_meta(&a.copy, s);
   if (e != cudaSuccess) return e;
   pages_resize_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, m.R, pool.layer_stride, a.src, a.dst,
-                              words, CopyTail{words, free_pages, m, nullptr}}, s);
+  if (e != cudaSuccess || a.copy_here) return e;
+  return launch_copy(a.pages, s);
 }
 
 cudaError_t launch_pages_fork(const PagePool& pool, const PageMeta& m, const int32_t* parent,
