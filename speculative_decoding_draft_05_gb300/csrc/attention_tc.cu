@@ -558,22 +558,6 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         ++steps;
         if (!ok) break;
         tc_fence_after();
-        // V rows past the item's end become zeros (by the stream that multiplies first).
-        if (k0 + kTN > c.end && (!two || s == 0)) {
-          const uint32_t i = run + j;
-          const uint32_t sl = base + (two ? 2 * j + 1 : j + 1 < c.nt || c.next_joined ? 2 * i + 2 : 2 * i + 1);
-          const int stage = (int)(sl % Lo::kStages);
-          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[stage], (sl / Lo::kStages) & 1u, abort_flag,
-                                                 tp.wait_budget));
-          if (!ok) break;
-          if (k0 + trow >= c.end) {
-            uint8_t* v = smem + Lo::kOffRing + stage * Lo::kTileBytes + trow * 128;
-#pragma unroll
-            for (int i = 0; i < Lo::kHalves * 8; ++i)
-              *(uint4*)(v + (i >> 3) * Lo::kHalfBytes + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async();
-        }
         if (warp_live) {
           // Two passes over S: the maximum, columns 0..63 then 64..127; then the
           // probabilities, 64..127 from registers and 0..63 read again (all 128
@@ -641,6 +625,22 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           tmem_wait_st();
         }
         tc_fence_before();
+        // V rows past the item's end become zeros (by the stream that multiplies first).
+        if (k0 + kTN > c.end && (!two || s == 0)) {
+          const uint32_t i = run + j;
+          const uint32_t sl = base + (two ? 2 * j + 1 : j + 1 < c.nt || c.next_joined ? 2 * i + 2 : 2 * i + 1);
+          const int stage = (int)(sl % Lo::kStages);
+          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[stage], (sl / Lo::kStages) & 1u, abort_flag,
+                                                 tp.wait_budget));
+          if (!ok) break;
+          if (k0 + trow >= c.end) {
+            uint8_t* v = smem + Lo::kOffRing + stage * Lo::kTileBytes + trow * 128;
+#pragma unroll
+            for (int i = 0; i < Lo::kHalves * 8; ++i)
+              *(uint4*)(v + (i >> 3) * Lo::kHalfBytes + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[s]);
       }
