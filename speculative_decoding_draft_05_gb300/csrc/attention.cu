@@ -28,7 +28,7 @@ template <typename T, int NI>  // NI = ceil(D / 32)
 __global__ void __launch_bounds__(kThreads)
 attention_simt_kernel(const AttnParams p) {
   extern __shared__ float4 smem4[];
-  __shared__ AttnStart st;
+  __shared__ AttnStart<kTN> st;
   __shared__ int flags;
   __shared__ __align__(16) float sp[kThreads / 32][kTN][kRowsPerWarp];  // probabilities of a warp's rows
   const int D = p.a.c.head_dim, ld = NI * 32 + 4;
@@ -41,13 +41,12 @@ attention_simt_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) flags = 0;
   __syncthreads();
-  attn_plan<kMR, kTN>(p, &st, &flags);
-  long long u0;
-  AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, st, &flags, &u0);
-  if (threadIdx.x == 0) attn_write_cut(p, w, u0);
+  attn_plan<kTN>(p, &st, &flags);
+  AttnWalk<kTN> w = st.walk;
+  if (threadIdx.x == 0) attn_write_cut(p, st);
 
-  for (; !w.done(); w.next()) {
-    const int rows = w.block_rows(), row0 = w.m * kMR;
+  for (; !w.done(); w.next(p, &flags)) {
+    const int rows = w.block_rows(p), row0 = w.m * kMR;
     __syncthreads();
     for (int i = threadIdx.x; i < kMR * NI * 32; i += kThreads) {
       const int a = i / (NI * 32), d = i - a * (NI * 32);
@@ -228,7 +227,7 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
         if (lane + 32 * k < D) o[k] = fmaf(part[lane + 32 * k], w, o[k]);
     }
   }
-  const int row = it.m * MR + a, tok = row / G, g = row - tok * G;
+  const int row = it.m * p.mr + a, tok = row / G, g = row - tok * G;
   const size_t dst = (size_t)(it.q0 + tok) * p.a.Hq + it.h * G + g;
   const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
 #pragma unroll
@@ -296,7 +295,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) 
   if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
-               (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f};
+               (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f,
+               kMR};
   const cudaError_t e = a.dtype == DSPARK_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(p, kMR, kSimtCtas, s);

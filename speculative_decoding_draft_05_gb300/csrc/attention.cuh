@@ -1,7 +1,7 @@
 // attention.cuh -- what the kernels of attention over the paged cache share:
 // the division of the work and the partial results that a division leaves.
 //
-// An item is a block of up to MR rows of one request's chunk for one K/V head.
+// An item is a block of up to `mr` rows of one request's chunk for one K/V head.
 // A row is (token, query head of the group): row = token * G + g, so all G
 // query heads that share a K/V head read its tiles once.  An item walks its
 // keys in tiles of TN; its work is counted as one unit a tile (an item without
@@ -59,6 +59,7 @@ struct AttnParams {
   float2* stats;     // [grid][2][MR] (m, l), m in log2 units
   float* part;       // [grid][2][MR][D]
   float scale_log2;  // scale * log2(e)
+  int mr;            // rows of an item, at most (partial results are MR >= mr rows apart)
 };
 
 struct AttnRequest {
@@ -84,9 +85,8 @@ __device__ __forceinline__ AttnRequest attn_request(const ChunkArgs& a, int page
 }
 
 // Keys that the rows of block m see: positions 0 .. end - 1.
-template <int MR>
-__device__ __forceinline__ int attn_item_end(const AttnRequest& q, int G, int m) {
-  int last = ((m + 1) * MR - 1) / G;
+__device__ __forceinline__ int attn_item_end(const AttnRequest& q, int G, int mr, int m) {
+  int last = ((m + 1) * mr - 1) / G;
   last = last < q.n - 1 ? last : q.n - 1;
   const int end = q.L - q.n + last + 1;
   return end < 0 ? 0 : end;
@@ -97,15 +97,9 @@ __device__ __forceinline__ int attn_tiles(int end) {
   return end <= TN ? 1 : (end + TN - 1) / TN;
 }
 
-template <int MR, int TN>
-__device__ __forceinline__ long long attn_request_units(const AttnRequest& q, int G, int Hkv) {
-  const long long rows = (long long)q.n * G;
-  if (rows == 0) return 0;
-  if (rows <= MR) return (long long)Hkv * (attn_tiles<TN>(q.L) + kAttnItemUnits);
-  const int blocks = (int)((rows + MR - 1) / MR);
-  long long u = (long long)blocks * kAttnItemUnits;
-  for (int m = 0; m < blocks; ++m) u += attn_tiles<TN>(attn_item_end<MR>(q, G, m));
-  return u * Hkv;
+// Row blocks of a request.
+__device__ __forceinline__ int attn_blocks(const AttnRequest& q, int G, int mr) {
+  return (int)(((long long)q.n * G + mr - 1) / mr);
 }
 
 // First unit of CTA c's share.  With fewer units than CTAs the first `units`
@@ -116,10 +110,8 @@ __device__ __forceinline__ long long attn_share(long long units, int ctas, int c
 }
 
 // The walk of one CTA (or one warp role of it) over its share.
-template <int MR, int TN>
+template <int TN>
 struct AttnWalk {
-  const AttnParams* p;
-  int* flags;        // the CTA's status bits (shared memory)
   AttnRequest q;
   int r, m, h;       // current item: request, row block, K/V head
   int end, n_tiles;  // its keys and tiles
@@ -139,54 +131,77 @@ struct AttnWalk {
   __device__ __forceinline__ void drop_empty() {
     if (left > 0 && last_tile() <= first_tile()) left = 0;
   }
-  __device__ __forceinline__ int block_rows() const {
-    const long long rest = (long long)q.n * p->a.G - (long long)m * MR;
-    return rest < MR ? (int)rest : MR;
+  __device__ __forceinline__ int block_rows(const AttnParams& p) const {
+    const long long rest = (long long)q.n * p.a.G - (long long)m * p.mr;
+    return rest < p.mr ? (int)rest : p.mr;
   }
 
-  __device__ __forceinline__ void next() {
+  // flags: the CTA's status bits.
+  __device__ __forceinline__ void next(const AttnParams& p, int* flags) {
     left -= n_tiles + kAttnItemUnits - pos;
     if (done()) return;
     pos = 0;
-    if (++h >= p->a.c.heads) {
+    if (++h >= p.a.c.heads) {
       h = 0;
-      if ((long long)(++m) * MR >= (long long)q.n * p->a.G) {
+      if ((long long)(++m) * p.mr >= (long long)q.n * p.a.G) {
         m = 0;
         do {
-          if (++r >= p->a.a.R) {  // (not reached: the units count the items)
+          if (++r >= p.a.a.R) {  // (not reached: the units count the items)
             left = 0;
             return;
           }
-          q = attn_request(p->a.a, p->a.c.page_size, r, flags);
+          q = attn_request(p.a.a, p.a.c.page_size, r, flags);
         } while (q.n == 0);
       }
-      end = attn_item_end<MR>(q, p->a.G, m);
+      end = attn_item_end(q, p.a.G, p.mr, m);
       n_tiles = attn_tiles<TN>(end);
     }
     drop_empty();
   }
 };
 
-// What a CTA's threads work out together at the start: the total units, and
-// the request in which the CTA's share begins.
+// What a CTA's threads work out together at the start: where its walk begins.
+template <int TN>
 struct AttnStart {
-  long long units, first;  // total; first unit of `request`
-  int request;
-  long long scan[33];
+  AttnWalk<TN> walk;
+  long long u0;  // the unit of the first item's first tile
+  long long units, scan[33];
 };
 
-// All threads of the CTA (a multiple of 32, at most 1024).  Ends with a barrier.
-// *flags (shared memory) collects the CTA's status bits.
-template <int MR, int TN>
-__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st, int* flags) {
+// All threads of the CTA (a multiple of 32, at most 1024).  *flags (shared
+// memory) collects the CTA's status bits.  Ends with a barrier.
+//
+// A prefix sum of the requests' units, one request a thread (or a run of
+// them); a request of many row blocks is summed by its thread's whole warp.
+template <int TN>
+__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st, int* flags) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int R = p.a.a.R;
+  const int R = p.a.a.R, G = p.a.G, Hkv = p.a.c.heads;
   const int per = (R + (int)blockDim.x - 1) / (int)blockDim.x;
-  const int r0 = min(R, (int)threadIdx.x * per), r1 = min(R, r0 + per);
+  const int r0 = (int)threadIdx.x * per;
+  // Units of the thread's i-th request, which all lanes of the warp call for together.
+  auto units_of = [&](int i, AttnRequest& q) -> long long {
+    const int r = r0 + i;
+    q = AttnRequest{0, 0, 0};
+    if (r < R) q = attn_request(p.a.a, p.a.c.page_size, r, flags);
+    const int blocks = attn_blocks(q, G, p.mr);
+    long long u = blocks == 1 ? attn_tiles<TN>(q.L) + kAttnItemUnits : 0;
+    for (unsigned todo = __ballot_sync(0xffffffffu, blocks > 1); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const AttnRequest w{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.L, src)};
+      const int nb = __shfl_sync(0xffffffffu, blocks, src);
+      long long sum = 0;
+      for (int m = lane; m < nb; m += 32)
+        sum += attn_tiles<TN>(attn_item_end(w, G, p.mr, m)) + kAttnItemUnits;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == src) u = sum;
+    }
+    return u * Hkv;
+  };
   long long mine = 0;
-  for (int r = r0; r < r1; ++r)
-    mine += attn_request_units<MR, TN>(attn_request(p.a.a, p.a.c.page_size, r, flags), p.a.G,
-                                       p.a.c.heads);
+  AttnRequest q;
+  for (int i = 0; i < per; ++i) mine += units_of(i, q);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -209,76 +224,77 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st, in
   __syncthreads();
   const long long units = st->units;
   const long long start = attn_share(units, gridDim.x, blockIdx.x);
-  long long at = st->scan[warp] + incl - mine;
-  if (start >= at && start < at + mine) {
-    for (int r = r0; r < r1; ++r) {
-      const long long k = attn_request_units<MR, TN>(
-          attn_request(p.a.a, p.a.c.page_size, r, flags), p.a.G, p.a.c.heads);
-      if (start < at + k) {
-        st->request = r;
-        st->first = at;
-        break;
+  const int left = (int)(attn_share(units, gridDim.x, blockIdx.x + 1) - start);
+  if (left <= 0) {
+    if (threadIdx.x == 0) st->walk.left = 0;
+  } else {
+    long long at = st->scan[warp] + incl - mine;  // the thread's first unit
+    if (__any_sync(0xffffffffu, start >= at && start < at + mine)) {  // one warp
+      for (int i = 0; i < per; ++i) {
+        const long long k = units_of(i, q);
+        const bool here = start >= at && start < at + k;  // one lane, for one i
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        if (who) {
+          // The row block, 32 at a time: the warp's lanes each weigh one.
+          const int src = __ffs(who) - 1;
+          AttnWalk<TN> w;
+          w.q.q0 = __shfl_sync(0xffffffffu, q.q0, src);
+          w.q.n = __shfl_sync(0xffffffffu, q.n, src);
+          w.q.L = __shfl_sync(0xffffffffu, q.L, src);
+          w.r = __shfl_sync(0xffffffffu, r0, src) + i;
+          long long base = __shfl_sync(0xffffffffu, at, src);
+          const int blocks = attn_blocks(w.q, G, p.mr);
+          for (int m0 = 0; m0 < blocks; m0 += 32) {
+            w.m = m0 + lane;
+            w.end = attn_item_end(w.q, G, p.mr, w.m);
+            w.n_tiles = attn_tiles<TN>(w.end);
+            const int item = w.n_tiles + kAttnItemUnits;
+            const long long own = w.m < blocks ? (long long)item * Hkv : 0;
+            long long upto = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+              if (lane >= o) upto += v;
+            }
+            const long long first = base + upto - own;
+            if (start >= first && start < first + own) {
+              const long long d = start - first;
+              w.h = (int)(d / item);
+              w.pos = (int)(d - (long long)w.h * item);
+              w.left = left;
+              w.drop_empty();
+              st->walk = w;
+              st->u0 = first + (long long)w.h * item + kAttnItemUnits;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
+          }
+        }
+        at += k;
       }
-      at += k;
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.units = units;
   __syncthreads();
 }
 
-// The walk over this CTA's share, from its first item; *u0 gets the unit of
-// that item's first tile.
-template <int MR, int TN>
-__device__ __forceinline__ AttnWalk<MR, TN> attn_walk(const AttnParams& p, const AttnStart& st,
-                                                      int* flags, long long* u0) {
-  AttnWalk<MR, TN> w;
-  w.p = &p;
-  w.flags = flags;
-  const long long u = attn_share(st.units, gridDim.x, blockIdx.x);
-  w.left = (int)(attn_share(st.units, gridDim.x, blockIdx.x + 1) - u);
-  long long at = st.first;
-  if (w.left > 0) {
-    const int G = p.a.G, Hkv = p.a.c.heads;
-    w.r = st.request;
-    w.q = attn_request(p.a.a, p.a.c.page_size, w.r, flags);
-    w.m = 0;
-    int per;
-    for (;;) {
-      w.end = attn_item_end<MR>(w.q, G, w.m);
-      w.n_tiles = attn_tiles<TN>(w.end);
-      per = w.n_tiles + kAttnItemUnits;
-      const long long k = (long long)per * Hkv;
-      if (u < at + k || (long long)(w.m + 1) * MR >= (long long)w.q.n * G) break;
-      at += k;
-      ++w.m;
-    }
-    w.h = (int)((u - at) / per);
-    at += (long long)w.h * per;
-    w.pos = (int)(u - at);
-    w.drop_empty();
-  }
-  *u0 = at + kAttnItemUnits;
-  return w;
-}
-
 // Written once a CTA: whether its share begins inside an item, and which.
-template <int MR, int TN>
-__device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnWalk<MR, TN>& w,
-                                               long long u0) {
+template <int TN>
+__device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnStart<TN>& st) {
+  const AttnWalk<TN>& w = st.walk;
   CutItem c;
   c.valid = !w.done() && w.first_tile() > 0;
   if (c.valid) {
     c.r = w.r, c.m = w.m, c.h = w.h;
-    c.n = w.q.n, c.q0 = w.q.q0, c.rows = w.block_rows(), c.n_tiles = w.n_tiles;
-    c.u0 = u0;
+    c.n = w.q.n, c.q0 = w.q.q0, c.rows = w.block_rows(p), c.n_tiles = w.n_tiles;
+    c.u0 = st.u0;
   }
   p.cuts[blockIdx.x] = c;
 }
 
 // Where the walk's current piece of its item goes: -1 whole (straight to the
 // output), 0 the item began in an earlier share, 1 it goes on in a later one.
-template <int MR, int TN>
-__device__ __forceinline__ int attn_slot(const AttnWalk<MR, TN>& w) {
+template <int TN>
+__device__ __forceinline__ int attn_slot(const AttnWalk<TN>& w) {
   if (w.first_tile() > 0) return 0;
   return w.last_tile() < w.n_tiles ? 1 : -1;
 }

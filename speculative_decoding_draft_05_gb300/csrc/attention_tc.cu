@@ -10,23 +10,25 @@
 // grew by more than 2^8: until then p_j <= 2^8 stays far inside bf16's and
 // fp32's range, and out = O / l is the same whatever m the two share.
 //
-// Structure (one CTA an SM, persistent over its share of the work):
-//   * warp 8 (producer): TMA of K and V pages into a ring of tiles; each lane
+// Structure (one CTA an SM, persistent over its share of the work; a piece is
+// the part of an item in it):
+//   * warp 11 (producer): TMA of K and V pages into a ring of tiles; each lane
 //     owns one (page, 64-column half) box of a tile, so a tile of 16-token
 //     pages is 16 boxes issued at once.
 //   * warp 9 (MMA): one thread issues tcgen05.mma; S from shared-memory
 //     descriptors, P V with P in TMEM and V as stored ([keys, D]: the N-major
 //     second operand).
-//   * warps 0..3 and 4..7: two softmax streams, one row a thread.  With more
-//     than 128 rows the streams are the two row blocks and share each K/V tile;
-//     with fewer they are alternate tiles of the same rows, and merge at the
-//     end of the item.  While one stream is in its softmax the tensor cores
-//     run the other's products.
-//   * warps 10, 11 (loaders): walk the share ahead of the others, load each
-//     piece's Q and publish what it is.  Pieces of up to 128 rows alternate
-//     between the two Q tiles, so the products of a run of such pieces follow
-//     one another without a gap: the next piece's Q K^T is issued while
-//     the last tiles of this one are in their softmax.
+//   * warp 10 (loader): walks the share ahead of the others, loads each piece's
+//     Q by TMA (boxes of G heads x tokens: the rows in order) and publishes
+//     what the piece is.  Pieces of one row block alternate between the two Q
+//     tiles, so the products of a run of such pieces follow one another
+//     without a gap.
+//   * warps 0..3 and 4..7: two softmax streams, one row a thread.  With two row
+//     blocks the streams are the blocks and share each K/V tile; with one they
+//     are alternate tiles of the same rows.  While one stream is in its softmax
+//     the tensor cores run the other's products.
+//   * warps 12..15 (results): merge a piece's streams, scale and write it, while
+//     the softmax warps are at the next piece.
 //   * Keys at or past an item's end: pages past it are not loaded, S is
 //     replaced by -inf, and V's rows are overwritten with zeros, since 0 x NaN of
 //     an unused cache slot would reach the sum.
@@ -45,12 +47,14 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMR = 256;  // rows of an item
+constexpr int kMR = 256;  // rows of an item, at most: two tiles of 128 / G tokens x G heads
 constexpr int kTN = 128;  // keys of a tile
-constexpr int kThreads = 384;  // three warpgroups: two of softmax, one with the producer and MMA warps
-// Registers a thread after the split: 256 x 184 + 128 x 128 of the launch's 384 x 168.
-constexpr int kRegsSoftmax = 184, kRegsOther = 128;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 512;  // four warpgroups: two of softmax, the single roles, the results
+// Registers a thread after the split: 256 x 168 + 128 x 96 + 128 x 80 of the
+// launch's 512 x 128.
+constexpr int kRegsSoftmax = 168, kRegsOther = 96, kRegsResult = 80;
+constexpr int kFirstRoleWarp = 8;  // (8 idles: warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
+constexpr int kMmaWarp = 9, kLoaderWarp = 10, kProducerWarp = 11, kResultWarp = 12;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTmemCols = 512;  // S0, S1, O0, O1: 128 columns each
@@ -67,7 +71,7 @@ struct Layout {
   static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
   static constexpr int kOffStart = kOffMerge;                        // (before the first merge)
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
-  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 1;
   static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 12 + 15) & ~15);  // PieceInfo [2]
   static constexpr int kEnd = kOffPiece + 2 * 64;
   // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
@@ -75,6 +79,16 @@ struct Layout {
   static constexpr int kBytes = kEnd + 1024 < 232448 ? kEnd + 1024 : 232448;
 };
 static_assert(Layout<128>::kEnd <= 232448, "shared memory");
+static_assert(sizeof(AttnStart<kTN>) <= 2 * 128 * 8, "the plan's scratch lies in the merge buffer");
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             int w, uint64_t* bar) {
@@ -83,15 +97,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
-}
-
-// 16 bytes global -> shared without a register in between; `bytes` of them read, the rest zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async() {
@@ -105,31 +110,50 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+// The MMA warp runs as a whole, and its instructions are issued under a
+// predicate that one lane holds: operands then are the same for the warp and
+// stay in uniform registers, which is where tcgen05.mma wants them.  (One lane
+// in a branch of its own took about 130 clocks an instruction to issue.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(lead)
       : "memory");
 }
 
 // D[tmem] (+)= A[smem] B[smem], K = 16.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+                                       uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem], K = 16: A is 8 columns of bf16 pairs.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+                                       uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
 
@@ -171,6 +195,24 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t* v) {
                  "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
                  "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
                  "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :
                : "memory");
 }
@@ -237,8 +279,10 @@ __device__ __forceinline__ void regs_inc() {
 
 struct TcParams {
   AttnParams p;
-  int box_tokens;  // tokens of a TMA box: min(page_size, 128)
-  int q_vec;       // q rows can be read in 16-byte pieces
+  int box_tokens;  // tokens of a K/V box: min(page_size, 128)
+  int q_tokens;    // tokens of a Q tile (a box): 128 / G
+  int tile_rows;   // rows of a Q tile: q_tokens G (128 where G > 128)
+  int q_tma;       // q can be loaded by TMA (else by the loader's threads)
   float sign;      // of the scale; |scale| is in p.scale_log2
   long long wait_budget;
 };
@@ -251,12 +295,12 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // One piece: the part of an item that lies in this CTA's share.
 struct alignas(16) PieceInfo {
   int t0, nt;       // first tile, tiles (0: no more pieces)
-  int rows, row0;   // rows of the block (more than 128: two row blocks), first row of the chunk
+  int rows, row0;   // rows of the block (more than tile_rows: two Q tiles), first row of the chunk
   int h, q0;        // K/V head, the chunk's first token
   int lim;          // keys that the chunk's token 0 sees (L - n + 1; may be <= 0)
   int end;          // keys of the item
   int slot;         // where the result goes (attn_slot)
-  int next_joined;  // both this piece and the next one have up to 128 rows
+  int next_joined;  // both this piece and the next one have one Q tile
   int pad[2];
 };
 static_assert(sizeof(PieceInfo) <= 64, "piece slot");
@@ -264,7 +308,7 @@ static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ TcParams tp) {
+                    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TcParams tp) {
   using Lo = Layout<DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -279,15 +323,17 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* kv_empty = bars + Lo::kStages;
   uint64_t* s_full = kv_empty + Lo::kStages;  // [2] S of a stream ready
   uint64_t* p_full = s_full + 2;              // [2] P of a stream written (4 warps)
-  uint64_t* q_full = p_full + 2;   // [2] piece n (n & 1) published and its Q loaded (2 warps)
-  uint64_t* q_empty = q_full + 2;  // [2] its last Q K^T done (1) and its info read (8 warps)
+  uint64_t* q_full = p_full + 2;   // [2] piece n (n & 1) published and its Q loaded
+  uint64_t* q_empty = q_full + 2;  // [2] its last Q K^T done (1) and its info read (12 warps)
   uint64_t* o_full = q_empty + 2;  // [2] piece n's last product done
-  uint64_t* pair = o_full + 2;     // the two streams meet (8 warps)
-  uint64_t* drain = pair + 1;
+  uint64_t* ml_full = o_full + 2;  // piece n's (m, l) written (8 softmax warps)
+  uint64_t* ml_empty = ml_full + 1;  // and read (4 result warps)
+  uint64_t* o_free = ml_empty + 1;   // piece n's O read (4 result warps)
+  uint64_t* drain = o_free + 1;
   uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   int* flags = (int*)(tmem_slot + 2);  // the CTA's status bits
-  AttnStart* st = (AttnStart*)(smem + Lo::kOffStart);
+  AttnStart<kTN>* st = (AttnStart<kTN>*)(smem + Lo::kOffStart);
   float2* merge = (float2*)(smem + Lo::kOffMerge);
   PieceInfo* infos = (PieceInfo*)(smem + Lo::kOffPiece);
 
@@ -300,11 +346,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
-      mbar_init(&q_full[i], 2);
-      mbar_init(&q_empty[i], 9);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 13);
       mbar_init(&o_full[i], 1);
     }
-    mbar_init(pair, 8);
+    mbar_init(ml_full, 8);
+    mbar_init(ml_empty, 4);
+    mbar_init(o_free, 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *flags = 0;
@@ -318,11 +366,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  attn_plan<kMR, kTN>(p, st, flags);  // ends with a barrier
+  attn_plan<kTN>(p, st, flags);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   bool ok = true;
 
   // (The register split stands in each role's own branch: after a join the
@@ -330,8 +378,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     regs_dec<kRegsOther>();
-    long long u0;
-    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, flags, &u0);
+    AttnWalk<kTN> w = st->walk;
     const int bt = tp.box_tokens, E = kTN / bt;  // boxes along a tile's keys
     const int S = p.a.c.page_size;
     const int e = lane / Lo::kHalves, half = lane % Lo::kHalves;  // this lane's box
@@ -356,7 +403,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // pieces, whose products run a tile ahead, K0 K1 V0 K2 V1 ..
     bool pending = false;  // a V that the next K goes before
     int pend_t = 0, pend_h = 0, pend_pg = -1;
-    for (; !w.done() && ok; w.next()) {
+    for (; !w.done() && ok; w.next(p, flags)) {
       const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
       // The page of this lane's box of tile t; -1 past the item's end.
       auto page_at = [&](int t) {
@@ -370,7 +417,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         return pg;
       };
       const int t1 = w.last_tile();
-      const bool two = w.block_rows() > 128;
+      const bool two = w.block_rows(p) > tp.tile_rows;
       if (two && pending) {
         ok = load(&tmV, pend_t, pend_h, pend_pg);
         pending = false;
@@ -398,14 +445,23 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     regs_dec<kRegsOther>();
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_one();
       const uint32_t id_s = make_idesc(128, kTN, false), id_o = make_idesc(128, DP, true);
       const uint32_t q0 = smem_addr(smem + Lo::kOffQ), ring = smem_addr(smem + Lo::kOffRing);
       uint32_t slot = 0;  // next ring slot, in the order of use
       uint32_t n = 0, steps0 = 0, steps1 = 0;  // piece, P tiles of each stream so far
+      // A piece's first products overwrite O: the results of the one before are read.
+      auto wait_o_free = [&](uint32_t piece) {
+        if (piece == 0) return true;
+        const bool r = __all_sync(0xffffffffu, mbar_wait(o_free, (piece - 1) & 1u, abort_flag, tp.wait_budget));
+        tc_fence_after();
+        return r;
+      };
       auto wait_full = [&](uint32_t sl) {
-        const bool r = mbar_wait(&kv_full[sl % Lo::kStages], (sl / Lo::kStages) & 1u, abort_flag,
-                                 tp.wait_budget);
+        const bool r = __all_sync(0xffffffffu, mbar_wait(&kv_full[sl % Lo::kStages],
+                                                         (sl / Lo::kStages) & 1u, abort_flag,
+                                                         tp.wait_budget));
         tc_fence_after();
         return r;
       };
@@ -418,26 +474,27 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const int off = ((kk / 4) * Lo::kHalfBytes + (kk % 4) * 32) >> 4;
-          mma_ss(tmem + s * 128, qt + off, kt + off, id_s, kk != 0);
+          mma_ss(tmem + s * 128, qt + off, kt + off, id_s, kk != 0, lead);
         }
-        tc_commit(&s_full[s]);
+        tc_commit(&s_full[s], lead);
       };
       auto pv = [&](int s, uint32_t sl, bool first) {  // O_s (+)= P_s V
         const uint64_t vt = v_desc + (sl % Lo::kStages) * (Lo::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTN / 16; ++kk)
           mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, vt + kk * (2048 >> 4), id_o,
-                 !(first && kk == 0));
+                 !(first && kk == 0), lead);
       };
-      auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages]); };
+      auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages], lead); };
       auto wait_p = [&](int s) {
         uint32_t& k = s ? steps1 : steps0;
-        const bool r = mbar_wait(&p_full[s], k++ & 1u, abort_flag, tp.wait_budget);
+        const bool r = __all_sync(0xffffffffu, mbar_wait(&p_full[s], k++ & 1u, abort_flag, tp.wait_budget));
         tc_fence_after();
         return r;
       };
       auto wait_piece = [&] {  // piece n published
-        const bool r = mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget);
+        const bool r = __all_sync(0xffffffffu, mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag,
+                                                         tp.wait_budget));
         tc_fence_after();
         return r;
       };
@@ -445,17 +502,17 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (!(ok = wait_piece())) break;
         int nt = infos[n & 1].nt;
         if (nt == 0) break;
-        if (infos[n & 1].rows > 128) {
+        if (infos[n & 1].rows > tp.tile_rows) {
           ok = wait_full(slot);
           if (!ok) break;
           qk(0, 0, slot);
           qk(1, 1, slot);
           release(slot);
-          if (nt == 1) tc_commit(&q_empty[n & 1]);
+          if (nt == 1) tc_commit(&q_empty[n & 1], lead);
           for (int j = 0; j < nt; ++j) {
             const uint32_t vs = slot + 1, ks = slot + 2;
             const bool more = j + 1 < nt;
-            if (!(ok = wait_full(vs) && wait_p(0))) break;
+            if (!(ok = wait_full(vs) && wait_p(0) && (j > 0 || wait_o_free(n)))) break;
             pv(0, vs, j == 0);
             if (more) {
               if (!(ok = wait_full(ks))) break;
@@ -467,18 +524,18 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (more) {
               qk(1, 1, ks);
               release(ks);
-              if (j + 2 == nt) tc_commit(&q_empty[n & 1]);
+              if (j + 2 == nt) tc_commit(&q_empty[n & 1], lead);
             }
             slot += 2;
           }
-          tc_commit(&o_full[n & 1]);
+          tc_commit(&o_full[n & 1], lead);
           ++n;
         } else {
           // A run of pieces of up to 128 rows: step i on stream i & 1; the
           // first product of step i + 2 follows the second of step i.
           int jq = 0;
           uint32_t iq = 0;           // steps whose first product is issued
-          uint32_t flags0 = 0, flags1 = 0;  // of the step in flight on a stream: 1 first, 2 last tile
+          uint32_t flags0 = 0, flags1 = 0;  // of the step in flight on a stream: 1 its first, 2 the piece's last, 4 its first
           bool open = true;
           uint32_t np = n;           // the piece of the second products
           auto issue_qk = [&] {
@@ -486,7 +543,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               ++n;
               if (!(ok = wait_piece())) return;
               nt = infos[n & 1].nt;
-              if (nt == 0 || infos[n & 1].rows > 128) {
+              if (nt == 0 || infos[n & 1].rows > tp.tile_rows) {
                 open = false;
                 return;
               }
@@ -497,8 +554,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             qk(s, n & 1, slot);
             release(slot++);
             const bool last = ++jq == nt;
-            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u);
-            if (last) tc_commit(&q_empty[n & 1]);
+            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u) | (jq == 1 ? 4u : 0u);
+            if (last) tc_commit(&q_empty[n & 1], lead);
             ++iq;
           };
           issue_qk();
@@ -507,18 +564,19 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const int s = i & 1;
             if (!(ok = wait_full(slot) && wait_p(s))) break;
             const uint32_t f = s ? flags1 : flags0;
+            if (f & 4u && !(ok = wait_o_free(np))) break;
             pv(s, slot, f & 1u);
             release(slot++);
-            if (f & 2u) tc_commit(&o_full[np++ & 1]);
+            if (f & 2u) tc_commit(&o_full[np++ & 1], lead);
             if (open) issue_qk();
           }
         }
       }
       // All products done before TMEM is freed.
-      tc_commit(drain);
+      tc_commit(drain, lead);
       mbar_drain(drain, 0, tp.wait_budget);
     }
-  } else if (warp < kProducerWarp) {
+  } else if (warp < kFirstRoleWarp) {
     // ------------------------------------------------------------ softmax
     regs_inc<kRegsSoftmax>();
     const int s = warp >> 2;               // stream
@@ -527,14 +585,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + 256;
     uint32_t base = 0;  // ring slot of the run's (or two-block piece's) first tile
     uint32_t run = 0;   // steps of the run before this piece
-    uint32_t n = 0, steps = 0, meets = 0;
-    // Both streams' warps reach this point (bounded, unlike a named barrier).
-    auto meet = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair);
-      return (bool)__all_sync(0xffffffffu,
-                              mbar_wait(pair, meets++ & 1u, abort_flag, tp.wait_budget));
-    };
+    uint32_t n = 0, steps = 0;
 
     while (true) {
       ok = __all_sync(0xffffffffu, mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget));
@@ -543,10 +594,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[n & 1]);
       if (c.nt == 0) break;
-      const bool two = c.rows > 128;
-      const int a = two ? s * 128 + trow : trow;  // row of the block
-      const bool live = a < c.rows;
-      const bool warp_live = (two ? s * 128 : 0) + (warp & 3) * 32 < c.rows;
+      const bool two = c.rows > tp.tile_rows;
+      const int a = two ? s * tp.tile_rows + trow : trow;  // row of the block
+      const bool live = trow < tp.tile_rows && a < c.rows;
+      const bool warp_live = (two ? s * tp.tile_rows : 0) + (warp & 3) * 32 < c.rows;
       const int lim = live ? c.lim + (c.row0 + a) / p.a.G : 0;  // keys the row sees
       float m = -INFINITY, l = 0.0f;
       bool first = true;
@@ -645,83 +696,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (lane == 0) mbar_arrive(&p_full[s]);
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait(&o_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget));
-      if (!ok) break;
-      tc_fence_after();
-
-      // ---- the piece's result
-      const int row = c.row0 + a, tok = row / p.a.G, g = row - tok * p.a.G, D = p.a.c.head_dim;
-      const size_t orow = (size_t)(c.q0 + tok) * p.a.Hq + c.h * p.a.G + g;
-      const size_t prow = ((size_t)blockIdx.x * 2 + (c.slot < 0 ? 0 : c.slot)) * kMR + a;
-      int c_lo = 0, c_hi = DP;
-      float w0 = 1.0f, w1 = 0.0f;  // weights of the two streams' O
-      uint32_t own = tO + s * 128;
-      const bool both = !two && c.nt > 1;
-      if (!two) {
-        merge[s * 128 + trow] = make_float2(m, l);
-        if (!(ok = meet())) break;
-        const int s0 = run & 1;  // the stream of the piece's first tile
-        const float2 x0 = merge[s0 * 128 + trow], x1 = merge[(s0 ^ 1) * 128 + trow];
-        m = fmaxf(x0.x, x1.x);
-        const float ms = m == -INFINITY ? 0.0f : m;
-        w0 = ex2(x0.x - ms);
-        w1 = ex2(x1.x - ms);
-        l = x0.y * w0 + x1.y * w1;
-        own = tO + s0 * 128;
-        c_lo = s * (DP / 2);  // each stream's threads write half of the columns
-        c_hi = c_lo + DP / 2;
+      // (m, l) to the result warps, once they have read the piece before's.
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(ml_empty, (n - 1) & 1u, abort_flag, tp.wait_budget));
+        if (!ok) break;
       }
-      const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-      if (warp_live) {
-        for (int k = c_lo; k < c_hi; k += 32) {
-          uint32_t o[32];
-          tmem_ld32(own + k, o);
-          if (both) {
-            uint32_t o1[32];
-            tmem_ld32((own ^ 128u) + k, o1);  // tO + 128 (s0 ^ 1): the base is 256-aligned
-            tmem_wait_ld32(o);
-            tmem_wait_ld32(o1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * w0 + __uint_as_float(o1[i]) * w1);
-          } else {
-            tmem_wait_ld32(o);
-          }
-          if (live) {
-            if (c.slot < 0) {
-              uint4* out = (uint4*)((__nv_bfloat16*)p.a.out + orow * D + k);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (k + 8 * i < D) {
-                  uint32_t v[4];
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    v[q] = pack_bf16(__uint_as_float(o[8 * i + 2 * q]) * inv,
-                                     __uint_as_float(o[8 * i + 2 * q + 1]) * inv);
-                  out[i] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-              }
-            } else {
-              float4* out = (float4*)(p.part + prow * D + k);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (k + 4 * i < D)
-                  out[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-            }
-          }
-        }
-        if (live && (two || s == 0)) {
-          if (c.slot < 0)
-            p.a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
-          else
-            p.stats[prow] = make_float2(m, l);
-        }
-      }
-      // The next piece's second products overwrite O0 and O1, which both streams' threads read.
-      tc_fence_before();
-      if (!two && !(ok = meet())) break;
+      merge[s * 128 + trow] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ml_full);
       if (two) {
         base += 2 * c.nt;
       } else {
@@ -733,81 +715,188 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       ++n;
     }
-  } else {
-    // ------------------------------------------------------------ loaders
-    regs_dec<kRegsOther>();
-    long long u0;
-    AttnWalk<kMR, kTN> w = attn_walk<kMR, kTN>(p, *st, flags, &u0);
-    if (threadIdx.x == (kMmaWarp + 1) * 32) attn_write_cut(p, w, u0);
+  } else if (warp >= kResultWarp) {
+    // ------------------------------------------------------------ results
+    regs_dec<kRegsResult>();
+    const int trow = threadIdx.x & 127;
+    const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + 256;
     const int D = p.a.c.head_dim, G = p.a.G;
-    const int lt = threadIdx.x - (kMmaWarp + 1) * 32;  // 0 .. 63
+    uint32_t n = 0, run = 0;
+    while (true) {
+      ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget, 64));
+      if (!ok) break;
+      const PieceInfo c = infos[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[n & 1]);
+      if (c.nt == 0) break;
+      const bool two = c.rows > tp.tile_rows;
+      ok = __all_sync(0xffffffffu, mbar_wait_idle(ml_full, n & 1u, abort_flag, tp.wait_budget, 64));
+      if (!ok) break;
+      const int s0 = two ? 0 : (int)(run & 1u);  // the stream of a one-block piece's first tile
+      float2 x0 = merge[s0 * 128 + trow];
+      const float2 x1 = merge[(s0 ^ 1) * 128 + trow];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ml_empty);
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_idle(&o_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget, 64));
+      if (!ok) break;
+      tc_fence_after();
+      float w0 = 1.0f, w1 = 0.0f;  // weights of the two streams' O
+      const bool both = !two && c.nt > 1;
+      if (!two) {
+        const float m = fmaxf(x0.x, x1.x), ms = m == -INFINITY ? 0.0f : m;
+        w0 = ex2(x0.x - ms);
+        w1 = ex2(x1.x - ms);
+        x0 = make_float2(m, x0.y * w0 + x1.y * w1);
+      }
+      for (int blk = 0; blk < (two ? 2 : 1); ++blk) {
+        const float m = blk ? x1.x : x0.x, l = blk ? x1.y : x0.y;
+        const int a = blk * tp.tile_rows + trow;
+        if (blk * tp.tile_rows + (warp & 3) * 32 >= c.rows) continue;
+        const bool live = trow < tp.tile_rows && a < c.rows;
+        const unsigned row = c.row0 + a, tok = row / (unsigned)G, g = row - tok * G;
+        const size_t orow = (size_t)(c.q0 + tok) * p.a.Hq + c.h * G + g;
+        const size_t prow = ((size_t)blockIdx.x * 2 + (c.slot < 0 ? 0 : c.slot)) * kMR + a;
+        const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        const uint32_t own = tO + (uint32_t)(two ? blk : s0) * 128;
+        const float f0 = w0 * inv, f1 = w1 * inv;
+#pragma unroll 1
+        for (int k = 0; k < DP; k += 16) {
+          uint32_t o[16];
+          tmem_ld16(own + k, o);
+          if (both) {
+            uint32_t o1[16];
+            tmem_ld16((own ^ 128u) + k, o1);  // the other stream's: the base is 256-aligned
+            tmem_wait_ld16(o);
+            tmem_wait_ld16(o1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(o1[i]) * f1);
+          } else {
+            tmem_wait_ld16(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+          }
+          if (live) {
+            if (c.slot < 0) {
+              uint4* out = (uint4*)((__nv_bfloat16*)p.a.out + orow * D + k);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (k + 8 * i < D) {
+                  uint32_t v[4];
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    v[q] = pack_bf16(__uint_as_float(o[8 * i + 2 * q]),
+                                     __uint_as_float(o[8 * i + 2 * q + 1]));
+                  out[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+              }
+            } else {
+              uint4* out = (uint4*)(p.part + prow * D + k);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (k + 4 * i < D)
+                  out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+        }
+        if (live) {
+          if (c.slot < 0)
+            p.a.lse[orow] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+          else
+            p.stats[prow] = make_float2(m, l);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      run = two || !c.next_joined ? 0 : run + c.nt;
+      ++n;
+    }
+  } else if (warp == kLoaderWarp) {
+    // ------------------------------------------------------------ loader
+    regs_dec<kRegsOther>();
+    AttnWalk<kTN> w = st->walk;
+    if (lane == 0) attn_write_cut(p, *st);
+    const int D = p.a.c.head_dim, G = p.a.G;
     bool prev_two = false;
-    for (uint32_t n = 0;; ++n) {
+    uint32_t n = 0;
+    for (;; ++n) {
       const bool end = w.done();
       PieceInfo c;
       c.t0 = end ? 0 : w.first_tile();
       c.nt = end ? 0 : w.last_tile() - c.t0;
-      c.rows = end ? 0 : w.block_rows();
-      c.row0 = w.m * kMR;
+      c.rows = end ? 0 : w.block_rows(p);
+      c.row0 = w.m * p.mr;
       c.h = w.h;
       c.q0 = w.q.q0;
       c.lim = w.q.L - w.q.n + 1;
       c.end = w.end;
       c.slot = end ? 0 : attn_slot(w);
       c.next_joined = 0;
-      const bool two = c.rows > 128;
+      const bool two = c.rows > tp.tile_rows;
       // The Q tile(s) of this piece and its info slot are free again: piece n - 2
       // is done with them, and piece n - 1 where either of the two takes both.
       if (n >= 2)
         ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_empty[n & 1], ((n - 2) >> 1) & 1u, abort_flag,
-                                               tp.wait_budget));
+                                                    tp.wait_budget));
       if (ok && n >= 1 && (two || prev_two))
         ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_empty[(n - 1) & 1], ((n - 1) >> 1) & 1u,
-                                               abort_flag, tp.wait_budget));
+                                                    abort_flag, tp.wait_budget));
       if (!ok) break;
+      uint8_t* tile = smem + Lo::kOffQ + (two ? 0 : (int)(n & 1) * Lo::kTileBytes);
       if (!end) {
-        // Rows into the swizzled tiles.  Columns past D are zero (K's are, by
-        // the tensor map's fill); rows past the block's are not written: their
-        // results are not read.
-        constexpr int kChunks = DP / 8;  // 16-byte chunks a row
-        uint8_t* tile = smem + Lo::kOffQ + (two ? 0 : (int)(n & 1) * Lo::kTileBytes);
-        const uint32_t tile_s = smem_addr(tile);
-        const bool async = tp.q_vec && tp.sign > 0.0f;
-        for (int i = lt; i < c.rows * kChunks; i += 64) {
-          const int a = i / kChunks, ch = i % kChunks;
-          const unsigned row = c.row0 + a, tok = row / (unsigned)G, g = row - tok * G;
-          const __nv_bfloat16* src = (const __nv_bfloat16*)p.a.q +
-                                     (long long)(c.q0 + tok) * p.a.q_token_stride +
-                                     (long long)(c.h * G + g) * p.a.q_head_stride;
-          const uint32_t off = (uint32_t)((a >> 7) * Lo::kTileBytes + (ch >> 3) * Lo::kHalfBytes) +
-                               swz(a & 127, ch & 7);
-          const bool in = ch * 8 < D;  // D % 8 == 0
-          if (async) {  // (no bytes read past D: zeros)
-            cp_async16(tile_s + off, in ? src + ch * 8 : src, in ? 16 : 0);
-            continue;
-          }
-          uint32_t v[4] = {0u, 0u, 0u, 0u};
-          if (in) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              v[k] = (uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k]) |
-                     ((uint32_t)__bfloat16_as_ushort(src[ch * 8 + 2 * k + 1]) << 16);
-              if (tp.sign < 0.0f) v[k] ^= 0x80008000u;
-            }
-          }
-          *(uint4*)(tile + off) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        cp_async_wait();
-        fence_proxy_async();
-        w.next();
-        c.next_joined = !two && !w.done() && w.block_rows() <= 128;
+        w.next(p, flags);
+        c.next_joined = !two && !w.done() && w.block_rows(p) <= tp.tile_rows;
       }
-      if (lt == 0) infos[n & 1] = c;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[n & 1]);
-      if (end) break;
+      if (lane == 0) infos[n & 1] = c;
+      if (end) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[n & 1]);
+        break;
+      }
+      if (tp.q_tma) {
+        // One box a tile and half: q_tokens tokens x G heads, the tile's rows in
+        // order (tokens past the chunk's bring rows that are not read).
+        if (lane == 0) {
+          const int boxes = (two ? 2 : 1) * Lo::kHalves;
+          const uint32_t bytes = (uint32_t)tp.tile_rows * 128u;
+          mbar_expect_tx(&q_full[n & 1], boxes * bytes);
+          const int tok = c.q0 + c.row0 / G;
+          for (int b = 0; b < boxes; ++b) {
+            const int blk = b / Lo::kHalves, half = b % Lo::kHalves;
+            tma_load_3d(tile + blk * Lo::kTileBytes + half * Lo::kHalfBytes, &tmQ, half * 64, c.h * G,
+                        tok + blk * tp.q_tokens, &q_full[n & 1]);
+          }
+        }
+      } else {
+        // Element by element into the swizzled tiles; columns past D are zero
+        // (K's are, by the tensor map's fill).
+        for (int i = lane; i < c.rows * DP; i += 32) {
+          const int a = i / DP, d = i % DP;
+          const unsigned row = c.row0 + a, tok = row / (unsigned)G, g = row - tok * G;
+          unsigned short x = 0;
+          if (d < D) {
+            x = __bfloat16_as_ushort(
+                ((const __nv_bfloat16*)p.a.q)[(long long)(c.q0 + tok) * p.a.q_token_stride +
+                                              (long long)(c.h * G + g) * p.a.q_head_stride + d]);
+            if (tp.sign < 0.0f) x ^= 0x8000u;
+          }
+          const int blk = a >= tp.tile_rows ? 1 : 0, t = a - blk * tp.tile_rows;
+          *(unsigned short*)(tile + blk * Lo::kTileBytes + (d >> 6) * Lo::kHalfBytes +
+                             swz(t, (d >> 3) & 7) + (d & 7) * 2) = x;
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[n & 1]);
+      }
       prev_two = two;
     }
+    if (!ok && tp.q_tma && lane == 0)  // the loads that may still be in flight
+      for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
+        mbar_drain(&q_full[i & 1], (i >> 1) & 1u, tp.wait_budget);
+  } else {
+    regs_dec<kRegsOther>();
   }
   if (*abort_flag && lane == 0) flag_status(flags, DSPARK_DEV_TIMEOUT);
   tc_fence_before();
@@ -851,6 +940,20 @@ bool encode_cache(CUtensorMap* map, const void* base, const CacheView& c, int bo
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q as (head_dim, head, token); boxes of 64 columns, G heads and `tokens` tokens.
+bool encode_q(CUtensorMap* map, const AttnArgs& a, int tokens) {
+  const auto fn = get_encode();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.c.head_dim, (cuuint64_t)a.Hq, (cuuint64_t)a.a.n_tokens};
+  const cuuint64_t strides[2] = {a.Hq == 1 ? 16 : (cuuint64_t)a.q_head_stride * 2,
+                                 a.a.n_tokens == 1 ? 16 : (cuuint64_t)a.q_token_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)tokens};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static const int n = [] {
     int dev = 0, v = 0;
@@ -863,11 +966,12 @@ int sm_count() {
 }
 
 template <int DP>
-cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                   cudaStream_t s) {
   static const cudaError_t attr = cudaFuncSetAttribute(
       attention_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
   if (attr != cudaSuccess) return attr;
-  attention_tc_kernel<DP><<<sm_count(), kThreads, Layout<DP>::kBytes, s>>>(k, v, tp);
+  attention_tc_kernel<DP><<<sm_count(), kThreads, Layout<DP>::kBytes, s>>>(k, v, q, tp);
   return cudaGetLastError();
 }
 
@@ -897,15 +1001,23 @@ cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),
                     // (not 0: a masked score is -inf times this)
-                    fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f)};
+                    fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f), kMR};
   tp.sign = a.scale < 0 ? -1.0f : 1.0f;
   tp.box_tokens = a.c.page_size < kTN ? a.c.page_size : kTN;
-  tp.q_vec = ((uintptr_t)a.q & 15u) == 0 && a.q_token_stride % 8 == 0 && a.q_head_stride % 8 == 0;
+  tp.q_tokens = a.G <= 128 ? 128 / a.G : 1;
+  tp.tile_rows = a.G <= 128 ? tp.q_tokens * a.G : 128;
+  tp.p.mr = 2 * tp.tile_rows;
+  const long long most = 1ll << 39;
+  tp.q_tma = a.G <= 128 && a.scale >= 0 && ((uintptr_t)a.q & 15u) == 0 &&
+             (a.Hq == 1 || (a.q_head_stride % 8 == 0 && a.q_head_stride > 0 && a.q_head_stride < most)) &&
+             (a.a.n_tokens == 1 ||
+              (a.q_token_stride % 8 == 0 && a.q_token_stride > 0 && a.q_token_stride < most));
   tp.wait_budget = kWaitBudget;
-  CUtensorMap mk, mv;
+  CUtensorMap mk, mv, mq = {};
   if (!encode_cache(&mk, a.c.k, a.c, tp.box_tokens) || !encode_cache(&mv, a.c.v, a.c, tp.box_tokens))
     return cudaErrorInvalidValue;
-  cudaError_t e = a.c.head_dim <= 64 ? launch<64>(tp, mk, mv, s) : launch<128>(tp, mk, mv, s);
+  if (tp.q_tma && !encode_q(&mq, a, tp.q_tokens)) return cudaErrorInvalidValue;
+  cudaError_t e = a.c.head_dim <= 64 ? launch<64>(tp, mk, mv, mq, s) : launch<128>(tp, mk, mv, mq, s);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(tp.p, kMR, sm_count(), s);
 }

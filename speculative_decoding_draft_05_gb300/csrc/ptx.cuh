@@ -59,11 +59,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // mbar_wait for roles that run ahead and wait long: sleeps between polls, so
 // that the poll takes no issue slots from the warps that compute.
 __device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity,
-                                               volatile int* abort_flag, long long budget) {
+                                               volatile int* abort_flag, long long budget,
+                                               uint32_t sleep_ns = 200) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    __nanosleep(200);
+    __nanosleep(sleep_ns);
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > budget) {

@@ -76,7 +76,7 @@ def reference(i, layer=0):
             if p >= 0:
                 Kh, Vh = (x[: p + 1].repeat_interleave(G, 1) for x in (K, V))
                 s = torch.einsum("hd,jhd->hj", q[t], Kh) * i["scale"]
-                ds = ((D + 3) * U * i["scale"] * torch.einsum("hd,jhd->hj", q[t].abs(), Kh.abs())).amax(1)
+                ds = ((D + 3) * U * abs(i["scale"]) * torch.einsum("hd,jhd->hj", q[t].abs(), Kh.abs())).amax(1)
                 ds = ds + 2 * U * s.abs().amax(1)
                 lse[t] = torch.logsumexp(s, 1)
                 pr = torch.exp(s - lse[t][:, None])
@@ -131,6 +131,11 @@ SHAPES = [
     ([20], [6001], 32, 2, 128, 16),
     ([1] * 130, [(7 * r) % 300 + 1 for r in range(130)], 4, 2, 64, 16),
     ([2] * 700, [(r % 5) + 1 for r in range(700)], 2, 1, 64, 16),  # more requests than threads
+    ([3, 2], [70, 300], 4, 2, 40, 16),                # narrower than a swizzled row
+    ([2, 40], [9, 200], 3, 1, 16, 32),
+    ([3, 1], [200, 20], 130, 1, 64, 16),              # more query heads a K/V head than rows of a tile
+    ([60, 30, 1, 70], [60, 300, 900, 70], 12, 4, 128, 16),  # pieces of one and of two row tiles in turn
+    ([1, 200, 1, 1, 300, 2], [50, 200, 1300, 7, 900, 2], 20, 4, 64, 64),
 ]
 
 
@@ -163,6 +168,14 @@ def test_attention_with_large_scores_and_a_growing_maximum():
         i["k"][0][pages] = k.cuda()
         i["qkv"][:] = 0
         i["qkv"][:, :, 0] = 16.0
+        check(i, attend(i))
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1.0])
+def test_scales(scale):
+    for dtype in (F32, BF16):
+        i = make(dtype, [3, 20], [300, 40], 8, 2, 128, 16, seed=21)
+        i["scale"] = scale
         check(i, attend(i))
 
 
