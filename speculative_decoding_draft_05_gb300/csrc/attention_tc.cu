@@ -261,6 +261,26 @@ __device__ __forceinline__ void mask_from(uint32_t* x, int n) {
     if (k >= n) x[k] = 0xff800000u;
 }
 
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // {hi, lo} rounded to bf16 and packed.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -598,7 +618,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       const int a = two ? s * tp.tile_rows + trow : trow;  // row of the block
       const bool live = trow < tp.tile_rows && a < c.rows;
       const bool warp_live = (two ? s * tp.tile_rows : 0) + (warp & 3) * 32 < c.rows;
-      const int lim = live ? c.lim + (c.row0 + a) / p.a.G : 0;  // keys the row sees
+      // Keys the row sees (rows past the block's: their scores are left as they
+      // are, since a mask would slow the whole warp, and they are never read).
+      const int lim = live ? c.lim + (c.row0 + a) / p.a.G : 0x7fffffff;
       float m = -INFINITY, l = 0.0f;
       bool first = true;
       // This stream's tiles: all with two row blocks, else those on steps of its parity.
@@ -610,69 +632,114 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (!ok) break;
         tc_fence_after();
         if (warp_live) {
-          // Two passes over S: the maximum, columns 0..63 then 64..127; then the
-          // probabilities, 64..127 from registers and 0..63 read again (all 128
-          // columns in registers would spill).  P goes to columns 64..127.
           const int vis = lim - k0;  // keys of the tile that the row sees
           const bool masked = __any_sync(0xffffffffu, vis < kTN);
-          uint32_t x[64];
-          float mx = -INFINITY;
+          bool done = false;
+          if (!masked && !first) {
+            // One pass: probabilities against the maximum in use, and this tile's
+            // maximum beside them.  They stand unless a row's maximum grew by
+            // more than 2^8 (mostly in a piece's first tiles).
+            uint32_t pk[64], xa[32], xb[32];
+            const float ms = m == -INFINITY ? 0.0f : m;
+            const f32x2 sc2 = pack2(p.scale_log2, p.scale_log2), ms2 = pack2(-ms, -ms);
+            f32x2 sum2[2] = {0ull, 0ull};
+            float mx = -INFINITY;
+            auto chunk = [&](const uint32_t* v, uint32_t* out) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            tmem_ld32(tS + 64 * hh, x);
-            tmem_ld32(tS + 64 * hh + 32, x + 32);
-            tmem_wait_ld32(x);
-            tmem_wait_ld32(x + 32);
-            if (masked) mask_from<64>(x, vis - 64 * hh);
-#pragma unroll
-            for (int k = 0; k < 64; k += 2)
-              mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-          }
-          mx *= p.scale_log2;
-          const bool grow = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mx : m;
-            const float f = grow ? ex2(m - mn) : 1.0f;  // 0 where nothing was summed yet
-            if (!first) {
-#pragma unroll
-              for (int k = 0; k < DP; k += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + s * 128 + k, o);
-                tmem_wait_ld32(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(tO + s * 128 + k, o);
+              for (int i = 0; i < 16; ++i) {
+                const float v0 = __uint_as_float(v[2 * i]), v1 = __uint_as_float(v[2 * i + 1]);
+                mx = fmax3(mx, v0, v1);
+                float y0, y1;
+                unpack2(fma2(pack2(v0, v1), sc2, ms2), y0, y1);
+                const float e0 = ex2(y0), e1 = ex2(y1);
+                sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
+                out[i] = pack_bf16(e0, e1);
               }
+            };
+            tmem_ld32(tS, xa);
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 32, xb);
+            chunk(xa, pk);
+            tmem_wait_ld32(xb);
+            tmem_ld32(tS + 64, xa);
+            chunk(xb, pk + 16);
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 96, xb);
+            chunk(xa, pk + 32);
+            tmem_wait_ld32(xb);
+            chunk(xb, pk + 48);
+            if (!__any_sync(0xffffffffu, live && mx * p.scale_log2 > m + kRescaleLog2)) {
+              tmem_st32(tS + 64, pk);
+              tmem_st32(tS + 96, pk + 32);
+              float s0, s1;
+              unpack2(add2(sum2[0], sum2[1]), s0, s1);
+              l += s0 + s1;
+              done = true;
             }
-            l *= f;
-            m = mn;
+          }
+          if (!done) {
+            // Two passes over S: the maximum, columns 0..63 then 64..127; then the
+            // probabilities, 64..127 from registers and 0..63 read again (all 128
+            // columns in registers would spill).  P goes to columns 64..127.
+            uint32_t x[64];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              tmem_ld32(tS + 64 * hh, x);
+              tmem_ld32(tS + 64 * hh + 32, x + 32);
+              tmem_wait_ld32(x);
+              tmem_wait_ld32(x + 32);
+              if (masked) mask_from<64>(x, vis - 64 * hh);
+#pragma unroll
+              for (int k = 0; k < 64; k += 2)
+                mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            }
+            mx *= p.scale_log2;
+            const bool grow = live && (mx > m + kRescaleLog2 || (m == -INFINITY && mx > m));
+            if (__any_sync(0xffffffffu, grow)) {
+              const float mn = grow ? mx : m;
+              const float f = grow ? ex2(m - mn) : 1.0f;  // 0 where nothing was summed yet
+              if (!first) {
+#pragma unroll
+                for (int k = 0; k < DP; k += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(tO + s * 128 + k, o);
+                  tmem_wait_ld32(o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st32(tO + s * 128 + k, o);
+                }
+              }
+              l *= f;
+              m = mn;
+            }
+            const float ms = m == -INFINITY ? 0.0f : m;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            auto probs = [&](const uint32_t* v, int k) {  // 32 columns -> P's columns k ..
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, -ms));
+                const float e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, -ms));
+                sum[i & 3] += e0 + e1;
+                pk[i] = pack_bf16(e0, e1);
+              }
+              tmem_st16(tS + 64 + k, pk);
+            };
+            uint32_t y[32];
+            tmem_ld32(tS, y);
+            probs(x, 32);
+            probs(x + 32, 48);
+            tmem_wait_ld32(y);
+            tmem_ld32(tS + 32, x);
+            if (masked) mask_from<32>(y, vis);
+            probs(y, 0);
+            tmem_wait_ld32(x);
+            if (masked) mask_from<32>(x, vis - 32);
+            probs(x, 16);
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
           first = false;
-          const float ms = m == -INFINITY ? 0.0f : m;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          auto probs = [&](const uint32_t* v, int k) {  // 32 columns -> P's columns k ..
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, -ms));
-              const float e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, -ms));
-              sum[i & 3] += e0 + e1;
-              pk[i] = pack_bf16(e0, e1);
-            }
-            tmem_st16(tS + 64 + k, pk);
-          };
-          uint32_t y[32];
-          tmem_ld32(tS, y);
-          probs(x, 32);
-          probs(x + 32, 48);
-          tmem_wait_ld32(y);
-          tmem_ld32(tS + 32, x);
-          if (masked) mask_from<32>(y, vis);
-          probs(y, 0);
-          tmem_wait_ld32(x);
-          if (masked) mask_from<32>(x, vis - 32);
-          probs(x, 16);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
         tc_fence_before();
