@@ -6,9 +6,12 @@
 //   m' = max(m, max_j s_j),  p_j = 2^{s_j - m'},  l' = l 2^{m-m'} + sum_j p_j,
 //   O' = O 2^{m-m'} + P V
 // in units of log2, with S and O in TMEM and P (bf16) written over half of S in TMEM as
-// the first operand of P V.  A larger maximum rescales O and l only when it
-// grew by more than 2^8: until then p_j <= 2^8 stays far inside bf16's and
-// fp32's range, and out = O / l is the same whatever m the two share.
+// the first operand of P V.  out = O / l is the same whatever reference m the
+// two share, and floating-point rounding does not depend on it either, as long
+// as nothing leaves the exponent range.  So m starts at 0 and stays until a
+// row's maximum lies more than 60 above it (or, in a piece's first tile, below):
+// p <= 2^60, sums stay under 2^100, and a term that underflows is under 2^-66 of
+// the largest.  The softmax then needs one pass over S, not two.
 //
 // Structure (one CTA an SM, persistent over its share of the work; a piece is
 // the part of an item in it):
@@ -39,6 +42,7 @@
 #include <math.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "ptx.cuh"
@@ -55,7 +59,7 @@ constexpr int kThreads = 512;  // four warpgroups: two of softmax, the single ro
 constexpr int kRegsSoftmax = 168, kRegsOther = 96, kRegsResult = 80;
 constexpr int kFirstRoleWarp = 8;  // (8 idles: warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
 constexpr int kMmaWarp = 9, kLoaderWarp = 10, kProducerWarp = 11, kResultWarp = 12;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRangeLog2 = 60.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTmemCols = 512;  // S0, S1, O0, O1: 128 columns each
 
@@ -251,6 +255,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Whether a tile's row maximum (log2 units) is too far from the reference m:
+// above it, or, before anything is summed, below it (-inf: no key seen).
+__device__ __forceinline__ bool out_of_range(float mx, float m, bool first) {
+  return mx > m + kRangeLog2 || (first && mx < m - kRangeLog2 && mx > -INFINITY);
 }
 
 // Scores of keys at or past the first `n` become -inf.
@@ -621,7 +631,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       // Keys the row sees (rows past the block's: their scores are left as they
       // are, since a mask would slow the whole warp, and they are never read).
       const int lim = live ? c.lim + (c.row0 + a) / p.a.G : 0x7fffffff;
-      float m = -INFINITY, l = 0.0f;
+      float m = 0.0f, l = 0.0f;  // the reference in use, and the sum relative to it
       bool first = true;
       // This stream's tiles: all with two row blocks, else those on steps of its parity.
       for (int j = two ? 0 : (int)((s ^ run) & 1u); j < c.nt; j += two ? 1 : 2) {
@@ -634,20 +644,21 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (warp_live) {
           const int vis = lim - k0;  // keys of the tile that the row sees
           const bool masked = __any_sync(0xffffffffu, vis < kTN);
-          bool done = false;
-          if (!masked && !first) {
-            // One pass: probabilities against the maximum in use, and this tile's
-            // maximum beside them.  They stand unless a row's maximum grew by
-            // more than 2^8 (mostly in a piece's first tiles).
+          // One pass: probabilities against the reference in use, and this tile's
+          // maximum beside them.  They stand unless a row's maximum is out of range.
+          auto one_pass = [&](auto with_mask) {
             uint32_t pk[64], xa[32], xb[32];
-            const float ms = m == -INFINITY ? 0.0f : m;
-            const f32x2 sc2 = pack2(p.scale_log2, p.scale_log2), ms2 = pack2(-ms, -ms);
+            const f32x2 sc2 = pack2(p.scale_log2, p.scale_log2), ms2 = pack2(-m, -m);
             f32x2 sum2[2] = {0ull, 0ull};
             float mx = -INFINITY;
-            auto chunk = [&](const uint32_t* v, uint32_t* out) {
+            auto chunk = [&](const uint32_t* v, uint32_t* out, int k) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float v0 = __uint_as_float(v[2 * i]), v1 = __uint_as_float(v[2 * i + 1]);
+                float v0 = __uint_as_float(v[2 * i]), v1 = __uint_as_float(v[2 * i + 1]);
+                if (with_mask) {
+                  v0 = k + 2 * i < vis ? v0 : -INFINITY;
+                  v1 = k + 2 * i + 1 < vis ? v1 : -INFINITY;
+                }
                 mx = fmax3(mx, v0, v1);
                 float y0, y1;
                 unpack2(fma2(pack2(v0, v1), sc2, ms2), y0, y1);
@@ -659,24 +670,25 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             tmem_ld32(tS, xa);
             tmem_wait_ld32(xa);
             tmem_ld32(tS + 32, xb);
-            chunk(xa, pk);
+            chunk(xa, pk, 0);
             tmem_wait_ld32(xb);
             tmem_ld32(tS + 64, xa);
-            chunk(xb, pk + 16);
+            chunk(xb, pk + 16, 32);
             tmem_wait_ld32(xa);
             tmem_ld32(tS + 96, xb);
-            chunk(xa, pk + 32);
+            chunk(xa, pk + 32, 64);
             tmem_wait_ld32(xb);
-            chunk(xb, pk + 48);
-            if (!__any_sync(0xffffffffu, live && mx * p.scale_log2 > m + kRescaleLog2)) {
-              tmem_st32(tS + 64, pk);
-              tmem_st32(tS + 96, pk + 32);
-              float s0, s1;
-              unpack2(add2(sum2[0], sum2[1]), s0, s1);
-              l += s0 + s1;
-              done = true;
-            }
-          }
+            chunk(xb, pk + 48, 96);
+            mx *= p.scale_log2;
+            if (__any_sync(0xffffffffu, live && out_of_range(mx, m, first))) return false;
+            tmem_st32(tS + 64, pk);
+            tmem_st32(tS + 96, pk + 32);
+            float s0, s1;
+            unpack2(add2(sum2[0], sum2[1]), s0, s1);
+            l += s0 + s1;
+            return true;
+          };
+          const bool done = masked ? one_pass(std::true_type{}) : one_pass(std::false_type{});
           if (!done) {
             // Two passes over S: the maximum, columns 0..63 then 64..127; then the
             // probabilities, 64..127 from registers and 0..63 read again (all 128
@@ -695,10 +707,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
             }
             mx *= p.scale_log2;
-            const bool grow = live && (mx > m + kRescaleLog2 || (m == -INFINITY && mx > m));
+            const bool grow = live && out_of_range(mx, m, first);
             if (__any_sync(0xffffffffu, grow)) {
               const float mn = grow ? mx : m;
-              const float f = grow ? ex2(m - mn) : 1.0f;  // 0 where nothing was summed yet
+              const float f = grow && !first ? ex2(m - mn) : 1.0f;  // (first: nothing is summed yet)
               if (!first) {
 #pragma unroll
                 for (int k = 0; k < DP; k += 32) {
@@ -713,14 +725,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               l *= f;
               m = mn;
             }
-            const float ms = m == -INFINITY ? 0.0f : m;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             auto probs = [&](const uint32_t* v, int k) {  // 32 columns -> P's columns k ..
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, -ms));
-                const float e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, -ms));
+                const float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, -m));
+                const float e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, -m));
                 sum[i & 3] += e0 + e1;
                 pk[i] = pack_bf16(e0, e1);
               }
@@ -768,7 +779,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         ok = __all_sync(0xffffffffu, mbar_wait(ml_empty, (n - 1) & 1u, abort_flag, tp.wait_budget));
         if (!ok) break;
       }
-      merge[s * 128 + trow] = make_float2(m, l);
+      merge[s * 128 + trow] = make_float2(l == 0.0f ? -INFINITY : m, l);  // (no key seen: no weight)
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_full);
       if (two) {

@@ -171,6 +171,31 @@ def test_attention_with_large_scores_and_a_growing_maximum():
         check(i, attend(i))
 
 
+@pytest.mark.parametrize("level", [-300.0, -90.0, 90.0, 300.0])
+def test_scores_far_from_zero(level):
+    # every score of a row is near `level`: nothing may under- or overflow
+    for dtype in (F32, BF16):
+        i = make(dtype, [4, 20], [500, 150], 4, 2, 64, 16, seed=22)
+        i["qkv"][:, :, 0] = 16.0
+        i["k"][..., 0] = torch.where(i["k"][..., 0].isnan(), i["k"][..., 0], level * 8 / 16.0)
+        check(i, attend(i))
+
+
+def test_rows_that_fall_and_rise():
+    # a run of low tiles, one far above them, then low ones again
+    for dtype in (F32, BF16):
+        i = make(dtype, [3], [1100], 4, 2, 64, 16, seed=23)
+        pages = i["table"][0, :69].long()
+        lev = torch.full((69, 16), -200.0)
+        lev[30:33] = 150.0
+        lev[50] = 155.0
+        i["qkv"][:, :, 0] = 16.0
+        k = i["k"][0][pages]
+        k[..., 0] = (lev * 8 / 16.0)[:, :, None].to(dtype).cuda()
+        i["k"][0][pages] = k
+        check(i, attend(i))
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1.0])
 def test_scales(scale):
     for dtype in (F32, BF16):
