@@ -173,8 +173,7 @@ attention_simt_kernel(const AttnParams p) {
 }
 
 // Adds the pieces of the items that shares cut.  Block (b, y): the item that
-// CTA b + 1's share begins inside of, if its first piece lies in CTA b's share
-// (so exactly one b takes it); a warp takes one of its rows.
+// CTA b + 1's share is the first to begin inside of; a warp takes one of its rows.
 template <typename T, int NI>
 __global__ void __launch_bounds__(256)
 attention_combine_kernel(const AttnParams p, int MR, int ctas) {
@@ -189,16 +188,9 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
   const int c = blockIdx.x + 1;
   if (c >= ctas) return;
   const CutItem it = p.cuts[c];
-  if (!it.valid) return;
-  const long long units = *p.units;
-  if (it.u0 < attn_share(units, ctas, c - 1)) return;
-  const long long end = it.u0 + it.n_tiles;
-  // The last share with a piece: the one that holds unit end - 1.
-  const long long shares = units < ctas ? units : ctas;
-  const int last = (int)((end * shares - 1) / units);
-  const int n = last - c + 2;  // pieces: slot 1 of CTA c - 1, slot 0 of c .. last
+  const int n = it.pieces;
   const int a = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (a >= it.rows) return;
+  if (n == 0 || a >= it.rows) return;
   const int lane = threadIdx.x & 31, D = p.a.c.head_dim, G = p.a.G;
   const auto at = [&](int i) {
     return (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
@@ -227,7 +219,7 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
         if (lane + 32 * k < D) o[k] = fmaf(part[lane + 32 * k], w, o[k]);
     }
   }
-  const int row = it.m * p.mr + a, tok = row / G, g = row - tok * G;
+  const int row = it.row0 + a, tok = row / G, g = row - tok * G;
   const size_t dst = (size_t)(it.q0 + tok) * p.a.Hq + it.h * G + g;
   const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
 #pragma unroll
@@ -294,7 +286,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) 
   if (a.a.n_tokens == 0) return cudaMemsetAsync(ws, 0, sizeof(int), s);
   if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
-  AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
+  AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f,
                kMR};
   const cudaError_t e = a.dtype == DSPARK_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);

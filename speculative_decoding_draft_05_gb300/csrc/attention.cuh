@@ -26,22 +26,21 @@ constexpr int kAttnMaxCtas = 320;  // CTAs of one attention launch, at most
 // CTAs' times spread over 165 .. 244 us without it, around 190 us with it.
 constexpr int kAttnItemUnits = 2;
 
-// A cut item, written by the CTA whose share begins inside it.
+// A cut item, written by the first CTA whose share begins inside it.
 struct CutItem {
-  int valid, r, m, h;     // request, row block, K/V head
-  int n, q0, rows, n_tiles;  // chunk length, first token, rows of the block, tiles
-  long long u0;           // the unit of the item's first tile
-  long long pad;
+  int pieces;       // slot 1 of the CTA before, slot 0 of this one and those after; 0: no such item
+  int row0, rows;   // rows of the block within the chunk
+  int h, q0;        // K/V head, the chunk's first token
+  int pad[3];
 };
 
-// Workspace: status word, total units, per-CTA status bits, cut items, partial
-// (m, l) and O.  Nothing in it has to be cleared before a call.
+// Workspace: status word, per-CTA status bits, cut items, partial (m, l) and
+// O.  Nothing in it has to be cleared before a call.
 struct AttnWorkspace {
-  size_t units, flags, cuts, stats, out, total;
+  size_t flags, cuts, stats, out, total;
 };
 inline AttnWorkspace attn_workspace_layout(int MR, int D) {
   AttnWorkspace w;
-  w.units = 64;
   w.flags = 256;
   w.cuts = align_up256(w.flags + kAttnMaxCtas * sizeof(int));
   w.stats = align_up256(w.cuts + kAttnMaxCtas * sizeof(CutItem));
@@ -54,7 +53,6 @@ struct AttnParams {
   AttnArgs a;
   int* status;       // written by the combine
   int* flags;        // [grid] status bits of each CTA
-  long long* units;  // total units (for the combine)
   CutItem* cuts;     // [grid]
   float2* stats;     // [grid][2][MR] (m, l), m in log2 units
   float* part;       // [grid][2][MR][D]
@@ -106,7 +104,9 @@ __device__ __forceinline__ int attn_blocks(const AttnRequest& q, int G, int mr) 
 // CTAs get one each, so that no share between two others is empty.
 __device__ __forceinline__ long long attn_share(long long units, int ctas, int c) {
   const long long n = units < ctas ? units : ctas;
-  return c >= n ? units : units * c / n;
+  if (c >= n) return units;
+  if (units < (1 << 23)) return (unsigned)(units * c) / (unsigned)n;  // (c < 320: below 2^32)
+  return units * c / n;
 }
 
 // The walk of one CTA (or one warp role of it) over its share.
@@ -259,7 +259,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
             const long long first = base + upto - own;
             if (start >= first && start < first + own) {
               const long long d = start - first;
-              w.h = (int)(d / item);
+              w.h = d >> 31 ? (int)(d / item) : (int)d / item;
               w.pos = (int)(d - (long long)w.h * item);
               w.left = left;
               w.drop_empty();
@@ -273,20 +273,24 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
       }
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.units = units;
   __syncthreads();
 }
 
-// Written once a CTA: whether its share begins inside an item, and which.
+// Written once a CTA: the item that its share begins inside of, if it is the
+// first share to do so (the CTA before holds the item's first tile).
 template <int TN>
 __device__ __forceinline__ void attn_write_cut(const AttnParams& p, const AttnStart<TN>& st) {
   const AttnWalk<TN>& w = st.walk;
   CutItem c;
-  c.valid = !w.done() && w.first_tile() > 0;
-  if (c.valid) {
-    c.r = w.r, c.m = w.m, c.h = w.h;
-    c.n = w.q.n, c.q0 = w.q.q0, c.rows = w.block_rows(p), c.n_tiles = w.n_tiles;
-    c.u0 = st.u0;
+  c.pieces = 0;
+  if (!w.done() && w.first_tile() > 0 &&
+      st.u0 >= attn_share(st.units, gridDim.x, (int)blockIdx.x - 1)) {
+    // The last piece is in the share that holds the item's last unit.
+    const long long end = st.u0 + w.n_tiles, shares = st.units < gridDim.x ? st.units : gridDim.x;
+    const int last = (int)((end * shares - 1) / st.units);
+    c.pieces = last - (int)blockIdx.x + 2;
+    c.row0 = w.m * p.mr, c.rows = w.block_rows(p);
+    c.h = w.h, c.q0 = w.q.q0;
   }
   p.cuts[blockIdx.x] = c;
 }

@@ -85,6 +85,10 @@ struct Layout {
 static_assert(Layout<128>::kEnd <= 232448, "shared memory");
 static_assert(sizeof(AttnStart<kTN>) <= 2 * 128 * 8, "the plan's scratch lies in the merge buffer");
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             uint64_t* bar) {
   asm volatile(
@@ -368,6 +372,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   PieceInfo* infos = (PieceInfo*)(smem + Lo::kOffPiece);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == kProducerWarp * 32) {
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
+  if (threadIdx.x == kLoaderWarp * 32 && tp.q_tma) prefetch_map(&tmQ);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lo::kStages; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -435,11 +444,12 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     int pend_t = 0, pend_h = 0, pend_pg = -1;
     for (; !w.done() && ok; w.next(p, flags)) {
       const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
-      // The page of this lane's box of tile t; -1 past the item's end.
-      auto page_at = [&](int t) {
-        const int key = t * kTN + e * bt;
-        if (e >= E || key >= w.end) return -1;
-        int pg = __ldg(table + key / S);
+      // The page of this lane's box of tile t, as the table has it, if the item
+      // has keys there.  It is checked when it is used, a tile later.
+      auto has_box = [&](int t) { return e < E && t * kTN + e * bt < w.end; };
+      auto page_at = [&](int t) { return has_box(t) ? __ldg(table + (t * kTN + e * bt) / S) : -1; };
+      auto checked = [&](int t, int pg) {
+        if (!has_box(t)) return -1;
         if (pg < 0 || pg >= p.a.c.n_pages) {
           flag_status(flags, DSPARK_DEV_BAD_INPUT);
           pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
@@ -452,9 +462,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         ok = load(&tmV, pend_t, pend_h, pend_pg);
         pending = false;
       }
-      int pg = page_at(w.first_tile());
+      int raw = page_at(w.first_tile());
       for (int t = w.first_tile(); t < t1 && ok; ++t) {
-        const int pg_next = t + 1 < t1 ? page_at(t + 1) : -1;  // read a tile ahead
+        const int raw_next = t + 1 < t1 ? page_at(t + 1) : -1;  // read a tile ahead
+        const int pg = checked(t, raw);
         ok = load(&tmK, t, w.h, pg);
         if (two) {
           ok = ok && load(&tmV, t, w.h, pg);
@@ -463,7 +474,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           pending = true;
           pend_t = t, pend_h = w.h, pend_pg = pg;
         }
-        pg = pg_next;
+        raw = raw_next;
       }
     }
     if (ok && pending) ok = load(&tmV, pend_t, pend_h, pend_pg);
@@ -1076,7 +1087,7 @@ size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout
 cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
   TcParams tp;
-  tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (long long*)(ws + w.units), (CutItem*)(ws + w.cuts),
+  tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),
                     // (not 0: a masked score is -inf times this)
                     fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f), kMR};

@@ -715,7 +715,10 @@ __device__ __forceinline__ int find_request(const int32_t* off, int R, int t) {
   return lo;
 }
 
-// One warp a token: VE elements (16 bytes, or one where alignment does not allow) a lane and step.
+// One warp a token: VE elements (16 bytes, or one where alignment does not
+// allow) a lane and step.  The first kAppendAhead steps' rows are loaded before
+// the token's request, position and page are looked up (four dependent loads).
+constexpr int kAppendAhead = 4;
 template <typename E, int VE>
 __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
   struct alignas(sizeof(E) * VE) Vec {
@@ -725,10 +728,22 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
   const int S = p.c.page_size;
   const int per_head = p.c.head_dim / VE, n = p.c.heads * per_head;
   for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.a.n_tokens; t += gridDim.x * 8) {
+    const E* kn = (const E*)p.k_new + t * p.tok_stride;
+    const E* vn = (const E*)p.v_new + t * p.tok_stride;
+    Vec kx[kAppendAhead], vx[kAppendAhead];
+#pragma unroll
+    for (int k = 0; k < kAppendAhead; ++k) {
+      const int i = lane + 32 * k;
+      if (i < n) {
+        const int h = i / per_head, d = (i - h * per_head) * VE;
+        kx[k] = *(const Vec*)(kn + h * p.head_stride + d);
+        vx[k] = *(const Vec*)(vn + h * p.head_stride + d);
+      }
+    }
     const int r = find_request(p.a.q_offsets, p.a.R, t);
     const int end = p.a.q_offsets[r + 1];
     const long long pos = (long long)p.a.kv_len[r] - end + t;
-    long long slot = pos / S;
+    const long long slot = pos / S;
     int page = -1;
     if (t >= p.a.q_offsets[r] && t < end && pos >= 0 && slot < p.a.max_pages)
       page = p.a.page_table[(size_t)r * p.a.max_pages + slot];
@@ -738,15 +753,22 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
       continue;
     }
     const long long dst0 = page * p.c.page_stride + (pos - slot * S) * p.c.token_stride;
-    const E* kn = (const E*)p.k_new + t * p.tok_stride;
-    const E* vn = (const E*)p.v_new + t * p.tok_stride;
+#pragma unroll
+    for (int k = 0; k < kAppendAhead; ++k) {
+      const int i = lane + 32 * k;
+      if (i < n) {
+        const int h = i / per_head, d = (i - h * per_head) * VE;
+        *(Vec*)((E*)p.c.k + dst0 + h * p.c.head_stride + d) = kx[k];
+        *(Vec*)((E*)p.c.v + dst0 + h * p.c.head_stride + d) = vx[k];
+      }
+    }
 #pragma unroll 4
-    for (int i = lane; i < n; i += 32) {
+    for (int i = lane + 32 * kAppendAhead; i < n; i += 32) {
       const int h = i / per_head, d = (i - h * per_head) * VE;
-      const Vec kx = *(const Vec*)(kn + h * p.head_stride + d);
-      const Vec vx = *(const Vec*)(vn + h * p.head_stride + d);
-      *(Vec*)((E*)p.c.k + dst0 + h * p.c.head_stride + d) = kx;
-      *(Vec*)((E*)p.c.v + dst0 + h * p.c.head_stride + d) = vx;
+      const Vec a = *(const Vec*)(kn + h * p.head_stride + d);
+      const Vec b = *(const Vec*)(vn + h * p.head_stride + d);
+      *(Vec*)((E*)p.c.k + dst0 + h * p.c.head_stride + d) = a;
+      *(Vec*)((E*)p.c.v + dst0 + h * p.c.head_stride + d) = b;
     }
   }
 }
