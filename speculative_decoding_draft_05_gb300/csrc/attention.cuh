@@ -179,11 +179,14 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
   const int R = p.a.a.R, G = p.a.G, Hkv = p.a.c.heads;
   const int per = (R + (int)blockDim.x - 1) / (int)blockDim.x;
   const int r0 = (int)threadIdx.x * per;
-  // Units of the thread's i-th request, which all lanes of the warp call for together.
-  auto units_of = [&](int i, AttnRequest& q) -> long long {
+  // Units of the thread's i-th request, which all lanes of the warp call for
+  // together.  (With one request a thread the second call finds it in q.)
+  auto units_of = [&](int i, AttnRequest& q, bool again) -> long long {
     const int r = r0 + i;
-    q = AttnRequest{0, 0, 0};
-    if (r < R) q = attn_request(p.a.a, p.a.c.page_size, r, flags);
+    if (!again || per > 1) {
+      q = AttnRequest{0, 0, 0};
+      if (r < R) q = attn_request(p.a.a, p.a.c.page_size, r, flags);
+    }
     const int blocks = attn_blocks(q, G, p.mr);
     long long u = blocks == 1 ? attn_tiles<TN>(q.L) + kAttnItemUnits : 0;
     for (unsigned todo = __ballot_sync(0xffffffffu, blocks > 1); todo; todo &= todo - 1) {
@@ -201,7 +204,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
   };
   long long mine = 0;
   AttnRequest q;
-  for (int i = 0; i < per; ++i) mine += units_of(i, q);
+  for (int i = 0; i < per; ++i) mine += units_of(i, q, false);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -231,7 +234,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
     long long at = st->scan[warp] + incl - mine;  // the thread's first unit
     if (__any_sync(0xffffffffu, start >= at && start < at + mine)) {  // one warp
       for (int i = 0; i < per; ++i) {
-        const long long k = units_of(i, q);
+        const long long k = units_of(i, q, true);
         const bool here = start >= at && start < at + k;  // one lane, for one i
         const unsigned who = __ballot_sync(0xffffffffu, here);
         if (who) {

@@ -75,7 +75,7 @@ struct Layout {
   static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
   static constexpr int kOffStart = kOffMerge;                        // (before the first merge)
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
-  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 1 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 1;
   static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 12 + 15) & ~15);  // PieceInfo [2]
   static constexpr int kEnd = kOffPiece + 2 * 64;
   // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
@@ -362,8 +362,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* o_full = q_empty + 2;  // [2] piece n's last product done
   uint64_t* ml_full = o_full + 2;  // piece n's (m, l) written (8 softmax warps)
   uint64_t* ml_empty = ml_full + 1;  // and read (4 result warps)
-  uint64_t* o_free = ml_empty + 1;   // piece n's O read (4 result warps)
-  uint64_t* drain = o_free + 1;
+  uint64_t* o_free = ml_empty + 1;   // [2] a stream's O of piece n read (4 result warps)
+  uint64_t* drain = o_free + 2;
   uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   int* flags = (int*)(tmem_slot + 2);  // the CTA's status bits
@@ -391,7 +391,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
     mbar_init(ml_full, 8);
     mbar_init(ml_empty, 4);
-    mbar_init(o_free, 4);
+    mbar_init(&o_free[0], 4);
+    mbar_init(&o_free[1], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *flags = 0;
@@ -493,9 +494,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       uint32_t slot = 0;  // next ring slot, in the order of use
       uint32_t n = 0, steps0 = 0, steps1 = 0;  // piece, P tiles of each stream so far
       // A piece's first products overwrite O: the results of the one before are read.
-      auto wait_o_free = [&](uint32_t piece) {
+      auto wait_o_free = [&](int s, uint32_t piece) {
         if (piece == 0) return true;
-        const bool r = __all_sync(0xffffffffu, mbar_wait(o_free, (piece - 1) & 1u, abort_flag, tp.wait_budget));
+        const bool r = __all_sync(0xffffffffu, mbar_wait(&o_free[s], (piece - 1) & 1u, abort_flag,
+                                                         tp.wait_budget));
         tc_fence_after();
         return r;
       };
@@ -553,13 +555,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           for (int j = 0; j < nt; ++j) {
             const uint32_t vs = slot + 1, ks = slot + 2;
             const bool more = j + 1 < nt;
-            if (!(ok = wait_full(vs) && wait_p(0) && (j > 0 || wait_o_free(n)))) break;
+            if (!(ok = wait_full(vs) && wait_p(0) && (j > 0 || wait_o_free(0, n)))) break;
             pv(0, vs, j == 0);
             if (more) {
               if (!(ok = wait_full(ks))) break;
               qk(0, 0, ks);
             }
-            if (!(ok = wait_p(1))) break;
+            if (!(ok = wait_p(1) && (j > 0 || wait_o_free(1, n)))) break;
             pv(1, vs, j == 0);
             release(vs);
             if (more) {
@@ -576,7 +578,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           // first product of step i + 2 follows the second of step i.
           int jq = 0;
           uint32_t iq = 0;           // steps whose first product is issued
-          uint32_t flags0 = 0, flags1 = 0;  // of the step in flight on a stream: 1 its first, 2 the piece's last, 4 its first
+          uint32_t flags0 = 0, flags1 = 0;  // of the step in flight on a stream: 1 its first, 2 the piece's last
           bool open = true;
           uint32_t np = n;           // the piece of the second products
           auto issue_qk = [&] {
@@ -595,7 +597,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             qk(s, n & 1, slot);
             release(slot++);
             const bool last = ++jq == nt;
-            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u) | (jq == 1 ? 4u : 0u);
+            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u);
             if (last) tc_commit(&q_empty[n & 1], lead);
             ++iq;
           };
@@ -605,7 +607,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const int s = i & 1;
             if (!(ok = wait_full(slot) && wait_p(s))) break;
             const uint32_t f = s ? flags1 : flags0;
-            if (f & 4u && !(ok = wait_o_free(np))) break;
+            if (f & 1u && !(ok = wait_o_free(s, np))) break;
             pv(s, slot, f & 1u);
             release(slot++);
             if (f & 2u) tc_commit(&o_full[np++ & 1], lead);
@@ -839,9 +841,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         x0 = make_float2(m, x0.y * w0 + x1.y * w1);
       }
       for (int blk = 0; blk < (two ? 2 : 1); ++blk) {
+        if (blk == 1) {  // the first block's O may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_free[0]);
+        }
         const float m = blk ? x1.x : x0.x, l = blk ? x1.y : x0.y;
         const int a = blk * tp.tile_rows + trow;
-        if (blk * tp.tile_rows + (warp & 3) * 32 >= c.rows) continue;
+        if (blk * tp.tile_rows + (warp & 3) * 32 >= c.rows) continue;  // (arrives below)
         const bool live = trow < tp.tile_rows && a < c.rows;
         const unsigned row = c.row0 + a, tok = row / (unsigned)G, g = row - tok * G;
         const size_t orow = (size_t)(c.q0 + tok) * p.a.Hq + c.h * G + g;
@@ -849,44 +856,51 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
         const uint32_t own = tO + (uint32_t)(two ? blk : s0) * 128;
         const float f0 = w0 * inv, f1 = w1 * inv;
+        // 16 columns at a time from both streams, or 32 from one.
+        auto store16 = [&](const uint32_t* o, int k) {
+          if (!live) return;
+          if (c.slot < 0) {
+            uint4* out = (uint4*)((__nv_bfloat16*)p.a.out + orow * D + k);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (k + 8 * i < D) {
+                uint32_t v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  v[q] = pack_bf16(__uint_as_float(o[8 * i + 2 * q]), __uint_as_float(o[8 * i + 2 * q + 1]));
+                out[i] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          } else {
+            uint4* out = (uint4*)(p.part + prow * D + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (k + 4 * i < D) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        };
+        if (both) {
 #pragma unroll 1
-        for (int k = 0; k < DP; k += 16) {
-          uint32_t o[16];
-          tmem_ld16(own + k, o);
-          if (both) {
-            uint32_t o1[16];
+          for (int k = 0; k < DP; k += 16) {
+            uint32_t o[16], o1[16];
+            tmem_ld16(own + k, o);
             tmem_ld16((own ^ 128u) + k, o1);  // the other stream's: the base is 256-aligned
             tmem_wait_ld16(o);
             tmem_wait_ld16(o1);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(o1[i]) * f1);
-          } else {
-            tmem_wait_ld16(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+            store16(o, k);
           }
-          if (live) {
-            if (c.slot < 0) {
-              uint4* out = (uint4*)((__nv_bfloat16*)p.a.out + orow * D + k);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < DP; k += 32) {
+            uint32_t o[32];
+            tmem_ld32(own + k, o);
+            tmem_wait_ld32(o);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (k + 8 * i < D) {
-                  uint32_t v[4];
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    v[q] = pack_bf16(__uint_as_float(o[8 * i + 2 * q]),
-                                     __uint_as_float(o[8 * i + 2 * q + 1]));
-                  out[i] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-              }
-            } else {
-              uint4* out = (uint4*)(p.part + prow * D + k);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (k + 4 * i < D)
-                  out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+            store16(o, k);
+            store16(o + 16, k + 16);
           }
         }
         if (live) {
@@ -898,7 +912,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) {
+        if (!two) mbar_arrive(&o_free[0]);
+        mbar_arrive(&o_free[1]);
+      }
       run = two || !c.next_joined ? 0 : run + c.nt;
       ++n;
     }
@@ -906,7 +923,6 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     // ------------------------------------------------------------ loader
     regs_dec<kRegsOther>();
     AttnWalk<kTN> w = st->walk;
-    if (lane == 0) attn_write_cut(p, *st);
     const int D = p.a.c.head_dim, G = p.a.G;
     bool prev_two = false;
     uint32_t n = 0;
@@ -986,6 +1002,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         mbar_drain(&q_full[i & 1], (i >> 1) & 1u, tp.wait_budget);
   } else {
     regs_dec<kRegsOther>();
+    if (lane == 0) attn_write_cut(p, *st);
   }
   if (*abort_flag && lane == 0) flag_status(flags, DSPARK_DEV_TIMEOUT);
   tc_fence_before();
