@@ -219,6 +219,23 @@ __device__ __forceinline__ void block_sums(const Block<T>& b, int v0, int V, flo
   a.t += ta;
 }
 
+struct RowOutputs {
+  float *logp, *entropy, *lse;  // [n_rows]
+  int32_t* top_ids;             // [n_rows, top]
+  float* top_logp;
+  int top;
+};
+
+__device__ __forceinline__ void skip_row(const RowOutputs& o, int r) {
+  const int lane = threadIdx.x & 31;
+  const float nan = __int_as_float(0x7fc00000);
+  if (lane == 0) o.logp[r] = o.entropy[r] = o.lse[r] = nan;
+  if (lane < o.top) {
+    o.top_ids[(size_t)r * o.top + lane] = -1;
+    o.top_logp[(size_t)r * o.top + lane] = nan;
+  }
+}
+
 // The wanted rows' chunks, dealt out to all warps in turn, so that the whole
 // GPU reads one moving window of memory (contiguous shares a CTA, hundreds of
 // places of a 2.6 GB array at once, took 214 us where this takes 156, with the
@@ -228,12 +245,17 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas)
 logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
                        const int32_t* __restrict__ tokens, int n_rows, int V, int chunks,
-                       int groups, float c, float4* parts, float* gmax, int* status) {
+                       int groups, float c, float4* parts, float* gmax, int* rows_wanted,
+                       const RowOutputs o, int* status) {
   __shared__ int sm[kRowWarps];
   __shared__ uint16_t list[kListRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
+  // Rows without a token get their results here.
+  for (int r = blockIdx.x * kRowWarps + warp; r < n_rows; r += gridDim.x * kRowWarps)
+    if (__ldg(tokens + r) < 0) skip_row(o, r);
+  int listed = 0;
   // A window of rows at a time (one, up to kListRows rows).
   for (int w0 = 0; w0 < n_rows; w0 += kListRows) {
     const int rows = min(kListRows, n_rows - w0);
@@ -252,6 +274,9 @@ logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
     for (int r = r0; r < r1; ++r)
       if (__ldg(tokens + w0 + r) >= 0) list[k++] = (uint16_t)r;
     __syncthreads();
+    if (blockIdx.x == 0)  // the second kernel's list: [0] how many, then the rows
+      for (int i = threadIdx.x; i < n; i += kRowThreads) rows_wanted[1 + listed + i] = w0 + list[i];
+    listed += n;
     const long long units = (long long)n * chunks;
     const int all_warps = gridDim.x * kRowWarps, me = blockIdx.x * kRowWarps + warp;
     const int dk = all_warps / chunks, dch = all_warps - dk * chunks;
@@ -275,7 +300,10 @@ logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
     __syncthreads();
   }
   const int any_bad = __syncthreads_or(bad);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = any_bad ? DSPARK_DEV_BAD_INPUT : 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *status = any_bad ? DSPARK_DEV_BAD_INPUT : 0;
+    rows_wanted[0] = listed;
+  }
 }
 
 // Order of the alternatives as unsigned keys: larger logit, larger key; NaN
@@ -305,23 +333,6 @@ struct RowScratch {
   unsigned long long cand[kMaxCand];  // key, then ~id: the larger comes first
   int picked[kMaxPicked], n_cand;
 };
-
-struct RowOutputs {
-  float *logp, *entropy, *lse;  // [n_rows]
-  int32_t* top_ids;             // [n_rows, top]
-  float* top_logp;
-  int top;
-};
-
-__device__ __forceinline__ void skip_row(const RowOutputs& o, int r) {
-  const int lane = threadIdx.x & 31;
-  const float nan = __int_as_float(0x7fc00000);
-  if (lane == 0) o.logp[r] = o.entropy[r] = o.lse[r] = nan;
-  if (lane < o.top) {
-    o.top_ids[(size_t)r * o.top + lane] = -1;
-    o.top_logp[(size_t)r * o.top + lane] = nan;
-  }
-}
 
 // Row r's results from its sums, by one warp; gm: its groups' largest logits (changed).
 template <typename T>
@@ -382,11 +393,12 @@ __device__ __forceinline__ void finish_row(const T* row, int r, float x_tok, int
     }
     __syncwarp();
     if (n_picked <= kMaxPicked) {
-      for (int i0 = 0; i0 < n_picked; i0 += 4) {
-        Eight<T> x[4];
-        int v[4];
+      constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;  // groups in flight
+      for (int i0 = 0; i0 < n_picked; i0 += kBatch) {
+        Eight<T> x[kBatch];
+        int v[kBatch];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
           v[k] = i0 + k < n_picked ? picked[i0 + k] * kGroupIds + lane * 8 : V;
           if (v[k] < V)
             x[k].load(row + v[k]);
@@ -394,7 +406,7 @@ __device__ __forceinline__ void finish_row(const T* row, int r, float x_tok, int
             x[k].fill_low();
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kBatch; ++k)
           if (x[k].max() >= floor_x) {  // few lanes
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -468,20 +480,23 @@ __device__ __forceinline__ void finish_row(const T* row, int r, float x_tok, int
   }
 }
 
-// Merges the chunks of a row and finishes it: one warp a row.
+// Merges the chunks of a wanted row and finishes it: one warp a row, the first
+// CTAs (the list keeps the SMs evenly loaded: with the rows in place, most of a
+// CTA's warps would have none).
 template <typename T>
 __global__ void __launch_bounds__(kFinishWarps * 32)
 logprobs_finish_kernel(const T* __restrict__ Z, long long row_stride,
-                       const int32_t* __restrict__ tokens, int n_rows, int V, int chunks, int groups,
-                       float c, float invT, const float4* parts, float* gmax, const RowOutputs o) {
+                       const int32_t* __restrict__ tokens, int V, int chunks, int groups, float c,
+                       float invT, const float4* parts, float* gmax, const int* rows_wanted,
+                       const RowOutputs o) {
   __shared__ RowScratch scratch[kFinishWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x * kFinishWarps + warp;
-  const int tok = r < n_rows ? __ldg(tokens + r) : -1;
-  const T* row = Z + (long long)r * row_stride;
-  const float x_tok = tok >= 0 && tok < V ? to_f32(row[tok]) : __int_as_float(0x7fc00000);
-  if (tok < 0 && r < n_rows) skip_row(o, r);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * kFinishWarps + warp;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tok < 0) return;
+  const int r = __ldcg(rows_wanted + 1 + i);  // (read with the count: a row of the list or, past it, unused)
+  if (i >= __ldcg(rows_wanted)) return;
+  const int tok = __ldg(tokens + r);
+  const T* row = Z + (long long)r * row_stride;
+  const float x_tok = tok < V ? to_f32(row[tok]) : __int_as_float(0x7fc00000);
 
   float m = -INFINITY, s = 0.0f, t = 0.0f;
   for (int k = lane; k < chunks; k += 32) {
@@ -554,6 +569,7 @@ cudaError_t launch(const void* Z, long long row_stride, const int32_t* tokens, i
                    cudaStream_t s) {
   float4* parts = (float4*)(ws + w.parts);
   float* gmax = (float*)(ws + w.gmax);
+  int* rows_wanted = (int*)(ws + w.rows);
   const int chunks = chunks_of(V), groups = groups_of(V);
   const float c = invT * kLog2e;
   const int row_ctas = (n_rows + kFinishWarps - 1) / kFinishWarps;
@@ -565,7 +581,8 @@ cudaError_t launch(const void* Z, long long row_stride, const int32_t* tokens, i
   long long ctas = ((long long)n_rows * chunks + kRowWarps - 1) / kRowWarps;
   if (ctas > 152 * kRowCtas) ctas = 152 * kRowCtas;
   logprobs_stream_kernel<T><<<(int)ctas, kRowThreads, 0, s>>>(
-      (const T*)Z, row_stride, tokens, n_rows, V, chunks, groups, c, parts, gmax, (int*)ws);
+      (const T*)Z, row_stride, tokens, n_rows, V, chunks, groups, c, parts, gmax, rows_wanted, o,
+      (int*)ws);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -577,15 +594,18 @@ cudaError_t launch(const void* Z, long long row_stride, const int32_t* tokens, i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_finish_kernel<T>, (const T*)Z, row_stride, tokens, n_rows,
-                            V, chunks, groups, c, invT, (const float4*)parts, gmax, o);
+  return cudaLaunchKernelEx(&cfg, logprobs_finish_kernel<T>, (const T*)Z, row_stride, tokens, V,
+                            chunks, groups, c, invT, (const float4*)parts, gmax,
+                            (const int*)rows_wanted, o);
 }
 
 }  // namespace
 
 LogprobsWorkspace logprobs_workspace_layout(int n_rows, int V) {
   LogprobsWorkspace w;
-  w.parts = 256;
+  w.rows = 256;
+  // (read up to a whole CTA of the second kernel past the last row)
+  w.parts = align_up256(w.rows + ((size_t)n_rows + 1 + kFinishWarps) * sizeof(int));
   w.gmax = align_up256(w.parts + (size_t)n_rows * chunks_of(V) * sizeof(float4));
   w.total = align_up256(w.gmax + (size_t)n_rows * groups_of(V) * sizeof(float));
   return w;

@@ -73,7 +73,7 @@ cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const in
 
 // Token log-probabilities.
 struct LogprobsWorkspace {
-  size_t parts, gmax, total;
+  size_t rows, parts, gmax, total;
 };
 LogprobsWorkspace logprobs_workspace_layout(int n_rows, int V);
 cudaError_t launch_logprobs(const void* Z, int dtype, long long row_stride, const int32_t* tokens,
