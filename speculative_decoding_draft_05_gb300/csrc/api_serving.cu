@@ -27,8 +27,9 @@ int check_cache(const dspark_cache* c, int layer) {
     return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(c->dtype) - 1);
   if (((uintptr_t)c->k & a) || ((uintptr_t)c->v & a)) return DSPARK_ERR_INVALID_ARG;
-  if (c->head_dim > 256 || c->heads > 1024 || c->page_size > 65536)
-    return unsupported("head_dim <= 256, heads <= 1024, page_size <= 65536");
+  if (c->head_dim > 256 || c->heads > 1024 || c->page_size > 65536 ||
+      (long long)c->page_size * c->heads * c->head_dim > (1ll << 30))
+    return unsupported("head_dim <= 256, heads <= 1024, page_size <= 65536, 2^30 elements a page");
   return DSPARK_OK;
 }
 
@@ -79,7 +80,8 @@ int dspark_cache_append(const dspark_cache* cache, int layer, const void* k_new,
                         void* stream) {
   int st = check_cache(cache, layer);
   if (st != DSPARK_OK) return st;
-  if (!k_new || !v_new || !q_offsets || !kv_len || !page_table) return DSPARK_ERR_INVALID_ARG;
+  if (!q_offsets || !kv_len || !page_table) return DSPARK_ERR_INVALID_ARG;
+  if (n_tokens != 0 && (!k_new || !v_new)) return DSPARK_ERR_INVALID_ARG;
   if (n_tokens < 0 || new_token_stride < 0 || new_head_stride < 0) return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(cache->dtype) - 1);
   if (((uintptr_t)k_new & a) || ((uintptr_t)v_new & a)) return DSPARK_ERR_INVALID_ARG;
@@ -109,7 +111,8 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
                            size_t workspace_bytes, void* stream) {
   int st = check_cache(cache, layer);
   if (st != DSPARK_OK) return st;
-  if (!q || !q_offsets || !kv_len || !page_table || !out || !lse) return DSPARK_ERR_INVALID_ARG;
+  if (!q_offsets || !kv_len || !page_table) return DSPARK_ERR_INVALID_ARG;
+  if (n_tokens != 0 && (!q || !out || !lse)) return DSPARK_ERR_INVALID_ARG;
   if (n_tokens < 0 || q_token_stride < 0 || q_head_stride < 0) return DSPARK_ERR_INVALID_ARG;
   if (Hq <= 0 || Hq % cache->heads != 0 || !isfinite(scale)) return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(cache->dtype) - 1);
@@ -166,7 +169,7 @@ int dspark_pages_fork(const dspark_cache* cache, const int32_t* page_table, cons
                       int R, int max_pages, int32_t* page_table_out, int32_t* kv_len_out,
                       int32_t* refcount_out, int32_t* free_pages, void* workspace,
                       size_t workspace_bytes, void* stream) {
-  if (!cache || !free_pages || !parent || !child) return DSPARK_ERR_INVALID_ARG;
+  if (!cache || !free_pages || (n != 0 && (!parent || !child))) return DSPARK_ERR_INVALID_ARG;
   if (n < 0 || n > R) return DSPARK_ERR_INVALID_ARG;
   const PageMeta m{page_table, kv_len, refcount, page_table_out, kv_len_out, refcount_out,
                    R, max_pages, cache->n_pages, cache->page_size};
@@ -204,7 +207,7 @@ int dspark_pages_copy(const dspark_cache* cache, const int32_t* src, const int32
                       void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_cache(cache, 0);
   if (st != DSPARK_OK) return st;
-  if (!src || !dst || n < 0) return DSPARK_ERR_INVALID_ARG;
+  if (n < 0 || (n != 0 && (!src || !dst))) return DSPARK_ERR_INVALID_ARG;
   st = check_workspace(workspace, workspace_bytes, 256);
   if (st != DSPARK_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;

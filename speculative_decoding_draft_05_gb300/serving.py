@@ -69,6 +69,12 @@ def _dev(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
+def _count(t, name) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.numel()
+
+
 def _cache(cache):
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
@@ -158,7 +164,7 @@ def dspark_cache_append(cache: PagedCache, layer: int, k_new, v_new, q_offsets, 
     kl = _dev(kv_len, "kv_len", _I32, (R,), dev)
     ws, wp, wn = _workspace(256, workspace, dev, stream)
     st = load().dspark_cache_append(cache.ref, layer, kp, vp, ts, hs, off, kl, pt, R, T, P, wp, wn,
-                                    _stream(dev, stream)) if T else 0
+                                    _stream(dev, stream))
     if st:
         raise DSparkError("dspark_cache_append", st)
     return dict(workspace=ws)
@@ -178,7 +184,7 @@ def dspark_paged_attention(q, cache: PagedCache, layer: int, q_offsets, kv_len, 
     lse, lp = _out(lse, "lse", (T, Hq), _F32, dev, stream)
     ws, wp, wn = _workspace(paged_attention_workspace_bytes(cache), workspace, dev, stream)
     st = load().dspark_paged_attention(qp, ts, hs, Hq, cache.ref, layer, off, kl, pt, R, T, P, scale, op, lp, wp,
-                                       wn, _stream(dev, stream)) if T else 0
+                                       wn, _stream(dev, stream))
     if st:
         raise DSparkError("dspark_paged_attention", st)
     return dict(out=out, lse=lse, workspace=ws)
@@ -213,7 +219,7 @@ def dspark_pages_fork(cache: PagedCache, page_table, kv_len, parent, child, refc
     """Requests child[i] become copies of parent[i] (int32 [n]): full pages shared, the last one copied."""
     dev, n_pages = _cache(cache).device, cache.n_pages
     R, P, pt, kl, rc = _meta(cache, page_table, kv_len, refcount, dev)
-    n = parent.numel()
+    n = _count(parent, "parent")
     pa = _dev(parent, "parent", _I32, (n,), dev)
     ch = _dev(child, "child", _I32, (n,), dev)
     pto, ptp = _out(page_table_out, "page_table_out", (R, P), _I32, dev, stream)
@@ -247,11 +253,11 @@ def dspark_pages_compact(cache: PagedCache, page_table, kv_len, refcount, *, pag
 def dspark_pages_copy(cache: PagedCache, src, dst, *, workspace=None, stream=None) -> dict:
     """Copy pages src[i] -> dst[i] (int32 [n]) of K and V in all layers."""
     dev = _cache(cache).device
-    n = src.numel()
+    n = _count(src, "src")
     sp = _dev(src, "src", _I32, (n,), dev)
     dp = _dev(dst, "dst", _I32, (n,), dev)
     ws, wp, wn = _workspace(256, workspace, dev, stream)
-    st = load().dspark_pages_copy(cache.ref, sp, dp, n, wp, wn, _stream(dev, stream)) if n else 0
+    st = load().dspark_pages_copy(cache.ref, sp, dp, n, wp, wn, _stream(dev, stream))
     if st:
         raise DSparkError("dspark_pages_copy", st)
     return dict(workspace=ws)
@@ -282,6 +288,9 @@ def dspark_logprobs(Z, tokens, temperature: float = 1.0, top: int = 0, *, logp=N
     top_ids, p3 = _out(top_ids, "top_ids", (*lead, top), _I32, dev, stream)
     top_logp, p4 = _out(top_logp, "top_logp", (*lead, top), _F32, dev, stream)
     ws, wp, wn = _workspace(logprobs_workspace_bytes(n, V), workspace, dev, stream)
+    if not n:  # no rows: a clean status and nothing else
+        with torch.cuda.stream(stream):
+            ws.zero_()
     st = load().dspark_logprobs(Z.data_ptr(), _dtype_code(Z), step, tk, n, V, temperature, top, p0, p1, p2, p3, p4,
                                 wp, wn, _stream(dev, stream)) if n else 0
     if st:

@@ -102,6 +102,26 @@ def test_verify_layout_and_skipped_rows():
     r = run(Z, torch.full_like(tokens, -1).cuda(), 1.0, 3)  # nothing wanted
 
 
+@pytest.mark.parametrize("n,V", [(30000, 24), (13000, 264), (5000, 4096)])
+def test_many_rows(n, V):
+    Z = logits((n, V), BF16, seed=n)
+    tokens = torch.randint(0, V, (n,), generator=torch.Generator().manual_seed(n)).int()
+    keep = torch.zeros(n, dtype=torch.bool)
+    keep[::97] = True  # few, but everywhere
+    keep[4000:4100] = keep[-3:] = True
+    if n == 30000:
+        keep[12288:24576] = False
+    tokens[~keep] = -1
+    run(Z, tokens.cuda(), 1.0, 4)
+
+
+def test_no_rows():
+    Z = logits((2, 64), F32)[:0]
+    r = dspark.dspark_logprobs(Z, torch.empty(0, dtype=torch.int32, device="cuda"), 1.0, 3,
+                               workspace=torch.full((512,), 255, dtype=torch.uint8, device="cuda"))
+    assert dspark.dspark_read_device_status(r["workspace"]) == 0 and r["top_ids"].shape == (0, 3)
+
+
 def test_ties_go_to_the_lowest_id():
     V = 2048
     Z = torch.zeros(3, V, dtype=BF16, device="cuda")

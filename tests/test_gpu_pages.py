@@ -232,6 +232,41 @@ def test_many_requests_and_pages(R, n_pages):
     p.do_compact(in_place=True)
 
 
+def test_large_pages_and_large_tables():
+    # shared pages of 256 KB each: their copies get a launch of their own
+    p = Pool(70, 4, 220, 16, Hkv=8, D=128, layers=4)
+    p.do_resize([40] + [0] * 69)
+    p.do_fork([(0, b) for b in range(1, 70)])
+    p.do_resize([24] * 70)               # all end inside the shared second page
+    p.do_resize([25 + b % 9 for b in range(70)])
+    p.do_resize([0] * 35 + [40] * 35, in_place=True)
+    p.do_compact()
+    # 1.2 M table entries: copied into the outputs by a launch of their own
+    p = Pool(300, 4001, 2000, 1, Hkv=1, D=8, layers=1)
+    p.do_resize([r % 13 for r in range(300)])
+    p.do_fork([(1, 0), (12, 13), (11, 26)])
+    p.do_compact()
+
+
+def test_a_call_for_nothing_clears_the_status():
+    p = Pool(3, 4, 16, 4)
+    p.do_resize([5, 0, 3])
+    t, n, c = p.dev()
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    r = dspark.dspark_pages_fork(p.cache, t, n, none, none, c, workspace=ws.clone())
+    p.check(r, p.fork([]))
+    r = dspark.dspark_pages_copy(p.cache, none, none, workspace=ws.clone())
+    assert dspark.dspark_read_device_status(r["workspace"]) == 0
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    kv = torch.empty(0, 2, 8, dtype=BF16, device="cuda")
+    r = dspark.dspark_cache_append(p.cache, 0, kv, kv, off, n, t, workspace=ws.clone())
+    assert dspark.dspark_read_device_status(r["workspace"]) == 0
+    big = torch.full((dspark.paged_attention_workspace_bytes(p.cache),), 255, dtype=torch.uint8, device="cuda")
+    r = dspark.dspark_paged_attention(kv, p.cache, 0, off, n, t, 1.0, workspace=big)
+    assert dspark.dspark_read_device_status(r["workspace"]) == 0 and r["out"].shape == (0, 2, 8)
+
+
 def test_bad_device_inputs_are_flagged():
     p = Pool(4, 4, 16, 4)
     p.do_resize([9, 5, 0, 0])

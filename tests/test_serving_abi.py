@@ -25,7 +25,7 @@ def cache(**kw):
 BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(dtype=3), 1), (dict(layers=0), 1), (dict(n_pages=0), 1),
               (dict(page_size=0), 1), (dict(heads=0), 1), (dict(head_dim=0), 1), (dict(page_stride=0), 1),
               (dict(token_stride=-1), 1), (dict(head_stride=0), 1), (dict(k=257), 1), (dict(head_dim=264), 2),
-              (dict(heads=1025), 2), (dict(page_size=65537), 2)]
+              (dict(heads=1025), 2), (dict(page_size=65537), 2), (dict(page_size=65536, heads=1024, head_dim=64), 2)]
 WS = 1 << 30
 
 
