@@ -131,6 +131,35 @@ def test_ties_go_to_the_lowest_id():
     run(Z, torch.tensor([3, 0, 1501], dtype=torch.int32, device="cuda"), 1.0, 32)
 
 
+@pytest.mark.parametrize("V", [16384, 40000, 262144])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_alternatives_of_long_rows(V, dtype):
+    Z = logits((9, V), dtype, seed=V)
+    Z[0] = 0.0                              # all tie
+    Z[1, : V // 2] = -math.inf              # the frequent half masked
+    Z[2] = -math.inf                        # fewer left than wanted
+    Z[2, [5, V - 1, V // 3]] = 1.0
+    Z[3] = Z[3].flip(0)                     # the best ids at the end
+    Z[4] = 1.0                              # a few above many that tie
+    Z[4, 7::997] = 2.0
+    Z[5] = torch.finfo(dtype).min
+    Z[5, V // 2 : V // 2 + 40] = 0.5
+    Z[6, ::5] = math.nan
+    Z[7, 1000] = math.inf
+    tok = torch.tensor([3, V - 2, 5, V - 1, 7, V // 2, 1, 2, 0], dtype=torch.int32, device="cuda")
+    for top in (1, 13, 32):
+        r = dspark.dspark_logprobs(Z, tok, 1.0, top)
+        w = reference(Z, tok, 1.0, top)
+        assert torch.equal(r["top_ids"].cpu().long(), w["ids"])
+        fine = [0, 1, 2, 3, 4, 8]
+        tol = 200 * U + 4 * U * float(Z[fine].float()[Z[fine].isfinite()].abs().max())
+        for name, key in (("lse", "lse"), ("logp", "logp"), ("top_logp", "top")):
+            close(r[name][fine], w[key][fine], tol, name)
+        close(r["lse"][5:6], w["lse"][5:6], tol, "lse over lowest values")
+        close(r["entropy"][:6], w["entropy"][:6], 400 * U * (1 + math.log(V)), "entropy")
+        assert r["lse"][6:8].isnan().all() and r["lse"][8].isfinite()
+
+
 def test_masked_ids():
     V = 1024
     for dtype in (F32, BF16):
