@@ -5,8 +5,8 @@
 // tile of 128 keys: S = Q K^T (128 x 128 x D), the online softmax
 //   m' = max(m, max_j s_j),  p_j = 2^{s_j - m'},  l' = l 2^{m-m'} + sum_j p_j,
 //   O' = O 2^{m-m'} + P V
-// in units of log2, with S and O in TMEM and P (bf16) written over half of S in TMEM as
-// the first operand of P V.  out = O / l is the same whatever reference m the
+// in units of log2, with S and O in TMEM and P (bf16) written over the lower half of
+// S in TMEM as the first operand of P V.  out = O / l is the same whatever reference m the
 // two share, and floating-point rounding does not depend on it either, as long
 // as nothing leaves the exponent range.  So m starts at 0 and stays until a
 // row's maximum lies more than 60 above it (or, in a piece's first tile, below):
@@ -29,7 +29,8 @@
 //   * warps 0..3 and 4..7: two softmax streams, one row a thread.  With two row
 //     blocks the streams are the blocks and share each K/V tile; with one they
 //     are alternate tiles of the same rows.  While one stream is in its softmax
-//     the tensor cores run the other's products.
+//     the tensor cores run the other's products, and the product of P's first 64
+//     keys begins while the rest of P is in the making.
 //   * warps 12..15 (results): merge a piece's streams, scale and write it, while
 //     the softmax warps are at the next piece.
 //   * Keys at or past an item's end: pages past it are not loaded, S is
@@ -75,7 +76,7 @@ struct Layout {
   static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
   static constexpr int kOffStart = kOffMerge;                        // (before the first merge)
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
-  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1;
   static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 12 + 15) & ~15);  // PieceInfo [2]
   static constexpr int kEnd = kOffPiece + 2 * 64;
   // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
@@ -363,7 +364,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* ml_full = o_full + 2;  // piece n's (m, l) written (8 softmax warps)
   uint64_t* ml_empty = ml_full + 1;  // and read (4 result warps)
   uint64_t* o_free = ml_empty + 1;   // [2] a stream's O of piece n read (4 result warps)
-  uint64_t* drain = o_free + 2;
+  uint64_t* h_full = o_free + 2;   // [2] P's first 64 keys written (4 warps)
+  uint64_t* h_done = h_full + 2;   // [2] and their product done
+  uint64_t* drain = h_done + 2;
   uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   int* flags = (int*)(tmem_slot + 2);  // the CTA's status bits
@@ -385,6 +388,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&h_full[i], 4);
+      mbar_init(&h_done[i], 1);
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 13);
       mbar_init(&o_full[i], 1);
@@ -521,17 +526,27 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         tc_commit(&s_full[s], lead);
       };
-      auto pv = [&](int s, uint32_t sl, bool first) {  // O_s (+)= P_s V
+      // O_s (+)= P_s V, the first 64 keys while the rest of P is in the making.
+      auto pv = [&](int s, uint32_t sl, bool first) {
         const uint64_t vt = v_desc + (sl % Lo::kStages) * (Lo::kTileBytes >> 4);
+        const uint32_t o = tmem + 256 + s * 128, pt = tmem + s * 128;
 #pragma unroll
-        for (int kk = 0; kk < kTN / 16; ++kk)
-          mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 + kk * 8, vt + kk * (2048 >> 4), id_o,
-                 !(first && kk == 0), lead);
-      };
-      auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages], lead); };
-      auto wait_p = [&](int s) {
+        for (int kk = 0; kk < kTN / 32; ++kk)
+          mma_ts(o, pt + kk * 8, vt + kk * (2048 >> 4), id_o, !(first && kk == 0), lead);
+        tc_commit(&h_done[s], lead);
         uint32_t& k = s ? steps1 : steps0;
         const bool r = __all_sync(0xffffffffu, mbar_wait(&p_full[s], k++ & 1u, abort_flag, tp.wait_budget));
+        tc_fence_after();
+        if (!r) return false;
+#pragma unroll
+        for (int kk = kTN / 32; kk < kTN / 16; ++kk)
+          mma_ts(o, pt + kk * 8, vt + kk * (2048 >> 4), id_o, 1u, lead);
+        return true;
+      };
+      auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages], lead); };
+      auto wait_half = [&](int s) {
+        const uint32_t k = s ? steps1 : steps0;
+        const bool r = __all_sync(0xffffffffu, mbar_wait(&h_full[s], k & 1u, abort_flag, tp.wait_budget));
         tc_fence_after();
         return r;
       };
@@ -555,14 +570,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           for (int j = 0; j < nt; ++j) {
             const uint32_t vs = slot + 1, ks = slot + 2;
             const bool more = j + 1 < nt;
-            if (!(ok = wait_full(vs) && wait_p(0) && (j > 0 || wait_o_free(0, n)))) break;
-            pv(0, vs, j == 0);
+            if (!(ok = wait_full(vs) && wait_half(0) && (j > 0 || wait_o_free(0, n)))) break;
+            if (!(ok = pv(0, vs, j == 0))) break;
             if (more) {
               if (!(ok = wait_full(ks))) break;
               qk(0, 0, ks);
             }
-            if (!(ok = wait_p(1) && (j > 0 || wait_o_free(1, n)))) break;
-            pv(1, vs, j == 0);
+            if (!(ok = wait_half(1) && (j > 0 || wait_o_free(1, n)))) break;
+            if (!(ok = pv(1, vs, j == 0))) break;
             release(vs);
             if (more) {
               qk(1, 1, ks);
@@ -605,10 +620,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           if (ok) issue_qk();
           for (uint32_t i = 0; i < iq && ok; ++i) {
             const int s = i & 1;
-            if (!(ok = wait_full(slot) && wait_p(s))) break;
+            if (!(ok = wait_full(slot) && wait_half(s))) break;
             const uint32_t f = s ? flags1 : flags0;
             if (f & 1u && !(ok = wait_o_free(s, np))) break;
-            pv(s, slot, f & 1u);
+            if (!(ok = pv(s, slot, f & 1u))) break;
             release(slot++);
             if (f & 2u) tc_commit(&o_full[np++ & 1], lead);
             if (open) issue_qk();
@@ -654,13 +669,17 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         ++steps;
         if (!ok) break;
         tc_fence_after();
+        bool early = false;  // P's first half is handed over
         if (warp_live) {
           const int vis = lim - k0;  // keys of the tile that the row sees
           const bool masked = __any_sync(0xffffffffu, vis < kTN);
           // One pass: probabilities against the reference in use, and this tile's
           // maximum beside them.  They stand unless a row's maximum is out of range.
+          // A tile without a mask hands over its first 64 keys on the way; if a
+          // row's maximum turns out to lie out of range after that, their product
+          // is waited for and O rescaled.  Returns whether P stands.
           auto one_pass = [&](auto with_mask) {
-            uint32_t pk[64], xa[32], xb[32];
+            uint32_t pk[32], xa[32], xb[32];
             const f32x2 sc2 = pack2(p.scale_log2, p.scale_log2), ms2 = pack2(-m, -m);
             f32x2 sum2[2] = {0ull, 0ull};
             float mx = -INFINITY;
@@ -680,6 +699,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 out[i] = pack_bf16(e0, e1);
               }
             };
+            auto add_sums = [&](f32x2 sums) {
+              float s0, s1;
+              unpack2(sums, s0, s1);
+              l += s0 + s1;
+            };
             tmem_ld32(tS, xa);
             tmem_wait_ld32(xa);
             tmem_ld32(tS + 32, xb);
@@ -687,81 +711,102 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             tmem_wait_ld32(xb);
             tmem_ld32(tS + 64, xa);
             chunk(xb, pk + 16, 32);
+            if (with_mask) {
+              uint32_t pk2[32];
+              tmem_wait_ld32(xa);
+              tmem_ld32(tS + 96, xb);
+              chunk(xa, pk2, 64);
+              tmem_wait_ld32(xb);
+              chunk(xb, pk2 + 16, 96);
+              if (__any_sync(0xffffffffu, live && out_of_range(mx * p.scale_log2, m, first))) return false;
+              tmem_st32(tS, pk);
+              tmem_st32(tS + 32, pk2);
+              add_sums(add2(sum2[0], sum2[1]));
+              return true;
+            }
+            const f32x2 half_sum = add2(sum2[0], sum2[1]);
+            sum2[0] = sum2[1] = 0ull;
+            const bool bad = __any_sync(0xffffffffu, live && out_of_range(mx * p.scale_log2, m, first));
             tmem_wait_ld32(xa);
+            if (bad) return false;
+            tmem_st32(tS, pk);
             tmem_ld32(tS + 96, xb);
-            chunk(xa, pk + 32, 64);
+            chunk(xa, pk, 64);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&h_full[s]);
+            early = true;
             tmem_wait_ld32(xb);
-            chunk(xb, pk + 48, 96);
+            chunk(xb, pk + 16, 96);
             mx *= p.scale_log2;
-            if (__any_sync(0xffffffffu, live && out_of_range(mx, m, first))) return false;
-            tmem_st32(tS + 64, pk);
-            tmem_st32(tS + 96, pk + 32);
-            float s0, s1;
-            unpack2(add2(sum2[0], sum2[1]), s0, s1);
-            l += s0 + s1;
+            if (__any_sync(0xffffffffu, live && out_of_range(mx, m, false))) {
+              add_sums(half_sum);
+              return false;
+            }
+            tmem_st32(tS + 32, pk);
+            add_sums(add2(half_sum, add2(sum2[0], sum2[1])));
             return true;
           };
           const bool done = masked ? one_pass(std::true_type{}) : one_pass(std::false_type{});
           if (!done) {
-            // Two passes over S: the maximum, columns 0..63 then 64..127; then the
-            // probabilities, 64..127 from registers and 0..63 read again (all 128
-            // columns in registers would spill).  P goes to columns 64..127.
-            uint32_t x[64];
+            // Two passes over S: the maximum, then the probabilities.  After a first
+            // half that stands only the second is left (its part of S is intact).
+            const int from = early ? 64 : 0;
+            if (early) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&h_done[s], (steps - 1) & 1u, abort_flag,
+                                                     tp.wait_budget));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            uint32_t x[32];
             float mx = -INFINITY;
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              tmem_ld32(tS + 64 * hh, x);
-              tmem_ld32(tS + 64 * hh + 32, x + 32);
+#pragma unroll 1
+            for (int k = from; k < kTN; k += 32) {
+              tmem_ld32(tS + k, x);
               tmem_wait_ld32(x);
-              tmem_wait_ld32(x + 32);
-              if (masked) mask_from<64>(x, vis - 64 * hh);
+              if (masked) mask_from<32>(x, vis - k);
 #pragma unroll
-              for (int k = 0; k < 64; k += 2)
-                mx = fmax3(mx, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+              for (int i = 0; i < 32; i += 2)
+                mx = fmax3(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
             }
             mx *= p.scale_log2;
-            const bool grow = live && out_of_range(mx, m, first);
+            const bool fresh = first && !early;  // nothing is summed yet
+            const bool grow = live && out_of_range(mx, m, fresh);
             if (__any_sync(0xffffffffu, grow)) {
               const float mn = grow ? mx : m;
-              const float f = grow && !first ? ex2(m - mn) : 1.0f;  // (first: nothing is summed yet)
-              if (!first) {
+              const float f = grow && !fresh ? ex2(m - mn) : 1.0f;
+              if (!fresh) {
 #pragma unroll
                 for (int k = 0; k < DP; k += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(tO + s * 128 + k, o);
-                  tmem_wait_ld32(o);
+                  tmem_ld32(tO + s * 128 + k, x);
+                  tmem_wait_ld32(x);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  tmem_st32(tO + s * 128 + k, o);
+                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                  tmem_st32(tO + s * 128 + k, x);
                 }
               }
               l *= f;
               m = mn;
             }
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            auto probs = [&](const uint32_t* v, int k) {  // 32 columns -> P's columns k ..
+            // (P's columns k / 2 .. lie over scores that are read by then)
+#pragma unroll 1
+            for (int k = from; k < kTN; k += 32) {
               uint32_t pk[16];
+              float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              tmem_ld32(tS + k, x);
+              tmem_wait_ld32(x);
+              if (masked) mask_from<32>(x, vis - k);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), p.scale_log2, -m));
-                const float e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), p.scale_log2, -m));
+                const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), p.scale_log2, -m));
+                const float e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), p.scale_log2, -m));
                 sum[i & 3] += e0 + e1;
                 pk[i] = pack_bf16(e0, e1);
               }
-              tmem_st16(tS + 64 + k, pk);
-            };
-            uint32_t y[32];
-            tmem_ld32(tS, y);
-            probs(x, 32);
-            probs(x + 32, 48);
-            tmem_wait_ld32(y);
-            tmem_ld32(tS + 32, x);
-            if (masked) mask_from<32>(y, vis);
-            probs(y, 0);
-            tmem_wait_ld32(x);
-            if (masked) mask_from<32>(x, vis - 32);
-            probs(x, 16);
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+              tmem_st16(tS + k / 2, pk);
+              l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            }
           }
           first = false;
           tmem_wait_st();
@@ -784,7 +829,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           fence_proxy_async();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[s]);
+        if (lane == 0) {
+          if (!early) mbar_arrive(&h_full[s]);
+          mbar_arrive(&p_full[s]);
+        }
       }
       if (!ok) break;
       // (m, l) to the result warps, once they have read the piece before's.

@@ -196,6 +196,22 @@ def test_rows_that_fall_and_rise():
         check(i, attend(i))
 
 
+@pytest.mark.parametrize("chunks", [[3], [70]], ids=["few", "many"])
+@pytest.mark.parametrize("rise", [[64], [100, 230], [64, 192, 320, 448], [192, 193, 700]])
+def test_a_maximum_that_rises_inside_a_tile(rise, chunks):
+    # the level goes up by 50 (72 in units of log2) at each of these positions
+    for dtype in (F32, BF16):
+        i = make(dtype, chunks, [1100], 8, 2, 128, 16, seed=24)
+        pages = i["table"][0, :69].long()
+        pos = torch.arange(69 * 16)
+        lev = sum(((pos >= x).float() * 50.0 for x in rise), -20.0 + 0 * pos)
+        i["qkv"][:, :, 0] = 16.0
+        k = i["k"][0][pages]
+        k[..., 0] = (lev * math.sqrt(128) / 16.0).view(69, 16, 1).to(dtype).cuda()
+        i["k"][0][pages] = k
+        check(i, attend(i))
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1.0])
 def test_scales(scale):
     for dtype in (F32, BF16):
