@@ -173,7 +173,9 @@ attention_simt_kernel(const AttnParams p) {
 }
 
 // Adds the pieces of the items that shares cut.  Block (b, y): the item that
-// CTA b + 1's share is the first to begin inside of; a warp takes one of its rows.
+// CTA b + 1's share is the first to begin inside of; its warps take the rows in
+// turn.  (As many blocks as the likely rows fill: for decoding, with a few rows
+// an item, blocks without a row cost more than they save others.)
 template <typename T, int NI>
 __global__ void __launch_bounds__(256)
 attention_combine_kernel(const AttnParams p, int MR, int ctas) {
@@ -189,48 +191,49 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
   if (c >= ctas) return;
   const CutItem it = p.cuts[c];
   const int n = it.pieces;
-  const int a = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (n == 0 || a >= it.rows) return;
+  if (n == 0) return;
   const int lane = threadIdx.x & 31, D = p.a.c.head_dim, G = p.a.G;
-  const auto at = [&](int i) {
-    return (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
-  };
-  // The weights of 32 pieces at a time, one a lane; columns lane + 32 k.
-  float m = -INFINITY, l = 0.0f;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[at(i)].x);
-  m = warp_max(m);
-  const float ms = m == -INFINITY ? 0.0f : m;
-  float o[NI] = {};
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float f = 0.0f, lf = 0.0f;
-    if (i0 + lane < n) {
-      const float2 st = p.stats[at(i0 + lane)];
-      f = exp2f(st.x - ms);
-      lf = st.y * f;
-    }
-    l += warp_sum(lf);
-    const int k1 = n - i0 < 32 ? n - i0 : 32;
+  for (int a = blockIdx.y * 8 + (threadIdx.x >> 5); a < it.rows; a += gridDim.y * 8) {
+    const auto at = [&](int i) {
+      return (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
+    };
+    // The weights of 32 pieces at a time, one a lane; columns lane + 32 k.
+    float m = -INFINITY, l = 0.0f;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[at(i)].x);
+    m = warp_max(m);
+    const float ms = m == -INFINITY ? 0.0f : m;
+    float o[NI] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float f = 0.0f, lf = 0.0f;
+      if (i0 + lane < n) {
+        const float2 st = p.stats[at(i0 + lane)];
+        f = exp2f(st.x - ms);
+        lf = st.y * f;
+      }
+      l += warp_sum(lf);
+      const int k1 = n - i0 < 32 ? n - i0 : 32;
 #pragma unroll 8
-    for (int i = 0; i < k1; ++i) {
-      const float w = __shfl_sync(0xffffffffu, f, i);
-      const float* part = p.part + at(i0 + i) * D;
+      for (int i = 0; i < k1; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        const float* part = p.part + at(i0 + i) * D;
 #pragma unroll
-      for (int k = 0; k < NI; ++k)
-        if (lane + 32 * k < D) o[k] = fmaf(part[lane + 32 * k], w, o[k]);
+        for (int k = 0; k < NI; ++k)
+          if (lane + 32 * k < D) o[k] = fmaf(part[lane + 32 * k], w, o[k]);
+      }
     }
+    const int row = it.row0 + a, tok = row / G, g = row - tok * G;
+    const size_t dst = (size_t)(it.q0 + tok) * p.a.Hq + it.h * G + g;
+    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+#pragma unroll
+    for (int k = 0; k < NI; ++k)
+      if (lane + 32 * k < D) {
+        if (std::is_same<T, float>::value)
+          ((float*)p.a.out)[dst * D + lane + 32 * k] = o[k] * inv;
+        else
+          ((__nv_bfloat16*)p.a.out)[dst * D + lane + 32 * k] = __float2bfloat16(o[k] * inv);
+      }
+    if (lane == 0) p.a.lse[dst] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
   }
-  const int row = it.row0 + a, tok = row / G, g = row - tok * G;
-  const size_t dst = (size_t)(it.q0 + tok) * p.a.Hq + it.h * G + g;
-  const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-#pragma unroll
-  for (int k = 0; k < NI; ++k)
-    if (lane + 32 * k < D) {
-      if (std::is_same<T, float>::value)
-        ((float*)p.a.out)[dst * D + lane + 32 * k] = o[k] * inv;
-      else
-        ((__nv_bfloat16*)p.a.out)[dst * D + lane + 32 * k] = __float2bfloat16(o[k] * inv);
-    }
-  if (lane == 0) p.a.lse[dst] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 constexpr int kSimtCtas = 304;
@@ -258,7 +261,7 @@ cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
 
 cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const long long rows = (long long)p.a.a.n_tokens * p.a.G;  // of an item, at most
+  const long long rows = attn_likely_rows(p.a);
   cfg.gridDim = dim3(ctas > 1 ? ctas - 1 : 1, (unsigned)((rows < MR ? rows : MR) + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
@@ -288,7 +291,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) 
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f,
-               kMR};
+               attn_item_units(a), kMR};
   const cudaError_t e = a.dtype == DSPARK_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(p, kMR, kSimtCtas, s);

@@ -5,7 +5,7 @@
 // A row is (token, query head of the group): row = token * G + g, so all G
 // query heads that share a K/V head read its tiles once.  An item walks its
 // keys in tiles of TN; its work is counted as one unit a tile (an item without
-// keys has one) and kAttnItemUnits more for its start and end.  The units of
+// keys has one) and `item_units` more for its start and end.  The units of
 // all items, in the order request, row block, head, tile, are cut into equal
 // contiguous shares, one a CTA: short and long requests, many rows and few,
 // all load every SM alike.  An item cut by a share's end leaves partial results
@@ -20,11 +20,19 @@ namespace dspark {
 
 constexpr int kAttnMaxCtas = 320;  // CTAs of one attention launch, at most
 
-// Units that an item counts beyond its tiles: its start and end (Q, merging the
-// streams, writing the result) cost a CTA about as much as two tiles.  Measured
-// with 64 requests of 500 .. 8192 positions (verify chunks, 8 K/V heads): the
-// CTAs' times spread over 165 .. 244 us without it, around 190 us with it.
-constexpr int kAttnItemUnits = 2;
+// Rows of most requests for a K/V head, as far as the host can tell: twice the mean.
+inline long long attn_likely_rows(const AttnArgs& a) {
+  const long long all = (long long)a.a.n_tokens * a.G, twice = 2 * all / a.a.R;
+  return twice < 1 ? 1 : twice < all ? twice : all;
+}
+
+// Units that an item counts beyond its tiles, for its start and end (Q, merging
+// the streams, writing the result): three for long chunks, whose items are 256
+// rows, else one.  Measured (us) at 0, 1, 2, 3 units:
+//   decoding, 16 requests of 200 .. 2048 positions      32.6   32.3  33.9  34.8
+//   verifying, 128 requests of 100 .. 600 positions     88.9   81.7  80.4  82.0
+//   prefill, 2 requests of 2901 .. 4096 tokens           438    436   433   430
+inline int attn_item_units(const AttnArgs& a) { return attn_likely_rows(a) > 256 ? 3 : 1; }
 
 // A cut item, written by the first CTA whose share begins inside it.
 struct CutItem {
@@ -57,6 +65,7 @@ struct AttnParams {
   float2* stats;     // [grid][2][MR] (m, l), m in log2 units
   float* part;       // [grid][2][MR][D]
   float scale_log2;  // scale * log2(e)
+  int item_units;    // units of an item beyond its tiles
   int mr;            // rows of an item, at most (partial results are MR >= mr rows apart)
 };
 
@@ -117,14 +126,15 @@ struct AttnWalk {
   int end, n_tiles;  // its keys and tiles
   int pos;           // the piece's first unit within the item
   int left;          // units of the share from there on
+  int extra;         // item_units
 
   __device__ __forceinline__ bool done() const { return left <= 0; }
-  // (the item's first kAttnItemUnits units stand for no tile)
+  // (the item's first item_units units stand for no tile)
   __device__ __forceinline__ int first_tile() const {
-    return pos > kAttnItemUnits ? pos - kAttnItemUnits : 0;
+    return pos > extra ? pos - extra : 0;
   }
   __device__ __forceinline__ int last_tile() const {  // one past the piece's last tile
-    const int e = pos + left - kAttnItemUnits;
+    const int e = pos + left - extra;
     return e < n_tiles ? e : n_tiles;
   }
   // A share that ends before the item's first tile has nothing of it.
@@ -138,7 +148,7 @@ struct AttnWalk {
 
   // flags: the CTA's status bits.
   __device__ __forceinline__ void next(const AttnParams& p, int* flags) {
-    left -= n_tiles + kAttnItemUnits - pos;
+    left -= n_tiles + extra - pos;
     if (done()) return;
     pos = 0;
     if (++h >= p.a.c.heads) {
@@ -188,14 +198,14 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
       if (r < R) q = attn_request(p.a.a, p.a.c.page_size, r, flags);
     }
     const int blocks = attn_blocks(q, G, p.mr);
-    long long u = blocks == 1 ? attn_tiles<TN>(q.L) + kAttnItemUnits : 0;
+    long long u = blocks == 1 ? attn_tiles<TN>(q.L) + p.item_units : 0;
     for (unsigned todo = __ballot_sync(0xffffffffu, blocks > 1); todo; todo &= todo - 1) {
       const int src = __ffs(todo) - 1;
       const AttnRequest w{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.L, src)};
       const int nb = __shfl_sync(0xffffffffu, blocks, src);
       long long sum = 0;
       for (int m = lane; m < nb; m += 32)
-        sum += attn_tiles<TN>(attn_item_end(w, G, p.mr, m)) + kAttnItemUnits;
+        sum += attn_tiles<TN>(attn_item_end(w, G, p.mr, m)) + p.item_units;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == src) u = sum;
@@ -251,7 +261,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
             w.m = m0 + lane;
             w.end = attn_item_end(w.q, G, p.mr, w.m);
             w.n_tiles = attn_tiles<TN>(w.end);
-            const int item = w.n_tiles + kAttnItemUnits;
+            const int item = w.n_tiles + p.item_units;
             const long long own = w.m < blocks ? (long long)item * Hkv : 0;
             long long upto = own;
 #pragma unroll
@@ -265,9 +275,10 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart<TN>* st
               w.h = d >> 31 ? (int)(d / item) : (int)d / item;
               w.pos = (int)(d - (long long)w.h * item);
               w.left = left;
+              w.extra = p.item_units;
               w.drop_empty();
               st->walk = w;
-              st->u0 = first + (long long)w.h * item + kAttnItemUnits;
+              st->u0 = first + (long long)w.h * item + p.item_units;
             }
             base += __shfl_sync(0xffffffffu, upto, 31);
           }

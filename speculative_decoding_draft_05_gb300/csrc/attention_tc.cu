@@ -1155,7 +1155,8 @@ cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),
                     // (not 0: a masked score is -inf times this)
-                    fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f), kMR};
+                    fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f),
+                    attn_item_units(a), kMR};
   tp.sign = a.scale < 0 ? -1.0f : 1.0f;
   tp.box_tokens = a.c.page_size < kTN ? a.c.page_size : kTN;
   tp.q_tokens = a.G <= 128 ? 128 / a.G : 1;
