@@ -715,6 +715,47 @@ __device__ __forceinline__ int find_request(const int32_t* off, int R, int t) {
   return lo;
 }
 
+// Whether any new token has no place in the cache, by one CTA, request by
+// request (a request a thread, its further pages by the warp): the status word, which so needs no clearing before the launch (a
+// launch of its own cost 2 of 12 us for 512 requests).
+__device__ __forceinline__ void append_status(const AppendArgs& p) {
+  const int lane = threadIdx.x & 31, S = p.c.page_size;
+  bool bad = false;
+  const auto check = [&](int r, long long j) {
+    const int page = p.a.page_table[(size_t)r * p.a.max_pages + j];
+    bad |= page < 0 || page >= p.c.n_pages;
+  };
+  for (int r0 = 0; r0 < p.a.R; r0 += blockDim.x) {  // a request a thread
+    const int r = r0 + (int)threadIdx.x;
+    long long s0 = 0, s1 = -1;  // the pages that its tokens go to
+    if (r < p.a.R) {
+      const int b = p.a.q_offsets[r], e = p.a.q_offsets[r + 1], L = p.a.kv_len[r];
+      bad |= b > e || (r == 0 && b != 0);
+      const int t0 = b < 0 ? 0 : b, t1 = e < p.a.n_tokens ? e : p.a.n_tokens;
+      if (t0 < t1) {
+        const long long base = (long long)L - e;  // a token's position less its number
+        bad |= base + t0 < 0;
+        s0 = base + t0 < 0 ? 0 : (base + t0) / S;
+        s1 = base + t1 - 1 < 0 ? -1 : (base + t1 - 1) / S;
+        bad |= s1 >= p.a.max_pages;
+        s1 = s1 < p.a.max_pages ? s1 : p.a.max_pages - 1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (s0 + k <= s1) check(r, s0 + k);
+    for (unsigned more = __ballot_sync(0xffffffffu, s0 + 2 <= s1); more; more &= more - 1) {
+      const int src = __ffs(more) - 1;
+      const long long j0 = __shfl_sync(0xffffffffu, s0, src) + 2, j1 = __shfl_sync(0xffffffffu, s1, src);
+      const int row = __shfl_sync(0xffffffffu, r, src);
+#pragma unroll 4
+      for (long long j = j0 + lane; j <= j1; j += 32) check(row, j);
+    }
+  }
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *p.status = any ? DSPARK_DEV_BAD_INPUT : 0;
+}
+
 // One warp a token: VE elements (16 bytes, or one where alignment does not
 // allow) a lane and step.  The first kAppendAhead steps' rows are loaded before
 // the token's request, position and page are looked up (four dependent loads).
@@ -727,7 +768,11 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
   const int lane = threadIdx.x & 31;
   const int S = p.c.page_size;
   const int per_head = p.c.head_dim / VE, n = p.c.heads * per_head;
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.a.n_tokens; t += gridDim.x * 8) {
+  if (blockIdx.x == 0) {
+    append_status(p);
+    return;
+  }
+  for (int t = (blockIdx.x - 1) * 8 + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * 8) {
     const E* kn = (const E*)p.k_new + t * p.tok_stride;
     const E* vn = (const E*)p.v_new + t * p.tok_stride;
     Vec kx[kAppendAhead], vx[kAppendAhead];
@@ -747,11 +792,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
     int page = -1;
     if (t >= p.a.q_offsets[r] && t < end && pos >= 0 && slot < p.a.max_pages)
       page = p.a.page_table[(size_t)r * p.a.max_pages + slot];
-    if (page < 0 || page >= p.c.n_pages) {
-      // (rows past the last request's are padding, not an error)
-      if (lane == 0 && t < p.a.q_offsets[p.a.R]) flag_status(p.status, DSPARK_DEV_BAD_INPUT);
-      continue;
-    }
+    if (page < 0 || page >= p.c.n_pages) continue;  // flagged by CTA 0, or padding
     const long long dst0 = page * p.c.page_stride + (pos - slot * S) * p.c.token_stride;
 #pragma unroll
     for (int k = 0; k < kAppendAhead; ++k) {
@@ -893,8 +934,7 @@ cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const in
 cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new, const void* v_new,
                                 long long new_token_stride, long long new_head_stride,
                                 const ChunkArgs& a, int* status, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), s);
-  if (e != cudaSuccess || a.n_tokens == 0) return e;
+  if (a.n_tokens == 0) return cudaMemsetAsync(status, 0, sizeof(int), s);
   AppendArgs p{c, a, k_new, v_new, new_token_stride, new_head_stride, status};
   const int ve = 16 / esize;
   const bool vec = c.head_dim % ve == 0 && c.page_stride % ve == 0 && c.token_stride % ve == 0 &&
@@ -902,7 +942,7 @@ cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new
                    new_head_stride % ve == 0 &&
                    (((uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)k_new | (uintptr_t)v_new) & 15u) == 0;
   int ctas = (a.n_tokens + 7) / 8;
-  if (ctas > 1216) ctas = 1216;
+  ctas = (ctas < 1215 ? ctas : 1215) + 1;  // (the first one for the status word)
   if (esize == 2) {
     if (vec)
       cache_append_kernel<uint16_t, 8><<<ctas, 256, 0, s>>>(p);

@@ -333,6 +333,31 @@ def test_append_leaves_out_what_is_out_of_range():
     assert torch.equal(i["k"], k0)
 
 
+@pytest.mark.parametrize("chunks,lens", [([2] * 600, [(5 * r) % 40 + 2 for r in range(600)]), ([700, 3, 650], [700, 9, 700])])
+def test_append_flags_any_page_out_of_range(chunks, lens):
+    i = make(BF16, chunks, lens, 2, 2, 64, 16, seed=25, poison=False)
+    cache = dspark.PagedCache(i["k"], i["v"])
+    kn, vn = i["qkv"][:, 2:4], i["qkv"][:, 4:]
+
+    def status(table):
+        return dspark.dspark_read_device_status(
+            dspark.dspark_cache_append(cache, 0, kn, vn, i["off"], i["lens"], table)["workspace"])
+
+    assert status(i["table"]) == 0
+    R = len(lens)
+    for r in (0, R // 2, R - 1):
+        first, last = (lens[r] - chunks[r]) // 16, (lens[r] - 1) // 16
+        for j in {first, (first + last) // 2, last}:
+            for bad in (-1, i["k"].shape[1]):
+                t = i["table"].clone()
+                t[r, j] = bad
+                assert status(t) == 1, (r, j)
+        t = i["table"].clone()
+        t[r, last + 1:] = 1 << 30  # pages that no token goes to
+        t[r, :first] = -5
+        assert status(t) == 0, r
+
+
 def test_append_of_unaligned_rows():
     # rows that start one element off a 16-byte boundary, and a pool that does
     for dtype in (F32, BF16):
