@@ -29,13 +29,22 @@
 //   * warps 0..3 and 4..7: two softmax streams, one row a thread.  With two row
 //     blocks the streams are the blocks and share each K/V tile; with one they
 //     are alternate tiles of the same rows.  While one stream is in its softmax
-//     the tensor cores run the other's products, and the product of P's first 64
+//     the tensor cores run the other's products, and the product of P's first 96
 //     keys begins while the rest of P is in the making.
 //   * warps 12..15 (results): merge a piece's streams, scale and write it, while
 //     the softmax warps are at the next piece.
 //   * Keys at or past an item's end: pages past it are not loaded, S is
 //     replaced by -inf, and V's rows are overwritten with zeros, since 0 x NaN of
 //     an unused cache slot would reach the sum.
+//   * What bounds it: with few rows the read of K and V (verifying, 64 requests
+//     of up to 17 tokens over 500 .. 8192 positions, 1.18 GB: 191 us, 6.1 TB/s;
+//     4 requests of 17 tokens over 100 k positions, 1.87 GB: 292 us, 6.4 TB/s;
+//     decoding, 16 requests of 200 .. 2048 positions, 85 MB: 32 us, of which 6
+//     pass before the first scores and 6 after the last); with many rows the
+//     chain of a stream, S, softmax, P V, against 1024 cycles of matrix
+//     instructions a tile: about 2850 cycles a tile of each of the two streams
+//     (prefill of 2901 + 4096 tokens at 5000 .. 8192 positions: 433 us, 1.53
+//     PFLOP/s, 81 % of a library product's rate).
 //   * Every mbarrier wait is bounded; on expiry the CTA flags
 //     DSPARK_DEV_TIMEOUT, drains what it issued, frees TMEM and returns.
 #include <cuda.h>
@@ -54,6 +63,7 @@ namespace {
 
 constexpr int kMR = 256;  // rows of an item, at most: two tiles of 128 / G tokens x G heads
 constexpr int kTN = 128;  // keys of a tile
+constexpr int kEarly = 96;  // of which the first are multiplied while the rest of P is in the making
 constexpr int kThreads = 512;  // four warpgroups: two of softmax, the single roles, the results
 // Registers a thread after the split: 256 x 168 + 128 x 96 + 128 x 80 of the
 // launch's 512 x 128.
@@ -364,7 +374,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* ml_full = o_full + 2;  // piece n's (m, l) written (8 softmax warps)
   uint64_t* ml_empty = ml_full + 1;  // and read (4 result warps)
   uint64_t* o_free = ml_empty + 1;   // [2] a stream's O of piece n read (4 result warps)
-  uint64_t* h_full = o_free + 2;   // [2] P's first 64 keys written (4 warps)
+  uint64_t* h_full = o_free + 2;   // [2] P's first kEarly keys written (4 warps)
   uint64_t* h_done = h_full + 2;   // [2] and their product done
   uint64_t* drain = h_done + 2;
   uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
@@ -526,12 +536,12 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         tc_commit(&s_full[s], lead);
       };
-      // O_s (+)= P_s V, the first 64 keys while the rest of P is in the making.
+      // O_s (+)= P_s V, the first kEarly keys while the rest of P is in the making.
       auto pv = [&](int s, uint32_t sl, bool first) {
         const uint64_t vt = v_desc + (sl % Lo::kStages) * (Lo::kTileBytes >> 4);
         const uint32_t o = tmem + 256 + s * 128, pt = tmem + s * 128;
 #pragma unroll
-        for (int kk = 0; kk < kTN / 32; ++kk)
+        for (int kk = 0; kk < kEarly / 16; ++kk)
           mma_ts(o, pt + kk * 8, vt + kk * (2048 >> 4), id_o, !(first && kk == 0), lead);
         tc_commit(&h_done[s], lead);
         uint32_t& k = s ? steps1 : steps0;
@@ -539,7 +549,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         tc_fence_after();
         if (!r) return false;
 #pragma unroll
-        for (int kk = kTN / 32; kk < kTN / 16; ++kk)
+        for (int kk = kEarly / 16; kk < kTN / 16; ++kk)
           mma_ts(o, pt + kk * 8, vt + kk * (2048 >> 4), id_o, 1u, lead);
         return true;
       };
@@ -669,17 +679,17 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         ++steps;
         if (!ok) break;
         tc_fence_after();
-        bool early = false;  // P's first half is handed over
+        bool early = false;  // P's first kEarly keys are handed over
         if (warp_live) {
           const int vis = lim - k0;  // keys of the tile that the row sees
           const bool masked = __any_sync(0xffffffffu, vis < kTN);
           // One pass: probabilities against the reference in use, and this tile's
           // maximum beside them.  They stand unless a row's maximum is out of range.
-          // A tile without a mask hands over its first 64 keys on the way; if a
+          // A tile without a mask hands over its first kEarly keys on the way; if a
           // row's maximum turns out to lie out of range after that, their product
           // is waited for and O rescaled.  Returns whether P stands.
           auto one_pass = [&](auto with_mask) {
-            uint32_t pk[32], xa[32], xb[32];
+            uint32_t pk[64], xa[32], xb[32];
             const f32x2 sc2 = pack2(p.scale_log2, p.scale_log2), ms2 = pack2(-m, -m);
             f32x2 sum2[2] = {0ull, 0ull};
             float mx = -INFINITY;
@@ -711,48 +721,45 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             tmem_wait_ld32(xb);
             tmem_ld32(tS + 64, xa);
             chunk(xb, pk + 16, 32);
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 96, xb);
+            chunk(xa, pk + 32, 64);
             if (with_mask) {
-              uint32_t pk2[32];
-              tmem_wait_ld32(xa);
-              tmem_ld32(tS + 96, xb);
-              chunk(xa, pk2, 64);
               tmem_wait_ld32(xb);
-              chunk(xb, pk2 + 16, 96);
+              chunk(xb, pk + 48, 96);
               if (__any_sync(0xffffffffu, live && out_of_range(mx * p.scale_log2, m, first))) return false;
               tmem_st32(tS, pk);
-              tmem_st32(tS + 32, pk2);
+              tmem_st32(tS + 32, pk + 32);
               add_sums(add2(sum2[0], sum2[1]));
               return true;
             }
-            const f32x2 half_sum = add2(sum2[0], sum2[1]);
+            const f32x2 early_sum = add2(sum2[0], sum2[1]);
             sum2[0] = sum2[1] = 0ull;
             const bool bad = __any_sync(0xffffffffu, live && out_of_range(mx * p.scale_log2, m, first));
-            tmem_wait_ld32(xa);
+            tmem_wait_ld32(xb);
             if (bad) return false;
             tmem_st32(tS, pk);
-            tmem_ld32(tS + 96, xb);
-            chunk(xa, pk, 64);
+            tmem_st16(tS + 32, pk + 32);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&h_full[s]);
             early = true;
-            tmem_wait_ld32(xb);
-            chunk(xb, pk + 16, 96);
+            chunk(xb, pk, 96);
             mx *= p.scale_log2;
             if (__any_sync(0xffffffffu, live && out_of_range(mx, m, false))) {
-              add_sums(half_sum);
+              add_sums(early_sum);
               return false;
             }
-            tmem_st32(tS + 32, pk);
-            add_sums(add2(half_sum, add2(sum2[0], sum2[1])));
+            tmem_st16(tS + 48, pk);
+            add_sums(add2(early_sum, add2(sum2[0], sum2[1])));
             return true;
           };
           const bool done = masked ? one_pass(std::true_type{}) : one_pass(std::false_type{});
           if (!done) {
             // Two passes over S: the maximum, then the probabilities.  After a first
-            // half that stands only the second is left (its part of S is intact).
-            const int from = early ? 64 : 0;
+            // part that stands only the rest is left (its part of S is intact).
+            const int from = early ? kEarly : 0;
             if (early) {
               ok = __all_sync(0xffffffffu, mbar_wait(&h_done[s], (steps - 1) & 1u, abort_flag,
                                                      tp.wait_budget));
