@@ -175,10 +175,19 @@ attention_simt_kernel(const AttnParams p) {
 // Adds the pieces of the items that shares cut.  Block (b, y): the item that
 // CTA b + 1's share is the first to begin inside of; its warps take the rows in
 // turn.  (As many blocks as the likely rows fill: for decoding, with a few rows
-// an item, blocks without a row cost more than they save others.)
-template <typename T, int NI>
-__global__ void __launch_bounds__(256)
+// an item, blocks without a row cost more than they save others.)  VE columns a
+// lane and step: four where rows are whole 16-byte vectors.  Bound by the read
+// of the pieces, which the attention kernel has just left in L2.
+template <typename T, int NI, int VE>
+__global__ void __launch_bounds__(256, NI * VE <= 4 ? 6 : 4)
 attention_combine_kernel(const AttnParams p, int MR, int ctas) {
+  struct alignas(4 * VE) Vec {
+    float e[VE];
+  };
+  struct alignas(sizeof(T) * VE) Out {
+    T e[VE];
+  };
+  constexpr int kAhead = 2;  // pieces in flight (four left room for half as many rows an SM: 436 for 429 us)
   // Launched while the attention kernel runs; everything below reads what it wrote.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // the call's status word
@@ -197,28 +206,40 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
     const auto at = [&](int i) {
       return (i == 0 ? (size_t)(c - 1) * 2 + 1 : (size_t)(c - 1 + i) * 2) * MR + a;
     };
-    // The weights of 32 pieces at a time, one a lane; columns lane + 32 k.
-    float m = -INFINITY, l = 0.0f;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[at(i)].x);
+    Vec v[kAhead][NI];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          v[i][k] = Vec{};
+          if (i0 + i < n && (lane + 32 * k) * VE < D)
+            v[i][k] = ((const Vec*)(p.part + at(i0 + i) * D))[lane + 32 * k];
+        }
+    };
+    load(0);
+    // The weights of 32 pieces at a time, one a lane.
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    float2 st = lane < n ? p.stats[at(lane)] : none;
+    float m = st.x, l = 0.0f;
+    for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, p.stats[at(i)].x);
     m = warp_max(m);
     const float ms = m == -INFINITY ? 0.0f : m;
-    float o[NI] = {};
+    float o[NI][VE] = {};
     for (int i0 = 0; i0 < n; i0 += 32) {
-      float f = 0.0f, lf = 0.0f;
-      if (i0 + lane < n) {
-        const float2 st = p.stats[at(i0 + lane)];
-        f = exp2f(st.x - ms);
-        lf = st.y * f;
-      }
-      l += warp_sum(lf);
-      const int k1 = n - i0 < 32 ? n - i0 : 32;
-#pragma unroll 8
-      for (int i = 0; i < k1; ++i) {
-        const float w = __shfl_sync(0xffffffffu, f, i);
-        const float* part = p.part + at(i0 + i) * D;
+      if (i0 > 0) st = i0 + lane < n ? p.stats[at(i0 + lane)] : none;
+      const float f = exp2f(st.x - ms);
+      l += warp_sum(st.y * f);
+      for (int i1 = 0; i1 < 32 && i0 + i1 < n; i1 += kAhead) {
+        if (i0 + i1 > 0) load(i0 + i1);
 #pragma unroll
-        for (int k = 0; k < NI; ++k)
-          if (lane + 32 * k < D) o[k] = fmaf(part[lane + 32 * k], w, o[k]);
+        for (int i = 0; i < kAhead; ++i) {
+          const float w = __shfl_sync(0xffffffffu, f, i1 + i);
+#pragma unroll
+          for (int k = 0; k < NI; ++k)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) o[k][e] = fmaf(v[i][k].e[e], w, o[k][e]);
+        }
       }
     }
     const int row = it.row0 + a, tok = row / G, g = row - tok * G;
@@ -226,14 +247,29 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
     const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
 #pragma unroll
     for (int k = 0; k < NI; ++k)
-      if (lane + 32 * k < D) {
-        if (std::is_same<T, float>::value)
-          ((float*)p.a.out)[dst * D + lane + 32 * k] = o[k] * inv;
-        else
-          ((__nv_bfloat16*)p.a.out)[dst * D + lane + 32 * k] = __float2bfloat16(o[k] * inv);
+      if ((lane + 32 * k) * VE < D) {
+        Out y;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          if constexpr (std::is_same<T, float>::value)
+            y.e[e] = o[k][e] * inv;
+          else
+            y.e[e] = __float2bfloat16(o[k][e] * inv);
+        }
+        ((Out*)((T*)p.a.out + dst * D))[lane + 32 * k] = y;
       }
     if (lane == 0) p.a.lse[dst] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
   }
+}
+
+template <typename T>
+cudaError_t launch_combine(const cudaLaunchConfig_t& cfg, const AttnParams& p, int MR, int ctas) {
+  const int D = p.a.c.head_dim;
+  if (D % 4 == 0)
+    return D <= 128 ? cudaLaunchKernelEx(&cfg, attention_combine_kernel<T, 1, 4>, p, MR, ctas)
+                    : cudaLaunchKernelEx(&cfg, attention_combine_kernel<T, 2, 4>, p, MR, ctas);
+  return D <= 128 ? cudaLaunchKernelEx(&cfg, attention_combine_kernel<T, 4, 1>, p, MR, ctas)
+                  : cudaLaunchKernelEx(&cfg, attention_combine_kernel<T, 8, 1>, p, MR, ctas);
 }
 
 constexpr int kSimtCtas = 304;
@@ -270,12 +306,8 @@ cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool wide = p.a.c.head_dim > 128;
-  return p.a.dtype == DSPARK_BF16
-             ? cudaLaunchKernelEx(&cfg, wide ? attention_combine_kernel<__nv_bfloat16, 8>
-                                             : attention_combine_kernel<__nv_bfloat16, 4>, p, MR, ctas)
-             : cudaLaunchKernelEx(&cfg, wide ? attention_combine_kernel<float, 8>
-                                             : attention_combine_kernel<float, 4>, p, MR, ctas);
+  return p.a.dtype == DSPARK_BF16 ? launch_combine<__nv_bfloat16>(cfg, p, MR, ctas)
+                                  : launch_combine<float>(cfg, p, MR, ctas);
 }
 
 size_t attention_workspace_bytes(int dtype, int head_dim) {
