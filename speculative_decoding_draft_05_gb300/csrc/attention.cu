@@ -18,24 +18,167 @@ namespace {
 constexpr int kMR = 32;  // rows of an item: 8 warps x 4 rows
 constexpr int kTN = 32;  // keys of a tile: one a lane
 constexpr int kThreads = 256;
-constexpr int kRowsPerWarp = 4;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowsPerWarp = 4;  // at most
+constexpr float kSlackLog2 = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// One warp holds 4 rows: lane j scores key j of the tile (K from shared memory,
-// row stride D + 4 floats, free of bank conflicts for 16-byte reads), then
-// lanes hold output columns lane + 32 i.
-template <typename T, int NI>  // NI = ceil(D / 32)
-__global__ void __launch_bounds__(kThreads)
-attention_simt_kernel(const AttnParams p) {
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Columns d .. d + 3 of a row of D values as floats, zeros past D; `vec`: rows
+// are whole, aligned 4-value vectors.
+__device__ __forceinline__ float4 load4(const float* row, int d, int D, bool vec) {
+  if (vec) return d < D ? *(const float4*)(row + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  return make_float4(d < D ? row[d] : 0.0f, d + 1 < D ? row[d + 1] : 0.0f,
+                     d + 2 < D ? row[d + 2] : 0.0f, d + 3 < D ? row[d + 3] : 0.0f);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* row, int d, int D, bool vec) {
+  if (vec) {
+    const uint2 q = d < D ? *(const uint2*)(row + d) : make_uint2(0u, 0u);
+    return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
+                       __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
+  }
+  return make_float4(d < D ? to_f32(row[d]) : 0.0f, d + 1 < D ? to_f32(row[d + 1]) : 0.0f,
+                     d + 2 < D ? to_f32(row[d + 2]) : 0.0f, d + 3 < D ? to_f32(row[d + 3]) : 0.0f);
+}
+
+// Division of n < 2^31 by a divisor known at launch: a multiplication and
+// shifts (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct Divider {
+  unsigned mul, sh1, sh2;
+  explicit Divider(unsigned d) {
+    unsigned l = 0;
+    while ((1ull << l) < d) ++l;
+    mul = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    sh1 = l < 1 ? l : 1;
+    sh2 = l < 1 ? 0 : l - 1;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    const unsigned t = __umulhi(mul, (unsigned)n);
+    return (int)((t + (((unsigned)n - t) >> sh1)) >> sh2);
+  }
+};
+
+// A warp's rows: reference m (the same in all lanes), this lane's part of the
+// sum l, and the output columns 2 lane + 64 k and the next.
+template <int NP>
+struct Rows {
+  float m[kRowsPerWarp], l[kRowsPerWarp];
+  int lim[kRowsPerWarp];  // keys that the row sees
+  f32x2 o[kRowsPerWarp][NP];
+};
+
+// One tile for RW rows.  Lane j scores key j (K from shared memory, row stride
+// ld = D + 4 floats: free of bank conflicts for 16-byte reads).  The reference
+// follows the maximum only where that lies 2^8 or more above it: mostly once.
+// Probabilities pass through shared memory as pairs (e, e), the operands of
+// packed products with two columns of V.
+template <int NI, int RW>
+__device__ __forceinline__ void simt_tile(Rows<NI / 2>& r, const float* sq, const float* sk,
+                                          const float* sv, f32x2 (*sp)[kRowsPerWarp], int j0,
+                                          float scale_log2) {
+  constexpr int ld = NI * 32 + 4;
+  const int lane = threadIdx.x & 31;
+  f32x2 s2[RW] = {};
+  const ulonglong2* kr = (const ulonglong2*)(sk + lane * ld);
+#pragma unroll 8
+  for (int d = 0; d < NI * 8; ++d) {
+    const ulonglong2 kx = kr[d];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const ulonglong2 qx = ((const ulonglong2*)(sq + i * ld))[d];
+      s2[i] = fma2(qx.x, kx.x, s2[i]);
+      s2[i] = fma2(qx.y, kx.y, s2[i]);
+    }
+  }
+  float x[RW];
+  bool up = false;
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    float a, b;
+    unpack2(s2[i], a, b);
+    x[i] = j0 + lane < r.lim[i] ? (a + b) * scale_log2 : -INFINITY;
+    up |= x[i] > r.m[i] + kSlackLog2;
+  }
+  if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const float mt = fmaxf(r.m[i], warp_max(x[i]));
+      const float f = mt == -INFINITY ? 1.0f : exp2f(r.m[i] - mt);
+      r.m[i] = mt;
+      r.l[i] *= f;
+#pragma unroll
+      for (int k = 0; k < NI / 2; ++k) r.o[i][k] = mul2(r.o[i][k], pack2(f, f));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const float e = exp2f(x[i] - (r.m[i] == -INFINITY ? 0.0f : r.m[i]));
+    r.l[i] += e;
+    sp[lane][i] = pack2(e, e);
+  }
+  __syncwarp();
+#pragma unroll 8
+  for (int j = 0; j < kTN; ++j) {
+    f32x2 e[RW];
+    if (RW == 1) {
+      e[0] = sp[j][0];
+    } else {
+#pragma unroll
+      for (int i = 0; i + 1 < RW; i += 2) {
+        const ulonglong2 q = *(const ulonglong2*)&sp[j][i];
+        e[i] = q.x, e[i + 1] = q.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NI / 2; ++k) {
+      const f32x2 v = *(const f32x2*)(sv + j * ld + 2 * lane + 64 * k);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) r.o[i][k] = fma2(e[i], v, r.o[i][k]);
+    }
+  }
+  __syncwarp();
+}
+
+// The rows of an item are spread over the warps, one, two or four a warp; a
+// tile of K and V is loaded into registers while the one before, in shared
+// memory, is worked on, and the pages of the one after are looked up.
+template <typename T, int NI>  // NI = ceil(D / 32), 2, 4 or 8
+__global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
+attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
   extern __shared__ float4 smem4[];
   __shared__ AttnStart<kTN> st;
   __shared__ int flags;
-  __shared__ __align__(16) float sp[kThreads / 32][kTN][kRowsPerWarp];  // probabilities of a warp's rows
-  const int D = p.a.c.head_dim, ld = NI * 32 + 4;
-  float* sq = (float*)smem4;       // [kMR][ld], scaled by scale * log2 e
+  __shared__ __align__(16) f32x2 sp[kWarps][kTN][kRowsPerWarp];  // probabilities of a warp's rows
+  constexpr int ld = NI * 32 + 4;
+  constexpr int kPer = NI * 8;               // threads a row, four columns each
+  constexpr int kPass = kThreads / kPer;     // rows a pass of the CTA; NI passes a tile
+  const int D = p.a.c.head_dim;
+  float* sq = (float*)smem4;       // [kMR][ld]
   float* sk = sq + kMR * ld;       // [kTN][ld]
   float* sv = sk + kTN * ld;       // [kTN][ld]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lr = threadIdx.x / kPer, lc = (threadIdx.x % kPer) * 4;  // first row and column it loads
   const int S = p.a.c.page_size, G = p.a.G;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -46,7 +189,39 @@ attention_simt_kernel(const AttnParams p) {
   if (threadIdx.x == 0) attn_write_cut(p, st);
 
   for (; !w.done(); w.next(p, &flags)) {
-    const int rows = w.block_rows(p), row0 = w.m * kMR;
+    const int rows = w.block_rows(p), row0 = w.m * kMR, t1 = w.last_tile();
+    const int rw = rows <= kWarps ? 1 : rows <= 2 * kWarps ? 2 : 4;
+    const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
+    int page[NI];
+    float4 kx[NI], vx[NI];
+    auto look_up = [&](int t) {  // the pages of tile t's rows; -1: past the item's keys
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        const int j = t * kTN + lr + u * kPass;
+        page[u] = t < t1 && j < w.end ? table[by_page(j)] : -1;
+      }
+    };
+    auto load = [&](int t) {  // positions at or past `end` read as zeros
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        const int j = t * kTN + lr + u * kPass;
+        kx[u] = vx[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (t < t1 && j < w.end) {
+          int pg = page[u];
+          if (pg < 0 || pg >= p.a.c.n_pages) {
+            flag_status(&flags, DSPARK_DEV_BAD_INPUT);
+            pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+          }
+          const long long at = pg * p.a.c.page_stride + (j - by_page(j) * S) * p.a.c.token_stride +
+                               w.h * p.a.c.head_stride;
+          kx[u] = load4((const T*)p.a.c.k + at, lc, D, vec);
+          vx[u] = load4((const T*)p.a.c.v + at, lc, D, vec);
+        }
+      }
+    };
+    look_up(w.first_tile());
+    load(w.first_tile());
+    look_up(w.first_tile() + 1);
     __syncthreads();
     for (int i = threadIdx.x; i < kMR * NI * 32; i += kThreads) {
       const int a = i / (NI * 32), d = i - a * (NI * 32);
@@ -58,113 +233,66 @@ attention_simt_kernel(const AttnParams p) {
       }
       sq[a * ld + d] = x;
     }
-    float m[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][NI];
-    int lim[kRowsPerWarp];  // keys that the row sees
+    Rows<NI / 2> r;
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
-      const int a = warp * kRowsPerWarp + i;
-      m[i] = -INFINITY, l[i] = 0.0f;
-      lim[i] = a < rows ? w.q.L - w.q.n + (row0 + a) / G + 1 : 0;
+      const int a = warp * rw + i;
+      r.m[i] = -INFINITY, r.l[i] = 0.0f;
+      r.lim[i] = i < rw && a < rows ? w.q.L - w.q.n + (row0 + a) / G + 1 : 0;
 #pragma unroll
-      for (int k = 0; k < NI; ++k) o[i][k] = 0.0f;
+      for (int k = 0; k < NI / 2; ++k) r.o[i][k] = 0ull;
     }
-    for (int t = w.first_tile(); t < w.last_tile(); ++t) {
-      const int j0 = t * kTN;
-      __syncthreads();
-      // K and V of the tile; positions at or past `end` read as zeros.
-      for (int a = warp; a < kTN; a += kThreads / 32) {
-        const int j = j0 + a;
-        int page = -1;
-        if (j < w.end) {
-          page = p.a.a.page_table[(size_t)w.r * p.a.a.max_pages + j / S];
-          if (page < 0 || page >= p.a.c.n_pages) {
-            if (lane == 0) flag_status(&flags, DSPARK_DEV_BAD_INPUT);
-            page = page < 0 ? 0 : p.a.c.n_pages - 1;
-          }
-        }
-        const long long at = page * p.a.c.page_stride + (j % S) * p.a.c.token_stride +
-                             w.h * p.a.c.head_stride;
+    for (int t = w.first_tile(); t < t1; ++t) {
+      if (t > w.first_tile()) __syncthreads();
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const int d = lane + 32 * k;
-          const bool in = page >= 0 && d < D;
-          sk[a * ld + d] = in ? to_f32(((const T*)p.a.c.k)[at + d]) : 0.0f;
-          sv[a * ld + d] = in ? to_f32(((const T*)p.a.c.v)[at + d]) : 0.0f;
-        }
+      for (int u = 0; u < NI; ++u) {
+        *(float4*)(sk + (lr + u * kPass) * ld + lc) = kx[u];
+        *(float4*)(sv + (lr + u * kPass) * ld + lc) = vx[u];
       }
       __syncthreads();
-      if (warp * kRowsPerWarp < rows) {
-        float s[kRowsPerWarp] = {};
-        const float4* kr = (const float4*)(sk + lane * ld);
-#pragma unroll 4
-        for (int d = 0; d < NI * 8; ++d) {
-          const float4 kx = kr[d];
-#pragma unroll
-          for (int i = 0; i < kRowsPerWarp; ++i) {
-            const float4 qx = ((const float4*)(sq + (warp * kRowsPerWarp + i) * ld))[d];
-            s[i] = fmaf(qx.x, kx.x, s[i]);
-            s[i] = fmaf(qx.y, kx.y, s[i]);
-            s[i] = fmaf(qx.z, kx.z, s[i]);
-            s[i] = fmaf(qx.w, kx.w, s[i]);
-          }
-        }
-        float f[kRowsPerWarp];
-#pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-          const float x = j0 + lane < lim[i] ? s[i] * p.scale_log2 : -INFINITY;
-          const float mt = fmaxf(m[i], warp_max(x));
-          const float ms = mt == -INFINITY ? 0.0f : mt;
-          f[i] = exp2f(m[i] - ms);
-          const float e = exp2f(x - ms);
-          l[i] = l[i] * f[i] + warp_sum(e);
-          m[i] = mt;
-          sp[warp][lane][i] = e;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i)
-#pragma unroll
-          for (int k = 0; k < NI; ++k) o[i][k] *= f[i];
-#pragma unroll 4
-        for (int j = 0; j < kTN; ++j) {
-          const float4 e = *(const float4*)sp[warp][j];
-#pragma unroll
-          for (int k = 0; k < NI; ++k) {
-            const float v = sv[j * ld + lane + 32 * k];
-            o[0][k] = fmaf(e.x, v, o[0][k]);
-            o[1][k] = fmaf(e.y, v, o[1][k]);
-            o[2][k] = fmaf(e.z, v, o[2][k]);
-            o[3][k] = fmaf(e.w, v, o[3][k]);
-          }
-        }
-        __syncwarp();
+      load(t + 1);
+      look_up(t + 2);
+      if (warp * rw < rows) {
+        const float* q = sq + warp * rw * ld;
+        if (rw == 1)
+          simt_tile<NI, 1>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
+        else if (rw == 2)
+          simt_tile<NI, 2>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
+        else
+          simt_tile<NI, 4>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
       }
     }
     const int slot = attn_slot(w);
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
-      const int a = warp * kRowsPerWarp + i;
-      if (a >= rows) continue;
-      if (slot < 0) {
-        const int tok = (row0 + a) / G, g = (row0 + a) - tok * G;
-        const size_t at = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + g;
-        const float inv = l[i] > 0.0f ? 1.0f / l[i] : l[i] == 0.0f ? 0.0f : l[i];
+      const int a = warp * rw + i;
+      if (i >= rw || a >= rows) continue;
+      const float l = warp_sum(r.l[i]);
+      const int tok = (row0 + a) / G, g = (row0 + a) - tok * G;
+      const size_t out = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + g;
+      const size_t part = ((size_t)blockIdx.x * 2 + slot) * kMR + a;
+      const float inv = slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
 #pragma unroll
-        for (int k = 0; k < NI; ++k)
-          if (lane + 32 * k < D) {
-            const float y = o[i][k] * inv;
-            if (std::is_same<T, float>::value)
-              ((float*)p.a.out)[at * D + lane + 32 * k] = y;
-            else
-              ((__nv_bfloat16*)p.a.out)[at * D + lane + 32 * k] = __float2bfloat16(y);
-          }
-        if (lane == 0) p.a.lse[at] = l[i] == 0.0f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
-      } else {
-        const size_t at = ((size_t)blockIdx.x * 2 + slot) * kMR + a;
+      for (int k = 0; k < NI / 2; ++k) {
+        float y[2];
+        unpack2(r.o[i][k], y[0], y[1]);
 #pragma unroll
-        for (int k = 0; k < NI; ++k)
-          if (lane + 32 * k < D) p.part[at * D + lane + 32 * k] = o[i][k];
-        if (lane == 0) p.stats[at] = make_float2(m[i], l[i]);
+        for (int e = 0; e < 2; ++e) {
+          const int d = 2 * lane + 64 * k + e;
+          if (d >= D) continue;
+          if (slot >= 0)
+            p.part[part * D + d] = y[e];
+          else if constexpr (std::is_same<T, float>::value)
+            ((float*)p.a.out)[out * D + d] = y[e] * inv;
+          else
+            ((__nv_bfloat16*)p.a.out)[out * D + d] = __float2bfloat16(y[e] * inv);
+        }
+      }
+      if (lane == 0) {
+        if (slot >= 0)
+          p.stats[part] = make_float2(r.m[i], l);
+        else
+          p.a.lse[out] = l == 0.0f ? -INFINITY : r.m[i] * kLn2 + logf(l);
       }
     }
   }
@@ -280,14 +408,18 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
   static const cudaError_t attr = cudaFuncSetAttribute(
       attention_simt_kernel<T, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (attr != cudaSuccess) return attr;
-  attention_simt_kernel<T, NI><<<kSimtCtas, kThreads, smem, s>>>(p);
+  // Rows that are whole 16-byte (fp32) or 8-byte (bf16) vectors load as such.
+  const CacheView& c = p.a.c;
+  const bool vec = c.head_dim % 4 == 0 && c.page_stride % 4 == 0 && c.token_stride % 4 == 0 &&
+                   c.head_stride % 4 == 0 &&
+                   (((uintptr_t)c.k | (uintptr_t)c.v) & (4 * sizeof(T) - 1)) == 0;
+  attention_simt_kernel<T, NI><<<kSimtCtas, kThreads, smem, s>>>(p, Divider((unsigned)c.page_size), vec);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
   const int ni = (p.a.c.head_dim + 31) / 32;
-  if (ni <= 1) return launch_simt<T, 1>(p, s);
   if (ni <= 2) return launch_simt<T, 2>(p, s);
   if (ni <= 4) return launch_simt<T, 4>(p, s);
   return launch_simt<T, 8>(p, s);

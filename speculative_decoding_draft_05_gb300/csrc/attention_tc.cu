@@ -324,7 +324,7 @@ __device__ __forceinline__ void regs_inc() {
 
 struct TcParams {
   AttnParams p;
-  int box_tokens;  // tokens of a K/V box: min(page_size, 128)
+  int box_tokens;  // tokens of a K/V box: the largest power of two in page_size, up to 128
   int q_tokens;    // tokens of a Q tile (a box): 128 / G
   int tile_rows;   // rows of a Q tile: q_tokens G (128 where G > 128)
   int q_tma;       // q can be loaded by TMA (else by the loader's threads)
@@ -1145,7 +1145,7 @@ cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& 
 bool attention_tc_supported(const AttnArgs& a) {
   const CacheView& c = a.c;
   if (a.dtype != DSPARK_BF16 || c.head_dim % 8 != 0 || c.head_dim > 128) return false;
-  if (c.page_size < 8 || (c.page_size & (c.page_size - 1)) != 0) return false;
+  if (c.page_size % 8 != 0) return false;  // (a tile is at most 16 boxes of 8 tokens, two halves each)
   if (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) return false;
   const long long most = 1ll << 39;  // elements: 2^40 bytes
   if (c.token_stride % 8 != 0 || c.token_stride >= most) return false;
@@ -1165,7 +1165,8 @@ cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
                     fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f),
                     attn_item_units(a), kMR};
   tp.sign = a.scale < 0 ? -1.0f : 1.0f;
-  tp.box_tokens = a.c.page_size < kTN ? a.c.page_size : kTN;
+  tp.box_tokens = a.c.page_size & -a.c.page_size;
+  if (tp.box_tokens > kTN) tp.box_tokens = kTN;
   tp.q_tokens = a.G <= 128 ? 128 / a.G : 1;
   tp.tile_rows = a.G <= 128 ? tp.q_tokens * a.G : 128;
   tp.p.mr = 2 * tp.tile_rows;

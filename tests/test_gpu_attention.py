@@ -134,6 +134,9 @@ SHAPES = [
     ([3, 2], [70, 300], 4, 2, 40, 16),                # narrower than a swizzled row
     ([2, 40], [9, 200], 3, 1, 16, 32),
     ([3, 1], [200, 20], 130, 1, 64, 16),              # more query heads a K/V head than rows of a tile
+    ([2, 17, 1], [65, 300, 24], 4, 2, 128, 24),       # pages of whole boxes of 8 tokens
+    ([20, 3], [400, 97], 8, 2, 64, 48),
+    ([90, 1], [300, 641], 8, 2, 128, 160),            # a page longer than a tile, not a multiple of it
     ([60, 30, 1, 70], [60, 300, 900, 70], 12, 4, 128, 16),  # pieces of one and of two row tiles in turn
     ([1, 200, 1, 1, 300, 2], [50, 200, 1300, 7, 900, 2], 20, 4, 64, 64),
 ]
