@@ -15,11 +15,12 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMR = 32;  // rows of an item: 8 warps x 4 rows
+constexpr int kMR = 64;  // rows of an item: 8 warps x 8 rows
 constexpr int kTN = 32;  // keys of a tile: one a lane
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowsPerWarp = 4;  // at most
+constexpr int kRowsPerWarp = 8;  // at most
+constexpr int kProbPairs = 128;  // (e, e) pairs of a warp in shared memory
 constexpr float kSlackLog2 = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -95,8 +96,7 @@ struct Rows {
 // packed products with two columns of V.
 template <int NI, int RW>
 __device__ __forceinline__ void simt_tile(Rows<NI / 2>& r, const float* sq, const float* sk,
-                                          const float* sv, f32x2 (*sp)[kRowsPerWarp], int j0,
-                                          float scale_log2) {
+                                          const float* sv, f32x2* sp, int j0, float scale_log2) {
   constexpr int ld = NI * 32 + 4;
   const int lane = threadIdx.x & 31;
   f32x2 s2[RW] = {};
@@ -133,50 +133,64 @@ __device__ __forceinline__ void simt_tile(Rows<NI / 2>& r, const float* sq, cons
   }
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
-    const float e = exp2f(x[i] - (r.m[i] == -INFINITY ? 0.0f : r.m[i]));
-    r.l[i] += e;
-    sp[lane][i] = pack2(e, e);
+    x[i] = exp2f(x[i] - (r.m[i] == -INFINITY ? 0.0f : r.m[i]));
+    r.l[i] += x[i];
   }
-  __syncwarp();
-#pragma unroll 8
-  for (int j = 0; j < kTN; ++j) {
-    f32x2 e[RW];
-    if (RW == 1) {
-      e[0] = sp[j][0];
-    } else {
+  constexpr int kKeys = RW <= 4 ? kTN : kProbPairs / RW;  // at a time
+#pragma unroll 1
+  for (int h = 0; h < kTN; h += kKeys) {
+    if (kKeys == kTN || (lane >= h && lane < h + kKeys)) {
 #pragma unroll
-      for (int i = 0; i + 1 < RW; i += 2) {
-        const ulonglong2 q = *(const ulonglong2*)&sp[j][i];
-        e[i] = q.x, e[i + 1] = q.y;
+      for (int i = 0; i < RW; ++i) sp[(lane - h) * RW + i] = pack2(x[i], x[i]);
+    }
+    __syncwarp();
+    const float* vh = sv + h * ld + 2 * lane;
+#pragma unroll 8
+    for (int j = 0; j < kKeys; ++j) {
+      f32x2 e[RW];
+      if (RW == 1) {
+        e[0] = sp[j];
+      } else {
+#pragma unroll
+        for (int i = 0; i + 1 < RW; i += 2) {
+          const ulonglong2 q = *(const ulonglong2*)&sp[j * RW + i];
+          e[i] = q.x, e[i + 1] = q.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NI / 2; ++k) {
+        const f32x2 v = *(const f32x2*)(vh + j * ld + 64 * k);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) r.o[i][k] = fma2(e[i], v, r.o[i][k]);
       }
     }
-#pragma unroll
-    for (int k = 0; k < NI / 2; ++k) {
-      const f32x2 v = *(const f32x2*)(sv + j * ld + 2 * lane + 64 * k);
-#pragma unroll
-      for (int i = 0; i < RW; ++i) r.o[i][k] = fma2(e[i], v, r.o[i][k]);
-    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
-// The rows of an item are spread over the warps, one, two or four a warp; a
-// tile of K and V is loaded into registers while the one before, in shared
-// memory, is worked on, and the pages of the one after are looked up.
+__device__ __forceinline__ void copy16(float* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+
+// The rows of an item are spread over the warps, one, two, four or eight a warp;
+// a tile of K and V is on its way to shared memory while the one before is
+// worked on, and the pages of the one after are looked up.
 template <typename T, int NI>  // NI = ceil(D / 32), 2, 4 or 8
 __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
   extern __shared__ float4 smem4[];
   __shared__ AttnStart<kTN> st;
   __shared__ int flags;
-  __shared__ __align__(16) f32x2 sp[kWarps][kTN][kRowsPerWarp];  // probabilities of a warp's rows
+  __shared__ __align__(16) f32x2 sp[kWarps][kProbPairs];  // probabilities of a warp's rows
   constexpr int ld = NI * 32 + 4;
   constexpr int kPer = NI * 8;               // threads a row, four columns each
   constexpr int kPass = kThreads / kPer;     // rows a pass of the CTA; NI passes a tile
   const int D = p.a.c.head_dim;
   float* sq = (float*)smem4;       // [kMR][ld]
-  float* sk = sq + kMR * ld;       // [kTN][ld]
-  float* sv = sk + kTN * ld;       // [kTN][ld]
+  float* skv = sq + kMR * ld;      // [2] K, V: [kTN][ld] each
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int lr = threadIdx.x / kPer, lc = (threadIdx.x % kPer) * 4;  // first row and column it loads
   const int S = p.a.c.page_size, G = p.a.G;
@@ -190,10 +204,9 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
 
   for (; !w.done(); w.next(p, &flags)) {
     const int rows = w.block_rows(p), row0 = w.m * kMR, t1 = w.last_tile();
-    const int rw = rows <= kWarps ? 1 : rows <= 2 * kWarps ? 2 : 4;
+    const int rw = rows <= kWarps ? 1 : rows <= 2 * kWarps ? 2 : rows <= 4 * kWarps ? 4 : 8;
     const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
     int page[NI];
-    float4 kx[NI], vx[NI];
     auto look_up = [&](int t) {  // the pages of tile t's rows; -1: past the item's keys
 #pragma unroll
       for (int u = 0; u < NI; ++u) {
@@ -201,11 +214,13 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
         page[u] = t < t1 && j < w.end ? table[by_page(j)] : -1;
       }
     };
-    auto load = [&](int t) {  // positions at or past `end` read as zeros
+    auto load = [&](int t) {  // into buffer t & 1; positions at or past `end` become zeros
+      float* sk = skv + (t & 1) * 2 * kTN * ld + lr * ld + lc;
 #pragma unroll
       for (int u = 0; u < NI; ++u) {
         const int j = t * kTN + lr + u * kPass;
-        kx[u] = vx[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float* k = sk + u * kPass * ld;
+        float* v = k + kTN * ld;
         if (t < t1 && j < w.end) {
           int pg = page[u];
           if (pg < 0 || pg >= p.a.c.n_pages) {
@@ -214,15 +229,22 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
           }
           const long long at = pg * p.a.c.page_stride + (j - by_page(j) * S) * p.a.c.token_stride +
                                w.h * p.a.c.head_stride;
-          kx[u] = load4((const T*)p.a.c.k + at, lc, D, vec);
-          vx[u] = load4((const T*)p.a.c.v + at, lc, D, vec);
+          if (std::is_same<T, float>::value && vec && lc < D) {
+            copy16(k, (const float*)p.a.c.k + at + lc);
+            copy16(v, (const float*)p.a.c.v + at + lc);
+          } else {
+            *(float4*)k = load4((const T*)p.a.c.k + at, lc, D, vec);
+            *(float4*)v = load4((const T*)p.a.c.v + at, lc, D, vec);
+          }
+        } else {
+          *(float4*)k = *(float4*)v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
       }
     };
+    __syncthreads();  // (the item before is done with both buffers)
     look_up(w.first_tile());
     load(w.first_tile());
     look_up(w.first_tile() + 1);
-    __syncthreads();
     for (int i = threadIdx.x; i < kMR * NI * 32; i += kThreads) {
       const int a = i / (NI * 32), d = i - a * (NI * 32);
       float x = 0.0f;
@@ -243,23 +265,22 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
       for (int k = 0; k < NI / 2; ++k) r.o[i][k] = 0ull;
     }
     for (int t = w.first_tile(); t < t1; ++t) {
-      if (t > w.first_tile()) __syncthreads();
-#pragma unroll
-      for (int u = 0; u < NI; ++u) {
-        *(float4*)(sk + (lr + u * kPass) * ld + lc) = kx[u];
-        *(float4*)(sv + (lr + u * kPass) * ld + lc) = vx[u];
-      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
-      load(t + 1);
+      load(t + 1);  // (all are past tile t - 1, which was in its buffer)
       look_up(t + 2);
       if (warp * rw < rows) {
         const float* q = sq + warp * rw * ld;
+        const float* sk = skv + (t & 1) * 2 * kTN * ld;
+        const float* sv = sk + kTN * ld;
         if (rw == 1)
           simt_tile<NI, 1>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
         else if (rw == 2)
           simt_tile<NI, 2>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
-        else
+        else if (rw == 4)
           simt_tile<NI, 4>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
+        else
+          simt_tile<NI, 8>(r, q, sk, sv, sp[warp], t * kTN, p.scale_log2);
       }
     }
     const int slot = attn_slot(w);
@@ -404,7 +425,7 @@ constexpr int kSimtCtas = 304;
 
 template <typename T, int NI>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
-  const int smem = 3 * kMR * (NI * 32 + 4) * (int)sizeof(float);
+  const int smem = (kMR + 4 * kTN) * (NI * 32 + 4) * (int)sizeof(float);
   static const cudaError_t attr = cudaFuncSetAttribute(
       attention_simt_kernel<T, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (attr != cudaSuccess) return attr;
