@@ -6,9 +6,16 @@
 // cache; what costs there is latency, so each operation is one kernel of one
 // thread-block cluster (8 CTAs x 1024 threads, phases separated by the
 // hardware's cluster barrier) and the copy kernel behind it, instead of a
-// chain of launches.  Which page an
-// allocation takes depends on nothing but the inputs: the lowest free ids, in
-// the order of the requests, found by a prefix sum over the counts.
+// chain of launches.  Which page an allocation takes depends on nothing but the
+// inputs: the lowest free ids, in the order of the requests, found by a prefix
+// sum over the counts.
+//
+// Bounds and figures: the cluster kernels are chains of dependent reads (resize
+// of 512 requests over 40,000 pages: 11 us in a graph, 20 us a call from Python,
+// whose host side is the longer; compact of 2000 pages 10 us); the copies and
+// the append move bytes: 240 MB of pages read and written in 78 us (6.7 TB/s),
+// 16 k new tokens of 8 x 128 (119 MB each way) in 35 us, 4.8 k tokens in 9 us,
+// four dependent look-ups behind their loads.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -665,13 +672,17 @@ MetaCopy meta_args(const PageMeta& m, bool table, bool len) {
 }
 
 // Tables of up to kMetaInKernel entries are copied by the cluster kernel
-// itself, larger ones by a launch of their own over all SMs (8 SMs move about
-// an eighth of a TB/s each way: at 1 M entries that is about the launch saved).
-constexpr size_t kMetaInKernel = 1u << 20;
+// itself, larger ones by a launch of their own over all SMs.  A resize whose
+// outputs are arrays of their own, inside a CUDA graph, with / without the extra
+// launch: 32 k entries 11.5 / 11.1 us, 262 k 11.4 / 13.4, 1 M 14.9 / 24.1; outside
+// a graph the launch costs the host 3 us more.
+constexpr size_t kMetaInKernel = 1u << 17;
 // A resize copies the shared pages that it has to split in the cluster kernel
-// where even all requests' pages come to this many bytes (8 SMs move about
-// 1 TB/s; it mostly has none or a few, and the second launch costs 5 us).
-constexpr size_t kCopyInKernel = 16u << 20;
+// where even all requests' pages come to this many bytes.  It mostly has none:
+// then the second launch costs 1.5 us in a graph and 5 us outside one; where
+// every request has one, the 8 SMs take 15 us for 1 MB (12.5 with the launch),
+// 23 for 4 MB (12.7) and 57 for 17 MB (16).
+constexpr size_t kCopyInKernel = 8u << 20;
 cudaError_t split_meta(MetaCopy* c, cudaStream_t s) {
   size_t most = 0, all = 0;
   for (int k = 0; k < 3; ++k)
