@@ -198,6 +198,7 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) flags = 0;
   __syncthreads();
+  wait_for_previous();
   attn_plan<kTN>(p, &st, &flags);
   AttnWalk<kTN> w = st.walk;
   if (threadIdx.x == 0) attn_write_cut(p, st);
@@ -337,8 +338,8 @@ attention_combine_kernel(const AttnParams p, int MR, int ctas) {
     T e[VE];
   };
   constexpr int kAhead = 2;  // pieces in flight (four left room for half as many rows an SM: 436 for 429 us)
-  // Launched while the attention kernel runs; everything below reads what it wrote.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();  // everything below reads what the attention kernel wrote
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // the call's status word
     int f = 0;
     for (int i = threadIdx.x; i < ctas; i += 32) f |= __ldcg(p.flags + i);
@@ -434,8 +435,9 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
   const bool vec = c.head_dim % 4 == 0 && c.page_stride % 4 == 0 && c.token_stride % 4 == 0 &&
                    c.head_stride % 4 == 0 &&
                    (((uintptr_t)c.k | (uintptr_t)c.v) & (4 * sizeof(T) - 1)) == 0;
-  attention_simt_kernel<T, NI><<<kSimtCtas, kThreads, smem, s>>>(p, Divider((unsigned)c.page_size), vec);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr_pdl;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(kSimtCtas), kThreads, smem, s, &attr_pdl);
+  return cudaLaunchKernelEx(&cfg, attention_simt_kernel<T, NI>, p, Divider((unsigned)c.page_size), vec);
 }
 
 template <typename T>
@@ -449,16 +451,10 @@ cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
   const long long rows = attn_likely_rows(p.a);
-  cfg.gridDim = dim3(ctas > 1 ? ctas - 1 : 1, (unsigned)((rows < MR ? rows : MR) + 7) / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const dim3 grid(ctas > 1 ? ctas - 1 : 1, (unsigned)((rows < MR ? rows : MR) + 7) / 8);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = overlapped_launch(grid, 256, 0, s, &attr);
   return p.a.dtype == DSPARK_BF16 ? launch_combine<__nv_bfloat16>(cfg, p, MR, ctas)
                                   : launch_combine<float>(cfg, p, MR, ctas);
 }

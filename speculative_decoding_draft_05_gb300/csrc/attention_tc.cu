@@ -421,6 +421,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  wait_for_previous();
   attn_plan<kTN>(p, st, flags);  // ends with a barrier
   tc_fence_before();
   __syncthreads();
@@ -1132,8 +1133,9 @@ cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& 
   static const cudaError_t attr = cudaFuncSetAttribute(
       attention_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
   if (attr != cudaSuccess) return attr;
-  attention_tc_kernel<DP><<<sm_count(), kThreads, Layout<DP>::kBytes, s>>>(k, v, q, tp);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr_pdl;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(sm_count()), kThreads, Layout<DP>::kBytes, s, &attr_pdl);
+  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<DP>, k, v, q, tp);
 }
 
 }  // namespace

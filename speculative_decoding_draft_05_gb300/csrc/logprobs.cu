@@ -273,6 +273,7 @@ logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
   __shared__ int sm[kRowWarps];
   __shared__ uint16_t list[kListRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
   // Rows without a token get their results here.
@@ -604,7 +605,7 @@ logprobs_finish_kernel(const T* __restrict__ Z, long long row_stride,
                        const RowOutputs o) {
   __shared__ RowScratch scratch[kFinishWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * kFinishWarps + warp;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   const int r = __ldcg(rows_wanted + 1 + i);  // (read with the count: a row of the list or, past it, unused)
   if (i >= __ldcg(rows_wanted)) return;
   float* gm = gmax + (size_t)r * groups;
@@ -643,6 +644,7 @@ logprobs_short_kernel(const T* __restrict__ Z, long long row_stride,
                       float invT, float* gmax, const RowOutputs o, int* status) {
   __shared__ RowScratch scratch[kFinishWarps];
   const int warp = threadIdx.x >> 5, r = blockIdx.x * kFinishWarps + warp;
+  wait_for_previous();
   if (blockIdx.x == 0) {  // the status word, from all tokens
     bool bad = false;
     for (int i = threadIdx.x; i < n_rows; i += kFinishWarps * 32) bad |= __ldg(tokens + i) >= V;
@@ -686,26 +688,20 @@ cudaError_t launch(const void* Z, long long row_stride, const int32_t* tokens, i
   const int blocks = blocks_of<T>(V), groups = groups_of(V);
   const float c = invT * kLog2e;
   const int row_ctas = (n_rows + kFinishWarps - 1) / kFinishWarps;
+  cudaLaunchAttribute attr;
   if (V <= kShortIds && n_rows <= kShortRows) {
-    logprobs_short_kernel<T><<<row_ctas, kFinishWarps * 32, 0, s>>>(
-        (const T*)Z, row_stride, tokens, n_rows, V, groups, c, invT, gmax, o, (int*)ws);
-    return cudaGetLastError();
+    const cudaLaunchConfig_t cfg = overlapped_launch(dim3(row_ctas), kFinishWarps * 32, 0, s, &attr);
+    return cudaLaunchKernelEx(&cfg, logprobs_short_kernel<T>, (const T*)Z, row_stride, tokens, n_rows,
+                              V, groups, c, invT, gmax, o, (int*)ws);
   }
   const long long units = (long long)n_rows * blocks;  // few: a block an SM first
-  logprobs_stream_kernel<T><<<(int)(units < 152 ? units : 152), kRowThreads, 0, s>>>(
-      (const T*)Z, row_stride, tokens, n_rows, V, blocks, groups, c, parts, gmax, rows_wanted, o,
-      (int*)ws);
-  cudaError_t e = cudaGetLastError();
+  const cudaLaunchConfig_t stream_cfg =
+      overlapped_launch(dim3((unsigned)(units < 152 ? units : 152)), kRowThreads, 0, s, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&stream_cfg, logprobs_stream_kernel<T>, (const T*)Z, row_stride,
+                                           tokens, n_rows, V, blocks, groups, c, parts, gmax,
+                                           rows_wanted, o, (int*)ws);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(row_ctas);
-  cfg.blockDim = dim3(kFinishWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(row_ctas), kFinishWarps * 32, 0, s, &attr);
   return cudaLaunchKernelEx(&cfg, logprobs_finish_kernel<T>, (const T*)Z, row_stride, tokens, V,
                             blocks, groups, c, invT, (const float4*)parts, gmax,
                             (const int*)rows_wanted, o);

@@ -198,7 +198,7 @@ constexpr int kCopyUnroll = 4;  // 16-byte loads in flight a thread
 __device__ __forceinline__ int copy_begin(const CopyArgs& a) {
   const CopyTail& t = a.tail;
   if (!t.words) return a.n_max;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   if (t.free_pages && blockIdx.x == 0 && threadIdx.x == 0) {
     int f = 0, freed = 0;
     for (int i = 0; i < kClusterCtas; ++i) {
@@ -333,6 +333,7 @@ pages_resize_kernel(const ResizeArgs a) {
   int* const status = &flags;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) flags = freed = 0;
+  wait_for_previous();
   __syncthreads();
   copy_meta(a.copy, gthread, kClusterCtas * kPageThreads);
   cl.sync();
@@ -511,6 +512,7 @@ pages_fork_kernel(const ForkArgs a) {
   int* const status = &flags;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) flags = 0;
+  wait_for_previous();
   __syncthreads();
   // Up to the last barrier only the inputs are read and, where the outputs are
   // arrays of their own, those filled from them.
@@ -634,6 +636,7 @@ pages_compact_kernel(const CompactArgs a) {
   const int32_t* rc = m.refcount;
   int lo, hi, none[1], live[1], at[2], n[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();
   page_share(m.n_pages, rank, lo, hi);
   copy_meta(a.copy, rank * kPageThreads + (int)threadIdx.x, kClusterCtas * kPageThreads);
   const int n_mine[1] = {warp_count(lo, hi, [&](int p) { return rc[p] > 0; })};
@@ -779,6 +782,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
   const int lane = threadIdx.x & 31;
   const int S = p.c.page_size;
   const int per_head = p.c.head_dim / VE, n = p.c.heads * per_head;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (attention over the cache mostly follows)
+  wait_for_previous();
   if (blockIdx.x == 0) {
     append_status(p);
     return;
@@ -870,15 +875,10 @@ static cudaError_t launch_copy(const CopyArgs& a, cudaStream_t s) {
                             : ((long long)c.page_size * c.heads + 7) / 8;
   // Up to 8 CTAs an SM.
   const long long units = per * 2 * a.layers * (a.n_max > 0 ? a.n_max : 1);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units < 1216 ? units : 1216));
-  cfg.blockDim = dim3(kCopyThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.tail.words ? 1 : 0;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg =
+      overlapped_launch(dim3((unsigned)(units < 1216 ? units : 1216)), kCopyThreads, 0, s, &attr);
+  if (!a.tail.words) cfg.numAttrs = 0;  // (a plain copy does not wait)
   return cudaLaunchKernelEx(&cfg, vec            ? pages_copy_dense_kernel
                                   : a.esize == 2 ? pages_copy_rows_kernel<uint16_t>
                                                  : pages_copy_rows_kernel<uint32_t>,
@@ -898,8 +898,9 @@ cudaError_t launch_pages_resize(const PagePool& pool, const PageMeta& m, const i
     a.copy_here = copy_vec(a.pages) ? 1 : 2;
   cudaError_t e = split_meta(&a.copy, s);
   if (e != cudaSuccess) return e;
-  pages_resize_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(kClusterCtas), kPageThreads, 0, s, &attr);
+  e = cudaLaunchKernelEx(&cfg, pages_resize_kernel, a);
   if (e != cudaSuccess || a.copy_here) return e;
   return launch_copy(a.pages, s);
 }
@@ -913,8 +914,9 @@ cudaError_t launch_pages_fork(const PagePool& pool, const PageMeta& m, const int
              (int*)(ws + w.dst)};
   cudaError_t e = split_meta(&a.copy, s);
   if (e != cudaSuccess) return e;
-  pages_fork_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(kClusterCtas), kPageThreads, 0, s, &attr);
+  e = cudaLaunchKernelEx(&cfg, pages_fork_kernel, a);
   if (e != cudaSuccess) return e;
   return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, n, pool.layer_stride, a.src, a.dst,
                               words, CopyTail{words, free_pages, m, nullptr}}, s);
@@ -927,8 +929,9 @@ cudaError_t launch_pages_compact(const PagePool& pool, const PageMeta& m, int32_
                 (int*)(ws + w.dst)};
   cudaError_t e = split_meta(&a.copy, s);
   if (e != cudaSuccess) return e;
-  pages_compact_kernel<<<kClusterCtas, kPageThreads, 0, s>>>(a);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(kClusterCtas), kPageThreads, 0, s, &attr);
+  e = cudaLaunchKernelEx(&cfg, pages_compact_kernel, a);
   if (e != cudaSuccess) return e;
   return launch_copy(CopyArgs{pool.c, pool.layers, pool.esize, m.n_pages, pool.layer_stride, a.src,
                               a.dst, words, CopyTail{words, nullptr, m, page_map}}, s);
@@ -954,18 +957,13 @@ cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new
                    (((uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)k_new | (uintptr_t)v_new) & 15u) == 0;
   int ctas = (a.n_tokens + 7) / 8;
   ctas = (ctas < 1215 ? ctas : 1215) + 1;  // (the first one for the status word)
-  if (esize == 2) {
-    if (vec)
-      cache_append_kernel<uint16_t, 8><<<ctas, 256, 0, s>>>(p);
-    else
-      cache_append_kernel<uint16_t, 1><<<ctas, 256, 0, s>>>(p);
-  } else {
-    if (vec)
-      cache_append_kernel<uint32_t, 4><<<ctas, 256, 0, s>>>(p);
-    else
-      cache_append_kernel<uint32_t, 1><<<ctas, 256, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(ctas), 256, 0, s, &attr);
+  if (esize == 2)
+    return vec ? cudaLaunchKernelEx(&cfg, cache_append_kernel<uint16_t, 8>, p)
+               : cudaLaunchKernelEx(&cfg, cache_append_kernel<uint16_t, 1>, p);
+  return vec ? cudaLaunchKernelEx(&cfg, cache_append_kernel<uint32_t, 4>, p)
+             : cudaLaunchKernelEx(&cfg, cache_append_kernel<uint32_t, 1>, p);
 }
 
 }  // namespace dspark

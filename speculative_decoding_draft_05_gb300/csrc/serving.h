@@ -95,4 +95,24 @@ struct AttnArgs {
 size_t attention_workspace_bytes(int dtype, int head_dim);
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s);
 
+// The kernels here may be launched while the one before them in the stream ends:
+// the launch, and what stands before this wait, then cost nothing.  What that
+// one wrote (and all before it) is read, and anything written, after the wait.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+inline cudaLaunchConfig_t overlapped_launch(dim3 grid, int threads, int smem, cudaStream_t s,
+                                            cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 }  // namespace dspark
