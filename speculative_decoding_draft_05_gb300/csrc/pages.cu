@@ -248,7 +248,12 @@ __device__ __forceinline__ void copy_dense(const CopyArgs& a, int n, int team, i
   const int piece = kThreads * kCopyUnroll;
   const int pieces = (vecs + piece - 1) / piece;
   const long long units = (long long)n * 2 * a.layers * pieces;
-  for (long long u = team; u < units; u += teams) {
+  // As many teams as share the units evenly: a last round that few of them had
+  // work in would leave the memory idle.
+  const long long rounds = (units + teams - 1) / teams;
+  const int used = rounds > 0 ? (int)((units + rounds - 1) / rounds) : 0;
+  if (team >= used) return;
+  for (long long u = team; u < units; u += used) {
     const int pc = (int)(u % pieces);
     long long w = u / pieces;
     const bool is_v = w & 1;
