@@ -37,14 +37,14 @@
 //     replaced by -inf, and V's rows are overwritten with zeros, since 0 x NaN of
 //     an unused cache slot would reach the sum.
 //   * What bounds it: with few rows the read of K and V (verifying, 64 requests
-//     of up to 17 tokens over 500 .. 8192 positions, 1.18 GB: 191 us, 6.1 TB/s;
-//     4 requests of 17 tokens over 100 k positions, 1.87 GB: 292 us, 6.4 TB/s;
-//     decoding, 16 requests of 200 .. 2048 positions, 85 MB: 32 us, of which 6
+//     of up to 17 tokens over 500 .. 8192 positions, 1.18 GB: 186 us, 6.3 TB/s;
+//     4 requests of 17 tokens over 100 k positions, 1.87 GB: 283 us, 6.6 TB/s;
+//     decoding, 16 requests of 200 .. 2048 positions, 85 MB: 29 us, of which 6
 //     pass before the first scores and 6 after the last); with many rows the
 //     chain of a stream, S, softmax, P V, against 1024 cycles of matrix
 //     instructions a tile: about 2850 cycles a tile of each of the two streams
-//     (prefill of 2901 + 4096 tokens at 5000 .. 8192 positions: 433 us, 1.53
-//     PFLOP/s, 81 % of a library product's rate).
+//     (prefill of 2901 + 4096 tokens at 5000 .. 8192 positions: 425 us, 1.56
+//     PFLOP/s, 83 % of a library product's rate).
 //   * Every mbarrier wait is bounded; on expiry the CTA flags
 //     DSPARK_DEV_TIMEOUT, drains what it issued, frees TMEM and returns.
 #include <cuda.h>

@@ -11,11 +11,11 @@
 // sum over the counts.
 //
 // Bounds and figures: the cluster kernels are chains of dependent reads (resize
-// of 512 requests over 40,000 pages: 11 us in a graph, 20 us a call from Python,
+// of 512 requests over 40,000 pages: 17 us in a graph, 20 us a call from Python,
 // whose host side is the longer; compact of 2000 pages 10 us); the copies and
-// the append move bytes: 240 MB of pages read and written in 78 us (6.7 TB/s),
-// 16 k new tokens of 8 x 128 (119 MB each way) in 35 us, 4.8 k tokens in 9 us,
-// four dependent look-ups behind their loads.
+// the append move bytes: 262 MB of pages read and written in 80 us (6.5 TB/s),
+// prompts of 8 k and 16 k new tokens of 8 x 128 (119 MB each way) in 37 us, 4.8 k
+// tokens of 512 requests in 7 us, four dependent look-ups behind their loads.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
