@@ -84,17 +84,24 @@ struct Layout {
   static constexpr int kOffQ = 0;  // two row blocks, or this piece's and the next one's rows
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
-  static constexpr int kOffStart = kOffMerge;                        // (before the first merge)
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
   static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1;
   static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 12 + 15) & ~15);  // PieceInfo [2]
-  static constexpr int kEnd = kOffPiece + 2 * 64;
+  // The plan has room of its own: the roles read it after the last barrier of
+  // all threads, so nothing may be written over it.
+  static constexpr int kOffStart = (kOffPiece + 2 * 64 + 15) & ~15;
+  static constexpr int kEnd = kOffStart + (int)sizeof(AttnStart<kTN>);
   // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
   // static shared memory; the slack covers most others, and the kernel checks.
   static constexpr int kBytes = kEnd + 1024 < 232448 ? kEnd + 1024 : 232448;
 };
-static_assert(Layout<128>::kEnd <= 232448, "shared memory");
-static_assert(sizeof(AttnStart<kTN>) <= 2 * 128 * 8, "the plan's scratch lies in the merge buffer");
+static_assert(Layout<64>::kEnd <= 232448 && Layout<128>::kEnd <= 232448, "shared memory");
+template <int DP>
+constexpr bool plan_apart() {  // from all that is written while roles may still read it
+  using Lo = Layout<DP>;
+  return Lo::kOffStart >= Lo::kOffMerge + 2 * 128 * 8 && Lo::kOffStart >= Lo::kOffPiece + 2 * 64;
+}
+static_assert(plan_apart<64>() && plan_apart<128>(), "the plan's room");
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
