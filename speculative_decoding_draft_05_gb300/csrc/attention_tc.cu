@@ -517,6 +517,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       uint32_t slot = 0;  // next ring slot, in the order of use
       uint32_t n = 0, steps0 = 0, steps1 = 0;  // piece, P tiles of each stream so far
       // A piece's first products overwrite O: the results of the one before are read.
+      // Every piece waits for both streams' hand-backs, also where it has products
+      // on one alone: a wait tells a phase by its parity, so no phase may be left out.
       auto wait_o_free = [&](int s, uint32_t piece) {
         if (piece == 0) return true;
         const bool r = __all_sync(0xffffffffu, mbar_wait(&o_free[s], (piece - 1) & 1u, abort_flag,
@@ -611,7 +613,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           // first product of step i + 2 follows the second of step i.
           int jq = 0;
           uint32_t iq = 0;           // steps whose first product is issued
-          uint32_t flags0 = 0, flags1 = 0;  // of the step in flight on a stream: 1 its first, 2 the piece's last
+          // Of the step in flight on a stream: 1 the stream's first of its piece, 2 the
+          // piece's last, 4 the piece's first.
+          uint32_t flags0 = 0, flags1 = 0;
           bool open = true;
           uint32_t np = n;           // the piece of the second products
           auto issue_qk = [&] {
@@ -630,7 +634,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             qk(s, n & 1, slot);
             release(slot++);
             const bool last = ++jq == nt;
-            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u);
+            (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u) | (jq == 1 ? 4u : 0u);
             if (last) tc_commit(&q_empty[n & 1], lead);
             ++iq;
           };
@@ -640,7 +644,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const int s = i & 1;
             if (!(ok = wait_full(slot) && wait_half(s))) break;
             const uint32_t f = s ? flags1 : flags0;
-            if (f & 1u && !(ok = wait_o_free(s, np))) break;
+            if (f & 4u && !(ok = wait_o_free(0, np) && wait_o_free(1, np))) break;
             if (!(ok = pv(s, slot, f & 1u))) break;
             release(slot++);
             if (f & 2u) tc_commit(&o_full[np++ & 1], lead);

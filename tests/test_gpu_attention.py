@@ -89,8 +89,34 @@ def reference(i, layer=0):
     return out, lse, tol, tol_lse
 
 
-def check(i, res, layer=0):
-    out, lse, tol, tol_lse = reference(i, layer)
+def reference_on_gpu(i):
+    """``reference`` of layer 0, a request at a time in 64 bits on the GPU (what only goes into tolerances: 32)."""
+    Hq, D, G, scale = i["Hq"], i["D"], i["Hq"] // i["Hkv"], i["scale"]
+    bf = i["k"].dtype == BF16
+    table, parts, t = i["table"].long(), [], 0
+    for r, (n, L) in enumerate(zip(i["chunks"], i["L"])):
+        pg = table[r, : -(-L // i["page"])]
+        K, V = (x[0][pg].reshape(-1, i["Hkv"], D)[:L].double().repeat_interleave(G, 1) for x in (i["k"], i["v"]))
+        q = i["q"][t:t + n].double()
+        t += n
+        pos = torch.arange(L - n, L, device="cuda")
+        see = torch.arange(L, device="cuda") <= pos[:, None, None]  # [n, 1, L]
+        s = torch.einsum("nhd,jhd->nhj", q, K) * scale
+        sa = torch.einsum("nhd,jhd->nhj", q.float().abs(), K.float().abs()) * abs(scale)
+        ds = (D + 3) * U * torch.where(see, sa, 0.0).amax(2) + 2 * U * torch.where(see, s.abs(), 0.0).amax(2)
+        s = torch.where(see, s, -math.inf)
+        lse = torch.logsumexp(s, 2)
+        pr = torch.where(see, torch.exp(s - lse[..., None].nan_to_num(neginf=0.0)), 0.0)
+        out = torch.einsum("nhj,jhd->nhd", pr, V)
+        mix = torch.einsum("nhj,jhd->nhd", pr.float(), V.float().abs())
+        sums = ((2 * pos + 16) * U)[:, None]
+        tol = (4 * ds + sums + (2.0 ** -8 if bf else 0))[..., None] * mix + (2.0 ** -8 * out.abs() if bf else 0)
+        parts.append((out, lse, tol, 2 * ds + sums + 4 * U * lse.abs()))
+    return [torch.cat(x).cpu() for x in zip(*parts)]
+
+
+def check(i, res, layer=0, want=None):
+    out, lse, tol, tol_lse = reference(i, layer) if want is None else want
     got, got_lse = res["out"].cpu().double(), res["lse"].cpu().double()
     assert not got.isnan().any()
     bad = (got - out).abs() > tol
@@ -147,6 +173,37 @@ SHAPES = [
 def test_attention_matches_the_definition(dtype, n):
     i = make(dtype, *SHAPES[n], layout="htd" if n % 2 else "thd", seed=n)
     check(i, attend(i))
+
+
+def mixed(kind):
+    """Long chunks and young requests in turn: (chunks, lens, Hq, Hkv, D, page)."""
+    g = torch.Generator().manual_seed(31)
+    young = torch.randint(5, 121, (400,), generator=g).tolist()
+    if kind == "chunks of 64, single tokens":
+        return [64, 1] * 128, sum(([900, n] for n in young[:128]), []), 32, 8, 128, 16
+    if kind == "prompts of 448, single tokens":
+        return [448, 1] * 32, sum(([448, n] for n in young[:32]), []), 32, 8, 128, 64
+    if kind == "verify chunks, all young":
+        c = [n % 17 + 1 for n in young[:256]]
+        return c, [max(a, n) for a, n in zip(c, young)], 32, 4, 128, 16
+    if kind == "one head, three kinds":
+        return [32, 9, 16] * 120, sum(([300, n, 129 + n] for n in young[:120]), []), 8, 1, 64, 16
+    # every second request has two row blocks of one tile, or one of one tile
+    return [40, 1, 1, 33] * 90, sum(([40, n, 1, 33] for n in young[:90]), []), 8, 1, 128, 8
+
+
+@pytest.mark.parametrize("kind", ["chunks of 64, single tokens", "prompts of 448, single tokens",
+                                  "verify chunks, all young", "one head, three kinds", "single tiles"])
+def test_shares_of_many_pieces_of_both_kinds(kind):
+    # A CTA's share holds a piece of two row blocks, one of a single tile and one
+    # more, in this order: the last one must not overwrite what the first one's
+    # results are still read from.
+    i = make(BF16, *mixed(kind), seed=31)
+    r = attend(i)
+    check(i, r, want=reference_on_gpu(i))
+    for _ in range(40):
+        b = attend(i, workspace=r["workspace"])
+        assert torch.equal(r["out"], b["out"]) and torch.equal(r["lse"], b["lse"])
 
 
 def test_attention_of_a_later_layer_and_given_outputs():
