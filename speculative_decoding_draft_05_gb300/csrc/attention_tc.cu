@@ -471,7 +471,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       // The page of this lane's box of tile t, as the table has it, if the item
       // has keys there.  It is checked when it is used, a tile later.
       auto has_box = [&](int t) { return e < E && t * kTN + e * bt < w.end; };
-      auto page_at = [&](int t) { return has_box(t) ? __ldg(table + (t * kTN + e * bt) / S) : -1; };
+      auto page_at = [&](int t) { return has_box(t) ? table[(t * kTN + e * bt) / S] : -1; };
       auto checked = [&](int t, int pg) {
         if (!has_box(t)) return -1;
         if (pg < 0 || pg >= p.a.c.n_pages) {

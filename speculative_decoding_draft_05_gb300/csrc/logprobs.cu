@@ -266,8 +266,8 @@ __device__ __forceinline__ void skip_row(const RowOutputs& o, int r) {
 // beside a launch and a list in memory).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 1)
-logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
-                       const int32_t* __restrict__ tokens, int n_rows, int V, int blocks,
+logprobs_stream_kernel(const T* Z, long long row_stride,
+                       const int32_t* tokens, int n_rows, int V, int blocks,
                        int groups, float c, float4* parts, float* gmax, int* rows_wanted,
                        const RowOutputs o, int* status) {
   __shared__ int sm[kRowWarps];
@@ -278,7 +278,7 @@ logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
   bool bad = false;
   // Rows without a token get their results here.
   for (int r = blockIdx.x * kRowWarps + warp; r < n_rows; r += gridDim.x * kRowWarps)
-    if (__ldg(tokens + r) < 0) skip_row(o, r);
+    if (tokens[r] < 0) skip_row(o, r);
   int listed = 0;
   // A window of rows at a time (one, up to kListRows rows).
   for (int w0 = 0; w0 < n_rows; w0 += kListRows) {
@@ -288,7 +288,7 @@ logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
     int mine = 0;
 #pragma unroll 8
     for (int r = r0; r < r1; ++r) {
-      const int tok = __ldg(tokens + w0 + r);
+      const int tok = tokens[w0 + r];
       mine += tok >= 0 ? 1 : 0;
       bad |= tok >= V;
     }
@@ -296,7 +296,7 @@ logprobs_stream_kernel(const T* __restrict__ Z, long long row_stride,
     int k = block_scan(mine, sm, &n);
 #pragma unroll 8
     for (int r = r0; r < r1; ++r)
-      if (__ldg(tokens + w0 + r) >= 0) list[k++] = (uint16_t)r;
+      if (tokens[w0 + r] >= 0) list[k++] = (uint16_t)r;
     __syncthreads();
     if (blockIdx.x == 0)  // the second kernel's list: [0] how many, then the rows
       for (int i = threadIdx.x; i < n; i += kRowThreads) rows_wanted[1 + listed + i] = w0 + list[i];
@@ -599,8 +599,8 @@ __device__ __forceinline__ void finish_row(const T* row, int r, float x_tok, int
 // CTA's warps would have none).
 template <typename T>
 __global__ void __launch_bounds__(kFinishWarps * 32, kFinishCtas)
-logprobs_finish_kernel(const T* __restrict__ Z, long long row_stride,
-                       const int32_t* __restrict__ tokens, int V, int blocks, int groups, float c,
+logprobs_finish_kernel(const T* Z, long long row_stride,
+                       const int32_t* tokens, int V, int blocks, int groups, float c,
                        float invT, const float4* parts, float* gmax, const int* rows_wanted,
                        const RowOutputs o) {
   __shared__ RowScratch scratch[kFinishWarps];
@@ -610,7 +610,7 @@ logprobs_finish_kernel(const T* __restrict__ Z, long long row_stride,
   if (i >= __ldcg(rows_wanted)) return;
   float* gm = gmax + (size_t)r * groups;
   const float4* part = parts + (size_t)r * blocks;
-  const int tok = __ldg(tokens + r);
+  const int tok = tokens[r];
   GroupTile tile;
   tile.load(gm, 0, groups);
   const T* row = Z + (long long)r * row_stride;
@@ -639,20 +639,20 @@ logprobs_finish_kernel(const T* __restrict__ Z, long long row_stride,
 // Short rows: sums and results by the same warp, in one launch.
 template <typename T>
 __global__ void __launch_bounds__(kFinishWarps * 32)
-logprobs_short_kernel(const T* __restrict__ Z, long long row_stride,
-                      const int32_t* __restrict__ tokens, int n_rows, int V, int groups, float c,
+logprobs_short_kernel(const T* Z, long long row_stride,
+                      const int32_t* tokens, int n_rows, int V, int groups, float c,
                       float invT, float* gmax, const RowOutputs o, int* status) {
   __shared__ RowScratch scratch[kFinishWarps];
   const int warp = threadIdx.x >> 5, r = blockIdx.x * kFinishWarps + warp;
   wait_for_previous();
   if (blockIdx.x == 0) {  // the status word, from all tokens
     bool bad = false;
-    for (int i = threadIdx.x; i < n_rows; i += kFinishWarps * 32) bad |= __ldg(tokens + i) >= V;
+    for (int i = threadIdx.x; i < n_rows; i += kFinishWarps * 32) bad |= tokens[i] >= V;
     const int any = __syncthreads_or(bad);
     if (threadIdx.x == 0) *status = any ? DSPARK_DEV_BAD_INPUT : 0;
   }
   if (r >= n_rows) return;
-  const int tok = __ldg(tokens + r);
+  const int tok = tokens[r];
   if (tok < 0) {
     skip_row(o, r);
     return;

@@ -97,7 +97,10 @@ cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s);
 
 // The kernels here may be launched while the one before them in the stream ends:
 // the launch, and what stands before this wait, then cost nothing.  What that
-// one wrote (and all before it) is read, and anything written, after the wait.
+// one wrote (and all before it) is read, and anything written, after the wait,
+// and never by the non-coherent path (__ldg, const __restrict__ parameters): that
+// asks for data that nothing writes while the kernel runs, which it does before
+// the wait too.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

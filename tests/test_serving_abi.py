@@ -122,3 +122,18 @@ def test_logprobs(lib):
     for kw in (dict(ws=None), dict(ws=64), dict(wsb=256)):
         assert call(**kw) == 3, kw
     assert lib.dspark_logprobs_workspace_bytes(0, 8) == 0 and lib.dspark_logprobs_workspace_bytes(1, 8) >= 256
+
+
+def test_serving_kernels_read_nothing_by_the_non_coherent_path():
+    # They may start while the kernel before them still writes what they read.
+    import os
+    import re
+
+    from speculative_decoding_draft_05_gb300 import build
+
+    for name in ("attention.cu", "attention.cuh", "attention_tc.cu", "logprobs.cu", "pages.cu"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert "griddepcontrol" in code or "wait_for_previous" in code or name.endswith(".cuh"), name
+        for word in ("__ldg", "__restrict__", "ld.global.nc"):
+            assert word not in code, (name, word)
