@@ -411,8 +411,9 @@ int dspark_verify_noalloc(const int32_t* x, const float* logp, const float* lse,
  * refcount[p] is the number of requests whose tables hold page p (0: free).
  *
  * Limits (else DSPARK_ERR_UNSUPPORTED): R <= 65535, heads <= 1024, head_dim <=
- * 256, page_size <= 65536, page_size * heads * head_dim <= 2^30, R * max_pages
- * < 2^31; kv_len counts positions and is at most max_pages * page_size.
+ * 256, page_size <= 65536, n_pages <= 2^31 - 2^16, page_size * heads * head_dim <=
+ * 2^30, R * max_pages < 2^31; kv_len counts positions and is at most max_pages * page_size, and at most
+ * 2^31 - 2^16 (a longer one is flagged and clamped).
  * ======================================================================== */
 typedef struct {
   void* k; /* DEVICE: page 0 of layer 0 */

@@ -27,9 +27,9 @@ int check_cache(const dspark_cache* c, int layer) {
     return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(c->dtype) - 1);
   if (((uintptr_t)c->k & a) || ((uintptr_t)c->v & a)) return DSPARK_ERR_INVALID_ARG;
-  if (c->head_dim > 256 || c->heads > 1024 || c->page_size > 65536 ||
+  if (c->head_dim > 256 || c->heads > 1024 || c->page_size > 65536 || c->n_pages > kMaxPositions ||
       (long long)c->page_size * c->heads * c->head_dim > (1ll << 30))
-    return unsupported("head_dim <= 256, heads <= 1024, page_size <= 65536, 2^30 elements a page");
+    return unsupported("head_dim <= 256, heads <= 1024, page_size <= 65536, n_pages <= 2^31 - 2^16, 2^30 elements a page");
   return DSPARK_OK;
 }
 

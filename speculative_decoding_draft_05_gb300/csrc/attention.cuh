@@ -77,8 +77,7 @@ __device__ __forceinline__ AttnRequest attn_request(const ChunkArgs& a, int page
                                                     int* status) {
   AttnRequest q;
   int b = a.q_offsets[r], e = a.q_offsets[r + 1], L = a.kv_len[r];
-  const long long most_l = (long long)a.max_pages * page_size;
-  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  const int most = most_positions(a.max_pages, page_size);
   if (b < 0 || e < b || e > a.n_tokens || L < 0 || L > most) {
     flag_status(status, DSPARK_DEV_BAD_INPUT);
     b = b < 0 ? 0 : b > a.n_tokens ? a.n_tokens : b;

@@ -37,7 +37,8 @@ constexpr int kPageWarps = kPageThreads / 32;
 // copies, and the free pages without those.
 enum { kWordStatus = 0, kWordCopies = 1, kWordFree = 2, kWordFlags = 8, kWordFreed = 16 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (a: a length, at most kMaxPositions, or a number of pages, at most as much)
+__device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + b - 1) / b); }
 
 __device__ __forceinline__ int warp_sum_int(int v) {
 #pragma unroll
@@ -79,7 +80,7 @@ __device__ __forceinline__ int block_scan_excl(int v, int* sm, int* total) {
 __device__ __forceinline__ void page_share(int n_pages, int rank, int& lo, int& hi) {
   const int warps = kClusterCtas * kPageWarps;
   const int per = ceil_div(ceil_div(n_pages, warps), 32) * 32;
-  const long long a = (long long)(rank * kPageWarps + (threadIdx.x >> 5)) * per;
+  const long long a = (long long)(rank * kPageWarps + (int)(threadIdx.x >> 5)) * per;
   lo = a < n_pages ? (int)a : n_pages;
   hi = a + per < n_pages ? (int)(a + per) : n_pages;
 }
@@ -211,8 +212,7 @@ __device__ __forceinline__ int copy_begin(const CopyArgs& a) {
   if (t.page_map) {
     const PageMeta& m = t.m;
     const size_t n = (size_t)m.R * m.max_pages;
-    const long long most_l = (long long)m.max_pages * m.page_size;
-    const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+    const int most = most_positions(m.max_pages, m.page_size);
     for (size_t i = (size_t)blockIdx.x * kCopyThreads + threadIdx.x; i < n;
          i += (size_t)gridDim.x * kCopyThreads) {
       const int r = (int)(i / m.max_pages), j = (int)(i - (size_t)r * m.max_pages);
@@ -332,8 +332,7 @@ pages_resize_kernel(const ResizeArgs a) {
   const int gwarp = rank * kPageWarps + (threadIdx.x >> 5), warps = kClusterCtas * kPageWarps;
   const PageMeta& m = a.m;
   const int S = m.page_size, P = m.max_pages;
-  const long long most_l = (long long)P * S;
-  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  const int most = most_positions(P, S);
   int* const rc = m.refcount_out;
   int* const status = &flags;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -511,8 +510,7 @@ pages_fork_kernel(const ForkArgs a) {
   const int gwarp = rank * kPageWarps + (threadIdx.x >> 5), warps = kClusterCtas * kPageWarps;
   const PageMeta& m = a.m;
   const int S = m.page_size, P = m.max_pages;
-  const long long most_l = (long long)P * S;
-  const int most = most_l > 0x7fffffffll ? 0x7fffffff : (int)most_l;
+  const int most = most_positions(P, S);
   int* const rc = m.refcount_out;
   int* const status = &flags;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -755,9 +753,9 @@ __device__ __forceinline__ void append_status(const AppendArgs& p) {
         const long long base = (long long)L - e;  // a token's position less its number
         bad |= base + t0 < 0;
         s0 = base + t0 < 0 ? 0 : (base + t0) / S;
-        s1 = base + t1 - 1 < 0 ? -1 : (base + t1 - 1) / S;
-        bad |= s1 >= p.a.max_pages;
-        s1 = s1 < p.a.max_pages ? s1 : p.a.max_pages - 1;
+        const long long last = base + t1 - 1, most = most_positions(p.a.max_pages, S);
+        bad |= last >= most;
+        s1 = last < 0 ? -1 : (last < most ? last : most - 1) / S;
       }
     }
 #pragma unroll
@@ -811,7 +809,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
     const long long pos = (long long)p.a.kv_len[r] - end + t;
     const long long slot = pos / S;
     int page = -1;
-    if (t >= p.a.q_offsets[r] && t < end && pos >= 0 && slot < p.a.max_pages)
+    if (t >= p.a.q_offsets[r] && t < end && pos >= 0 && pos < most_positions(p.a.max_pages, S))
       page = p.a.page_table[(size_t)r * p.a.max_pages + slot];
     if (page < 0 || page >= p.c.n_pages) continue;  // flagged by CTA 0, or padding
     const long long dst0 = page * p.c.page_stride + (pos - slot * S) * p.c.token_stride;

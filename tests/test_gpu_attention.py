@@ -350,7 +350,52 @@ def test_bad_device_inputs_are_flagged_and_stay_in_bounds():
     assert status() == 0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_a_request_of_2_to_the_31_positions(dtype):
+    # The longest request there is, 2^31 - 2^16 positions, whose table names one
+    # page of 65,536 again and again: 32,767 times its keys, so the same
+    # probabilities over it.  Chains of sums: l adds 2^26 / 304 tiles of 32 keys
+    # a lane (bf16: 2^24 / 152 / 2 tiles of 64 pairs), out 2^31 / 304 keys one
+    # after another (bf16: 8 products a tile, truncated at 2^-23).
+    longest = 2 ** 31 - 2 ** 16
+    i = make(dtype, [1], [65536], 2, 1, 16, 65536, seed=33, poison=False)
+    i["table"] = torch.full((1, 32768), int(i["table"][0, 0]), dtype=torch.int32, device="cuda")
+    cache = dspark.PagedCache(i["k"], i["v"])
+
+    def call(L):
+        r = dspark.dspark_paged_attention(i["q"], cache, 0, i["off"], torch.tensor([L], dtype=torch.int32, device="cuda"),
+                                          i["table"], i["scale"])
+        return r, dspark.dspark_read_device_status(r["workspace"])
+
+    want, lse, tol, tol_lse = reference(i)
+    lse = lse + math.log(longest // 65536)
+    r, status = call(longest)
+    assert status == 0
+    chain = (2 ** 31 / 304 * U) if dtype == F32 else 2 ** 24 / 152 * 8 * 2 * U
+    mix = 1.0  # sum p |v| of normal values: 0.8
+    assert ((r["out"].cpu().double() - want).abs() <= tol + chain * mix).all()
+    assert ((r["lse"].cpu().double() - lse).abs() <= tol_lse + 2 ** 26 / 304 * U + 4 * U * lse.abs()).all()
+    for L in (longest + 1, 2 ** 31 - 1):
+        b, status = call(L)
+        assert status == 1 and torch.equal(b["out"], r["out"])  # clamped
+
+
 # ------------------------------------------------------------------ append
+@pytest.mark.parametrize("L", [2 ** 31 - 2 ** 16, 2 ** 31 - 2 ** 16 + 1, 2 ** 31 - 1])
+def test_append_at_the_last_positions(L):
+    i = make(BF16, [2], [2], 2, 2, 8, 65536, seed=34, poison=False, spare=1)
+    k0, longest = i["k"].clone(), 2 ** 31 - 2 ** 16
+    table = torch.full((1, 32768), 1, dtype=torch.int32, device="cuda")
+    kn, vn = i["qkv"][:, 2:4], i["qkv"][:, 4:]
+    r = dspark.dspark_cache_append(dspark.PagedCache(i["k"], i["v"]), 0, kn, vn, i["off"],
+                                   torch.tensor([L], dtype=torch.int32, device="cuda"), table)
+    assert dspark.dspark_read_device_status(r["workspace"]) == (0 if L <= longest else 1)
+    for a, p in enumerate((L - 2, L - 1)):
+        if p < longest:
+            k0[0, 1, p % 65536] = kn[a]
+    assert torch.equal(i["k"], k0)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("layout", ["thd", "htd"])
 @pytest.mark.parametrize("chunks,lens,Hkv,D,page", [

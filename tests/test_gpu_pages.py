@@ -293,6 +293,29 @@ def test_bad_device_inputs_are_flagged():
     assert status(r) == BAD
 
 
+LONGEST = 2 ** 31 - 2 ** 16  # positions of a request
+
+
+@pytest.mark.parametrize("want,status", [(LONGEST, NO_PAGES), (LONGEST + 1, NO_PAGES | BAD), (2 ** 31 - 1, NO_PAGES | BAD)])
+def test_lengths_near_2_to_the_31(want, status):
+    # 65,536 positions a page: a table of 32,768 entries holds 2^31
+    p = Pool(2, 32768, 5, 65536, Hkv=1, D=8, layers=1)
+    t, n, c = p.dev()
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for L in (0, 7):
+        # the first request takes two pages, the second one all that are left
+        a = dspark.dspark_pages_resize(p.cache, t, i(0, 0), i(70000, L), c)
+        b = dspark.dspark_pages_resize(p.cache, a["page_table"], a["kv_len"], i(70000, want), a["refcount"])
+        assert dspark.dspark_read_device_status(b["workspace"]) == status
+        assert b["kv_len"].tolist() == [70000, 3 * 65536] and b["free_pages"].item() == 0
+        assert b["page_table"][:, :4].tolist() == [[0, 1, -1, -1], [2, 3, 4, -1]]
+        assert (b["page_table"][:, 4:] == -1).all() and b["refcount"].tolist() == [1] * 5
+        # ... and gives them back
+        e = dspark.dspark_pages_resize(p.cache, b["page_table"], b["kv_len"], i(0, 0), b["refcount"])
+        assert dspark.dspark_read_device_status(e["workspace"]) == 0
+        assert (e["page_table"] == -1).all() and e["free_pages"].item() == 5
+
+
 @pytest.mark.parametrize("layout", ["thd", "htd"])
 @pytest.mark.parametrize("dtype,S,Hkv,D,layers", [(BF16, 16, 8, 128, 3), (F32, 4, 2, 64, 1), (BF16, 3, 2, 5, 2),
                                                   (F32, 1, 1, 1, 1), (BF16, 64, 1, 128, 2)])

@@ -137,3 +137,7 @@ def test_serving_kernels_read_nothing_by_the_non_coherent_path():
         assert "griddepcontrol" in code or "wait_for_previous" in code or name.endswith(".cuh"), name
         for word in ("__ldg", "__restrict__", "ld.global.nc"):
             assert word not in code, (name, word)
+
+
+def test_a_pool_of_more_pages_than_their_numbers_can_be_rounded(lib):
+    assert attention(lib, cache(n_pages=0x7fff0001)) == 2
