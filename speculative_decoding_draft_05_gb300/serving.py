@@ -103,9 +103,16 @@ def _stream(dev, stream) -> int:
 
 
 def _new(shape, dtype, dev, stream):
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:  # allocated on the current stream, used on another
-        t.record_stream(stream)
+    """A tensor for the launch stream: of that stream's memory, since a block of the current stream's
+    may still be in use there by work launched before it was freed.  The current stream, where the
+    caller mostly reads it, is recorded as a user."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    current = torch.cuda.current_stream(dev)
+    if current != stream:
+        t.record_stream(current)
     return t
 
 
