@@ -732,9 +732,11 @@ __device__ __forceinline__ int find_request(const int32_t* off, int R, int t) {
   return lo;
 }
 
-// Whether any new token has no place in the cache, by one CTA, request by
-// request (a request a thread, its further pages by the warp): the status word, which so needs no clearing before the launch (a
-// launch of its own cost 2 of 12 us for 512 requests).
+// Whether any new token has no place in the cache, or an offset lies past the
+// rows given (the positions counted for them stay unwritten), by one CTA, request
+// by request (a request a thread, its further pages by the warp): the status word,
+// which so needs no clearing before the launch (a launch of its own cost 2 of 12
+// us for 512 requests).
 __device__ __forceinline__ void append_status(const AppendArgs& p) {
   const int lane = threadIdx.x & 31, S = p.c.page_size;
   bool bad = false;
@@ -747,7 +749,7 @@ __device__ __forceinline__ void append_status(const AppendArgs& p) {
     long long s0 = 0, s1 = -1;  // the pages that its tokens go to
     if (r < p.a.R) {
       const int b = p.a.q_offsets[r], e = p.a.q_offsets[r + 1], L = p.a.kv_len[r];
-      bad |= b > e || (r == 0 && b != 0);
+      bad |= b > e || e > p.a.n_tokens || (r == 0 && b != 0);
       const int t0 = b < 0 ? 0 : b, t1 = e < p.a.n_tokens ? e : p.a.n_tokens;
       if (t0 < t1) {
         const long long base = (long long)L - e;  // a token's position less its number
@@ -951,7 +953,6 @@ cudaError_t launch_pages_copy(const PagePool& pool, const int32_t* src, const in
 cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new, const void* v_new,
                                 long long new_token_stride, long long new_head_stride,
                                 const ChunkArgs& a, int* status, cudaStream_t s) {
-  if (a.n_tokens == 0) return cudaMemsetAsync(status, 0, sizeof(int), s);
   AppendArgs p{c, a, k_new, v_new, new_token_stride, new_head_stride, status};
   const int ve = 16 / esize;
   const bool vec = c.head_dim % ve == 0 && c.page_stride % ve == 0 && c.token_stride % ve == 0 &&
@@ -959,7 +960,7 @@ cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new
                    new_head_stride % ve == 0 &&
                    (((uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)k_new | (uintptr_t)v_new) & 15u) == 0;
   int ctas = (a.n_tokens + 7) / 8;
-  ctas = (ctas < 1215 ? ctas : 1215) + 1;  // (the first one for the status word)
+  ctas = (ctas < 1215 ? ctas : 1215) + 1;  // (the first one for the status word: also without tokens)
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = overlapped_launch(dim3(ctas), 256, 0, s, &attr);
   if (esize == 2)

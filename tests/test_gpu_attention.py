@@ -463,6 +463,27 @@ def test_append_flags_any_page_out_of_range(chunks, lens):
         assert status(t) == 0, r
 
 
+def test_append_flags_offsets_past_the_rows():
+    # the requests' positions would be counted, and never written
+    i = make(BF16, [2, 3], [40, 60], 2, 2, 64, 16, seed=35, poison=False)
+    cache = dspark.PagedCache(i["k"], i["v"])
+    kn, vn = i["qkv"][:, 2:4], i["qkv"][:, 4:]
+
+    def status(*off):
+        r = dspark.dspark_cache_append(cache, 0, kn, vn, torch.tensor(off, dtype=torch.int32, device="cuda"), i["lens"],
+                                       i["table"])
+        return dspark.dspark_read_device_status(r["workspace"])
+
+    assert status(0, 2, 5) == 0 and status(0, 2, 4) == 0
+    assert status(0, 2, 6) == 1 and status(0, 2, 9) == 1     # the last one
+    assert status(0, 6, 6) == 1 and status(0, 6, 7) == 1     # one before it
+    assert status(0, 9, 5) == 1 and status(0, -1, 5) == 1
+    none = kn[:0]
+    r = dspark.dspark_cache_append(cache, 0, none, none, torch.tensor([0, 0, 1], dtype=torch.int32, device="cuda"),
+                                   i["lens"], i["table"])
+    assert dspark.dspark_read_device_status(r["workspace"]) == 1
+
+
 def test_append_of_unaligned_rows():
     # rows that start one element off a 16-byte boundary, and a pool that does
     for dtype in (F32, BF16):
