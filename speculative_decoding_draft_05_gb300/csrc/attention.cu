@@ -471,7 +471,6 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
-  if (a.a.n_tokens == 0) return cudaMemsetAsync(ws, 0, sizeof(int), s);
   if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),

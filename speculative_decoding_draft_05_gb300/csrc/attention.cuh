@@ -78,7 +78,7 @@ __device__ __forceinline__ AttnRequest attn_request(const ChunkArgs& a, int page
   AttnRequest q;
   int b = a.q_offsets[r], e = a.q_offsets[r + 1], L = a.kv_len[r];
   const int most = most_positions(a.max_pages, page_size);
-  if (b < 0 || e < b || e > a.n_tokens || L < 0 || L > most) {
+  if (b < 0 || e < b || e > a.n_tokens || L < 0 || L > most || (r == 0 && b != 0)) {
     flag_status(status, DSPARK_DEV_BAD_INPUT);
     b = b < 0 ? 0 : b > a.n_tokens ? a.n_tokens : b;
     e = e < b ? b : e > a.n_tokens ? a.n_tokens : e;

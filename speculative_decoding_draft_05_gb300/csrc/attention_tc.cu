@@ -1152,11 +1152,13 @@ cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& 
 }  // namespace
 
 // The tensor-core kernel takes bf16 with head_dim a multiple of 8 up to 128 (two
-// 64-column halves of 128-byte rows), pages of 2^k >= 8 tokens (whole
-// 8-row swizzle groups; a power of two divides the 128-key tile or is a multiple of it), and what TMA asks
-// of addresses and strides (16 bytes).
+// 64-column halves of 128-byte rows), pages of any multiple of 8 tokens (whole
+// 8-row swizzle groups: a box is the largest power of two in the page size, up to
+// the 128 keys of a tile), and what TMA asks of addresses and strides (16 bytes).
+// (A call without tokens, which only checks its offsets, needs no map of q.)
 bool attention_tc_supported(const AttnArgs& a) {
   const CacheView& c = a.c;
+  if (a.a.n_tokens == 0) return false;
   if (a.dtype != DSPARK_BF16 || c.head_dim % 8 != 0 || c.head_dim > 128) return false;
   if (c.page_size % 8 != 0) return false;  // (a tile is at most 16 boxes of 8 tokens, two halves each)
   if (((uintptr_t)c.k | (uintptr_t)c.v) & 15u) return false;

@@ -380,6 +380,26 @@ def test_a_request_of_2_to_the_31_positions(dtype):
         assert status == 1 and torch.equal(b["out"], r["out"])  # clamped
 
 
+def test_offsets_that_do_not_start_at_zero_are_flagged():
+    # rows before the first offset belong to no request and get no result
+    for dtype in (F32, BF16):
+        i = make(dtype, [2, 3], [40, 60], 8, 2, 64, 16, seed=36)
+        cache = dspark.PagedCache(i["k"], i["v"])
+        for off, want in (([1, 2, 5], 1), ([2, 2, 5], 1), ([0, 0, 5], 0), ([0, 2, 4], 0)):
+            r = dspark.dspark_paged_attention(i["q"], cache, 0, torch.tensor(off, dtype=torch.int32, device="cuda"),
+                                              i["lens"], i["table"], i["scale"])
+            assert dspark.dspark_read_device_status(r["workspace"]) == want, off
+
+
+def test_no_rows_and_offsets_past_them_are_flagged():
+    i = make(BF16, [2, 3], [40, 60], 8, 2, 64, 16, seed=37)
+    cache = dspark.PagedCache(i["k"], i["v"])
+    for off, want in (([0, 0, 0], 0), ([0, 0, 1], 1)):
+        r = dspark.dspark_paged_attention(i["q"][:0], cache, 0, torch.tensor(off, dtype=torch.int32, device="cuda"),
+                                          i["lens"], i["table"], i["scale"])
+        assert dspark.dspark_read_device_status(r["workspace"]) == want, off
+
+
 # ------------------------------------------------------------------ append
 @pytest.mark.parametrize("L", [2 ** 31 - 2 ** 16, 2 ** 31 - 2 ** 16 + 1, 2 ** 31 - 1])
 def test_append_at_the_last_positions(L):
