@@ -283,11 +283,8 @@ def dspark_logprobs(Z, tokens, temperature: float = 1.0, top: int = 0, *, logp=N
     n = tokens.numel()
     if Z.stride(-1) != 1:
         raise ValueError("Z: the vocabulary must be contiguous")
-    if n == 1 or Z.is_contiguous():
-        step = V
-    elif Z.dim() == 2 or _even(Z):
-        step = Z.stride(-2)
-    else:
+    step = _row_step(Z)
+    if step is None:
         raise ValueError("Z: the leading dimensions must step evenly")
     logp, p0 = _out(logp, "logp", lead, _F32, dev, stream)
     entropy, p1 = _out(entropy, "entropy", lead, _F32, dev, stream)
@@ -305,11 +302,17 @@ def dspark_logprobs(Z, tokens, temperature: float = 1.0, top: int = 0, *, logp=N
     return dict(logp=logp, entropy=entropy, lse=lse, top_ids=top_ids, top_logp=top_logp, workspace=ws)
 
 
-def _even(Z) -> bool:
-    """Whether Z's rows (all but the last dimension) lie one fixed step apart."""
-    step = Z.stride(-2)
-    for i in range(Z.dim() - 3, -1, -1):
-        step *= Z.shape[i + 1]
-        if Z.stride(i) != step:
-            return False
-    return True
+def _row_step(Z):
+    """Elements from a row of Z (all but the last dimension) to the next; None: they do not step evenly."""
+    if Z.is_contiguous():
+        return Z.shape[-1]
+    step = want = None
+    for n, s in zip(Z.shape[-2::-1], Z.stride()[-2::-1]):
+        if n == 1:  # its stride carries no meaning
+            continue
+        if step is None:
+            step = s
+        elif s != want:
+            return None
+        want = s * n
+    return Z.shape[-1] if step is None else step

@@ -55,6 +55,18 @@ def close(got, want, tol, what):
     assert err.numel() == 0 or err.max() <= tol, f"{what}: {err.max():.3g} > {tol:.3g}"
 
 
+@pytest.mark.parametrize("V", [1024, 9000])
+def test_one_row_of_each_request(V):
+    # [R, 1, V] of a wider array: the rows step evenly, the stride of the dimension of one says nothing
+    Z = torch.randn(6, 4, V, generator=torch.Generator().manual_seed(41)).cuda()
+    tok = torch.tensor([[3], [-1], [7], [0], [V - 1], [9]], dtype=torch.int32, device="cuda")
+    a, b = run(Z[:, 2:3], tok, top=3), run(Z[:, 2:3].contiguous(), tok, top=3)
+    for key in ("logp", "entropy", "lse", "top_ids", "top_logp"):
+        assert torch.equal(a[key].nan_to_num(9.0), b[key].nan_to_num(9.0)), key
+    with pytest.raises(ValueError):
+        run(Z[:, :2], torch.zeros(6, 2, dtype=torch.int32, device="cuda"))
+
+
 def run(Z, tokens, T=1.0, top=0, status=0, **kw):
     r = dspark.dspark_logprobs(Z, tokens, T, top, **kw)
     assert dspark.dspark_read_device_status(r["workspace"], kw.get("stream")) == status

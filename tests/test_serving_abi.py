@@ -124,6 +124,24 @@ def test_logprobs(lib):
     assert lib.dspark_logprobs_workspace_bytes(0, 8) == 0 and lib.dspark_logprobs_workspace_bytes(1, 8) >= 256
 
 
+def test_rows_that_step_evenly():
+    import torch
+
+    from speculative_decoding_draft_05_gb300.serving import _row_step
+
+    Z = torch.empty(5, 7, 16)
+    V = 16
+    assert _row_step(Z) == V and _row_step(Z[0]) == V and _row_step(Z[0, 0]) == V
+    assert _row_step(Z[:, :1]) == 7 * V and _row_step(Z[:, 3:4]) == 7 * V   # a dimension of one: its stride says nothing
+    assert _row_step(Z[1:2]) == V and _row_step(Z[:1, ::2]) == 2 * V
+    assert _row_step(Z[:, 0]) == 7 * V and _row_step(Z[2:3, 1:2]) == V
+    assert _row_step(Z.view(5, 1, 7, 16)[:, :, :1]) == 7 * V
+    assert _row_step(torch.empty(5, 7, 24)[..., :16]) == 24
+    assert _row_step(Z[:, :6]) is None and _row_step(Z.transpose(0, 1)) is None
+    assert _row_step(torch.empty(2, 3, 4, 16)[:, :, :2]) is None
+    assert _row_step(torch.empty(2, 3, 4, 16)[:, ::3, ::4]) == 3 * 4 * V
+
+
 def test_serving_kernels_read_nothing_by_the_non_coherent_path():
     # They may start while the kernel before them still writes what they read.
     import os
