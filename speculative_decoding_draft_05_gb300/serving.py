@@ -26,6 +26,15 @@ class _CacheStruct(ctypes.Structure):
         [(n, ctypes.c_longlong) for n in ("layer_stride", "page_stride", "token_stride", "head_stride")]
 
 
+def _strides(t):
+    """Strides, those of dimensions of one, which carry no meaning, as those of an array without gaps."""
+    out, dense = [], 1
+    for n, s in zip(reversed(t.shape), reversed(t.stride())):
+        out.append(dense if n == 1 else s)
+        dense = (dense if n == 1 else s) * n
+    return out[::-1]
+
+
 class PagedCache:
     """K and V of all layers as pages: ``k``, ``v`` [layers, n_pages, page_size, heads, head_dim]
     (float32 or bfloat16) with any strides, the same for both, and head_dim contiguous.  A pool
@@ -39,14 +48,12 @@ class PagedCache:
                 raise ValueError(f"{name} must be [layers, n_pages, page_size, heads, head_dim], got {tuple(t.shape)}")
             if t.stride(4) != 1 and t.shape[4] > 1:
                 raise ValueError(f"{name}: head_dim must be contiguous")
-        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.device != v.device:
+        if k.shape != v.shape or k.dtype != v.dtype or _strides(k) != _strides(v) or k.device != v.device:
             raise ValueError("k and v must agree in shape, dtype, strides and device")
         self.k, self.v = k, v
         self.layers, self.n_pages, self.page_size, self.heads, self.head_dim = k.shape
         self.dtype, self.device = k.dtype, k.device
-        # the stride of a dimension of size 1 carries no meaning; the library wants it positive
-        st = [max(1, s) if n == 1 else s for s, n in zip(k.stride(), k.shape)]
-        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _dtype_code(k), *k.shape, *st[:4])
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _dtype_code(k), *k.shape, *_strides(k)[:4])
         self.ref = ctypes.byref(self.struct)
         self.attention_bytes = None  # workspace of dspark_paged_attention, once asked for
 
@@ -94,7 +101,9 @@ def _rows(t, name, dtype, heads, dim, dev):
         raise ValueError(f"{name}: the head dimension must be contiguous")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    return t.data_ptr(), st[0], st[1]
+    # (the stride of a dimension of one carries no meaning)
+    hs = dim if t.shape[1] == 1 else st[1]
+    return t.data_ptr(), (t.shape[1] * hs if t.shape[0] <= 1 else st[0]), hs
 
 
 def _stream(dev, stream) -> int:

@@ -524,6 +524,26 @@ def test_append_of_unaligned_rows():
         check(i, attend(i))
 
 
+def test_strides_of_dimensions_of_one():
+    # they say nothing, so they need not agree: pools of one layer cut from arrays
+    # of different depth, one head, one page, and a single new token
+    for Hkv, lens in ((2, [20]), (1, [9])):
+        i = make(BF16, [1], lens, 4, Hkv, 64, 16, seed=38, spare=0)
+        v = torch.empty(3, *i["v"].shape[1:], dtype=BF16, device="cuda")[::3]
+        v.copy_(i["v"])
+        assert v.stride() != i["k"].stride()
+        j = dict(i, v=v)
+        check(i, attend(j))
+        kn = i["qkv"][:, 4:4 + Hkv]                                   # token stride of the projection
+        vn = torch.randn(1, Hkv, 64, device="cuda").bfloat16()        # and of an array of its own
+        assert kn.stride() != vn.stride()
+        r = dspark.dspark_cache_append(dspark.PagedCache(i["k"], v), 0, kn, vn, i["off"], i["lens"], i["table"])
+        assert dspark.dspark_read_device_status(r["workspace"]) == 0
+        p = lens[0] - 1
+        pg = int(i["table"][0, p // 16])
+        assert torch.equal(i["k"][0, pg, p % 16], kn[0]) and torch.equal(v[0, pg, p % 16], vn[0])
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals():
     i = make(BF16, [2, 3], [40, 60], 8, 2, 128, 16, seed=7)
