@@ -545,7 +545,8 @@ int dspark_pages_copy(const dspark_cache* cache, const int32_t* src, const int32
  * Masked ids (-inf) have probability 0 and come last among the alternatives,
  * with logp -inf; a row of nothing but -inf gives lse = -inf and NaN
  * otherwise.  NaN or +inf in a row makes lse, logp and entropy NaN; NaN ranks as -inf.
- * Limits: 8 <= V <= 2^30, V % 8 == 0, 0 <= top <= min(32, V).
+ * Limits: 8 <= V <= 2^30, V % 8 == 0, 0 <= top <= min(32, V); T with a finite
+ * log2(e) / T (from 4.3e-39).
  * workspace: >= dspark_logprobs_workspace_bytes(n_rows, V) bytes, 256-byte
  *   aligned.
  * ---------------------------------------------------------------------- */

@@ -11,6 +11,8 @@ using namespace dspark;
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;  // the kernels' exponentials are powers of two
+
 int check_workspace(const void* ws, size_t have, size_t need) {
   return !ws || have < need || ((uintptr_t)ws & 255u) ? DSPARK_ERR_WORKSPACE : DSPARK_OK;
 }
@@ -114,7 +116,7 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
   if (!q_offsets || !kv_len || !page_table) return DSPARK_ERR_INVALID_ARG;
   if (n_tokens != 0 && (!q || !out || !lse)) return DSPARK_ERR_INVALID_ARG;
   if (n_tokens < 0 || q_token_stride < 0 || q_head_stride < 0) return DSPARK_ERR_INVALID_ARG;
-  if (Hq <= 0 || Hq % cache->heads != 0 || !isfinite(scale)) return DSPARK_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % cache->heads != 0 || !isfinite(scale * kLog2e)) return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(cache->dtype) - 1);
   if (((uintptr_t)q & a) || ((uintptr_t)out & 15u)) return DSPARK_ERR_INVALID_ARG;
   st = check_tables(R, max_pages);
@@ -229,7 +231,8 @@ int dspark_logprobs(const void* Z, int dtype, long long row_stride, const int32_
   if (!Z || !tokens || !logp || !entropy || !lse) return DSPARK_ERR_INVALID_ARG;
   if (top < 0 || (top > 0 && (!top_ids || !top_logp))) return DSPARK_ERR_INVALID_ARG;
   if (n_rows <= 0 || V <= 0 || row_stride < V) return DSPARK_ERR_INVALID_ARG;
-  if (!(temperature > 0.0f) || !isfinite(temperature)) return DSPARK_ERR_INVALID_ARG;
+  if (!(temperature > 0.0f) || !isfinite(temperature) || !isfinite(1.0f / temperature * kLog2e))
+    return DSPARK_ERR_INVALID_ARG;
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARG;
   if (V % 8 != 0 || V > (1 << 30) || top > 32 || top > V)
     return unsupported("V % 8 == 0, V <= 2^30, top <= min(32, V)");

@@ -124,6 +124,13 @@ def test_logprobs(lib):
     assert lib.dspark_logprobs_workspace_bytes(0, 8) == 0 and lib.dspark_logprobs_workspace_bytes(1, 8) >= 256
 
 
+def test_factors_past_the_largest_float(lib):
+    # log2(e) scale, or log2(e) / T: every result would be NaN
+    assert attention(lib, scale=3e38) == 1 and attention(lib, scale=-2.5e38) == 1
+    for T in (1e-45, 1e-39, 4e-39):
+        assert lib.dspark_logprobs(256, 1, 1024, 16, 4, 1024, T, 5, 16, 16, 16, 16, 16, 256, WS, None) == 1, T
+
+
 def test_rows_that_step_evenly():
     import torch
 
