@@ -107,7 +107,10 @@ def _rows(t, name, dtype, heads, dim, dev):
 
 
 def _stream(dev, stream) -> int:
-    """Handle of the launch stream: the device's current one, or the one given."""
+    """Handle of the launch stream: the device's current one, or the one given.  The device has to be
+    the current one, where launches go."""
+    if torch._C._cuda_getDevice() != dev.index:
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 

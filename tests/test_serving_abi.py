@@ -131,6 +131,21 @@ def test_factors_past_the_largest_float(lib):
         assert lib.dspark_logprobs(256, 1, 1024, 16, 4, 1024, T, 5, 16, 16, 16, 16, 16, 256, WS, None) == 1, T
 
 
+def test_another_device_than_the_current_one_is_refused(monkeypatch):
+    # a launch goes to the current device, whatever the stream and the tensors
+    import torch
+
+    from speculative_decoding_draft_05_gb300 import serving
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 7 + index)
+    assert serving._stream(torch.device("cuda", 0), None) == 7
+    with pytest.raises(ValueError, match="current device"):
+        serving._stream(torch.device("cuda", 1), None)
+    with pytest.raises(ValueError, match="current device"):
+        serving._stream(torch.device("cuda", 1), type("Stream", (), dict(cuda_stream=9))())
+
+
 def test_rows_that_step_evenly():
     import torch
 
