@@ -426,7 +426,8 @@ cudaError_t launch_combine(const cudaLaunchConfig_t& cfg, const AttnParams& p, i
                   : cudaLaunchKernelEx(&cfg, attention_combine_kernel<T, 8, 1>, p, MR, ctas);
 }
 
-constexpr int kSimtCtas = 304;
+constexpr int kSimtCtas = 304;  // two an SM
+static_assert(kSimtCtas <= kAttnMaxCtas, "");
 
 template <typename T, int NI>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
@@ -464,7 +465,7 @@ cudaError_t launch_attn_combine(const AttnParams& p, int MR, int ctas, cudaStrea
 }
 
 size_t attention_workspace_bytes(int dtype, int head_dim) {
-  const size_t simt = attn_workspace_layout(kMR, head_dim).total;
+  const size_t simt = attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
   if (dtype != DSPARK_BF16 || head_dim > 128) return simt;
   const size_t tc = attention_tc_workspace_bytes(head_dim);
   return tc > simt ? tc : simt;
@@ -472,7 +473,7 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
 
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
   if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
-  const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
+  const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kSimtCtas);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f,
                attn_item_units(a), kMR};

@@ -18,7 +18,7 @@
 
 namespace dspark {
 
-constexpr int kAttnMaxCtas = 320;  // CTAs of one attention launch, at most
+constexpr int kAttnMaxCtas = 320;  // CTAs of one attention launch, at most (attn_share counts on it)
 
 // Rows of most requests for a K/V head, as far as the host can tell: twice the mean.
 inline long long attn_likely_rows(const AttnArgs& a) {
@@ -42,18 +42,18 @@ struct CutItem {
   int pad[3];
 };
 
-// Workspace: status word, per-CTA status bits, cut items, partial (m, l) and
-// O.  Nothing in it has to be cleared before a call.
+// Workspace of a launch of `ctas` CTAs: status word, per-CTA status bits, cut
+// items, partial (m, l) and O.  Nothing in it has to be cleared before a call.
 struct AttnWorkspace {
   size_t flags, cuts, stats, out, total;
 };
-inline AttnWorkspace attn_workspace_layout(int MR, int D) {
+inline AttnWorkspace attn_workspace_layout(int MR, int D, int ctas) {
   AttnWorkspace w;
   w.flags = 256;
-  w.cuts = align_up256(w.flags + kAttnMaxCtas * sizeof(int));
-  w.stats = align_up256(w.cuts + kAttnMaxCtas * sizeof(CutItem));
-  w.out = align_up256(w.stats + (size_t)kAttnMaxCtas * 2 * MR * sizeof(float2));
-  w.total = align_up256(w.out + (size_t)kAttnMaxCtas * 2 * MR * D * sizeof(float));
+  w.cuts = align_up256(w.flags + ctas * sizeof(int));
+  w.stats = align_up256(w.cuts + ctas * sizeof(CutItem));
+  w.out = align_up256(w.stats + (size_t)ctas * 2 * MR * sizeof(float2));
+  w.total = align_up256(w.out + (size_t)ctas * 2 * MR * D * sizeof(float));
   return w;
 }
 

@@ -64,6 +64,8 @@ namespace {
 constexpr int kMR = 256;  // rows of an item, at most: two tiles of 128 / G tokens x G heads
 constexpr int kTN = 128;  // keys of a tile
 constexpr int kEarly = 96;  // of which the first are multiplied while the rest of P is in the making
+constexpr int kMaxCtas = 152;  // one an SM of GB300; what the workspace holds pieces of
+static_assert(kMaxCtas <= kAttnMaxCtas, "");
 constexpr int kThreads = 512;  // four warpgroups: two of softmax, the single roles, the results
 // Registers a thread after the split: 256 x 168 + 128 x 96 + 128 x 80 of the
 // launch's 512 x 128.
@@ -1133,7 +1135,7 @@ int sm_count() {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
       v = 1;
-    return v < kAttnMaxCtas ? v : kAttnMaxCtas;
+    return v < kMaxCtas ? v : kMaxCtas;
   }();
   return n;
 }
@@ -1169,10 +1171,10 @@ bool attention_tc_supported(const AttnArgs& a) {
   return get_encode() != nullptr;
 }
 
-size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout(kMR, head_dim).total; }
+size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout(kMR, head_dim, kMaxCtas).total; }
 
 cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
-  const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim);
+  const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kMaxCtas);
   TcParams tp;
   tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),

@@ -146,6 +146,18 @@ def test_another_device_than_the_current_one_is_refused(monkeypatch):
         serving._stream(torch.device("cuda", 1), type("Stream", (), dict(cuda_stream=9))())
 
 
+def test_attention_workspace_holds_the_launched_ctas_pieces(lib):
+    # two pieces a CTA: rows of head_dim floats, a maximum and a sum; 152 CTAs of 256 rows, or 304 of 64
+    def floor(D, bf16):
+        simt, tc = 304 * 2 * 64 * (4 * D + 8), 152 * 2 * 256 * (4 * D + 8)
+        return max(simt, tc) if bf16 and D <= 128 else simt
+
+    for D in (16, 64, 128, 256):
+        for dtype in (0, 1):
+            n = lib.dspark_paged_attention_workspace_bytes(cache(dtype=dtype, head_dim=D))
+            assert floor(D, dtype == 1) <= n <= floor(D, dtype == 1) + (1 << 15), (D, dtype, n)
+
+
 def test_rows_that_step_evenly():
     import torch
 
