@@ -11,8 +11,10 @@
 // sum over the counts.
 //
 // Bounds and figures: the cluster kernels are chains of dependent reads (resize
-// of 512 requests over 40,000 pages: 17 us in a graph, 20 us a call from Python,
-// whose host side is the longer; compact of 2000 pages 10 us); the copies and
+// of 512 requests over 40,000 pages: 16 us in a graph, 22 us a call from Python,
+// whose host side is the longer.  In a graph 11 of them where no length changes; 3
+// more for growth, one for releases and one for 19 split pages; compact of 2000
+// pages 10 us); the copies and
 // the append move bytes: 262 MB of pages read and written in 80 us (6.5 TB/s),
 // prompts of 8 k and 16 k new tokens of 8 x 128 (119 MB each way) in 37 us, 4.8 k
 // tokens of 512 requests in 7 us, four dependent look-ups behind their loads.
@@ -684,11 +686,16 @@ MetaCopy meta_args(const PageMeta& m, bool table, bool len) {
 // a graph the launch costs the host 3 us more.
 constexpr size_t kMetaInKernel = 1u << 17;
 // A resize copies the shared pages that it has to split in the cluster kernel
-// where even all requests' pages come to this many bytes.  It mostly has none:
-// then the second launch costs 1.5 us in a graph and 5 us outside one; where
-// every request has one, the 8 SMs take 15 us for 1 MB (12.5 with the launch),
-// 23 for 4 MB (12.7) and 57 for 17 MB (16).
-constexpr size_t kCopyInKernel = 8u << 20;
+// where even all requests' pages come to this many bytes: about as far as a call
+// that has to split all of them loses no more by it than one that splits none
+// gains.  In a graph, 256 requests, in the kernel / by the second launch:
+//                      1 MB         2 MB         4 MB         8 MB         16 MB
+//   no split         8.8 / 10.0   8.8 / 10.0   8.8 / 10.1   8.7 / 10.7   8.8 / 11.0
+//   every 16th      12.5 / 11.4  12.5 / 11.4  12.4 / 11.4  12.5 / 12.2  13.9 / 12.4
+//   all             14.3 / 12.5  16.9 / 12.5  22.4 / 12.5  33.6 / 14.4  55.2 / 17.8
+// Calls outside a graph, outputs given: none 9.1 / 10.7 .. 11.1, all 14.9 / 12.4
+// (1 MB), 23.0 / 12.5 (4 MB), 34.2 / 14.4 (8 MB).
+constexpr size_t kCopyInKernel = 1u << 20;
 cudaError_t split_meta(MetaCopy* c, cudaStream_t s) {
   size_t most = 0, all = 0;
   for (int k = 0; k < 3; ++k)
