@@ -459,11 +459,13 @@ int dspark_cache_append(const dspark_cache* cache, int layer, const void* k_new,
  *      contiguous; Hq a multiple of the cache's heads
  * out  [n_tokens, Hq, head_dim] cache dtype, dense
  * lse  [n_tokens, Hq] float
- * Rows at or past q_offsets[R] are neither read nor written.  Cache positions at or past
- * kv_len[r] never reach the outputs, whatever they hold; those before it, of
- * the pages in use, have to be finite (a value that is not may reach every
- * row of its request's chunk, also tokens before it).  Offsets, lengths or pages out
- * of range are flagged (DSPARK_DEV_BAD_INPUT) and clamped.
+ * Rows at or past q_offsets[R] are neither read nor written.  A row depends on
+ * the positions that it sees and on no others, whatever those hold (unused
+ * slots, positions past kv_len[r], later tokens of the chunk).  A K or V that is
+ * not finite gives rows that do see it results that are not finite; a V in
+ * the chunk's own positions may make the whole of such a row, and its lse, NaN.
+ * Offsets, lengths or pages out of range are flagged (DSPARK_DEV_BAD_INPUT) and
+ * clamped.
  * workspace: >= dspark_paged_attention_workspace_bytes(cache) bytes,
  *   256-byte aligned.
  * ---------------------------------------------------------------------- */

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
   extern __shared__ float4 smem4[];
   __shared__ AttnStart<kTN> st;
-  __shared__ int flags;
+  __shared__ int flags, bad_from;  // (bad_from: see hide_bad_v)
   __shared__ __align__(16) f32x2 sp[kWarps][kProbPairs];  // probabilities of a warp's rows
   constexpr int ld = NI * 32 + 4;
   constexpr int kPer = NI * 8;               // threads a row, four columns each
@@ -246,7 +246,27 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
         }
       }
     };
-    __syncthreads();  // (the item before is done with both buffers)
+    __syncthreads();  // (the item before is done with both buffers and bad_from)
+    if (threadIdx.x == 0) bad_from = 0x7fffffff;
+    const int all_see = w.q.L - w.q.n + row0 / G + 1;  // keys that all rows of the block see
+    // Keys that some rows see and some do not (positions of the chunk itself): 0
+    // times a V that is not finite would reach the latter, so such a V is cleared
+    // and the rows that do see it become NaN at the end.
+    auto hide_bad_v = [&](float* sv, int j0) {
+      const int from = max(all_see - j0, 0), to = min(w.end - j0, kTN);
+      if (from >= to) return;
+      for (int j = from + warp; j < to; j += kWarps) {
+        float* v = sv + j * ld;
+        bool bad = false;
+#pragma unroll
+        for (int d = 0; d < NI; ++d) bad |= (__float_as_uint(v[d * 32 + lane]) & 0x7f800000u) == 0x7f800000u;
+        if (!__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll
+        for (int d = 0; d < NI; ++d) v[d * 32 + lane] = 0.0f;
+        if (lane == 0) atomicMin(&bad_from, j0 + j);
+      }
+      __syncthreads();
+    };
     look_up(w.first_tile());
     load(w.first_tile());
     look_up(w.first_tile() + 1);
@@ -274,6 +294,7 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
       __syncthreads();
       load(t + 1);  // (all are past tile t - 1, which was in its buffer)
       look_up(t + 2);
+      hide_bad_v(skv + ((t & 1) * 2 + 1) * kTN * ld, t * kTN);
       if (warp * rw < rows) {
         const float* q = sq + warp * rw * ld;
         const float* sk = skv + (t & 1) * 2 * kTN * ld;
@@ -293,7 +314,7 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
     for (int i = 0; i < kRowsPerWarp; ++i) {
       const int a = warp * rw + i;
       if (i >= rw || a >= rows) continue;
-      const float l = warp_sum(r.l[i]);
+      const float sum = warp_sum(r.l[i]), l = r.lim[i] > bad_from ? __int_as_float(0x7fc00000) : sum;
       const int tok = (row0 + a) / G, g = (row0 + a) - tok * G;
       const size_t out = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + g;
       const size_t part = ((size_t)blockIdx.x * 2 + slot) * kMR + a;

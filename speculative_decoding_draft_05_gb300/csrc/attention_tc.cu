@@ -35,7 +35,10 @@
 //     the softmax warps are at the next piece.
 //   * Keys at or past an item's end: pages past it are not loaded, S is
 //     replaced by -inf, and V's rows are overwritten with zeros, since 0 x NaN of
-//     an unused cache slot would reach the sum.
+//     an unused cache slot would reach the sum.  The same for a V that is not
+//     finite at a key that some rows of the block see and some do not (positions
+//     of the chunk itself): its row is cleared, and the rows that do see it become
+//     NaN when the results are written.
 //   * What bounds it: with few rows the read of K and V (verifying, 64 requests
 //     of up to 17 tokens over 500 .. 8192 positions, 1.18 GB: 186 us, 6.3 TB/s;
 //     4 requests of 17 tokens over 100 k positions, 1.87 GB: 283 us, 6.6 TB/s;
@@ -88,10 +91,11 @@ struct Layout {
   static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
   static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1;
-  static constexpr int kOffPiece = kOffBar + ((kBars * 8 + 12 + 15) & ~15);  // PieceInfo [2]
+  static constexpr int kOffBad = kOffBar + kBars * 8;  // [2] words (see bad_v)
+  static constexpr int kOffPiece = (kOffBad + 2 * 8 + 12 + 15) & ~15;  // PieceInfo [4]
   // The plan has room of its own: the roles read it after the last barrier of
   // all threads, so nothing may be written over it.
-  static constexpr int kOffStart = (kOffPiece + 2 * 64 + 15) & ~15;
+  static constexpr int kOffStart = (kOffPiece + 4 * 64 + 15) & ~15;
   static constexpr int kEnd = kOffStart + (int)sizeof(AttnStart<kTN>);
   // Dynamic shared memory starts on a 1024-byte boundary when a kernel has no
   // static shared memory; the slack covers most others, and the kernel checks.
@@ -101,7 +105,7 @@ static_assert(Layout<64>::kEnd <= 232448 && Layout<128>::kEnd <= 232448, "shared
 template <int DP>
 constexpr bool plan_apart() {  // from all that is written while roles may still read it
   using Lo = Layout<DP>;
-  return Lo::kOffStart >= Lo::kOffMerge + 2 * 128 * 8 && Lo::kOffStart >= Lo::kOffPiece + 2 * 64;
+  return Lo::kOffStart >= Lo::kOffMerge + 2 * 128 * 8 && Lo::kOffStart >= Lo::kOffPiece + 4 * 64;
 }
 static_assert(plan_apart<64>() && plan_apart<128>(), "the plan's room");
 
@@ -346,7 +350,10 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// One piece: the part of an item that lies in this CTA's share.
+// One piece: the part of an item that lies in this CTA's share.  Piece n's is in
+// slot n & 3 and stays there while any warp is at it: the loader publishes piece
+// n + 4 after all warps have read that piece n + 2 is there, which they do one
+// after the other.
 struct alignas(16) PieceInfo {
   int t0, nt;       // first tile, tiles (0: no more pieces)
   int rows, row0;   // rows of the block (more than tile_rows: two Q tiles), first row of the chunk
@@ -355,7 +362,8 @@ struct alignas(16) PieceInfo {
   int end;          // keys of the item
   int slot;         // where the result goes (attn_slot)
   int next_joined;  // both this piece and the next one have one Q tile
-  int pad[2];
+  int all_see;      // keys that all rows of the block see
+  int masked;       // the piece's tiles from this one on have keys that not all rows see
 };
 static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 
@@ -386,7 +394,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* h_full = o_free + 2;   // [2] P's first kEarly keys written (4 warps)
   uint64_t* h_done = h_full + 2;   // [2] and their product done
   uint64_t* drain = h_done + 2;
-  uint32_t* tmem_slot = (uint32_t*)(bars + Lo::kBars);
+  // Piece n's first key with a V that is not finite among those that not all of
+  // its rows see: word n & 1, (n + 1) << 32 | 2^31 - 1 - key, the largest counts.
+  // (Of another piece: none.  The tag spares the clearing between pieces.)
+  unsigned long long* bad_v = (unsigned long long*)(smem + Lo::kOffBad);
+  uint32_t* tmem_slot = (uint32_t*)(bad_v + 2);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   int* flags = (int*)(tmem_slot + 2);  // the CTA's status bits
   AttnStart<kTN>* st = (AttnStart<kTN>*)(smem + Lo::kOffStart);
@@ -418,6 +430,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     mbar_init(&o_free[0], 4);
     mbar_init(&o_free[1], 4);
     mbar_init(drain, 1);
+    bad_v[0] = bad_v[1] = 0ull;
     *abort_flag = 0;
     *flags = 0;
     fence_barrier_init();
@@ -580,9 +593,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       };
       while (ok) {
         if (!(ok = wait_piece())) break;
-        int nt = infos[n & 1].nt;
+        int nt = infos[n & 3].nt;
         if (nt == 0) break;
-        if (infos[n & 1].rows > tp.tile_rows) {
+        if (infos[n & 3].rows > tp.tile_rows) {
           ok = wait_full(slot);
           if (!ok) break;
           qk(0, 0, slot);
@@ -624,8 +637,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (jq == nt) {  // the next piece, if it belongs to the run
               ++n;
               if (!(ok = wait_piece())) return;
-              nt = infos[n & 1].nt;
-              if (nt == 0 || infos[n & 1].rows > tp.tile_rows) {
+              nt = infos[n & 3].nt;
+              if (nt == 0 || infos[n & 3].rows > tp.tile_rows) {
                 open = false;
                 return;
               }
@@ -672,7 +685,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     while (true) {
       ok = __all_sync(0xffffffffu, mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget));
       if (!ok) break;
-      const PieceInfo c = infos[n & 1];
+      const PieceInfo c = infos[n & 3];
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[n & 1]);
       if (c.nt == 0) break;
@@ -696,7 +709,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         bool early = false;  // P's first kEarly keys are handed over
         if (warp_live) {
           const int vis = lim - k0;  // keys of the tile that the row sees
-          const bool masked = __any_sync(0xffffffffu, vis < kTN);
+          // (By the piece's tile as well: V is looked through before any warp hands P
+          // over early.  By that alone the compiler spills 100 bytes: verify 196 us.)
+          const bool masked = __any_sync(0xffffffffu, vis < kTN || j >= c.masked);
           // One pass: probabilities against the reference in use, and this tile's
           // maximum beside them.  They stand unless a row's maximum is out of range.
           // A tile without a mask hands over its first kEarly keys on the way; if a
@@ -833,19 +848,38 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           tmem_wait_st();
         }
         tc_fence_before();
-        // V rows past the item's end become zeros (by the stream that multiplies first).
-        if (k0 + kTN > c.end && (!two || s == 0)) {
+        // V rows past the item's end, and those that are not finite where not all
+        // rows see them, become zeros (by the stream that multiplies first).
+        if (j >= c.masked && (!two || s == 0)) {
+          const int all_see = infos[n & 3].all_see, end = infos[n & 3].end;
           const uint32_t i = run + j;
           const uint32_t sl = base + (two ? 2 * j + 1 : j + 1 < c.nt || c.next_joined ? 2 * i + 2 : 2 * i + 1);
           const int stage = (int)(sl % Lo::kStages);
           ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[stage], (sl / Lo::kStages) & 1u, abort_flag,
                                                  tp.wait_budget));
           if (!ok) break;
-          if (k0 + trow >= c.end) {
-            uint8_t* v = smem + Lo::kOffRing + stage * Lo::kTileBytes + trow * 128;
+          const int key = k0 + trow;
+          // (16-byte chunks in an order of the row's own: free of bank conflicts)
+          uint8_t* v = smem + Lo::kOffRing + stage * Lo::kTileBytes + trow * 128;
+          auto chunk_of = [&](int i) {
+            return (uint4*)(v + (i >> 3) * Lo::kHalfBytes + (((i ^ trow) & 7) << 4));
+          };
+          bool clear = key >= end;
+          if (key >= all_see && !clear) {
+            uint32_t bad = 0;  // an exponent of all ones carries into bit 15 or 31
 #pragma unroll
-            for (int i = 0; i < Lo::kHalves * 8; ++i)
-              *(uint4*)(v + (i >> 3) * Lo::kHalfBytes + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < Lo::kHalves * 8; ++i) {
+              const uint4 x = *chunk_of(i);
+              bad |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                     ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+            }
+            clear = bad & 0x80008000u;
+            if (clear)
+              atomicMax(&bad_v[n & 1], (unsigned long long)(n + 1) << 32 | (uint32_t)(0x7fffffff - key));
+          }
+          if (clear) {
+#pragma unroll
+            for (int i = 0; i < Lo::kHalves * 8; ++i) *chunk_of(i) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async();
         }
@@ -885,7 +919,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     while (true) {
       ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget, 64));
       if (!ok) break;
-      const PieceInfo c = infos[n & 1];
+      const PieceInfo c = infos[n & 3];
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[n & 1]);
       if (c.nt == 0) break;
@@ -895,6 +929,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       const int s0 = two ? 0 : (int)(run & 1u);  // the stream of a one-block piece's first tile
       float2 x0 = merge[s0 * 128 + trow];
       const float2 x1 = merge[(s0 ^ 1) * 128 + trow];
+      const unsigned long long bad = *(volatile unsigned long long*)&bad_v[n & 1];
+      const int bad_from = bad >> 32 == n + 1 ? 0x7fffffff - (int)(uint32_t)bad : 0x7fffffff;
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_empty);
       ok = __all_sync(0xffffffffu,
@@ -915,11 +951,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_free[0]);
         }
-        const float m = blk ? x1.x : x0.x, l = blk ? x1.y : x0.y;
+        const float m = blk ? x1.x : x0.x;
+        float l = blk ? x1.y : x0.y;
         const int a = blk * tp.tile_rows + trow;
         if (blk * tp.tile_rows + (warp & 3) * 32 >= c.rows) continue;  // (arrives below)
         const bool live = trow < tp.tile_rows && a < c.rows;
         const unsigned row = c.row0 + a, tok = row / (unsigned)G, g = row - tok * G;
+        if (c.lim + (int)tok > bad_from) l = __int_as_float(0x7fc00000);
         const size_t orow = (size_t)(c.q0 + tok) * p.a.Hq + c.h * G + g;
         const size_t prow = ((size_t)blockIdx.x * 2 + (c.slot < 0 ? 0 : c.slot)) * kMR + a;
         const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
@@ -1005,6 +1043,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       c.h = w.h;
       c.q0 = w.q.q0;
       c.lim = w.q.L - w.q.n + 1;
+      c.all_see = c.lim + c.row0 / G;
+      c.masked = (c.all_see > 0 ? c.all_see / kTN : 0) - c.t0;
       c.end = w.end;
       c.slot = end ? 0 : attn_slot(w);
       c.next_joined = 0;
@@ -1023,7 +1063,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         w.next(p, flags);
         c.next_joined = !two && !w.done() && w.block_rows(p) <= tp.tile_rows;
       }
-      if (lane == 0) infos[n & 1] = c;
+      if (lane == 0) infos[n & 3] = c;
       if (end) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[n & 1]);

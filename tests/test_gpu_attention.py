@@ -216,6 +216,52 @@ def test_attention_of_a_later_layer_and_given_outputs():
     check(i, r, layer=2)
 
 
+HIDDEN = [
+    # chunks, lens, Hq, Hkv, D, page, tokens of the first request whose K or V is not finite
+    ([17], [400], 8, 2, 128, 16, (0, 9, 16)),
+    ([17, 3], [130, 40], 8, 2, 64, 16, (1, 2, 14)),   # the chunk lies over two tiles
+    ([5, 2], [5, 30], 4, 2, 64, 16, (0, 1, 4)),
+    ([10], [4], 4, 2, 64, 16, (6, 9)),                # the first tokens see nothing
+    ([64, 1], [900, 50], 32, 8, 128, 16, (3, 62)),
+    ([300], [300], 8, 1, 128, 64, (0, 31, 32, 130, 299)),
+    ([129, 40], [700, 40], 16, 2, 96, 16, (5, 128)),
+    ([20], [6001], 32, 2, 128, 16, (19, 4)),          # many CTAs, cut pieces
+    ([80], [3000], 10, 2, 40, 24, (79, 0, 44)),
+    ([4, 2], [9, 3], 130, 1, 64, 16, (1, 3)),
+    ([20], [90], 4, 2, 256, 16, (7, 19)),
+    ([3], [20], 2, 1, 12, 5, (1,)),
+]
+
+
+@pytest.mark.parametrize("what", ["v nan", "v inf", "v -inf", "k nan"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n", range(len(HIDDEN)))
+def test_later_tokens_that_are_not_finite_stay_out_of_earlier_rows(dtype, what, n):
+    *shape, places = HIDDEN[n]
+    i = make(dtype, *shape, layout="thd" if n % 2 else "htd", seed=50 + n)
+    out, lse, tol, tol_lse = reference(i)
+    count, L, G = shape[0][0], shape[1][0], shape[2] // shape[3]
+    clean = [i[x].clone() for x in "kv"]
+    for a in places:
+        i["k"].copy_(clean[0])
+        i["v"].copy_(clean[1])
+        p = L - count + a
+        page = i["table"][0, p // i["page"]].long()
+        if what[0] == "v":
+            i["v"][0, page, p % i["page"], 0, 3] = float(what[2:])
+        else:
+            i["k"][0, page, p % i["page"], 0, 5] = math.nan
+        r = attend(i)
+        got, got_lse = r["out"].cpu().double(), r["lse"].cpu().double()
+        sees = torch.zeros(lse.shape, dtype=torch.bool)  # rows of the first K/V head from token a on
+        sees[a:count, :G] = True
+        assert not got[sees][:, 3].isfinite().any(), a
+        rest, none = ~sees, torch.isinf(lse)
+        assert ((got - out).abs() <= tol)[rest].all(), a
+        assert (got_lse[rest & none] == -math.inf).all()
+        assert ((got_lse - lse).abs() <= tol_lse)[rest & ~none].all(), a
+
+
 def test_attention_with_large_scores_and_a_growing_maximum():
     # keys in order of rising score: every tile raises the running maximum
     for dtype in (F32, BF16):
