@@ -412,7 +412,8 @@ int dspark_verify_noalloc(const int32_t* x, const float* logp, const float* lse,
  *
  * Limits (else DSPARK_ERR_UNSUPPORTED): R <= 65535, heads <= 1024, head_dim <=
  * 256, page_size <= 65536, n_pages <= 2^31 - 2^16, page_size * heads * head_dim <=
- * 2^30, R * max_pages < 2^31; kv_len counts positions and is at most max_pages * page_size, and at most
+ * 2^30, R * max_pages < 2^31, n_tokens (for attention n_tokens * Hq) <= 2^31 -
+ * 2^16; kv_len counts positions and is at most max_pages * page_size, and at most
  * 2^31 - 2^16 (a longer one is flagged and clamped).
  * ======================================================================== */
 typedef struct {
@@ -547,8 +548,8 @@ int dspark_pages_copy(const dspark_cache* cache, const int32_t* src, const int32
  * Masked ids (-inf) have probability 0 and come last among the alternatives,
  * with logp -inf; a row of nothing but -inf gives lse = -inf and NaN
  * otherwise.  NaN or +inf in a row makes lse, logp and entropy NaN; NaN ranks as -inf.
- * Limits: 8 <= V <= 2^30, V % 8 == 0, 0 <= top <= min(32, V); T with a finite
- * log2(e) / T (from 4.3e-39).
+ * Limits: 8 <= V <= 2^30, V % 8 == 0, n_rows <= 2^30, 0 <= top <= min(32, V); T
+ * with a finite log2(e) / T (from 4.3e-39).
  * workspace: >= dspark_logprobs_workspace_bytes(n_rows, V) bytes, 256-byte
  *   aligned.
  * ---------------------------------------------------------------------- */

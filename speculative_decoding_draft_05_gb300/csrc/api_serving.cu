@@ -29,7 +29,7 @@ int check_cache(const dspark_cache* c, int layer) {
     return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(c->dtype) - 1);
   if (((uintptr_t)c->k & a) || ((uintptr_t)c->v & a)) return DSPARK_ERR_INVALID_ARG;
-  if (c->head_dim > 256 || c->heads > 1024 || c->page_size > 65536 || c->n_pages > kMaxPositions ||
+  if (c->head_dim > 256 || c->heads > 1024 || c->page_size > 65536 || c->n_pages > kMaxCount ||
       (long long)c->page_size * c->heads * c->head_dim > (1ll << 30))
     return unsupported("head_dim <= 256, heads <= 1024, page_size <= 65536, n_pages <= 2^31 - 2^16, 2^30 elements a page");
   return DSPARK_OK;
@@ -89,6 +89,7 @@ int dspark_cache_append(const dspark_cache* cache, int layer, const void* k_new,
   if (((uintptr_t)k_new & a) || ((uintptr_t)v_new & a)) return DSPARK_ERR_INVALID_ARG;
   st = check_tables(R, max_pages);
   if (st != DSPARK_OK) return st;
+  if (n_tokens > kMaxCount) return unsupported("n_tokens <= 2^31 - 2^16");
   st = check_workspace(workspace, workspace_bytes, 256);
   if (st != DSPARK_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
@@ -121,7 +122,7 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
   if (((uintptr_t)q & a) || ((uintptr_t)out & 15u)) return DSPARK_ERR_INVALID_ARG;
   st = check_tables(R, max_pages);
   if (st != DSPARK_OK) return st;
-  if ((long long)n_tokens * Hq >= (1ll << 31)) return unsupported("n_tokens * Hq < 2^31");
+  if ((long long)n_tokens * Hq > kMaxCount) return unsupported("n_tokens * Hq <= 2^31 - 2^16");
   st = check_workspace(workspace, workspace_bytes, dspark_paged_attention_workspace_bytes(cache));
   if (st != DSPARK_OK) return st;
   AttnArgs p;
@@ -234,8 +235,8 @@ int dspark_logprobs(const void* Z, int dtype, long long row_stride, const int32_
   if (!(temperature > 0.0f) || !isfinite(temperature) || !isfinite(1.0f / temperature * kLog2e))
     return DSPARK_ERR_INVALID_ARG;
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARG;
-  if (V % 8 != 0 || V > (1 << 30) || top > 32 || top > V)
-    return unsupported("V % 8 == 0, V <= 2^30, top <= min(32, V)");
+  if (V % 8 != 0 || V > (1 << 30) || n_rows > (1 << 30) || top > 32 || top > V)
+    return unsupported("V % 8 == 0, V <= 2^30, n_rows <= 2^30, top <= min(32, V)");
   if (((uintptr_t)Z & 15u) || (row_stride * esize_of(dtype)) % 16 != 0) return DSPARK_ERR_INVALID_ARG;
   const LogprobsWorkspace w = logprobs_workspace_layout(n_rows, V);
   const int st = check_workspace(workspace, workspace_bytes, w.total);

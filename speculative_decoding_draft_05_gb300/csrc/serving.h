@@ -32,7 +32,10 @@ struct CacheView {
 // 2^31 - 2^16, so that rounding a length up to whole pages (of up to 2^16
 // positions) or tiles stays an int.  (Without that bound a page count of a length
 // near 2^31 came out negative, and table entries before the row would be written.)
-constexpr int kMaxPositions = 0x7fff0000;  // (also the most pages of a pool, for the same reason)
+// The same bound holds for what kernels step through: the pages of a pool, the
+// rows of a chunk.
+constexpr int kMaxCount = 0x7fff0000;
+constexpr int kMaxPositions = kMaxCount;
 __host__ __device__ __forceinline__ int most_positions(int max_pages, int page_size) {
   const long long n = (long long)max_pages * page_size;
   return n > kMaxPositions ? kMaxPositions : (int)n;

@@ -158,6 +158,13 @@ def test_attention_workspace_holds_the_launched_ctas_pieces(lib):
             assert floor(D, dtype == 1) <= n <= floor(D, dtype == 1) + (1 << 15), (D, dtype, n)
 
 
+def test_counts_that_a_step_past_the_end_would_overflow(lib):
+    assert attention(lib, Hq=2, T=0x3fff8001) == 2   # 2^31 - 2^16 + 2 rows
+    assert lib.dspark_cache_append(cache(), 0, 256, 256, 128, 64, 16, 16, 16, 2, 0x7fff0001, 4, 256, WS, None) == 2
+    n = (1 << 30) + 1
+    assert lib.dspark_logprobs(256, 1, 8, 16, n, 8, 1.0, 5, 16, 16, 16, 16, 16, 256, 1 << 60, None) == 2
+
+
 def test_rows_that_step_evenly():
     import torch
 
