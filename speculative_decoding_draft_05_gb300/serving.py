@@ -94,16 +94,20 @@ def _rows(t, name, dtype, heads, dim, dev):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1 and dim > 1:
-        raise ValueError(f"{name}: the head dimension must be contiguous")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim}], got {tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    # (the stride of a dimension of one carries no meaning)
-    hs = dim if t.shape[1] == 1 else st[1]
-    return t.data_ptr(), (t.shape[1] * hs if t.shape[0] <= 1 else st[0]), hs
+    ts, hs, ds = st
+    if ds != 1 and dim > 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    n, h, _ = shape
+    if h == 1:  # the stride of a dimension of one carries no meaning
+        hs = dim
+    if n <= 1:
+        ts = h * hs
+    return t.data_ptr(), ts, hs
 
 
 def _stream(dev, stream) -> int:
