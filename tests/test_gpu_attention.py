@@ -216,6 +216,28 @@ def test_attention_of_a_later_layer_and_given_outputs():
     check(i, r, layer=2)
 
 
+@pytest.mark.parametrize("D", [8, 24, 56, 72, 104, 120, 136, 248])
+def test_head_dims(D):
+    for dtype in (F32, BF16):
+        i = make(dtype, [3, 1, 40], [150, 20, 300], 8, 2, D, 16, seed=60)
+        check(i, attend(i))
+
+
+@pytest.mark.parametrize("G", [3, 11, 33, 43, 64, 65, 100, 127, 128, 129, 300])
+def test_query_heads_of_a_head(G):
+    # row blocks of whole tokens that do not fill 128 rows, and tokens of more rows than a block
+    for dtype in (F32, BF16):
+        i = make(dtype, [1, 2, 5, 9], [140, 1, 30, 260], 2 * G, 2, 64, 16, seed=61)
+        check(i, attend(i), want=reference_on_gpu(i))
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 40, 56, 72, 104, 128, 136, 200, 264])
+def test_page_sizes(page):
+    for dtype in (F32, BF16):
+        i = make(dtype, [17, 1, 60], [500, 129, 260], 8, 2, 128, page, layout="htd", seed=62)
+        check(i, attend(i), want=reference_on_gpu(i))
+
+
 HIDDEN = [
     # chunks, lens, Hq, Hkv, D, page, tokens of the first request whose K or V is not finite
     ([17], [400], 8, 2, 128, 16, (0, 9, 16)),
