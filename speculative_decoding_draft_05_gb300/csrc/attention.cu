@@ -172,6 +172,25 @@ __device__ __forceinline__ void simt_tile(Rows<NI / 2>& r, const float* sq, cons
   }
 }
 
+// Keys [from, to) of a tile, those that some rows of the block see and some do not
+// (positions of the chunk itself): 0 times a V that is not finite would reach the
+// latter, so such a V is cleared and the rows that do see it become NaN at the end.
+template <int NI>
+__device__ __forceinline__ void hide_bad_v(float* sv, int j0, int from, int to, int* bad_from) {
+  constexpr int ld = NI * 32 + 4;
+  const int lane = threadIdx.x & 31;
+  for (int j = from + (int)(threadIdx.x >> 5); j < to; j += kWarps) {
+    float* v = sv + j * ld;
+    bool bad = false;
+#pragma unroll
+    for (int d = 0; d < NI; ++d) bad |= (__float_as_uint(v[d * 32 + lane]) & 0x7f800000u) == 0x7f800000u;
+    if (!__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll
+    for (int d = 0; d < NI; ++d) v[d * 32 + lane] = 0.0f;
+    if (lane == 0) atomicMin(bad_from, j0 + j);
+  }
+}
+
 __device__ __forceinline__ void copy16(float* dst, const float* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                    (uint32_t)__cvta_generic_to_shared(dst)),
@@ -187,7 +206,10 @@ __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
   extern __shared__ float4 smem4[];
   __shared__ AttnStart<kTN> st;
-  __shared__ int flags, bad_from;  // (bad_from: see hide_bad_v)
+  // Of the item: keys that all rows of the block see, the first tile with others,
+  // and the first of those whose V is not finite (hide_bad_v).  Not in registers:
+  // there they cost what fp32 decoding of 128 requests shows, 290 us for 286.
+  __shared__ int flags, all_see, t_hidden, bad_from;
   __shared__ __align__(16) f32x2 sp[kWarps][kProbPairs];  // probabilities of a warp's rows
   constexpr int ld = NI * 32 + 4;
   constexpr int kPer = NI * 8;               // threads a row, four columns each
@@ -247,26 +269,12 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
       }
     };
     __syncthreads();  // (the item before is done with both buffers and bad_from)
-    if (threadIdx.x == 0) bad_from = 0x7fffffff;
-    const int all_see = w.q.L - w.q.n + row0 / G + 1;  // keys that all rows of the block see
-    // Keys that some rows see and some do not (positions of the chunk itself): 0
-    // times a V that is not finite would reach the latter, so such a V is cleared
-    // and the rows that do see it become NaN at the end.
-    auto hide_bad_v = [&](float* sv, int j0) {
-      const int from = max(all_see - j0, 0), to = min(w.end - j0, kTN);
-      if (from >= to) return;
-      for (int j = from + warp; j < to; j += kWarps) {
-        float* v = sv + j * ld;
-        bool bad = false;
-#pragma unroll
-        for (int d = 0; d < NI; ++d) bad |= (__float_as_uint(v[d * 32 + lane]) & 0x7f800000u) == 0x7f800000u;
-        if (!__any_sync(0xffffffffu, bad)) continue;
-#pragma unroll
-        for (int d = 0; d < NI; ++d) v[d * 32 + lane] = 0.0f;
-        if (lane == 0) atomicMin(&bad_from, j0 + j);
-      }
-      __syncthreads();
-    };
+    if (threadIdx.x == 0) {
+      const int a = w.q.L - w.q.n + row0 / G + 1;
+      all_see = a;
+      t_hidden = a < w.end ? max(a, 0) / kTN : 0x7fffffff;
+      bad_from = 0x7fffffff;
+    }
     look_up(w.first_tile());
     load(w.first_tile());
     look_up(w.first_tile() + 1);
@@ -294,7 +302,11 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
       __syncthreads();
       load(t + 1);  // (all are past tile t - 1, which was in its buffer)
       look_up(t + 2);
-      hide_bad_v(skv + ((t & 1) * 2 + 1) * kTN * ld, t * kTN);
+      if (t >= t_hidden) {
+        hide_bad_v<NI>(skv + ((t & 1) * 2 + 1) * kTN * ld, t * kTN, max(all_see - t * kTN, 0),
+                       min(w.end - t * kTN, kTN), &bad_from);
+        __syncthreads();
+      }
       if (warp * rw < rows) {
         const float* q = sq + warp * rw * ld;
         const float* sk = skv + (t & 1) * 2 * kTN * ld;
