@@ -436,7 +436,7 @@ typedef struct {
  *              q_offsets[R] are padding and are not used
  * kv_len       [R] int32; page_table [R, max_pages] int32
  * Tokens whose position or page is out of range are flagged
- * (DSPARK_DEV_BAD_INPUT) and left out, and offsets past n_tokens are flagged.  The pages written must not be shared
+ * (DSPARK_DEV_BAD_INPUT) and left out; offsets past n_tokens are flagged too.  The pages written must not be shared
  * (dspark_pages_resize sees to that).  n_tokens may be 0.
  * workspace: >= 256 bytes, 256-byte aligned (the status word).
  * ---------------------------------------------------------------------- */

@@ -39,6 +39,10 @@
 //     finite at a key that some rows of the block see and some do not (positions
 //     of the chunk itself): its row is cleared, and the rows that do see it become
 //     NaN when the results are written.
+//   * P is rounded to bf16, the type of V, as both operands of a product are of
+//     one type.  Against 64 bits the output is then off by 2.3e-3 of its norm,
+//     with P in 32 bits by 1.7e-3, which is the rounding of the output itself.
+//     All sums, and l, take p before it is rounded; an fp32 cache keeps 32 bits.
 //   * What bounds it: with few rows the read of K and V (verifying, 64 requests
 //     of up to 17 tokens over 500 .. 8192 positions, 1.18 GB: 186 us, 6.3 TB/s;
 //     4 requests of 17 tokens over 100 k positions, 1.87 GB: 283 us, 6.6 TB/s;
@@ -47,7 +51,9 @@
 //     chain of a stream, S, softmax, P V, against 1024 cycles of matrix
 //     instructions a tile: about 2850 cycles a tile of each of the two streams
 //     (prefill of 2901 + 4096 tokens at 5000 .. 8192 positions: 425 us, 1.56
-//     PFLOP/s, 83 % of a library product's rate).
+//     PFLOP/s, 83 % of a library product's rate, for the first tenth of a second
+//     at 2070 MHz; 458 us, 1.44 PFLOP/s, once the power limit holds the clock at
+//     1.75 .. 1.95 GHz).
 //   * Every mbarrier wait is bounded; on expiry the CTA flags
 //     DSPARK_DEV_TIMEOUT, drains what it issued, frees TMEM and returns.
 #include <cuda.h>
