@@ -42,7 +42,8 @@
 //   * P is rounded to bf16, the type of V, as both operands of a product are of
 //     one type.  Against 64 bits the output is then off by 2.3e-3 of its norm,
 //     with P in 32 bits by 1.7e-3, which is the rounding of the output itself.
-//     All sums, and l, take p before it is rounded; an fp32 cache keeps 32 bits.
+//     l sums p before it is rounded and all sums are fp32; an fp32 cache keeps P in
+//     32 bits too.
 //   * What bounds it: with few rows the read of K and V (verifying, 64 requests
 //     of up to 17 tokens over 500 .. 8192 positions, 1.18 GB: 186 us, 6.3 TB/s;
 //     4 requests of 17 tokens over 100 k positions, 1.87 GB: 283 us, 6.6 TB/s;

@@ -231,6 +231,15 @@ def test_query_heads_of_a_head(G):
         check(i, attend(i), want=reference_on_gpu(i))
 
 
+@pytest.mark.parametrize("chunks,lens", [([300, 1, 700], [900, 50, 700]), ([257, 256, 255], [257, 300, 4000]), ([1100], [1100])])
+def test_long_chunks_of_one_query_head(chunks, lens):
+    # a row block is 128 or 256 tokens: the causal mask lies over several tiles
+    for dtype in (F32, BF16):
+        for D in (64, 128):
+            i = make(dtype, chunks, lens, 2, 2, D, 16, seed=63)
+            check(i, attend(i), want=reference_on_gpu(i))
+
+
 @pytest.mark.parametrize("page", [1, 3, 8, 40, 56, 72, 104, 128, 136, 200, 264])
 def test_page_sizes(page):
     for dtype in (F32, BF16):
@@ -252,6 +261,9 @@ HIDDEN = [
     ([4, 2], [9, 3], 130, 1, 64, 16, (1, 3)),
     ([20], [90], 4, 2, 256, 16, (7, 19)),
     ([3], [20], 2, 1, 12, 5, (1,)),
+    ([300], [700], 2, 2, 128, 16, (0, 130, 299)),     # one query head a K/V head: masks over several tiles
+    ([700], [700], 1, 1, 64, 64, (0, 200, 511, 699)),
+    ([260, 2], [3000, 5], 2, 2, 128, 24, (1, 255)),
 ]
 
 
