@@ -99,6 +99,12 @@ def reference_on_gpu(i):
         K, V = (x[0][pg].reshape(-1, i["Hkv"], D)[:L].double().repeat_interleave(G, 1) for x in (i["k"], i["v"]))
         q = i["q"][t:t + n].double()
         t += n
+        if n == 0:
+            continue
+        if L == 0:  # nothing to see
+            z = torch.zeros(n, Hq, D, dtype=torch.float64, device="cuda")
+            parts.append((z, z[..., 0] - math.inf, z, z[..., 0]))
+            continue
         pos = torch.arange(L - n, L, device="cuda")
         see = torch.arange(L, device="cuda") <= pos[:, None, None]  # [n, 1, L]
         s = torch.einsum("nhd,jhd->nhj", q, K) * scale
@@ -214,6 +220,13 @@ def test_attention_of_a_later_layer_and_given_outputs():
     r = attend(i, layer=2, out=out, lse=lse)
     assert r["out"] is out and r["lse"] is lse
     check(i, r, layer=2)
+
+
+def test_requests_without_positions():
+    for dtype in (F32, BF16):
+        i = make(dtype, [2, 0, 3, 200, 0], [0, 0, 40, 0, 7], 8, 2, 64, 16, seed=64)
+        check(i, attend(i), want=reference_on_gpu(i))
+        check(i, attend(i))
 
 
 @pytest.mark.parametrize("D", [8, 24, 56, 72, 104, 120, 136, 248])
