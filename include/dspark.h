@@ -78,7 +78,7 @@ typedef enum {
   DSPARK_ERR_TIMEOUT = 6       /* (device status) a bounded device-side wait gave up */
 } dspark_status;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_FP4 = 2 /* a paged cache's alone */ } dspark_dtype;
 
 enum {
   DSPARK_PURPOSE_DRAFT = 0,
@@ -419,7 +419,7 @@ int dspark_verify_noalloc(const int32_t* x, const float* logp, const float* lse,
 typedef struct {
   void* k; /* DEVICE: page 0 of layer 0 */
   void* v;
-  int dtype; /* DSPARK_F32 or DSPARK_BF16 */
+  int dtype; /* DSPARK_F32 or DSPARK_BF16; DSPARK_FP4: see below */
   int layers, n_pages, page_size, heads, head_dim;
   long long layer_stride, page_stride, token_stride, head_stride;
 } dspark_cache;
@@ -476,6 +476,90 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
                            const int32_t* kv_len, const int32_t* page_table, int R, int n_tokens,
                            int max_pages, float scale, void* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit cache (dtype DSPARK_FP4): 4.5 bits an element, for long contexts.
+ * The K of a head in a page is page_size / 16 blocks of 9 * head_dim bytes, one
+ * after the other, V's likewise.  A block holds 16 positions: [16, head_dim / 2]
+ * bytes of e2m1 codes (+-0, 0.5, 1, 1.5, 2, 3, 4, 6; the even element in the low
+ * four bits), then [16, head_dim / 16] e4m3 scales, one for 16 elements.  A
+ * value is code * scale * factor, where k_factor and v_factor (HOST floats, 2^-60 ..
+ * 2^60; 1 does for most) are given with each call.
+ *
+ * In `dspark_cache` the strides then count bytes and are multiples of 16, as
+ * are the addresses k and v; token_stride is that of a block, 9 * head_dim.
+ * head_dim % 32 == 0 and page_size % 16 == 0 (else DSPARK_ERR_UNSUPPORTED).
+ * dspark_pages_resize, _fork, _compact and _copy take such a cache as they take
+ * the others.  dspark_cache_append and dspark_paged_attention do not; the calls
+ * below do.
+ *
+ * dspark_cache_append_rotary -- dspark_cache_append for any cache, with K, and
+ * the chunk's queries if given, rotated on the way.  Pair i of a row at position
+ * p, with c = cos_sin[p][i] and s = cos_sin[p][dim / 2 + i]:
+ *   (a, b) -> (a c - b s, b c + a s)
+ * where a, b are elements i and i + dim / 2, or 2 i and 2 i + 1 (interleaved);
+ * elements from `dim` on are left as they are.  Without a rotation (rotary NULL)
+ * rows are stored as they are, which is how a 4-bit cache is filled from rotated rows.
+ * Into a 4-bit cache: for each group y of 16 elements, after the rotation and
+ * divided by the factor,
+ *   scale = e4m3(max |y| / 6),  code_j = e2m1(y_j / scale)
+ * each the nearest, ties to even, at most 448 and 6.  With a factor that is a
+ * power of two the bytes are those of the formula in infinite precision.  A group with
+ * an element that is not finite gets the scale NaN, and reads as NaN.
+ *
+ * rotary    HOST struct, read by the call: cos_sin [n_positions, dim] float, dim
+ *           even, 2 .. head_dim: dim / 2 cosines, then as many sines, of each position;
+ *           positions [n_tokens] int32, the table's row for each token, or
+ *           NULL: its position in the cache
+ * dtype     of k_new, v_new, q, q_out: DSPARK_F32 or DSPARK_BF16, the cache's where
+ *           that is one of them
+ * q, q_out  [n_tokens, Hq, head_dim], strides in elements, head_dim contiguous;
+ *           q_out may be q itself (with its strides), and may not overlap it
+ *           otherwise.  Hq = 0: no queries.
+ * A token whose position lies past the table is flagged (DSPARK_DEV_BAD_INPUT)
+ * and left out, like one whose position or page is out of range: its cache slot and
+ * its row of q_out stay as they were, as do the rows at or past q_offsets[R].
+ * All else as in dspark_cache_append.
+ *
+ * dspark_cache_read -- the inverse of an append: rows q_offsets[r] ..
+ * q_offsets[r + 1] - 1 of k_out and v_out get the values at request r's last
+ * positions, row q_offsets[r + 1] - 1 those at kv_len[r] - 1.  (With q_offsets
+ * the sums of kv_len: all positions.)  Any cache.
+ * dtype     of k_out, v_out [n_tokens, heads, head_dim], dense and 16-byte
+ *           aligned: the cache's, or either for a 4-bit cache
+ * Rows without a place are flagged and left as they were.  workspace: >= 256 bytes.
+ *
+ * dspark_paged_attention_fp4 -- dspark_paged_attention over a 4-bit cache; dtype
+ * is that of q and out.  Codes times scales are exact in fp16: bf16 queries are
+ * multiplied as fp16 (a row by a power of two that brings it into range;
+ * elements below 2^-28 of the row's largest keep fewer bits), the probabilities
+ * rounded to fp16.  fp32 queries are multiplied in fp32.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  const float* cos_sin; /* DEVICE */
+  const int32_t* positions; /* DEVICE, or NULL */
+  int n_positions, dim, interleaved;
+} dspark_rotary;
+int dspark_cache_append_rotary(const dspark_cache* cache, int layer, float k_factor, float v_factor,
+                               const dspark_rotary* rotary, int dtype, const void* k_new,
+                               const void* v_new, long long new_token_stride,
+                               long long new_head_stride, const void* q, long long q_token_stride,
+                               long long q_head_stride, int Hq, void* q_out,
+                               long long q_out_token_stride, long long q_out_head_stride,
+                               const int32_t* q_offsets, const int32_t* kv_len,
+                               const int32_t* page_table, int R, int n_tokens, int max_pages,
+                               void* workspace, size_t workspace_bytes, void* stream);
+int dspark_cache_read(const dspark_cache* cache, int layer, float k_factor, float v_factor, int dtype,
+                      const int32_t* q_offsets, const int32_t* kv_len, const int32_t* page_table,
+                      int R, int n_tokens, int max_pages, void* k_out, void* v_out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+size_t dspark_paged_attention_fp4_workspace_bytes(const dspark_cache* cache, int dtype);
+int dspark_paged_attention_fp4(const void* q, long long q_token_stride, long long q_head_stride, int Hq,
+                               int dtype, const dspark_cache* cache, int layer, float k_factor,
+                               float v_factor, const int32_t* q_offsets, const int32_t* kv_len,
+                               const int32_t* page_table, int R, int n_tokens, int max_pages,
+                               float scale, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Page management.  Each call reads the state (page_table, kv_len, refcount)

@@ -105,6 +105,15 @@ def load() -> ctypes.CDLL:
     L.dspark_paged_attention_workspace_bytes.restype = SZ
     L.dspark_paged_attention.argtypes = [P, LL, LL, I, P, I, P, P, P, I, I, I, F, P, P, P, SZ, P]
     L.dspark_paged_attention.restype = I
+    L.dspark_cache_append_rotary.argtypes = [P, I, F, F, P, I, P, P, LL, LL, P, LL, LL, I, P, LL, LL, P, P, P,
+                                             I, I, I, P, SZ, P]
+    L.dspark_cache_append_rotary.restype = I
+    L.dspark_cache_read.argtypes = [P, I, F, F, I, P, P, P, I, I, I, P, P, P, SZ, P]
+    L.dspark_cache_read.restype = I
+    L.dspark_paged_attention_fp4_workspace_bytes.argtypes = [P, I]
+    L.dspark_paged_attention_fp4_workspace_bytes.restype = SZ
+    L.dspark_paged_attention_fp4.argtypes = [P, LL, LL, I, I, P, I, F, F, P, P, P, I, I, I, F, P, P, P, SZ, P]
+    L.dspark_paged_attention_fp4.restype = I
     L.dspark_pages_workspace_bytes.argtypes = [I, I]
     L.dspark_pages_workspace_bytes.restype = SZ
     L.dspark_pages_resize.argtypes = [P, P, P, P, P, I, I, P, P, P, P, P, SZ, P]

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "attention.cuh"
+#include "fp4.cuh"
 
 namespace dspark {
 
@@ -65,6 +66,14 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* row, int d, int D, 
   }
   return make_float4(d < D ? to_f32(row[d]) : 0.0f, d + 1 < D ? to_f32(row[d + 1]) : 0.0f,
                      d + 2 < D ? to_f32(row[d + 2]) : 0.0f, d + 3 < D ? to_f32(row[d + 3]) : 0.0f);
+}
+
+// Four elements of a 4-bit row (codes: their two bytes), times the scale and the factor.
+__device__ __forceinline__ float4 load4_fp4(const uint8_t* codes, const uint8_t* scale, float factor) {
+  uint32_t h[4];
+  fp4x8_to_half(*(const uint16_t*)codes, h);
+  const float s = e4m3_to_float(*scale) * factor;
+  return make_float4(half_lo(h[0]) * s, half_hi(h[0]) * s, half_lo(h[1]) * s, half_hi(h[1]) * s);
 }
 
 // Division of n < 2^31 by a divisor known at launch: a multiplication and
@@ -202,7 +211,7 @@ __device__ __forceinline__ void copy16(float* dst, const float* src) {
 // The rows of an item are spread over the warps, one, two, four or eight a warp;
 // a tile of K and V is on its way to shared memory while the one before is
 // worked on, and the pages of the one after are looked up.
-template <typename T, int NI>  // NI = ceil(D / 32), 2, 4 or 8
+template <typename T, int NI, bool FP4>  // NI = ceil(D / 32), 2, 4 or 8
 __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
   extern __shared__ float4 smem4[];
@@ -254,6 +263,16 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
           if (pg < 0 || pg >= p.a.c.n_pages) {
             flag_status(&flags, DSPARK_DEV_BAD_INPUT);
             pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+          }
+          if constexpr (FP4) {
+            const int D = p.a.c.head_dim, slot = j - by_page(j) * S;
+            const long long at = pg * p.a.c.page_stride + w.h * p.a.c.head_stride;
+            const long long codes = at + fp4_codes_at(slot, D) + lc / 2, scale = at + fp4_scales_at(slot, D) + lc / 16;
+            const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const uint8_t *kb = (const uint8_t*)p.a.c.k, *vb = (const uint8_t*)p.a.c.v;
+            *(float4*)k = lc < D ? load4_fp4(kb + codes, kb + scale, 1.0f) : zero;
+            *(float4*)v = lc < D ? load4_fp4(vb + codes, vb + scale, p.a.v_factor) : zero;
+            continue;
           }
           const long long at = pg * p.a.c.page_stride + (j - by_page(j) * S) * p.a.c.token_stride +
                                w.h * p.a.c.head_stride;
@@ -463,11 +482,11 @@ cudaError_t launch_combine(const cudaLaunchConfig_t& cfg, const AttnParams& p, i
 constexpr int kSimtCtas = 304;  // two an SM
 static_assert(kSimtCtas <= kAttnMaxCtas, "");
 
-template <typename T, int NI>
+template <typename T, int NI, bool FP4>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
   const int smem = (kMR + 4 * kTN) * (NI * 32 + 4) * (int)sizeof(float);
   static const cudaError_t attr = cudaFuncSetAttribute(
-      attention_simt_kernel<T, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      attention_simt_kernel<T, NI, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (attr != cudaSuccess) return attr;
   // Rows that are whole 16-byte (fp32) or 8-byte (bf16) vectors load as such.
   const CacheView& c = p.a.c;
@@ -476,15 +495,15 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
                    (((uintptr_t)c.k | (uintptr_t)c.v) & (4 * sizeof(T) - 1)) == 0;
   cudaLaunchAttribute attr_pdl;
   const cudaLaunchConfig_t cfg = overlapped_launch(dim3(kSimtCtas), kThreads, smem, s, &attr_pdl);
-  return cudaLaunchKernelEx(&cfg, attention_simt_kernel<T, NI>, p, Divider((unsigned)c.page_size), vec);
+  return cudaLaunchKernelEx(&cfg, attention_simt_kernel<T, NI, FP4>, p, Divider((unsigned)c.page_size), vec);
 }
 
-template <typename T>
+template <typename T, bool FP4>
 cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
   const int ni = (p.a.c.head_dim + 31) / 32;
-  if (ni <= 2) return launch_simt<T, 2>(p, s);
-  if (ni <= 4) return launch_simt<T, 4>(p, s);
-  return launch_simt<T, 8>(p, s);
+  if (ni <= 2) return launch_simt<T, 2, FP4>(p, s);
+  if (ni <= 4) return launch_simt<T, 4, FP4>(p, s);
+  return launch_simt<T, 8, FP4>(p, s);
 }
 
 }  // namespace
@@ -505,13 +524,20 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
   return tc > simt ? tc : simt;
 }
 
+size_t attention_fp4_workspace_bytes(int dtype, int head_dim) {
+  return attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
+}
+
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
-  if (attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
+  if (!a.fp4 && attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kSimtCtas);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                (float2*)(ws + w.stats), (float*)(ws + w.out), a.scale * 1.4426950408889634f,
                attn_item_units(a), kMR};
-  const cudaError_t e = a.dtype == DSPARK_BF16 ? launch_simt_dim<__nv_bfloat16>(p, s) : launch_simt_dim<float>(p, s);
+  const bool bf = a.dtype == DSPARK_BF16;
+  const cudaError_t e = a.fp4 ? bf ? launch_simt_dim<__nv_bfloat16, true>(p, s) : launch_simt_dim<float, true>(p, s)
+                        : bf  ? launch_simt_dim<__nv_bfloat16, false>(p, s)
+                              : launch_simt_dim<float, false>(p, s);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(p, kMR, kSimtCtas, s);
 }

@@ -20,6 +20,7 @@
 // tokens of 512 requests in 7 us, four dependent look-ups behind their loads.
 #include <cooperative_groups.h>
 
+#include "append.cuh"
 #include "common.cuh"
 #include "serving.h"
 
@@ -720,68 +721,6 @@ struct AppendArgs {
   int* status;
 };
 
-// The request whose chunk holds token t: the largest r with q_offsets[r] <= t
-// (later empty requests have larger offsets or follow it with the same one).
-// 32 probes a step: two dependent loads for up to 1024 requests.
-__device__ __forceinline__ int find_request(const int32_t* off, int R, int t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = R;  // off[lo] <= t (taken as given for lo = 0), off[hi] > t
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + (lane + 1) * step;
-    const bool le = i < hi && off[i] <= t;
-    const int k = __popc(__ballot_sync(0xffffffffu, le));
-    const int nlo = lo + k * step;
-    const int nhi = nlo + step;
-    lo = nlo;
-    hi = nhi < hi ? nhi : hi;
-  }
-  return lo;
-}
-
-// Whether any new token has no place in the cache, or an offset lies past the
-// rows given (the positions counted for them stay unwritten), by one CTA, request
-// by request (a request a thread, its further pages by the warp): the status word,
-// which so needs no clearing before the launch (a launch of its own cost 2 of 12
-// us for 512 requests).
-__device__ __forceinline__ void append_status(const AppendArgs& p) {
-  const int lane = threadIdx.x & 31, S = p.c.page_size;
-  bool bad = false;
-  const auto check = [&](int r, long long j) {
-    const int page = p.a.page_table[(size_t)r * p.a.max_pages + j];
-    bad |= page < 0 || page >= p.c.n_pages;
-  };
-  for (int r0 = 0; r0 < p.a.R; r0 += blockDim.x) {  // a request a thread
-    const int r = r0 + (int)threadIdx.x;
-    long long s0 = 0, s1 = -1;  // the pages that its tokens go to
-    if (r < p.a.R) {
-      const int b = p.a.q_offsets[r], e = p.a.q_offsets[r + 1], L = p.a.kv_len[r];
-      bad |= b > e || e > p.a.n_tokens || (r == 0 && b != 0);
-      const int t0 = b < 0 ? 0 : b, t1 = e < p.a.n_tokens ? e : p.a.n_tokens;
-      if (t0 < t1) {
-        const long long base = (long long)L - e;  // a token's position less its number
-        bad |= base + t0 < 0;
-        s0 = base + t0 < 0 ? 0 : (base + t0) / S;
-        const long long last = base + t1 - 1, most = most_positions(p.a.max_pages, S);
-        bad |= last >= most;
-        s1 = last < 0 ? -1 : (last < most ? last : most - 1) / S;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (s0 + k <= s1) check(r, s0 + k);
-    for (unsigned more = __ballot_sync(0xffffffffu, s0 + 2 <= s1); more; more &= more - 1) {
-      const int src = __ffs(more) - 1;
-      const long long j0 = __shfl_sync(0xffffffffu, s0, src) + 2, j1 = __shfl_sync(0xffffffffu, s1, src);
-      const int row = __shfl_sync(0xffffffffu, r, src);
-#pragma unroll 4
-      for (long long j = j0 + lane; j <= j1; j += 32) check(row, j);
-    }
-  }
-  const int any = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *p.status = any ? DSPARK_DEV_BAD_INPUT : 0;
-}
-
 // One warp a token: VE elements (16 bytes, or one where alignment does not
 // allow) a lane and step.  The first kAppendAhead steps' rows are loaded before
 // the token's request, position and page are looked up (four dependent loads).
@@ -797,7 +736,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (attention over the cache mostly follows)
   wait_for_previous();
   if (blockIdx.x == 0) {
-    append_status(p);
+    append_status(p.c, p.a, p.status);
     return;
   }
   for (int t = (blockIdx.x - 1) * 8 + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * 8) {

@@ -53,6 +53,34 @@ cudaError_t launch_cache_append(const CacheView& c, int esize, const void* k_new
                                 long long new_token_stride, long long new_head_stride,
                                 const ChunkArgs& a, int* status, cudaStream_t s);
 
+// The same with K (and the chunk's queries) rotated on the way, and into a 4-bit
+// cache (CacheView's strides then in bytes).
+struct RotaryAppendArgs {
+  CacheView c;
+  ChunkArgs a;
+  const void *k_new, *v_new, *q;
+  void* q_out;
+  long long tok_stride, head_stride;               // of k_new and v_new
+  long long q_tok, q_head, qo_tok, qo_head;
+  int Hq;                                          // 0: no queries
+  const float* cos_sin;                            // [n_positions, rot]
+  const int32_t* positions;                        // [n_tokens], or null: those in the cache
+  int rot, n_positions, interleaved;
+  float2 k_factor, v_factor;                       // and their inverses (4-bit)
+  int* status;
+};
+cudaError_t launch_append_rotary(const RotaryAppendArgs& p, int dtype, bool fp4, cudaStream_t s);
+
+// A chunk's rows out of the cache, dense [n_tokens, heads, head_dim].
+struct CacheReadArgs {
+  CacheView c;
+  ChunkArgs a;
+  void *k_out, *v_out;
+  float k_factor, v_factor;  // (4-bit)
+  int* status;
+};
+cudaError_t launch_cache_read(const CacheReadArgs& p, int esize, bool fp4, cudaStream_t s);
+
 // Page management.  Workspace (byte offsets, 256-aligned): words (the status
 // word first), per-request or per-pair scratch, the free list and copy list.
 struct PagesWorkspace {
@@ -104,8 +132,13 @@ struct AttnArgs {
   float scale;
   void* out;    // [n_tokens, Hq, D]
   float* lse;   // [n_tokens, Hq]
+  // A 4-bit cache (c's strides in bytes): values are code x scale x factor.  K's
+  // factor is in `scale`.
+  bool fp4 = false;
+  float v_factor = 1.0f;
 };
 size_t attention_workspace_bytes(int dtype, int head_dim);
+size_t attention_fp4_workspace_bytes(int dtype, int head_dim);
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s);
 
 // The kernels here may be launched while the one before them in the stream ends:
