@@ -525,10 +525,14 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
 }
 
 size_t attention_fp4_workspace_bytes(int dtype, int head_dim) {
-  return attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
+  const size_t simt = attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
+  if (dtype != DSPARK_BF16 || head_dim > 128) return simt;
+  const size_t rows = attention_fp4_rows_workspace_bytes(head_dim);
+  return rows > simt ? rows : simt;
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
+  if (attention_fp4_rows_supported(a)) return launch_attention_fp4_rows(a, ws, s);
   if (!a.fp4 && attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kSimtCtas);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),

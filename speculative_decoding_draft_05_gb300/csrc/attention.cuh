@@ -323,4 +323,9 @@ bool attention_tc_supported(const AttnArgs& a);
 size_t attention_tc_workspace_bytes(int head_dim);
 cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s);
 
+// Few rows over a 4-bit cache (attention_fp4.cu).
+bool attention_fp4_rows_supported(const AttnArgs& a);
+size_t attention_fp4_rows_workspace_bytes(int head_dim);
+cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s);
+
 }  // namespace dspark

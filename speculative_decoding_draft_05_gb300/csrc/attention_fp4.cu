@@ -1,0 +1,525 @@
+// attention_fp4.cu -- attention of few rows a K/V head over the 4-bit paged cache
+// (bf16 queries, head_dim up to 128): decoding, and short chunks.
+//
+// Codes times scales are exact in fp16, so both products are of fp16 operands
+// with fp32 sums, and codes become operands in registers: shared memory holds
+// what the cache holds, 9 bytes for 16 elements, and is read once.
+//   S^T = K Q^T: the 16 keys of a block are the rows of the product, 8 query
+//     rows its columns.  The order of head_dim along the sum is free, so a
+//     thread takes a contiguous quarter of a key's codes, and Q is laid out alike.
+//   O^T = V^T P^T: S^T's fragments, transposed in registers, are its second
+//     operand.  The order of V's columns over the rows of the product is free too:
+//     a thread takes a contiguous eighth of a key's codes, and pairs of
+//     keys are interleaved code by code before the conversion.
+// Queries are multiplied by a power of two a row that brings the largest into fp16's
+// upper range, which the scores' factor takes back: exact but for elements below
+// 2^-28 of the row's largest.
+//
+// Softmax: p = 2^{s - m} with m 8 below the maximum of the first block that the row
+// sees, moved (O and l rescaled) only when a score lies more than 15 above it: p < 2^15
+// fits fp16, and what underflows is below 2^-32 of the largest.  l sums p before rounding.
+//
+// A CTA walks its share in tiles of 128 keys, a block of 16 keys a warp; one warp
+// brings blocks by bulk copies (9 head_dim bytes each, K's and V's) into a ring.
+// A piece's eight partial results meet in shared memory.
+#include <cuda_fp16.h>
+
+#include "attention.cuh"
+#include "fp4.cuh"
+#include "ptx.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kWarps = 8;  // that compute; one more loads
+constexpr int kTN = kWarps * kFp4Block;
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kMaxRows = 16;  // of an item
+constexpr float kRise = 15.0f, kBelow = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, int NB>
+struct Shape {
+  static constexpr int kCtasPerSm = NB == 1 ? 2 : 1;
+  static constexpr int kCtas = 152 * kCtasPerSm;
+  static constexpr int kBlock = 9 * D;
+  static constexpr int kStage = 2 * kWarps * kBlock;  // K, V
+  static constexpr int kRow = D + 4;                  // floats of a row of partial results
+  static constexpr int kMerge = kWarps * 8 * kRow * 4;
+  static constexpr int kRoom = 232448 / kCtasPerSm - 2048;
+  static constexpr int kFit = (kRoom - kMerge) / kStage;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kBytes = kMerge + kStages * kStage;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sync_warps() {  // those that compute
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+}
+
+// N consecutive 32-bit words.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (N == 4) {
+    const uint4 x = *(const uint4*)p;
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *(const uint2*)p;
+    w[0] = x.x, w[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = ((const uint32_t*)p)[i];
+  }
+}
+
+struct Fp4Params {
+  AttnParams p;
+  long long wait_budget;
+  int q_vec;  // q's rows are whole 16-byte vectors
+};
+
+template <int D, int NB>  // NB blocks of 8 rows an item
+__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
+attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
+  using Sh = Shape<D, NB>;
+  constexpr int kSteps = D / 16;  // of the first product; tiles of 16 columns of the second
+  constexpr int KW = D / 32;      // words of K's codes a thread and key
+  constexpr int VW = (KW + 1) / 2;  // of V's
+  constexpr int kPer = D / 8;     // columns of O a thread and row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ AttnStart<kTN> st;
+  __shared__ uint64_t full[Sh::kStages], empty[Sh::kStages];
+  __shared__ float2 stats[2][kWarps][8 * NB];  // by the parity of the piece
+  __shared__ int flags, bad_from[2];
+  __shared__ volatile int abort_flag;
+  const AttnParams& p = fp.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + Sh::kMerge;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    flags = 0;
+    abort_flag = 0;
+    bad_from[0] = bad_from[1] = 0x7fffffff;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  wait_for_previous();
+  attn_plan<kTN>(p, &st, &flags);
+  AttnWalk<kTN> w = st.walk;
+  bool ok = true;
+  uint32_t slot = 0;  // tiles so far
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) attn_write_cut(p, st);
+    const int S = p.a.c.page_size;
+    const int e = lane & (kWarps - 1);
+    const bool mine = lane < 2 * kWarps;
+    const uint8_t* pool = (const uint8_t*)(lane < kWarps ? p.a.c.k : p.a.c.v);
+    for (; !w.done() && ok; w.next(p, &flags)) {
+      const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
+      const int t1 = w.last_tile();
+      auto key_of = [&](int t) { return t * kTN + e * kFp4Block; };
+      auto page_at = [&](int t) { return mine && t < t1 && key_of(t) < w.end ? table[key_of(t) / S] : -1; };
+      int raw = page_at(w.first_tile());
+      for (int t = w.first_tile(); t < t1 && ok; ++t, ++slot) {
+        const int next = page_at(t + 1);  // read a tile ahead
+        const int stage = (int)(slot % Sh::kStages);
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], ((slot / Sh::kStages) & 1u) ^ 1u, (volatile int*)&abort_flag,
+                                               fp.wait_budget));
+        if (!ok) break;
+        const int key = key_of(t);
+        const bool has = mine && key < w.end;
+        int pg = raw;
+        if (has && (pg < 0 || pg >= p.a.c.n_pages)) {
+          flag_status(&flags, DSPARK_DEV_BAD_INPUT);
+          pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+        }
+        const unsigned blocks = __ballot_sync(0xffffffffu, has);
+        if (lane == 0) mbar_expect_tx(&full[stage], (uint32_t)__popc(blocks) * Sh::kBlock);
+        __syncwarp();
+        if (has)
+          bulk_load(ring + stage * Sh::kStage + lane * Sh::kBlock,
+                    pool + pg * p.a.c.page_stride + w.h * p.a.c.head_stride +
+                        (long long)((key % S) / kFp4Block) * Sh::kBlock,
+                    Sh::kBlock, &full[stage]);
+        raw = next;
+      }
+    }
+    if (!ok && lane == 0)  // the loads still in flight
+      for (uint32_t i = slot > Sh::kStages ? slot - Sh::kStages : 0; i < slot; ++i)
+        mbar_drain(&full[i % Sh::kStages], (i / Sh::kStages) & 1u, fp.wait_budget);
+  } else {
+    // ------------------------------------------------------------ products
+    const int g = lane >> 2, t4 = lane & 3;
+    // Slot s of a block's eight keys holds key s ^ (s >> 1 & 1): rows of both
+    // parities meet in the reads of V, whose 64-byte rows would else fall on the same banks.
+    const int key_a = g ^ ((g >> 1) & 1);            // of the first product's row g (and 8 more)
+    const int key_v = 2 * t4 ^ (t4 & 1);             // of the second's columns 2 t4 (and 8 more)
+    const int key_w = key_v ^ 1;                     // and 2 t4 + 1
+    const int G = p.a.G;
+    uint32_t piece = 0;
+    for (; !w.done(); w.next(p, &flags), ++piece) {
+      const int rows = w.block_rows(p), row0 = w.m * p.mr, t1 = w.last_tile();
+      const int n0 = w.q.L - w.q.n + 1;  // keys that the chunk's first token sees
+      const int all_see = n0 + row0 / G;
+      uint32_t qf[NB][kSteps][2];
+      float sc[NB][2];   // of the thread's columns: rows 2 t4 and 2 t4 + 1
+      int lim[NB][2];    // keys that they see
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int a = 8 * b + g;
+        const bool live = a < rows;
+        uint32_t raw[kSteps * 2];
+#pragma unroll
+        for (int i = 0; i < kSteps * 2; ++i) raw[i] = 0u;
+        if (live) {
+          const unsigned row = row0 + a, tok = row / (unsigned)G, hq = row - tok * G;
+          const uint16_t* src = (const uint16_t*)p.a.q + (long long)(w.q.q0 + tok) * p.a.q_token_stride +
+                                (long long)(w.h * G + hq) * p.a.q_head_stride + t4 * (D / 4);
+          if (fp.q_vec) {
+#pragma unroll
+            for (int i = 0; i < kSteps / 2; ++i) {
+              const uint4 x = ((const uint4*)src)[i];
+              raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kSteps * 2; ++i) raw[i] = src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
+          }
+        }
+        uint32_t top = 0;  // the row's largest magnitude, as bf16 bits
+#pragma unroll
+        for (int i = 0; i < kSteps * 2; ++i) top = max(top, max(raw[i] & 0x7fffu, (raw[i] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^k that brings it to 2^14 .. 2^15 (field 141 - (its - 127)), as far as 2^-k is normal
+        const int field = (int)(top >> 7), up = field == 0 || field == 255 ? 127 : min(268 - field, 253);
+        const float f = __uint_as_float((uint32_t)up << 23);
+        const float back = __uint_as_float((uint32_t)(254 - up) << 23) * p.scale_log2;
+#pragma unroll
+        for (int i = 0; i < kSteps * 2; ++i)
+          qf[b][i >> 1][i & 1] = pack_half(__uint_as_float(raw[i] << 16) * f, __uint_as_float(raw[i] & 0xffff0000u) * f);
+        const int lim_a = live ? n0 + (int)((unsigned)(row0 + a) / (unsigned)G) : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sc[b][i] = __shfl_sync(0xffffffffu, back, (2 * t4 + i) * 4);
+          lim[b][i] = __shfl_sync(0xffffffffu, lim_a, (2 * t4 + i) * 4);
+        }
+      }
+      float o[NB][kSteps][4], m[NB][2], l[NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
+        m[b][0] = m[b][1] = -INFINITY;
+        l[b][0] = l[b][1] = 0.0f;
+      }
+
+      for (int t = w.first_tile(); t < t1; ++t, ++slot) {
+        const int stage = (int)(slot % Sh::kStages);
+        if (ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], (slot / Sh::kStages) & 1u, (volatile int*)&abort_flag,
+                                                 fp.wait_budget));
+        const int k0 = t * kTN + warp * kFp4Block;
+        if (k0 < w.end && ok) {
+          const uint8_t* kb = ring + stage * Sh::kStage + warp * Sh::kBlock;
+          const uint8_t* vb = kb + kWarps * Sh::kBlock;
+          const bool masked = k0 + kFp4Block > all_see;
+          // S^T
+          float s[NB][4] = {};
+          {
+            uint32_t lo[KW], hi[KW];
+            load_words<KW>(kb + key_a * (D / 2) + t4 * (D / 8), lo);
+            load_words<KW>(kb + (key_a + 8) * (D / 2) + t4 * (D / 8), hi);
+            const uint8_t* ks = kb + 8 * D + key_a * (D / 16);
+            uint32_t slo = 0, shi = 0;
+            if (KW == 4) {
+              slo = e4m3x2_to_half(*(const uint16_t*)(ks + 2 * t4));
+              shi = e4m3x2_to_half(*(const uint16_t*)(ks + 8 * (D / 16) + 2 * t4));
+            }
+#pragma unroll
+            for (int j = 0; j < KW; ++j) {
+              uint32_t fl, fh;  // the scale twice
+              if (KW == 4) {
+                fl = __byte_perm(slo, 0, j < 2 ? 0x1010 : 0x3232);
+                fh = __byte_perm(shi, 0, j < 2 ? 0x1010 : 0x3232);
+              } else {
+                const int grp = (t4 * KW + j) >> 1;
+                fl = e4m3x2_to_half(ks[grp] * 0x101u);
+                fh = e4m3x2_to_half(ks[8 * (D / 16) + grp] * 0x101u);
+              }
+              uint32_t xl[4], xh[4];
+              fp4x8_to_half(lo[j], xl);
+              fp4x8_to_half(hi[j], xh);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a[4] = {hmul2(xl[2 * h], fl), hmul2(xh[2 * h], fh), hmul2(xl[2 * h + 1], fl),
+                                       hmul2(xh[2 * h + 1], fh)};
+#pragma unroll
+                for (int b = 0; b < NB; ++b) mma16816(s[b], a, qf[b][2 * j + h][0], qf[b][2 * j + h][1]);
+              }
+            }
+          }
+          // P^T
+          uint32_t pf[NB][2];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = s[b][i] * sc[b][i & 1];
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (k0 + key_a + 8 * (i >> 1) >= lim[b][i & 1]) x[i] = -INFINITY;
+            }
+            const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
+            if (__any_sync(0xffffffffu, x0 > m[b][0] + kRise || x1 > m[b][1] + kRise)) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float mx = i ? x1 : x0;
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                if (mx > m[b][i] + kRise) {
+                  const float mn = mx - kBelow, f = ex2(m[b][i] - mn);
+                  m[b][i] = mn;
+                  l[b][i] *= f;
+#pragma unroll
+                  for (int k = 0; k < kSteps; ++k) o[b][k][i] *= f, o[b][k][i + 2] *= f;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = ex2(x[i] - (m[b][i & 1] == -INFINITY ? 0.0f : m[b][i & 1]));
+            l[b][0] += x[0] + x[2];
+            l[b][1] += x[1] + x[3];
+            pf[b][0] = transpose8x8(pack_half(x[0], x[1]));
+            pf[b][1] = transpose8x8(pack_half(x[2], x[3]));
+          }
+          // O^T
+          {
+            uint32_t v[4][VW];  // keys key_v, key_w, and 8 more
+            uint32_t vs[4][KW == 3 ? 3 : 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = (i & 1 ? key_w : key_v) + 8 * (i >> 1);
+              const uint8_t* row = vb + key * (D / 2) + g * (D / 16);
+              if constexpr (KW == 4 || KW == 2) {
+                load_words<VW>(row, v[i]);
+              } else {
+                v[i][0] = *(const uint16_t*)row;
+                if (KW == 3) {
+                  v[i][0] |= (uint32_t)((const uint16_t*)row)[1] << 16;
+                  v[i][VW - 1] = ((const uint16_t*)row)[2];
+                }
+              }
+              const uint8_t* scale = vb + 8 * D + key * (D / 16);
+#pragma unroll
+              for (int u = 0; u < (KW == 3 ? 3 : 1); ++u) {
+                uint32_t sv = scale[KW == 3 ? (3 * g + u) >> 2 : g * KW >> 2];
+                if (masked) {
+                  // Past the item's end: any bytes.  Where some rows of the block do not see the
+                  // key, a scale that is NaN is hidden from them, and makes the others NaN below.
+                  if (k0 + key >= all_see && (k0 + key >= w.end || (sv & 0x7fu) == 0x7fu)) {
+                    if (k0 + key < w.end) atomicMin(&bad_from[piece & 1], k0 + key);
+                    sv = 0u;
+                  }
+                }
+                vs[i][u] = sv;
+              }
+            }
+#pragma unroll
+            for (int wi = 0; wi < VW; ++wi) {
+              // Code by code: even columns in x, odd ones in y, the pair's two keys beside one another.
+              uint32_t x[2][4], y[2][4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t a = v[2 * i][wi], c = v[2 * i + 1][wi];
+                fp4x8_to_half((a & 0x0f0f0f0fu) | ((c << 4) & 0xf0f0f0f0u), x[i]);
+                fp4x8_to_half(((a >> 4) & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u), y[i]);
+              }
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int mt = 4 * wi + c;
+                if (mt >= kSteps) break;
+                const int u = KW == 3 ? mt >> 1 : 0;
+                const uint32_t f0 = e4m3x2_to_half(vs[0][u] | vs[1][u] << 8);
+                const uint32_t f1 = e4m3x2_to_half(vs[2][u] | vs[3][u] << 8);
+                const uint32_t a[4] = {hmul2(x[0][c], f0), hmul2(y[0][c], f0), hmul2(x[1][c], f1), hmul2(y[1][c], f1)};
+#pragma unroll
+                for (int b = 0; b < NB; ++b) mma16816(o[b][mt], a, pf[b][0], pf[b][1]);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+      }
+
+      // The eight warps' results.  (stats and bad_from of two pieces take turns: a warp
+      // writes those of piece n + 2 after the barriers of piece n + 1.)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], d);
+          if (g == 0) stats[piece & 1][warp][8 * b + 2 * t4 + i] = make_float2(m[b][i], l[b][i]);
+        }
+      const int where = attn_slot(w);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (8 * b >= rows) break;
+        sync_warps();  // stats; the block before is read
+        if (b == 0 && threadIdx.x == 0) bad_from[(piece + 1) & 1] = 0x7fffffff;  // (none is at the next piece yet)
+        float* buf = (float*)smem;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int a = 2 * t4 + i;
+          float top = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) top = fmaxf(top, stats[piece & 1][x][8 * b + a].x);
+          const float f = m[b][i] == -INFINITY ? 0.0f : ex2(m[b][i] - top);
+          float* dst = buf + (warp * 8 + a) * Sh::kRow + g * kPer;
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            const float4 v = make_float4(o[b][k][i] * f, o[b][k][i + 2] * f, o[b][k + 1][i] * f, o[b][k + 1][i + 2] * f);
+            *(float4*)(dst + 2 * k) = v;
+          }
+        }
+        sync_warps();
+        const int bad = *(volatile int*)&bad_from[piece & 1];
+        for (int i = threadIdx.x; i < 8 * (D / 4); i += kWarps * 32) {
+          const int a = i / (D / 4), d = i % (D / 4) * 4, r = 8 * b + a;
+          if (r >= rows) continue;
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            const float4 v = *(const float4*)(buf + (x * 8 + a) * Sh::kRow + d);
+            y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+            top = fmaxf(top, stats[piece & 1][x][r].x);
+          }
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            const float2 q = stats[piece & 1][x][r];
+            sum += q.x == -INFINITY ? q.y : q.y * ex2(q.x - top);  // (q.y: 0, or NaN)
+          }
+          const unsigned row = row0 + r, tok = row / (unsigned)G, hq = row - tok * G;
+          if (n0 + (int)tok > bad) sum = __int_as_float(0x7fc00000);
+          if (where < 0) {
+            const size_t out = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + hq;
+            const float inv = sum > 0.0f ? p.a.v_factor / sum : sum == 0.0f ? 0.0f : sum;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * inv, y.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * inv, y.w * inv);
+            *(uint2*)((__nv_bfloat16*)p.a.out + out * D + d) = make_uint2(*(const uint32_t*)&lo, *(const uint32_t*)&hi);
+            if (d == 0) p.a.lse[out] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+          } else {
+            const size_t part = ((size_t)blockIdx.x * 2 + where) * kMaxRows + r;
+            const float f = p.a.v_factor;
+            *(float4*)(p.part + part * D + d) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+            if (d == 0) p.stats[part] = make_float2(top, sum);
+          }
+        }
+      }
+    }
+  }
+  if (abort_flag && lane == 0) flag_status(&flags, DSPARK_DEV_TIMEOUT);
+  __syncthreads();
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = flags;
+}
+
+template <int D, int NB>
+cudaError_t launch(Fp4Params fp, char* ws, cudaStream_t s) {
+  using Sh = Shape<D, NB>;
+  static_assert(Sh::kCtas <= kAttnMaxCtas && Sh::kStages >= 2, "");
+  const AttnWorkspace w = attn_workspace_layout(kMaxRows, D, Sh::kCtas);
+  AttnParams& p = fp.p;
+  p.status = (int*)ws;
+  p.flags = (int*)(ws + w.flags);
+  p.cuts = (CutItem*)(ws + w.cuts);
+  p.stats = (float2*)(ws + w.stats);
+  p.part = (float*)(ws + w.out);
+  p.mr = 8 * NB;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      attention_fp4_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+  if (attr != cudaSuccess) return attr;
+  cudaLaunchAttribute attr_pdl;
+  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(Sh::kCtas), kThreads, Sh::kBytes, s, &attr_pdl);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_fp4_kernel<D, NB>, fp);
+  return e != cudaSuccess ? e : launch_attn_combine(p, kMaxRows, Sh::kCtas, s);
+}
+
+// Rows of most requests: where there are no more tokens than requests, a token's.
+long long fp4_rows(const AttnArgs& a) { return a.a.n_tokens <= a.a.R ? a.G : attn_likely_rows(a); }
+
+template <int D>
+cudaError_t launch_rows(const Fp4Params& fp, char* ws, cudaStream_t s) {
+  return fp4_rows(fp.p.a) <= 8 ? launch<D, 1>(fp, ws, s) : launch<D, 2>(fp, ws, s);
+}
+
+}  // namespace
+
+size_t attention_fp4_rows_workspace_bytes(int head_dim) {
+  return attn_workspace_layout(kMaxRows, head_dim, kAttnMaxCtas).total;
+}
+
+bool attention_fp4_rows_supported(const AttnArgs& a) {
+  return a.fp4 && a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0;
+}
+
+cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s) {
+  Fp4Params fp;
+  fp.p = AttnParams{a};
+  fp.p.scale_log2 = a.scale * 1.4426950408889634f;
+  fp.p.item_units = 1;
+  fp.wait_budget = kWaitBudget;
+  fp.q_vec = ((uintptr_t)a.q & 15u) == 0 && a.q_head_stride % 8 == 0 && a.q_token_stride % 8 == 0;
+  switch (a.c.head_dim) {
+    case 32: return launch_rows<32>(fp, ws, s);
+    case 64: return launch_rows<64>(fp, ws, s);
+    case 96: return launch_rows<96>(fp, ws, s);
+    default: return launch_rows<128>(fp, ws, s);
+  }
+}
+
+}  // namespace dspark
