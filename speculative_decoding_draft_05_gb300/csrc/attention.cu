@@ -76,24 +76,6 @@ __device__ __forceinline__ float4 load4_fp4(const uint8_t* codes, const uint8_t*
   return make_float4(half_lo(h[0]) * s, half_hi(h[0]) * s, half_lo(h[1]) * s, half_hi(h[1]) * s);
 }
 
-// Division of n < 2^31 by a divisor known at launch: a multiplication and
-// shifts (Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994).
-struct Divider {
-  unsigned mul, sh1, sh2;
-  explicit Divider(unsigned d) {
-    unsigned l = 0;
-    while ((1ull << l) < d) ++l;
-    mul = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
-    sh1 = l < 1 ? l : 1;
-    sh2 = l < 1 ? 0 : l - 1;
-  }
-  __device__ __forceinline__ int operator()(int n) const {
-    const unsigned t = __umulhi(mul, (unsigned)n);
-    return (int)((t + (((unsigned)n - t) >> sh1)) >> sh2);
-  }
-};
-
 // A warp's rows: reference m (the same in all lanes), this lane's part of the
 // sum l, and the output columns 2 lane + 64 k and the next.
 template <int NP>
@@ -525,14 +507,14 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
 }
 
 size_t attention_fp4_workspace_bytes(int dtype, int head_dim) {
-  const size_t simt = attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
-  if (dtype != DSPARK_BF16 || head_dim > 128) return simt;
-  const size_t rows = attention_fp4_rows_workspace_bytes(head_dim);
-  return rows > simt ? rows : simt;
+  if (dtype != DSPARK_BF16 || head_dim > 128) return attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
+  const size_t rows = attention_fp4_rows_workspace_bytes(head_dim), tc = attention_tc_workspace_bytes(head_dim);
+  return tc > rows ? tc : rows;
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
-  if (attention_fp4_rows_supported(a)) return launch_attention_fp4_rows(a, ws, s);
+  if (a.fp4 && attention_fp4_few_rows(a)) return launch_attention_fp4_rows(a, ws, s);
+  if (attention_tc_fp4_supported(a)) return launch_attention_tc_fp4(a, ws, s);
   if (!a.fp4 && attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kSimtCtas);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),

@@ -503,8 +503,8 @@ size_t attention_fp4_rows_workspace_bytes(int head_dim) {
   return attn_workspace_layout(kMaxRows, head_dim, kAttnMaxCtas).total;
 }
 
-bool attention_fp4_rows_supported(const AttnArgs& a) {
-  return a.fp4 && a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0;
+bool attention_fp4_few_rows(const AttnArgs& a) {
+  return a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0 && fp4_rows(a) <= kMaxRows;
 }
 
 cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s) {

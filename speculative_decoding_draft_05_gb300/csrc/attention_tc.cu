@@ -65,6 +65,7 @@
 #include <type_traits>
 
 #include "attention.cuh"
+#include "fp4.cuh"
 #include "ptx.cuh"
 
 namespace dspark {
@@ -76,30 +77,58 @@ constexpr int kTN = 128;  // keys of a tile
 constexpr int kEarly = 96;  // of which the first are multiplied while the rest of P is in the making
 constexpr int kMaxCtas = 152;  // one an SM of GB300; what the workspace holds pieces of
 static_assert(kMaxCtas <= kAttnMaxCtas, "");
-constexpr int kThreads = 512;  // four warpgroups: two of softmax, the single roles, the results
+// Four warpgroups: two of softmax, the single roles, the results; with a 4-bit
+// cache two more that turn codes into the products' operands.
+template <bool FP4>
+constexpr int kThreads = FP4 ? 768 : 512;
 // Registers a thread after the split: 256 x 168 + 128 x 96 + 128 x 80 of the
-// launch's 512 x 128.
-constexpr int kRegsSoftmax = 168, kRegsOther = 96, kRegsResult = 80;
+// launch's 512 x 128; with a 4-bit cache 256 x 112 + 128 x 56 + 128 x 88 + 256 x
+// 56 of 768 x 80.
+template <bool FP4>
+constexpr int kRegsSoftmax = FP4 ? 112 : 168;
+template <bool FP4>
+constexpr int kRegsOther = FP4 ? 56 : 96;
+template <bool FP4>
+constexpr int kRegsResult = FP4 ? 88 : 80;
+constexpr int kRegsDecode = 56;
+template <bool FP4>
+constexpr int kRegsLaunch = FP4 ? 80 : 128;
+static_assert(256 * kRegsSoftmax<false> + 128 * kRegsOther<false> + 128 * kRegsResult<false> <=
+                  kThreads<false> * kRegsLaunch<false>, "a split above the launch's registers waits forever");
+static_assert(256 * kRegsSoftmax<true> + 128 * kRegsOther<true> + 128 * kRegsResult<true> + 256 * kRegsDecode <=
+                  kThreads<true> * kRegsLaunch<true>, "a split above the launch's registers waits forever");
+static_assert(kThreads<true> * kRegsLaunch<true> <= 65536 && kThreads<false> * kRegsLaunch<false> <= 65536, "registers");
 constexpr int kFirstRoleWarp = 8;  // (8 idles: warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
 constexpr int kMmaWarp = 9, kLoaderWarp = 10, kProducerWarp = 11, kResultWarp = 12;
+constexpr int kDecodeWarp = 16, kDecodeWarps = 4;  // (4-bit) two teams, tiles in turn, a quarter of the keys a warp
 constexpr float kRangeLog2 = 60.0f;
+// P in fp16 (4-bit): m is kBelow below the maximum that sets it, and stays until a
+// score lies kRise above it: p < 2^15, and what underflows is below 2^-31 of the largest.
+constexpr float kRise = 15.0f, kBelow = 8.0f, kLeast = 7.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTmemCols = 512;  // S0, S1, O0, O1: 128 columns each
 
 // Shared memory for head_dim padded to DP (64 or 128), from a 1024-aligned base.
-template <int DP>
+template <int DP, bool FP4>
 struct Layout {
   static constexpr int kHalves = DP / 64;
   static constexpr int kHalfBytes = 128 * 128;             // 128 rows of 128 bytes
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
-  static constexpr int kStages = DP == 128 ? 5 : 10;
+  static constexpr int kStages = FP4 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
+  // (4-bit) tiles as the cache holds them, and the factors of Q's rows
+  static constexpr int kRawStages = FP4 ? (DP == 128 ? 6 : 12) : 0;
+  static constexpr int kRawBytes = kTN / kFp4Block * fp4_block_bytes(DP);
   static constexpr int kOffQ = 0;  // two row blocks, or this piece's and the next one's rows
   static constexpr int kOffRing = 2 * kTileBytes;
-  static constexpr int kOffMerge = kOffRing + kStages * kTileBytes;  // (m, l) [2][128]
+  static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffTile = kOffRaw + kRawStages * kRawBytes;   // RawTile [kRawStages]
+  static constexpr int kOffScale = kOffTile + kRawStages * 16;        // [2][128]
+  static constexpr int kOffMerge = kOffScale + (FP4 ? 2 * 128 * 4 : 0);  // (m, l) [2][128]
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
-  static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1;
-  static constexpr int kOffBad = kOffBar + kBars * 8;  // [2] words (see bad_v)
-  static constexpr int kOffPiece = (kOffBad + 2 * 8 + 12 + 15) & ~15;  // PieceInfo [4]
+  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1 + (FP4 ? 2 : 0);
+  static constexpr int kBadWords = FP4 ? 4 : 2;
+  static constexpr int kOffBad = kOffBar + kBars * 8;  // (see bad_v)
+  static constexpr int kOffPiece = (kOffBad + kBadWords * 8 + 12 + 15) & ~15;  // PieceInfo [4]
   // The plan has room of its own: the roles read it after the last barrier of
   // all threads, so nothing may be written over it.
   static constexpr int kOffStart = (kOffPiece + 4 * 64 + 15) & ~15;
@@ -108,13 +137,15 @@ struct Layout {
   // static shared memory; the slack covers most others, and the kernel checks.
   static constexpr int kBytes = kEnd + 1024 < 232448 ? kEnd + 1024 : 232448;
 };
-static_assert(Layout<64>::kEnd <= 232448 && Layout<128>::kEnd <= 232448, "shared memory");
-template <int DP>
+static_assert(Layout<64, false>::kEnd <= 232448 && Layout<128, false>::kEnd <= 232448, "shared memory");
+static_assert(Layout<64, true>::kEnd <= 232448 && Layout<128, true>::kEnd <= 232448, "shared memory");
+template <int DP, bool FP4>
 constexpr bool plan_apart() {  // from all that is written while roles may still read it
-  using Lo = Layout<DP>;
+  using Lo = Layout<DP, FP4>;
   return Lo::kOffStart >= Lo::kOffMerge + 2 * 128 * 8 && Lo::kOffStart >= Lo::kOffPiece + 4 * 64;
 }
-static_assert(plan_apart<64>() && plan_apart<128>(), "the plan's room");
+static_assert(plan_apart<64, false>() && plan_apart<128, false>(), "the plan's room");
+static_assert(plan_apart<64, true>() && plan_apart<128, true>(), "the plan's room");
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -207,9 +238,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
-// Instruction descriptor, kind::f16: fp32 accumulator, bf16 operands, A K-major.
-__host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool b_n_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_n_major ? 1u : 0u) << 16) |
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 operands (or fp16), A K-major.
+__host__ __device__ constexpr uint32_t make_idesc(int M, int N, bool b_n_major, bool half) {
+  return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | ((b_n_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
@@ -294,7 +325,9 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 
 // Whether a tile's row maximum (log2 units) is too far from the reference m:
 // above it, or, before anything is summed, below it (-inf: no key seen).
+template <bool FP4>
 __device__ __forceinline__ bool out_of_range(float mx, float m, bool first) {
+  if (FP4) return mx > m + kRise || (first && mx < m + kLeast && mx > -INFINITY);
   return mx > m + kRangeLog2 || (first && mx < m - kRangeLog2 && mx > -INFINITY);
 }
 
@@ -333,21 +366,60 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Accesses by shared-memory address.
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared2(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A warp's registers from the launch's number to N.
+template <int Launch, int N>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (N > Launch)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 struct TcParams {
+  explicit TcParams(int G) : by_g((unsigned)G) {}
   AttnParams p;
   int box_tokens;  // tokens of a K/V box: the largest power of two in page_size, up to 128
   int q_tokens;    // tokens of a Q tile (a box): 128 / G
   int tile_rows;   // rows of a Q tile: q_tokens G (128 where G > 128)
   int q_tma;       // q can be loaded by TMA (else by the loader's threads)
+  int q_vec;       // (4-bit) q's rows are whole 16-byte vectors
+  Divider by_g;    // (4-bit)
   float sign;      // of the scale; |scale| is in p.scale_log2
   long long wait_budget;
 };
@@ -374,11 +446,56 @@ struct alignas(16) PieceInfo {
 };
 static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+// The order in which tiles pass through the ring.  With two row blocks K0 V0 K1 V1 ..;
+// over a run of smaller pieces, whose products run a tile ahead, K0 K1 V0 K2 V1 ..
+// load(is_v, t, piece): one tile; open(walk, n): the piece of which the next K tiles are.
+struct TilePiece {
+  int h, end, all_see, n;
+  const int32_t* table;
+};
+template <typename Load>
+__device__ __forceinline__ bool walk_tiles(AttnWalk<kTN> w, const AttnParams& p, int tile_rows, int* flags,
+                                           Load load) {
+  bool ok = true, pending = false;  // a V that the next K goes before
+  int pend_t = 0, n = 0;
+  TilePiece pend = {};
+  for (; !w.done() && ok; w.next(p, flags), ++n) {
+    const TilePiece c{w.h, w.end, w.q.L - w.q.n + 1 + w.m * p.mr / p.a.G, n,
+                      p.a.a.page_table + (size_t)w.r * p.a.a.max_pages};
+    const bool two = w.block_rows(p) > tile_rows;
+    if (two && pending) {
+      ok = load(true, pend_t, pend);
+      pending = false;
+    }
+    const int t1 = w.last_tile();
+    for (int t = w.first_tile(); t < t1 && ok; ++t) {
+      ok = load(false, t, c);
+      if (two) {
+        ok = ok && load(true, t, c);
+      } else {
+        if (pending) ok = ok && load(true, pend_t, pend);
+        pending = true;
+        pend_t = t, pend = c;
+      }
+    }
+  }
+  if (ok && pending) ok = load(true, pend_t, pend);
+  return ok;
+}
+
+// What the decoding warps have to know of a tile of codes (its loader writes it).
+struct alignas(16) RawTile {
+  int key0;     // -1: no more tiles
+  int end;      // keys of the item from key0 on
+  int all_see;  // of which all rows of the block see this many
+  int tag;      // piece + 1, of a tile of V; else 0
+};
+
+template <int DP, bool FP4>
+__global__ void __launch_bounds__(kThreads<FP4>, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TcParams tp) {
-  using Lo = Layout<DP>;
+  using Lo = Layout<DP, FP4>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const AttnParams& p = tp.p;
@@ -401,11 +518,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* h_full = o_free + 2;   // [2] P's first kEarly keys written (4 warps)
   uint64_t* h_done = h_full + 2;   // [2] and their product done
   uint64_t* drain = h_done + 2;
+  uint64_t* raw_full = drain + 1;                // (4-bit) a tile's codes loaded
+  uint64_t* raw_empty = raw_full + Lo::kRawStages;  // and read (the decoding warps)
+  uint64_t* i_full = raw_empty + Lo::kRawStages;    // (4-bit) [2] piece n (n & 1) published
   // Piece n's first key with a V that is not finite among those that not all of
-  // its rows see: word n & 1, (n + 1) << 32 | 2^31 - 1 - key, the largest counts.
+  // its rows see: word n & 1 (4-bit: n & 3, as codes are decoded ahead of the piece before's results), (n + 1) << 32 | 2^31 - 1 - key, the largest counts.
   // (Of another piece: none.  The tag spares the clearing between pieces.)
   unsigned long long* bad_v = (unsigned long long*)(smem + Lo::kOffBad);
-  uint32_t* tmem_slot = (uint32_t*)(bad_v + 2);
+  uint32_t* tmem_slot = (uint32_t*)(bad_v + Lo::kBadWords);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   int* flags = (int*)(tmem_slot + 2);  // the CTA's status bits
   AttnStart<kTN>* st = (AttnStart<kTN>*)(smem + Lo::kOffStart);
@@ -413,14 +533,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   PieceInfo* infos = (PieceInfo*)(smem + Lo::kOffPiece);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == kProducerWarp * 32) {
+  if (!FP4 && threadIdx.x == kProducerWarp * 32) {
     prefetch_map(&tmK);
     prefetch_map(&tmV);
   }
-  if (threadIdx.x == kLoaderWarp * 32 && tp.q_tma) prefetch_map(&tmQ);
+  if (!FP4 && threadIdx.x == kLoaderWarp * 32 && tp.q_tma) prefetch_map(&tmQ);
   if (threadIdx.x == 0) {
     for (int i = 0; i < Lo::kStages; ++i) {
-      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_full[i], FP4 ? kDecodeWarps : 1);
       mbar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -428,7 +548,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       mbar_init(&p_full[i], 4);
       mbar_init(&h_full[i], 4);
       mbar_init(&h_done[i], 1);
-      mbar_init(&q_full[i], 1);
+      mbar_init(&q_full[i], FP4 ? 4 : 1);
+      if (FP4) mbar_init(&i_full[i], 1);
       mbar_init(&q_empty[i], 13);
       mbar_init(&o_full[i], 1);
     }
@@ -437,10 +558,19 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     mbar_init(&o_free[0], 4);
     mbar_init(&o_free[1], 4);
     mbar_init(drain, 1);
-    bad_v[0] = bad_v[1] = 0ull;
+    for (int i = 0; i < Lo::kRawStages; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kDecodeWarps);
+    }
+    for (int i = 0; i < Lo::kBadWords; ++i) bad_v[i] = 0ull;
     *abort_flag = 0;
     *flags = 0;
     fence_barrier_init();
+  }
+  if (FP4 && p.a.c.head_dim < DP) {  // the columns that no code fills
+    for (int i = threadIdx.x; i < Lo::kStages * Lo::kTileBytes / 16; i += kThreads<FP4>)
+      ((uint4*)(smem + Lo::kOffRing))[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -460,9 +590,154 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
   // (The register split stands in each role's own branch: after a join the
   // compiler would hold every role to the smaller number.)
-  if (warp == kProducerWarp) {
+  if (FP4 && warp >= kDecodeWarp) {
+    // ------------------------------------------------------------ decoding (4-bit)
+    if constexpr (FP4) {
+      set_regs<kRegsLaunch<FP4>, kRegsDecode>();
+      const int D = p.a.c.head_dim, block = fp4_block_bytes(D);
+      const int team = (warp - kDecodeWarp) / kDecodeWarps, row0 = (warp - kDecodeWarp) % kDecodeWarps * 32;
+      const RawTile* tiles = (const RawTile*)(smem + Lo::kOffTile);
+      for (uint32_t sl = team;; sl += 2) {
+        const int stage = (int)(sl % Lo::kStages), rs = (int)(sl % Lo::kRawStages);
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], (sl / Lo::kRawStages) & 1u, abort_flag, tp.wait_budget));
+        if (!ok) break;
+        const RawTile c = tiles[rs];
+        if (c.key0 < 0) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], ((sl / Lo::kStages) & 1u) ^ 1u, abort_flag,
+                                               tp.wait_budget));
+        if (!ok) break;
+        const uint32_t raw = smem_addr(smem + Lo::kOffRaw) + rs * Lo::kRawBytes;
+        const uint32_t tile = smem_addr(smem + Lo::kOffRing) + stage * Lo::kTileBytes;
+        const bool masked = c.all_see < kTN;
+        // A unit: 32 elements of a key, 16 bytes x of codes and two scales, to the four 16-byte chunks
+        // of the row from `to` on (a row's chunk k at to ^ 16 k).
+        auto decode = [&](int row, uint4 x, uint32_t sc, uint32_t to, auto offset) {
+          if (masked && row >= c.all_see) {
+            // Past the item's end: any bytes.  Where some rows of the block do not see the key, V's
+            // scales that are NaN are hidden from them, and make the others NaN in the results.
+            if (row >= c.end) {
+              sc = 0u;
+            } else if (c.tag && ((sc & 0x7fu) == 0x7fu || (sc & 0x7f00u) == 0x7f00u)) {
+              sc = 0u;
+              atomicMax(&bad_v[(c.tag - 1) & 3], (unsigned long long)c.tag << 32 | (uint32_t)(0x7fffffff - (c.key0 + row)));
+            }
+          }
+          const uint32_t s2 = e4m3x2_to_half(sc), f0 = __byte_perm(s2, 0, 0x1010), f1 = __byte_perm(s2, 0, 0x3232);
+          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            fp4x8_to_half(w4[k], h);
+            const uint32_t f = k < 2 ? f0 : f1;
+            st_shared16((to ^ (k << 4)) + offset, hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f), hmul2(h[3], f));
+          }
+        };
+        if (D == DP) {
+          // Eight rows a step (64-element rows: 16), all loaded before the first is decoded.  Eight
+          // consecutive lanes have one half's columns, so that their stores do not meet on a bank.
+          constexpr int kUnits = DP / 32, kRows = 32 / kUnits;  // of a key; keys a step
+          const int r = DP == 128 ? (lane >> 1) & 7 : lane >> 1, col = (lane & 1) + (DP == 128 ? lane >> 4 << 1 : 0);
+          const uint32_t from = raw + (row0 >> 4) * fp4_block_bytes(DP) + r * (DP / 2) + col * 16;
+          const uint32_t scale = raw + (row0 >> 4) * fp4_block_bytes(DP) + 8 * DP + r * (DP / 16) + col * 2;
+          const uint32_t to = tile + (col >> 1) * Lo::kHalfBytes + swz(row0 + r, (col & 1) * 4);
+          uint4 x[kUnits];
+          uint32_t sc[kUnits];
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int b = i * kRows / 16 * fp4_block_bytes(DP), q = i * kRows % 16;
+            x[i] = ld_shared16(from + b + q * (DP / 2));
+            sc[i] = ld_shared2(scale + b + q * (DP / 16));
+          }
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) decode(row0 + i * kRows + r, x[i], sc[i], to, i * kRows * 128);
+        } else {
+          const int units = D / 32;
+          for (int u = lane; u < 32 * units; u += 32) {
+            const int r = u / units, col = u - r * units, row = row0 + r;
+            const uint32_t b = raw + (row >> 4) * block;
+            decode(row, ld_shared16(b + (row & 15) * (D / 2) + col * 16),
+                   ld_shared2(b + 8 * D + (row & 15) * (D / 16) + col * 2),
+                   tile + (col >> 1) * Lo::kHalfBytes + swz(row, (col & 1) * 4), 0);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[rs]);
+          mbar_arrive(&kv_full[stage]);
+        }
+      }
+    }
+  } else if (FP4 && warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer (4-bit)
+    if constexpr (FP4) {
+      set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
+      const int S = p.a.c.page_size, block = fp4_block_bytes(p.a.c.head_dim);
+      constexpr int kBlocks = kTN / kFp4Block;  // of a tile; a lane looks one up
+      constexpr int kTiles = 32 / kBlocks;      // looked up at once, the next ones ahead
+      uint32_t slot = 0;
+      int ids = 0, ids_next = 0, from = 0, piece = -1;  // pages of tiles from ..
+      int pg = 0, pg_before = 0, pg_t = -1;             // of the last K tile, and the one before
+      ok = walk_tiles(st->walk, p, tp.tile_rows, flags, [&](bool is_v, int t, const TilePiece& c) {
+        const int rs = (int)(slot % Lo::kRawStages);
+        const int key = t * kTN + lane * kFp4Block;
+        const bool has = lane < kBlocks && key < c.end;
+        if (!is_v) {
+          auto look_up = [&](int t0) {
+            const int k = t0 * kTN + lane * kFp4Block;
+            return k < c.end ? c.table[k / S] : 0;
+          };
+          if (c.n != piece) {
+            piece = c.n, from = t;
+            ids = look_up(from), ids_next = look_up(from + kTiles);
+          } else if (t == from + kTiles) {
+            from = t;
+            ids = ids_next, ids_next = look_up(from + kTiles);
+          }
+          pg_before = pg;
+          pg = __shfl_sync(0xffffffffu, ids, (t - from) * kBlocks + (lane & (kBlocks - 1)));
+          pg_t = t;
+          if (has && (pg < 0 || pg >= p.a.c.n_pages)) {
+            flag_status(flags, DSPARK_DEV_BAD_INPUT);
+            pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+          }
+        }
+        const int page = is_v && !(t == pg_t && c.n == piece) ? pg_before : pg;
+        if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[rs], ((slot / Lo::kRawStages) & 1u) ^ 1u, abort_flag,
+                                               tp.wait_budget)))
+          return false;
+        const unsigned blocks = __ballot_sync(0xffffffffu, has);
+        if (lane == 0) {
+          ((RawTile*)(smem + Lo::kOffTile))[rs] =
+              RawTile{t * kTN, c.end - t * kTN, c.all_see - t * kTN, is_v ? c.n + 1 : 0};
+          mbar_expect_tx(&raw_full[rs], (uint32_t)__popc(blocks) * block);
+        }
+        __syncwarp();
+        if (has)
+          bulk_load(smem + Lo::kOffRaw + rs * Lo::kRawBytes + lane * block,
+                    (const uint8_t*)(is_v ? p.a.c.v : p.a.c.k) + page * p.a.c.page_stride + c.h * p.a.c.head_stride +
+                        (long long)((key % S) / kFp4Block) * block,
+                    block, &raw_full[rs]);
+        ++slot;
+        return true;
+      });
+      for (int i = 0; i < 2 && ok; ++i, ++slot) {  // to each team: no more tiles
+        const int rs = (int)(slot % Lo::kRawStages);
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[rs], ((slot / Lo::kRawStages) & 1u) ^ 1u, abort_flag,
+                                               tp.wait_budget));
+        if (!ok) break;
+        if (lane == 0) {
+          ((RawTile*)(smem + Lo::kOffTile))[rs].key0 = -1;
+          mbar_arrive(&raw_full[rs]);
+        }
+      }
+      if (!ok && lane == 0)  // the loads still in flight
+        for (uint32_t i = slot > Lo::kRawStages ? slot - Lo::kRawStages : 0; i < slot; ++i)
+          mbar_drain(&raw_full[i % Lo::kRawStages], (i / Lo::kRawStages) & 1u, tp.wait_budget);
+    }
+  } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
-    regs_dec<kRegsOther>();
+    set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
     AttnWalk<kTN> w = st->walk;
     const int bt = tp.box_tokens, E = kTN / bt;  // boxes along a tile's keys
     const int S = p.a.c.page_size;
@@ -531,10 +806,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    regs_dec<kRegsOther>();
+    set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
     {
       const uint32_t lead = elect_one();
-      const uint32_t id_s = make_idesc(128, kTN, false), id_o = make_idesc(128, DP, true);
+      const uint32_t id_s = make_idesc(128, kTN, false, FP4), id_o = make_idesc(128, DP, true, FP4);
       const uint32_t q0 = smem_addr(smem + Lo::kOffQ), ring = smem_addr(smem + Lo::kOffRing);
       uint32_t slot = 0;  // next ring slot, in the order of use
       uint32_t n = 0, steps0 = 0, steps1 = 0;  // piece, P tiles of each stream so far
@@ -680,7 +955,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
   } else if (warp < kFirstRoleWarp) {
     // ------------------------------------------------------------ softmax
-    regs_inc<kRegsSoftmax>();
+    set_regs<kRegsLaunch<FP4>, kRegsSoftmax<FP4>>();
     const int s = warp >> 2;               // stream
     const int trow = threadIdx.x & 127;    // row in the 128-row tile (TMEM lane)
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp
@@ -693,6 +968,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       ok = __all_sync(0xffffffffu, mbar_wait(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget));
       if (!ok) break;
       const PieceInfo c = infos[n & 3];
+      float scale = p.scale_log2;
+      if (FP4) scale = ((const float*)(smem + Lo::kOffScale))[(c.rows > tp.tile_rows ? s : (int)(n & 1)) * 128 + trow];
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[n & 1]);
       if (c.nt == 0) break;
@@ -703,7 +980,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       // Keys the row sees (rows past the block's: their scores are left as they
       // are, since a mask would slow the whole warp, and they are never read).
       const int lim = live ? c.lim + (c.row0 + a) / p.a.G : 0x7fffffff;
-      float m = 0.0f, l = 0.0f;  // the reference in use, and the sum relative to it
+      float m = FP4 ? -kBelow : 0.0f, l = 0.0f;  // the reference in use, and the sum relative to it
       bool first = true;
       // This stream's tiles: all with two row blocks, else those on steps of its parity.
       for (int j = two ? 0 : (int)((s ^ run) & 1u); j < c.nt; j += two ? 1 : 2) {
@@ -716,6 +993,85 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         bool early = false;  // P's first kEarly keys are handed over
         if (warp_live) {
           const int vis = lim - k0;  // keys of the tile that the row sees
+          if constexpr (FP4) {
+            // Two passes over S, the maximum and the probabilities: m is set before any of P is
+            // written, which fp16's range asks for, and the threads get by with few registers.
+            const bool masked = __any_sync(0xffffffffu, vis < kTN);
+            uint32_t xa[32], xb[32];
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto largest = [&](uint32_t* x, int k) {
+              if (masked) mask_from<32>(x, vis - k);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                top[i / 2 & 3] = fmax3(top[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            };
+            tmem_ld32(tS, xa);
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 32, xb);
+            largest(xa, 0);
+            tmem_wait_ld32(xb);
+            tmem_ld32(tS + 64, xa);
+            largest(xb, 32);
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 96, xb);
+            largest(xa, 64);
+            tmem_wait_ld32(xb);
+            tmem_ld32(tS, xa);
+            largest(xb, 96);
+            const float mx = fmax3(fmaxf(top[0], top[1]), top[2], top[3]) * scale;
+            const bool grow = live && out_of_range<true>(mx, m, l == 0.0f);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float mn = grow ? mx - kBelow : m;
+              const float f = grow && l != 0.0f ? ex2(m - mn) : 1.0f;
+              tmem_wait_ld32(xa);
+              if (!first) {  // (before, O is the piece before's, whose products may go on)
+#pragma unroll 1
+                for (int k = 0; k < DP; k += 32) {
+                  tmem_ld32(tO + s * 128 + k, xb);
+                  tmem_wait_ld32(xb);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * f);
+                  tmem_st32(tO + s * 128 + k, xb);
+                }
+              }
+              l *= f;
+              m = mn;
+            }
+            const f32x2 sc2 = pack2(scale, scale), ms2 = pack2(-m, -m);
+            f32x2 sum2[2] = {0ull, 0ull};
+            auto chunk = [&](uint32_t* x, int k) {
+              uint32_t pk[16];
+              if (masked) mask_from<32>(x, vis - k);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float y0, y1;
+                unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, ms2), y0, y1);
+                const float e0 = ex2(y0), e1 = ex2(y1);
+                sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
+                pk[i] = pack_half(e0, e1);
+              }
+              tmem_st16(tS + k / 2, pk);  // (over scores that are read by then)
+            };
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 32, xb);
+            chunk(xa, 0);
+            tmem_wait_ld32(xb);
+            tmem_ld32(tS + 64, xa);
+            chunk(xb, 32);
+            tmem_wait_ld32(xa);
+            tmem_ld32(tS + 96, xb);
+            chunk(xa, 64);
+            tmem_wait_ld32(xb);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&h_full[s]);
+            early = true;
+            chunk(xb, 96);
+            float s0, s1;
+            unpack2(add2(sum2[0], sum2[1]), s0, s1);
+            l += s0 + s1;
+          } else {
           // (By the piece's tile as well: V is looked through before any warp hands P
           // over early.  By that alone the compiler spills 100 bytes: verify 196 us.)
           const bool masked = __any_sync(0xffffffffu, vis < kTN || j >= c.masked);
@@ -763,7 +1119,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (with_mask) {
               tmem_wait_ld32(xb);
               chunk(xb, pk + 48, 96);
-              if (__any_sync(0xffffffffu, live && out_of_range(mx * p.scale_log2, m, first))) return false;
+              if (__any_sync(0xffffffffu, live && out_of_range<false>(mx * p.scale_log2, m, first))) return false;
               tmem_st32(tS, pk);
               tmem_st32(tS + 32, pk + 32);
               add_sums(add2(sum2[0], sum2[1]));
@@ -771,7 +1127,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
             const f32x2 early_sum = add2(sum2[0], sum2[1]);
             sum2[0] = sum2[1] = 0ull;
-            const bool bad = __any_sync(0xffffffffu, live && out_of_range(mx * p.scale_log2, m, first));
+            const bool bad = __any_sync(0xffffffffu, live && out_of_range<false>(mx * p.scale_log2, m, first));
             tmem_wait_ld32(xb);
             if (bad) return false;
             tmem_st32(tS, pk);
@@ -783,7 +1139,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             early = true;
             chunk(xb, pk, 96);
             mx *= p.scale_log2;
-            if (__any_sync(0xffffffffu, live && out_of_range(mx, m, false))) {
+            if (__any_sync(0xffffffffu, live && out_of_range<false>(mx, m, false))) {
               add_sums(early_sum);
               return false;
             }
@@ -815,7 +1171,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
             mx *= p.scale_log2;
             const bool fresh = first && !early;  // nothing is summed yet
-            const bool grow = live && out_of_range(mx, m, fresh);
+            const bool grow = live && out_of_range<false>(mx, m, fresh);
             if (__any_sync(0xffffffffu, grow)) {
               const float mn = grow ? mx : m;
               const float f = grow && !fresh ? ex2(m - mn) : 1.0f;
@@ -851,13 +1207,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
           }
+          }
           first = false;
           tmem_wait_st();
         }
         tc_fence_before();
         // V rows past the item's end, and those that are not finite where not all
         // rows see them, become zeros (by the stream that multiplies first).
-        if (j >= c.masked && (!two || s == 0)) {
+        if (!FP4 && j >= c.masked && (!two || s == 0)) {
           const int all_see = infos[n & 3].all_see, end = infos[n & 3].end;
           const uint32_t i = run + j;
           const uint32_t sl = base + (two ? 2 * j + 1 : j + 1 < c.nt || c.next_joined ? 2 * i + 2 : 2 * i + 1);
@@ -918,17 +1275,79 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
   } else if (warp >= kResultWarp) {
     // ------------------------------------------------------------ results
-    regs_dec<kRegsResult>();
+    set_regs<kRegsLaunch<FP4>, kRegsResult<FP4>>();
     const int trow = threadIdx.x & 127;
     const uint32_t tO = tmem + ((uint32_t)(warp & 3) << 21) + 256;
     const int D = p.a.c.head_dim, G = p.a.G;
     uint32_t n = 0, run = 0;
+    // (4-bit) Piece q's rows of Q as fp16, a row times the power of two that brings its largest to
+    // 2^14 .. 2^15; the scores' factor takes it back.  Four lanes a row.
+    auto load_q = [&](uint32_t q) {
+      if (!__all_sync(0xffffffffu, mbar_wait_idle(&i_full[q & 1], (q >> 1) & 1u, abort_flag, tp.wait_budget, 64)))
+        return false;
+      const int rows = infos[q & 3].rows, row0 = infos[q & 3].row0, h = infos[q & 3].h, q0 = infos[q & 3].q0;
+      const bool two = rows > tp.tile_rows;
+      const uint32_t tile = smem_addr(smem + Lo::kOffQ) + (two ? 0 : (q & 1) * Lo::kTileBytes);
+      float* scales = (float*)(smem + Lo::kOffScale) + (two ? 0 : (q & 1) * 128);
+      const int part = lane & 3;
+      constexpr int kChunks = DP / 32;  // of a lane: columns 8 (part + 4 j) ..
+      for (int a0 = (warp & 3) * 8; a0 < rows; a0 += 32) {
+        const int a = a0 + (lane >> 2);
+        const bool live = a < rows;
+        uint4 x[kChunks];
+        const int tok = tp.by_g(row0 + (live ? a : 0)), g = row0 + (live ? a : 0) - tok * G;
+        const uint16_t* src = (const uint16_t*)p.a.q + (long long)(q0 + tok) * p.a.q_token_stride +
+                              (long long)(h * G + g) * p.a.q_head_stride + part * 8;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          x[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (live && 32 * j < D) {
+            const uint16_t* e = src + 32 * j;
+            x[j] = tp.q_vec ? *(const uint4*)e
+                            : make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
+                                         e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+          }
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          const uint32_t w4[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, max(w4[i] & 0x7fffu, (w4[i] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int field = (int)(top >> 7), up = field == 0 || field == 255 ? 127 : min(268 - field, 253);
+        const float f = __uint_as_float((uint32_t)up << 23) * tp.sign;
+        const int blk = a >> 7, t = a & 127;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+          uint32_t w4[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w4[i] = pack_half(__uint_as_float(w4[i] << 16) * f, __uint_as_float(w4[i] & 0xffff0000u) * f);
+          const int c = part + 4 * j;
+          if (live)
+            st_shared16(tile + blk * Lo::kTileBytes + (c >> 3) * Lo::kHalfBytes + swz(t, c & 7), w4[0], w4[1], w4[2], w4[3]);
+        }
+        // (not 0: a masked score is -inf times this)
+        if (live && part == 0)
+          scales[a] = fmaxf(__uint_as_float((uint32_t)(254 - up) << 23) * p.scale_log2, 1e-37f);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[q & 1]);
+      return true;
+    };
+    if (FP4) ok = load_q(0);
     while (true) {
-      ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget, 64));
+      if (!FP4)
+        ok = __all_sync(0xffffffffu, mbar_wait_idle(&q_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget, 64));
       if (!ok) break;
       const PieceInfo c = infos[n & 3];
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[n & 1]);
+      if (FP4 && c.nt != 0 && !(ok = load_q(n + 1))) break;
       if (c.nt == 0) break;
       const bool two = c.rows > tp.tile_rows;
       ok = __all_sync(0xffffffffu, mbar_wait_idle(ml_full, n & 1u, abort_flag, tp.wait_budget, 64));
@@ -936,14 +1355,15 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       const int s0 = two ? 0 : (int)(run & 1u);  // the stream of a one-block piece's first tile
       float2 x0 = merge[s0 * 128 + trow];
       const float2 x1 = merge[(s0 ^ 1) * 128 + trow];
-      const unsigned long long bad = *(volatile unsigned long long*)&bad_v[n & 1];
-      const int bad_from = bad >> 32 == n + 1 ? 0x7fffffff - (int)(uint32_t)bad : 0x7fffffff;
+      unsigned long long bad = FP4 ? 0ull : *(volatile unsigned long long*)&bad_v[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(ml_empty);
       ok = __all_sync(0xffffffffu,
                       mbar_wait_idle(&o_full[n & 1], (n >> 1) & 1u, abort_flag, tp.wait_budget, 64));
       if (!ok) break;
       tc_fence_after();
+      if (FP4) bad = *(volatile unsigned long long*)&bad_v[n & 3];  // (all of the piece's V are decoded)
+      const int bad_from = bad >> 32 == n + 1 ? 0x7fffffff - (int)(uint32_t)bad : 0x7fffffff;
       float w0 = 1.0f, w1 = 0.0f;  // weights of the two streams' O
       const bool both = !two && c.nt > 1;
       if (!two) {
@@ -969,7 +1389,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const size_t prow = ((size_t)blockIdx.x * 2 + (c.slot < 0 ? 0 : c.slot)) * kMR + a;
         const float inv = c.slot >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
         const uint32_t own = tO + (uint32_t)(two ? blk : s0) * 128;
-        const float f0 = w0 * inv, f1 = w1 * inv;
+        const float f0 = FP4 ? w0 * inv * p.a.v_factor : w0 * inv, f1 = FP4 ? w1 * inv * p.a.v_factor : w1 * inv;
         // 16 columns at a time from both streams, or 32 from one.
         auto store16 = [&](const uint32_t* o, int k) {
           if (!live) return;
@@ -1035,7 +1455,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
   } else if (warp == kLoaderWarp) {
     // ------------------------------------------------------------ loader
-    regs_dec<kRegsOther>();
+    set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
     AttnWalk<kTN> w = st->walk;
     const int D = p.a.c.head_dim, G = p.a.G;
     bool prev_two = false;
@@ -1073,10 +1493,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       if (lane == 0) infos[n & 3] = c;
       if (end) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[n & 1]);
+        if (lane == 0) mbar_arrive(FP4 ? &i_full[n & 1] : &q_full[n & 1]);
         break;
       }
-      if (tp.q_tma) {
+      if constexpr (FP4) {  // (the results' warps load the rows)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_full[n & 1]);
+      } else if (tp.q_tma) {
         // One box a tile and half: q_tokens tokens x G heads, the tile's rows in
         // order (tokens past the chunk's bring rows that are not read).
         if (lane == 0) {
@@ -1113,11 +1536,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       prev_two = two;
     }
-    if (!ok && tp.q_tma && lane == 0)  // the loads that may still be in flight
+    if (!FP4 && !ok && tp.q_tma && lane == 0)  // the loads that may still be in flight
       for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
         mbar_drain(&q_full[i & 1], (i >> 1) & 1u, tp.wait_budget);
   } else {
-    regs_dec<kRegsOther>();
+    set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
     if (lane == 0) attn_write_cut(p, *st);
   }
   if (*abort_flag && lane == 0) flag_status(flags, DSPARK_DEV_TIMEOUT);
@@ -1187,15 +1610,16 @@ int sm_count() {
   return n;
 }
 
-template <int DP>
+template <int DP, bool FP4>
 cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
                    cudaStream_t s) {
   static const cudaError_t attr = cudaFuncSetAttribute(
-      attention_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
+      attention_tc_kernel<DP, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, FP4>::kBytes);
   if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute attr_pdl;
-  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(sm_count()), kThreads, Layout<DP>::kBytes, s, &attr_pdl);
-  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<DP>, k, v, q, tp);
+  const cudaLaunchConfig_t cfg =
+      overlapped_launch(dim3(sm_count()), kThreads<FP4>, Layout<DP, FP4>::kBytes, s, &attr_pdl);
+  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<DP, FP4>, k, v, q, tp);
 }
 
 }  // namespace
@@ -1218,11 +1642,32 @@ bool attention_tc_supported(const AttnArgs& a) {
   return get_encode() != nullptr;
 }
 
+// Over a 4-bit cache: head_dim up to 128, bf16 queries.
+bool attention_tc_fp4_supported(const AttnArgs& a) {
+  return a.fp4 && a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0;
+}
+
+cudaError_t launch_attention_tc_fp4(const AttnArgs& a, char* ws, cudaStream_t s) {
+  const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kMaxCtas);
+  TcParams tp(a.G);
+  tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
+                    (float2*)(ws + w.stats), (float*)(ws + w.out), fabsf(a.scale) * 1.4426950408889634f,
+                    attn_item_units(a), kMR};
+  tp.sign = a.scale < 0 ? -1.0f : 1.0f;
+  tp.tile_rows = 128;
+  tp.q_vec = ((uintptr_t)a.q & 15u) == 0 && a.q_head_stride % 8 == 0 && a.q_token_stride % 8 == 0;
+  tp.wait_budget = kWaitBudget;
+  const CUtensorMap none = {};
+  const cudaError_t e = a.c.head_dim <= 64 ? launch<64, true>(tp, none, none, none, s)
+                                           : launch<128, true>(tp, none, none, none, s);
+  return e != cudaSuccess ? e : launch_attn_combine(tp.p, kMR, sm_count(), s);
+}
+
 size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout(kMR, head_dim, kMaxCtas).total; }
 
 cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kMaxCtas);
-  TcParams tp;
+  TcParams tp(a.G);
   tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),
                     // (not 0: a masked score is -inf times this)
@@ -1244,7 +1689,7 @@ cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   if (!encode_cache(&mk, a.c.k, a.c, tp.box_tokens) || !encode_cache(&mv, a.c.v, a.c, tp.box_tokens))
     return cudaErrorInvalidValue;
   if (tp.q_tma && !encode_q(&mq, a, tp.q_tokens)) return cudaErrorInvalidValue;
-  cudaError_t e = a.c.head_dim <= 64 ? launch<64>(tp, mk, mv, mq, s) : launch<128>(tp, mk, mv, mq, s);
+  cudaError_t e = a.c.head_dim <= 64 ? launch<64, false>(tp, mk, mv, mq, s) : launch<128, false>(tp, mk, mv, mq, s);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(tp.p, kMR, sm_count(), s);
 }
