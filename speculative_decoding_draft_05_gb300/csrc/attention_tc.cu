@@ -301,6 +301,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
       "r"(v[30]), "r"(v[31]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -448,7 +454,8 @@ static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 
 // The order in which tiles pass through the ring.  With two row blocks K0 V0 K1 V1 ..;
 // over a run of smaller pieces, whose products run a tile ahead, K0 K1 V0 K2 V1 ..
-// load(is_v, t, piece): one tile; open(walk, n): the piece of which the next K tiles are.
+// load(is_v, t, piece): one tile; false: stop.  (One call of it in the code: all that the roles
+// execute at a time has to fit the instruction cache.)
 struct TilePiece {
   int h, end, all_see, n;
   const int32_t* table;
@@ -456,31 +463,39 @@ struct TilePiece {
 template <typename Load>
 __device__ __forceinline__ bool walk_tiles(AttnWalk<kTN> w, const AttnParams& p, int tile_rows, int* flags,
                                            Load load) {
-  bool ok = true, pending = false;  // a V that the next K goes before
-  int pend_t = 0, n = 0;
-  TilePiece pend = {};
-  for (; !w.done() && ok; w.next(p, flags), ++n) {
-    const TilePiece c{w.h, w.end, w.q.L - w.q.n + 1 + w.m * p.mr / p.a.G, n,
-                      p.a.a.page_table + (size_t)w.r * p.a.a.max_pages};
-    const bool two = w.block_rows(p) > tile_rows;
-    if (two && pending) {
-      ok = load(true, pend_t, pend);
-      pending = false;
-    }
-    const int t1 = w.last_tile();
-    for (int t = w.first_tile(); t < t1 && ok; ++t) {
-      ok = load(false, t, c);
-      if (two) {
-        ok = ok && load(true, t, c);
-      } else {
-        if (pending) ok = ok && load(true, pend_t, pend);
-        pending = true;
-        pend_t = t, pend = c;
+  TilePiece c = {}, v = {};  // K's piece; the piece of V's tile vt, which is to come
+  int t = 0, t1 = 0, vt = 0, n = -1;
+  bool two = false, done = false, v_next = false, pending = false;  // pending: vt goes behind the next K
+  for (;;) {
+    bool is_v = v_next;
+    if (!is_v) {
+      if (t == t1 && !done) {
+        if (n >= 0) w.next(p, flags);
+        done = w.done();
+        if (!done) {
+          c = TilePiece{w.h, w.end, w.q.L - w.q.n + 1 + w.m * p.mr / p.a.G, ++n,
+                        p.a.a.page_table + (size_t)w.r * p.a.a.max_pages};
+          two = w.block_rows(p) > tile_rows;
+          t = w.first_tile(), t1 = w.last_tile();
+        }
       }
+      if (pending && (done || two))
+        is_v = true;
+      else if (done)
+        return true;
+    }
+    if (!load(is_v, is_v ? vt : t, is_v ? v : c)) return false;
+    if (is_v) {
+      pending = v_next && !two;
+      if (pending) vt = t - 1, v = c;  // the K before it
+      v_next = false;
+    } else {
+      v_next = two || pending;
+      if (two || !pending) vt = t, v = c;
+      pending = pending || !two;
+      ++t;
     }
   }
-  if (ok && pending) ok = load(true, pend_t, pend);
-  return ok;
 }
 
 // What the decoding warps have to know of a tile of codes (its loader writes it).
@@ -633,23 +648,29 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           }
         };
         if (D == DP) {
-          // Eight rows a step (64-element rows: 16), all loaded before the first is decoded.  Eight
+          // Eight rows a step (64-element rows: 16), the next loaded before the last is decoded.  Eight
           // consecutive lanes have one half's columns, so that their stores do not meet on a bank.
           constexpr int kUnits = DP / 32, kRows = 32 / kUnits;  // of a key; keys a step
           const int r = DP == 128 ? (lane >> 1) & 7 : lane >> 1, col = (lane & 1) + (DP == 128 ? lane >> 4 << 1 : 0);
           const uint32_t from = raw + (row0 >> 4) * fp4_block_bytes(DP) + r * (DP / 2) + col * 16;
           const uint32_t scale = raw + (row0 >> 4) * fp4_block_bytes(DP) + 8 * DP + r * (DP / 16) + col * 2;
           const uint32_t to = tile + (col >> 1) * Lo::kHalfBytes + swz(row0 + r, (col & 1) * 4);
-          uint4 x[kUnits];
-          uint32_t sc[kUnits];
-#pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
+          // (A loop, not a run of copies: the kernel's code as a whole has to fit the SM's instruction cache.)
+          constexpr int kStep = kRows * 128;
+          auto load = [&](int i, uint4& x, uint32_t& sc) {
             const int b = i * kRows / 16 * fp4_block_bytes(DP), q = i * kRows % 16;
-            x[i] = ld_shared16(from + b + q * (DP / 2));
-            sc[i] = ld_shared2(scale + b + q * (DP / 16));
+            x = ld_shared16(from + b + q * (DP / 2));
+            sc = ld_shared2(scale + b + q * (DP / 16));
+          };
+          uint4 x, next;
+          uint32_t sc, sc_next;
+          load(0, x, sc);
+#pragma unroll 1
+          for (int i = 0; i < kUnits; ++i) {
+            load(i + 1 < kUnits ? i + 1 : i, next, sc_next);
+            decode(row0 + i * kRows + r, x, sc, to, i * kStep);
+            x = next, sc = sc_next;
           }
-#pragma unroll
-          for (int i = 0; i < kUnits; ++i) decode(row0 + i * kRows + r, x[i], sc[i], to, i * kRows * 128);
         } else {
           const int units = D / 32;
           for (int u = lane; u < 32 * units; u += 32) {
@@ -996,42 +1017,49 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           if constexpr (FP4) {
             // Two passes over S, the maximum and the probabilities: m is set before any of P is
             // written, which fp16's range asks for, and the threads get by with few registers.
-            const bool masked = __any_sync(0xffffffffu, vis < kTN);
-            uint32_t xa[32], xb[32];
+            // Loops, and masks written into S beforehand: what the roles execute at a time has to
+            // fit the SM's instruction cache.  (Unrolled, with the masks in line: verify 355 us for 265.)
+            uint32_t xa[16], xb[16];
+            if (__any_sync(0xffffffffu, vis < kTN)) {
+#pragma unroll 1
+              for (int k = 0; k < kTN; k += 16) {
+                tmem_ld16(tS + k, xa);
+                tmem_wait_ld16(xa);
+                mask_from<16>(xa, vis - k);
+                tmem_st16(tS + k, xa);
+              }
+              tmem_wait_st();
+            }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto largest = [&](uint32_t* x, int k) {
-              if (masked) mask_from<32>(x, vis - k);
+            auto largest = [&](const uint32_t* x) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
+              for (int i = 0; i < 16; i += 2)
                 top[i / 2 & 3] = fmax3(top[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
             };
-            tmem_ld32(tS, xa);
-            tmem_wait_ld32(xa);
-            tmem_ld32(tS + 32, xb);
-            largest(xa, 0);
-            tmem_wait_ld32(xb);
-            tmem_ld32(tS + 64, xa);
-            largest(xb, 32);
-            tmem_wait_ld32(xa);
-            tmem_ld32(tS + 96, xb);
-            largest(xa, 64);
-            tmem_wait_ld32(xb);
-            tmem_ld32(tS, xa);
-            largest(xb, 96);
+            tmem_ld16(tS, xa);
+#pragma unroll 1
+            for (int k = 0; k < kTN; k += 32) {
+              tmem_wait_ld16(xa);
+              tmem_ld16(tS + k + 16, xb);
+              largest(xa);
+              tmem_wait_ld16(xb);
+              tmem_ld16(tS + (k + 32) % kTN, xa);  // (at last the first again)
+              largest(xb);
+            }
             const float mx = fmax3(fmaxf(top[0], top[1]), top[2], top[3]) * scale;
             const bool grow = live && out_of_range<true>(mx, m, l == 0.0f);
             if (__any_sync(0xffffffffu, grow)) {
               const float mn = grow ? mx - kBelow : m;
               const float f = grow && l != 0.0f ? ex2(m - mn) : 1.0f;
-              tmem_wait_ld32(xa);
+              tmem_wait_ld16(xa);
               if (!first) {  // (before, O is the piece before's, whose products may go on)
 #pragma unroll 1
-                for (int k = 0; k < DP; k += 32) {
-                  tmem_ld32(tO + s * 128 + k, xb);
-                  tmem_wait_ld32(xb);
+                for (int k = 0; k < DP; k += 16) {
+                  tmem_ld16(tO + s * 128 + k, xb);
+                  tmem_wait_ld16(xb);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * f);
-                  tmem_st32(tO + s * 128 + k, xb);
+                  for (int i = 0; i < 16; ++i) xb[i] = __float_as_uint(__uint_as_float(xb[i]) * f);
+                  tmem_st16(tO + s * 128 + k, xb);
                 }
               }
               l *= f;
@@ -1039,35 +1067,34 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
             const f32x2 sc2 = pack2(scale, scale), ms2 = pack2(-m, -m);
             f32x2 sum2[2] = {0ull, 0ull};
-            auto chunk = [&](uint32_t* x, int k) {
-              uint32_t pk[16];
-              if (masked) mask_from<32>(x, vis - k);
+            auto chunk = [&](const uint32_t* x, int k) {
+              uint32_t pk[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 float y0, y1;
                 unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, ms2), y0, y1);
                 const float e0 = ex2(y0), e1 = ex2(y1);
                 sum2[i & 1] = add2(sum2[i & 1], pack2(e0, e1));
                 pk[i] = pack_half(e0, e1);
               }
-              tmem_st16(tS + k / 2, pk);  // (over scores that are read by then)
+              tmem_st8(tS + k / 2, pk);  // (over scores that are read by then)
             };
-            tmem_wait_ld32(xa);
-            tmem_ld32(tS + 32, xb);
-            chunk(xa, 0);
-            tmem_wait_ld32(xb);
-            tmem_ld32(tS + 64, xa);
-            chunk(xb, 32);
-            tmem_wait_ld32(xa);
-            tmem_ld32(tS + 96, xb);
-            chunk(xa, 64);
-            tmem_wait_ld32(xb);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&h_full[s]);
+#pragma unroll 1
+            for (int k = 0; k < kTN; k += 32) {
+              tmem_wait_ld16(xa);
+              tmem_ld16(tS + k + 16, xb);
+              if (k == kEarly) {  // the first keys are written
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&h_full[s]);
+              }
+              chunk(xa, k);
+              tmem_wait_ld16(xb);
+              if (k + 32 < kTN) tmem_ld16(tS + k + 32, xa);
+              chunk(xb, k + 16);
+            }
             early = true;
-            chunk(xb, 96);
             float s0, s1;
             unpack2(add2(sum2[0], sum2[1]), s0, s1);
             l += s0 + s1;
