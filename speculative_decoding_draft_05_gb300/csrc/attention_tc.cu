@@ -100,7 +100,8 @@ static_assert(256 * kRegsSoftmax<true> + 128 * kRegsOther<true> + 128 * kRegsRes
 static_assert(kThreads<true> * kRegsLaunch<true> <= 65536 && kThreads<false> * kRegsLaunch<false> <= 65536, "registers");
 constexpr int kFirstRoleWarp = 8;  // (8 idles: warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
 constexpr int kMmaWarp = 9, kLoaderWarp = 10, kProducerWarp = 11, kResultWarp = 12;
-constexpr int kDecodeWarp = 16, kDecodeWarps = 4;  // (4-bit) two teams, tiles in turn, a quarter of the keys a warp
+constexpr int kDecodeWarp = 16, kDecodeWarps = 4;  // (4-bit) two teams, K's and V's, a quarter of the keys a warp
+constexpr int kProducerVWarp = 8;  // (4-bit) of V's codes; the other one brings K's
 constexpr float kRangeLog2 = 60.0f;
 // P in fp16 (4-bit): m is kBelow below the maximum that sets it, and stays until a
 // score lies kRise above it: p < 2^15, and what underflows is below 2^-31 of the largest.
@@ -115,14 +116,14 @@ struct Layout {
   static constexpr int kHalfBytes = 128 * 128;             // 128 rows of 128 bytes
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
   static constexpr int kStages = FP4 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
-  // (4-bit) tiles as the cache holds them, and the factors of Q's rows
+  // (4-bit) tiles as the cache holds them, half of them K's, and the factors of Q's rows
   static constexpr int kRawStages = FP4 ? (DP == 128 ? 6 : 12) : 0;
   static constexpr int kRawBytes = kTN / kFp4Block * fp4_block_bytes(DP);
   static constexpr int kOffQ = 0;  // two row blocks, or this piece's and the next one's rows
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
   static constexpr int kOffTile = kOffRaw + kRawStages * kRawBytes;   // RawTile [kRawStages]
-  static constexpr int kOffScale = kOffTile + kRawStages * 16;        // [2][128]
+  static constexpr int kOffScale = kOffTile + kRawStages * 32;        // [2][128]
   static constexpr int kOffMerge = kOffScale + (FP4 ? 2 * 128 * 4 : 0);  // (m, l) [2][128]
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
   static constexpr int kBars = 2 * kStages + 2 * kRawStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1 + (FP4 ? 2 : 0);
@@ -382,10 +383,10 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
+          dst),
       "l"(src), "r"(bytes), "r"(smem_addr(bar))
       : "memory");
 }
@@ -418,14 +419,14 @@ __device__ __forceinline__ void set_regs() {
 }
 
 struct TcParams {
-  explicit TcParams(int G) : by_g((unsigned)G) {}
+  explicit TcParams(const AttnArgs& a) : by_g((unsigned)a.G), by_page((unsigned)a.c.page_size) {}
   AttnParams p;
   int box_tokens;  // tokens of a K/V box: the largest power of two in page_size, up to 128
   int q_tokens;    // tokens of a Q tile (a box): 128 / G
   int tile_rows;   // rows of a Q tile: q_tokens G (128 where G > 128)
   int q_tma;       // q can be loaded by TMA (else by the loader's threads)
   int q_vec;       // (4-bit) q's rows are whole 16-byte vectors
-  Divider by_g;    // (4-bit)
+  Divider by_g, by_page;  // (4-bit)
   float sign;      // of the scale; |scale| is in p.scale_log2
   long long wait_budget;
 };
@@ -452,58 +453,13 @@ struct alignas(16) PieceInfo {
 };
 static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 
-// The order in which tiles pass through the ring.  With two row blocks K0 V0 K1 V1 ..;
-// over a run of smaller pieces, whose products run a tile ahead, K0 K1 V0 K2 V1 ..
-// load(is_v, t, piece): one tile; false: stop.  (One call of it in the code: all that the roles
-// execute at a time has to fit the instruction cache.)
-struct TilePiece {
-  int h, end, all_see, n;
-  const int32_t* table;
-};
-template <typename Load>
-__device__ __forceinline__ bool walk_tiles(AttnWalk<kTN> w, const AttnParams& p, int tile_rows, int* flags,
-                                           Load load) {
-  TilePiece c = {}, v = {};  // K's piece; the piece of V's tile vt, which is to come
-  int t = 0, t1 = 0, vt = 0, n = -1;
-  bool two = false, done = false, v_next = false, pending = false;  // pending: vt goes behind the next K
-  for (;;) {
-    bool is_v = v_next;
-    if (!is_v) {
-      if (t == t1 && !done) {
-        if (n >= 0) w.next(p, flags);
-        done = w.done();
-        if (!done) {
-          c = TilePiece{w.h, w.end, w.q.L - w.q.n + 1 + w.m * p.mr / p.a.G, ++n,
-                        p.a.a.page_table + (size_t)w.r * p.a.a.max_pages};
-          two = w.block_rows(p) > tile_rows;
-          t = w.first_tile(), t1 = w.last_tile();
-        }
-      }
-      if (pending && (done || two))
-        is_v = true;
-      else if (done)
-        return true;
-    }
-    if (!load(is_v, is_v ? vt : t, is_v ? v : c)) return false;
-    if (is_v) {
-      pending = v_next && !two;
-      if (pending) vt = t - 1, v = c;  // the K before it
-      v_next = false;
-    } else {
-      v_next = two || pending;
-      if (two || !pending) vt = t, v = c;
-      pending = pending || !two;
-      ++t;
-    }
-  }
-}
-
 // What the decoding warps have to know of a tile of codes (its loader writes it).
-struct alignas(16) RawTile {
+struct alignas(32) RawTile {
   int key0;     // -1: no more tiles
   int end;      // keys of the item from key0 on
   int all_see;  // of which all rows of the block see this many
-  int tag;      // piece + 1, of a tile of V; else 0
+  int tag;      // piece + 1
+  uint32_t slot;  // in the ring of the products' operands
 };
 
 template <int DP, bool FP4>
@@ -611,14 +567,16 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       set_regs<kRegsLaunch<FP4>, kRegsDecode>();
       const int D = p.a.c.head_dim, block = fp4_block_bytes(D);
       const int team = (warp - kDecodeWarp) / kDecodeWarps, row0 = (warp - kDecodeWarp) % kDecodeWarps * 32;
-      const RawTile* tiles = (const RawTile*)(smem + Lo::kOffTile);
-      for (uint32_t sl = team;; sl += 2) {
-        const int stage = (int)(sl % Lo::kStages), rs = (int)(sl % Lo::kRawStages);
-        ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], (sl / Lo::kRawStages) & 1u, abort_flag, tp.wait_budget));
+      constexpr int kStages = Lo::kRawStages / 2;  // of a team
+      const RawTile* tiles = (const RawTile*)(smem + Lo::kOffTile) + team * kStages;
+      for (uint32_t i = 0, phase = 0;; i == kStages - 1 ? (i = 0, phase ^= 1u) : ++i) {
+        const int rs = team * kStages + i;
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], phase, abort_flag, tp.wait_budget));
         if (!ok) break;
-        const RawTile c = tiles[rs];
+        const RawTile c = tiles[i];
         if (c.key0 < 0) break;
-        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], ((sl / Lo::kStages) & 1u) ^ 1u, abort_flag,
+        const int stage = (int)(c.slot % Lo::kStages);
+        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], ((c.slot / Lo::kStages) & 1u) ^ 1u, abort_flag,
                                                tp.wait_budget));
         if (!ok) break;
         const uint32_t raw = smem_addr(smem + Lo::kOffRaw) + rs * Lo::kRawBytes;
@@ -632,7 +590,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             // scales that are NaN are hidden from them, and make the others NaN in the results.
             if (row >= c.end) {
               sc = 0u;
-            } else if (c.tag && ((sc & 0x7fu) == 0x7fu || (sc & 0x7f00u) == 0x7f00u)) {
+            } else if (team == 1 && ((sc & 0x7fu) == 0x7fu || (sc & 0x7f00u) == 0x7f00u)) {
               sc = 0u;
               atomicMax(&bad_v[(c.tag - 1) & 3], (unsigned long long)c.tag << 32 | (uint32_t)(0x7fffffff - (c.key0 + row)));
             }
@@ -689,72 +647,88 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
       }
     }
-  } else if (FP4 && warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer (4-bit)
+  } else if (FP4 && (warp == kProducerWarp || warp == kProducerVWarp)) {
+    // ------------------------------------------------------------ producers (4-bit)
     if constexpr (FP4) {
       set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
+      const bool is_v = warp == kProducerVWarp;
+      if (is_v && lane == 0) attn_write_cut(p, *st);
+      constexpr int kStages = Lo::kRawStages / 2;  // of one of them
+      constexpr int kBlocks = kTN / kFp4Block;     // of a tile; a lane looks one up
+      constexpr int kTiles = 32 / kBlocks;         // looked up at once, the next ones ahead
       const int S = p.a.c.page_size, block = fp4_block_bytes(p.a.c.head_dim);
-      constexpr int kBlocks = kTN / kFp4Block;  // of a tile; a lane looks one up
-      constexpr int kTiles = 32 / kBlocks;      // looked up at once, the next ones ahead
-      uint32_t slot = 0;
-      int ids = 0, ids_next = 0, from = 0, piece = -1;  // pages of tiles from ..
-      int pg = 0, pg_before = 0, pg_t = -1;             // of the last K tile, and the one before
-      ok = walk_tiles(st->walk, p, tp.tile_rows, flags, [&](bool is_v, int t, const TilePiece& c) {
-        const int rs = (int)(slot % Lo::kRawStages);
-        const int key = t * kTN + lane * kFp4Block;
-        const bool has = lane < kBlocks && key < c.end;
-        if (!is_v) {
-          auto look_up = [&](int t0) {
-            const int k = t0 * kTN + lane * kFp4Block;
-            return k < c.end ? c.table[k / S] : 0;
-          };
-          if (c.n != piece) {
-            piece = c.n, from = t;
-            ids = look_up(from), ids_next = look_up(from + kTiles);
-          } else if (t == from + kTiles) {
-            from = t;
-            ids = ids_next, ids_next = look_up(from + kTiles);
+      const uint8_t* pool = (const uint8_t*)(is_v ? p.a.c.v : p.a.c.k);
+      const int first = is_v ? kStages : 0;
+      RawTile* tiles = (RawTile*)(smem + Lo::kOffTile) + first;
+      const uint32_t raw0 = smem_addr(smem + Lo::kOffRaw) + first * Lo::kRawBytes + lane * block;
+      uint32_t rs = 0, phase = 1, n = 0;  // place in the ring, and the parity of its being empty; piece
+      // Order of the operands' ring: with two row blocks K0 V0 K1 V1 ..; over a run of smaller pieces,
+      // whose products run a tile ahead, K0 K1 V0 K2 V1 ..
+      uint32_t base = 0, run = 0;  // slot of the run's first tile, steps of it before this piece
+      AttnWalk<kTN> w = st->walk;
+      while (!w.done() && ok) {
+        const AttnWalk<kTN> cur = w;
+        w.next(p, flags);
+        const bool two = cur.block_rows(p) > tp.tile_rows;
+        const bool joined = !two && !w.done() && w.block_rows(p) <= tp.tile_rows;
+        const int all_see = cur.q.L - cur.q.n + 1 + tp.by_g(cur.m * p.mr);
+        const int32_t* table = p.a.a.page_table + (size_t)cur.r * p.a.a.max_pages;
+        const long long head = cur.h * p.a.c.head_stride;
+        const int t1 = cur.last_tile();
+        auto look_up = [&](int t) {
+          const int k = t * kTN + lane * kFp4Block;
+          return k < cur.end ? table[tp.by_page(k)] : 0;
+        };
+        int t = cur.first_tile(), left = kTiles;
+        int ids = look_up(t), ids_next = look_up(t + kTiles);
+        // (a run's K_i is at 2 i - 1, but the first; V_i behind K_{i + 1}, but the last)
+        uint32_t slot = two ? base + (is_v ? 1 : 0) : base + 2 * run + (is_v ? 2 : -1);
+        if (!joined) base += 2 * (run + (t1 - t));  // (run: 0 where there are two blocks)
+        for (; t < t1; ++t, slot += 2) {
+          if (left == 0) {
+            left = kTiles;
+            ids = ids_next, ids_next = look_up(t + kTiles);
           }
-          pg_before = pg;
-          pg = __shfl_sync(0xffffffffu, ids, (t - from) * kBlocks + (lane & (kBlocks - 1)));
-          pg_t = t;
+          const int key = t * kTN + lane * kFp4Block, keys = cur.end - key;  // from the lane's block on
+          const bool has = lane < kBlocks && keys > 0;
+          int pg = __shfl_sync(0xffffffffu, ids, (kTiles - left--) * kBlocks + (lane & (kBlocks - 1)));
           if (has && (pg < 0 || pg >= p.a.c.n_pages)) {
             flag_status(flags, DSPARK_DEV_BAD_INPUT);
             pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
           }
+          const int in_page = (key - tp.by_page(key) * S) / kFp4Block;
+          // Blocks of one page follow one another: the first lane of each page brings them all.
+          // (Each copy takes the warp's time to issue.)
+          int count = 0;
+          if (has && (lane == 0 || in_page == 0))
+            count = min(min(S / kFp4Block - in_page, kBlocks - lane), (keys + kFp4Block - 1) / kFp4Block);
+          const uint8_t* from = pool + pg * p.a.c.page_stride + head + in_page * block;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[first + rs], phase, abort_flag, tp.wait_budget)))) break;
+          if (lane == 0) {  // (keys: the tile's)
+            const uint32_t sl = two ? slot : !is_v ? (run == 0 && t == cur.first_tile() ? slot + 1 : slot)
+                                           : (!joined && t == t1 - 1 ? slot - 1 : slot);
+            tiles[rs] = RawTile{key, keys, all_see - key, (int)n + 1, sl};
+            const int blocks = keys >= kTN ? kBlocks : (keys + kFp4Block - 1) / kFp4Block;
+            mbar_expect_tx(&raw_full[first + rs], (uint32_t)(keys > 0 ? blocks : 0) * block);
+          }
+          __syncwarp();
+          if (count > 0) bulk_load(raw0 + rs * Lo::kRawBytes, from, count * block, &raw_full[first + rs]);
+          if (++rs == kStages) rs = 0, phase ^= 1u;
         }
-        const int page = is_v && !(t == pg_t && c.n == piece) ? pg_before : pg;
-        if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[rs], ((slot / Lo::kRawStages) & 1u) ^ 1u, abort_flag,
-                                               tp.wait_budget)))
-          return false;
-        const unsigned blocks = __ballot_sync(0xffffffffu, has);
-        if (lane == 0) {
-          ((RawTile*)(smem + Lo::kOffTile))[rs] =
-              RawTile{t * kTN, c.end - t * kTN, c.all_see - t * kTN, is_v ? c.n + 1 : 0};
-          mbar_expect_tx(&raw_full[rs], (uint32_t)__popc(blocks) * block);
-        }
-        __syncwarp();
-        if (has)
-          bulk_load(smem + Lo::kOffRaw + rs * Lo::kRawBytes + lane * block,
-                    (const uint8_t*)(is_v ? p.a.c.v : p.a.c.k) + page * p.a.c.page_stride + c.h * p.a.c.head_stride +
-                        (long long)((key % S) / kFp4Block) * block,
-                    block, &raw_full[rs]);
-        ++slot;
-        return true;
-      });
-      for (int i = 0; i < 2 && ok; ++i, ++slot) {  // to each team: no more tiles
-        const int rs = (int)(slot % Lo::kRawStages);
-        ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[rs], ((slot / Lo::kRawStages) & 1u) ^ 1u, abort_flag,
-                                               tp.wait_budget));
-        if (!ok) break;
-        if (lane == 0) {
-          ((RawTile*)(smem + Lo::kOffTile))[rs].key0 = -1;
-          mbar_arrive(&raw_full[rs]);
-        }
+        run = joined ? run + (t1 - cur.first_tile()) : 0;
+        ++n;
       }
-      if (!ok && lane == 0)  // the loads still in flight
-        for (uint32_t i = slot > Lo::kRawStages ? slot - Lo::kRawStages : 0; i < slot; ++i)
-          mbar_drain(&raw_full[i % Lo::kRawStages], (i / Lo::kRawStages) & 1u, tp.wait_budget);
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[first + rs], phase, abort_flag, tp.wait_budget));
+      if (ok) {
+        if (lane == 0) {
+          tiles[rs].key0 = -1;  // no more
+          mbar_arrive(&raw_full[first + rs]);
+        }
+      } else if (lane == 0) {  // the loads still in flight: the last of each stage
+        for (int i = 0; i < kStages; ++i)
+          mbar_drain(&raw_full[first + i], i < (int)rs ? phase ^ 1u : phase, tp.wait_budget);
+      }
     }
   } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
@@ -1566,7 +1540,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if (!FP4 && !ok && tp.q_tma && lane == 0)  // the loads that may still be in flight
       for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
         mbar_drain(&q_full[i & 1], (i >> 1) & 1u, tp.wait_budget);
-  } else {
+  } else {  // (4-bit: none)
     set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
     if (lane == 0) attn_write_cut(p, *st);
   }
@@ -1676,7 +1650,7 @@ bool attention_tc_fp4_supported(const AttnArgs& a) {
 
 cudaError_t launch_attention_tc_fp4(const AttnArgs& a, char* ws, cudaStream_t s) {
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kMaxCtas);
-  TcParams tp(a.G);
+  TcParams tp(a);
   tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out), fabsf(a.scale) * 1.4426950408889634f,
                     attn_item_units(a), kMR};
@@ -1694,7 +1668,7 @@ size_t attention_tc_workspace_bytes(int head_dim) { return attn_workspace_layout
 
 cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s) {
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kMaxCtas);
-  TcParams tp(a.G);
+  TcParams tp(a);
   tp.p = AttnParams{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),
                     (float2*)(ws + w.stats), (float*)(ws + w.out),
                     // (not 0: a masked score is -inf times this)
