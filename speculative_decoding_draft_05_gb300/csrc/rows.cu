@@ -171,6 +171,155 @@ __global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const Ro
   }
 }
 
+// Rows of whole groups of 16 on 16-byte boundaries, pairs whose groups are whole too:
+// a lane takes a group and the one it is paired with (or, interleaved or past
+// the rotated part, one alone), so that nothing crosses lanes.  K and V are on their way
+// before the token's place is looked up, then the queries, two units a lane at a time.
+template <typename T, bool FP4, bool Inter>
+__global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const RotaryAppendArgs p) {
+  const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();
+  if (blockIdx.x == 0) {
+    rotary_status(p);
+    return;
+  }
+  // Units of a row: those that are rotated first.  A unit's groups begin at column d0 and, if it is a pair, d0 + half.
+  const int turned = Inter ? p.rot / 16 : p.rot / 32, units = turned + (D - p.rot) / 16;
+  const int n = p.c.heads * units, groups = D / 16, nv = p.c.heads * groups, nq = p.Hq * units;
+  struct Unit {
+    int h, d0;
+    bool turn;
+  };
+  const auto unit = [&](int i) {
+    const int h = i / units, j = i - h * units;
+    return Unit{h, j < turned ? 16 * j : p.rot + 16 * (j - turned), j < turned};
+  };
+  for (int t = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * kWarps) {
+    const T* kn = (const T*)p.k_new + t * p.tok_stride;
+    const T* vn = (const T*)p.v_new + t * p.tok_stride;
+    const T* qn = (const T*)p.q + t * p.q_tok;
+    T* qo = (T*)p.q_out + t * p.qo_tok;
+    const auto load = [&](const T* row, const Unit& u, Group<T>& a, Group<T>& b) {
+      a.load(row + u.d0);
+      if (!Inter && u.turn) b.load(row + u.d0 + half);
+    };
+    Group<T> ka, kb, va[2];
+    Unit ku = unit(lane < n ? lane : 0);
+    if (lane < n) load(kn + ku.h * p.head_stride, ku, ka, kb);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      if (i < nv) va[k].load(vn + i / groups * p.head_stride + i % groups * 16);
+    }
+    const RowPlace pl = find_place(p.c, p.a, t);
+    const float* cs = nullptr;
+    if (!table_row(p, pl, t, &cs)) continue;
+    const CacheRow at = cache_row<FP4>(p.c, pl);
+    float c[16], s[16];  // of the columns from `cd` on
+    int cd = -1;
+    const auto angles = [&](const Unit& u) {
+      if (!u.turn || cd == u.d0) return;
+      cd = u.d0;
+      const int i0 = Inter ? u.d0 / 2 : u.d0;
+#pragma unroll
+      for (int i = 0; i < (Inter ? 8 : 16); ++i) c[i] = cs[i0 + i], s[i] = cs[half + i0 + i];
+    };
+    // One rotated value: exactly rounded to odd for the choice of codes, else in fp32.
+    const auto turned_value = [](float x, float c, float y, float s, auto exact) {
+      return exact ? rotated_odd(x, c, y, s) : fmaf(x, c, y * s);
+    };
+    const auto rotate = [&](const Unit& u, const Group<T>& a, const Group<T>& b, float* x, float* y, auto exact) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = a.get(i), y[i] = Inter || !u.turn ? 0.0f : b.get(i);
+      if (!u.turn) return;
+      if (Inter) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = x[2 * i], o = x[2 * i + 1];
+          x[2 * i] = turned_value(e, c[i], o, -s[i], exact);
+          x[2 * i + 1] = turned_value(o, c[i], e, s[i], exact);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = x[i], o = y[i];
+          x[i] = turned_value(e, c[i], o, -s[i], exact);
+          y[i] = turned_value(o, c[i], e, s[i], exact);
+        }
+      }
+    };
+    const auto store = [&](T* row, const Unit& u, const float* x, const float* y) {
+      Group<T> g;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g.set(i, x[i]);
+      g.store(row + u.d0);
+      if (!Inter && u.turn) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g.set(i, y[i]);
+        g.store(row + u.d0 + half);
+      }
+    };
+    const auto put_k = [&](const Unit& u, const Group<T>& a, const Group<T>& b) {
+      float x[16], y[16];
+      angles(u);
+      rotate(u, a, b, x, y, std::integral_constant<bool, FP4>{});
+      if constexpr (FP4) {
+        uint8_t* base = (uint8_t*)p.c.k + u.h * p.c.head_stride;
+        store_fp4(x, p.k_factor, base + at.codes + u.d0 / 2, base + at.scales + u.d0 / 16);
+        if (!Inter && u.turn)
+          store_fp4(y, p.k_factor, base + at.codes + (u.d0 + half) / 2, base + at.scales + (u.d0 + half) / 16);
+      } else {
+        store((T*)p.c.k + at.at + u.h * p.c.head_stride, u, x, y);
+      }
+    };
+    const auto put_v = [&](int i, const Group<T>& g) {
+      const int h = i / groups, j = i - h * groups;
+      if constexpr (FP4) {
+        uint8_t* base = (uint8_t*)p.c.v + h * p.c.head_stride;
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = g.get(e);
+        store_fp4(x, p.v_factor, base + at.codes + j * 8, base + at.scales + j);
+      } else {
+        g.store((T*)p.c.v + at.at + h * p.c.head_stride + j * 16);
+      }
+    };
+    if (lane < n) put_k(ku, ka, kb);
+    for (int i = lane + 32; i < n; i += 32) {
+      ku = unit(i);
+      load(kn + ku.h * p.head_stride, ku, ka, kb);
+      put_k(ku, ka, kb);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lane + 32 * k < nv) put_v(lane + 32 * k, va[k]);
+    for (int i = lane + 64; i < nv; i += 32) {
+      Group<T> g;
+      g.load(vn + i / groups * p.head_stride + i % groups * 16);
+      put_v(i, g);
+    }
+    for (int i0 = lane; i0 < nq; i0 += 64) {
+      Group<T> a[2], b[2];
+      Unit u[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (i0 + 32 * k < nq) {
+          u[k] = unit(i0 + 32 * k);
+          load(qn + u[k].h * p.q_head, u[k], a[k], b[k]);
+        }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (i0 + 32 * k < nq) {
+          float x[16], y[16];
+          angles(u[k]);
+          rotate(u[k], a[k], b[k], x, y, std::false_type{});
+          store(qo + u[k].h * p.qo_head, u[k], x, y);
+        }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ read
 // Rows of the cache as values: a row a warp; 4-bit rows in groups of 16, a group a lane.
 template <typename T>
@@ -243,15 +392,30 @@ int row_ctas(int n_tokens) {  // (the first one for the status word: also withou
 
 }  // namespace
 
+// Whether rows are whole groups on 16-byte boundaries, and pairs lie in whole groups.
+static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4) {
+  const CacheView& c = p.c;
+  const int ve = 16 / esize;
+  uintptr_t at = (uintptr_t)p.k_new | (uintptr_t)p.v_new | (uintptr_t)p.cos_sin;
+  long long strides = p.tok_stride | p.head_stride;
+  if (p.Hq > 0) at |= (uintptr_t)p.q | (uintptr_t)p.q_out, strides |= p.q_tok | p.q_head | p.qo_tok | p.qo_head;
+  if (!fp4) at |= (uintptr_t)c.k | (uintptr_t)c.v, strides |= c.page_stride | c.token_stride | c.head_stride;
+  return c.head_dim % 16 == 0 && p.rot % (p.interleaved ? 16 : 32) == 0 && strides % ve == 0 && (at & 15u) == 0;
+}
+
+template <typename T, bool FP4>
+static cudaError_t launch_append(const RotaryAppendArgs& p, const cudaLaunchConfig_t& cfg) {
+  if (!whole_groups(p, sizeof(T), FP4)) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true>, p)
+                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false>, p);
+}
+
 cudaError_t launch_append_rotary(const RotaryAppendArgs& p, int dtype, bool fp4, cudaStream_t s) {
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = overlapped_launch(dim3(row_ctas(p.a.n_tokens)), kWarps * 32, 0, s, &attr);
-  const bool bf = dtype == DSPARK_BF16;
-  if (fp4)
-    return bf ? cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<__nv_bfloat16, true>, p)
-              : cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<float, true>, p);
-  return bf ? cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<__nv_bfloat16, false>, p)
-            : cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<float, false>, p);
+  if (dtype == DSPARK_BF16)
+    return fp4 ? launch_append<__nv_bfloat16, true>(p, cfg) : launch_append<__nv_bfloat16, false>(p, cfg);
+  return fp4 ? launch_append<float, true>(p, cfg) : launch_append<float, false>(p, cfg);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs& p, int esize, bool fp4, cudaStream_t s) {
