@@ -69,24 +69,6 @@ struct AttnParams {
   int mr;            // rows of an item, at most (partial results are MR >= mr rows apart)
 };
 
-// Division of n < 2^31 by a divisor known at launch: a multiplication and
-// shifts (Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994).
-struct Divider {
-  unsigned mul, sh1, sh2;
-  explicit Divider(unsigned d) {
-    unsigned l = 0;
-    while ((1ull << l) < d) ++l;
-    mul = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
-    sh1 = l < 1 ? l : 1;
-    sh2 = l < 1 ? 0 : l - 1;
-  }
-  __device__ __forceinline__ int operator()(int n) const {
-    const unsigned t = __umulhi(mul, (unsigned)n);
-    return (int)((t + (((unsigned)n - t) >> sh1)) >> sh2);
-  }
-};
-
 struct AttnRequest {
   int q0, n, L;  // first token, chunk length, cached positions
 };

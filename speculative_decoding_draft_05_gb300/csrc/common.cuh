@@ -217,6 +217,24 @@ __device__ __forceinline__ float ord_key(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
+// Division of n < 2^31 by a divisor known at launch: a multiplication and
+// shifts (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct Divider {
+  unsigned mul, sh1, sh2;
+  explicit Divider(unsigned d) {
+    unsigned l = 0;
+    while ((1ull << l) < d) ++l;
+    mul = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    sh1 = l < 1 ? l : 1;
+    sh2 = l < 1 ? 0 : l - 1;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    const unsigned t = __umulhi(mul, (unsigned)n);
+    return (int)((t + (((unsigned)n - t) >> sh1)) >> sh2);
+  }
+};
+
 // Device status word: OR bits in with an atomic.
 __device__ __forceinline__ void flag_status(int* status, int bits) {
   if (status) atomicOr(status, bits);

@@ -36,37 +36,39 @@ __device__ __forceinline__ float to_type<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
 
-// Sixteen consecutive elements as they lie in memory.
-template <typename T>
+// N consecutive elements as they lie in memory (a whole number of 16-byte vectors).
+template <typename T, int N>
 struct Group {
-  Vec16<T> v[sizeof(T)];
+  static constexpr int kPer = 16 / sizeof(T), kVecs = N / kPer;
+  Vec16<T> v[kVecs];
   __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) v[i] = ((const Vec16<T>*)src)[i];
+    for (int i = 0; i < kVecs; ++i) v[i] = ((const Vec16<T>*)src)[i];
   }
   __device__ __forceinline__ void store(T* dst) const {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) ((Vec16<T>*)dst)[i] = v[i];
+    for (int i = 0; i < kVecs; ++i) ((Vec16<T>*)dst)[i] = v[i];
   }
-  static constexpr int kPer = 16 / sizeof(T);
   __device__ __forceinline__ float get(int i) const { return to_f32(v[i / kPer].e[i % kPer]); }
   __device__ __forceinline__ void set(int i, float x) { v[i / kPer].e[i % kPer] = to_type<T>(x); }
 };
 
-// Writes a group's codes and scale.
-__device__ __forceinline__ void store_fp4(const float* y, const float2& f, uint8_t* codes, uint8_t* scale) {
+// Codes and scale of a group of 16, by two neighbouring lanes of `mask` with eight values each.
+__device__ __forceinline__ void store_fp4(unsigned mask, const float* y, const float2& f, uint8_t* codes,
+                                          uint8_t* scale) {
   uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
+  amax = max(amax, __shfl_xor_sync(mask, amax, 1));
   const Fp4Scale s = fp4_scale(amax, f.x, f.y);
-  uint32_t w[2] = {0u, 0u};
+  uint32_t w = 0u;
   if (s.inverse != 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= floats_to_fp4x2(fp4_quotient(y[2 * i], s), fp4_quotient(y[2 * i + 1], s)) << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i)
+      w |= floats_to_fp4x2(fp4_quotient(y[2 * i], s), fp4_quotient(y[2 * i + 1], s)) << (8 * i);
   }
-  *(uint2*)codes = make_uint2(w[0], w[1]);
-  *scale = (uint8_t)s.byte;
+  *(uint32_t*)codes = w;
+  if (!(threadIdx.x & 1)) *scale = (uint8_t)s.byte;
 }
 
 // Where a token's rows go in the cache.
@@ -172,11 +174,14 @@ __global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const Ro
 }
 
 // Rows of whole groups of 16 on 16-byte boundaries, pairs whose groups are whole too:
-// a lane takes a group and the one it is paired with (or, interleaved or past
-// the rotated part, one alone), so that nothing crosses lanes.  K and V are on their way
-// before the token's place is looked up, then the queries, two units a lane at a time.
+// a lane takes eight columns and the eight that they are paired with (or, interleaved
+// or past the rotated part, eight alone), so that rotation crosses no lanes; two
+// neighbours have a 4-bit group.  K and V are on their way before the token's place is
+// looked up, then the queries, four units a lane at a time.
 template <typename T, bool FP4, bool Inter>
-__global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const RotaryAppendArgs p) {
+__global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const RotaryAppendArgs p, const Divider by_units, const Divider by_chunks) {
+  typedef Group<T, 8> Cols;
+  constexpr int kKAhead = sizeof(T) == 2 ? 2 : 1, kVAhead = 2 * kKAhead, kQ = 2;  // units a lane at a time
   const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   wait_for_previous();
@@ -184,137 +189,170 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const Rot
     rotary_status(p);
     return;
   }
-  // Units of a row: those that are rotated first.  A unit's groups begin at column d0 and, if it is a pair, d0 + half.
-  const int turned = Inter ? p.rot / 16 : p.rot / 32, units = turned + (D - p.rot) / 16;
-  const int n = p.c.heads * units, groups = D / 16, nv = p.c.heads * groups, nq = p.Hq * units;
+  // Units of a row: those that are rotated first.  A unit's columns begin at d0 and, if it is a pair, d0 + half.
+  // (Both counts are even: neighbouring lanes have neighbouring units of the same row.)
+  const int turned = Inter ? p.rot / 8 : p.rot / 16, units = turned + (D - p.rot) / 8;
+  const int n = p.c.heads * units, chunks = D / 8, nv = p.c.heads * chunks, nq = p.Hq * units;
   struct Unit {
     int h, d0;
     bool turn;
   };
   const auto unit = [&](int i) {
-    const int h = i / units, j = i - h * units;
-    return Unit{h, j < turned ? 16 * j : p.rot + 16 * (j - turned), j < turned};
+    const int h = by_units(i), j = i - h * units;
+    return Unit{h, j < turned ? 8 * j : p.rot + 8 * (j - turned), j < turned};
   };
   for (int t = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * kWarps) {
     const T* kn = (const T*)p.k_new + t * p.tok_stride;
     const T* vn = (const T*)p.v_new + t * p.tok_stride;
     const T* qn = (const T*)p.q + t * p.q_tok;
     T* qo = (T*)p.q_out + t * p.qo_tok;
-    const auto load = [&](const T* row, const Unit& u, Group<T>& a, Group<T>& b) {
+    const auto load = [&](const T* row, const Unit& u, Cols& a, Cols& b) {
       a.load(row + u.d0);
       if (!Inter && u.turn) b.load(row + u.d0 + half);
     };
-    Group<T> ka, kb, va[2];
-    Unit ku = unit(lane < n ? lane : 0);
-    if (lane < n) load(kn + ku.h * p.head_stride, ku, ka, kb);
+    const auto v_at = [&](int i) {
+      const int h = by_chunks(i);
+      return h * p.head_stride + (i - h * chunks) * 8;
+    };
+    Cols ka[kKAhead], kb[kKAhead], va[kVAhead];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = lane + 32 * k;
-      if (i < nv) va[k].load(vn + i / groups * p.head_stride + i % groups * 16);
-    }
+    for (int k = 0; k < kKAhead; ++k)
+      if (lane + 32 * k < n) {
+        const Unit u = unit(lane + 32 * k);
+        load(kn + u.h * p.head_stride, u, ka[k], kb[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < kVAhead; ++k)
+      if (lane + 32 * k < nv) va[k].load(vn + v_at(lane + 32 * k));
     const RowPlace pl = find_place(p.c, p.a, t);
     const float* cs = nullptr;
     if (!table_row(p, pl, t, &cs)) continue;
     const CacheRow at = cache_row<FP4>(p.c, pl);
-    float c[16], s[16];  // of the columns from `cd` on
+    constexpr int kAngles = Inter ? 4 : 8;
+    float c[kAngles], s[kAngles];  // of the unit at column `cd`
     int cd = -1;
     const auto angles = [&](const Unit& u) {
       if (!u.turn || cd == u.d0) return;
       cd = u.d0;
-      const int i0 = Inter ? u.d0 / 2 : u.d0;
+      const float4* from = (const float4*)(cs + (Inter ? u.d0 / 2 : u.d0));
 #pragma unroll
-      for (int i = 0; i < (Inter ? 8 : 16); ++i) c[i] = cs[i0 + i], s[i] = cs[half + i0 + i];
+      for (int i = 0; i < kAngles; i += 4) {
+        const float4 x = from[i / 4], y = *(const float4*)((const float*)(from + i / 4) + half);
+        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+      }
     };
-    // One rotated value: exactly rounded to odd for the choice of codes, else in fp32.
-    const auto turned_value = [](float x, float c, float y, float s, auto exact) {
+    // One rotated value: rounded to odd for the choice of codes, else in fp32.
+    const auto value = [](float x, float c, float y, float s, auto exact) {
       return exact ? rotated_odd(x, c, y, s) : fmaf(x, c, y * s);
     };
-    const auto rotate = [&](const Unit& u, const Group<T>& a, const Group<T>& b, float* x, float* y, auto exact) {
+    const auto rotate = [&](const Unit& u, const Cols& a, const Cols& b, float* x, float* y, auto exact) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = a.get(i), y[i] = Inter || !u.turn ? 0.0f : b.get(i);
+      for (int i = 0; i < 8; ++i) x[i] = a.get(i), y[i] = Inter || !u.turn ? 0.0f : b.get(i);
       if (!u.turn) return;
       if (Inter) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = x[2 * i], o = x[2 * i + 1];
-          x[2 * i] = turned_value(e, c[i], o, -s[i], exact);
-          x[2 * i + 1] = turned_value(o, c[i], e, s[i], exact);
+        for (int i = 0; i < kAngles; ++i) {
+          const float e = x[2 * i % 8], o = x[(2 * i + 1) % 8];
+          x[2 * i % 8] = value(e, c[i], o, -s[i], exact);
+          x[(2 * i + 1) % 8] = value(o, c[i], e, s[i], exact);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kAngles; ++i) {
           const float e = x[i], o = y[i];
-          x[i] = turned_value(e, c[i], o, -s[i], exact);
-          y[i] = turned_value(o, c[i], e, s[i], exact);
+          x[i] = value(e, c[i], o, -s[i], exact);
+          y[i] = value(o, c[i], e, s[i], exact);
         }
       }
     };
     const auto store = [&](T* row, const Unit& u, const float* x, const float* y) {
-      Group<T> g;
+      Cols g;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) g.set(i, x[i]);
+      for (int i = 0; i < 8; ++i) g.set(i, x[i]);
       g.store(row + u.d0);
       if (!Inter && u.turn) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g.set(i, y[i]);
+        for (int i = 0; i < 8; ++i) g.set(i, y[i]);
         g.store(row + u.d0 + half);
       }
     };
-    const auto put_k = [&](const Unit& u, const Group<T>& a, const Group<T>& b) {
-      float x[16], y[16];
+    // mask: the lanes that have one (both of a group, as their units are in range together).
+    const auto put_k = [&](unsigned mask, int i, const Cols& a, const Cols& b) {
+      const Unit u = unit(i);
+      float x[8], y[8];
       angles(u);
       rotate(u, a, b, x, y, std::integral_constant<bool, FP4>{});
       if constexpr (FP4) {
         uint8_t* base = (uint8_t*)p.c.k + u.h * p.c.head_stride;
-        store_fp4(x, p.k_factor, base + at.codes + u.d0 / 2, base + at.scales + u.d0 / 16);
-        if (!Inter && u.turn)
-          store_fp4(y, p.k_factor, base + at.codes + (u.d0 + half) / 2, base + at.scales + (u.d0 + half) / 16);
+        store_fp4(mask, x, p.k_factor, base + at.codes + u.d0 / 2, base + at.scales + u.d0 / 16);
+        if (!Inter) {
+          const unsigned pairs = __ballot_sync(mask, u.turn);
+          if (u.turn)
+            store_fp4(pairs, y, p.k_factor, base + at.codes + (u.d0 + half) / 2, base + at.scales + (u.d0 + half) / 16);
+        }
       } else {
         store((T*)p.c.k + at.at + u.h * p.c.head_stride, u, x, y);
       }
     };
-    const auto put_v = [&](int i, const Group<T>& g) {
-      const int h = i / groups, j = i - h * groups;
+    const auto put_v = [&](unsigned mask, int i, const Cols& g) {
+      const int h = by_chunks(i), j = i - h * chunks;
       if constexpr (FP4) {
         uint8_t* base = (uint8_t*)p.c.v + h * p.c.head_stride;
-        float x[16];
+        float x[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = g.get(e);
-        store_fp4(x, p.v_factor, base + at.codes + j * 8, base + at.scales + j);
+        for (int e = 0; e < 8; ++e) x[e] = g.get(e);
+        store_fp4(mask, x, p.v_factor, base + at.codes + j * 4, base + at.scales + j / 2);
       } else {
-        g.store((T*)p.c.v + at.at + h * p.c.head_stride + j * 16);
+        g.store((T*)p.c.v + at.at + h * p.c.head_stride + j * 8);
       }
     };
-    if (lane < n) put_k(ku, ka, kb);
-    for (int i = lane + 32; i < n; i += 32) {
-      ku = unit(i);
-      load(kn + ku.h * p.head_stride, ku, ka, kb);
-      put_k(ku, ka, kb);
+#pragma unroll
+    for (int k = 0; k < kKAhead; ++k) {
+      const unsigned mask = __ballot_sync(0xffffffffu, lane + 32 * k < n);
+      if (lane + 32 * k < n) put_k(mask, lane + 32 * k, ka[k], kb[k]);
+    }
+#pragma unroll 1
+    for (int i0 = 32 * kKAhead; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const unsigned mask = __ballot_sync(0xffffffffu, i < n);
+      if (i < n) {
+        const Unit u = unit(i);
+        load(kn + u.h * p.head_stride, u, ka[0], kb[0]);
+        put_k(mask, i, ka[0], kb[0]);
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (lane + 32 * k < nv) put_v(lane + 32 * k, va[k]);
-    for (int i = lane + 64; i < nv; i += 32) {
-      Group<T> g;
-      g.load(vn + i / groups * p.head_stride + i % groups * 16);
-      put_v(i, g);
+    for (int k = 0; k < kVAhead; ++k) {
+      const unsigned mask = __ballot_sync(0xffffffffu, lane + 32 * k < nv);
+      if (lane + 32 * k < nv) put_v(mask, lane + 32 * k, va[k]);
     }
-    for (int i0 = lane; i0 < nq; i0 += 64) {
-      Group<T> a[2], b[2];
-      Unit u[2];
+#pragma unroll 1
+    for (int i0 = 32 * kVAhead; i0 < nv; i0 += 32) {
+      const int i = i0 + lane;
+      const unsigned mask = __ballot_sync(0xffffffffu, i < nv);
+      if (i < nv) {
+        va[0].load(vn + v_at(i));
+        put_v(mask, i, va[0]);
+      }
+    }
+#pragma unroll 1
+    for (int i0 = lane; i0 < nq; i0 += 32 * kQ) {
+      Cols a[kQ], b[kQ];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < kQ; ++k)
         if (i0 + 32 * k < nq) {
-          u[k] = unit(i0 + 32 * k);
-          load(qn + u[k].h * p.q_head, u[k], a[k], b[k]);
+          const Unit u = unit(i0 + 32 * k);
+          load(qn + u.h * p.q_head, u, a[k], b[k]);
         }
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < kQ; ++k)
         if (i0 + 32 * k < nq) {
-          float x[16], y[16];
-          angles(u[k]);
-          rotate(u[k], a[k], b[k], x, y, std::false_type{});
-          store(qo + u[k].h * p.qo_head, u[k], x, y);
+          const Unit u = unit(i0 + 32 * k);
+          float x[8], y[8];
+          angles(u);
+          rotate(u, a[k], b[k], x, y, std::false_type{});
+          store(qo + u.h * p.qo_head, u, x, y);
         }
     }
   }
@@ -345,7 +383,7 @@ __global__ void __launch_bounds__(kWarps * 32) read_fp4_kernel(const CacheReadAr
       uint32_t x[8];
       fp4x8_to_half(w.x, x);
       fp4x8_to_half(w.y, x + 4);
-      Group<T> out;
+      Group<T, 16> out;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // (code x scale is exact in 32 bits; the factor rounds once)
         out.set(2 * j, half_lo(x[j]) * s * f);
@@ -405,9 +443,11 @@ static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4) {
 
 template <typename T, bool FP4>
 static cudaError_t launch_append(const RotaryAppendArgs& p, const cudaLaunchConfig_t& cfg) {
+  const int pairs = p.rot / (p.interleaved ? 8 : 16);
+  const Divider by_units((unsigned)(pairs + (p.c.head_dim - p.rot) / 8)), by_chunks((unsigned)p.c.head_dim / 8);
   if (!whole_groups(p, sizeof(T), FP4)) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
-  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true>, p)
-                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false>, p);
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true>, p, by_units, by_chunks)
+                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false>, p, by_units, by_chunks);
 }
 
 cudaError_t launch_append_rotary(const RotaryAppendArgs& p, int dtype, bool fp4, cudaStream_t s) {
