@@ -30,27 +30,6 @@ constexpr int kProbPairs = 128;  // (e, e) pairs of a warp in shared memory
 constexpr float kSlackLog2 = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-typedef unsigned long long f32x2;
-
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Columns d .. d + 3 of a row of D values as floats, zeros past D; `vec`: rows
 // are whole, aligned 4-value vectors.
 __device__ __forceinline__ float4 load4(const float* row, int d, int D, bool vec) {

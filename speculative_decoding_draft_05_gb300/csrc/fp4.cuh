@@ -14,6 +14,8 @@
 
 #include <stdint.h>
 
+#include "f32x2.cuh"
+
 namespace dspark {
 
 constexpr int kFp4Block = 16;  // positions of a block, and elements of a scale
@@ -80,16 +82,27 @@ __device__ __forceinline__ uint32_t floats_to_fp4x2(float lo, float hi) {
 // The scale of a group from its largest magnitude (as bits, so that what is not
 // finite counts as the largest): its byte, and what its elements are divided by.
 // A group with an element that is not finite gets the scale NaN, and reads as NaN.
-struct Fp4Scale {
+struct Fp4Scale {  // (inverse: of value, nearly)
   uint32_t byte;
   float value, inverse;  // scale x factor; 0 where the scale is 0 or NaN: all codes are 0
 };
+__device__ __forceinline__ float reciprocal(float x) {  // within a step or so; x is normal
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The e4m3 nearest to a / (6 factor).  (The sixth is refined by its exact remainder like fp4_quotient's.)
+__device__ __forceinline__ uint32_t fp4_scale_byte(float a, float inv_factor) {
+  a = fminf(a * inv_factor, 3e38f);
+  const float sixth = 1.0f / 6.0f, q = a * sixth;
+  return float_to_e4m3(__fmaf_rn(__fmaf_rn(-q, 6.0f, a), sixth, q));
+}
 __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, float factor, float inv_factor) {
   Fp4Scale s;
   if (amax_bits >= 0x7f800000u) return Fp4Scale{0x7fu, 0.0f, 0.0f};
-  s.byte = float_to_e4m3(fminf(__uint_as_float(amax_bits) * inv_factor, 3e38f) / 6.0f);
+  s.byte = fp4_scale_byte(__uint_as_float(amax_bits), inv_factor);
   s.value = e4m3_to_float(s.byte) * factor;
-  s.inverse = s.byte == 0u ? 0.0f : 1.0f / s.value;
+  s.inverse = s.byte == 0u ? 0.0f : reciprocal(s.value);
   return s;
 }
 
@@ -102,11 +115,19 @@ __device__ __forceinline__ float fp4_quotient(float x, const Fp4Scale& s) {
   return __fmaf_rn(__fmaf_rn(-q, s.value, x), s.inverse, q);
 }
 
-// a c + b s to 24 bits with the last one set wherever the sum is not exact
-// (rounding to odd: Boldo and Melquiond, "Emulation of FMA and correctly rounded
-// sums", 2008), so that a later rounding to fewer bits, or a comparison with a
-// number of fewer, is that of the sum itself.  Products and sum as unevaluated
-// pairs (Dekker 1971, Knuth's two-sum).
+// h rounded to nearest and what it leaves, l, to one number: h with its last bit set
+// wherever l is not 0 ("rounding to odd": Boldo and Melquiond, "Emulation of FMA and
+// correctly rounded sums", 2008), so that a later rounding to fewer bits, or a comparison
+// with a number of fewer, is that of h + l.
+__device__ __forceinline__ float to_odd(float h, float l) {
+  uint32_t bits = __float_as_uint(h);
+  // (l is NaN where h is not finite)
+  if (fabsf(l) > 0.0f && !(bits & 1u)) bits += (__float_as_uint(l) ^ bits) >> 31 ? -1 : 1;
+  return __uint_as_float(bits);
+}
+
+// a c + b s, rounded to odd at 24 bits.  Products and sums as unevaluated pairs
+// (Dekker 1971, Knuth's two-sum).
 __device__ __forceinline__ float rotated_odd(float a, float c, float b, float s) {
   const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
   const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
@@ -114,11 +135,23 @@ __device__ __forceinline__ float rotated_odd(float a, float c, float b, float s)
   const float er = __fadd_rn(__fsub_rn(p, __fsub_rn(r, t)), __fsub_rn(q, t));
   const float lo = __fadd_rn(er, __fadd_rn(ep, eq));
   const float h = __fadd_rn(r, lo), u = __fsub_rn(h, r);
-  const float l = __fadd_rn(__fsub_rn(r, __fsub_rn(h, u)), __fsub_rn(lo, u));
-  uint32_t bits = __float_as_uint(h);
-  // (l is NaN where h is not finite)
-  if (l != 0.0f && !(bits & 1u) && l == l) bits += (__float_as_uint(l) ^ bits) >> 31 ? -1 : 1;
-  return __uint_as_float(bits);
+  return to_odd(h, __fadd_rn(__fsub_rn(r, __fsub_rn(h, u)), __fsub_rn(lo, u)));
+}
+
+// Two at a time.  nc, ns: c and s negated.
+__device__ __forceinline__ void rotated_odd2(f32x2 a, f32x2 c, f32x2 nc, f32x2 b, f32x2 s, f32x2 ns, float& y0,
+                                             float& y1) {
+  const f32x2 p = mul2(a, c), q = mul2(b, s);
+  const f32x2 e = add2(fma2(a, c, mul2(a, nc)), fma2(b, s, mul2(b, ns)));
+  const f32x2 r = add2(p, q), t = sub2(r, p);
+  const f32x2 lo = add2(add2(sub2(p, sub2(r, t)), sub2(q, t)), e);
+  const f32x2 h = add2(r, lo), u = sub2(h, r);
+  const f32x2 l = add2(sub2(r, sub2(h, u)), sub2(lo, u));
+  float h0, h1, l0, l1;
+  unpack2(h, h0, h1);
+  unpack2(l, l0, l1);
+  y0 = to_odd(h0, l0);
+  y1 = to_odd(h1, l1);
 }
 
 }  // namespace dspark

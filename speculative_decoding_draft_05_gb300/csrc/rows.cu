@@ -25,50 +25,111 @@ namespace {
 constexpr int kWarps = 8;  // of a CTA; a token a warp
 
 template <typename T>
-struct alignas(16) Vec16 {  // 16 bytes
-  T e[16 / sizeof(T)];
-};
-
-template <typename T>
 __device__ __forceinline__ T to_type(float x);
 template <>
 __device__ __forceinline__ float to_type<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 to_type<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
 
-// N consecutive elements as they lie in memory (a whole number of 16-byte vectors).
-template <typename T, int N>
-struct Group {
-  static constexpr int kPer = 16 / sizeof(T), kVecs = N / kPer;
-  Vec16<T> v[kVecs];
+// Eight consecutive elements as they lie in memory: one or two 16-byte vectors.
+template <typename T>
+struct Cols {
+  uint4 v[sizeof(T) / 2];
   __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = ((const Vec16<T>*)src)[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = ((const uint4*)src)[i];
   }
   __device__ __forceinline__ void store(T* dst) const {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) ((Vec16<T>*)dst)[i] = v[i];
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) ((uint4*)dst)[i] = v[i];
   }
-  __device__ __forceinline__ float get(int i) const { return to_f32(v[i / kPer].e[i % kPer]); }
-  __device__ __forceinline__ void set(int i, float x) { v[i / kPer].e[i % kPer] = to_type<T>(x); }
+  __device__ __forceinline__ uint32_t& word(int i) {
+    uint4& q = v[i / 4];
+    return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+  }
+  __device__ __forceinline__ f32x2 get(int i) {  // elements 2 i and 2 i + 1
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w = word(i);
+      return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+      return pack2(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+    }
+  }
+  __device__ __forceinline__ void set(int i, f32x2 y) {
+    float y0, y1;
+    unpack2(y, y0, y1);
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+      word(i) = *(const uint32_t*)&h;
+    } else {
+      word(2 * i) = __float_as_uint(y0), word(2 * i + 1) = __float_as_uint(y1);
+    }
+  }
 };
+
+// The largest magnitude of eight values, as bits; what is not a number counts as the largest.
+__device__ __forceinline__ uint32_t largest8(const float* y) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(y[i])), "f"(fabsf(y[i + 1])));
+  return __float_as_uint(m) & 0x7fffffffu;
+}
+
+// Eight codes of a group whose scale is s.  (fp4_quotient, two at a time.)
+__device__ __forceinline__ uint32_t codes8(const float* y, const Fp4Scale& s) {
+  if (s.inverse == 0.0f) return 0u;
+  const f32x2 inv = pack2(s.inverse, s.inverse), value = pack2(-s.value, -s.value);
+  uint32_t w = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 x = pack2(y[2 * i], y[2 * i + 1]), q = mul2(x, inv);
+    float q0, q1;
+    unpack2(fma2(fma2(q, value, x), inv, q), q0, q1);
+    w |= floats_to_fp4x2(q0, q1) << (8 * i);
+  }
+  return w;
+}
 
 // Codes and scale of a group of 16, by two neighbouring lanes of `mask` with eight values each.
 __device__ __forceinline__ void store_fp4(unsigned mask, const float* y, const float2& f, uint8_t* codes,
                                           uint8_t* scale) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
+  uint32_t amax = largest8(y);
   amax = max(amax, __shfl_xor_sync(mask, amax, 1));
   const Fp4Scale s = fp4_scale(amax, f.x, f.y);
-  uint32_t w = 0u;
-  if (s.inverse != 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w |= floats_to_fp4x2(fp4_quotient(y[2 * i], s), fp4_quotient(y[2 * i + 1], s)) << (8 * i);
-  }
-  *(uint32_t*)codes = w;
+  *(uint32_t*)codes = codes8(y, s);
   if (!(threadIdx.x & 1)) *scale = (uint8_t)s.byte;
+}
+
+// The same for values that may be off by `error`: false, and nothing written, if one of the mask's
+// groups might then get another scale or another code.  (Any lane of the mask: all are told.)
+__device__ __forceinline__ bool store_fp4_if_sure(unsigned mask, const float* y, float error, const float2& f,
+                                                  uint8_t* codes, uint8_t* scale) {
+  uint32_t amax = largest8(y);
+  amax = max(amax, __shfl_xor_sync(mask, amax, 1));
+  const float a = __uint_as_float(amax);
+  const Fp4Scale s = fp4_scale(amax, f.x, f.y);
+  bool sure = fp4_scale_byte(fmaxf(a - error, 0.0f), f.y) == fp4_scale_byte(a + error, f.y);
+  // Codes at both ends of each value's range.  (The quotient itself is off by 2^-22 of 6.5 at most.)
+  const float d = error * s.inverse + 4e-6f;
+  const f32x2 inv = pack2(s.inverse, s.inverse), up = pack2(d, d), down = pack2(-d, -d);
+  uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 q = mul2(pack2(y[2 * i], y[2 * i + 1]), inv);
+    float q0, q1;
+    unpack2(add2(q, down), q0, q1);
+    lo |= floats_to_fp4x2(q0, q1) << (8 * i);
+    unpack2(add2(q, up), q0, q1);
+    hi |= floats_to_fp4x2(q0, q1) << (8 * i);
+  }
+  // (A zero's sign does not count.  A group that is not finite, or all zero, is the exact path's.)
+  const uint32_t diff = (lo ^ hi) & 0x77777777u, sign = (lo ^ hi) & 0x88888888u;
+  sure = sure && diff == 0u && !(sign & ((lo << 1 | lo << 2 | lo << 3))) && amax < 0x7f800000u && s.inverse != 0.0f;
+  if (!__all_sync(mask, sure)) return false;
+  *(uint32_t*)codes = lo;
+  if (!(threadIdx.x & 1)) *scale = (uint8_t)s.byte;
+  return true;
 }
 
 // Where a token's rows go in the cache.
@@ -174,14 +235,21 @@ __global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const Ro
 }
 
 // Rows of whole groups of 16 on 16-byte boundaries, pairs whose groups are whole too:
-// a lane takes eight columns and the eight that they are paired with (or, interleaved
-// or past the rotated part, eight alone), so that rotation crosses no lanes; two
-// neighbours have a 4-bit group.  K and V are on their way before the token's place is
-// looked up, then the queries, four units a lane at a time.
+// a lane takes units of eight columns and the eight that they are paired with (or,
+// interleaved or past the rotated part, eight alone), so that rotation crosses no lanes;
+// two neighbours have a 4-bit group.  A warp has a token's K and V, or a part of
+// its queries; its rows are on their way before the token's place is looked up.
+struct RowSteps {
+  int turned, units, step_h, step_j;  // units of a row, rotated ones first; 32 units are step_h rows and step_j units
+  int parts;                          // warps a token: one for all, or one for K and V and the others for the queries
+  Divider by_units, by_chunks, by_parts;
+};
+constexpr int kAhead = 4;  // units a lane of a part of the queries
+constexpr int kFillTokens = 2400;
 template <typename T, bool FP4, bool Inter>
-__global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const RotaryAppendArgs p, const Divider by_units, const Divider by_chunks) {
-  typedef Group<T, 8> Cols;
-  constexpr int kKAhead = sizeof(T) == 2 ? 2 : 1, kVAhead = 2 * kKAhead, kQ = 2;  // units a lane at a time
+__global__ void __launch_bounds__(kWarps * 32, 2)
+append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
+  constexpr int kKAhead = sizeof(T) == 2 ? 2 : 1, kVAhead = 2 * kKAhead;  // units of K and V a lane at a time
   const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   wait_for_previous();
@@ -189,138 +257,230 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const Rot
     rotary_status(p);
     return;
   }
-  // Units of a row: those that are rotated first.  A unit's columns begin at d0 and, if it is a pair, d0 + half.
-  // (Both counts are even: neighbouring lanes have neighbouring units of the same row.)
-  const int turned = Inter ? p.rot / 8 : p.rot / 16, units = turned + (D - p.rot) / 8;
-  const int n = p.c.heads * units, chunks = D / 8, nv = p.c.heads * chunks, nq = p.Hq * units;
+  // Strides as 32-bit numbers (the launcher checks).
+  const int k_head = (int)p.head_stride, q_head = (int)p.q_head, qo_head = (int)p.qo_head, c_head = (int)p.c.head_stride;
   struct Unit {
-    int h, d0;
-    bool turn;
+    int h, j;
   };
-  const auto unit = [&](int i) {
-    const int h = by_units(i), j = i - h * units;
-    return Unit{h, j < turned ? 8 * j : p.rot + 8 * (j - turned), j < turned};
+  const auto next = [&](Unit u) {  // 32 units on
+    u.h += rs.step_h, u.j += rs.step_j;
+    if (u.j >= rs.units) u.j -= rs.units, ++u.h;
+    return u;
   };
-  for (int t = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * kWarps) {
+  const auto turns = [&](const Unit& u) { return u.j < rs.turned; };
+  const auto column = [&](const Unit& u) { return turns(u) ? 8 * u.j : p.rot + 8 * (u.j - rs.turned); };
+  const auto load = [&](const T* row, const Unit& u, Cols<T>& a, Cols<T>& b) {
+    const int d = column(u);
+    a.load(row + d);
+    if (!Inter && turns(u)) b.load(row + d + half);
+  };
+  Unit first;
+  first.h = rs.by_units(lane);
+  first.j = lane - first.h * rs.units;
+
+  const int jobs = p.a.n_tokens * rs.parts;
+  for (int job = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); job < jobs; job += (gridDim.x - 1) * kWarps) {
+    const int t = rs.by_parts(job), part = job - t * rs.parts;
+    const float* cs = nullptr;
+    constexpr int kAngles = Inter ? 2 : 4;  // pairs of them, of the unit `at_j`
+    f32x2 c[kAngles], s[kAngles];
+    int at_j = -1;
+    const auto angles = [&](const Unit& u) {
+      if (!turns(u) || at_j == u.j) return;
+      at_j = u.j;
+      const float* from = cs + (Inter ? 4 : 8) * u.j;
+#pragma unroll
+      for (int i = 0; i < kAngles; i += 2) {
+        const float4 x = *(const float4*)(from + 2 * i), y = *(const float4*)(from + half + 2 * i);
+        c[i] = pack2(x.x, x.y), c[i + 1] = pack2(x.z, x.w);
+        s[i] = pack2(y.x, y.y), s[i + 1] = pack2(y.z, y.w);
+      }
+    };
+    const auto minus = [](f32x2 x) { return x ^ 0x8000000080000000ull; };
+    // The unit's columns (and those paired with them, y) rotated, as fp32 pairs: the plain products and sum.
+    const auto rotate = [&](const Unit& u, Cols<T>& a, Cols<T>& b, f32x2* x, f32x2* y) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = a.get(i);
+      if (!turns(u)) return;
+      if (Inter) {  // pair i is (x0, x1) of x[i]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float e, o, ci[2], si[2];
+          unpack2(x[i], e, o);
+          unpack2(c[i / 2 % kAngles], ci[0], ci[1]);
+          unpack2(s[i / 2 % kAngles], si[0], si[1]);
+          x[i] = pack2(fmaf(e, ci[i & 1], -o * si[i & 1]), fmaf(o, ci[i & 1], e * si[i & 1]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 e = x[i], o = b.get(i);
+          x[i] = fma2(e, c[i % kAngles], mul2(o, minus(s[i % kAngles])));
+          y[i] = fma2(o, c[i % kAngles], mul2(e, s[i % kAngles]));
+        }
+      }
+    };
+    // Units i0 .. of the queries, kAhead a lane; found: the token's place is looked up.
+    const auto queries = [&](int i0, bool found) {
+      const int n = p.Hq * rs.units - i0;
+      const T* row = (const T*)p.q + t * p.q_tok;
+      T* to = (T*)p.q_out + t * p.qo_tok;
+      Unit u[kAhead];
+      Cols<T> a[kAhead], b[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k > 0) {
+          u[k] = next(u[k - 1]);
+        } else {
+          u[0].h = rs.by_units(i0 + lane), u[0].j = i0 + lane - u[0].h * rs.units;
+        }
+        if (lane + 32 * k < n) load(row + (long long)u[k].h * q_head, u[k], a[k], b[k]);
+      }
+      if (!found) {
+        const RowPlace pl = find_place(p.c, p.a, t);
+        if (!table_row(p, pl, t, &cs)) return;
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (lane + 32 * k < n) {
+          f32x2 x[4], y[4];
+          angles(u[k]);
+          rotate(u[k], a[k], b[k], x, y);
+          T* dst = to + (long long)u[k].h * qo_head + column(u[k]);
+          Cols<T> g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g.set(i, x[i]);
+          g.store(dst);
+          if (!Inter && turns(u[k])) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g.set(i, y[i]);
+            g.store(dst + half);
+          }
+        }
+      }
+    };
+    if (part > 0) {
+      queries((part - 1) * 32 * kAhead, false);
+      continue;
+    }
+    // -------------------------------------------- K and V
     const T* kn = (const T*)p.k_new + t * p.tok_stride;
     const T* vn = (const T*)p.v_new + t * p.tok_stride;
-    const T* qn = (const T*)p.q + t * p.q_tok;
-    T* qo = (T*)p.q_out + t * p.qo_tok;
-    const auto load = [&](const T* row, const Unit& u, Cols& a, Cols& b) {
-      a.load(row + u.d0);
-      if (!Inter && u.turn) b.load(row + u.d0 + half);
+    const int n = p.c.heads * rs.units, chunks = D / 8, nv = p.c.heads * chunks;
+    const auto v_from = [&](int i) {
+      const int h = rs.by_chunks(i);
+      return vn + (long long)h * k_head + (i - h * chunks) * 8;
     };
-    const auto v_at = [&](int i) {
-      const int h = by_chunks(i);
-      return h * p.head_stride + (i - h * chunks) * 8;
-    };
-    Cols ka[kKAhead], kb[kKAhead], va[kVAhead];
+    Cols<T> ka[kKAhead], kb[kKAhead], va[kVAhead];
+    Unit u = first;
 #pragma unroll
-    for (int k = 0; k < kKAhead; ++k)
-      if (lane + 32 * k < n) {
-        const Unit u = unit(lane + 32 * k);
-        load(kn + u.h * p.head_stride, u, ka[k], kb[k]);
-      }
+    for (int k = 0; k < kKAhead; ++k) {
+      if (lane + 32 * k < n) load(kn + (long long)u.h * k_head, u, ka[k], kb[k]);
+      u = next(u);
+    }
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k)
-      if (lane + 32 * k < nv) va[k].load(vn + v_at(lane + 32 * k));
+      if (lane + 32 * k < nv) va[k].load(v_from(lane + 32 * k));
     const RowPlace pl = find_place(p.c, p.a, t);
-    const float* cs = nullptr;
     if (!table_row(p, pl, t, &cs)) continue;
     const CacheRow at = cache_row<FP4>(p.c, pl);
-    constexpr int kAngles = Inter ? 4 : 8;
-    float c[kAngles], s[kAngles];  // of the unit at column `cd`
-    int cd = -1;
-    const auto angles = [&](const Unit& u) {
-      if (!u.turn || cd == u.d0) return;
-      cd = u.d0;
-      const float4* from = (const float4*)(cs + (Inter ? u.d0 / 2 : u.d0));
-#pragma unroll
-      for (int i = 0; i < kAngles; i += 4) {
-        const float4 x = from[i / 4], y = *(const float4*)((const float*)(from + i / 4) + half);
-        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-      }
-    };
-    // One rotated value: rounded to odd for the choice of codes, else in fp32.
-    const auto value = [](float x, float c, float y, float s, auto exact) {
-      return exact ? rotated_odd(x, c, y, s) : fmaf(x, c, y * s);
-    };
-    const auto rotate = [&](const Unit& u, const Cols& a, const Cols& b, float* x, float* y, auto exact) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = a.get(i), y[i] = Inter || !u.turn ? 0.0f : b.get(i);
-      if (!u.turn) return;
-      if (Inter) {
-#pragma unroll
-        for (int i = 0; i < kAngles; ++i) {
-          const float e = x[2 * i % 8], o = x[(2 * i + 1) % 8];
-          x[2 * i % 8] = value(e, c[i], o, -s[i], exact);
-          x[(2 * i + 1) % 8] = value(o, c[i], e, s[i], exact);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kAngles; ++i) {
-          const float e = x[i], o = y[i];
-          x[i] = value(e, c[i], o, -s[i], exact);
-          y[i] = value(o, c[i], e, s[i], exact);
-        }
-      }
-    };
-    const auto store = [&](T* row, const Unit& u, const float* x, const float* y) {
-      Cols g;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g.set(i, x[i]);
-      g.store(row + u.d0);
-      if (!Inter && u.turn) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g.set(i, y[i]);
-        g.store(row + u.d0 + half);
-      }
-    };
     // mask: the lanes that have one (both of a group, as their units are in range together).
-    const auto put_k = [&](unsigned mask, int i, const Cols& a, const Cols& b) {
-      const Unit u = unit(i);
-      float x[8], y[8];
+    const auto put_k = [&](unsigned mask, const Unit& u, Cols<T>& a, Cols<T>& b) {
       angles(u);
-      rotate(u, a, b, x, y, std::integral_constant<bool, FP4>{});
+      const int d = column(u);
       if constexpr (FP4) {
-        uint8_t* base = (uint8_t*)p.c.k + u.h * p.c.head_stride;
-        store_fp4(mask, x, p.k_factor, base + at.codes + u.d0 / 2, base + at.scales + u.d0 / 16);
-        if (!Inter) {
-          const unsigned pairs = __ballot_sync(mask, u.turn);
-          if (u.turn)
-            store_fp4(pairs, y, p.k_factor, base + at.codes + (u.d0 + half) / 2, base + at.scales + (u.d0 + half) / 16);
+        uint8_t* base = (uint8_t*)p.c.k + (long long)u.h * c_head;
+        uint8_t *codes = base + at.codes + d / 2, *scale = base + at.scales + d / 16;
+        const unsigned pairs = Inter ? 0u : __ballot_sync(mask, turns(u));
+        float x[8], y[8];
+        const bool any_turn = __any_sync(mask, turns(u));
+        if (any_turn) {
+          // In fp32, whose error is at most 2^-22 of the larger of the two: mostly no code and no
+          // scale hangs on it.
+          f32x2 x2[4], y2[4];
+          rotate(u, a, b, x2, y2);
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float e0, e1;
+            unpack2(a.get(i), e0, e1);
+            top = fmaxf(top, fmaxf(fabsf(e0), fabsf(e1)));
+            if (!Inter && turns(u)) {
+              unpack2(b.get(i), e0, e1);
+              top = fmaxf(top, fmaxf(fabsf(e0), fabsf(e1)));
+            }
+            unpack2(x2[i], x[2 * i], x[2 * i + 1]);
+            unpack2(y2[i], y[2 * i], y[2 * i + 1]);
+          }
+          top = fmaxf(top, __shfl_xor_sync(mask, top, 1)) * 2.4e-7f;
+          bool sure = store_fp4_if_sure(mask, x, top, p.k_factor, codes, scale);
+          if (!Inter && turns(u))
+            sure = store_fp4_if_sure(pairs, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;
+          if (__all_sync(mask, sure)) return;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 e = a.get(i);
+          unpack2(e, x[2 * i], x[2 * i + 1]);
+          if (turns(u)) {
+            if (Inter) {
+              const float e0 = x[2 * i], o0 = x[2 * i + 1];
+              float ci[2], si[2];
+              unpack2(c[i / 2 % kAngles], ci[0], ci[1]);
+              unpack2(s[i / 2 % kAngles], si[0], si[1]);
+              x[2 * i] = rotated_odd(e0, ci[i & 1], o0, -si[i & 1]);
+              x[2 * i + 1] = rotated_odd(o0, ci[i & 1], e0, si[i & 1]);
+            } else {
+              const f32x2 o = b.get(i), ci = c[i % kAngles], si = s[i % kAngles], nc = minus(ci), ns = minus(si);
+              rotated_odd2(e, ci, nc, o, ns, si, x[2 * i], x[2 * i + 1]);
+              rotated_odd2(o, ci, nc, e, si, ns, y[2 * i], y[2 * i + 1]);
+            }
+          }
+        }
+        store_fp4(mask, x, p.k_factor, codes, scale);
+        if (!Inter && turns(u)) store_fp4(pairs, y, p.k_factor, codes + half / 2, scale + half / 16);
       } else {
-        store((T*)p.c.k + at.at + u.h * p.c.head_stride, u, x, y);
+        f32x2 x[4], y[4];
+        rotate(u, a, b, x, y);
+        T* dst = (T*)p.c.k + at.at + (long long)u.h * c_head + d;
+        Cols<T> g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g.set(i, x[i]);
+        g.store(dst);
+        if (!Inter && turns(u)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g.set(i, y[i]);
+          g.store(dst + half);
+        }
       }
     };
-    const auto put_v = [&](unsigned mask, int i, const Cols& g) {
-      const int h = by_chunks(i), j = i - h * chunks;
+    const auto put_v = [&](unsigned mask, int i, Cols<T>& g) {
+      const int h = rs.by_chunks(i), j = i - h * chunks;
       if constexpr (FP4) {
-        uint8_t* base = (uint8_t*)p.c.v + h * p.c.head_stride;
+        uint8_t* base = (uint8_t*)p.c.v + (long long)h * c_head;
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = g.get(e);
+        for (int e = 0; e < 4; ++e) unpack2(g.get(e), x[2 * e], x[2 * e + 1]);
         store_fp4(mask, x, p.v_factor, base + at.codes + j * 4, base + at.scales + j / 2);
       } else {
-        g.store((T*)p.c.v + at.at + h * p.c.head_stride + j * 8);
+        g.store((T*)p.c.v + at.at + (long long)h * c_head + j * 8);
       }
     };
+    u = first;
 #pragma unroll
     for (int k = 0; k < kKAhead; ++k) {
       const unsigned mask = __ballot_sync(0xffffffffu, lane + 32 * k < n);
-      if (lane + 32 * k < n) put_k(mask, lane + 32 * k, ka[k], kb[k]);
+      if (lane + 32 * k < n) put_k(mask, u, ka[k], kb[k]);
+      u = next(u);
     }
 #pragma unroll 1
     for (int i0 = 32 * kKAhead; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned mask = __ballot_sync(0xffffffffu, i < n);
-      if (i < n) {
-        const Unit u = unit(i);
-        load(kn + u.h * p.head_stride, u, ka[0], kb[0]);
-        put_k(mask, i, ka[0], kb[0]);
+      const unsigned mask = __ballot_sync(0xffffffffu, i0 + lane < n);
+      if (i0 + lane < n) {
+        load(kn + (long long)u.h * k_head, u, ka[0], kb[0]);
+        put_k(mask, u, ka[0], kb[0]);
       }
+      u = next(u);
     }
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k) {
@@ -329,31 +489,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_rotary_kernel(const Rot
     }
 #pragma unroll 1
     for (int i0 = 32 * kVAhead; i0 < nv; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned mask = __ballot_sync(0xffffffffu, i < nv);
-      if (i < nv) {
-        va[0].load(vn + v_at(i));
-        put_v(mask, i, va[0]);
+      const unsigned mask = __ballot_sync(0xffffffffu, i0 + lane < nv);
+      if (i0 + lane < nv) {
+        va[0].load(v_from(i0 + lane));
+        put_v(mask, i0 + lane, va[0]);
       }
     }
+    if (rs.parts == 1) {
 #pragma unroll 1
-    for (int i0 = lane; i0 < nq; i0 += 32 * kQ) {
-      Cols a[kQ], b[kQ];
-#pragma unroll
-      for (int k = 0; k < kQ; ++k)
-        if (i0 + 32 * k < nq) {
-          const Unit u = unit(i0 + 32 * k);
-          load(qn + u.h * p.q_head, u, a[k], b[k]);
-        }
-#pragma unroll
-      for (int k = 0; k < kQ; ++k)
-        if (i0 + 32 * k < nq) {
-          const Unit u = unit(i0 + 32 * k);
-          float x[8], y[8];
-          angles(u);
-          rotate(u, a[k], b[k], x, y, std::false_type{});
-          store(qo + u.h * p.qo_head, u, x, y);
-        }
+      for (int i0 = 0; i0 < p.Hq * rs.units; i0 += 32 * kAhead) queries(i0, true);
     }
   }
 }
@@ -383,13 +527,14 @@ __global__ void __launch_bounds__(kWarps * 32) read_fp4_kernel(const CacheReadAr
       uint32_t x[8];
       fp4x8_to_half(w.x, x);
       fp4x8_to_half(w.y, x + 4);
-      Group<T, 16> out;
+      T* to = (T*)(is_v ? p.v_out : p.k_out) + ((long long)t * p.c.heads + h) * D + g * 16;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // (code x scale is exact in 32 bits; the factor rounds once)
-        out.set(2 * j, half_lo(x[j]) * s * f);
-        out.set(2 * j + 1, half_hi(x[j]) * s * f);
+      for (int j = 0; j < 2; ++j) {  // (code x scale is exact in 32 bits; the factor rounds once)
+        Cols<T> out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out.set(e, pack2(half_lo(x[4 * j + e]) * s * f, half_hi(x[4 * j + e]) * s * f));
+        out.store(to + 8 * j);
       }
-      out.store((T*)(is_v ? p.v_out : p.k_out) + ((long long)t * p.c.heads + h) * D + g * 16);
     }
   }
 }
@@ -430,32 +575,41 @@ int row_ctas(int n_tokens) {  // (the first one for the status word: also withou
 
 }  // namespace
 
-// Whether rows are whole groups on 16-byte boundaries, and pairs lie in whole groups.
-static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4) {
+// Whether rows are whole groups on 16-byte boundaries, pairs lie in whole groups, and
+// strides and the number of jobs fit 32 bits.
+static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4, int parts) {
   const CacheView& c = p.c;
   const int ve = 16 / esize;
   uintptr_t at = (uintptr_t)p.k_new | (uintptr_t)p.v_new | (uintptr_t)p.cos_sin;
   long long strides = p.tok_stride | p.head_stride;
   if (p.Hq > 0) at |= (uintptr_t)p.q | (uintptr_t)p.q_out, strides |= p.q_tok | p.q_head | p.qo_tok | p.qo_head;
   if (!fp4) at |= (uintptr_t)c.k | (uintptr_t)c.v, strides |= c.page_stride | c.token_stride | c.head_stride;
-  return c.head_dim % 16 == 0 && p.rot % (p.interleaved ? 16 : 32) == 0 && strides % ve == 0 && (at & 15u) == 0;
+  const long long most = 0x7fffffff;
+  return c.head_dim % 16 == 0 && p.rot % (p.interleaved ? 16 : 32) == 0 && strides % ve == 0 && (at & 15u) == 0 &&
+         p.head_stride <= most && p.q_head <= most && p.qo_head <= most && c.head_stride <= most &&
+         (long long)p.a.n_tokens * parts < 0x40000000;
 }
 
 template <typename T, bool FP4>
-static cudaError_t launch_append(const RotaryAppendArgs& p, const cudaLaunchConfig_t& cfg) {
-  const int pairs = p.rot / (p.interleaved ? 8 : 16);
-  const Divider by_units((unsigned)(pairs + (p.c.head_dim - p.rot) / 8)), by_chunks((unsigned)p.c.head_dim / 8);
-  if (!whole_groups(p, sizeof(T), FP4)) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
-  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true>, p, by_units, by_chunks)
-                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false>, p, by_units, by_chunks);
+static cudaError_t launch_append(const RotaryAppendArgs& p, cudaStream_t s) {
+  const int turned = p.rot / (p.interleaved ? 8 : 16), units = turned + (p.c.head_dim - p.rot) / 8;
+  // A warp a token where those fill the GPU (each part looks the token up again), else one a part.
+  const int split = 1 + (p.Hq * units + 32 * kAhead - 1) / (32 * kAhead);
+  const int parts = p.a.n_tokens >= kFillTokens ? 1 : split;
+  const bool vec = whole_groups(p, sizeof(T), FP4, parts);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg =
+      overlapped_launch(dim3(row_ctas(vec ? p.a.n_tokens * parts : p.a.n_tokens)), kWarps * 32, 0, s, &attr);
+  if (!vec) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
+  const RowSteps rs{turned, units, 32 / units, 32 % units, parts, Divider((unsigned)units),
+                    Divider((unsigned)p.c.head_dim / 8), Divider((unsigned)parts)};
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true>, p, rs)
+                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false>, p, rs);
 }
 
 cudaError_t launch_append_rotary(const RotaryAppendArgs& p, int dtype, bool fp4, cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = overlapped_launch(dim3(row_ctas(p.a.n_tokens)), kWarps * 32, 0, s, &attr);
-  if (dtype == DSPARK_BF16)
-    return fp4 ? launch_append<__nv_bfloat16, true>(p, cfg) : launch_append<__nv_bfloat16, false>(p, cfg);
-  return fp4 ? launch_append<float, true>(p, cfg) : launch_append<float, false>(p, cfg);
+  if (dtype == DSPARK_BF16) return fp4 ? launch_append<__nv_bfloat16, true>(p, s) : launch_append<__nv_bfloat16, false>(p, s);
+  return fp4 ? launch_append<float, true>(p, s) : launch_append<float, false>(p, s);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs& p, int esize, bool fp4, cudaStream_t s) {
