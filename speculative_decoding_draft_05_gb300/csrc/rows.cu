@@ -244,12 +244,12 @@ struct RowSteps {
   int parts;                          // warps a token: one for all, or one for K and V and the others for the queries
   Divider by_units, by_chunks, by_parts;
 };
-constexpr int kAhead = 4;  // units a lane of a part of the queries
+constexpr int kQUnits = 2;  // units a lane of a part of the queries
 constexpr int kFillTokens = 2400;
-template <typename T, bool FP4, bool Inter>
+template <typename T, bool FP4, bool Inter, bool Full>  // Full: the whole head is rotated
 __global__ void __launch_bounds__(kWarps * 32, 2)
 append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
-  constexpr int kKAhead = sizeof(T) == 2 ? 2 : 1, kVAhead = 2 * kKAhead;  // units of K and V a lane at a time
+  constexpr int kAhead = kQUnits, kKAhead = sizeof(T) == 2 ? 2 : 1, kVAhead = sizeof(T) == 2 ? 4 : 1;  // units a lane at a time
   const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   wait_for_previous();
@@ -267,7 +267,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     if (u.j >= rs.units) u.j -= rs.units, ++u.h;
     return u;
   };
-  const auto turns = [&](const Unit& u) { return u.j < rs.turned; };
+  const auto turns = [&](const Unit& u) { return Full || u.j < rs.turned; };
   const auto column = [&](const Unit& u) { return turns(u) ? 8 * u.j : p.rot + 8 * (u.j - rs.turned); };
   const auto load = [&](const T* row, const Unit& u, Cols<T>& a, Cols<T>& b) {
     const int d = column(u);
@@ -417,6 +417,10 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
           if (!Inter && turns(u))
             sure = store_fp4_if_sure(pairs, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;
           if (__all_sync(mask, sure)) return;
+          // (Rows and angles again: kept, they would cost the common path their registers.)
+          load(kn + (long long)u.h * k_head, u, a, b);
+          at_j = -1;
+          angles(u);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -594,7 +598,7 @@ template <typename T, bool FP4>
 static cudaError_t launch_append(const RotaryAppendArgs& p, cudaStream_t s) {
   const int turned = p.rot / (p.interleaved ? 8 : 16), units = turned + (p.c.head_dim - p.rot) / 8;
   // A warp a token where those fill the GPU (each part looks the token up again), else one a part.
-  const int split = 1 + (p.Hq * units + 32 * kAhead - 1) / (32 * kAhead);
+  const int split = 1 + (p.Hq * units + 32 * kQUnits - 1) / (32 * kQUnits);
   const int parts = p.a.n_tokens >= kFillTokens ? 1 : split;
   const bool vec = whole_groups(p, sizeof(T), FP4, parts);
   cudaLaunchAttribute attr;
@@ -603,8 +607,11 @@ static cudaError_t launch_append(const RotaryAppendArgs& p, cudaStream_t s) {
   if (!vec) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
   const RowSteps rs{turned, units, 32 / units, 32 % units, parts, Divider((unsigned)units),
                     Divider((unsigned)p.c.head_dim / 8), Divider((unsigned)parts)};
-  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true>, p, rs)
-                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false>, p, rs);
+  if (p.rot == p.c.head_dim)
+    return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true, true>, p, rs)
+                         : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false, true>, p, rs);
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true, false>, p, rs)
+                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false, false>, p, rs);
 }
 
 cudaError_t launch_append_rotary(const RotaryAppendArgs& p, int dtype, bool fp4, cudaStream_t s) {
