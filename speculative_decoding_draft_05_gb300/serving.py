@@ -169,6 +169,20 @@ def _rows(t, name, dtype, heads, dim, dev):
     return t.data_ptr(), ts, hs
 
 
+def _new_rows(k_new, v_new, dt, cache, dev):
+    """Pointers of K's and V's new rows and their strides, which are the same."""
+    kp, ts, hs = _rows(k_new, "k_new", dt, cache.heads, cache.head_dim, dev)
+    try:  # alike in all respects, as parts of one projection are: nothing more to look at
+        if v_new.dtype is dt and v_new.shape == k_new.shape and v_new.stride() == k_new.stride() and v_new.device == dev:
+            return kp, v_new.data_ptr(), ts, hs
+    except AttributeError:
+        pass
+    vp, vts, vhs = _rows(v_new, "v_new", dt, cache.heads, cache.head_dim, dev)
+    if v_new.shape[0] != k_new.shape[0] or ts != vts or hs != vhs:
+        raise ValueError("k_new and v_new must agree in shape and strides")
+    return kp, vp, ts, hs
+
+
 def _stream(dev, stream) -> int:
     """Handle of the launch stream: the device's current one, or the one given.  The device has to be
     the current one, where launches go."""
@@ -271,11 +285,8 @@ def dspark_cache_append_rotary(cache, layer: int, k_new, v_new, q_offsets, kv_le
     ``q`` rotated: q_out, which may be q itself, or a new tensor (rows past q_offsets[R] unwritten)."""
     dev = _cache(cache).device
     dt = _row_dtype(cache, k_new, "k_new")
-    kp, ts, hs = _rows(k_new, "k_new", dt, cache.heads, cache.head_dim, dev)
-    vp, vts, vhs = _rows(v_new, "v_new", dt, cache.heads, cache.head_dim, dev)
+    kp, vp, ts, hs = _new_rows(k_new, v_new, dt, cache, dev)
     T = k_new.shape[0]
-    if v_new.shape[0] != T or ts != vts or hs != vhs:
-        raise ValueError("k_new and v_new must agree in shape and strides")
     R, P, pt = _table(page_table, dev)
     off = _dev(q_offsets, "q_offsets", _I32, (R + 1,), dev)
     kl = _dev(kv_len, "kv_len", _I32, (R,), dev)
@@ -297,9 +308,12 @@ def dspark_cache_append_rotary(cache, layer: int, k_new, v_new, q_offsets, kv_le
             raise ValueError(f"q must have {T} tokens, got {q.shape[0]}")
         if q_out is None:
             q_out = _new(q.shape, dt, dev, stream)
-        op, ots, ohs = _rows(q_out, "q_out", dt, Hq, cache.head_dim, dev)
-        if q_out.shape[0] != T:
-            raise ValueError(f"q_out must have {T} tokens, got {q_out.shape[0]}")
+            op, ohs = q_out.data_ptr(), cache.head_dim
+            ots = Hq * ohs
+        else:
+            op, ots, ohs = _rows(q_out, "q_out", dt, Hq, cache.head_dim, dev)
+            if q_out.shape[0] != T:
+                raise ValueError(f"q_out must have {T} tokens, got {q_out.shape[0]}")
     elif q_out is not None:
         raise ValueError("q_out without q")
     fp4 = isinstance(cache, PagedCacheFp4)
