@@ -19,46 +19,49 @@
 // sees, moved (O and l rescaled) only when a score lies more than 15 above it: p < 2^15
 // fits fp16, and what underflows is below 2^-32 of the largest.  l sums p before rounding.
 //
-// A CTA walks its share in tiles of 128 keys, a block of 16 keys a warp; one warp
-// brings blocks by bulk copies (9 head_dim bytes each, K's and V's) into a ring.
-// A piece's eight partial results meet in shared memory.
+// A CTA walks its share in tiles of 128 keys, a block of 16 keys a warp.  A warp brings its
+// own blocks (9 head_dim bytes each, K's and V's) by asynchronous copies into a ring of its
+// own, so that within a piece no warp waits for another.  (A warp that brought all of them by bulk
+// copies took 150 cycles to issue each, and was the bottleneck: 173 us for decoding of 64.)
+// A piece's eight partial results meet in shared memory, while the next piece's first
+// tiles are on their way.
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
 #include "fp4.cuh"
-#include "ptx.cuh"
 
 namespace dspark {
 
 namespace {
 
-constexpr int kWarps = 8;  // that compute; one more loads
+constexpr int kWarps = 8;
 constexpr int kTN = kWarps * kFp4Block;
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 16;  // of an item
 constexpr float kRise = 15.0f, kBelow = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D, int NB>
 struct Shape {
-  static constexpr int kCtasPerSm = NB == 1 ? 2 : 1;
-  static constexpr int kCtas = 152 * kCtasPerSm;
+  static constexpr int kCtas = 152 * 2;               // two an SM
   static constexpr int kBlock = 9 * D;
-  static constexpr int kStage = 2 * kWarps * kBlock;  // K, V
+  static constexpr int kStage = 2 * kBlock;           // K, V of a warp's 16 keys
   static constexpr int kRow = D + 4;                  // floats of a row of partial results
   static constexpr int kMerge = kWarps * 8 * kRow * 4;
-  static constexpr int kRoom = 232448 / kCtasPerSm - 2048;
-  static constexpr int kFit = (kRoom - kMerge) / kStage;
+  static constexpr int kQ = NB > 1 ? NB * D / 16 * 32 * 8 : 0;  // Q's fragments, where registers have no room
+  static constexpr int kRoom = 232448 / 2 - 2 * kQ - 4096;
+  static constexpr int kFit = (kRoom - kMerge) / (kWarps * kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr int kBytes = kMerge + kStages * kStage;
+  static constexpr int kBytes = kMerge + 2 * kQ + kStages * kWarps * kStage;
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
-      : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -87,10 +90,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void sync_warps() {  // those that compute
-  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-}
-
 // N consecutive 32-bit words.
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -107,13 +106,14 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 }
 
 struct Fp4Params {
+  explicit Fp4Params(const AttnArgs& a) : p{a}, by_page((unsigned)a.c.page_size) {}
   AttnParams p;
-  long long wait_budget;
+  Divider by_page;
   int q_vec;  // q's rows are whole 16-byte vectors
 };
 
 template <int D, int NB>  // NB blocks of 8 rows an item
-__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, 2)
 attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
   using Sh = Shape<D, NB>;
   constexpr int kSteps = D / 16;  // of the first product; tiles of 16 columns of the second
@@ -122,74 +122,72 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
   constexpr int kPer = D / 8;     // columns of O a thread and row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnStart<kTN> st;
-  __shared__ uint64_t full[Sh::kStages], empty[Sh::kStages];
   __shared__ float2 stats[2][kWarps][8 * NB];  // by the parity of the piece
   __shared__ int flags, bad_from[2];
-  __shared__ volatile int abort_flag;
   const AttnParams& p = fp.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + Sh::kMerge;
+  uint8_t* ring = smem + Sh::kMerge + 2 * Sh::kQ + warp * Sh::kStages * Sh::kStage;  // the warp's
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Sh::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
     flags = 0;
-    abort_flag = 0;
     bad_from[0] = bad_from[1] = 0x7fffffff;
-    fence_barrier_init();
   }
   __syncthreads();
   wait_for_previous();
   attn_plan<kTN>(p, &st, &flags);
   AttnWalk<kTN> w = st.walk;
-  bool ok = true;
-  uint32_t slot = 0;  // tiles so far
+  if (threadIdx.x == 0) attn_write_cut(p, st);
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0) attn_write_cut(p, st);
-    const int S = p.a.c.page_size;
-    const int e = lane & (kWarps - 1);
-    const bool mine = lane < 2 * kWarps;
-    const uint8_t* pool = (const uint8_t*)(lane < kWarps ? p.a.c.k : p.a.c.v);
-    for (; !w.done() && ok; w.next(p, &flags)) {
-      const int32_t* table = p.a.a.page_table + (size_t)w.r * p.a.a.max_pages;
-      const int t1 = w.last_tile();
-      auto key_of = [&](int t) { return t * kTN + e * kFp4Block; };
-      auto page_at = [&](int t) { return mine && t < t1 && key_of(t) < w.end ? table[key_of(t) / S] : -1; };
-      int raw = page_at(w.first_tile());
-      for (int t = w.first_tile(); t < t1 && ok; ++t, ++slot) {
-        const int next = page_at(t + 1);  // read a tile ahead
-        const int stage = (int)(slot % Sh::kStages);
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], ((slot / Sh::kStages) & 1u) ^ 1u, (volatile int*)&abort_flag,
-                                               fp.wait_budget));
-        if (!ok) break;
-        const int key = key_of(t);
-        const bool has = mine && key < w.end;
-        int pg = raw;
-        if (has && (pg < 0 || pg >= p.a.c.n_pages)) {
-          flag_status(&flags, DSPARK_DEV_BAD_INPUT);
-          pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
-        }
-        const unsigned blocks = __ballot_sync(0xffffffffu, has);
-        if (lane == 0) mbar_expect_tx(&full[stage], (uint32_t)__popc(blocks) * Sh::kBlock);
-        __syncwarp();
-        if (has)
-          bulk_load(ring + stage * Sh::kStage + lane * Sh::kBlock,
-                    pool + pg * p.a.c.page_stride + w.h * p.a.c.head_stride +
-                        (long long)((key % S) / kFp4Block) * Sh::kBlock,
-                    Sh::kBlock, &full[stage]);
-        raw = next;
+  // Loads of the walk's piece, the warp's block of a tile each: groups of copies, one a tile.
+  const int S = p.a.c.page_size;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  int ids = 0, ids_next = 0;  // pages of 32 tiles, a lane each, and of the 32 after
+  auto look_up = [&](const AttnWalk<kTN>& c, int t) {
+    const int key = (t + lane) * kTN + warp * kFp4Block;
+    return key < c.end && t + lane < c.last_tile() ? p.a.a.page_table[(size_t)c.r * p.a.a.max_pages + fp.by_page(key)] : 0;
+  };
+  uint32_t fill = 0, use = 0;  // stages of the ring
+  auto load = [&](const AttnWalk<kTN>& c, int t) {  // tile t: called in order from the piece's first
+    const int i = (t - c.first_tile()) & 31;
+    if (i == 0) {
+      ids = t == c.first_tile() ? look_up(c, t) : ids_next;
+      ids_next = look_up(c, t + 32);
+    }
+    const int key = t * kTN + warp * kFp4Block;
+    int pg = __shfl_sync(0xffffffffu, ids, i);
+    if (key < c.end) {
+      if (pg < 0 || pg >= p.a.c.n_pages) {
+        if (lane == 0) flag_status(&flags, DSPARK_DEV_BAD_INPUT);
+        pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+      }
+      const long long at = pg * p.a.c.page_stride + c.h * p.a.c.head_stride +
+                           (key - fp.by_page(key) * S) / kFp4Block * Sh::kBlock + lane * 16;
+      const uint8_t *k = (const uint8_t*)p.a.c.k + at, *v = (const uint8_t*)p.a.c.v + at - Sh::kBlock;
+      const uint32_t dst = ring_at + fill * Sh::kStage + lane * 16;
+      constexpr int kChunks = Sh::kBlock / 16;  // of K; then V's
+#pragma unroll
+      for (int j = 0; j < (2 * kChunks + 31) / 32; ++j) {
+        const int c0 = 32 * j;
+        if (c0 + 32 <= 2 * kChunks || c0 + lane < 2 * kChunks)
+          copy16(dst + 512 * j, (c0 + 32 <= kChunks || (c0 < kChunks && c0 + lane < kChunks) ? k : v) + 512 * j);
       }
     }
-    if (!ok && lane == 0)  // the loads still in flight
-      for (uint32_t i = slot > Sh::kStages ? slot - Sh::kStages : 0; i < slot; ++i)
-        mbar_drain(&full[i % Sh::kStages], (i / Sh::kStages) & 1u, fp.wait_budget);
-  } else {
-    // ------------------------------------------------------------ products
+    copy_commit();
+    fill = fill + 1 == Sh::kStages ? 0 : fill + 1;
+  };
+  constexpr int kAhead = Sh::kStages - 1;
+  auto load_first = [&](const AttnWalk<kTN>& c) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!c.done() && c.first_tile() + i < c.last_tile())
+        load(c, c.first_tile() + i);
+      else
+        copy_commit(), fill = fill + 1 == Sh::kStages ? 0 : fill + 1;
+    }
+  };
+  load_first(w);
+  {
     const int g = lane >> 2, t4 = lane & 3;
     // Slot s of a block's eight keys holds key s ^ (s >> 1 & 1): rows of both
     // parities meet in the reads of V, whose 64-byte rows would else fall on the same banks.
@@ -198,11 +196,12 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
     const int key_w = key_v ^ 1;                     // and 2 t4 + 1
     const int G = p.a.G;
     uint32_t piece = 0;
-    for (; !w.done(); w.next(p, &flags), ++piece) {
+    for (; !w.done(); ++piece) {
       const int rows = w.block_rows(p), row0 = w.m * p.mr, t1 = w.last_tile();
       const int n0 = w.q.L - w.q.n + 1;  // keys that the chunk's first token sees
       const int all_see = n0 + row0 / G;
-      uint32_t qf[NB][kSteps][2];
+      uint32_t qf[NB == 1 ? kSteps : 1][2];
+      uint2* q_frags = (uint2*)(smem + Sh::kMerge + (piece & 1) * Sh::kQ);  // [NB][kSteps][32]
       float sc[NB][2];   // of the thread's columns: rows 2 t4 and 2 t4 + 1
       int lim[NB][2];    // keys that they see
 #pragma unroll
@@ -238,7 +237,14 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
         const float back = __uint_as_float((uint32_t)(254 - up) << 23) * p.scale_log2;
 #pragma unroll
         for (int i = 0; i < kSteps * 2; ++i)
-          qf[b][i >> 1][i & 1] = pack_half(__uint_as_float(raw[i] << 16) * f, __uint_as_float(raw[i] & 0xffff0000u) * f);
+          raw[i] = pack_half(__uint_as_float(raw[i] << 16) * f, __uint_as_float(raw[i] & 0xffff0000u) * f);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          if constexpr (NB == 1)
+            qf[i][0] = raw[2 * i], qf[i][1] = raw[2 * i + 1];
+          else if (warp == 0)
+            q_frags[(b * kSteps + i) * 32 + lane] = make_uint2(raw[2 * i], raw[2 * i + 1]);
+        }
         const int lim_a = live ? n0 + (int)((unsigned)(row0 + a) / (unsigned)G) : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -246,6 +252,8 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
           lim[b][i] = __shfl_sync(0xffffffffu, lim_a, (2 * t4 + i) * 4);
         }
       }
+      // (Those of the piece before the last are not read any more: its merge is behind.)
+      if (NB > 1) __syncthreads();
       float o[NB][kSteps][4], m[NB][2], l[NB][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -255,15 +263,17 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
         l[b][0] = l[b][1] = 0.0f;
       }
 
-      for (int t = w.first_tile(); t < t1; ++t, ++slot) {
-        const int stage = (int)(slot % Sh::kStages);
-        if (ok)
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], (slot / Sh::kStages) & 1u, (volatile int*)&abort_flag,
-                                                 fp.wait_budget));
+      for (int t = w.first_tile(); t < t1; ++t) {
+        if (t + kAhead < t1)
+          load(w, t + kAhead);
+        else
+          copy_commit(), fill = fill + 1 == Sh::kStages ? 0 : fill + 1;
+        copy_wait<kAhead>();
+        __syncwarp();
         const int k0 = t * kTN + warp * kFp4Block;
-        if (k0 < w.end && ok) {
-          const uint8_t* kb = ring + stage * Sh::kStage + warp * Sh::kBlock;
-          const uint8_t* vb = kb + kWarps * Sh::kBlock;
+        if (k0 < w.end) {
+          const uint8_t* kb = ring + use * Sh::kStage;
+          const uint8_t* vb = kb + Sh::kBlock;
           const bool masked = k0 + kFp4Block > all_see;
           // S^T
           float s[NB][4] = {};
@@ -296,7 +306,14 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
                 const uint32_t a[4] = {hmul2(xl[2 * h], fl), hmul2(xh[2 * h], fh), hmul2(xl[2 * h + 1], fl),
                                        hmul2(xh[2 * h + 1], fh)};
 #pragma unroll
-                for (int b = 0; b < NB; ++b) mma16816(s[b], a, qf[b][2 * j + h][0], qf[b][2 * j + h][1]);
+                for (int b = 0; b < NB; ++b) {
+                  if constexpr (NB == 1) {
+                    mma16816(s[b], a, qf[2 * j + h][0], qf[2 * j + h][1]);
+                  } else {
+                    const uint2 q = q_frags[(b * kSteps + 2 * j + h) * 32 + lane];
+                    mma16816(s[b], a, q.x, q.y);
+                  }
+                }
               }
             }
           }
@@ -391,9 +408,16 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        use = use + 1 == Sh::kStages ? 0 : use + 1;
+        __syncwarp();  // (the stage is read)
       }
+
+      // The next piece's first tiles, then this one's results.
+      const AttnWalk<kTN> cur = w;
+      w.next(p, &flags);
+      // (The ring's stages that empty groups stood for are passed over.)
+      use = fill;
+      load_first(w);
 
       // The eight warps' results.  (stats and bad_from of two pieces take turns: a warp
       // writes those of piece n + 2 after the barriers of piece n + 1.)
@@ -405,11 +429,11 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
           for (int d = 4; d < 32; d *= 2) l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], d);
           if (g == 0) stats[piece & 1][warp][8 * b + 2 * t4 + i] = make_float2(m[b][i], l[b][i]);
         }
-      const int where = attn_slot(w);
+      const int where = attn_slot(cur);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if (8 * b >= rows) break;
-        sync_warps();  // stats; the block before is read
+        __syncthreads();  // stats; the block before is read
         if (b == 0 && threadIdx.x == 0) bad_from[(piece + 1) & 1] = 0x7fffffff;  // (none is at the next piece yet)
         float* buf = (float*)smem;
 #pragma unroll
@@ -426,7 +450,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
             *(float4*)(dst + 2 * k) = v;
           }
         }
-        sync_warps();
+        __syncthreads();
         const int bad = *(volatile int*)&bad_from[piece & 1];
         for (int i = threadIdx.x; i < 8 * (D / 4); i += kWarps * 32) {
           const int a = i / (D / 4), d = i % (D / 4) * 4, r = 8 * b + a;
@@ -447,7 +471,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
           const unsigned row = row0 + r, tok = row / (unsigned)G, hq = row - tok * G;
           if (n0 + (int)tok > bad) sum = __int_as_float(0x7fc00000);
           if (where < 0) {
-            const size_t out = (size_t)(w.q.q0 + tok) * p.a.Hq + w.h * G + hq;
+            const size_t out = (size_t)(cur.q.q0 + tok) * p.a.Hq + cur.h * G + hq;
             const float inv = sum > 0.0f ? p.a.v_factor / sum : sum == 0.0f ? 0.0f : sum;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * inv, y.y * inv);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * inv, y.w * inv);
@@ -463,7 +487,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
       }
     }
   }
-  if (abort_flag && lane == 0) flag_status(&flags, DSPARK_DEV_TIMEOUT);
+  copy_wait<0>();
   __syncthreads();
   if (threadIdx.x == 0) p.flags[blockIdx.x] = flags;
 }
@@ -471,7 +495,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
 template <int D, int NB>
 cudaError_t launch(Fp4Params fp, char* ws, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  static_assert(Sh::kCtas <= kAttnMaxCtas && Sh::kStages >= 2, "");
+  static_assert(Sh::kCtas <= kAttnMaxCtas && Sh::kStages >= 3 && 2 * (Sh::kBytes + 4096) <= 233472, "");
   const AttnWorkspace w = attn_workspace_layout(kMaxRows, D, Sh::kCtas);
   AttnParams& p = fp.p;
   p.status = (int*)ws;
@@ -508,11 +532,9 @@ bool attention_fp4_few_rows(const AttnArgs& a) {
 }
 
 cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s) {
-  Fp4Params fp;
-  fp.p = AttnParams{a};
+  Fp4Params fp(a);
   fp.p.scale_log2 = a.scale * 1.4426950408889634f;
   fp.p.item_units = 1;
-  fp.wait_budget = kWaitBudget;
   fp.q_vec = ((uintptr_t)a.q & 15u) == 0 && a.q_head_stride % 8 == 0 && a.q_token_stride % 8 == 0;
   switch (a.c.head_dim) {
     case 32: return launch_rows<32>(fp, ws, s);
