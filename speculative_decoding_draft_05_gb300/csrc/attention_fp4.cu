@@ -51,7 +51,8 @@ struct Shape {
   static constexpr int kQ = NB > 1 ? NB * D / 16 * 32 * 8 : 0;  // Q's fragments, where registers have no room
   static constexpr int kRoom = 232448 / 2 - 2 * kQ - 4096;
   static constexpr int kFit = (kRoom - kMerge) / (kWarps * kStage);
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kTiles = NB == 1 ? 2 : 1;      // worked on side by side
+  static constexpr int kStages = kFit >= 8 ? 8 : NB == 1 ? kFit & ~1 : kFit;
   static constexpr int kBytes = kMerge + 2 * kQ + kStages * kWarps * kStage;
 };
 
@@ -147,7 +148,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
     const int key = (t + lane) * kTN + warp * kFp4Block;
     return key < c.end && t + lane < c.last_tile() ? p.a.a.page_table[(size_t)c.r * p.a.a.max_pages + fp.by_page(key)] : 0;
   };
-  uint32_t fill = 0, use = 0;  // stages of the ring
+  uint32_t stage = 0;  // of the ring
   auto load = [&](const AttnWalk<kTN>& c, int t) {  // tile t: called in order from the piece's first
     const int i = (t - c.first_tile()) & 31;
     if (i == 0) {
@@ -164,7 +165,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
       const long long at = pg * p.a.c.page_stride + c.h * p.a.c.head_stride +
                            (key - fp.by_page(key) * S) / kFp4Block * Sh::kBlock + lane * 16;
       const uint8_t *k = (const uint8_t*)p.a.c.k + at, *v = (const uint8_t*)p.a.c.v + at - Sh::kBlock;
-      const uint32_t dst = ring_at + fill * Sh::kStage + lane * 16;
+      const uint32_t dst = ring_at + stage * Sh::kStage + lane * 16;
       constexpr int kChunks = Sh::kBlock / 16;  // of K; then V's
 #pragma unroll
       for (int j = 0; j < (2 * kChunks + 31) / 32; ++j) {
@@ -174,16 +175,19 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
       }
     }
     copy_commit();
-    fill = fill + 1 == Sh::kStages ? 0 : fill + 1;
+    stage = stage + 1 == Sh::kStages ? 0 : stage + 1;
   };
-  constexpr int kAhead = Sh::kStages - 1;
+  auto load_none = [&] {
+    copy_commit();
+    stage = stage + 1 == Sh::kStages ? 0 : stage + 1;
+  };
   auto load_first = [&](const AttnWalk<kTN>& c) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < Sh::kStages; ++i) {
       if (!c.done() && c.first_tile() + i < c.last_tile())
         load(c, c.first_tile() + i);
       else
-        copy_commit(), fill = fill + 1 == Sh::kStages ? 0 : fill + 1;
+        load_none();
     }
   };
   load_first(w);
@@ -263,25 +267,30 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
         l[b][0] = l[b][1] = 0.0f;
       }
 
-      for (int t = w.first_tile(); t < t1; ++t) {
-        if (t + kAhead < t1)
-          load(w, t + kAhead);
-        else
-          copy_commit(), fill = fill + 1 == Sh::kStages ? 0 : fill + 1;
-        copy_wait<kAhead>();
+      constexpr int U = Sh::kTiles;
+      for (int t = w.first_tile(); t < t1; t += U) {
+        copy_wait<Sh::kStages - U>();
         __syncwarp();
-        const int k0 = t * kTN + warp * kFp4Block;
-        if (k0 < w.end) {
-          const uint8_t* kb = ring + use * Sh::kStage;
-          const uint8_t* vb = kb + Sh::kBlock;
-          const bool masked = k0 + kFp4Block > all_see;
-          // S^T
-          float s[NB][4] = {};
-          {
+        // U tiles at a time: their chains of products run side by side.  (A tile past the piece's
+        // last, like keys past the item's end, has any bytes, and is masked.)
+        int k0[U];
+        const uint8_t* kb[U];
+        bool masked = false;
+#pragma unroll
+        for (int c = 0; c < U; ++c) {
+          k0[c] = t + c < t1 ? (t + c) * kTN + warp * kFp4Block : 0x40000000;
+          kb[c] = ring + (stage + c) * Sh::kStage;
+          masked |= k0[c] + kFp4Block > all_see;
+        }
+        if (k0[0] < w.end) {
+          // S^T, each of a block's by two chains of products
+          float s[U][NB][2][4] = {};
+#pragma unroll
+          for (int c = 0; c < U; ++c) {
             uint32_t lo[KW], hi[KW];
-            load_words<KW>(kb + key_a * (D / 2) + t4 * (D / 8), lo);
-            load_words<KW>(kb + (key_a + 8) * (D / 2) + t4 * (D / 8), hi);
-            const uint8_t* ks = kb + 8 * D + key_a * (D / 16);
+            load_words<KW>(kb[c] + key_a * (D / 2) + t4 * (D / 8), lo);
+            load_words<KW>(kb[c] + (key_a + 8) * (D / 2) + t4 * (D / 8), hi);
+            const uint8_t* ks = kb[c] + 8 * D + key_a * (D / 16);
             uint32_t slo = 0, shi = 0;
             if (KW == 4) {
               slo = e4m3x2_to_half(*(const uint16_t*)(ks + 2 * t4));
@@ -308,28 +317,36 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                   if constexpr (NB == 1) {
-                    mma16816(s[b], a, qf[2 * j + h][0], qf[2 * j + h][1]);
+                    mma16816(s[c][b][h], a, qf[2 * j + h][0], qf[2 * j + h][1]);
                   } else {
                     const uint2 q = q_frags[(b * kSteps + 2 * j + h) * 32 + lane];
-                    mma16816(s[b], a, q.x, q.y);
+                    mma16816(s[c][b][h], a, q.x, q.y);
                   }
                 }
               }
             }
           }
           // P^T
-          uint32_t pf[NB][2];
+          uint32_t pf[U][NB][2];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            float x[4];
+            float x[U][4], x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = s[b][i] * sc[b][i & 1];
+            for (int c = 0; c < U; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[c][i] = (s[c][b][0][i] + s[c][b][1][i]) * sc[b][i & 1];
             if (masked) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (k0 + key_a + 8 * (i >> 1) >= lim[b][i & 1]) x[i] = -INFINITY;
+              for (int c = 0; c < U; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (k0[c] + key_a + 8 * (i >> 1) >= lim[b][i & 1]) x[c][i] = -INFINITY;
             }
-            const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
+#pragma unroll
+            for (int c = 0; c < U; ++c) {
+              x0 = fmaxf(x0, fmaxf(x[c][0], x[c][2]));
+              x1 = fmaxf(x1, fmaxf(x[c][1], x[c][3]));
+            }
             if (__any_sync(0xffffffffu, x0 > m[b][0] + kRise || x1 > m[b][1] + kRise)) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -345,21 +362,27 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
                 }
               }
             }
+            const float m0 = m[b][0] == -INFINITY ? 0.0f : m[b][0], m1 = m[b][1] == -INFINITY ? 0.0f : m[b][1];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = ex2(x[i] - (m[b][i & 1] == -INFINITY ? 0.0f : m[b][i & 1]));
-            l[b][0] += x[0] + x[2];
-            l[b][1] += x[1] + x[3];
-            pf[b][0] = transpose8x8(pack_half(x[0], x[1]));
-            pf[b][1] = transpose8x8(pack_half(x[2], x[3]));
+            for (int c = 0; c < U; ++c) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[c][i] = ex2(x[c][i] - (i & 1 ? m1 : m0));
+              l[b][0] += x[c][0] + x[c][2];
+              l[b][1] += x[c][1] + x[c][3];
+              pf[c][b][0] = transpose8x8(pack_half(x[c][0], x[c][1]));
+              pf[c][b][1] = transpose8x8(pack_half(x[c][2], x[c][3]));
+            }
           }
           // O^T
-          {
-            uint32_t v[4][VW];  // keys key_v, key_w, and 8 more
-            uint32_t vs[4][KW == 3 ? 3 : 1];
+#pragma unroll
+          for (int c = 0; c < U; ++c) {
+            const uint8_t* vb = kb[c] + Sh::kBlock;
+            constexpr int VS = KW == 3 ? 3 : 1;
+            uint32_t v[4][VW], vs[4][VS];  // keys key_v, key_w, and 8 more
+            auto key_of = [&](int i) { return (i & 1 ? key_w : key_v) + 8 * (i >> 1); };
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int key = (i & 1 ? key_w : key_v) + 8 * (i >> 1);
-              const uint8_t* row = vb + key * (D / 2) + g * (D / 16);
+              const uint8_t* row = vb + key_of(i) * (D / 2) + g * (D / 16);
               if constexpr (KW == 4 || KW == 2) {
                 load_words<VW>(row, v[i]);
               } else {
@@ -369,20 +392,29 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
                   v[i][VW - 1] = ((const uint16_t*)row)[2];
                 }
               }
-              const uint8_t* scale = vb + 8 * D + key * (D / 16);
+              const uint8_t* scale = vb + 8 * D + key_of(i) * (D / 16);
 #pragma unroll
-              for (int u = 0; u < (KW == 3 ? 3 : 1); ++u) {
-                uint32_t sv = scale[KW == 3 ? (3 * g + u) >> 2 : g * KW >> 2];
-                if (masked) {
-                  // Past the item's end: any bytes.  Where some rows of the block do not see the
-                  // key, a scale that is NaN is hidden from them, and makes the others NaN below.
-                  if (k0 + key >= all_see && (k0 + key >= w.end || (sv & 0x7fu) == 0x7fu)) {
-                    if (k0 + key < w.end) atomicMin(&bad_from[piece & 1], k0 + key);
-                    sv = 0u;
+              for (int u = 0; u < VS; ++u) vs[i][u] = scale[KW == 3 ? (3 * g + u) >> 2 : g * KW >> 2];
+            }
+            if (masked) {
+              // Past the item's end: any bytes.  Where some rows of the block do not see the
+              // key, a scale that is NaN is hidden from them, and makes the others NaN below.
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = k0[c] + key_of(i);
+#pragma unroll
+                for (int u = 0; u < VS; ++u)
+                  if (key >= all_see && (key >= w.end || (vs[i][u] & 0x7fu) == 0x7fu)) {
+                    if (key < w.end) atomicMin(&bad_from[piece & 1], key);
+                    vs[i][u] = 0u;
                   }
-                }
-                vs[i][u] = sv;
               }
+            }
+            uint32_t f0[VS], f1[VS];
+#pragma unroll
+            for (int u = 0; u < VS; ++u) {
+              f0[u] = e4m3x2_to_half(vs[0][u] | vs[1][u] << 8);
+              f1[u] = e4m3x2_to_half(vs[2][u] | vs[3][u] << 8);
             }
 #pragma unroll
             for (int wi = 0; wi < VW; ++wi) {
@@ -390,33 +422,36 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
               uint32_t x[2][4], y[2][4];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t a = v[2 * i][wi], c = v[2 * i + 1][wi];
-                fp4x8_to_half((a & 0x0f0f0f0fu) | ((c << 4) & 0xf0f0f0f0u), x[i]);
-                fp4x8_to_half(((a >> 4) & 0x0f0f0f0fu) | (c & 0xf0f0f0f0u), y[i]);
+                const uint32_t a = v[2 * i][wi], e = v[2 * i + 1][wi];
+                fp4x8_to_half((a & 0x0f0f0f0fu) | ((e << 4) & 0xf0f0f0f0u), x[i]);
+                fp4x8_to_half(((a >> 4) & 0x0f0f0f0fu) | (e & 0xf0f0f0f0u), y[i]);
               }
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int mt = 4 * wi + c;
+              for (int q = 0; q < 4; ++q) {
+                const int mt = 4 * wi + q;
                 if (mt >= kSteps) break;
                 const int u = KW == 3 ? mt >> 1 : 0;
-                const uint32_t f0 = e4m3x2_to_half(vs[0][u] | vs[1][u] << 8);
-                const uint32_t f1 = e4m3x2_to_half(vs[2][u] | vs[3][u] << 8);
-                const uint32_t a[4] = {hmul2(x[0][c], f0), hmul2(y[0][c], f0), hmul2(x[1][c], f1), hmul2(y[1][c], f1)};
+                const uint32_t a[4] = {hmul2(x[0][q], f0[u]), hmul2(y[0][q], f0[u]), hmul2(x[1][q], f1[u]),
+                                       hmul2(y[1][q], f1[u])};
 #pragma unroll
-                for (int b = 0; b < NB; ++b) mma16816(o[b][mt], a, pf[b][0], pf[b][1]);
+                for (int b = 0; b < NB; ++b) mma16816(o[b][mt], a, pf[c][b][0], pf[c][b][1]);
               }
             }
           }
         }
-        use = use + 1 == Sh::kStages ? 0 : use + 1;
-        __syncwarp();  // (the stage is read)
+        __syncwarp();  // (the stages are read)
+#pragma unroll 1
+        for (int c = 0; c < U; ++c) {
+          if (t + Sh::kStages + c < t1)
+            load(w, t + Sh::kStages + c);
+          else
+            load_none();
+        }
       }
 
       // The next piece's first tiles, then this one's results.
       const AttnWalk<kTN> cur = w;
       w.next(p, &flags);
-      // (The ring's stages that empty groups stood for are passed over.)
-      use = fill;
       load_first(w);
 
       // The eight warps' results.  (stats and bad_from of two pieces take turns: a warp
@@ -495,7 +530,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
 template <int D, int NB>
 cudaError_t launch(Fp4Params fp, char* ws, cudaStream_t s) {
   using Sh = Shape<D, NB>;
-  static_assert(Sh::kCtas <= kAttnMaxCtas && Sh::kStages >= 3 && 2 * (Sh::kBytes + 4096) <= 233472, "");
+  static_assert(Sh::kCtas <= kAttnMaxCtas && Sh::kStages >= 2 * Sh::kTiles && 2 * (Sh::kBytes + 4096) <= 233472, "");
   const AttnWorkspace w = attn_workspace_layout(kMaxRows, D, Sh::kCtas);
   AttnParams& p = fp.p;
   p.status = (int*)ws;
