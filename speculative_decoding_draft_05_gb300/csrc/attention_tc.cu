@@ -825,7 +825,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
         for (int kk = 0; kk < kEarly / 16; ++kk)
           mma_ts(o, pt + kk * 8, vt + kk * (2048 >> 4), id_o, !(first && kk == 0), lead);
-        tc_commit(&h_done[s], lead);
+        if (!FP4) tc_commit(&h_done[s], lead);  // (4-bit: P stands once it is written)
         uint32_t& k = s ? steps1 : steps0;
         const bool r = __all_sync(0xffffffffu, mbar_wait(&p_full[s], k++ & 1u, abort_flag, tp.wait_budget));
         tc_fence_after();

@@ -507,9 +507,11 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
 }
 
 // ------------------------------------------------------------------ read
-// Rows of the cache as values: a row a warp; 4-bit rows in groups of 16, a group a lane.
+// Rows of the cache as values: a row a warp.  4-bit rows in units of eight elements, whose
+// results are whole vectors of neighbouring lanes, several a lane in flight.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) read_fp4_kernel(const CacheReadArgs p) {
+__global__ void __launch_bounds__(kWarps * 32) read_fp4_kernel(const CacheReadArgs p, const Divider by_units) {
+  constexpr int kAhead = 8;
   const int lane = threadIdx.x & 31, D = p.c.head_dim;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   wait_for_previous();
@@ -517,27 +519,38 @@ __global__ void __launch_bounds__(kWarps * 32) read_fp4_kernel(const CacheReadAr
     append_status(p.c, p.a, p.status);
     return;
   }
-  const int groups = D / 16, n = p.c.heads * groups;
+  const int units = D / 8, n = p.c.heads * units;
   for (int t = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * kWarps) {
     const RowPlace pl = find_place(p.c, p.a, t);
     if (pl.page < 0) continue;
     const CacheRow at = cache_row<true>(p.c, pl);
-    for (int i = lane; i < 2 * n; i += 32) {
-      const bool is_v = i >= n;
-      const int u = is_v ? i - n : i, h = u / groups, g = u - h * groups;
-      const uint8_t* src = (const uint8_t*)(is_v ? p.c.v : p.c.k) + h * p.c.head_stride;
-      const uint2 w = *(const uint2*)(src + at.codes + g * 8);
-      const float s = e4m3_to_float(src[at.scales + g]), f = is_v ? p.v_factor : p.k_factor;
-      uint32_t x[8];
-      fp4x8_to_half(w.x, x);
-      fp4x8_to_half(w.y, x + 4);
-      T* to = (T*)(is_v ? p.v_out : p.k_out) + ((long long)t * p.c.heads + h) * D + g * 16;
+    const long long to = (long long)t * p.c.heads * D;
+#pragma unroll 1
+    for (int i0 = lane; i0 < 2 * n; i0 += 32 * kAhead) {
+      uint32_t w[kAhead], sc[kAhead];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {  // (code x scale is exact in 32 bits; the factor rounds once)
-        Cols<T> out;
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + 32 * k;
+        if (i < 2 * n) {
+          const int u = i < n ? i : i - n, h = by_units(u), j = u - h * units;
+          const uint8_t* src = (const uint8_t*)(i < n ? p.c.k : p.c.v) + h * p.c.head_stride;
+          w[k] = *(const uint32_t*)(src + at.codes + j * 4);
+          sc[k] = src[at.scales + j / 2];
+        }
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out.set(e, pack2(half_lo(x[4 * j + e]) * s * f, half_hi(x[4 * j + e]) * s * f));
-        out.store(to + 8 * j);
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + 32 * k;
+        if (i < 2 * n) {
+          // (code x scale is exact in 32 bits; the factor rounds once)
+          const float s = e4m3_to_float(sc[k]), f = i < n ? p.k_factor : p.v_factor;
+          uint32_t x[4];
+          fp4x8_to_half(w[k], x);
+          Cols<T> out;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out.set(e, pack2(half_lo(x[e]) * s * f, half_hi(x[e]) * s * f));
+          out.store(i < n ? (T*)p.k_out + to + i * 8 : (T*)p.v_out + to + (i - n) * 8);
+        }
       }
     }
   }
@@ -623,8 +636,8 @@ cudaError_t launch_cache_read(const CacheReadArgs& p, int esize, bool fp4, cudaS
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = overlapped_launch(dim3(row_ctas(p.a.n_tokens)), kWarps * 32, 0, s, &attr);
   if (fp4)
-    return esize == 2 ? cudaLaunchKernelEx(&cfg, read_fp4_kernel<__nv_bfloat16>, p)
-                      : cudaLaunchKernelEx(&cfg, read_fp4_kernel<float>, p);
+    return esize == 2 ? cudaLaunchKernelEx(&cfg, read_fp4_kernel<__nv_bfloat16>, p, Divider(p.c.head_dim / 8))
+                      : cudaLaunchKernelEx(&cfg, read_fp4_kernel<float>, p, Divider(p.c.head_dim / 8));
   const CacheView& c = p.c;
   const int ve = 16 / esize;
   const bool vec = c.head_dim % ve == 0 && c.page_stride % ve == 0 && c.token_stride % ve == 0 &&
