@@ -100,7 +100,7 @@ static_assert(256 * kRegsSoftmax<true> + 128 * kRegsOther<true> + 128 * kRegsRes
 static_assert(kThreads<true> * kRegsLaunch<true> <= 65536 && kThreads<false> * kRegsLaunch<false> <= 65536, "registers");
 constexpr int kFirstRoleWarp = 8;  // (8 idles: warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
 constexpr int kMmaWarp = 9, kLoaderWarp = 10, kProducerWarp = 11, kResultWarp = 12;
-constexpr int kDecodeWarp = 16, kDecodeWarps = 4;  // (4-bit) two teams, K's and V's, a quarter of the keys a warp
+constexpr int kDecodeWarp = 16, kDecodeWarps = 8;  // (4-bit) an eighth of a tile's keys each
 constexpr int kProducerVWarp = 8;  // (4-bit) of V's codes; the other one brings K's
 constexpr float kRangeLog2 = 60.0f;
 // P in fp16 (4-bit): m is kBelow below the maximum that sets it, and stays until a
@@ -116,14 +116,14 @@ struct Layout {
   static constexpr int kHalfBytes = 128 * 128;             // 128 rows of 128 bytes
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
   static constexpr int kStages = FP4 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
-  // (4-bit) tiles as the cache holds them, half of them K's, and the factors of Q's rows
+  // (4-bit) tiles as the cache holds them, and the factors of Q's rows
   static constexpr int kRawStages = FP4 ? (DP == 128 ? 6 : 12) : 0;
   static constexpr int kRawBytes = kTN / kFp4Block * fp4_block_bytes(DP);
   static constexpr int kOffQ = 0;  // two row blocks, or this piece's and the next one's rows
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
   static constexpr int kOffTile = kOffRaw + kRawStages * kRawBytes;   // RawTile [kRawStages]
-  static constexpr int kOffScale = kOffTile + kRawStages * 32;        // [2][128]
+  static constexpr int kOffScale = kOffTile + kRawStages * 16;        // [2][128]
   static constexpr int kOffMerge = kOffScale + (FP4 ? 2 * 128 * 4 : 0);  // (m, l) [2][128]
   static constexpr int kOffBar = kOffMerge + 2 * 128 * 8;
   static constexpr int kBars = 2 * kStages + 2 * kRawStages + 2 + 2 + 2 + 2 + 2 + 1 + 1 + 2 + 2 + 2 + 1 + (FP4 ? 2 : 0);
@@ -434,12 +434,11 @@ struct alignas(16) PieceInfo {
 static_assert(sizeof(PieceInfo) <= 64, "piece slot");
 
 // What the decoding warps have to know of a tile of codes (its loader writes it).
-struct alignas(32) RawTile {
+struct alignas(16) RawTile {
   int key0;     // -1: no more tiles
   int end;      // keys of the item from key0 on
   int all_see;  // of which all rows of the block see this many
-  int tag;      // piece + 1
-  uint32_t slot;  // in the ring of the products' operands
+  int tag;      // piece + 1, of a tile of V; else 0
 };
 
 template <int DP, bool FP4>
@@ -546,17 +545,17 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if constexpr (FP4) {
       set_regs<kRegsLaunch<FP4>, kRegsDecode>();
       const int D = p.a.c.head_dim, block = fp4_block_bytes(D);
-      const int team = (warp - kDecodeWarp) / kDecodeWarps, row0 = (warp - kDecodeWarp) % kDecodeWarps * 32;
-      constexpr int kStages = Lo::kRawStages / 2;  // of a team
-      const RawTile* tiles = (const RawTile*)(smem + Lo::kOffTile) + team * kStages;
-      for (uint32_t i = 0, phase = 0;; i == kStages - 1 ? (i = 0, phase ^= 1u) : ++i) {
-        const int rs = team * kStages + i;
-        ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], phase, abort_flag, tp.wait_budget));
+      constexpr int kKeys = kTN / kDecodeWarps;  // of a warp
+      static_assert(kKeys == kFp4Block, "a block a warp");
+      const int row0 = (warp - kDecodeWarp) * kKeys;
+      const RawTile* tiles = (const RawTile*)(smem + Lo::kOffTile);
+      for (uint32_t sl = 0;; ++sl) {
+        const int stage = (int)(sl % Lo::kStages), rs = (int)(sl % Lo::kRawStages);
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], (sl / Lo::kRawStages) & 1u, abort_flag, tp.wait_budget));
         if (!ok) break;
-        const RawTile c = tiles[i];
+        const RawTile c = tiles[rs];
         if (c.key0 < 0) break;
-        const int stage = (int)(c.slot % Lo::kStages);
-        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], ((c.slot / Lo::kStages) & 1u) ^ 1u, abort_flag,
+        ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stage], ((sl / Lo::kStages) & 1u) ^ 1u, abort_flag,
                                                tp.wait_budget));
         if (!ok) break;
         const uint32_t raw = smem_addr(smem + Lo::kOffRaw) + rs * Lo::kRawBytes;
@@ -570,7 +569,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             // scales that are NaN are hidden from them, and make the others NaN in the results.
             if (row >= c.end) {
               sc = 0u;
-            } else if (team == 1 && ((sc & 0x7fu) == 0x7fu || (sc & 0x7f00u) == 0x7f00u)) {
+            } else if (c.tag && ((sc & 0x7fu) == 0x7fu || (sc & 0x7f00u) == 0x7f00u)) {
               sc = 0u;
               atomicMax(&bad_v[(c.tag - 1) & 3], (unsigned long long)c.tag << 32 | (uint32_t)(0x7fffffff - (c.key0 + row)));
             }
@@ -586,32 +585,24 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           }
         };
         if (D == DP) {
-          // Eight rows a step (64-element rows: 16), the next loaded before the last is decoded.  Eight
-          // consecutive lanes have one half's columns, so that their stores do not meet on a bank.
-          constexpr int kUnits = DP / 32, kRows = 32 / kUnits;  // of a key; keys a step
+          // Eight rows a step (64-element rows: 16).  Eight consecutive lanes have one half's columns,
+          // so that their stores do not meet on a bank.
+          constexpr int kUnits = DP / 32, kRows = 32 / kUnits, kRun = kKeys / kRows;  // of a key; keys a step; steps
           const int r = DP == 128 ? (lane >> 1) & 7 : lane >> 1, col = (lane & 1) + (DP == 128 ? lane >> 4 << 1 : 0);
-          const uint32_t from = raw + (row0 >> 4) * fp4_block_bytes(DP) + r * (DP / 2) + col * 16;
-          const uint32_t scale = raw + (row0 >> 4) * fp4_block_bytes(DP) + 8 * DP + r * (DP / 16) + col * 2;
+          const uint32_t block0 = raw + (row0 >> 4) * fp4_block_bytes(DP);
           const uint32_t to = tile + (col >> 1) * Lo::kHalfBytes + swz(row0 + r, (col & 1) * 4);
-          // (A loop, not a run of copies: the kernel's code as a whole has to fit the SM's instruction cache.)
-          constexpr int kStep = kRows * 128;
-          auto load = [&](int i, uint4& x, uint32_t& sc) {
-            const int b = i * kRows / 16 * fp4_block_bytes(DP), q = i * kRows % 16;
-            x = ld_shared16(from + b + q * (DP / 2));
-            sc = ld_shared2(scale + b + q * (DP / 16));
-          };
-          uint4 x, next;
-          uint32_t sc, sc_next;
-          load(0, x, sc);
-#pragma unroll 1
-          for (int i = 0; i < kUnits; ++i) {
-            load(i + 1 < kUnits ? i + 1 : i, next, sc_next);
-            decode(row0 + i * kRows + r, x, sc, to, i * kStep);
-            x = next, sc = sc_next;
+          uint4 x[kRun];
+          uint32_t sc[kRun];
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) {
+            x[i] = ld_shared16(block0 + (r + i * kRows) * (DP / 2) + col * 16);
+            sc[i] = ld_shared2(block0 + 8 * DP + (r + i * kRows) * (DP / 16) + col * 2);
           }
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) decode(row0 + i * kRows + r, x[i], sc[i], to, i * kRows * 128);
         } else {
           const int units = D / 32;
-          for (int u = lane; u < 32 * units; u += 32) {
+          for (int u = lane; u < kKeys * units; u += 32) {
             const int r = u / units, col = u - r * units, row = row0 + r;
             const uint32_t b = raw + (row >> 4) * block;
             decode(row, ld_shared16(b + (row & 15) * (D / 2) + col * 16),
@@ -633,15 +624,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       set_regs<kRegsLaunch<FP4>, kRegsOther<FP4>>();
       const bool is_v = warp == kProducerVWarp;
       if (is_v && lane == 0) attn_write_cut(p, *st);
-      constexpr int kStages = Lo::kRawStages / 2;  // of one of them
       constexpr int kBlocks = kTN / kFp4Block;     // of a tile; a lane looks one up
       constexpr int kTiles = 32 / kBlocks;         // looked up at once, the next ones ahead
       const int S = p.a.c.page_size, block = fp4_block_bytes(p.a.c.head_dim);
       const uint8_t* pool = (const uint8_t*)(is_v ? p.a.c.v : p.a.c.k);
-      const int first = is_v ? kStages : 0;
-      RawTile* tiles = (RawTile*)(smem + Lo::kOffTile) + first;
-      const uint32_t raw0 = smem_addr(smem + Lo::kOffRaw) + first * Lo::kRawBytes + lane * block;
-      uint32_t rs = 0, phase = 1, n = 0;  // place in the ring, and the parity of its being empty; piece
+      RawTile* tiles = (RawTile*)(smem + Lo::kOffTile);
+      const uint32_t raw0 = smem_addr(smem + Lo::kOffRaw) + lane * block;
+      uint32_t n = 0, last = 0;  // piece; one past the slot of the last load
       // Order of the operands' ring: with two row blocks K0 V0 K1 V1 ..; over a run of smaller pieces,
       // whose products run a tile ahead, K0 K1 V0 K2 V1 ..
       uint32_t base = 0, run = 0;  // slot of the run's first tile, steps of it before this piece
@@ -683,32 +672,36 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           if (has && (lane == 0 || in_page == 0))
             count = min(min(S / kFp4Block - in_page, kBlocks - lane), (keys + kFp4Block - 1) / kFp4Block);
           const uint8_t* from = pool + pg * p.a.c.page_stride + head + in_page * block;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[first + rs], phase, abort_flag, tp.wait_budget)))) break;
+          const uint32_t sl = two ? slot : !is_v ? (run == 0 && t == cur.first_tile() ? slot + 1 : slot)
+                                         : (!joined && t == t1 - 1 ? slot - 1 : slot);
+          const int rs = (int)(sl % Lo::kRawStages);
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[rs], ((sl / Lo::kRawStages) & 1u) ^ 1u, abort_flag,
+                                                       tp.wait_budget))))
+            break;
           if (lane == 0) {  // (keys: the tile's)
-            const uint32_t sl = two ? slot : !is_v ? (run == 0 && t == cur.first_tile() ? slot + 1 : slot)
-                                           : (!joined && t == t1 - 1 ? slot - 1 : slot);
-            tiles[rs] = RawTile{key, keys, all_see - key, (int)n + 1, sl};
+            tiles[rs] = RawTile{key, keys, all_see - key, is_v ? (int)n + 1 : 0};
             const int blocks = keys >= kTN ? kBlocks : (keys + kFp4Block - 1) / kFp4Block;
-            mbar_expect_tx(&raw_full[first + rs], (uint32_t)(keys > 0 ? blocks : 0) * block);
+            mbar_expect_tx(&raw_full[rs], (uint32_t)(keys > 0 ? blocks : 0) * block);
           }
           __syncwarp();
-          if (count > 0) bulk_load(raw0 + rs * Lo::kRawBytes, from, count * block, &raw_full[first + rs]);
-          if (++rs == kStages) rs = 0, phase ^= 1u;
+          if (count > 0) bulk_load(raw0 + rs * Lo::kRawBytes, from, count * block, &raw_full[rs]);
+          last = sl + 1;
         }
         run = joined ? run + (t1 - cur.first_tile()) : 0;
         ++n;
       }
-      if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[first + rs], phase, abort_flag, tp.wait_budget));
-      if (ok) {
-        if (lane == 0) {
-          tiles[rs].key0 = -1;  // no more
-          mbar_arrive(&raw_full[first + rs]);
+      if (ok && !is_v) {  // no more, after the slots of the last run
+        const int rs = (int)(base % Lo::kRawStages);
+        ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[rs], ((base / Lo::kRawStages) & 1u) ^ 1u, abort_flag,
+                                               tp.wait_budget));
+        if (ok && lane == 0) {
+          tiles[rs].key0 = -1;
+          mbar_arrive(&raw_full[rs]);
         }
-      } else if (lane == 0) {  // the loads still in flight: the last of each stage
-        for (int i = 0; i < kStages; ++i)
-          mbar_drain(&raw_full[first + i], i < (int)rs ? phase ^ 1u : phase, tp.wait_budget);
       }
+      if (!ok && lane == 0)  // the loads still in flight, the other warp's among them
+        for (uint32_t i = last > Lo::kRawStages ? last - Lo::kRawStages : 0; i < last; ++i)
+          mbar_drain(&raw_full[i % Lo::kRawStages], (i / Lo::kRawStages) & 1u, tp.wait_budget);
     }
   } else if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
@@ -835,6 +828,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           mma_ts(o, pt + kk * 8, vt + kk * (2048 >> 4), id_o, 1u, lead);
         return true;
       };
+      // A tile's slot is free once its products are done.  (4-bit: K's by the softmax warps, as S is ready.)
       auto release = [&](uint32_t sl) { tc_commit(&kv_empty[sl % Lo::kStages], lead); };
       auto wait_half = [&](int s) {
         const uint32_t k = s ? steps1 : steps0;
@@ -857,7 +851,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           if (!ok) break;
           qk(0, 0, slot);
           qk(1, 1, slot);
-          release(slot);
+          if (!FP4) release(slot);
           if (nt == 1) tc_commit(&q_empty[n & 1], lead);
           for (int j = 0; j < nt; ++j) {
             const uint32_t vs = slot + 1, ks = slot + 2;
@@ -873,7 +867,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             release(vs);
             if (more) {
               qk(1, 1, ks);
-              release(ks);
+              if (!FP4) release(ks);
               if (j + 2 == nt) tc_commit(&q_empty[n & 1], lead);
             }
             slot += 2;
@@ -904,7 +898,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (!(ok = wait_full(slot))) return;
             const int s = iq & 1;
             qk(s, n & 1, slot);
-            release(slot++);
+            if (!FP4) release(slot);
+            ++slot;
             const bool last = ++jq == nt;
             (s ? flags1 : flags0) = (jq <= 2 ? 1u : 0u) | (last ? 2u : 0u) | (jq == 1 ? 4u : 0u);
             if (last) tc_commit(&q_empty[n & 1], lead);
@@ -965,6 +960,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         ++steps;
         if (!ok) break;
         tc_fence_after();
+        if (FP4 && (warp & 3) == 0 && lane == 0 && (!two || s == 1)) {  // K's slot
+          const uint32_t i = two ? j : run + j;
+          mbar_arrive(&kv_empty[(two || i == 0 ? base + 2 * i : base + 2 * i - 1) % Lo::kStages]);
+        }
         bool early = false;  // P's first kEarly keys are handed over
         if (warp_live) {
           const int vis = lim - k0;  // keys of the tile that the row sees
