@@ -13,8 +13,10 @@ requests with the library's calls in the order a serving loop makes them:
 and, between rounds, dspark_pages_fork (one request continued twice) and
 dspark_pages_compact.  The host reads nothing back inside a round: chunks are
 laid out flat with offsets on the device, padded to R (gamma + 1) rows.
+With rotary positions K and the queries are rotated on the way into the cache
+(dspark_cache_append_rotary); the cache may hold 4 bits an element.
 
-    python examples/paged_rounds.py
+    python examples/paged_rounds.py [--rotary] [--fp4]
 """
 from __future__ import annotations
 
@@ -44,6 +46,8 @@ class Sizes:
     n_pages: int = 96
     max_pages: int = 12
     dtype: torch.dtype = torch.bfloat16
+    rotary: bool = False  # positions by rotation of K and Q, not by a learned vector
+    fp4: bool = False     # a 4-bit cache (dspark.PagedCacheFp4)
 
 
 class Model:
@@ -65,6 +69,9 @@ class Model:
         a, self.W2 = w(d, s.r, std=1.0 / math.sqrt(d)), w(s.r, s.V, std=2.0 / math.sqrt(s.r))
         self.head = (a.float() @ self.W2.float()).to(s.dtype)
         self.W1 = (self.embed.float() @ a.float()).to(s.dtype).contiguous()
+        inv = 10000.0 ** (-torch.arange(0, s.D, 2, dtype=torch.float64) / s.D)
+        angle = torch.arange(s.page * s.max_pages, dtype=torch.float64)[:, None] * inv
+        self.cos_sin = torch.cat((angle.cos(), angle.sin()), 1).float().to(dev)
 
 
 class Server:
@@ -73,7 +80,11 @@ class Server:
         self.m = Model(s, seed, self.dev)
         shape = (s.layers, s.n_pages, s.page, s.Hkv, s.D)
         # Uninitialised on purpose: positions past a request's length are never read.
-        self.cache = dspark.PagedCache(*(torch.empty(shape, dtype=s.dtype, device=self.dev) for _ in range(2)))
+        if s.fp4:
+            shape = (s.layers, s.n_pages, s.Hkv, s.page // 16, 9 * s.D)
+            self.cache = dspark.PagedCacheFp4(*(torch.empty(shape, dtype=torch.uint8, device=self.dev) for _ in range(2)))
+        else:
+            self.cache = dspark.PagedCache(*(torch.empty(shape, dtype=s.dtype, device=self.dev) for _ in range(2)))
         i32 = dict(dtype=torch.int32, device=self.dev)
         self.table = torch.full((s.R, s.max_pages), -1, **i32)
         self.len = torch.zeros(s.R, **i32)        # positions in the cache
@@ -98,13 +109,20 @@ class Server:
     def _forward(self, tokens, q_offsets, position):
         """Target logits [T, V] of a flat chunk whose rows are appended to the cache."""
         s, m = self.s, self.m
-        h = m.embed[tokens.clamp(min=0).long()] + m.pos[position.clamp(0, m.pos.shape[0] - 1).long()]
+        h = m.embed[tokens.clamp(min=0).long()]
+        if not s.rotary:
+            h = h + m.pos[position.clamp(0, m.pos.shape[0] - 1).long()]
         T = h.shape[0]
         for layer in range(s.layers):
             qkv = (h @ m.qkv[layer]).view(T, s.Hq + 2 * s.Hkv, s.D)
             q, k, v = qkv.split([s.Hq, s.Hkv, s.Hkv], dim=1)  # parts of one array: strided rows
-            self._keep("append", dspark.dspark_cache_append(
-                self.cache, layer, k, v, q_offsets, self.len, self.table, workspace=self.ws.get("append")))
+            if s.rotary:  # q in place; K on its way into the cache
+                self._keep("append", dspark.dspark_cache_append_rotary(
+                    self.cache, layer, k, v, q_offsets, self.len, self.table, m.cos_sin, q=q, q_out=q,
+                    workspace=self.ws.get("append")))
+            else:
+                self._keep("append", dspark.dspark_cache_append(
+                    self.cache, layer, k, v, q_offsets, self.len, self.table, workspace=self.ws.get("append")))
             a = self._keep("attention", dspark.dspark_paged_attention(
                 q, self.cache, layer, q_offsets, self.len, self.table, 1.0 / math.sqrt(s.D),
                 workspace=self.ws.get("attention")))["out"]
@@ -192,7 +210,7 @@ class Server:
 
 
 def main():
-    srv = Server()
+    srv = Server(Sizes(rotary="--rotary" in sys.argv, fp4="--fp4" in sys.argv))
     g = torch.Generator().manual_seed(1)
     for slot in range(4):
         srv.prefill(slot, torch.randint(0, srv.s.V, (5 + 9 * slot,), generator=g).tolist())

@@ -245,7 +245,15 @@ struct RowSteps {
   Divider by_units, by_chunks, by_parts;
 };
 constexpr int kQUnits = 2;  // units a lane of a part of the queries
-constexpr int kFillTokens = 2400;
+// From so many tokens on a warp has a whole token: below, the parts of a token are apart, for
+// the latency, though each has to look up the token's place.  Measured (us) in a graph, whole / apart, 32 query
+// and 8 K/V heads of 128:
+//   tokens                   8            64           256          608          1216         4864
+//   bf16                     5.1 / 2.6    5.3 / 2.9    5.5 / 3.3    6.2 / 5.7    8.6 / 8.7    24.8 / 26.9
+//   bf16 to 4 bits           7.1 / 4.3    7.6 / 4.8    7.9 / 5.3    8.4 / 9.4    10.5 / 14.2  28.0 / 50.1
+//   fp32                     8.2 / 3.9    8.4 / 4.3    8.5 / 5.8    10.7 / 11.2  16.3 / 19.2  42.0 / 58.1
+template <typename T, bool FP4>
+constexpr int kWholeTokens = FP4 || sizeof(T) == 4 ? 512 : 1024;
 template <typename T, bool FP4, bool Inter, bool Full>  // Full: the whole head is rotated
 __global__ void __launch_bounds__(kWarps * 32, 2)
 append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
@@ -610,9 +618,8 @@ static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4, int par
 template <typename T, bool FP4>
 static cudaError_t launch_append(const RotaryAppendArgs& p, cudaStream_t s) {
   const int turned = p.rot / (p.interleaved ? 8 : 16), units = turned + (p.c.head_dim - p.rot) / 8;
-  // A warp a token where those fill the GPU (each part looks the token up again), else one a part.
   const int split = 1 + (p.Hq * units + 32 * kQUnits - 1) / (32 * kQUnits);
-  const int parts = p.a.n_tokens >= kFillTokens ? 1 : split;
+  const int parts = p.a.n_tokens >= kWholeTokens<T, FP4> ? 1 : split;
   const bool vec = whole_groups(p, sizeof(T), FP4, parts);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =

@@ -232,3 +232,24 @@ def test_bad_pages_and_lengths_are_flagged_and_stay_inside():
                 i["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
                 i["table"].clamp_(min=0)
                 attend(i, status=dspark.binding.DEV_BAD_INPUT)
+
+
+@pytest.mark.parametrize("chunks", [[1, 1, 1], [3, 2, 4], [20, 3, 150]])
+def test_queries_of_other_strides_and_alignments(chunks):
+    i = make(BF16, chunks, [50, 200, 300], 8, 2, 128, 16, seed=20)
+    want = attend(i)
+    T = sum(chunks)
+    for wide in (torch.zeros(T, 8, 131, dtype=BF16, device="cuda")[:, :, 1:129],
+                 torch.zeros(8, T, 136, dtype=BF16, device="cuda").transpose(0, 1)[:, :, 8:]):
+        wide.copy_(i["q"])
+        r = attend(dict(i, q=wide))
+        assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
+
+
+def test_requests_of_both_kinds_of_rows_in_one_call():
+    # the kernel is chosen by the mean: some requests have far more rows than that, some fewer
+    for Hq in (8, 32):
+        for chunks in ([1] * 60 + [300, 90], [100, 1, 1, 1], [1] * 10 + [64], [5, 0, 0, 0, 0, 0, 0, 0]):
+            lens = [max(n, (37 * r) % 700 + 1) for r, n in enumerate(chunks)]
+            i = make(BF16, chunks, lens, Hq, 2, 128, 16, seed=21)
+            check(i, attend(i))

@@ -485,3 +485,171 @@ def test_two_captured_graphs_share_workspaces():
         graphs[n][0].replay()
         torch.cuda.synchronize()
         assert torch.equal(graphs[n][1]["out"], want[n][0]) and torch.equal(graphs[n][1]["lse"], want[n][1])
+
+
+# ---------------------------------------------------------------------------- the example
+def dense_rotary(srv, tokens):
+    """Logits [n, V] of a token sequence by the definition, positions by rotation."""
+    s, m = srv.s, srv.m
+    n = len(tokens)
+    f = lambda x: x.double().cpu()  # noqa: E731
+    h = f(m.embed)[tokens]
+    mask = torch.ones(n, n).tril().bool()
+    cs = f(m.cos_sin)[:n]
+    for layer in range(s.layers):
+        q, k, v = (h @ f(m.qkv[layer])).view(n, -1, s.D).split([s.Hq, s.Hkv, s.Hkv], dim=1)
+        q, k = rotated(q, cs, False)[0], rotated(k, cs, False)[0]
+        k, v = (x.repeat_interleave(s.Hq // s.Hkv, 1) for x in (k, v))
+        a = torch.einsum("ihd,jhd->hij", q, k) / math.sqrt(s.D)
+        p = torch.softmax(a.masked_fill(~mask, -math.inf), -1)
+        h = h + torch.einsum("hij,jhd->ihd", p, v).reshape(n, -1) @ f(m.out[layer])
+    return h @ f(m.head)
+
+
+def example():
+    import importlib.util
+    import os
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("paged_rounds_rotary", os.path.join(root, "examples", "paged_rounds.py"))
+    mod = importlib.util.module_from_spec(spec)
+    sys.modules["paged_rounds_rotary"] = mod
+    spec.loader.exec_module(mod)
+    return mod
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["rows", "fp4"])
+def test_the_serving_example_with_rotary_positions(kind, dtype):
+    ex = example()
+    srv = ex.Server(ex.Sizes(dtype=dtype, n_pages=40, rotary=True, fp4=kind == "fp4"), seed=3)
+    g = torch.Generator().manual_seed(2)
+    history = {}
+    for slot, n in ((0, 3), (1, 17), (2, 40), (4, 2)):
+        history[slot] = torch.randint(0, srv.s.V, (n,), generator=g).tolist()
+        srv.prefill(slot, history[slot])
+    # bf16: four products a layer and K's rotation round their results (2^-8 of values whose sums grow with two
+    # layers of residuals); fp32: the same with 2^-24 and the sums' lengths.
+    tol = 0.08 if dtype == BF16 else 1e-4
+    for k in range(7):
+        if k == 3:
+            srv.fork(2, 5)
+            history[5] = list(history[2])
+        if k == 5:
+            srv.end(1)
+            del history[1]
+            srv.compact()
+        r = srv.round()
+        off, chunk = r["offsets"].tolist(), r["chunk"].tolist()
+        for slot in history:
+            part = chunk[off[slot]: off[slot + 1]]
+            got = r["logits"][off[slot]: off[slot + 1]].double().cpu()
+            assert got.isfinite().all()
+            if kind == "rows":
+                want = dense_rotary(srv, history[slot][:-1] + part)[-len(part):]
+                assert (got - want).norm() <= tol * want.norm(), (k, slot)
+            history[slot] += [x for x in r["tokens"][slot].tolist() if x >= 0]
+            assert srv.len[slot].item() == len(history[slot]) - 1
+        held = torch.zeros(srv.s.n_pages, dtype=torch.int32)
+        for row, n in zip(srv.table.tolist(), srv.len.tolist()):
+            for p in row[: -(-n // srv.s.page)]:
+                held[p] += 1
+        assert torch.equal(held, srv.refcount.cpu())
+
+
+# ---------------------------------------------------------------------------- what is easily forgotten
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_borders_between_codes_with_rotation(interleaved):
+    """Rotated values on a tie, and beside one by far less than fp32's step: K is a tie times a scale, and the
+    other of its pair is turned in by a sine of 0 or of +-2^-40.  The bytes are the formula's."""
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    D, half = 64, 32
+    for dtype in (F32, BF16):
+        tab = torch.zeros(4, D, device="cuda")
+        tab[:, :half] = 1.0
+        tab[1, half:], tab[2, half:] = 2.0 ** -40, -2.0 ** -40
+        tab[3, half:] = 1.0
+        tab[3, :half] = 0.0  # a quarter turn: each of a pair becomes the other
+        scales = fp4.E4M3[1:120]
+        rows = torch.zeros(len(scales), D, dtype=torch.float64)
+        for n, s in enumerate(scales.tolist()):
+            for i in range(D):
+                rows[n, i] = border[(n + i) % 7] * s * (-1) ** (i // 7)
+            rows[n, ::16] = 6 * s  # fixes the groups' scales
+        fits = (rows.to(dtype).double() == rows).all(1)
+        rows = rows[fits] if fits.sum() > 20 else rows
+        T = 4 * len(rows)
+        i = make("fp4", dtype, [T], [T], 1, 1, D, 16, factors=(1.0, 1.0))
+        i["kn"] = rows.repeat_interleave(4, 0).view(T, 1, D).to(dtype).cuda()
+        i["vn"] = torch.zeros_like(i["kn"])
+        before = dict(k=i["k"].clone(), v=i["v"].clone())
+        pos = (torch.arange(T, dtype=torch.int32) % 4).cuda()
+        append(i, tab, positions=pos, interleaved=interleaved)
+        check(i, tab[pos.long()], interleaved, before)
+
+
+def test_large_chunks_take_whole_tokens_a_warp():
+    for kind, dtype in (("rows", BF16), ("fp4", BF16), ("rows", F32), ("fp4", F32)):
+        for D, dim, inter in ((128, 128, False), (128, 64, False), (64, 64, True), (96, 32, True)):
+            i = make(kind, dtype, [700, 650], [900, 650], 12, 3, D, 32, seed=15, pad=1)
+            before = dict(k=i["k"].clone(), v=i["v"].clone())
+            tab = table_of(i["n"], dim)
+            r = append(i, tab, q=i["q"], interleaved=inter)
+            check(i, tab[i["pos"]], inter, before, r["q"])
+
+
+def test_rows_of_queries_with_other_strides_than_the_new_ones():
+    for kind in ("rows", "fp4"):
+        i = make(kind, BF16, [5, 20], [50, 20], 8, 2, 64, 16, seed=16)
+        tab = table_of(i["n"], 64)
+        want = append(i, tab, q=i["q"])["q"]
+        wide = torch.full((25, 9, 3, 64), 7.0, dtype=BF16, device="cuda")
+        out = wide[:, 1:, 1]
+        assert append(i, tab, q=i["q"], q_out=out)["q"] is out
+        assert torch.equal(out, want) and (wide[:, 0] == 7).all() and (wide[:, :, [0, 2]] == 7).all()
+        odd = torch.full((25, 8, 65), 7.0, dtype=BF16, device="cuda")[:, :, 1:]  # rows that are no 16-byte vectors
+        assert torch.equal(append(i, tab, q=i["q"], q_out=odd)["q"], want)
+
+
+def test_calls_without_tokens():
+    for kind in ("rows", "fp4"):
+        i = make(kind, BF16, [0, 0], [50, 20], 8, 2, 64, 16, seed=17)
+        before = dict(k=i["k"].clone(), v=i["v"].clone())
+        r = append(i, table_of(60, 64), q=i["q"])
+        assert r["q"].shape == (0, 8, 64)
+        assert read(i, i["off"], 0)["k"].shape == (0, 2, 64)
+        a = dspark.dspark_paged_attention(i["q"], i["cache"], 0, i["off"], i["lens"], i["table"], 0.1)
+        assert a["out"].shape == (0, 8, 64) and dspark.dspark_read_device_status(a["workspace"]) == 0
+        assert torch.equal(i["k"], before["k"]) and torch.equal(i["v"], before["v"])
+        i["off"][2] = 3  # rows that the call was not given
+        append(i, table_of(60, 64), status=BAD, q=i["q"])
+        read(i, i["off"], 0, status=BAD)
+
+
+def test_pages_past_2_to_the_32_bytes():
+    n_pages, page, Hkv, D = 60000, 16, 8, 128   # 9216 bytes a page and head: 4.4 GB each of K and V
+    k, v = (torch.empty(1, n_pages, Hkv, 1, 9 * D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    cache = dspark.PagedCacheFp4(k, v)
+    lens = [100, 30, 700]
+    held = [-(-n // page) for n in lens]
+    ids = torch.randperm(2000)[:sum(held)].int() + n_pages - 2000
+    table = torch.full((3, max(held)), -1, dtype=torch.int32)
+    for r, h in enumerate(held):
+        table[r, :h] = ids[sum(held[:r]): sum(held[:r + 1])]
+    small = make("fp4", BF16, lens, lens, 32, Hkv, D, page, seed=18, factors=(1.0, 1.0))
+    big = dict(small, cache=cache, k=k, v=v, table=table.cuda())
+    tab = table_of(800, D)
+    qs = [append(x, tab, q=x["q"])["q"] for x in (small, big)]
+    assert torch.equal(*qs)
+    a, b = (read(x, x["off"], x["T"]) for x in (small, big))
+    assert torch.equal(a["k"], b["k"]) and torch.equal(a["v"], b["v"])
+    for counts in ([1, 1, 1], [17, 5, 200]):
+        for q in (qs[0], qs[0].float()):
+            off = torch.tensor([sum(counts[:r]) for r in range(4)], dtype=torch.int32).cuda()
+            a, b = (dspark.dspark_paged_attention(q[:sum(counts)], x["cache"], 0, off, x["lens"], x["table"], 0.1)
+                    for x in (small, big))
+            assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+    moved = torch.tensor([n_pages - 1], dtype=torch.int32).cuda(), torch.tensor([3], dtype=torch.int32).cuda()
+    dspark.dspark_pages_copy(cache, *moved)
+    assert torch.equal(k[:, n_pages - 1], k[:, 3]) and torch.equal(v[:, n_pages - 1], v[:, 3])
