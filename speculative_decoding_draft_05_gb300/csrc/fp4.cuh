@@ -127,7 +127,8 @@ __device__ __forceinline__ float to_odd(float h, float l) {
 }
 
 // a c + b s, rounded to odd at 24 bits.  Products and sums as unevaluated pairs
-// (Dekker 1971, Knuth's two-sum).
+// (Dekker 1971, Knuth's two-sum).  Not in packed arithmetic: there the compiler joins a
+// product and a sum to one operation, also where they are written as roundings of their own.
 __device__ __forceinline__ float rotated_odd(float a, float c, float b, float s) {
   const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
   const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
@@ -136,22 +137,6 @@ __device__ __forceinline__ float rotated_odd(float a, float c, float b, float s)
   const float lo = __fadd_rn(er, __fadd_rn(ep, eq));
   const float h = __fadd_rn(r, lo), u = __fsub_rn(h, r);
   return to_odd(h, __fadd_rn(__fsub_rn(r, __fsub_rn(h, u)), __fsub_rn(lo, u)));
-}
-
-// Two at a time.  nc, ns: c and s negated.
-__device__ __forceinline__ void rotated_odd2(f32x2 a, f32x2 c, f32x2 nc, f32x2 b, f32x2 s, f32x2 ns, float& y0,
-                                             float& y1) {
-  const f32x2 p = mul2(a, c), q = mul2(b, s);
-  const f32x2 e = add2(fma2(a, c, mul2(a, nc)), fma2(b, s, mul2(b, ns)));
-  const f32x2 r = add2(p, q), t = sub2(r, p);
-  const f32x2 lo = add2(add2(sub2(p, sub2(r, t)), sub2(q, t)), e);
-  const f32x2 h = add2(r, lo), u = sub2(h, r);
-  const f32x2 l = add2(sub2(r, sub2(h, u)), sub2(lo, u));
-  float h0, h1, l0, l1;
-  unpack2(h, h0, h1);
-  unpack2(l, l0, l1);
-  y0 = to_odd(h0, l0);
-  y1 = to_odd(h1, l1);
 }
 
 }  // namespace dspark

@@ -432,20 +432,23 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x2 e = a.get(i);
-          unpack2(e, x[2 * i], x[2 * i + 1]);
-          if (turns(u)) {
-            if (Inter) {
-              const float e0 = x[2 * i], o0 = x[2 * i + 1];
-              float ci[2], si[2];
-              unpack2(c[i / 2 % kAngles], ci[0], ci[1]);
-              unpack2(s[i / 2 % kAngles], si[0], si[1]);
-              x[2 * i] = rotated_odd(e0, ci[i & 1], o0, -si[i & 1]);
-              x[2 * i + 1] = rotated_odd(o0, ci[i & 1], e0, si[i & 1]);
-            } else {
-              const f32x2 o = b.get(i), ci = c[i % kAngles], si = s[i % kAngles], nc = minus(ci), ns = minus(si);
-              rotated_odd2(e, ci, nc, o, ns, si, x[2 * i], x[2 * i + 1]);
-              rotated_odd2(o, ci, nc, e, si, ns, y[2 * i], y[2 * i + 1]);
+          unpack2(a.get(i), x[2 * i], x[2 * i + 1]);
+          if (!turns(u)) continue;
+          float ci[2], si[2];
+          unpack2(c[(Inter ? i / 2 : i) % kAngles], ci[0], ci[1]);
+          unpack2(s[(Inter ? i / 2 : i) % kAngles], si[0], si[1]);
+          if (Inter) {
+            const float e = x[2 * i], o = x[2 * i + 1];
+            x[2 * i] = rotated_odd(e, ci[i & 1], o, -si[i & 1]);
+            x[2 * i + 1] = rotated_odd(o, ci[i & 1], e, si[i & 1]);
+          } else {
+            float o[2];
+            unpack2(b.get(i), o[0], o[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float e = x[2 * i + k];
+              x[2 * i + k] = rotated_odd(e, ci[k], o[k], -si[k]);
+              y[2 * i + k] = rotated_odd(o[k], ci[k], e, si[k]);
             }
           }
         }

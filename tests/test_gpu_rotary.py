@@ -653,3 +653,38 @@ def test_pages_past_2_to_the_32_bytes():
     moved = torch.tensor([n_pages - 1], dtype=torch.int32).cuda(), torch.tensor([3], dtype=torch.int32).cuda()
     dspark.dspark_pages_copy(cache, *moved)
     assert torch.equal(k[:, n_pages - 1], k[:, 3]) and torch.equal(v[:, n_pages - 1], v[:, 3])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_rotated_values_nearer_to_a_border_than_fp32_tells(dtype, interleaved):
+    """For random a, b and sine the cosine is the float for which a c - b s comes nearest to a border between two
+    codes: mostly within 2^-25 of it, on either side.  The bytes are the formula's."""
+    g = torch.Generator().manual_seed(30)
+    T, D, half = 1500, 64, 32
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    scale = fp4.E4M3[40:80][torch.randint(0, 40, (T, 1), generator=g)]
+    target = border[torch.randint(0, 7, (T, half), generator=g)] * scale * (1 - 2 * torch.randint(0, 2, (T, half), generator=g))
+    a, b = ((torch.rand(T, half, generator=g) + 0.5) * scale * 3).to(dtype).double(), \
+        (torch.randn(T, half, generator=g) * scale).to(dtype).double()
+    sin = torch.rand(T, half, generator=g).float()
+    cos = ((target + b * sin.double()) / a).float()
+    per = 8 if interleaved else 16  # pairs whose first outputs are in one group of 16
+    fix = torch.arange(0, half, per)
+    a[:, fix], b[:, fix], cos[:, fix], sin[:, fix] = 6 * scale, 0.0, 1.0, 0.0  # the group's scale
+    if interleaved:  # the others of the pairs lie in the same group: keep them small
+        small = torch.arange(half) % per != 0
+        b[:, small], sin[:, small] = 0.0, sin[:, small] * 0.25
+        sin = sin.to(torch.float32)
+        cos[:, small] = (target[:, small] / a[:, small]).float()
+    y = a * cos.double() - b * sin.double()
+    near_ = ((y - target).abs() <= 2.0 ** -23 * target.abs()).float().mean()
+    assert near_ > 0.5
+    rows = torch.stack((a, b), -1).flatten(-2) if interleaved else torch.cat((a, b), -1)
+    i = make("fp4", dtype, [T], [T], 1, 1, D, 16, factors=(1.0, 1.0))
+    i["kn"] = rows.view(T, 1, D).to(dtype).cuda()
+    i["vn"] = torch.zeros_like(i["kn"])
+    tab = torch.cat((cos, sin), 1).cuda()
+    before = dict(k=i["k"].clone(), v=i["v"].clone())
+    append(i, tab, interleaved=interleaved)
+    check(i, tab[i["pos"]], interleaved, before)
