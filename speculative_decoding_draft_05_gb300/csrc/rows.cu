@@ -5,8 +5,8 @@
 //   (a, b) -> (a c - b s, b c + a s),   pairs (i, i + rot / 2) or (2 i, 2 i + 1).
 // Quantisation of a group y of 16 (after the rotation, divided by the factor):
 //   scale = e4m3(max |y| / 6), code_j = e2m1(y_j / scale), both nearest, ties to even.
-// K's rotated values are kept exact enough for that (rotated_odd), so that the
-// stored bytes are those of the formula in infinite precision.
+// K's rotated values are kept exact enough for that (rotated_odd: to about 2^-46 of the
+// products), so that the stored bytes are those of the formula.
 //
 // Bound by memory: a row is read once and written once; the chain before a store
 // (request, length, page: four dependent loads, then the table's row) is
@@ -293,6 +293,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     constexpr int kAngles = Inter ? 2 : 4;  // pairs of them, of the unit `at_j`
     f32x2 c[kAngles], s[kAngles];
     int at_j = -1;
+    float largest = 1.0f;  // of their magnitudes and 1 (4-bit)
     const auto angles = [&](const Unit& u) {
       if (!turns(u) || at_j == u.j) return;
       at_j = u.j;
@@ -302,6 +303,17 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         const float4 x = *(const float4*)(from + 2 * i), y = *(const float4*)(from + half + 2 * i);
         c[i] = pack2(x.x, x.y), c[i + 1] = pack2(x.z, x.w);
         s[i] = pack2(y.x, y.y), s[i + 1] = pack2(y.z, y.w);
+      }
+      if constexpr (FP4) {
+        largest = 1.0f;
+#pragma unroll
+        for (int i = 0; i < kAngles; ++i) {
+          float x0, x1;
+          unpack2(c[i], x0, x1);
+          largest = fmaxf(largest, fmaxf(fabsf(x0), fabsf(x1)));
+          unpack2(s[i], x0, x1);
+          largest = fmaxf(largest, fmaxf(fabsf(x0), fabsf(x1)));
+        }
       }
     };
     const auto minus = [](f32x2 x) { return x ^ 0x8000000080000000ull; };
@@ -403,8 +415,9 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         float x[8], y[8];
         const bool any_turn = __any_sync(mask, turns(u));
         if (any_turn) {
-          // In fp32, whose error is at most 2^-22 of the larger of the two: mostly no code and no
-          // scale hangs on it.
+          // In fp32, whose error is at most 3 2^-24 of the largest element times the largest of the
+          // angles (which a table scaled for long contexts has above 1): mostly no code and no scale
+          // hangs on it.
           f32x2 x2[4], y2[4];
           rotate(u, a, b, x2, y2);
           float top = 0.0f;
@@ -420,7 +433,8 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
             unpack2(x2[i], x[2 * i], x[2 * i + 1]);
             unpack2(y2[i], y[2 * i], y[2 * i + 1]);
           }
-          top = fmaxf(top, __shfl_xor_sync(mask, top, 1)) * 2.4e-7f;
+          top *= largest * 2.4e-7f;
+          top = fmaxf(top, __shfl_xor_sync(mask, top, 1));
           bool sure = store_fp4_if_sure(mask, x, top, p.k_factor, codes, scale);
           if (!Inter && turns(u))
             sure = store_fp4_if_sure(pairs, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;

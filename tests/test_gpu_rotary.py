@@ -688,3 +688,30 @@ def test_rotated_values_nearer_to_a_border_than_fp32_tells(dtype, interleaved):
     before = dict(k=i["k"].clone(), v=i["v"].clone())
     append(i, tab, interleaved=interleaved)
     check(i, tab[i["pos"]], interleaved, before)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim", [64, 32])
+def test_a_table_of_more_than_cosines_and_sines(dtype, interleaved, dim):
+    """Tables scaled for long contexts hold more than 1; here products up to a thousand times the value that is
+    left of them, next to a border between two codes.  The bytes are the formula's."""
+    g = torch.Generator().manual_seed(31)
+    T, D, half = 1500, 64, dim // 2
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    target = border[torch.randint(0, 7, (T, half), generator=g)]
+    a = (torch.rand(T, half, generator=g) + 0.5).to(dtype).double()
+    b = torch.randn(T, half, generator=g).to(dtype).double()
+    sin = (torch.randn(T, half, generator=g) * 500).float()
+    cos = ((target + b * sin.double()) / a).float()
+    a[:, ::16], b[:, ::16], cos[:, ::16], sin[:, ::16] = 6.0, 0.0, 1.0, 0.0  # a group's scale is 1 (if it has one output)
+    i = make("fp4", dtype, [T], [T], 1, 1, D, 16, factors=(1.0, 1.0))
+    k = torch.zeros(T, D, dtype=torch.float64)
+    j = torch.arange(half)
+    k[:, 2 * j if interleaved else j], k[:, 2 * j + 1 if interleaved else j + half] = a, b
+    i["kn"] = k.view(T, 1, D).to(dtype).cuda()
+    i["vn"] = torch.zeros_like(i["kn"])
+    tab = torch.cat((cos, sin), 1).cuda()
+    before = dict(k=i["k"].clone(), v=i["v"].clone())
+    append(i, tab, interleaved=interleaved)
+    check(i, tab[i["pos"]], interleaved, before)
