@@ -278,7 +278,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
         bool masked = false;
 #pragma unroll
         for (int c = 0; c < U; ++c) {
-          k0[c] = t + c < t1 ? (t + c) * kTN + warp * kFp4Block : 0x40000000;
+          k0[c] = t + c < t1 ? (t + c) * kTN + warp * kFp4Block : 0x7fffff00;  // (past any length)
           kb[c] = ring + (stage + c) * Sh::kStage;
           masked |= k0[c] + kFp4Block > all_see;
         }

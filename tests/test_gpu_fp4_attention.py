@@ -253,3 +253,23 @@ def test_requests_of_both_kinds_of_rows_in_one_call():
             lens = [max(n, (37 * r) % 700 + 1) for r, n in enumerate(chunks)]
             i = make(BF16, chunks, lens, Hq, 2, 128, 16, seed=21)
             check(i, attend(i))
+
+
+@pytest.mark.parametrize("chunk, dtype", [(1, BF16), (2, BF16), (40, BF16), (2, F32)])
+def test_a_request_of_2_to_the_31_positions(chunk, dtype):
+    """The longest request there is, of one page many times over: K is 0 and V is 1, so that every partial sum is
+    a number of positions (times a power of two), exact up to 2^24.  304 or fewer partial results meet: (304 + 16)
+    2^-24."""
+    L, page = 2 ** 31 - 2 ** 16, 65536
+    P = 32768
+    k = torch.zeros(1, 1, 1, page // 16, 9 * 32, dtype=torch.uint8, device="cuda")
+    v = torch.full_like(k, 0x22)
+    fp4.parts(v)[1].fill_(0x38)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    i = dict(k=k, v=v, factors=(1.0, 1.0), q=torch.ones(chunk, 4, 32, dtype=dtype, device="cuda"), scale=0.2,
+             off=torch.tensor([0, chunk], **i32), lens=torch.tensor([L], **i32), table=torch.zeros(1, P, **i32))
+    r = attend(i)
+    tol = 320 * 2.0 ** -24
+    want = torch.tensor([math.log(L - chunk + 1 + t) for t in range(chunk)], dtype=torch.float64)[:, None]
+    assert ((r["out"].double() - 1).abs() <= tol + (2.0 ** -8 if dtype == BF16 else 0)).all()
+    assert ((r["lse"].cpu().double() - want).abs() <= tol + 8 * 2.0 ** -24 * want).all()
