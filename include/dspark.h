@@ -504,7 +504,8 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
  * divided by the factor,
  *   scale = e4m3(max |y| / 6),  code_j = e2m1(y_j / scale)
  * each the nearest, ties to even, at most 448 and 6.  With a factor that is a
- * power of two the bytes are those of the formula in infinite precision.  A group with
+ * power of two the bytes are those of the formula in infinite precision, as far as
+ * 2^-46 (|a c| + |b s|) decides and products stay in fp32's range.  A group with
  * an element that is not finite gets the scale NaN, and reads as NaN.
  *
  * rotary    HOST struct, read by the call: cos_sin [n_positions, dim] float, dim
@@ -513,7 +514,8 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
  *           NULL: its position in the cache
  * dtype     of k_new, v_new, q, q_out: DSPARK_F32 or DSPARK_BF16, the cache's where
  *           that is one of them
- * q, q_out  [n_tokens, Hq, head_dim], strides in elements, head_dim contiguous;
+ * q, q_out  [n_tokens, Hq, head_dim], strides in elements (q_out's no less than
+ *           head_dim), head_dim contiguous;
  *           q_out may be q itself (with its strides), and may not overlap it
  *           otherwise.  Hq = 0: no queries.
  * A token whose position lies past the table is flagged (DSPARK_DEV_BAD_INPUT)

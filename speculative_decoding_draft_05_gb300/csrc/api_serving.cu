@@ -219,6 +219,9 @@ int dspark_cache_append_rotary(const dspark_cache* cache, int layer, float k_fac
     return DSPARK_ERR_INVALID_ARG;
   if (Hq > 0 && n_tokens != 0 && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
     return DSPARK_ERR_INVALID_ARG;
+  if ((Hq > 1 && n_tokens != 0 && q_out_head_stride < cache->head_dim) ||
+      (Hq > 0 && n_tokens > 1 && q_out_token_stride < cache->head_dim))  // rows of q_out one over the other
+    return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(dtype) - 1);
   if (((uintptr_t)k_new & a) || ((uintptr_t)v_new & a) || ((uintptr_t)q & a) || ((uintptr_t)q_out & a))
     return DSPARK_ERR_INVALID_ARG;

@@ -102,7 +102,7 @@ def test_append(lib):
     for kw in (dict(k=None), dict(v=None), dict(q=None), dict(qo=None), dict(off=None), dict(kv=None), dict(tab=None),
                dict(T=-1), dict(ts=-1), dict(hs=-1), dict(qts=-1), dict(qhs=-1), dict(ots=-1), dict(ohs=-1), dict(Hq=-1),
                dict(k=257), dict(q=257), dict(qo=257), dict(dt=2), dict(R=0), dict(P=0), dict(layer=2),
-               dict(q=512, ots=300), dict(q=512, ohs=80)):
+               dict(q=512, ots=300), dict(q=512, ohs=80), dict(ots=0), dict(ots=63), dict(ohs=0), dict(ohs=63)):
         assert append(lib, None, good, **kw) == 1, kw
     for f in FACTORS:
         assert append(lib, None, good, kf=f) == 1 and append(lib, None, good, vf=f) == 1, f
