@@ -55,6 +55,18 @@
 //     PFLOP/s, 83 % of a library product's rate, for the first tenth of a second
 //     at 2070 MHz; 458 us, 1.44 PFLOP/s, once the power limit holds the clock at
 //     1.75 .. 1.95 GHz).
+//   * Over a 4-bit cache (FP4), operands are fp16, in which code x scale is exact:
+//     - warps 11 and 8 bring blocks of K's and V's codes (bulk copies, the blocks of a page
+//       in one) and warps 16..23 turn them into the ring's tiles, a block of 16 keys each, with
+//       the keys past an item's end as zeros and the NaN scales of V dealt with on the way;
+//       results' warps load Q, a row times a power of two; the factor of V is in the results.
+//     - P is fp16, so m has to stand before P is written: two passes over S (see the softmax).
+//     - 768 threads share the registers and the instruction cache, which decides more than
+//       the arithmetic does: loops, not unrolled code, 112 / 88 / 56 registers.
+//     - What bounds it: the chain of a stream again, about 2500 cycles for a K and V tile of
+//       each stream whether a block has 8 rows or 68; 1600 of them are the traffic of shared memory.
+//       Verify as above, 349 MB: 177 us; 4 requests over 100 k positions, 569 MB: 259 us; prompts of
+//       3556 + 4096 tokens: 607 us, 1.06 PFLOP/s.
 //   * Every mbarrier wait is bounded; on expiry the CTA flags
 //     DSPARK_DEV_TIMEOUT, drains what it issued, frees TMEM and returns.
 #include <cuda.h>
@@ -98,7 +110,7 @@ static_assert(256 * kRegsSoftmax<false> + 128 * kRegsOther<false> + 128 * kRegsR
 static_assert(256 * kRegsSoftmax<true> + 128 * kRegsOther<true> + 128 * kRegsResult<true> + 256 * kRegsDecode <=
                   kThreads<true> * kRegsLaunch<true>, "a split above the launch's registers waits forever");
 static_assert(kThreads<true> * kRegsLaunch<true> <= 65536 && kThreads<false> * kRegsLaunch<false> <= 65536, "registers");
-constexpr int kFirstRoleWarp = 8;  // (8 idles: warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
+constexpr int kFirstRoleWarp = 8;  // (bf16: 8 idles, as warps 0, 4 and 12 share its scheduler, the busiest one for few rows)
 constexpr int kMmaWarp = 9, kLoaderWarp = 10, kProducerWarp = 11, kResultWarp = 12;
 constexpr int kDecodeWarp = 16, kDecodeWarps = 8;  // (4-bit) an eighth of a tile's keys each
 constexpr int kProducerVWarp = 8;  // (4-bit) of V's codes; the other one brings K's
@@ -472,7 +484,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   uint64_t* raw_empty = raw_full + Lo::kRawStages;  // and read (the decoding warps)
   uint64_t* i_full = raw_empty + Lo::kRawStages;    // (4-bit) [2] piece n (n & 1) published
   // Piece n's first key with a V that is not finite among those that not all of
-  // its rows see: word n & 1 (4-bit: n & 3, as codes are decoded ahead of the piece before's results), (n + 1) << 32 | 2^31 - 1 - key, the largest counts.
+  // its rows see: word n & 1 (4-bit: n & 3, as codes are decoded ahead of the results of the
+  // piece before), (n + 1) << 32 | 2^31 - 1 - key, the largest counts.
   // (Of another piece: none.  The tag spares the clearing between pieces.)
   unsigned long long* bad_v = (unsigned long long*)(smem + Lo::kOffBad);
   uint32_t* tmem_slot = (uint32_t*)(bad_v + Lo::kBadWords);

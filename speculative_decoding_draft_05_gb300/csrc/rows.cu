@@ -11,6 +11,10 @@
 // Bound by memory: a row is read once and written once; the chain before a store
 // (request, length, page: four dependent loads, then the table's row) is
 // hidden by the rows of other warps, and by loading a row's K and V ahead of it.
+// Measured, 32 query and 8 K/V heads of 128: 4868 tokens of 512 requests into a bf16
+// cache 25.5 us in a graph (122 MB, 4.8 TB/s); prompts of 26,418 tokens into a 4-bit cache
+// 126 us (580 MB, 4.6 TB/s, half of the issue slots taken by rotation, error bound and
+// conversions); reading 36,321 positions of a 4-bit cache 36 us (191 MB, 5.4 TB/s).
 #include <type_traits>
 
 #include "append.cuh"
