@@ -12,9 +12,10 @@
 // (request, length, page: four dependent loads, then the table's row) is
 // hidden by the rows of other warps, and by loading a row's K and V ahead of it.
 // Measured, 32 query and 8 K/V heads of 128: 4868 tokens of 512 requests into a bf16
-// cache 25.5 us in a graph (122 MB, 4.8 TB/s); prompts of 26,418 tokens into a 4-bit cache
-// 126 us (580 MB, 4.6 TB/s, half of the issue slots taken by rotation, error bound and
-// conversions); reading 36,321 positions of a 4-bit cache 36 us (191 MB, 5.4 TB/s).
+// cache 25.5 us in a graph (122 MB, 4.8 TB/s); prompts of 16,384 tokens into a bf16 cache 70 us
+// (411 MB, 5.9 TB/s; of half-rotated heads 90), into a 4-bit one 79 us (362 MB, 4.6 TB/s, half of the
+// issue slots taken by rotation, error bound and conversions; half-rotated 100); reading 36,321
+// positions of a 4-bit cache 35 us (191 MB, 5.5 TB/s).
 #include <type_traits>
 
 #include "append.cuh"
@@ -239,29 +240,34 @@ __global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const Ro
 }
 
 // Rows of whole groups of 16 on 16-byte boundaries, pairs whose groups are whole too:
-// a lane takes units of eight columns and the eight that they are paired with (or,
-// interleaved or past the rotated part, eight alone), so that rotation crosses no lanes;
-// two neighbours have a 4-bit group.  A warp has a token's K and V, or a part of
-// its queries; its rows are on their way before the token's place is looked up.
+// a lane takes units of eight rotated columns and the eight that they are paired with (or,
+// interleaved, eight alone), so that rotation crosses no lanes, and chunks of eight of what is
+// not rotated; two neighbours have a 4-bit group.  A warp has a token's K and V, or a part
+// of its queries; its rows are on their way before the token's place is looked up.
 struct RowSteps {
-  int turned, units, step_h, step_j;  // units of a row, rotated ones first; 32 units are step_h rows and step_j units
-  int parts;                          // warps a token: one for all, or one for K and V and the others for the queries
-  Divider by_units, by_chunks, by_parts;
+  int units, step_h, step_j;  // rotated units of a row; 32 of them are step_h rows and step_j units
+  int plain;                  // chunks of a row of K or Q that are not rotated
+  int parts;                  // warps a token
+  Divider by_units, by_plain, by_chunks, by_parts;
 };
-constexpr int kQUnits = 2;  // units a lane of a part of the queries
-// From so many tokens on a warp has a whole token: below, the parts of a token are apart, for
-// the latency, though each has to look up the token's place.  Measured (us) in a graph, whole / apart, 32 query
-// and 8 K/V heads of 128:
-//   tokens                   8            64           256          608          1216         4864
-//   bf16                     5.1 / 2.6    5.3 / 2.9    5.5 / 3.3    6.2 / 5.7    8.6 / 8.7    24.8 / 26.9
-//   bf16 to 4 bits           7.1 / 4.3    7.6 / 4.8    7.9 / 5.3    8.4 / 9.4    10.5 / 14.2  28.0 / 50.1
-//   fp32                     8.2 / 3.9    8.4 / 4.3    8.5 / 5.8    10.7 / 11.2  16.3 / 19.2  42.0 / 58.1
-template <typename T, bool FP4>
-constexpr int kWholeTokens = FP4 || sizeof(T) == 4 ? 512 : 1024;
+template <bool Wide>
+constexpr int kQUnits = Wide ? 4 : 2;  // units a lane of a part of the queries
+// A token is dealt to as many warps as run at once in all (two CTAs an SM): one for K, V and
+// the queries, or one for K and V and the others for the queries, for the latency. More only
+// repeat the look-ups of the token's place.  Measured (us) in a graph, by the warps a token, 32
+// query and 8 K/V heads of 128:
+//   tokens                 256: 1     2     5      608: 1     2     3     4     5      1216: 1     2     3      2432: 1     2
+//   bf16                   5.5   4.5   3.4        6.2   4.8   4.0   4.1   5.6          8.1   7.0   7.5          13.4  15.4
+//   bf16 to 4 bits         8.0   5.7   5.8        8.8   6.2   6.5   6.6   9.7         10.4   7.5  10.8          15.1  16.5
+//   fp32                   8.0   6.2   5.6       11.4   8.5   8.1   7.4  10.5         16.0  12.5  16.5          22.2  22.4
+constexpr int kWarpsAtOnce = 152 * 2 * kWarps;
 template <typename T, bool FP4, bool Inter, bool Full>  // Full: the whole head is rotated
 __global__ void __launch_bounds__(kWarps * 32, 2)
 append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
-  constexpr int kAhead = kQUnits, kKAhead = sizeof(T) == 2 ? 2 : 1, kVAhead = sizeof(T) == 2 ? 4 : 1;  // units a lane at a time
+  // Units a lane at a time (interleaved ones are half as much; more in partly rotated rows spill: prompts
+  // into a bf16 cache 86 -> 93 us).
+  constexpr int kAhead = kQUnits<Inter && Full>, kKAhead = (sizeof(T) == 2 ? 2 : 1) * (Inter && Full ? 2 : 1);
+  constexpr int kVAhead = sizeof(T) == 2 ? 4 : 1, kMore = Full || sizeof(T) == 4 ? 1 : 2;
   const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   wait_for_previous();
@@ -279,12 +285,9 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     if (u.j >= rs.units) u.j -= rs.units, ++u.h;
     return u;
   };
-  const auto turns = [&](const Unit& u) { return Full || u.j < rs.turned; };
-  const auto column = [&](const Unit& u) { return turns(u) ? 8 * u.j : p.rot + 8 * (u.j - rs.turned); };
   const auto load = [&](const T* row, const Unit& u, Cols<T>& a, Cols<T>& b) {
-    const int d = column(u);
-    a.load(row + d);
-    if (!Inter && turns(u)) b.load(row + d + half);
+    a.load(row + 8 * u.j);
+    if (!Inter) b.load(row + 8 * u.j + half);
   };
   Unit first;
   first.h = rs.by_units(lane);
@@ -299,7 +302,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     int at_j = -1;
     float largest = 1.0f;  // of their magnitudes and 1 (4-bit)
     const auto angles = [&](const Unit& u) {
-      if (!turns(u) || at_j == u.j) return;
+      if (at_j == u.j) return;
       at_j = u.j;
       const float* from = cs + (Inter ? 4 : 8) * u.j;
 #pragma unroll
@@ -322,10 +325,9 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     };
     const auto minus = [](f32x2 x) { return x ^ 0x8000000080000000ull; };
     // The unit's columns (and those paired with them, y) rotated, as fp32 pairs: the plain products and sum.
-    const auto rotate = [&](const Unit& u, Cols<T>& a, Cols<T>& b, f32x2* x, f32x2* y) {
+    const auto rotate = [&](Cols<T>& a, Cols<T>& b, f32x2* x, f32x2* y) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = a.get(i);
-      if (!turns(u)) return;
       if (Inter) {  // pair i is (x0, x1) of x[i]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -344,8 +346,8 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         }
       }
     };
-    // Units i0 .. of the queries, kAhead a lane; found: the token's place is looked up.
-    const auto queries = [&](int i0, bool found) {
+    // Units i0 .. of the queries, kAhead a lane.
+    const auto queries = [&](int i0, auto find) {
       const int n = p.Hq * rs.units - i0;
       const T* row = (const T*)p.q + t * p.q_tok;
       T* to = (T*)p.q_out + t * p.qo_tok;
@@ -360,22 +362,19 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         }
         if (lane + 32 * k < n) load(row + (long long)u[k].h * q_head, u[k], a[k], b[k]);
       }
-      if (!found) {
-        const RowPlace pl = find_place(p.c, p.a, t);
-        if (!table_row(p, pl, t, &cs)) return;
-      }
+      if (!find()) return;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (lane + 32 * k < n) {
           f32x2 x[4], y[4];
           angles(u[k]);
-          rotate(u[k], a[k], b[k], x, y);
-          T* dst = to + (long long)u[k].h * qo_head + column(u[k]);
+          rotate(a[k], b[k], x, y);
+          T* dst = to + (long long)u[k].h * qo_head + 8 * u[k].j;
           Cols<T> g;
 #pragma unroll
           for (int i = 0; i < 4; ++i) g.set(i, x[i]);
           g.store(dst);
-          if (!Inter && turns(u[k])) {
+          if (!Inter) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) g.set(i, y[i]);
             g.store(dst + half);
@@ -383,17 +382,54 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         }
       }
     };
+    // Part i of n of the queries.  find: whether the token has a place, looked up behind the first loads.
+    // (What is not rotated stands already where q_out is q.)
+    const auto some_queries = [&](int i, int n, auto find) {
+#pragma unroll 1
+      for (int i0 = i * 32 * kAhead; i0 < p.Hq * rs.units; i0 += n * 32 * kAhead) queries(i0, find);
+      if constexpr (!Full) {
+        if (p.q == p.q_out) return;
+#pragma unroll 1
+        for (int i0 = i * 32 * kVAhead; i0 < p.Hq * rs.plain; i0 += n * 32 * kVAhead) {
+          Cols<T> g[kVAhead];
+          const auto at = [&](int k, int head) {
+            const int c = i0 + lane + 32 * k, h = rs.by_plain(c);
+            return (long long)h * head + p.rot + (c - h * rs.plain) * 8;
+          };
+#pragma unroll
+          for (int k = 0; k < kVAhead; ++k)
+            if (i0 + lane + 32 * k < p.Hq * rs.plain) g[k].load((const T*)p.q + t * p.q_tok + at(k, q_head));
+          if (!find()) return;
+#pragma unroll
+          for (int k = 0; k < kVAhead; ++k)
+            if (i0 + lane + 32 * k < p.Hq * rs.plain) g[k].store((T*)p.q_out + t * p.qo_tok + at(k, qo_head));
+        }
+      }
+    };
     if (part > 0) {
-      queries((part - 1) * 32 * kAhead, false);
+      int place = 0;  // 0 not looked up yet, 1, -1
+      some_queries(part - 1, rs.parts - 1, [&] {
+        if (place == 0) place = table_row(p, find_place(p.c, p.a, t), t, &cs) ? 1 : -1;
+        return place > 0;
+      });
       continue;
     }
     // -------------------------------------------- K and V
     const T* kn = (const T*)p.k_new + t * p.tok_stride;
     const T* vn = (const T*)p.v_new + t * p.tok_stride;
     const int n = p.c.heads * rs.units, chunks = D / 8, nv = p.c.heads * chunks;
-    const auto v_from = [&](int i) {
-      const int h = rs.by_chunks(i);
-      return vn + (long long)h * k_head + (i - h * chunks) * 8;
+    const int nc = Full ? nv : nv + p.c.heads * rs.plain;  // chunks of V, then those of K
+    struct Chunk {
+      int h, d;
+    };
+    const auto chunk = [&](int i) {
+      const bool v = Full || i < nv;
+      const int h = v ? rs.by_chunks(i) : rs.by_plain(i - nv);
+      return v ? Chunk{h, (i - h * chunks) * 8} : Chunk{h, p.rot + (i - nv - h * rs.plain) * 8};
+    };
+    const auto chunk_from = [&](int i) {
+      const Chunk c = chunk(i);
+      return (Full || i < nv ? vn : kn) + (long long)c.h * k_head + c.d;
     };
     Cols<T> ka[kKAhead], kb[kKAhead], va[kVAhead];
     Unit u = first;
@@ -404,45 +440,42 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     }
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k)
-      if (lane + 32 * k < nv) va[k].load(v_from(lane + 32 * k));
+      if (lane + 32 * k < nc) va[k].load(chunk_from(lane + 32 * k));
     const RowPlace pl = find_place(p.c, p.a, t);
     if (!table_row(p, pl, t, &cs)) continue;
     const CacheRow at = cache_row<FP4>(p.c, pl);
     // mask: the lanes that have one (both of a group, as their units are in range together).
     const auto put_k = [&](unsigned mask, const Unit& u, Cols<T>& a, Cols<T>& b) {
       angles(u);
-      const int d = column(u);
+      const int d = 8 * u.j;
       if constexpr (FP4) {
         uint8_t* base = (uint8_t*)p.c.k + (long long)u.h * c_head;
         uint8_t *codes = base + at.codes + d / 2, *scale = base + at.scales + d / 16;
-        const unsigned pairs = Inter ? 0u : __ballot_sync(mask, turns(u));
         float x[8], y[8];
-        const bool any_turn = __any_sync(mask, turns(u));
-        if (any_turn) {
+        {
           // In fp32, whose error is at most 3 2^-24 of the largest element times the largest of the
           // angles (which a table scaled for long contexts has above 1): mostly no code and no scale
           // hangs on it.
           f32x2 x2[4], y2[4];
-          rotate(u, a, b, x2, y2);
+          rotate(a, b, x2, y2);
           float top = 0.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float e0, e1;
             unpack2(a.get(i), e0, e1);
             top = fmaxf(top, fmaxf(fabsf(e0), fabsf(e1)));
-            if (!Inter && turns(u)) {
+            if (!Inter) {
               unpack2(b.get(i), e0, e1);
               top = fmaxf(top, fmaxf(fabsf(e0), fabsf(e1)));
+              unpack2(y2[i], y[2 * i], y[2 * i + 1]);
             }
             unpack2(x2[i], x[2 * i], x[2 * i + 1]);
-            unpack2(y2[i], y[2 * i], y[2 * i + 1]);
           }
           top *= largest * 2.4e-7f;
           top = fmaxf(top, __shfl_xor_sync(mask, top, 1));
           bool sure = store_fp4_if_sure(mask, x, top, p.k_factor, codes, scale);
-          if (!Inter && turns(u))
-            sure = store_fp4_if_sure(pairs, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;
-          if (__all_sync(mask, sure)) return;
+          if (!Inter) sure = store_fp4_if_sure(mask, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;
+          if (sure) return;  // (all lanes)
           // (Rows and angles again: kept, they would cost the common path their registers.)
           load(kn + (long long)u.h * k_head, u, a, b);
           at_j = -1;
@@ -451,7 +484,6 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           unpack2(a.get(i), x[2 * i], x[2 * i + 1]);
-          if (!turns(u)) continue;
           float ci[2], si[2];
           unpack2(c[(Inter ? i / 2 : i) % kAngles], ci[0], ci[1]);
           unpack2(s[(Inter ? i / 2 : i) % kAngles], si[0], si[1]);
@@ -471,32 +503,33 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
           }
         }
         store_fp4(mask, x, p.k_factor, codes, scale);
-        if (!Inter && turns(u)) store_fp4(pairs, y, p.k_factor, codes + half / 2, scale + half / 16);
+        if (!Inter) store_fp4(mask, y, p.k_factor, codes + half / 2, scale + half / 16);
       } else {
         f32x2 x[4], y[4];
-        rotate(u, a, b, x, y);
+        rotate(a, b, x, y);
         T* dst = (T*)p.c.k + at.at + (long long)u.h * c_head + d;
         Cols<T> g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) g.set(i, x[i]);
         g.store(dst);
-        if (!Inter && turns(u)) {
+        if (!Inter) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) g.set(i, y[i]);
           g.store(dst + half);
         }
       }
     };
-    const auto put_v = [&](unsigned mask, int i, Cols<T>& g) {
-      const int h = rs.by_chunks(i), j = i - h * chunks;
+    const auto put = [&](unsigned mask, int i, Cols<T>& g) {
+      const Chunk c = chunk(i);
+      void* pool = Full || i < nv ? p.c.v : p.c.k;
       if constexpr (FP4) {
-        uint8_t* base = (uint8_t*)p.c.v + (long long)h * c_head;
+        uint8_t* base = (uint8_t*)pool + (long long)c.h * c_head;
         float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) unpack2(g.get(e), x[2 * e], x[2 * e + 1]);
-        store_fp4(mask, x, p.v_factor, base + at.codes + j * 4, base + at.scales + j / 2);
+        store_fp4(mask, x, Full || i < nv ? p.v_factor : p.k_factor, base + at.codes + c.d / 2, base + at.scales + c.d / 16);
       } else {
-        g.store((T*)p.c.v + at.at + (long long)h * c_head + j * 8);
+        g.store((T*)pool + at.at + (long long)c.h * c_head + c.d);
       }
     };
     u = first;
@@ -517,21 +550,21 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     }
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k) {
-      const unsigned mask = __ballot_sync(0xffffffffu, lane + 32 * k < nv);
-      if (lane + 32 * k < nv) put_v(mask, lane + 32 * k, va[k]);
+      const unsigned mask = __ballot_sync(0xffffffffu, lane + 32 * k < nc);
+      if (lane + 32 * k < nc) put(mask, lane + 32 * k, va[k]);
     }
 #pragma unroll 1
-    for (int i0 = 32 * kVAhead; i0 < nv; i0 += 32) {
-      const unsigned mask = __ballot_sync(0xffffffffu, i0 + lane < nv);
-      if (i0 + lane < nv) {
-        va[0].load(v_from(i0 + lane));
-        put_v(mask, i0 + lane, va[0]);
+    for (int i0 = 32 * kVAhead; i0 < nc; i0 += 32 * kMore) {
+#pragma unroll
+      for (int k = 0; k < kMore; ++k)
+        if (i0 + lane + 32 * k < nc) va[k].load(chunk_from(i0 + lane + 32 * k));
+#pragma unroll
+      for (int k = 0; k < kMore; ++k) {
+        const unsigned mask = __ballot_sync(0xffffffffu, i0 + lane + 32 * k < nc);
+        if (i0 + lane + 32 * k < nc) put(mask, i0 + lane + 32 * k, va[k]);
       }
     }
-    if (rs.parts == 1) {
-#pragma unroll 1
-      for (int i0 = 0; i0 < p.Hq * rs.units; i0 += 32 * kAhead) queries(i0, true);
-    }
+    if (rs.parts == 1) some_queries(0, 1, [] { return true; });
   }
 }
 
@@ -571,13 +604,17 @@ __global__ void __launch_bounds__(kWarps * 32) read_fp4_kernel(const CacheReadAr
       for (int k = 0; k < kAhead; ++k) {
         const int i = i0 + 32 * k;
         if (i < 2 * n) {
-          // (code x scale is exact in 32 bits; the factor rounds once)
-          const float s = e4m3_to_float(sc[k]), f = i < n ? p.k_factor : p.v_factor;
+          // (code x scale is exact in fp16; the factor rounds once)
+          const uint32_t s = e4m3x2_to_half(sc[k] * 0x101u);
+          const float f = i < n ? p.k_factor : p.v_factor;
           uint32_t x[4];
           fp4x8_to_half(w[k], x);
           Cols<T> out;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) out.set(e, pack2(half_lo(x[e]) * s * f, half_hi(x[e]) * s * f));
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = hmul2(x[e], s);
+            out.set(e, mul2(pack2(half_lo(y), half_hi(y)), pack2(f, f)));
+          }
           out.store(i < n ? (T*)p.k_out + to + i * 8 : (T*)p.v_out + to + (i - n) * 8);
         }
       }
@@ -638,17 +675,19 @@ static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4, int par
 
 template <typename T, bool FP4>
 static cudaError_t launch_append(const RotaryAppendArgs& p, cudaStream_t s) {
-  const int turned = p.rot / (p.interleaved ? 8 : 16), units = turned + (p.c.head_dim - p.rot) / 8;
-  const int split = 1 + (p.Hq * units + 32 * kQUnits - 1) / (32 * kQUnits);
-  const int parts = p.a.n_tokens >= kWholeTokens<T, FP4> ? 1 : split;
+  const int units = p.rot / (p.interleaved ? 8 : 16), plain = (p.c.head_dim - p.rot) / 8, some = units > 0 ? units : 1;
+  const int step = 32 * (p.interleaved && plain == 0 ? kQUnits<true> : kQUnits<false>), work = units + plain / (p.interleaved ? 1 : 2);
+  const int split = 1 + (p.Hq * work + step - 1) / step;
+  const int at_once = kWarpsAtOnce / (p.a.n_tokens > 0 ? p.a.n_tokens : 1);
+  const int parts = at_once < 1 ? 1 : at_once < split ? at_once : split;
   const bool vec = whole_groups(p, sizeof(T), FP4, parts);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
       overlapped_launch(dim3(row_ctas(vec ? p.a.n_tokens * parts : p.a.n_tokens)), kWarps * 32, 0, s, &attr);
   if (!vec) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
-  const RowSteps rs{turned, units, 32 / units, 32 % units, parts, Divider((unsigned)units),
-                    Divider((unsigned)p.c.head_dim / 8), Divider((unsigned)parts)};
-  if (p.rot == p.c.head_dim)
+  const RowSteps rs{units, 32 / some, 32 % some, plain, parts, Divider((unsigned)some),
+                    Divider((unsigned)(plain > 0 ? plain : 1)), Divider((unsigned)p.c.head_dim / 8), Divider((unsigned)parts)};
+  if (plain == 0)
     return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true, true>, p, rs)
                          : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false, true>, p, rs);
   return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true, false>, p, rs)

@@ -155,6 +155,24 @@ def test_append_matches_the_definition(kind, n):
     assert torch.equal(i["k"], again["k"]) and torch.equal(i["v"], again["v"])
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp4 of bf16", "fp4 of f32"])
+@pytest.mark.parametrize("dim, inter", [(128, False), (128, True), (64, False), (64, True), (96, True), (0, False)])
+def test_from_few_tokens_to_more_than_run_at_once(kind, dim, inter):
+    # a token's rows are dealt to one warp or to several, by the tokens there are
+    dtype = F32 if kind.endswith("f32") else BF16
+    for chunks, Hq, Hkv in (([2, 9], 32, 8), ([300, 1, 130], 32, 2), ([700], 20, 3), ([1300, 5], 9, 8), ([900, 1800], 4, 9)):
+        i = make("fp4" if "fp4" in kind else "rows", dtype, chunks, [n + 30 for n in chunks], Hq, Hkv, 128, 16, seed=50,
+                 layout="htd", pad=2)
+        before = dict(k=i["k"].clone(), v=i["v"].clone())
+        tab = table_of(i["n"], dim) if dim else None
+        out = torch.full_like(i["q"], 7.0)
+        append(i, tab, q=i["q"], q_out=out, interleaved=inter)
+        assert (out[i["T"]:] == 7).all()
+        check(i, tab[i["pos"]] if dim else None, inter, before, out)
+        append(i, tab, q=i["q"], q_out=i["q"], interleaved=inter)
+        assert torch.equal(i["q"][:i["T"]], out[:i["T"]])
+
+
 def test_rows_of_other_sizes_and_strides():
     # bf16 and fp32 caches of heads that are no multiple of 16, rows on odd addresses
     for dtype in (F32, BF16):
