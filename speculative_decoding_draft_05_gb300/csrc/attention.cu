@@ -47,11 +47,11 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* row, int d, int D, 
                      d + 2 < D ? to_f32(row[d + 2]) : 0.0f, d + 3 < D ? to_f32(row[d + 3]) : 0.0f);
 }
 
-// Four elements of a 4-bit row (codes: their two bytes), times the scale and the factor.
-__device__ __forceinline__ float4 load4_fp4(const uint8_t* codes, const uint8_t* scale, float factor) {
+// Four elements of a 4-bit row (two bytes of codes), times their scale and the factor.
+__device__ __forceinline__ float4 values4_fp4(uint32_t codes, uint32_t scale, float factor) {
   uint32_t h[4];
-  fp4x8_to_half(*(const uint16_t*)codes, h);
-  const float s = e4m3_to_float(*scale) * factor;
+  fp4x8_to_half(codes, h);
+  const float s = e4m3_to_float(scale) * factor;
   return make_float4(half_lo(h[0]) * s, half_hi(h[0]) * s, half_lo(h[1]) * s, half_hi(h[1]) * s);
 }
 
@@ -173,8 +173,10 @@ __device__ __forceinline__ void copy16(float* dst, const float* src) {
 // a tile of K and V is on its way to shared memory while the one before is
 // worked on, and the pages of the one after are looked up.
 // FP4: codes become floats as they are put into shared memory, which then holds what it does for
-// an fp32 cache; for fp32 queries, whose precision the tensor cores do not have, and for wide heads
-// (4 requests of up to 5 tokens over 300 positions: 13.9 us in a graph, two kernels' latency).
+// an fp32 cache; for fp32 queries, whose precision the tensor cores do not have, and for wide heads.
+// Codes wait in registers while the tile before is worked on (loaded and converted at once:
+// decoding in fp32 of 16 requests of 2000 .. 3900 positions, 32 heads over 8, 172 us for 143; heads
+// of 256 882 us for 609).  4 requests of up to 5 tokens over 300 positions: 13.9 us, two kernels' latency.
 template <typename T, int NI, bool FP4>  // NI = ceil(D / 32), 2, 4 or 8
 __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
@@ -228,16 +230,6 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
             flag_status(&flags, DSPARK_DEV_BAD_INPUT);
             pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
           }
-          if constexpr (FP4) {
-            const int D = p.a.c.head_dim, slot = j - by_page(j) * S;
-            const long long at = pg * p.a.c.page_stride + w.h * p.a.c.head_stride;
-            const long long codes = at + fp4_codes_at(slot, D) + lc / 2, scale = at + fp4_scales_at(slot, D) + lc / 16;
-            const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const uint8_t *kb = (const uint8_t*)p.a.c.k, *vb = (const uint8_t*)p.a.c.v;
-            *(float4*)k = lc < D ? load4_fp4(kb + codes, kb + scale, 1.0f) : zero;
-            *(float4*)v = lc < D ? load4_fp4(vb + codes, vb + scale, p.a.v_factor) : zero;
-            continue;
-          }
           const long long at = pg * p.a.c.page_stride + (j - by_page(j) * S) * p.a.c.token_stride +
                                w.h * p.a.c.head_stride;
           if (std::is_same<T, float>::value && vec && lc < D) {
@@ -252,6 +244,36 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
         }
       }
     };
+    // FP4: tile t's codes and scales to registers, and as floats from there into its buffer.
+    uint32_t codes[FP4 ? NI : 1], scales[FP4 ? NI : 1];  // of K, and V's above
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        const int j = t * kTN + lr + u * kPass;
+        codes[u] = scales[u] = 0u;
+        if (t >= t1 || j >= w.end || lc >= D) continue;
+        int pg = page[u];
+        if (pg < 0 || pg >= p.a.c.n_pages) {
+          flag_status(&flags, DSPARK_DEV_BAD_INPUT);
+          pg = pg < 0 ? 0 : p.a.c.n_pages - 1;
+        }
+        const int slot = j - by_page(j) * S;
+        const long long at = pg * p.a.c.page_stride + w.h * p.a.c.head_stride;
+        const long long c = at + fp4_codes_at(slot, D) + lc / 2, s = at + fp4_scales_at(slot, D) + lc / 16;
+        const uint8_t *kb = (const uint8_t*)p.a.c.k, *vb = (const uint8_t*)p.a.c.v;
+        codes[u] = *(const uint16_t*)(kb + c) | (uint32_t)*(const uint16_t*)(vb + c) << 16;
+        scales[u] = kb[s] | (uint32_t)vb[s] << 8;
+      }
+    };
+    auto put = [&](int t) {
+      float* sk = skv + (t & 1) * 2 * kTN * ld + lr * ld + lc;
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        float* k = sk + u * kPass * ld;
+        *(float4*)k = values4_fp4(codes[u] & 0xffffu, scales[u], 1.0f);
+        *(float4*)(k + kTN * ld) = values4_fp4(codes[u] >> 16, scales[u] >> 8, p.a.v_factor);
+      }
+    };
     __syncthreads();  // (the item before is done with both buffers and bad_from)
     if (threadIdx.x == 0) {
       const int a = w.q.L - w.q.n + row0 / G + 1;
@@ -260,7 +282,10 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
       bad_from = 0x7fffffff;
     }
     look_up(w.first_tile());
-    load(w.first_tile());
+    if constexpr (FP4)
+      fetch(w.first_tile());
+    else
+      load(w.first_tile());
     look_up(w.first_tile() + 1);
     for (int i = threadIdx.x; i < kMR * NI * 32; i += kThreads) {
       const int a = i / (NI * 32), d = i - a * (NI * 32);
@@ -282,9 +307,16 @@ attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec)
       for (int k = 0; k < NI / 2; ++k) r.o[i][k] = 0ull;
     }
     for (int t = w.first_tile(); t < t1; ++t) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncthreads();
-      load(t + 1);  // (all are past tile t - 1, which was in its buffer)
+      // (all are past tile t - 1 behind the barrier, which was in the buffer of t + 1)
+      if constexpr (FP4) {
+        put(t);
+        __syncthreads();
+        fetch(t + 1);
+      } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        load(t + 1);
+      }
       look_up(t + 2);
       if (t >= t_hidden) {
         hide_bad_v<NI>(skv + ((t & 1) * 2 + 1) * kTN * ld, t * kTN, max(all_see - t * kTN, 0),
