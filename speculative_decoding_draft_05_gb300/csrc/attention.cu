@@ -49,8 +49,8 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* row, int d, int D, 
 
 // Four elements of a 4-bit row (two bytes of codes), times their scale and the factor.
 __device__ __forceinline__ float4 values4_fp4(uint32_t codes, uint32_t scale, float factor) {
-  uint32_t h[4];
-  fp4x8_to_half(codes, h);
+  uint32_t h[2];
+  fp4x4_to_half(codes, h);
   const float s = e4m3_to_float(scale) * factor;
   return make_float4(half_lo(h[0]) * s, half_hi(h[0]) * s, half_lo(h[1]) * s, half_hi(h[1]) * s);
 }
@@ -173,10 +173,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src) {
 // a tile of K and V is on its way to shared memory while the one before is
 // worked on, and the pages of the one after are looked up.
 // FP4: codes become floats as they are put into shared memory, which then holds what it does for
-// an fp32 cache; for fp32 queries, whose precision the tensor cores do not have, and for wide heads.
-// Codes wait in registers while the tile before is worked on (loaded and converted at once:
-// decoding in fp32 of 16 requests of 2000 .. 3900 positions, 32 heads over 8, 172 us for 143; heads
-// of 256 882 us for 609).  4 requests of up to 5 tokens over 300 positions: 13.9 us, two kernels' latency.
+// an fp32 cache; for many rows of fp32 queries, whose precision the tensor cores do not have, or of wide heads.
+// Codes wait in registers while the tile before is worked on (loaded and converted at once, chunks
+// of up to 17 tokens, four heads of 256, of 16 requests of 2000 .. 3900 positions: 1552 us for 1271).
 template <typename T, int NI, bool FP4>  // NI = ceil(D / 32), 2, 4 or 8
 __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_simt_kernel(const AttnParams p, const Divider by_page, const bool vec) {
@@ -521,7 +520,11 @@ size_t attention_workspace_bytes(int dtype, int head_dim) {
 }
 
 size_t attention_fp4_workspace_bytes(int dtype, int head_dim) {
-  if (dtype != DSPARK_BF16 || head_dim > 128) return attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
+  if (dtype != DSPARK_BF16 || head_dim > 128) {
+    const size_t few = attention_fp4_simt_workspace_bytes(head_dim);
+    const size_t many = attn_workspace_layout(kMR, head_dim, kSimtCtas).total;
+    return few > many ? few : many;
+  }
   const size_t rows = attention_fp4_rows_workspace_bytes(head_dim), tc = attention_tc_workspace_bytes(head_dim);
   return tc > rows ? tc : rows;
 }
@@ -529,6 +532,7 @@ size_t attention_fp4_workspace_bytes(int dtype, int head_dim) {
 cudaError_t launch_paged_attention(const AttnArgs& a, char* ws, cudaStream_t s) {
   if (a.fp4 && attention_fp4_few_rows(a)) return launch_attention_fp4_rows(a, ws, s);
   if (attention_tc_fp4_supported(a)) return launch_attention_tc_fp4(a, ws, s);
+  if (attention_fp4_simt_few_rows(a)) return launch_attention_fp4_simt(a, ws, s);
   if (!a.fp4 && attention_tc_supported(a)) return launch_attention_tc(a, ws, s);
   const AttnWorkspace w = attn_workspace_layout(kMR, a.c.head_dim, kSimtCtas);
   AttnParams p{a, (int*)ws, (int*)(ws + w.flags), (CutItem*)(ws + w.cuts),

@@ -327,9 +327,13 @@ cudaError_t launch_attention_tc(const AttnArgs& a, char* ws, cudaStream_t s);
 bool attention_tc_fp4_supported(const AttnArgs& a);
 cudaError_t launch_attention_tc_fp4(const AttnArgs& a, char* ws, cudaStream_t s);
 
-// Few rows over a 4-bit cache (attention_fp4.cu).
+// Few rows over a 4-bit cache (attention_fp4.cu; in fp32, or wide heads: attention_fp4_simt.cu).
+long long attention_fp4_rows(const AttnArgs& a);
 bool attention_fp4_few_rows(const AttnArgs& a);
 size_t attention_fp4_rows_workspace_bytes(int head_dim);
 cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s);
+bool attention_fp4_simt_few_rows(const AttnArgs& a);
+size_t attention_fp4_simt_workspace_bytes(int head_dim);
+cudaError_t launch_attention_fp4_simt(const AttnArgs& a, char* ws, cudaStream_t s);
 
 }  // namespace dspark

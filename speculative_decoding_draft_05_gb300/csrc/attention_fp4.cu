@@ -548,20 +548,20 @@ cudaError_t launch(Fp4Params fp, char* ws, cudaStream_t s) {
   return e != cudaSuccess ? e : launch_attn_combine(p, kMaxRows, Sh::kCtas, s);
 }
 
+template <int D>
+cudaError_t launch_rows(const Fp4Params& fp, char* ws, cudaStream_t s) {
+  return attention_fp4_rows(fp.p.a) <= 8 ? launch<D, 1>(fp, ws, s) : launch<D, 2>(fp, ws, s);
+}
+
+}  // namespace
+
 // Rows of most requests, as far as the host can tell: where there are no more tokens than
 // requests, a token's; else the mean and a third.
-long long fp4_rows(const AttnArgs& a) {
+long long attention_fp4_rows(const AttnArgs& a) {
   if (a.a.n_tokens <= a.a.R) return a.G;
   const long long all = (long long)a.a.n_tokens * a.G;
   return (all + all / 3 + a.a.R - 1) / a.a.R;
 }
-
-template <int D>
-cudaError_t launch_rows(const Fp4Params& fp, char* ws, cudaStream_t s) {
-  return fp4_rows(fp.p.a) <= 8 ? launch<D, 1>(fp, ws, s) : launch<D, 2>(fp, ws, s);
-}
-
-}  // namespace
 
 size_t attention_fp4_rows_workspace_bytes(int head_dim) {
   return attn_workspace_layout(kMaxRows, head_dim, kAttnMaxCtas).total;
@@ -573,7 +573,7 @@ size_t attention_fp4_rows_workspace_bytes(int head_dim) {
 //   8 rows  57 / 95   47 / 85      16  82 / 95   68 / 88
 //   12      80 / 95   64 / 89      20  156 / 95  125 / 88
 bool attention_fp4_few_rows(const AttnArgs& a) {
-  return a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0 && fp4_rows(a) <= kMaxRows;
+  return a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0 && attention_fp4_rows(a) <= kMaxRows;
 }
 
 cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s) {

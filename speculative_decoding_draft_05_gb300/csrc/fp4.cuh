@@ -41,6 +41,15 @@ __device__ __forceinline__ void fp4x8_to_half(uint32_t w, uint32_t* h) {
       : "r"(w));
 }
 
+__device__ __forceinline__ void fp4x4_to_half(uint32_t w, uint32_t* h) {  // the low four codes
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+      : "=r"(h[0]), "=r"(h[1])
+      : "r"(w));
+}
+
 // Two e4m3 scales (the low 16 bits of s) as a pair of fp16.
 __device__ __forceinline__ uint32_t e4m3x2_to_half(uint32_t s) {
   uint32_t h;

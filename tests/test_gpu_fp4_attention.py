@@ -83,6 +83,15 @@ def test_query_heads_of_a_head(G):
         check(i, attend(i))
 
 
+@pytest.mark.parametrize("D, dtype", [(32, F32), (64, F32), (96, F32), (128, F32), (160, F32), (256, F32), (192, BF16),
+                                      (256, BF16)])
+def test_query_heads_of_a_head_in_fp32_and_of_wide_heads(D, dtype):
+    for G in (1, 2, 4, 5, 8, 9, 16, 33, 65):
+        for chunks in ([1, 1, 1, 1], [1, 2, 5, 9]):
+            i = make(dtype, chunks, [140, 2, 30, 260], 2 * G, 2, D, 16, seed=62)
+            check(i, attend(i))
+
+
 @pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
 def test_head_dims(D):
     for dtype in (F32, BF16):
