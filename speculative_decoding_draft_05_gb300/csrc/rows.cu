@@ -178,10 +178,11 @@ __device__ __forceinline__ bool table_row(const RotaryAppendArgs& p, const RowPl
   return true;
 }
 
-// Any sizes, strides, alignments and pairs: a row passes through shared memory
-// and is then taken element by element, the head dimension over the lanes.
+// Any sizes, strides, alignments and pairs: a warp has some heads of a token's K and V, or of its
+// queries; a row passes through shared memory and is then taken element by element, the
+// head dimension over the lanes.  (A token always a warp: 64 tokens of 48 rows of 96 36 us for 4.7.)
 template <typename T, bool FP4>
-__global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const RotaryAppendArgs p) {
+__global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const RotaryAppendArgs p, int parts) {
   __shared__ float rows[kWarps][256];
   const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
   float* row = rows[threadIdx.x >> 5];
@@ -191,7 +192,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const Ro
     rotary_status(p);
     return;
   }
-  for (int t = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); t < p.a.n_tokens; t += (gridDim.x - 1) * kWarps) {
+  const int heads = p.c.heads + p.Hq;
+  const long long jobs = (long long)p.a.n_tokens * parts;  // of every so many heads
+  for (long long job = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); job < jobs; job += (gridDim.x - 1) * kWarps) {
+    const int t = (int)(job / parts), part = (int)(job - (long long)t * parts);
     const RowPlace pl = find_place(p.c, p.a, t);
     const float* cs = nullptr;
     if (!table_row(p, pl, t, &cs)) continue;
@@ -224,31 +228,34 @@ __global__ void __launch_bounds__(kWarps * 32) append_rotary_any_kernel(const Ro
         if (d < D) ((T*)base)[at.at + h * p.c.head_stride + d] = to_type<T>(y);
       }
     };
-    for (int h = 0; h < p.c.heads; ++h) {
-      load((const T*)p.k_new + t * p.tok_stride + h * p.head_stride);
-      for (int d = lane; d - lane < D; d += 32)
-        put(p.c.k, h, d, d < D ? value(d, std::integral_constant<bool, FP4>{}) : 0.0f, p.k_factor);
-      const T* vn = (const T*)p.v_new + t * p.tok_stride + h * p.head_stride;
-      for (int d = lane; d - lane < D; d += 32) put(p.c.v, h, d, d < D ? to_f32(vn[d]) : 0.0f, p.v_factor);
-    }
-    for (int h = 0; h < p.Hq; ++h) {
-      load((const T*)p.q + t * p.q_tok + h * p.q_head);
-      for (int d = lane; d < D; d += 32)
-        ((T*)p.q_out)[t * p.qo_tok + h * p.qo_head + d] = to_type<T>(value(d, std::false_type{}));
+    for (int h = part; h < heads; h += parts) {
+      if (h < p.c.heads) {
+        load((const T*)p.k_new + t * p.tok_stride + h * p.head_stride);
+        for (int d = lane; d - lane < D; d += 32)
+          put(p.c.k, h, d, d < D ? value(d, std::integral_constant<bool, FP4>{}) : 0.0f, p.k_factor);
+        const T* vn = (const T*)p.v_new + t * p.tok_stride + h * p.head_stride;
+        for (int d = lane; d - lane < D; d += 32) put(p.c.v, h, d, d < D ? to_f32(vn[d]) : 0.0f, p.v_factor);
+      } else {
+        const int q = h - p.c.heads;
+        load((const T*)p.q + t * p.q_tok + q * p.q_head);
+        for (int d = lane; d < D; d += 32)
+          ((T*)p.q_out)[t * p.qo_tok + q * p.qo_head + d] = to_type<T>(value(d, std::false_type{}));
+      }
     }
   }
 }
 
-// Rows of whole groups of 16 on 16-byte boundaries, pairs whose groups are whole too:
+// Rows of whole groups of 16 on 16-byte boundaries, pairs of whole eights:
 // a lane takes units of eight rotated columns and the eight that they are paired with (or,
 // interleaved, eight alone), so that rotation crosses no lanes, and chunks of eight of what is
 // not rotated; two neighbours have a 4-bit group.  A warp has a token's K and V, or a part
 // of its queries; its rows are on their way before the token's place is looked up.
 struct RowSteps {
   int units, step_h, step_j;  // rotated units of a row; 32 of them are step_h rows and step_j units
+  int q_units, q_step_h, q_step_j;  // of Q
   int plain;                  // chunks of a row of K or Q that are not rotated
   int parts;                  // warps a token
-  Divider by_units, by_plain, by_chunks, by_parts;
+  Divider by_units, by_q_units, by_plain, by_chunks, by_parts;
 };
 template <bool Wide>
 constexpr int kQUnits = Wide ? 4 : 2;  // units a lane of a part of the queries
@@ -261,9 +268,17 @@ constexpr int kQUnits = Wide ? 4 : 2;  // units a lane of a part of the queries
 //   bf16 to 4 bits         8.0   5.7   5.8        8.8   6.2   6.5   6.6   9.7         10.4   7.5  10.8          15.1  16.5
 //   fp32                   8.0   6.2   5.6       11.4   8.5   8.1   7.4  10.5         16.0  12.5  16.5          22.2  22.4
 constexpr int kWarpsAtOnce = 152 * 2 * kWarps;
-template <typename T, bool FP4, bool Inter, bool Full>  // Full: the whole head is rotated
+enum Pairs {
+  kHalves,      // (i, i + rot / 2): a unit is eight columns and those they are paired with
+  kNeighbours,  // (2 i, 2 i + 1): eight columns
+  kHalf,        // as kHalves, but a unit of K is eight columns, and the others are looked at: for 4-bit groups
+                // of both halves, where rot / 2 is no multiple of 16.  (Not of Q, which may be rotated in place.)
+};
+template <typename T, bool FP4, Pairs P, bool Full>  // Full: the whole head is rotated
 __global__ void __launch_bounds__(kWarps * 32, 2)
 append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
+  constexpr bool Inter = P == kNeighbours;
+  constexpr Pairs kOfQ = P == kHalf ? kHalves : P;
   // Units a lane at a time (interleaved ones are half as much; more in partly rotated rows spill: prompts
   // into a bf16 cache 86 -> 93 us).
   constexpr int kAhead = kQUnits<Inter && Full>, kKAhead = (sizeof(T) == 2 ? 2 : 1) * (Inter && Full ? 2 : 1);
@@ -280,14 +295,15 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
   struct Unit {
     int h, j;
   };
-  const auto next = [&](Unit u) {  // 32 units on
-    u.h += rs.step_h, u.j += rs.step_j;
-    if (u.j >= rs.units) u.j -= rs.units, ++u.h;
+  const auto next = [&](Unit u, int units, int step_h, int step_j) {  // 32 units on
+    u.h += step_h, u.j += step_j;
+    if (u.j >= units) u.j -= units, ++u.h;
     return u;
   };
-  const auto load = [&](const T* row, const Unit& u, Cols<T>& a, Cols<T>& b) {
+  const auto load = [&](const T* row, const Unit& u, Cols<T>& a, Cols<T>& b, auto pairs) {
     a.load(row + 8 * u.j);
-    if (!Inter) b.load(row + 8 * u.j + half);
+    if (pairs == kHalves) b.load(row + 8 * u.j + half);
+    if (pairs == kHalf) b.load(row + 8 * u.j + (8 * u.j < half ? half : -half));
   };
   Unit first;
   first.h = rs.by_units(lane);
@@ -301,15 +317,18 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     f32x2 c[kAngles], s[kAngles];
     int at_j = -1;
     float largest = 1.0f;  // of their magnitudes and 1 (4-bit)
-    const auto angles = [&](const Unit& u) {
+    const auto minus = [](f32x2 x) { return x ^ 0x8000000080000000ull; };
+    const auto angles = [&](const Unit& u, auto pairs) {
       if (at_j == u.j) return;
       at_j = u.j;
-      const float* from = cs + (Inter ? 4 : 8) * u.j;
+      const bool second = pairs == kHalf && 8 * u.j >= half;
+      const float* from = cs + (Inter ? 4 : 8) * u.j - (second ? half : 0);
 #pragma unroll
       for (int i = 0; i < kAngles; i += 2) {
         const float4 x = *(const float4*)(from + 2 * i), y = *(const float4*)(from + half + 2 * i);
         c[i] = pack2(x.x, x.y), c[i + 1] = pack2(x.z, x.w);
         s[i] = pack2(y.x, y.y), s[i + 1] = pack2(y.z, y.w);
+        if (pairs == kHalf && !second) s[i] = minus(s[i]), s[i + 1] = minus(s[i + 1]);
       }
       if constexpr (FP4) {
         largest = 1.0f;
@@ -323,9 +342,8 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         }
       }
     };
-    const auto minus = [](f32x2 x) { return x ^ 0x8000000080000000ull; };
     // The unit's columns (and those paired with them, y) rotated, as fp32 pairs: the plain products and sum.
-    const auto rotate = [&](Cols<T>& a, Cols<T>& b, f32x2* x, f32x2* y) {
+    const auto rotate = [&](Cols<T>& a, Cols<T>& b, f32x2* x, f32x2* y, auto pairs) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = a.get(i);
       if (Inter) {  // pair i is (x0, x1) of x[i]
@@ -340,15 +358,16 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x2 e = x[i], o = b.get(i);
-          x[i] = fma2(e, c[i % kAngles], mul2(o, minus(s[i % kAngles])));
-          y[i] = fma2(o, c[i % kAngles], mul2(e, s[i % kAngles]));
+          const f32x2 e = x[i], o = b.get(i), si = s[i % kAngles];
+          x[i] = fma2(e, c[i % kAngles], mul2(o, pairs == kHalf ? si : minus(si)));
+          if (pairs == kHalves) y[i] = fma2(o, c[i % kAngles], mul2(e, si));
         }
       }
     };
     // Units i0 .. of the queries, kAhead a lane.
+    const std::integral_constant<Pairs, kOfQ> of_q;
     const auto queries = [&](int i0, auto find) {
-      const int n = p.Hq * rs.units - i0;
+      const int n = p.Hq * rs.q_units - i0;
       const T* row = (const T*)p.q + t * p.q_tok;
       T* to = (T*)p.q_out + t * p.qo_tok;
       Unit u[kAhead];
@@ -356,25 +375,25 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (k > 0) {
-          u[k] = next(u[k - 1]);
+          u[k] = next(u[k - 1], rs.q_units, rs.q_step_h, rs.q_step_j);
         } else {
-          u[0].h = rs.by_units(i0 + lane), u[0].j = i0 + lane - u[0].h * rs.units;
+          u[0].h = rs.by_q_units(i0 + lane), u[0].j = i0 + lane - u[0].h * rs.q_units;
         }
-        if (lane + 32 * k < n) load(row + (long long)u[k].h * q_head, u[k], a[k], b[k]);
+        if (lane + 32 * k < n) load(row + (long long)u[k].h * q_head, u[k], a[k], b[k], of_q);
       }
       if (!find()) return;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (lane + 32 * k < n) {
           f32x2 x[4], y[4];
-          angles(u[k]);
-          rotate(a[k], b[k], x, y);
+          angles(u[k], of_q);
+          rotate(a[k], b[k], x, y, of_q);
           T* dst = to + (long long)u[k].h * qo_head + 8 * u[k].j;
           Cols<T> g;
 #pragma unroll
           for (int i = 0; i < 4; ++i) g.set(i, x[i]);
           g.store(dst);
-          if (!Inter) {
+          if (kOfQ == kHalves) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) g.set(i, y[i]);
             g.store(dst + half);
@@ -386,7 +405,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     // (What is not rotated stands already where q_out is q.)
     const auto some_queries = [&](int i, int n, auto find) {
 #pragma unroll 1
-      for (int i0 = i * 32 * kAhead; i0 < p.Hq * rs.units; i0 += n * 32 * kAhead) queries(i0, find);
+      for (int i0 = i * 32 * kAhead; i0 < p.Hq * rs.q_units; i0 += n * 32 * kAhead) queries(i0, find);
       if constexpr (!Full) {
         if (p.q == p.q_out) return;
 #pragma unroll 1
@@ -415,6 +434,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
       continue;
     }
     // -------------------------------------------- K and V
+    const std::integral_constant<Pairs, P> of_k;
     const T* kn = (const T*)p.k_new + t * p.tok_stride;
     const T* vn = (const T*)p.v_new + t * p.tok_stride;
     const int n = p.c.heads * rs.units, chunks = D / 8, nv = p.c.heads * chunks;
@@ -435,8 +455,8 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     Unit u = first;
 #pragma unroll
     for (int k = 0; k < kKAhead; ++k) {
-      if (lane + 32 * k < n) load(kn + (long long)u.h * k_head, u, ka[k], kb[k]);
-      u = next(u);
+      if (lane + 32 * k < n) load(kn + (long long)u.h * k_head, u, ka[k], kb[k], of_k);
+      u = next(u, rs.units, rs.step_h, rs.step_j);
     }
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k)
@@ -446,7 +466,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     const CacheRow at = cache_row<FP4>(p.c, pl);
     // mask: the lanes that have one (both of a group, as their units are in range together).
     const auto put_k = [&](unsigned mask, const Unit& u, Cols<T>& a, Cols<T>& b) {
-      angles(u);
+      angles(u, of_k);
       const int d = 8 * u.j;
       if constexpr (FP4) {
         uint8_t* base = (uint8_t*)p.c.k + (long long)u.h * c_head;
@@ -457,7 +477,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
           // angles (which a table scaled for long contexts has above 1): mostly no code and no scale
           // hangs on it.
           f32x2 x2[4], y2[4];
-          rotate(a, b, x2, y2);
+          rotate(a, b, x2, y2, of_k);
           float top = 0.0f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -467,19 +487,19 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
             if (!Inter) {
               unpack2(b.get(i), e0, e1);
               top = fmaxf(top, fmaxf(fabsf(e0), fabsf(e1)));
-              unpack2(y2[i], y[2 * i], y[2 * i + 1]);
+              if (P == kHalves) unpack2(y2[i], y[2 * i], y[2 * i + 1]);
             }
             unpack2(x2[i], x[2 * i], x[2 * i + 1]);
           }
           top *= largest * 2.4e-7f;
           top = fmaxf(top, __shfl_xor_sync(mask, top, 1));
           bool sure = store_fp4_if_sure(mask, x, top, p.k_factor, codes, scale);
-          if (!Inter) sure = store_fp4_if_sure(mask, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;
+          if (P == kHalves) sure = store_fp4_if_sure(mask, y, top, p.k_factor, codes + half / 2, scale + half / 16) && sure;
           if (sure) return;  // (all lanes)
           // (Rows and angles again: kept, they would cost the common path their registers.)
-          load(kn + (long long)u.h * k_head, u, a, b);
+          load(kn + (long long)u.h * k_head, u, a, b, of_k);
           at_j = -1;
-          angles(u);
+          angles(u, of_k);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -497,22 +517,22 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const float e = x[2 * i + k];
-              x[2 * i + k] = rotated_odd(e, ci[k], o[k], -si[k]);
-              y[2 * i + k] = rotated_odd(o[k], ci[k], e, si[k]);
+              x[2 * i + k] = rotated_odd(e, ci[k], o[k], P == kHalf ? si[k] : -si[k]);
+              if (P == kHalves) y[2 * i + k] = rotated_odd(o[k], ci[k], e, si[k]);
             }
           }
         }
         store_fp4(mask, x, p.k_factor, codes, scale);
-        if (!Inter) store_fp4(mask, y, p.k_factor, codes + half / 2, scale + half / 16);
+        if (P == kHalves) store_fp4(mask, y, p.k_factor, codes + half / 2, scale + half / 16);
       } else {
         f32x2 x[4], y[4];
-        rotate(a, b, x, y);
+        rotate(a, b, x, y, of_k);
         T* dst = (T*)p.c.k + at.at + (long long)u.h * c_head + d;
         Cols<T> g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) g.set(i, x[i]);
         g.store(dst);
-        if (!Inter) {
+        if (P == kHalves) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) g.set(i, y[i]);
           g.store(dst + half);
@@ -537,16 +557,16 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
     for (int k = 0; k < kKAhead; ++k) {
       const unsigned mask = __ballot_sync(0xffffffffu, lane + 32 * k < n);
       if (lane + 32 * k < n) put_k(mask, u, ka[k], kb[k]);
-      u = next(u);
+      u = next(u, rs.units, rs.step_h, rs.step_j);
     }
 #pragma unroll 1
     for (int i0 = 32 * kKAhead; i0 < n; i0 += 32) {
       const unsigned mask = __ballot_sync(0xffffffffu, i0 + lane < n);
       if (i0 + lane < n) {
-        load(kn + (long long)u.h * k_head, u, ka[0], kb[0]);
+        load(kn + (long long)u.h * k_head, u, ka[0], kb[0], of_k);
         put_k(mask, u, ka[0], kb[0]);
       }
-      u = next(u);
+      u = next(u, rs.units, rs.step_h, rs.step_j);
     }
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k) {
@@ -564,6 +584,7 @@ append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
         if (i0 + lane + 32 * k < nc) put(mask, i0 + lane + 32 * k, va[k]);
       }
     }
+    if (P == kHalf) at_j = -1;  // (a unit is another one now)
     if (rs.parts == 1) some_queries(0, 1, [] { return true; });
   }
 }
@@ -651,14 +672,14 @@ __global__ void __launch_bounds__(kWarps * 32) read_rows_kernel(const CacheReadA
   }
 }
 
-int row_ctas(int n_tokens) {  // (the first one for the status word: also without tokens)
-  const int ctas = (n_tokens + kWarps - 1) / kWarps;
-  return (ctas < 1215 ? ctas : 1215) + 1;
+int row_ctas(long long jobs) {  // a warp each (the first CTA for the status word: also without any)
+  const long long ctas = (jobs + kWarps - 1) / kWarps;
+  return (int)(ctas < 1215 ? ctas : 1215) + 1;
 }
 
 }  // namespace
 
-// Whether rows are whole groups on 16-byte boundaries, pairs lie in whole groups, and
+// Whether rows are whole groups on 16-byte boundaries, pairs lie in whole eights, and
 // strides and the number of jobs fit 32 bits.
 static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4, int parts) {
   const CacheView& c = p.c;
@@ -668,30 +689,37 @@ static bool whole_groups(const RotaryAppendArgs& p, int esize, bool fp4, int par
   if (p.Hq > 0) at |= (uintptr_t)p.q | (uintptr_t)p.q_out, strides |= p.q_tok | p.q_head | p.qo_tok | p.qo_head;
   if (!fp4) at |= (uintptr_t)c.k | (uintptr_t)c.v, strides |= c.page_stride | c.token_stride | c.head_stride;
   const long long most = 0x7fffffff;
-  return c.head_dim % 16 == 0 && p.rot % (p.interleaved ? 16 : 32) == 0 && strides % ve == 0 && (at & 15u) == 0 &&
+  return c.head_dim % 16 == 0 && p.rot % 16 == 0 && strides % ve == 0 && (at & 15u) == 0 &&
          p.head_stride <= most && p.q_head <= most && p.qo_head <= most && c.head_stride <= most &&
          (long long)p.a.n_tokens * parts < 0x40000000;
 }
 
 template <typename T, bool FP4>
 static cudaError_t launch_append(const RotaryAppendArgs& p, cudaStream_t s) {
-  const int units = p.rot / (p.interleaved ? 8 : 16), plain = (p.c.head_dim - p.rot) / 8, some = units > 0 ? units : 1;
-  const int step = 32 * (p.interleaved && plain == 0 ? kQUnits<true> : kQUnits<false>), work = units + plain / (p.interleaved ? 1 : 2);
-  const int split = 1 + (p.Hq * work + step - 1) / step;
+  const Pairs pairs = p.interleaved ? kNeighbours : FP4 && p.rot % 32 != 0 ? kHalf : kHalves;
+  const int units = p.rot / (pairs == kHalves ? 16 : 8), plain = (p.c.head_dim - p.rot) / 8, some = units > 0 ? units : 1;
+  const int step = 32 * (p.interleaved && plain == 0 ? kQUnits<true> : kQUnits<false>);
+  const int q_units = p.rot / (p.interleaved ? 8 : 16), q_some = q_units > 0 ? q_units : 1;
+  const int split = 1 + (p.Hq * (q_units + plain / (p.interleaved ? 1 : 2)) + step - 1) / step;
   const int at_once = kWarpsAtOnce / (p.a.n_tokens > 0 ? p.a.n_tokens : 1);
-  const int parts = at_once < 1 ? 1 : at_once < split ? at_once : split;
-  const bool vec = whole_groups(p, sizeof(T), FP4, parts);
+  const auto warps = [&](int most) { return at_once < 1 ? 1 : at_once < most ? at_once : most; };  // a token
+  const bool vec = whole_groups(p, sizeof(T), FP4, warps(split));
+  const int parts = warps(vec ? split : p.c.heads + p.Hq);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
-      overlapped_launch(dim3(row_ctas(vec ? p.a.n_tokens * parts : p.a.n_tokens)), kWarps * 32, 0, s, &attr);
-  if (!vec) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p);
-  const RowSteps rs{units, 32 / some, 32 % some, plain, parts, Divider((unsigned)some),
-                    Divider((unsigned)(plain > 0 ? plain : 1)), Divider((unsigned)p.c.head_dim / 8), Divider((unsigned)parts)};
+      overlapped_launch(dim3(row_ctas((long long)p.a.n_tokens * parts)), kWarps * 32, 0, s, &attr);
+  if (!vec) return cudaLaunchKernelEx(&cfg, append_rotary_any_kernel<T, FP4>, p, parts);
+  const RowSteps rs{units, 32 / some, 32 % some, q_units, 32 / q_some, 32 % q_some, plain, parts,
+                    Divider((unsigned)some), Divider((unsigned)q_some), Divider((unsigned)(plain > 0 ? plain : 1)), Divider((unsigned)p.c.head_dim / 8),
+                    Divider((unsigned)parts)};
+  if constexpr (FP4) {  // (a whole head is a multiple of 32 there)
+    if (pairs == kHalf) return cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, kHalf, false>, p, rs);
+  }
   if (plain == 0)
-    return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true, true>, p, rs)
-                         : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false, true>, p, rs);
-  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, true, false>, p, rs)
-                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, false, false>, p, rs);
+    return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, kNeighbours, true>, p, rs)
+                         : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, kHalves, true>, p, rs);
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, kNeighbours, false>, p, rs)
+                       : cudaLaunchKernelEx(&cfg, append_rotary_kernel<T, FP4, kHalves, false>, p, rs);
 }
 
 cudaError_t launch_append_rotary(const RotaryAppendArgs& p, int dtype, bool fp4, cudaStream_t s) {

@@ -156,7 +156,8 @@ def test_append_matches_the_definition(kind, n):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "fp4 of bf16", "fp4 of f32"])
-@pytest.mark.parametrize("dim, inter", [(128, False), (128, True), (64, False), (64, True), (96, True), (0, False)])
+@pytest.mark.parametrize("dim, inter", [(128, False), (128, True), (64, False), (64, True), (96, True), (0, False), (48, False), (112, False),
+                                        (12, False), (6, True)])
 def test_from_few_tokens_to_more_than_run_at_once(kind, dim, inter):
     # a token's rows are dealt to one warp or to several, by the tokens there are
     dtype = F32 if kind.endswith("f32") else BF16
