@@ -12,8 +12,9 @@
 // As in the kernel for bf16 (attention_fp4.cu), a CTA walks its share in tiles of 128 keys, a warp brings its own
 // blocks by asynchronous copies into a ring of its own, and a piece's eight partial results meet in shared memory.
 //
-// What bounds it: the issue of instructions (55 % of the slots) and shared memory (43 %).  Decoding in fp32, 16
-// requests of 2000 .. 3900 positions, 32 query heads over 8 of 128: 58 us, 59 MB; bf16 heads of 256: 138 us.
+// What bounds it: the issue of instructions (55 % of the slots; 1506 for a block of 16 keys of 128 and four rows),
+// and what waits for shared memory.  Decoding in fp32, 16 requests of 2000 .. 3900 positions, 32 query heads over
+// 8 of 128: 58 us, 59 MB; bf16 heads of 256: 138 us.
 #include "attention.cuh"
 #include "f32x2.cuh"
 #include "fp4.cuh"
