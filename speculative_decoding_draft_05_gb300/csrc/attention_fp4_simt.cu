@@ -15,6 +15,8 @@
 // What bounds it: the issue of instructions (55 % of the slots; 1506 for a block of 16 keys of 128 and four rows),
 // and what waits for shared memory.  Decoding in fp32, 16 requests of 2000 .. 3900 positions, 32 query heads over
 // 8 of 128: 58 us, 59 MB; bf16 heads of 256: 138 us.
+#include <type_traits>
+
 #include "attention.cuh"
 #include "f32x2.cuh"
 #include "fp4.cuh"
@@ -222,9 +224,7 @@ attention_fp4_simt_kernel(const __grid_constant__ SimtParams fp) {
           if (half == 0) sp[key_l * RW + i] = pack2(x[i], x[i]);
         }
         __syncwarp();
-        const bool masked = k0 + kFp4Block > all_see;
-#pragma unroll 4
-        for (int j = 0; j < kFp4Block; ++j) {
+        auto add = [&](int j, auto masked) {
           f32x2 v[NP];
 #pragma unroll
           for (int k = 0; k < kRuns; ++k) {
@@ -232,7 +232,7 @@ attention_fp4_simt_kernel(const __grid_constant__ SimtParams fp) {
             v[kCols / 2 * k] = v[kCols / 2 * k + kCols / 2 - 1] = 0ull;
             if (d < D) {
               uint32_t sc = vb[8 * D + j * (D / 16) + (d >> 4)];
-              if (masked && k0 + j >= all_see) {
+              if (masked.value && k0 + j >= all_see) {
                 // Past the item's end: any bytes.  Where some rows of the block do not see the key, a scale
                 // that is NaN is hidden from them, and makes the others NaN below.
                 if (k0 + j >= w.end) {
@@ -259,6 +259,13 @@ attention_fp4_simt_kernel(const __grid_constant__ SimtParams fp) {
 #pragma unroll
             for (int k = 0; k < NP; ++k) o[i][k] = fma2(e, v[k], o[i][k]);
           }
+        };
+        if (k0 + kFp4Block > all_see) {
+#pragma unroll 1
+          for (int j = 0; j < kFp4Block; ++j) add(j, std::true_type{});
+        } else {
+#pragma unroll 4
+          for (int j = 0; j < kFp4Block; ++j) add(j, std::false_type{});
         }
       }
       __syncwarp();  // (the stage and the probabilities are read)
