@@ -12,9 +12,9 @@
 // As in the kernel for bf16 (attention_fp4.cu), a CTA walks its share in tiles of 128 keys, a warp brings its own
 // blocks by asynchronous copies into a ring of its own, and a piece's eight partial results meet in shared memory.
 //
-// What bounds it: the issue of instructions (55 % of the slots; 1506 for a block of 16 keys of 128 and four rows),
-// and what waits for shared memory.  Decoding in fp32, 16 requests of 2000 .. 3900 positions, 32 query heads over
-// 8 of 128: 58 us, 59 MB; bf16 heads of 256: 138 us.
+// What bounds it: the issue of instructions (55 % of the slots; some 1400 for a block of 16 keys of 128 and four
+// rows), and what waits for shared memory.  Decoding in fp32, 16 requests of 2000 .. 3900 positions, 32 query heads over
+// 8 of 128: 52 us, 59 MB; bf16 heads of 256: 119 us.
 #include <type_traits>
 
 #include "attention.cuh"
@@ -368,9 +368,9 @@ cudaError_t launch_rows(const SimtParams& fp, char* ws, cudaStream_t s) {
 // Up to 36 rows a request on average (48 as attention_fp4_rows counts), in items of eight; else in attention.cu, in
 // items of 64.  Measured (us), here / there, 16 requests of 1000 .. 2000 positions, eight K/V heads:
 //   rows               8          16          32          64          9 tokens of 4 heads on average, 1 .. 17
-//   fp32, heads of 128 50 / 97    94 / 115    164 / 155   305 / 248   344 / 494 (2000 .. 3900 positions)
-//   fp32, heads of 64  38 / 58    71 / 69     119 / 95    217 / 152
-//   bf16, heads of 256 106 / 263  199 / 310   373 / 378   723 / 638   827 / 1264
+//   fp32, heads of 128 49 / 97    91 / 115    157 / 155   291 / 248   326 / 494 (2000 .. 3900 positions)
+//   fp32, heads of 64  37 / 58    68 / 69     113 / 95    203 / 152
+//   bf16, heads of 256 97 / 263   182 / 310   337 / 378   656 / 638   740 / 1264
 bool attention_fp4_simt_few_rows(const AttnArgs& a) {
   return a.fp4 && (a.dtype != DSPARK_BF16 || a.c.head_dim > 128) && a.a.n_tokens > 0 && attention_fp4_rows(a) <= 48;
 }
