@@ -124,7 +124,17 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, float factor, 
 // lies on it: the quotient by the rounded inverse, refined once by its exact
 // remainder.  (A border times the scale has at most seven bits, so an x beside it
 // is at least 2^-24 away relatively, more than half a step of the quotient.)
+// Under any scale but the largest the quotient is at most 6 and a half.  Under that one it may
+// leave fp32's range, and the remainder would be inf - inf: what is past 8 counts as 8, whose
+// code is that of 6.
+constexpr uint32_t kFp4LargestScale = 0x7eu;  // 448
+__device__ __forceinline__ float at_most_8(float x, const Fp4Scale& s) {
+  float y;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(8.0f * s.value));
+  return y;
+}
 __device__ __forceinline__ float fp4_quotient(float x, const Fp4Scale& s) {
+  x = at_most_8(x, s);
   const float q = x * s.inverse;
   return __fmaf_rn(__fmaf_rn(-q, s.value, x), s.inverse, q);
 }
