@@ -236,7 +236,7 @@ attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^k that brings it to 2^14 .. 2^15 (field 141 - (its - 127)), as far as 2^-k is normal
-        const int field = (int)(top >> 7), up = field == 0 || field == 255 ? 127 : min(268 - field, 253);
+        const int field = (int)(top >> 7), up = field == 255 ? 127 : min(268 - field, 253);
         const float f = __uint_as_float((uint32_t)up << 23);
         const float back = __uint_as_float((uint32_t)(254 - up) << 23) * p.scale_log2;
 #pragma unroll

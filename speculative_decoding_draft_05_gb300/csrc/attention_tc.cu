@@ -1305,7 +1305,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int field = (int)(top >> 7), up = field == 0 || field == 255 ? 127 : min(268 - field, 253);
+        const int field = (int)(top >> 7), up = field == 255 ? 127 : min(268 - field, 253);
         const float f = __uint_as_float((uint32_t)up << 23) * tp.sign;
         const int blk = a >> 7, t = a & 127;
 #pragma unroll

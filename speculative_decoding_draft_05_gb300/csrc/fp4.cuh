@@ -124,7 +124,7 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t amax_bits, float factor, 
 // lies on it: the quotient by the rounded inverse, refined once by its exact
 // remainder.  (A border times the scale has at most seven bits, so an x beside it
 // is at least 2^-24 away relatively, more than half a step of the quotient.)
-// Under any scale but the largest the quotient is at most 6 and a half.  Under that one it may
+// Under any scale but the largest the quotient is at most 9 (for a subnormal scale).  Under that one it may
 // leave fp32's range, and the remainder would be inf - inf: what is past 8 counts as 8, whose
 // code is that of 6.
 constexpr uint32_t kFp4LargestScale = 0x7eu;  // 448
