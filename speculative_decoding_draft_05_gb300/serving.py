@@ -140,7 +140,7 @@ def _cache(cache):
 
 def _row_dtype(cache, t, name):
     """The type of rows written to or asked of a cache: its own, or either for a 4-bit cache."""
-    if type(cache) is PagedCache:
+    if isinstance(cache, PagedCache):
         return cache.dtype
     if not isinstance(t, torch.Tensor) or t.dtype not in (_F32, torch.bfloat16):
         raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor")
