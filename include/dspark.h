@@ -514,8 +514,8 @@ int dspark_paged_attention(const void* q, long long q_token_stride, long long q_
  *           NULL: its position in the cache
  * dtype     of k_new, v_new, q, q_out: DSPARK_F32 or DSPARK_BF16, the cache's where
  *           that is one of them
- * q, q_out  [n_tokens, Hq, head_dim], strides in elements (q_out's no less than
- *           head_dim), head_dim contiguous;
+ * q, q_out  [n_tokens, Hq, head_dim], strides in elements, head_dim contiguous;
+ *           rows of q_out may not lie one over the other (they are refused);
  *           q_out may be q itself (with its strides), and may not overlap it
  *           otherwise.  Hq = 0: no queries.
  * A token whose position lies past the table is flagged (DSPARK_DEV_BAD_INPUT)

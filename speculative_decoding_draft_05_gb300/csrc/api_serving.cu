@@ -92,6 +92,17 @@ int check_meta(const dspark_cache* cache, const PageMeta& m, void* workspace, si
   return check_workspace(workspace, bytes, pages_workspace_layout(m.R, m.n_pages).total);
 }
 
+// Whether rows of D elements at t * token + h * head (t < T, h < H) do not lie one over the other.
+bool rows_apart(long long token, long long head, int T, int H, int D) {
+  if ((H > 1 && head < D) || (T > 1 && token < D)) return false;
+  if (H == 1 || T == 1 || (token - D) / head >= H - 1 || (head - D) / token >= T - 1) return true;
+  for (int h = 1; h < H; ++h) {  // heads h apart: the tokens apart that come nearest
+    const __int128 at = (__int128)h * head, t = at / token, over = at - t * token;
+    if ((t < T && over < D) || (t + 1 < T && token - over < D)) return false;
+  }
+  return true;
+}
+
 // Attention of either kind of cache, which is checked already.  dtype: of q and out.
 int attend(const void* q, long long q_token_stride, long long q_head_stride, int Hq, int dtype,
            const dspark_cache* cache, int layer, float k_factor, float v_factor,
@@ -219,8 +230,7 @@ int dspark_cache_append_rotary(const dspark_cache* cache, int layer, float k_fac
     return DSPARK_ERR_INVALID_ARG;
   if (Hq > 0 && n_tokens != 0 && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
     return DSPARK_ERR_INVALID_ARG;
-  if ((Hq > 1 && n_tokens != 0 && q_out_head_stride < cache->head_dim) ||
-      (Hq > 0 && n_tokens > 1 && q_out_token_stride < cache->head_dim))  // rows of q_out one over the other
+  if (Hq > 0 && n_tokens != 0 && !rows_apart(q_out_token_stride, q_out_head_stride, n_tokens, Hq, cache->head_dim))
     return DSPARK_ERR_INVALID_ARG;
   const uintptr_t a = (uintptr_t)(esize_of(dtype) - 1);
   if (((uintptr_t)k_new & a) || ((uintptr_t)v_new & a) || ((uintptr_t)q & a) || ((uintptr_t)q_out & a))
