@@ -16,6 +16,7 @@
 
 #include "attention.cuh"
 #include "fp4.cuh"
+#include "per_device.h"
 
 namespace dspark {
 
@@ -480,8 +481,7 @@ static_assert(kSimtCtas <= kAttnMaxCtas, "");
 template <typename T, int NI, bool FP4>
 cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
   const int smem = (kMR + 4 * kTN) * (NI * 32 + 4) * (int)sizeof(float);
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      attention_simt_kernel<T, NI, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t attr = once_per_device([=] { return allow_smem(attention_simt_kernel<T, NI, FP4>, smem); });
   if (attr != cudaSuccess) return attr;
   // Rows that are whole 16-byte (fp32) or 8-byte (bf16) vectors load as such.
   const CacheView& c = p.a.c;

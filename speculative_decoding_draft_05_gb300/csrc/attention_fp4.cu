@@ -34,6 +34,7 @@
 
 #include "attention.cuh"
 #include "fp4.cuh"
+#include "per_device.h"
 
 namespace dspark {
 
@@ -539,8 +540,7 @@ cudaError_t launch(Fp4Params fp, char* ws, cudaStream_t s) {
   p.stats = (float2*)(ws + w.stats);
   p.part = (float*)(ws + w.out);
   p.mr = 8 * NB;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      attention_fp4_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+  const cudaError_t attr = once_per_device([] { return allow_smem(attention_fp4_kernel<D, NB>, Sh::kBytes); });
   if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute attr_pdl;
   const cudaLaunchConfig_t cfg = overlapped_launch(dim3(Sh::kCtas), kThreads, Sh::kBytes, s, &attr_pdl);

@@ -20,6 +20,7 @@
 #include "attention.cuh"
 #include "f32x2.cuh"
 #include "fp4.cuh"
+#include "per_device.h"
 
 namespace dspark {
 
@@ -347,8 +348,7 @@ cudaError_t launch(SimtParams fp, char* ws, cudaStream_t s) {
   p.stats = (float2*)(ws + w.stats);
   p.part = (float*)(ws + w.out);
   p.mr = RW;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      attention_fp4_simt_kernel<T, NI, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+  const cudaError_t attr = once_per_device([] { return allow_smem(attention_fp4_simt_kernel<T, NI, RW>, Sh::kBytes); });
   if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute attr_pdl;
   const cudaLaunchConfig_t cfg = overlapped_launch(dim3(Sh::kCtas), kThreads, Sh::kBytes, s, &attr_pdl);

@@ -78,6 +78,7 @@
 
 #include "attention.cuh"
 #include "fp4.cuh"
+#include "per_device.h"
 #include "ptx.cuh"
 
 namespace dspark {
@@ -1588,21 +1589,15 @@ bool encode_q(CUtensorMap* map, const AttnArgs& a, int tokens) {
 }
 
 int sm_count() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
-      v = 1;
-    return v < kMaxCtas ? v : kMaxCtas;
-  }();
-  return n;
+  const int n = device_sms();
+  return n < kMaxCtas ? n : kMaxCtas;
 }
 
 template <int DP, bool FP4>
 cudaError_t launch(const TcParams& tp, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
                    cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      attention_tc_kernel<DP, FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, FP4>::kBytes);
+  const cudaError_t attr =
+      once_per_device([] { return allow_smem(attention_tc_kernel<DP, FP4>, Layout<DP, FP4>::kBytes); });
   if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute attr_pdl;
   const cudaLaunchConfig_t cfg =

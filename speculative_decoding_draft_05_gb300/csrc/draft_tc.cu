@@ -57,6 +57,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "per_device.h"
 #include "ptx.cuh"
 
 namespace dspark {
@@ -933,28 +934,10 @@ bool encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
   return r == CUDA_SUCCESS;
 }
 
-// L2 size of the current device (bytes), once.
-static size_t l2_bytes() {
-  static size_t n = 0;
-  if (n == 0) {
-    int dev = 0, v = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&v, cudaDevAttrL2CacheSize, dev);
-    n = v > 0 ? (size_t)v : 1;
-  }
-  return n;
-}
+// L2 size of the current device (bytes).
+static size_t l2_bytes() { return (size_t)device_attribute<cudaDevAttrL2CacheSize>(); }
 
-int sm_count() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 1;
-  }
-  return n;
-}
+int sm_count() { return device_sms(); }
 
 }  // namespace
 
@@ -1002,15 +985,10 @@ cudaError_t prepare_draft_tc(DraftTcPlan* plan, const void* U, const void* W2T, 
                 CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  // Once per process (thread-safe initialisation of a function-local static).
-  static const cudaError_t attr_err = [] {
-    cudaError_t e = cudaFuncSetAttribute(draft_step_tc_kernel<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(draft_step_tc_kernel<true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    return e;
-  }();
+  const cudaError_t attr_err = once_per_device([] {
+    const cudaError_t e = allow_smem(draft_step_tc_kernel<false>, kSmemBytes);
+    return e != cudaSuccess ? e : allow_smem(draft_step_tc_kernel<true>, kSmemBytes);
+  });
   if (attr_err != cudaSuccess) return attr_err;
   plan->scores = scores;
   plan->w2t = W2T;

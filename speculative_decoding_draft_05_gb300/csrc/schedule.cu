@@ -36,6 +36,7 @@
 // order (schedule_topk, one CTA).
 #include "common.cuh"
 #include "kernels.h"
+#include "per_device.h"
 
 namespace dspark {
 
@@ -387,9 +388,9 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int grid, cudaStream_t s
 
 // The scheduler's kernels ask for the largest shared-memory carveout, the one
 // the draft steps run with, so that an SM can hold a CTA of each at once (an
-// SM changes its carveout only when idle).  Once per process.
+// SM changes its carveout only when idle).
 cudaError_t set_carveouts() {
-  static const cudaError_t err = [] {
+  return once_per_device([] {
     const int kMax = (int)cudaSharedmemCarveoutMaxShared;
     cudaError_t e = cudaFuncSetAttribute(schedule_keys_kernel,
                                          cudaFuncAttributePreferredSharedMemoryCarveout, kMax);
@@ -403,8 +404,7 @@ cudaError_t set_carveouts() {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(schedule_topk_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kMax);
     return e;
-  }();
-  return err;
+  });
 }
 
 }  // namespace

@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "ptx.cuh"
 #include "kernels.h"
+#include "per_device.h"
 
 namespace dspark {
 
@@ -857,16 +858,7 @@ verify_emit_kernel(const int32_t* __restrict__ x, const float* __restrict__ lse,
 
 }  // namespace
 
-int verify_sm_count() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 1;
-  }
-  return n;
-}
+int verify_sm_count() { return device_sms(); }
 
 // Launch `kernel` as a programmatic dependent of the stream's previous kernel
 // (the kernel waits for it with griddepcontrol.wait at entry).
@@ -941,14 +933,10 @@ cudaError_t launch_verify_draw(const float* lse, const float* scores, const void
   const int chunks = draw_chunks(V, gpt);
   dim3 grid(chunks, R);
   if (dtype == DSPARK_BF16) {
-    static bool smem_set = false;  // the staged bonus draw's shared memory (> 48 KB: opt in)
-    if (!smem_set) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          verify_draw_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-          kDrawSmemBytes);
-      if (e != cudaSuccess) return e;
-      smem_set = true;
-    }
+    // The staged bonus draw's shared memory (> 48 KB: opt in).
+    const cudaError_t e =
+        once_per_device([] { return allow_smem(verify_draw_kernel<__nv_bfloat16>, kDrawSmemBytes); });
+    if (e != cudaSuccess) return e;
     return launch_chained_smem(verify_draw_kernel<__nv_bfloat16>, grid, dim3(kDrawThreads),
                                gpt == 4 ? (size_t)kDrawSmemBytes : 0, s, lse, scores,
                                (const __nv_bfloat16*)Z, ell, gamma, V, invT, philox_keys(seed),
