@@ -328,6 +328,7 @@ bool attention_tc_fp4_supported(const AttnArgs& a);
 cudaError_t launch_attention_tc_fp4(const AttnArgs& a, char* ws, cudaStream_t s);
 
 // Few rows over a 4-bit cache (attention_fp4.cu; in fp32, or wide heads: attention_fp4_simt.cu).
+bool attention_even_chunks(const AttnArgs& a);
 long long attention_fp4_rows(const AttnArgs& a);
 bool attention_fp4_few_rows(const AttnArgs& a);
 size_t attention_fp4_rows_workspace_bytes(int head_dim);

@@ -555,23 +555,33 @@ cudaError_t launch_rows(const Fp4Params& fp, char* ws, cudaStream_t s) {
 
 }  // namespace
 
-// Rows of most requests, as far as the host can tell: where there are no more tokens than
-// requests, a token's; else the mean and a third.
+// Rows of most requests, as far as the host can tell.  Where there are no more tokens than requests, a
+// token's.  Where they divide evenly, as many tokens each: chunks of one length, which a fixed number of drafted
+// tokens gives, or rows padded to the longest.  Else the mean and a third, as a chunk longer than the mean takes
+// another item.
+bool attention_even_chunks(const AttnArgs& a) { return a.a.n_tokens <= a.a.R || a.a.n_tokens % a.a.R == 0; }
 long long attention_fp4_rows(const AttnArgs& a) {
   if (a.a.n_tokens <= a.a.R) return a.G;
   const long long all = (long long)a.a.n_tokens * a.G;
-  return (all + all / 3 + a.a.R - 1) / a.a.R;
+  return attention_even_chunks(a) ? all / a.a.R : (all + all / 3 + a.a.R - 1) / a.a.R;
 }
 
 size_t attention_fp4_rows_workspace_bytes(int head_dim) {
   return attn_workspace_layout(kMaxRows, head_dim, kAttnMaxCtas).total;
 }
 
-// Up to 16 rows a request here, more in attention_tc.cu, whose products are of 128 rows whatever there
-// are.  Measured (us), here / there, requests of 2000 .. 8192 positions (32 of them) and of 100 ..
-// 600 (128), eight K/V heads of 128:
-//   8 rows  57 / 95   47 / 85      16  82 / 95   68 / 88
-//   12      80 / 95   64 / 89      20  156 / 95  125 / 88
+// Up to 16 rows a request here, by the count above, and of them up to 8 in items of 8; more in attention_tc.cu,
+// whose products are of 128 rows whatever there are.  Measured (us), items of 8 / of 16 / there, requests of 2000
+// .. 8192 positions (32 of them) and of 100 .. 600 (128), eight K/V heads of 128:
+//   chunks alike    8 rows   56 / 76 / 100     47 / 53 / 83
+//                   12       112 / 80 / 101    93 / 62 / 85
+//                   16       113 / 83 / 102    95 / 66 / 84
+//                   20       154 / 157 / 103   130 / 119 / 85
+//   uneven, on average 7.6   66 / 77 / 99      56 / 53 / 83       (counted as 10)
+//                   11.2                       79 / 66 / 83       (15)
+//                   13.2     114 / 104 / 101                      (18)
+//                   14.6                       96 / 82 / 83       (20)
+//                   18 .. 20 132 / 118 / 103   121 / 106 / 84
 bool attention_fp4_few_rows(const AttnArgs& a) {
   return a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0 && attention_fp4_rows(a) <= kMaxRows;
 }
