@@ -365,14 +365,29 @@ cudaError_t launch_rows(const SimtParams& fp, char* ws, cudaStream_t s) {
 
 }  // namespace
 
-// Up to 36 rows a request on average (48 as attention_fp4_rows counts), in items of eight; else in attention.cu, in
-// items of 64.  Measured (us), here / there, 16 requests of 1000 .. 2000 positions, eight K/V heads:
-//   rows               8          16          32          64          9 tokens of 4 heads on average, 1 .. 17
-//   fp32, heads of 128 49 / 97    91 / 115    157 / 155   291 / 248   326 / 494 (2000 .. 3900 positions)
-//   fp32, heads of 64  37 / 58    68 / 69     113 / 95    203 / 152
-//   bf16, heads of 256 97 / 263   182 / 310   337 / 378   656 / 638   740 / 1264
+// Few rows here, in items of eight, more in attention.cu, in items of 64: chunks of one length fill those, uneven
+// ones leave much of them empty.  So the rule has a bound for either, of rows as attention_fp4_rows counts them, for
+// heads up to 64 and for wider ones.  Measured (us), here / there, 16 requests of 1000 .. 2000 positions, four query
+// heads of each of eight K/V heads:
+//   chunks alike, rows    8          16         24         32         40         48         64
+//   fp32, heads of 64     36 / 54    64 / 67    85 / 79    107 / 92   128 / 108  148 / 126  191 / 146
+//   fp32, heads of 128    48 / 92    86 / 110   116 / 133  148 / 147  179 / 191  209 / 218  273 / 236
+//   bf16, heads of 256    90 / 238   174 / 278  244 / 314  320 / 348  393 / 473  468 / 508  618 / 589
+// and 64 requests of 200 .. 3000 positions:
+//   fp32, heads of 64     109 / 211  223 / 261  320 / 304  418 / 353             615 / 494  810 / 589
+//   fp32, heads of 128    158 / 457  315 / 521  456 / 591  603 / 668             878 / 955  1166 / 1032
+// Uneven chunks, 16 requests as above, by the count (the mean and a third):
+//   fp32, heads of 64     15: 51 / 72      48: 123 / 129    64: 154 / 163    82: 196 / 183    98: 218 / 218
+//   fp32, heads of 128    20: 90 / 129     43: 160 / 214    80: 260 / 304    134: 422 / 448   175: 528 / 550
+//   bf16, heads of 256    20: 178 / 326    56: 411 / 627    98: 721 / 825    140: 1001 / 1120
+// and 64 requests:
+//   fp32, heads of 64     40: 392 / 527    74: 740 / 786    82: 798 / 816    114: 1127 / 1058
+//   fp32, heads of 128    45: 629 / 989    84: 1149 / 1432  145: 1859 / 2047 153: 2155 / 2332
 bool attention_fp4_simt_few_rows(const AttnArgs& a) {
-  return a.fp4 && (a.dtype != DSPARK_BF16 || a.c.head_dim > 128) && a.a.n_tokens > 0 && attention_fp4_rows(a) <= 48;
+  if (!a.fp4 || (a.dtype == DSPARK_BF16 && a.c.head_dim <= 128) || a.a.n_tokens == 0) return false;
+  const bool narrow = a.c.head_dim <= 64;
+  const int most = attention_even_chunks(a) ? (narrow ? 20 : 48) : (narrow ? 80 : 160);
+  return attention_fp4_rows(a) <= most;
 }
 
 size_t attention_fp4_simt_workspace_bytes(int head_dim) {

@@ -29,3 +29,18 @@ def test_rows_of_bf16_queries(tmp_path):
     got = kernels([dict(R=R, T=T, G=G) for (R, T, G), _ in want], tmp_path)
     for (c, w), g in zip(want, got):
         assert w in g, (c, w, g)
+
+
+@pytest.mark.parametrize("dtype, D", [("f32", 32), ("f32", 64), ("f32", 96), ("f32", 128), ("f32", 256), ("bf16", 160),
+                                      ("bf16", 256)])
+def test_rows_on_cuda_cores(tmp_path, dtype, D):
+    narrow = D <= 64
+    want = [((16, 16, 4), SIMT), ((16, 64, 4), SIMT), ((16, 80, 4), SIMT), ((16, 16, 20), SIMT),      # chunks alike
+            ((16, 208, 4), TILES), ((16, 16, 49), TILES), ((1, 49, 1), TILES)]
+    for T, G in ((96, 4), (128, 4), (192, 4), (16, 21), (16, 48)):
+        want.append(((16, T, G), TILES if narrow else SIMT))
+    want += [((16, 143, 4), SIMT), ((16, 239, 4), SIMT), ((16, 241, 4), TILES if narrow else SIMT),   # uneven
+             ((16, 479, 4), TILES if narrow else SIMT), ((16, 481, 4), TILES)]
+    got = kernels([dict(R=R, T=T, G=G, dtype=dtype, D=D) for (R, T, G), _ in want], tmp_path)
+    for (c, w), g in zip(want, got):
+        assert w in g, (c, w, g)
