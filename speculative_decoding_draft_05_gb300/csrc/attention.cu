@@ -496,8 +496,10 @@ cudaError_t launch_simt(const AttnParams& p, cudaStream_t s) {
 template <typename T, bool FP4>
 cudaError_t launch_simt_dim(const AttnParams& p, cudaStream_t s) {
   const int ni = (p.a.c.head_dim + 31) / 32;
-  if (ni <= 2) return launch_simt<T, 2, FP4>(p, s);
-  if (ni <= 4) return launch_simt<T, 4, FP4>(p, s);
+  if constexpr (!FP4 || sizeof(T) == 4) {  // (bf16 queries over a 4-bit cache: only wide heads come here)
+    if (ni <= 2) return launch_simt<T, 2, FP4>(p, s);
+    if (ni <= 4) return launch_simt<T, 4, FP4>(p, s);
+  }
   return launch_simt<T, 8, FP4>(p, s);
 }
 

@@ -583,7 +583,8 @@ size_t attention_fp4_rows_workspace_bytes(int head_dim) {
 //                   14.6                       96 / 82 / 83       (20)
 //                   18 .. 20 132 / 118 / 103   121 / 106 / 84
 bool attention_fp4_few_rows(const AttnArgs& a) {
-  return a.dtype == DSPARK_BF16 && a.c.head_dim <= 128 && a.a.n_tokens > 0 && attention_fp4_rows(a) <= kMaxRows;
+  if (a.dtype != DSPARK_BF16 || a.c.head_dim > 128) return false;
+  return a.a.n_tokens == 0 || attention_fp4_rows(a) <= kMaxRows;  // (without tokens a call only checks its offsets)
 }
 
 cudaError_t launch_attention_fp4_rows(const AttnArgs& a, char* ws, cudaStream_t s) {

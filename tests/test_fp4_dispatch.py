@@ -44,3 +44,13 @@ def test_rows_on_cuda_cores(tmp_path, dtype, D):
     got = kernels([dict(R=R, T=T, G=G, dtype=dtype, D=D) for (R, T, G), _ in want], tmp_path)
     for (c, w), g in zip(want, got):
         assert w in g, (c, w, g)
+
+
+def test_calls_without_tokens(tmp_path):
+    """They check their offsets in a kernel that other calls run too."""
+    calls = [dict(R=4, T=0, G=G, D=D) for G in (1, 40) for D in (32, 64, 96, 128)]
+    for c, k in zip(calls, kernels(calls, tmp_path)):
+        assert f"attention_fp4_kernelILi{c['D']}" in k, (c, k)
+    calls = [dict(R=4, T=0, G=4, D=D, dtype=t) for D, t in ((64, "f32"), (128, "f32"), (256, "f32"), (160, "bf16"))]
+    for c, k in zip(calls, kernels(calls, tmp_path)):
+        assert TILES in k, (c, k)
