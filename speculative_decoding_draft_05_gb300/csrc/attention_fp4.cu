@@ -114,6 +114,7 @@ struct Fp4Params {
   int q_vec;  // q's rows are whole 16-byte vectors
 };
 
+// (Of 128 registers; heads of 128 spill 8 bytes, and 104 with two blocks of rows, whose sums take 32 registers more.)
 template <int D, int NB>  // NB blocks of 8 rows an item
 __global__ void __launch_bounds__(kThreads, 2)
 attention_fp4_kernel(const __grid_constant__ Fp4Params fp) {

@@ -12,7 +12,7 @@
 // As in the kernel for bf16 (attention_fp4.cu), a CTA walks its share in tiles of 128 keys, a warp brings its own
 // blocks by asynchronous copies into a ring of its own, and a piece's eight partial results meet in shared memory.
 //
-// What bounds it: the issue of instructions (55 % of the slots; some 1400 for a block of 16 keys of 128 and four
+// What bounds it: the issue of instructions (57 % of the slots; 1365 for a block of 16 keys of 128 and four
 // rows), and what waits for shared memory.  Decoding in fp32, 16 requests of 2000 .. 3900 positions, 32 query heads over
 // 8 of 128: 52 us, 59 MB; bf16 heads of 256: 119 us.
 #include <type_traits>
@@ -65,6 +65,7 @@ struct SimtParams {
   Divider by_page;
 };
 
+// (Of 128 registers; items of eight rows spill 52 bytes with heads of 128, 20 with 64.)
 template <typename T, int NI, int RW>  // head_dim up to 32 NI; RW rows an item
 __global__ void __launch_bounds__(kThreads, NI <= 4 ? 2 : 1)
 attention_fp4_simt_kernel(const __grid_constant__ SimtParams fp) {

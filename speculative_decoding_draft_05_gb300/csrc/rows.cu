@@ -13,8 +13,8 @@
 // hidden by the rows of other warps, and by loading a row's K and V ahead of it.
 // Measured, 32 query and 8 K/V heads of 128: 4868 tokens of 512 requests into a bf16
 // cache 25.5 us in a graph (122 MB, 4.8 TB/s); prompts of 16,384 tokens into a bf16 cache 70 us
-// (411 MB, 5.9 TB/s; of half-rotated heads 90), into a 4-bit one 79 us (362 MB, 4.6 TB/s, half of the
-// issue slots taken by rotation, error bound and conversions; half-rotated 100); reading 36,321
+// (411 MB, 5.9 TB/s; of half-rotated heads 89), into a 4-bit one 79 us (362 MB, 4.6 TB/s, half of the
+// issue slots taken by rotation, error bound and conversions; half-rotated 101); reading 36,321
 // positions of a 4-bit cache 35 us (191 MB, 5.5 TB/s).
 #include <type_traits>
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t largest8(const float* y) {
 
 // Eight codes of a group whose scale is s.  (fp4_quotient, two at a time; its bound in a branch, as most groups
 // need none.  16,384 tokens: 78.6 us without it, 79.3 so; where such groups have scalar code of their own
-// whole heads take 80.5 and half-rotated ones, whose code grows past the instruction cache, 127 for 100.)
+// whole heads take 80.5 and half-rotated ones 127 for 101.)
 __device__ __forceinline__ uint32_t codes8(const float* y, const Fp4Scale& s) {
   if (s.inverse == 0.0f) return 0u;
   float z[8];
@@ -288,8 +288,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 append_rotary_kernel(const RotaryAppendArgs p, const RowSteps rs) {
   constexpr bool Inter = P == kNeighbours;
   constexpr Pairs kOfQ = P == kHalf ? kHalves : P;
-  // Units a lane at a time (interleaved ones are half as much; more in partly rotated rows spill: prompts
-  // into a bf16 cache 86 -> 93 us).
+  // Units a lane at a time (interleaved ones are half as much; more in partly rotated rows: prompts into a
+  // bf16 cache 86 -> 93 us).  Two CTAs an SM leave 128 registers.  Of whole heads in halves only fp32 rows spill
+  // (8 bytes, into 4 bits 184), interleaved ones up to 64 bytes; partly rotated halves spill 68 (bf16), 132
+  // (fp32) and 232 .. 244 (into 4 bits), a part of what they take longer.
   constexpr int kAhead = kQUnits<Inter && Full>, kKAhead = (sizeof(T) == 2 ? 2 : 1) * (Inter && Full ? 2 : 1);
   constexpr int kVAhead = sizeof(T) == 2 ? 4 : 1, kMore = Full || sizeof(T) == 4 ? 1 : 2;
   const int lane = threadIdx.x & 31, D = p.c.head_dim, half = p.rot / 2;
